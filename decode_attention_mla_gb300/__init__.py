@@ -64,6 +64,63 @@ class Args(ctypes.Structure):
                 ("lse", ctypes.c_void_p), ("kv_scale", ctypes.c_float)]
 
 
+class RopeSpec(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int), ("scaling", ctypes.c_int), ("base", ctypes.c_double),
+                ("factor", ctypes.c_double), ("original_ctx", ctypes.c_double), ("beta_fast", ctypes.c_double),
+                ("beta_slow", ctypes.c_double)]
+
+
+class RopeArgs(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int), ("tokens", ctypes.c_int), ("heads", ctypes.c_int), ("rot_dim", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("amplitude", ctypes.c_float), ("turns", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p), ("n_tokens", ctypes.c_void_p),
+                ("q_rope", ctypes.c_void_p), ("q_rope_batch", ctypes.c_longlong), ("q_rope_token", ctypes.c_longlong),
+                ("q_rope_head", ctypes.c_longlong),
+                ("q_out", ctypes.c_void_p), ("q_out_batch", ctypes.c_longlong), ("q_out_token", ctypes.c_longlong),
+                ("q_out_head", ctypes.c_longlong),
+                ("c", ctypes.c_void_p), ("c_batch", ctypes.c_longlong), ("c_token", ctypes.c_longlong),
+                ("k_rope", ctypes.c_void_p), ("k_rope_batch", ctypes.c_longlong), ("k_rope_token", ctypes.c_longlong),
+                ("kv", ctypes.c_void_p), ("kv_rows", ctypes.c_longlong), ("row_stride", ctypes.c_longlong),
+                ("kv_fp8", ctypes.c_int), ("kv_scale", ctypes.c_float),
+                ("d_pos", ctypes.c_void_p), ("row_offset", ctypes.c_void_p),
+                ("row_positions", ctypes.c_void_p), ("row_weights", ctypes.c_void_p)]
+
+
+class TreeShape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int), ("tokens", ctypes.c_int), ("heads", ctypes.c_int), ("scale", ctypes.c_float),
+                ("num_sms", ctypes.c_int), ("pdl", ctypes.c_int), ("stall_test", ctypes.c_int)]
+
+
+class TreePlan(ctypes.Structure):
+    _fields_ = [("shape", TreeShape), ("magic", ctypes.c_int), ("num_sms", ctypes.c_int), ("grid", ctypes.c_int),
+                ("scratch_bytes", ctypes.c_size_t), ("status_offset", ctypes.c_size_t),
+                ("part_offset", ctypes.c_size_t), ("lse_part_offset", ctypes.c_size_t)]
+
+
+class TreeArgs(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("kv", ctypes.c_void_p), ("kv_rows", ctypes.c_longlong),
+                ("row_stride", ctypes.c_longlong), ("d_pos", ctypes.c_void_p), ("row_offset", ctypes.c_void_p),
+                ("mask", ctypes.c_void_p), ("n_tokens", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("out_fp32", ctypes.c_int), ("lse", ctypes.c_void_p)]
+
+
+class TreeCommitArgs(ctypes.Structure):
+    _fields_ = [("kv", ctypes.c_void_p), ("kv_rows", ctypes.c_longlong), ("row_stride", ctypes.c_longlong),
+                ("kv_fp8", ctypes.c_int), ("batch", ctypes.c_int), ("tokens", ctypes.c_int),
+                ("accept", ctypes.c_void_p), ("n_accept", ctypes.c_void_p), ("d_pos", ctypes.c_void_p),
+                ("d_pos_out", ctypes.c_void_p), ("row_offset", ctypes.c_void_p),
+                ("row_positions", ctypes.c_void_p), ("row_weights", ctypes.c_void_p)]
+
+
+class EvictArgs(ctypes.Structure):
+    _fields_ = [("kv", ctypes.c_void_p), ("kv_rows", ctypes.c_longlong), ("row_stride", ctypes.c_longlong),
+                ("kv_fp8", ctypes.c_int), ("batch", ctypes.c_int), ("keep", ctypes.c_int), ("sink", ctypes.c_int),
+                ("recent", ctypes.c_int), ("max_rows", ctypes.c_int), ("weights", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p), ("d_pos", ctypes.c_void_p), ("next_pos", ctypes.c_void_p),
+                ("row_offset", ctypes.c_void_p), ("weights_out", ctypes.c_void_p), ("positions_out", ctypes.c_void_p),
+                ("d_pos_out", ctypes.c_void_p)]
+
+
 class MLADecodeError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -76,7 +133,9 @@ _lib = None
 EXPORTED = ("mla_decode_abi_version", "mla_decode_plan", "mla_decode_run", "mla_decode_combine",
             "mla_decode_forward", "mla_decode_append", "mla_decode_advance", "mla_decode_scratch_init",
             "mla_decode_strerror", "mla_decode_forward_static", "mla_decode_project", "mla_decode_forward_step",
-            "mla_floor_empty_pair", "mla_floor_read", "mla_floor_gather", "mla_decode_static_status", "mla_decode_static_reset")
+            "mla_floor_empty_pair", "mla_floor_read", "mla_floor_gather", "mla_decode_static_status", "mla_decode_static_reset",
+            "mla_rope_table", "mla_rope_append", "mla_tree_plan", "mla_tree_forward", "mla_tree_weights",
+            "mla_tree_commit", "mla_evict_scratch_bytes", "mla_evict")
 
 
 def lib():
@@ -122,6 +181,23 @@ def lib():
         L.mla_floor_read.argtypes = [P, SZ, I, P, P, I, P]
         L.mla_floor_gather.restype = I
         L.mla_floor_gather.argtypes = [P, LL, LL, I, P, LL, I, P, P, I, P]
+        F = ctypes.c_float
+        L.mla_rope_table.restype = I
+        L.mla_rope_table.argtypes = [ctypes.POINTER(RopeSpec), ctypes.POINTER(ctypes.c_ulonglong)]
+        L.mla_rope_append.restype = I
+        L.mla_rope_append.argtypes = [ctypes.POINTER(RopeArgs), P]
+        L.mla_tree_plan.restype = I
+        L.mla_tree_plan.argtypes = [ctypes.POINTER(TreeShape), ctypes.POINTER(TreePlan)]
+        L.mla_tree_forward.restype = I
+        L.mla_tree_forward.argtypes = [ctypes.POINTER(TreePlan), ctypes.POINTER(TreeArgs), P, SZ, P]
+        L.mla_tree_weights.restype = I
+        L.mla_tree_weights.argtypes = [ctypes.POINTER(TreePlan), ctypes.POINTER(TreeArgs), P, F, P, SZ, P]
+        L.mla_tree_commit.restype = I
+        L.mla_tree_commit.argtypes = [ctypes.POINTER(TreeCommitArgs), P]
+        L.mla_evict_scratch_bytes.restype = SZ
+        L.mla_evict_scratch_bytes.argtypes = [I, I]
+        L.mla_evict.restype = I
+        L.mla_evict.argtypes = [ctypes.POINTER(EvictArgs), P, SZ, P]
         _lib = L
         return L
 
@@ -295,6 +371,295 @@ def project(latent, wv_b, y, *, pdl: bool = False, stream=None) -> None:
 def advance(d_pos, stream=None) -> None:
     """``mla_decode_advance``: d_pos += 1 on the device."""
     _check(lib().mla_decode_advance(_ptr(d_pos), int(d_pos.numel()), _stream(stream)), "mla_decode_advance")
+
+
+# ---- drafted tokens, their rotation, and a bounded cache ---------------------
+# Arguments that stay the same from call to call are laid out once
+# (``*_make_args``), which also checks the tensors; the ``*_args`` calls then
+# pass them on.  The returned structures keep their tensors alive.
+
+def _need(t, name, dtypes, shape=None, contiguous=True):
+    """Check a tensor of a call: CUDA, on the current device, type, shape, layout."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name}: a CUDA tensor is needed (tensors passed to the MLA decode kernels must be "
+                         "CUDA tensors)")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is {torch.cuda.current_device()}")
+    if not isinstance(dtypes, tuple):
+        dtypes = (dtypes,)
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if shape is not None and (t.dim() != len(shape) or any(e is not None and e != s for s, e in zip(t.shape, shape))):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple('*' if e is None else e for e in shape)}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def _maybe(t, name, dtypes, shape):
+    return None if t is None else _need(t, name, dtypes, shape)
+
+
+def _cache(kv, kv_rows, row_stride, fp8_ok=True):
+    """(pointer, rows, row stride, fp8) of a cache tensor [rows, >= 576 columns]."""
+    import torch
+    fp8 = (torch.uint8, torch.float8_e4m3fn) if fp8_ok else ()
+    p = _need(kv, "kv", (torch.bfloat16,) + fp8, contiguous=False)
+    if kv.dim() != 2 or kv.shape[1] != D_ROW or kv.stride(1) != 1:
+        raise ValueError("kv must be [rows, 576] with contiguous rows")
+    if kv.shape[0] == 0:
+        raise ValueError("kv has no rows")
+    stride = int(kv.stride(0)) if kv.shape[0] > 1 else max(int(kv.stride(0)), D_ROW)
+    if kv_rows is not None and not 1 <= kv_rows <= kv.shape[0]:
+        raise ValueError("kv_rows is outside the tensor")
+    if row_stride is not None and row_stride != stride:
+        raise ValueError("row_stride differs from the tensor's")
+    return p, int(kv_rows if kv_rows is not None else kv.shape[0]), stride, int(kv.dtype != torch.bfloat16)
+
+
+def _strides(t, name, shape, last):
+    """Pointer and leading strides of a bf16 tensor whose last dimension is contiguous."""
+    import torch
+    p = _need(t, name, torch.bfloat16, shape, contiguous=False)
+    if t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    # the stride of a dimension of one is never used: 0 passes every check
+    return [p] + [int(t.stride(i)) if t.shape[i] > 1 else 0 for i in range(last)]
+
+
+class RopeTable:
+    """Angles per position of the rotated pairs (``mla_rope_table``), on the device."""
+
+    def __init__(self, turns, rot_dim, interleaved, amplitude):
+        self.turns, self.rot_dim, self.interleaved, self.amplitude = turns, rot_dim, interleaved, amplitude
+
+
+ROPE_SCALING = {"none": 0, "linear": 1, "yarn": 2}
+
+
+def rope_turns(rot_dim: int = D_ROPE, base: float = 10000.0, *, scaling: str = "none", factor: float = 1.0,
+               original_ctx: float = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0) -> list:
+    """``mla_rope_table``: angle per position of each pair, as 64-bit fractions of a turn (host integers)."""
+    if scaling not in ROPE_SCALING:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALING)}")
+    spec = RopeSpec(rot_dim=rot_dim, scaling=ROPE_SCALING[scaling], base=base, factor=factor,
+                    original_ctx=original_ctx, beta_fast=beta_fast, beta_slow=beta_slow)
+    buf = (ctypes.c_ulonglong * 32)()
+    _check(lib().mla_rope_table(ctypes.byref(spec), buf), "mla_rope_table")
+    return list(buf[:rot_dim // 2])
+
+
+def rope_table(rot_dim: int = D_ROPE, base: float = 10000.0, *, interleaved: bool = True, scaling: str = "none",
+               factor: float = 1.0, original_ctx: float = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0,
+               amplitude: float = 1.0, device=None) -> RopeTable:
+    """Rotation table on the device: pairs (2j, 2j+1) if ``interleaved``, else (j, j + rot_dim/2);
+    ``scaling``: "none", "linear" or "yarn"; ``amplitude`` multiplies sines and cosines."""
+    import torch
+    turns = rope_turns(rot_dim, base, scaling=scaling, factor=factor, original_ctx=original_ctx,
+                       beta_fast=beta_fast, beta_slow=beta_slow)
+    t = torch.tensor(turns, dtype=torch.int64, device=device or "cuda")       # all below 2^62
+    return RopeTable(t, rot_dim, bool(interleaved), float(amplitude))
+
+
+def rope_make_args(table: RopeTable, positions, *, q_rope=None, q=None, c=None, k_rope=None, kv=None, d_pos=None,
+                   row_offset=None, n_tokens=None, kv_scale: float = 1.0, row_positions=None, row_weights=None,
+                   kv_rows: int | None = None, row_stride: int | None = None) -> RopeArgs:
+    """Arguments of :func:`rope_append_args`.
+
+    ``positions``: int32 [B, N].  Queries: ``q_rope`` bf16 [B, N, H, 64] (any strides, multiples of 8) is
+    rotated into ``q[..., 512:]`` of bf16 [B, N, H, 576].  Rows: ``c`` bf16 [B, N, 512] and ``k_rope``
+    bf16 [B, N, 64] go to cache row ``row_offset[b] + d_pos[b] + n`` of ``kv`` (bf16, or E4M3 bytes of
+    value / ``kv_scale``); ``row_positions`` (int32 [rows]) takes the positions, ``row_weights``
+    (fp32 [rows]) zeros.  Either part may be left out."""
+    import torch
+    B, N = positions.shape
+    a = RopeArgs(batch=int(B), tokens=int(N), rot_dim=table.rot_dim, interleaved=int(table.interleaved),
+                 amplitude=table.amplitude, turns=_need(table.turns, "table", torch.int64),
+                 positions=_need(positions, "positions", torch.int32, (B, N)),
+                 n_tokens=_maybe(n_tokens, "n_tokens", torch.int32, (B,)), kv_scale=float(kv_scale))
+    if (q_rope is None) != (q is None):
+        raise ValueError("q_rope and q go together")
+    if q is not None:
+        H = q.shape[2] if q.dim() == 4 else -1
+        a.heads = int(H)
+        a.q_rope, a.q_rope_batch, a.q_rope_token, a.q_rope_head = _strides(q_rope, "q_rope", (B, N, H, D_ROPE), 3)
+        _need(q, "q", torch.bfloat16, (B, N, H, D_ROW), contiguous=False)
+        part = q[..., D_LATENT:]
+        a.q_out, a.q_out_batch, a.q_out_token, a.q_out_head = _strides(part, "q", (B, N, H, D_ROPE), 3)
+    if not (c is None) == (k_rope is None) == (kv is None) == (d_pos is None):
+        raise ValueError("c, k_rope, kv and d_pos go together")
+    if kv is not None:
+        a.c, a.c_batch, a.c_token = _strides(c, "c", (B, N, D_LATENT), 2)
+        a.k_rope, a.k_rope_batch, a.k_rope_token = _strides(k_rope, "k_rope", (B, N, D_ROPE), 2)
+        a.kv, a.kv_rows, a.row_stride, a.kv_fp8 = _cache(kv, kv_rows, row_stride)
+        a.d_pos = _need(d_pos, "d_pos", torch.int32, (B,))
+        a.row_offset = _maybe(row_offset, "row_offset", torch.int64, (B,))
+        a.row_positions = _side(row_positions, "row_positions", torch.int32, a.kv_rows)
+        a.row_weights = _side(row_weights, "row_weights", torch.float32, a.kv_rows)
+    a._keep = (table, positions, q_rope, q, c, k_rope, kv, d_pos, row_offset, n_tokens, row_positions, row_weights)
+    return a
+
+
+def _side(t, name, dtype, rows):
+    """A per-row array: at least one entry for every cache row."""
+    if t is None:
+        return None
+    p = _need(t, name, dtype, (None,))
+    if t.shape[0] < rows:
+        raise ValueError(f"{name} needs an entry for each of the {rows} cache rows")
+    return p
+
+
+def rope_append_args(a: RopeArgs, stream=None) -> None:
+    """``mla_rope_append`` with prebuilt arguments."""
+    _check(lib().mla_rope_append(ctypes.byref(a), _stream(stream)), "mla_rope_append")
+
+
+def rope_append(table: RopeTable, positions, *, stream=None, **kw) -> None:
+    """Rotate the new tokens' queries and keys by their positions and append their rows to the cache
+    (arguments as for :func:`rope_make_args`)."""
+    rope_append_args(rope_make_args(table, positions, **kw), stream)
+
+
+def tree_plan(*, batch: int, tokens: int, heads: int, scale: float, num_sms: int = 0, pdl: bool = False,
+              stall_test: bool = False) -> TreePlan:
+    """``mla_tree_plan``: up to ``tokens`` (<= 64) drafted tokens per request."""
+    s = TreeShape(batch=batch, tokens=tokens, heads=heads, scale=scale, num_sms=num_sms, pdl=int(bool(pdl)),
+                  stall_test=int(bool(stall_test)))
+    p = TreePlan()
+    _check(lib().mla_tree_plan(ctypes.byref(s), ctypes.byref(p)), "mla_tree_plan")
+    return p
+
+
+def tree_alloc_scratch(p: TreePlan, device=None):
+    """Allocate and zero the scratch of a tree plan (outside capture); :func:`status_word` reads its status."""
+    return alloc_scratch(p, device)
+
+
+def tree_make_args(q, kv, out, lse, *, d_pos, row_offset=None, mask=None, n_tokens=None,
+                   kv_rows: int | None = None, row_stride: int | None = None) -> TreeArgs:
+    """Arguments of :func:`tree_forward_args` and :func:`tree_weights_args` (which needs no ``out``).
+
+    ``q``: bf16 [B, Q, H, 576]; ``kv``: bf16 [rows, 576]; ``out``: bf16 or fp32 [B, Q, H, 512]; ``lse``: fp32
+    [B, Q, H]; ``mask``: int64 [B, Q], bit j of word i: token i attends drafted token j (None: a chain)."""
+    import torch
+    if q.dim() != 4:
+        raise ValueError("q must be [B, Q, H, 576]")
+    B, Q, H, _ = q.shape
+    kvp, rows, stride, _ = _cache(kv, kv_rows, row_stride, fp8_ok=False)
+    a = TreeArgs(q=_need(q, "q", torch.bfloat16, (B, Q, H, D_ROW)), kv=kvp, kv_rows=rows, row_stride=stride,
+                 d_pos=_need(d_pos, "d_pos", torch.int32, (B,)),
+                 row_offset=_maybe(row_offset, "row_offset", torch.int64, (B,)),
+                 mask=_maybe(mask, "mask", torch.int64, (B, Q)),
+                 n_tokens=_maybe(n_tokens, "n_tokens", torch.int32, (B,)),
+                 out=_maybe(out, "out", (torch.bfloat16, torch.float32), (B, Q, H, D_LATENT)),
+                 out_fp32=int(out is not None and out.dtype == torch.float32),
+                 lse=_need(lse, "lse", torch.float32, (B, Q, H)))
+    a._keep = (q, kv, d_pos, row_offset, mask, n_tokens, out, lse)
+    a._dims = (int(B), int(Q), int(H))
+    return a
+
+
+def _tree_dims(p: TreePlan, a: TreeArgs):
+    """The arguments' [B, Q, H] must be the plan's: the kernels index by the plan."""
+    if a._dims != (p.shape.batch, p.shape.tokens, p.shape.heads):
+        raise ValueError(f"arguments of shape {a._dims} for a plan of "
+                         f"{(p.shape.batch, p.shape.tokens, p.shape.heads)}")
+
+
+def tree_forward_args(p: TreePlan, a: TreeArgs, scratch, stream=None) -> None:
+    """``mla_tree_forward`` with prebuilt arguments."""
+    _tree_dims(p, a)
+    sp, sb = _scratch_args(scratch)
+    _check(lib().mla_tree_forward(ctypes.byref(p), ctypes.byref(a), sp, sb, _stream(stream)), "mla_tree_forward")
+
+
+def tree_forward(p: TreePlan, q, kv, out, lse, scratch, *, stream=None, **kw) -> None:
+    """Attention of each request's drafted tokens over its committed rows and the drafted rows that their
+    masks name (arguments as for :func:`tree_make_args`)."""
+    tree_forward_args(p, tree_make_args(q, kv, out, lse, **kw), scratch, stream)
+
+
+def tree_weights_args(p: TreePlan, a: TreeArgs, scratch, weights, *, decay: float = 1.0, stream=None) -> None:
+    """``mla_tree_weights`` with prebuilt arguments: ``weights`` fp32 [rows], one entry per cache row."""
+    import torch
+    _tree_dims(p, a)
+    w = _side(weights, "weights", torch.float32, a.kv_rows)
+    sp, sb = _scratch_args(scratch)
+    _check(lib().mla_tree_weights(ctypes.byref(p), ctypes.byref(a), w, float(decay), sp, sb, _stream(stream)),
+           "mla_tree_weights")
+
+
+def tree_weights(p: TreePlan, q, kv, lse, scratch, weights, *, decay: float = 1.0, stream=None, **kw) -> None:
+    """``weights[row] = decay * weights[row] +`` the attention weight the row got from every token and head,
+    given the log-sum-exps that :func:`tree_forward` returned."""
+    tree_weights_args(p, tree_make_args(q, kv, None, lse, **kw), scratch, weights, decay=decay, stream=stream)
+
+
+def tree_commit(kv, accept, n_accept, *, d_pos, d_pos_out=None, row_offset=None, row_positions=None,
+                row_weights=None, kv_rows: int | None = None, row_stride: int | None = None, stream=None) -> None:
+    """``mla_tree_commit``: rows ``d_pos + accept[b, k]`` move to ``d_pos + k`` for k < n_accept[b]
+    (``accept``: int32 [B, Q]); ``d_pos_out`` (may be ``d_pos``) takes d_pos + n_accept."""
+    import torch
+    B, Q = accept.shape
+    kvp, rows, stride, fp8 = _cache(kv, kv_rows, row_stride)
+    a = TreeCommitArgs(kv=kvp, kv_rows=rows, row_stride=stride, kv_fp8=fp8, batch=int(B), tokens=int(Q),
+                       accept=_need(accept, "accept", torch.int32, (B, Q)),
+                       n_accept=_need(n_accept, "n_accept", torch.int32, (B,)),
+                       d_pos=_need(d_pos, "d_pos", torch.int32, (B,)),
+                       d_pos_out=_maybe(d_pos_out, "d_pos_out", torch.int32, (B,)),
+                       row_offset=_maybe(row_offset, "row_offset", torch.int64, (B,)),
+                       row_positions=_side(row_positions, "row_positions", torch.int32, rows),
+                       row_weights=_side(row_weights, "row_weights", torch.float32, rows))
+    _check(lib().mla_tree_commit(ctypes.byref(a), _stream(stream)), "mla_tree_commit")
+
+
+def evict_alloc_scratch(*, batch: int, keep: int, device=None):
+    """Scratch of :func:`evict` for a batch and a budget."""
+    import torch
+    n = int(lib().mla_evict_scratch_bytes(batch, keep))
+    if n == 0:
+        raise ValueError("batch must be 1 .. 65535 and keep at least 1")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def evict_make_args(kv, weights, positions, *, d_pos, next_pos, keep: int, sink: int = 0, recent: int = 0,
+                    row_offset=None, max_rows: int | None = None, weights_out=None, positions_out=None,
+                    d_pos_out=None, kv_rows: int | None = None, row_stride: int | None = None) -> EvictArgs:
+    """Arguments of :func:`evict_args`.  ``weights`` fp32 [rows] and ``positions`` int32 [rows] have an entry
+    per cache row; the ``*_out`` tensors default to the inputs (in place).  ``max_rows``: largest ``d_pos``
+    expected (sizes the launch; default: the cache's rows)."""
+    import torch
+    B = int(d_pos.shape[0])
+    kvp, rows, stride, fp8 = _cache(kv, kv_rows, row_stride)
+    wo = weights if weights_out is None else weights_out
+    po = positions if positions_out is None else positions_out
+    do = d_pos if d_pos_out is None else d_pos_out
+    a = EvictArgs(kv=kvp, kv_rows=rows, row_stride=stride, kv_fp8=fp8, batch=B, keep=int(keep), sink=int(sink),
+                  recent=int(recent), max_rows=int(min(rows, 0x7fffffff) if max_rows is None else max_rows),
+                  weights=_side(weights, "weights", torch.float32, rows),
+                  positions=_side(positions, "positions", torch.int32, rows),
+                  d_pos=_need(d_pos, "d_pos", torch.int32, (B,)),
+                  next_pos=_need(next_pos, "next_pos", torch.int32, (B,)),
+                  row_offset=_maybe(row_offset, "row_offset", torch.int64, (B,)),
+                  weights_out=_side(wo, "weights_out", torch.float32, rows),
+                  positions_out=_side(po, "positions_out", torch.int32, rows),
+                  d_pos_out=_need(do, "d_pos_out", torch.int32, (B,)))
+    a._keep = (kv, weights, positions, d_pos, next_pos, row_offset, wo, po, do)
+    return a
+
+
+def evict_args(a: EvictArgs, scratch, stream=None) -> None:
+    """``mla_evict`` with prebuilt arguments."""
+    sp, sb = _scratch_args(scratch)
+    _check(lib().mla_evict(ctypes.byref(a), sp, sb, _stream(stream)), "mla_evict")
+
+
+def evict(kv, weights, positions, scratch, *, stream=None, **kw) -> None:
+    """Keep each request's ``keep`` rows of largest weight (the first ``sink`` and the last ``recent``
+    positions before all others), compacted in place (arguments as for :func:`evict_make_args`)."""
+    evict_args(evict_make_args(kv, weights, positions, **kw), scratch, stream)
 
 
 def floor_empty_pair(a, b, *, pdl: bool = True, stream=None) -> None:

@@ -1,0 +1,79 @@
+// mla_commit.cu -- the accepted path of a tree of drafts moved together behind
+// the committed rows (mla_tree_commit in include/mla_tree.h):
+//   row d_pos + k  <-  row d_pos + accept[k],   k < n_accept
+//
+// One CTA per request reads every moved row into registers (at most 64 rows of
+// 72 16-byte units, five units a thread) and writes after a barrier, so any
+// order of the path is right although source and destination rows overlap.
+// Bound: latency (a path is at most 74 KB); a row already in place is skipped.
+#include <cstdint>
+
+#include "device_utils.cuh"
+#include "mla_internal.h"
+#include "mla_tree.h"
+
+namespace mla {
+namespace {
+
+constexpr int kCommitThreads = 1024;
+constexpr int kCommitUnits = (MLA_TREE_MAX_TOKENS * (kRowBytes / 16) + kCommitThreads - 1) / kCommitThreads;
+
+__global__ void __launch_bounds__(kCommitThreads) mla_commit_kernel(const mla_tree_commit_args a) {
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const int b = blockIdx.x;
+    const int tid = threadIdx.x;
+    __shared__ int src[MLA_TREE_MAX_TOKENS];               // source draft of each path entry, or -1
+    const int d = a.d_pos[b];
+    const int n = min(max(a.n_accept[b], 0), a.tokens);
+    const long long first = (a.row_offset ? a.row_offset[b] : 0) + d;
+    if (tid < n) {
+        const int j = a.accept[static_cast<long long>(b) * a.tokens + tid];
+        const bool in_cache = first + tid >= 0 && first + tid < a.kv_rows && first + j >= 0 && first + j < a.kv_rows;
+        src[tid] = d >= 0 && j >= 0 && j < MLA_TREE_MAX_TOKENS && j != tid && in_cache ? j : -1;
+    }
+    __syncthreads();
+    const int units = a.kv_fp8 ? kDRow / 16 : kRowBytes / 16;
+    const long long stride = a.row_stride * (a.kv_fp8 ? 1 : 2);
+    char* base = static_cast<char*>(a.kv) + first * stride;
+    uint4 v[kCommitUnits];
+#pragma unroll
+    for (int i = 0; i < kCommitUnits; ++i) {
+        const int w = tid + i * kCommitThreads;
+        const int k = w / units;
+        if (k < n && src[k] >= 0) v[i] = reinterpret_cast<const uint4*>(base + src[k] * stride)[w - k * units];
+    }
+    int pos = 0;
+    float weight = 0.f;
+    const bool side = tid < n && src[tid] >= 0;
+    if (side && a.row_positions) pos = a.row_positions[first + src[tid]];
+    if (side && a.row_weights) weight = a.row_weights[first + src[tid]];
+    __syncthreads();                                       // every source (and d_pos) is read
+#pragma unroll
+    for (int i = 0; i < kCommitUnits; ++i) {
+        const int w = tid + i * kCommitThreads;
+        const int k = w / units;
+        if (k < n && src[k] >= 0) reinterpret_cast<uint4*>(base + k * stride)[w - k * units] = v[i];
+    }
+    if (side && a.row_positions) a.row_positions[first + tid] = pos;
+    if (side && a.row_weights) a.row_weights[first + tid] = weight;
+    if (tid == 0 && a.d_pos_out) a.d_pos_out[b] = d < 0 ? d : d + n;
+}
+
+bool off(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to != 0; }
+
+}  // namespace
+}  // namespace mla
+
+extern "C" int mla_tree_commit(const mla_tree_commit_args* a, void* stream) {
+    if (!a || !a->kv || !a->accept || !a->n_accept || !a->d_pos) return MLA_EINVAL;
+    if (a->batch < 1 || a->batch > 65535 || a->tokens < 1 || a->tokens > MLA_TREE_MAX_TOKENS) return MLA_EINVAL;
+    if (a->kv_fp8 != 0 && a->kv_fp8 != 1) return MLA_EINVAL;
+    if (a->kv_rows < 1 || a->row_stride < MLA_D_ROW || (a->batch > 1 && !a->row_offset)) return MLA_EINVAL;
+    if (a->row_stride % (a->kv_fp8 ? 16 : 8) != 0 || mla::off(a->kv, 16) || mla::off(a->accept, 4) ||
+        mla::off(a->n_accept, 4) || mla::off(a->d_pos, 4) || mla::off(a->d_pos_out, 4) ||
+        mla::off(a->row_offset, 8) || mla::off(a->row_positions, 4) || mla::off(a->row_weights, 4))
+        return MLA_EALIGN;
+    mla::mla_commit_kernel<<<a->batch, mla::kCommitThreads, 0, static_cast<cudaStream_t>(stream)>>>(*a);
+    return mla::launch_status(cudaGetLastError());
+}

@@ -16,7 +16,6 @@ namespace {
 
 constexpr int kPlanMagic = 0x4d4c4131;       // "MLA1"
 static_assert(mla::kStaticScratchBytes == MLA_STATIC_SCRATCH_BYTES, "static scratch size differs from the header");
-constexpr int kMaxDevices = 64;
 // The partial kernel is persistent with one CTA per SM: its 5-stage ring of
 // cache rows fills the shared memory.  The two-CTAs-per-SM target named in
 // "Launch Geometry" (Lecture 04, s.4: kMlaBlocksPerSm = 2) was there so one
@@ -61,6 +60,8 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 // Rank-3 view of bf16 rows of 576: {64 elements, rows, 9 chunks of 64} with
 // strides {row stride, 128 bytes}; a box {64, box_rows, box_chunks} lands in
 // shared memory as [chunk][row][64], 128-byte swizzled.
+}  // namespace
+namespace mla {
 int encode_bf16_row_chunks(CUtensorMap* map, const void* base, long long rows, long long row_stride_elems,
                            uint32_t box_rows, uint32_t box_chunks) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
@@ -74,6 +75,9 @@ int encode_bf16_row_chunks(CUtensorMap* map, const void* base, long long rows, l
                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? MLA_OK : MLA_ECUDA;
 }
+}  // namespace mla
+namespace {
+using mla::encode_bf16_row_chunks;
 
 // Rank-3 view of E4M3 rows of 576 bytes: {64 bytes, rows, 9 chunks of 64}
 // with strides {row stride, 64 bytes}; a box {64, 32, 9} lands in shared
@@ -91,20 +95,22 @@ int encode_e4m3_row_chunks(CUtensorMap* map, const void* base, long long rows, l
     return r == CUDA_SUCCESS ? MLA_OK : MLA_ECUDA;
 }
 
-std::atomic<int> g_sm_count[kMaxDevices];
-std::atomic<int> g_prepared[kMaxDevices];
+std::atomic<int> g_sm_count[mla::kMaxDevices];
+std::atomic<int> g_prepared[mla::kMaxDevices];
 std::mutex g_prepare_mutex;
 
 size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) != 0; }
 
+}  // namespace
+namespace mla {
 int current_device(int* dev) {
     if (cudaGetDevice(dev) != cudaSuccess) {
         cudaGetLastError();
         return MLA_ECUDA;
     }
-    if (*dev < 0 || *dev >= kMaxDevices) return MLA_ECUDA;
+    if (*dev < 0 || *dev >= mla::kMaxDevices) return MLA_ECUDA;
     return MLA_OK;
 }
 
@@ -122,6 +128,17 @@ int device_sm_count(int dev, int* sms) {
     *sms = cached;
     return MLA_OK;
 }
+
+int launch_status(cudaError_t e) {
+    if (e == cudaSuccess) return MLA_OK;
+    cudaGetLastError();
+    return MLA_ECUDA;
+}
+}  // namespace mla
+namespace {
+using mla::current_device;
+using mla::device_sm_count;
+using mla::launch_status;
 
 // Kernel attributes are set once per device, outside any capture
 // ("Graph-resident decode", Lecture 08, s.3: lazy initialisation inside a
@@ -260,12 +277,6 @@ int check_args(const mla_decode_plan_t* pl, const mla_decode_args* a) {
 int check_scratch(const mla_decode_plan_t* pl, const void* scratch, size_t bytes) {
     if (!scratch || misaligned(scratch, kScratchAlign) || bytes < pl->scratch_bytes) return MLA_ESCRATCH;
     return MLA_OK;
-}
-
-int launch_status(cudaError_t e) {
-    if (e == cudaSuccess) return MLA_OK;
-    cudaGetLastError();
-    return MLA_ECUDA;
 }
 
 // Fused decode-step state update (mla_decode_forward_step): the new rows

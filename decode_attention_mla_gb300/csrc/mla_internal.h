@@ -118,6 +118,15 @@ struct TcMaps {
     CUtensorMap q;
 };
 
+// Host helpers shared by the C entry points (mla_decode_api.cu); each returns
+// an mla_status.
+constexpr int kMaxDevices = 64;
+int current_device(int* dev);
+int device_sm_count(int dev, int* sms);
+int launch_status(cudaError_t e);
+int encode_bf16_row_chunks(CUtensorMap* map, const void* base, long long rows, long long row_stride_elems,
+                           uint32_t box_rows, uint32_t box_chunks);
+
 // Launch helpers (each returns the cudaError_t of the launch).
 cudaError_t partial_mma_prepare(int device);
 size_t partial_mma_smem_bytes(bool fp8 = false, bool tc_pv = false);
