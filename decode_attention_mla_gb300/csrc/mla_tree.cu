@@ -1,50 +1,18 @@
 // mla_tree.cu -- attention of a tree of drafted tokens over the latent cache,
 // and the weight that each cache row gets from it (include/mla_tree.h).
+#include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 
-#include "device_utils.cuh"
-#include "mla_internal.h"
-#include "mla_tree.h"
+#include "mla_tree.cuh"
 
 namespace mla {
 namespace {
 
 constexpr int kTreeMagic = 0x4d4c5431;                     // "MLT1"
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kMinTiles = 1;
 constexpr int kThreads = 256;
-
-struct TreeParams {
-    mla_tree_args a;
-    int batch, tokens, heads;
-    float scale_log2;
-    float* weights;
-    float decay;
-};
-
-struct Request {
-    long long base;
-    int d_pos, n_tok;
-    int lo, hi;                                            // rows [lo, hi) of the request lie inside the cache
-};
-
-__device__ __forceinline__ Request load_request(const TreeParams& p, int b) {
-    Request r;
-    r.base = p.a.row_offset ? p.a.row_offset[b] : 0;
-    r.d_pos = p.a.d_pos[b];
-    r.n_tok = p.a.n_tokens ? min(max(p.a.n_tokens[b], 0), p.tokens) : p.tokens;
-    const long long rows = r.d_pos < 0 ? 0 : static_cast<long long>(r.d_pos) + r.n_tok;
-    const long long lo = r.base < 0 ? -r.base : 0, hi = p.a.kv_rows - r.base;
-    r.hi = static_cast<int>(hi < rows ? (hi < 0 ? 0 : hi) : rows);
-    r.lo = static_cast<int>(lo < r.hi ? lo : r.hi);
-    return r;
-}
-__device__ __forceinline__ unsigned long long token_mask(const TreeParams& p, int b, int i, int n_tok) {
-    const unsigned long long m =
-        p.a.mask ? p.a.mask[static_cast<long long>(b) * p.tokens + i] : (~0ull >> (63 - i));
-    return n_tok < 64 ? m & ((1ull << n_tok) - 1) : m;
-}
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -61,63 +29,19 @@ __device__ __forceinline__ void load_row(const uint16_t* row, int lane, float (&
     }
 }
 
-// One warp per (request, token, head).
-__global__ void __launch_bounds__(kThreads) mla_tree_kernel(const TreeParams p) {
-    grid_dependency_wait();
-    const int lane = threadIdx.x & 31;
-    const long long w = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-    if (w >= static_cast<long long>(p.batch) * p.tokens * p.heads) return;
-    const int b = static_cast<int>(w / (p.tokens * p.heads));
-    const int i = static_cast<int>(w / p.heads - static_cast<long long>(b) * p.tokens);
-    const Request r = load_request(p, b);
-    if (i >= r.n_tok) return;
-    const unsigned long long mask = token_mask(p, b, i, r.n_tok);
-    float q[18], k[18], o[16];
-    load_row(static_cast<const uint16_t*>(p.a.q) + w * kDRow, lane, q);
-#pragma unroll
-    for (int j = 0; j < 16; ++j) o[j] = 0.f;
-    float m = -INFINITY, l = 0.f;
-    for (int t = r.lo; t < r.hi; ++t) {
-        if (t >= r.d_pos && !(mask >> (t - r.d_pos) & 1)) continue;
-        load_row(static_cast<const uint16_t*>(p.a.kv) + (r.base + t) * p.a.row_stride, lane, k);
-        float s = 0.f;
-#pragma unroll
-        for (int j = 0; j < 18; ++j) s += q[j] * k[j];
-        s = warp_sum(s) * p.scale_log2;
-        const float mn = fmaxf(m, s);
-        const float al = m == -INFINITY ? 0.f : exp2f(m - mn);
-        const float pr = s == -INFINITY ? 0.f : exp2f(s - mn);
-        l = l * al + pr;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) o[j] = o[j] * al + pr * k[j];
-        m = mn;
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const long long at = w * kDLatent + 2 * lane + 64 * j;
-        if (p.a.out_fp32)
-            *reinterpret_cast<float2*>(static_cast<float*>(p.a.out) + at) = make_float2(o[2 * j] * inv, o[2 * j + 1] * inv);
-        else
-            *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.a.out) + at) =
-                pack_bf16x2(o[2 * j] * inv, o[2 * j + 1] * inv);
-    }
-    if (lane == 0) p.a.lse[w] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-}
-
 // One warp per cache row of a request.
 __global__ void __launch_bounds__(kThreads) mla_tree_weights_kernel(const TreeParams p) {
     grid_dependency_wait();
     const int lane = threadIdx.x & 31;
     const int b = blockIdx.y;
-    const Request r = load_request(p, b);
+    const TreeRequest r = load_tree_request(p, b);
     const int warps = gridDim.x * (kThreads / 32);
     for (int t = r.lo + blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); t < r.hi; t += warps) {
         float q[18], k[18];
         load_row(static_cast<const uint16_t*>(p.a.kv) + (r.base + t) * p.a.row_stride, lane, k);
         float sum = 0.f;
         for (int i = 0; i < r.n_tok; ++i) {
-            if (t >= r.d_pos && !(token_mask(p, b, i, r.n_tok) >> (t - r.d_pos) & 1)) continue;
+            if (t >= r.d_pos && !(tree_mask(p, b, i, r.n_tok) >> (t - r.d_pos) & 1)) continue;
             for (int h = 0; h < p.heads; ++h) {
                 const long long w = (static_cast<long long>(b) * p.tokens + i) * p.heads + h;
                 const float lse = p.a.lse[w];
@@ -149,12 +73,16 @@ int check_shape(const mla_tree_shape* s) {
     return MLA_OK;
 }
 
+// Scratch: status word, the pairs' merge notes, their pieces (two each) and
+// the pieces' log-sum-exps, each region 256-byte aligned.
+constexpr size_t kMergeOffset = 256;
 void layout(mla_tree_plan_t* pl) {
-    pl->grid = pl->num_sms;
+    const size_t pairs = pl->num_sms > 1 ? pl->num_sms / 2 : 1;
+    pl->grid = static_cast<int>(2 * pairs);
     pl->status_offset = 0;
-    pl->part_offset = 256;
-    pl->lse_part_offset = 256;
-    pl->scratch_bytes = 256;
+    pl->part_offset = up256(kMergeOffset + pairs * sizeof(TreeMerge));
+    pl->lse_part_offset = pl->part_offset + pairs * 2 * kTreeBlockRows * kDLatent * sizeof(float);
+    pl->scratch_bytes = up256(pl->lse_part_offset + pairs * 2 * kTreeBlockRows * sizeof(float));
 }
 
 int check_plan(const mla_tree_plan_t* pl) {
@@ -183,6 +111,55 @@ int check_scratch(const mla_tree_plan_t* pl, const void* scratch, size_t bytes) 
     return !scratch || off(scratch, 256) || bytes < pl->scratch_bytes ? MLA_ESCRATCH : MLA_OK;
 }
 
+std::atomic<int> g_tree_prepared[kMaxDevices];
+std::mutex g_tree_mutex;
+
+// Kernel attributes, once per device, outside any capture.
+int prepare(cudaStream_t st, bool may_capture) {
+    int dev = 0;
+    const int rc = current_device(&dev);
+    if (rc != MLA_OK) return rc;
+    if (g_tree_prepared[dev].load(std::memory_order_acquire)) return MLA_OK;
+    if (may_capture) {
+        cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+        if (cudaStreamIsCapturing(st, &cs) != cudaSuccess) {
+            cudaGetLastError();
+            return MLA_ECUDA;
+        }
+        if (cs != cudaStreamCaptureStatusNone) return MLA_ENOTREADY;
+    }
+    std::lock_guard<std::mutex> lock(g_tree_mutex);
+    if (launch_status(tree_attend_prepare()) != MLA_OK) return MLA_ECUDA;
+    g_tree_prepared[dev].store(1, std::memory_order_release);
+    return MLA_OK;
+}
+
+TreeParams params(const mla_tree_plan_t* pl, const mla_tree_args* a, void* scratch) {
+    char* base = static_cast<char*>(scratch);
+    TreeParams p{};
+    p.a = *a;
+    p.batch = pl->shape.batch;
+    p.tokens = pl->shape.tokens;
+    p.heads = pl->shape.heads;
+    p.clusters = pl->grid / 2;
+    p.min_tiles = kMinTiles;
+    p.scale_log2 = pl->shape.scale * kLog2e;
+    p.merge = reinterpret_cast<TreeMerge*>(base + kMergeOffset);
+    p.part = reinterpret_cast<float*>(base + pl->part_offset);
+    p.lse_part = reinterpret_cast<float*>(base + pl->lse_part_offset);
+    p.status = reinterpret_cast<int*>(base + pl->status_offset);
+    p.stall_test = pl->shape.stall_test;
+    return p;
+}
+
+int encode_maps(const mla_tree_plan_t* pl, const mla_tree_args* a, TreeMaps* m) {
+    const long long rows = static_cast<long long>(pl->shape.batch) * pl->shape.tokens * pl->shape.heads;
+    int rc = encode_bf16_row_chunks(&m->kv, a->kv, a->kv_rows, a->row_stride, 64, 2);
+    if (rc == MLA_OK) rc = encode_bf16_row_chunks(&m->rope, a->kv, a->kv_rows, a->row_stride, 64, 1);
+    if (rc == MLA_OK) rc = encode_bf16_row_chunks(&m->q, a->q, rows, MLA_D_ROW, 64, 9);
+    return rc;
+}
+
 }  // namespace
 }  // namespace mla
 
@@ -200,6 +177,7 @@ int mla_tree_plan(const mla_tree_shape* shape, mla_tree_plan_t* plan) {
         int dev = 0;
         rc = mla::current_device(&dev);
         if (rc == MLA_OK) rc = mla::device_sm_count(dev, &pl.num_sms);
+        if (rc == MLA_OK) rc = mla::prepare(nullptr, false);
         if (rc != MLA_OK) return rc;
     }
     mla::layout(&pl);
@@ -213,12 +191,14 @@ int mla_tree_forward(const mla_tree_plan_t* plan, const mla_tree_args* args, voi
     if (rc == MLA_OK) rc = mla::check_args(plan, args, false);
     if (rc == MLA_OK) rc = mla::check_scratch(plan, scratch, scratch_bytes);
     if (rc != MLA_OK) return rc;
-    mla::TreeParams p{*args, plan->shape.batch, plan->shape.tokens, plan->shape.heads,
-                      plan->shape.scale * mla::kLog2e, nullptr, 0.f};
-    const long long rows = static_cast<long long>(p.batch) * p.tokens * p.heads;
-    const unsigned grid = static_cast<unsigned>((rows + mla::kThreads / 32 - 1) / (mla::kThreads / 32));
-    mla::mla_tree_kernel<<<grid, mla::kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    return mla::launch_status(cudaGetLastError());
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    rc = mla::prepare(st, true);
+    if (rc != MLA_OK) return rc;
+    mla::TreeMaps maps;
+    rc = mla::encode_maps(plan, args, &maps);
+    if (rc != MLA_OK) return rc;
+    return mla::launch_status(
+        mla::launch_tree_attend(maps, mla::params(plan, args, scratch), plan->shape.pdl != 0, st));
 }
 
 int mla_tree_weights(const mla_tree_plan_t* plan, const mla_tree_args* args, float* weights, float decay,
@@ -229,8 +209,9 @@ int mla_tree_weights(const mla_tree_plan_t* plan, const mla_tree_args* args, flo
     if (rc == MLA_OK && mla::off(weights, 4)) rc = MLA_EALIGN;
     if (rc == MLA_OK) rc = mla::check_scratch(plan, scratch, scratch_bytes);
     if (rc != MLA_OK) return rc;
-    mla::TreeParams p{*args, plan->shape.batch, plan->shape.tokens, plan->shape.heads,
-                      plan->shape.scale * mla::kLog2e, weights, decay};
+    mla::TreeParams p = mla::params(plan, args, scratch);
+    p.weights = weights;
+    p.decay = decay;
     mla::mla_tree_weights_kernel<<<dim3(plan->num_sms * 4, p.batch), mla::kThreads, 0,
                                    static_cast<cudaStream_t>(stream)>>>(p);
     return mla::launch_status(cudaGetLastError());
