@@ -76,8 +76,10 @@ int check_shape(const mla_tree_shape* s) {
 // Scratch: status word, the pairs' merge notes, their pieces (two each) and
 // the pieces' log-sum-exps, each region 256-byte aligned.
 constexpr size_t kMergeOffset = 256;
+// Pairs of SMs to use; the merge holds the weights of at most so many pieces.
+int tree_pairs(int num_sms) { return num_sms < 2 ? 1 : num_sms > 2048 ? 1024 : num_sms / 2; }
 void layout(mla_tree_plan_t* pl) {
-    const size_t pairs = pl->num_sms > 1 ? pl->num_sms / 2 : 1;
+    const size_t pairs = static_cast<size_t>(tree_pairs(pl->num_sms));
     pl->grid = static_cast<int>(2 * pairs);
     pl->status_offset = 0;
     pl->part_offset = up256(kMergeOffset + pairs * sizeof(TreeMerge));

@@ -29,8 +29,8 @@
 // L2 hits).  QK of tile g + 1 is issued before PV of tile g, so the softmax of a
 // tile runs under the next tile's QK.
 //
-// Warps of a CTA: 0-3 softmax and epilogue (thread = tensor-memory lane), 4
-// TMA producer, 5 MMA issue (even CTA only) and tensor memory.  Barriers that
+// Warps of a CTA: 0-7 softmax and epilogue, 8 TMA of Q and K, 9 MMA issue (even
+// CTA only) and tensor memory, 10 TMA of V, 11 relay of P's readiness.  Barriers that
 // the MMA thread waits on live in the even CTA and take arrivals of both.
 //
 // Rounding: P is rounded to bf16 for the product (relative 2^-8 at most per
@@ -45,7 +45,7 @@
 // Every wait is bounded; a wait that runs out raises MLA_EDEVICE in the status
 // word, both CTAs leave their loops and meet at a cluster barrier, and copies
 // still in flight get time to land before shared memory is given up.
-#include <cfloat>
+#include <algorithm>
 #include <cmath>
 
 #include "mla_tree.cuh"
@@ -54,13 +54,14 @@
 namespace mla {
 namespace {
 
-constexpr int kSlots = 8;
+constexpr int kKSlots = 3, kVSlots = 4;
 constexpr uint32_t kSlotBytes = 16384;                     // 2 column chunks of 64 rows x 128 bytes
 constexpr uint32_t kChunkBytes = 8192;
 constexpr uint32_t kQBytes = 9 * kChunkBytes;
-constexpr int kThreads = 192;
-constexpr int kSoftmaxThreads = 128;
-constexpr int kProducerWarp = 4, kMmaWarp = 5;
+constexpr int kThreads = 384;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
+constexpr int kProducerWarp = 8, kMmaWarp = 9, kValueWarp = 10, kRelayWarp = 11;
 constexpr int kBarSoftmax = 1;                             // hardware barrier of the softmax warps
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 0, kTmemS = 256;               // O: 2 x 128 columns, S: 2 x 64 columns
@@ -69,25 +70,31 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr long long kDrainCycles = 2000ll * 1000ll;        // about 1 ms: time for copies in flight after an abort
 
 struct Work {                                              // this cluster's run of units
-    int b;
-    long long rel, count, per;                             // first unit of the run within request b, units, run length
+    long long count, per;                                  // units of the run, and of every cluster's
+    TreeRequest r;                                         // its first unit
+    int b, rb, tile;
 };
 
 struct __align__(1024) Shared {
-    uint8_t ring[kSlots][kSlotBytes];
+    uint8_t k[kKSlots][kSlotBytes];                        // ring: 64 keys x 128 columns, QK operand
+    uint8_t v[kVSlots][kSlotBytes];                        // (feature half i, key half kb) at 2 i + kb, PV operand
     uint8_t rope[kChunkBytes];                             // this CTA's 64 keys, rope columns
     uint8_t q[kQBytes];                                    // 9 chunks of 64 query rows
-    uint8_t p[2][kChunkBytes];                             // P, 64 rows x 128 keys, two key atoms
-    float red_max[kSoftmaxThreads], red_sum[kSoftmaxThreads];
-    uint64_t ready[kSlots], rope_ready, q_ready, p_ready, o_free;   // used in the even CTA, arrivals of both
-    uint64_t empty[kSlots], rope_empty, q_empty, s_full[2], o_done; // in each CTA, arrivals of the MMA thread
+    uint8_t p[2][2][kChunkBytes];                          // P of two tiles, 64 rows x 128 keys in two key atoms
+    float red_max[4][64], red_sum[4][64];                  // by quarter of the tile's keys, row
+    // used in the even CTA, arrivals of both
+    uint64_t k_ready[kKSlots], v_ready[kVSlots], rope_ready, q_ready, s_free[2], p_peer[2], o_free;
+    // in each CTA, arrivals of the MMA thread
+    uint64_t k_empty[kKSlots], v_empty[kVSlots], rope_empty, q_empty, s_full[2], o_done[2];
+    // this CTA's P is written; (even CTA) both CTAs' are
+    uint64_t p_local[2], p_ready[2];
     uint64_t v_local[2];                                   // V of a tile with drafted rows has landed in this CTA
     uint64_t stall_bar;
     Work work;
     uint32_t tmem_base;
     int abort_flag;
 };
-static_assert(sizeof(Shared) + 1024 <= 227 * 1024, "fits shared memory");
+static_assert(sizeof(Shared) <= 227 * 1024, "fits shared memory");
 
 __device__ __forceinline__ int row_blocks(const TreeParams& p, const TreeRequest& r) {
     return (r.n_tok * p.heads + kTreeBlockRows - 1) / kTreeBlockRows;
@@ -98,7 +105,7 @@ __device__ __forceinline__ int tiles_of(const TreeRequest& r) { return (r.hi + k
 struct Cursor {
     TreeRequest r;
     int b, rb, n_rb, tile, n_tiles;
-    long long left;                                        // tiles of the run from here on, this one included
+    int left;                                              // tiles of the run from here on, this one included
     int g;                                                 // tiles of the run before this one
     int item;                                              // row blocks (or parts) before this one
     bool first;                                            // first tile of its item
@@ -110,13 +117,14 @@ struct Cursor {
     }
     __device__ __forceinline__ void start(const TreeParams& p, const Work& w) {
         b = w.b;
-        left = w.count;
+        rb = w.rb;
+        tile = w.tile;
+        left = static_cast<int>(w.count);
         g = item = 0;
         first = true;
-        if (left <= 0) return;
-        request(p);
-        rb = static_cast<int>(w.rel / n_tiles);
-        tile = static_cast<int>(w.rel - static_cast<long long>(rb) * n_tiles);
+        r = w.r;
+        n_rb = row_blocks(p, r);
+        n_tiles = tiles_of(r);
     }
     __device__ __forceinline__ bool last() const { return left == 1 || tile == n_tiles - 1; }
     __device__ __forceinline__ void next(const TreeParams& p) {
@@ -145,47 +153,77 @@ __device__ __forceinline__ void raise_error(Shared& sh, int* status) {
     if (status) atomicCAS(status, 0, static_cast<int>(MLA_EDEVICE));
 }
 
+// Quotient of non-negative numbers; 64-bit division is a slow call.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
 // One warp: this cluster's run.  All units in order of (request, row block,
 // tile); run length = ceil(units / clusters), at least min_tiles.
 __device__ void find_work(const TreeParams& p, int cluster, int lane, Work* out) {
-    auto units_of = [&](int b) -> long long {
-        if (b >= p.batch) return 0;
-        const TreeRequest r = load_tree_request(p, b);
-        return static_cast<long long>(row_blocks(p, r)) * tiles_of(r);
+    auto request_of = [&](int b) {
+        TreeRequest r{};
+        if (b < p.batch) r = load_tree_request(p, b);
+        return r;
     };
-    const long long mine = units_of(lane);                 // requests 0 .. 31 stay in registers
-    long long total = 0;
-    for (int b0 = 0; b0 < p.batch; b0 += 32) total += b0 == 0 ? mine : units_of(b0 + lane);
+    auto units_of = [&](const TreeRequest& r) { return static_cast<long long>(row_blocks(p, r)) * tiles_of(r); };
+    TreeRequest r = request_of(lane);                      // requests 0 .. 31 stay in registers
+    long long total = units_of(r);
+    for (int b0 = 32; b0 < p.batch; b0 += 32) total += units_of(request_of(b0 + lane));
+    if (p.batch > 1) {
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    long long per = (total + p.clusters - 1) / p.clusters;
+        for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    } else {
+        total = __shfl_sync(0xffffffffu, total, 0);
+    }
+    long long per = quotient(total + p.clusters - 1, p.clusters);
     if (per < p.min_tiles) per = p.min_tiles;
     const long long u0 = per * cluster;
-    Work w;
-    w.per = per;
-    w.b = 0;
-    w.rel = 0;
-    w.count = u0 >= total ? 0 : (total - u0 < per ? total - u0 : per);
+    const long long count = u0 >= total ? 0 : (total - u0 < per ? total - u0 : per);
+    if (lane == 0) {
+        out->per = per;
+        out->count = count;
+    }
     long long before = 0;
-    for (int b0 = 0; b0 < p.batch && w.count > 0; b0 += 32) {
-        const long long u = b0 == 0 ? mine : units_of(b0 + lane);
+    for (int b0 = 0; b0 < p.batch && count > 0; b0 += 32) {
+        if (b0 > 0) r = request_of(b0 + lane);
+        const long long u = units_of(r);
         long long incl = u;
+        if (p.batch > 1) {
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
         }
-        const bool here = u0 >= before + incl - u && u0 < before + incl;
-        const uint32_t at = __ballot_sync(0xffffffffu, here);
-        if (at) {
-            const int src = __ffs(at) - 1;
-            w.b = b0 + src;
-            w.rel = u0 - before - __shfl_sync(0xffffffffu, incl - u, src);
-            break;
+        const long long first = before + incl - u;         // this lane's request is units [first, first + u)
+        const bool here = u0 >= first && u0 < first + u;
+        if (here) {
+            const int n_tiles = tiles_of(r);
+            out->rb = static_cast<int>(quotient(u0 - first, n_tiles));
+            out->tile = static_cast<int>(u0 - first - static_cast<long long>(out->rb) * n_tiles);
+            out->b = b0 + lane;
+            out->r = r;
         }
+        if (__any_sync(0xffffffffu, here)) break;
         before += __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (lane == 0) *out = w;
+}
+
+// Bounded wait whose usual case (the phase is over) is one instruction inline.
+__device__ __noinline__ bool wait_slowly(uint64_t* bar, uint32_t parity, int* abort_flag) {
+    return mbar_wait_bounded(bar, parity, abort_flag);
+}
+__device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity) {
+    return mbar_try_wait(bar, parity) || wait_slowly(bar, parity, &sh.abort_flag);
+}
+// The same by a whole warp (every thread polls: with one lane polling for the
+// others each hand-off took longer), with one answer for all of its lanes.
+__device__ __forceinline__ bool warp_wait(Shared& sh, uint64_t* bar, uint32_t parity) {
+    const bool ok = __all_sync(0xffffffffu, wait(sh, bar, parity));
+    tc_fence_after_sync();
+    return ok;
 }
 
 // ============================== producer ==================================
@@ -195,60 +233,62 @@ struct Producer {
     Shared& sh;
     uint32_t rank;
     uint64_t pol_kv, pol_q;
-    uint32_t n = 0;                                        // ring slots filled so far
+    uint32_t slot = 0, round = 0;                          // K ring: next slot, times around
     uint32_t specials = 0;
 
-    __device__ __forceinline__ bool slot_free() {
-        return n < kSlots || mbar_wait_bounded_cluster(&sh.empty[n % kSlots], ((n / kSlots) - 1) & 1, &sh.abort_flag);
+    // The even CTA's barrier of a load; that CTA announces both CTAs' bytes (the odd
+    // CTA's may land first: the phase is open until the announcement arrives).
+    __device__ __forceinline__ uint32_t expect(uint64_t* bar, uint32_t bytes) {
+        if (rank == 0) mbar_arrive_expect_tx(bar, 2 * bytes);
+        return map_to_rank(bar, 0);
     }
     __device__ bool load_q(const Cursor& c) {
-        if (c.item > 0 && !mbar_wait_bounded_cluster(&sh.q_empty, (c.item - 1) & 1, &sh.abort_flag)) return false;
-        const uint32_t bar = map_to_rank(&sh.q_ready, 0);
-        mbar_arrive_expect_tx_cluster(bar, kQBytes);
+        if (c.item > 0 && !mbar_wait_bounded(&sh.q_empty, (c.item - 1) & 1, &sh.abort_flag)) return false;
+        const uint32_t bar = expect(&sh.q_ready, kQBytes);
         const int row = c.b * p.tokens * p.heads + c.rb * kTreeBlockRows + static_cast<int>(rank) * 64;
         tma_load_3d_pair(sh.q, &maps.q, 0, row, 0, bar, pol_q);
         return true;
     }
-    // QK operands: this CTA's 64 keys, 128 columns a slot, then the rope columns
+    // QK operands: this CTA's 64 keys, the rope columns, then 128 columns a slot
     __device__ bool load_k(const Cursor& c) {
         const int y = static_cast<int>(c.r.base) + c.tile * kTreeTileKeys + static_cast<int>(rank) * 64;
+        if (c.g > 0 && !mbar_wait_bounded(&sh.rope_empty, (c.g - 1) & 1, &sh.abort_flag)) return false;
+        tma_load_3d_pair(sh.rope, &maps.rope, 0, y, 8, expect(&sh.rope_ready, kChunkBytes), pol_kv);
 #pragma unroll 1
-        for (int s = 0; s < 4; ++s, ++n) {
-            if (!slot_free()) return false;
-            const uint32_t bar = map_to_rank(&sh.ready[n % kSlots], 0);
-            mbar_arrive_expect_tx_cluster(bar, kSlotBytes);
-            tma_load_3d_pair(sh.ring[n % kSlots], &maps.kv, 0, y, 2 * s, bar, pol_kv);
+        for (int s = 0; s < 4; ++s) {
+            if (round > 0 && !mbar_wait_bounded(&sh.k_empty[slot], (round - 1) & 1, &sh.abort_flag)) return false;
+            const uint32_t bar = expect(&sh.k_ready[slot], kSlotBytes);
+            tma_load_3d_pair(sh.k[slot], &maps.kv, 0, y, 2 * s, bar, pol_kv);
+            if (++slot == kKSlots) {
+                slot = 0;
+                ++round;
+            }
         }
-        if (c.g > 0 && !mbar_wait_bounded_cluster(&sh.rope_empty, (c.g - 1) & 1, &sh.abort_flag)) return false;
-        const uint32_t bar = map_to_rank(&sh.rope_ready, 0);
-        mbar_arrive_expect_tx_cluster(bar, kChunkBytes);
-        tma_load_3d_pair(sh.rope, &maps.rope, 0, y, 8, bar, pol_kv);
         return true;
     }
     // PV operands: features 256 i + 128 rank .. + 127 of the keys of half kb
     __device__ bool load_v(const Cursor& c) {
         const int y = static_cast<int>(c.r.base) + c.tile * kTreeTileKeys;
         const bool special = c.special();
-        // two barriers: V of two such tiles may be staged at once, of three not
-        // (V of tile g + 2 takes the slots of V of tile g)
+        // (two barriers: the bytes of the next such tile are announced here while the
+        // softmax threads may still be waiting for this one's)
         uint64_t* local = &sh.v_local[specials & 1];
         if (special) {
             mbar_arrive_expect_tx(local, 4 * kSlotBytes);
             ++specials;
         }
 #pragma unroll 1
-        for (int s = 0; s < 4; ++s, ++n) {
-            if (!slot_free()) return false;
-            const uint32_t bar = map_to_rank(&sh.ready[n % kSlots], 0);
+        for (int s = 0; s < 4; ++s) {
+            if (c.g > 0 && !mbar_wait_bounded(&sh.v_empty[s], (c.g - 1) & 1, &sh.abort_flag)) return false;
             const int i = s >> 1, kb = s & 1;
             if (special) {
                 // the softmax threads wait for these bytes and vouch for them with P
-                tma_load_3d(sh.ring[n % kSlots], &maps.kv, 0, y + 64 * kb, 4 * i + 2 * static_cast<int>(rank),
+                tma_load_3d(sh.v[s], &maps.kv, 0, y + 64 * kb, 4 * i + 2 * static_cast<int>(rank),
                             local, pol_kv);
-                mbar_arrive_cluster(bar);
+                if (rank == 0) mbar_arrive(&sh.v_ready[s]);
             } else {
-                mbar_arrive_expect_tx_cluster(bar, kSlotBytes);
-                tma_load_3d_pair(sh.ring[n % kSlots], &maps.kv, 0, y + 64 * kb, 4 * i + 2 * static_cast<int>(rank),
+                const uint32_t bar = expect(&sh.v_ready[s], kSlotBytes);
+                tma_load_3d_pair(sh.v[s], &maps.kv, 0, y + 64 * kb, 4 * i + 2 * static_cast<int>(rank),
                                  bar, pol_kv);
             }
         }
@@ -256,106 +296,125 @@ struct Producer {
     }
 };
 
-__device__ void produce(const TreeMaps& maps, const TreeParams& p, Shared& sh, uint32_t rank) {
+// One thread for the query rows and K, one for V: K of a tile is taken before V
+// of the tile before it, so neither waits in the other's queue.
+__device__ void produce(const TreeMaps& maps, const TreeParams& p, Shared& sh, uint32_t rank, bool values) {
     Producer pr{maps, p, sh, rank, l2_policy_evict_normal(), l2_policy_evict_normal()};
     Cursor c;
-    c.start(p, sh.work);
-    if (c.left <= 0) return;
-    bool ok = pr.load_q(c) && pr.load_k(c);
-    while (ok) {
-        Cursor nx = c;
-        const bool more = c.left > 1;
-        if (more) nx.next(p);
-        // the order in which the MMA thread takes them
-        if (more && !nx.first) ok = pr.load_k(nx);
-        ok = ok && pr.load_v(c);
-        if (ok && more && nx.first) ok = pr.load_q(nx) && pr.load_k(nx);
-        if (!more) break;
-        c = nx;
+    bool ok = true;
+    for (c.start(p, sh.work); c.left > 0 && ok; c.next(p)) {
+        if (values)
+            ok = pr.load_v(c);
+        else
+            ok = (!c.first || pr.load_q(c)) && pr.load_k(c);
     }
     if (!ok) raise_error(sh, p.status);
 }
 
 // ============================== MMA issue ==================================
-struct Issuer {
-    const TreeParams& p;
-    Shared& sh;
-    uint32_t tmem;
-    uint64_t ring_k, ring_v, rope, q, pd;
-    uint32_t n = 0;
-
-    __device__ __forceinline__ bool slot_ready() {
-        const bool ok = mbar_wait_bounded_cluster(&sh.ready[n % kSlots], (n / kSlots) & 1, &sh.abort_flag);
-        tc_fence_after_sync();
-        return ok;
-    }
-    __device__ bool qk(const Cursor& c) {
-        constexpr uint32_t idesc = make_idesc_bf16(128, 128, 0, 0);
-        const uint32_t d = tmem + kTmemS + 64 * (c.g & 1);
-        if (c.first && !mbar_wait_bounded_cluster(&sh.q_ready, c.item & 1, &sh.abort_flag)) return false;
-#pragma unroll 1
-        for (int s = 0; s < 4; ++s, ++n) {
-            if (!slot_ready()) return false;
-            const uint64_t kb = ring_k + ((n % kSlots) * kSlotBytes >> 4);
-            const uint64_t qb = q + (2 * s * kChunkBytes >> 4);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const uint32_t off = ((k >> 2) * kChunkBytes + (k & 3) * 32u) >> 4;
-                umma_pair_bf16(d, qb + off, kb + off, idesc, (s | k) ? 1u : 0u);
-            }
-            umma_commit_pair(&sh.empty[n % kSlots]);
-        }
-        if (!mbar_wait_bounded_cluster(&sh.rope_ready, c.g & 1, &sh.abort_flag)) return false;
-        tc_fence_after_sync();
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            umma_pair_bf16(d, q + ((8 * kChunkBytes + k * 32u) >> 4), rope + (k * 32u >> 4), idesc, 1u);
-        umma_commit_pair(&sh.rope_empty);
-        umma_commit_pair(&sh.s_full[c.g & 1]);
-        if (c.last()) umma_commit_pair(&sh.q_empty);
-        return true;
-    }
-    __device__ bool pv(const Cursor& c) {
-        constexpr uint32_t idesc = make_idesc_bf16(128, 256, 0, 1);
-        if (!mbar_wait_bounded_cluster(&sh.p_ready, c.g & 1, &sh.abort_flag)) return false;
-        if (c.first && c.item > 0 && !mbar_wait_bounded_cluster(&sh.o_free, (c.item - 1) & 1, &sh.abort_flag))
-            return false;
-        tc_fence_after_sync();
-#pragma unroll 1
-        for (int s = 0; s < 4; ++s, ++n) {
-            if (!slot_ready()) return false;
-            const uint64_t vb = ring_v + ((n % kSlots) * kSlotBytes >> 4);
-            const uint64_t pb = pd + ((s & 1) * kChunkBytes >> 4);
-            const uint32_t d = tmem + kTmemO + 128 * (s >> 1);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                umma_pair_bf16(d, pb + (k * 32u >> 4), vb + (k * 2048u >> 4), idesc,
-                               (c.first && (s & 1) == 0 && k == 0) ? 0u : 1u);
-            umma_commit_pair(&sh.empty[n % kSlots]);
-        }
-        umma_commit_pair(&sh.o_done);
-        return true;
-    }
-};
-
+// One warp issues everything: the tensor pipe takes the MMAs in order, and QK and
+// PV interleaved from two warps ran at half the rate.  Its queue is short, so what
+// the warp does between two MMAs costs tensor time: the waits are on barriers of
+// its own CTA that completed long ago (P is two tiles behind: the order is QK(g),
+// PV(g - 2)), and all that crosses CTAs goes through the relay warp.  The whole
+// warp walks the tiles and waits, one lane issues (with a single thread doing all
+// of it an MMA took 100 cycles to issue, now about 36).
 __device__ void issue(const TreeParams& p, Shared& sh, uint32_t tmem) {
-    Issuer is{p, sh, tmem, make_sdesc(smem_u32(sh.ring), 16, 1024, kLayoutSw128),
-              make_sdesc(smem_u32(sh.ring), kChunkBytes, 1024, kLayoutSw128),
-              make_sdesc(smem_u32(sh.rope), 16, 1024, kLayoutSw128), make_sdesc(smem_u32(sh.q), 16, 1024, kLayoutSw128),
-              make_sdesc(smem_u32(sh.p), 16, 1024, kLayoutSw128)};
+    constexpr uint32_t idesc_qk = make_idesc_bf16(128, 128, 0, 0);
+    constexpr uint32_t idesc_pv = make_idesc_bf16(128, 256, 0, 1);
+    const bool lead = elect_one();
+    const uint64_t kd = make_sdesc(smem_u32(sh.k), 16, 1024, kLayoutSw128);
+    const uint64_t vd = make_sdesc(smem_u32(sh.v), kChunkBytes, 1024, kLayoutSw128);
+    const uint64_t rope = make_sdesc(smem_u32(sh.rope), 16, 1024, kLayoutSw128);
+    const uint64_t q = make_sdesc(smem_u32(sh.q), 16, 1024, kLayoutSw128);
+    const uint64_t pd = make_sdesc(smem_u32(sh.p), 16, 1024, kLayoutSw128);
+    uint32_t slot = 0, round = 0;                          // K ring
+    uint32_t firsts = 0;                                   // bit i: the tile i QKs ago was the first of its item
+    int pv_item = -1;
+    bool ok = true;
     Cursor c;
     c.start(p, sh.work);
-    if (c.left <= 0) return;
-    bool ok = is.qk(c);
-    while (ok) {
-        Cursor nx = c;
-        const bool more = c.left > 1;
-        if (more) nx.next(p);
-        if (more && !nx.first) ok = is.qk(nx);
-        ok = ok && is.pv(c);
-        if (ok && more && nx.first) ok = is.qk(nx);
-        if (!more) break;
-        c = nx;
+    const int total = c.left;
+    for (int g = 0; g < total + 2 && ok; ++g) {
+        const int buf = g & 1;
+        firsts <<= 1;
+        if (g < total) {
+            const uint32_t d = tmem + kTmemS + 64 * buf;
+            const bool last = c.last();
+            firsts |= c.first ? 1u : 0u;
+            if (c.first) ok = warp_wait(sh, &sh.q_ready, c.item & 1);
+            // both CTAs have read the scores of tile g - 2
+            if (g >= 2) ok = ok && warp_wait(sh, &sh.s_free[buf], ((g >> 1) - 1) & 1);
+            ok = ok && warp_wait(sh, &sh.rope_ready, g & 1);
+            if (lead && ok) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    umma_pair_bf16(d, q + ((8 * kChunkBytes + k * 32u) >> 4), rope + (k * 32u >> 4), idesc_qk,
+                                   k ? 1u : 0u);
+                umma_commit_pair(&sh.rope_empty);
+            }
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                ok = ok && warp_wait(sh, &sh.k_ready[slot], round & 1);
+                if (lead && ok) {
+                    const uint64_t kb = kd + (slot * kSlotBytes >> 4);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const uint32_t off = ((k >> 2) * kChunkBytes + (k & 3) * 32u) >> 4;
+                        umma_pair_bf16(d, q + (2 * s * kChunkBytes >> 4) + off, kb + off, idesc_qk, 1u);
+                    }
+                    umma_commit_pair(&sh.k_empty[slot]);
+                }
+                if (++slot == kKSlots) {
+                    slot = 0;
+                    ++round;
+                }
+            }
+            if (lead && ok) {
+                umma_commit_pair(&sh.s_full[buf]);
+                if (last) umma_commit_pair(&sh.q_empty);
+            }
+            c.next(p);
+        }
+        if (g >= 2) {
+            const uint32_t first = firsts >> 2 & 1u;
+            ok = ok && warp_wait(sh, &sh.p_ready[buf], ((g >> 1) - 1) & 1);
+            if (first && ++pv_item > 0) ok = ok && warp_wait(sh, &sh.o_free, (pv_item - 1) & 1);
+            const uint64_t pb = pd + (buf * 2 * kChunkBytes >> 4);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                ok = ok && warp_wait(sh, &sh.v_ready[s], g & 1);
+                if (lead && ok) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        umma_pair_bf16(tmem + kTmemO + 128 * (s >> 1), pb + (((s & 1) * kChunkBytes + k * 32u) >> 4),
+                                       vd + ((s * kSlotBytes + k * 2048u) >> 4), idesc_pv,
+                                       (s & 1) == 0 && k == 0 ? first ^ 1u : 1u);
+                    umma_commit_pair(&sh.v_empty[s]);
+                }
+            }
+            if (lead && ok) umma_commit_pair(&sh.o_done[buf]);
+        }
+    }
+    if (!ok && lead) raise_error(sh, p.status);
+}
+
+// Carries "P of the tile is written" to the MMA warp, one thread in each CTA:
+// a release that the other CTA sees takes about 1000 cycles, which neither the
+// softmax threads nor the MMA warp should spend.
+__device__ void relay(const TreeParams& p, Shared& sh, uint32_t rank) {
+    const int total = static_cast<int>(sh.work.count);
+    const uint32_t peer = map_to_rank(&sh.p_peer[0], 0);
+    bool ok = true;
+    for (int g = 0; g < total && ok; ++g) {
+        const int buf = g & 1;
+        ok = wait(sh, &sh.p_local[buf], (g >> 1) & 1);
+        if (rank != 0) {
+            if (ok) mbar_arrive_cluster(peer + 8 * buf);
+        } else {
+            ok = ok && mbar_wait_bounded_cluster(&sh.p_peer[buf], (g >> 1) & 1, &sh.abort_flag);
+            if (ok) mbar_arrive(&sh.p_ready[buf]);
+        }
     }
     if (!ok) raise_error(sh, p.status);
 }
@@ -366,15 +425,15 @@ __device__ __forceinline__ bool has_nonfinite(uint32_t w) {
 }
 
 // Clear what must not meet P = 0 in the staged V of a tile: rows behind the
-// end, and non-finite values of drafted rows.  Slots n0 .. n0 + 3 of the ring.
-__device__ void clean_v(Shared& sh, const Cursor& c, uint32_t n0, int tid) {
+// end, and non-finite values of drafted rows.
+__device__ void clean_v(Shared& sh, const Cursor& c, int tid) {
     const int t0 = c.tile * kTreeTileKeys;
     const int from = max(0, c.r.d_pos - t0);
     const int end = min(kTreeTileKeys, c.r.d_pos + c.r.n_tok - t0);   // rows from here on are behind the drafts
     // unit w of a row: 2 feature halves x 2 chunks x 8 units of 16 bytes
     for (int e = tid; e < (kTreeTileKeys - from) * 32; e += kSoftmaxThreads) {
         const int key = from + (e >> 5), w = e & 31;
-        uint8_t* slot = sh.ring[(n0 + 2 * (w >> 4) + (key >> 6)) % kSlots];
+        uint8_t* slot = sh.v[2 * (w >> 4) + (key >> 6)];
         uint4* at = reinterpret_cast<uint4*>(slot + ((w >> 3) & 1) * kChunkBytes + (key & 63) * 128 +
                                              (((w & 7) ^ (key & 7)) << 4));
         if (key >= end) {
@@ -394,37 +453,51 @@ __device__ void clean_v(Shared& sh, const Cursor& c, uint32_t n0, int tid) {
     }
 }
 
-// out[0 .. 127] of a row's feature run, in the output's type
-__device__ __forceinline__ void store32(const TreeParams& p, bool whole, long long at, const uint32_t (&o)[32],
-                                        float inv, float* part) {
-    if (!whole || p.a.out_fp32) {
-        float4* dst = reinterpret_cast<float4*>((whole ? static_cast<float*>(p.a.out) : part) + at);
+// 32 features of a warp's 32 rows, through its 4 KB of shared memory so that
+// the stores of a row run along its features (16-byte units, swizzled by row:
+// 128 bytes per row in fp32, 64 in bf16).  `dst`: row 0's first feature,
+// rows 512 elements apart; rows at or past n_rows are not written.
+template <bool kBf16>
+__device__ __forceinline__ void store_rows(uint32_t stage, const uint32_t (&o)[32], float inv, void* dst, int n_rows,
+                                           int lane) {
+    constexpr int kUnits = kBf16 ? 4 : 8;                  // 16-byte units per row
+    __syncwarp();                                          // the reads of the block before are done
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            dst[i] = make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
-                                 __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
-    } else {
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.a.out) + at);
+    for (int u = 0; u < kUnits; ++u) {
+        uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                w[j] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * j]) * inv, __uint_as_float(o[8 * i + 2 * j + 1]) * inv);
-            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            if constexpr (kBf16)
+                w[i] = pack_bf16x2(__uint_as_float(o[8 * u + 2 * i]) * inv, __uint_as_float(o[8 * u + 2 * i + 1]) * inv);
+            else
+                w[i] = __float_as_uint(__uint_as_float(o[4 * u + i]) * inv);
         }
+        st_shared_v4(stage + lane * 128 + ((u ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+    }
+    __syncwarp();
+    constexpr int kRows = 32 / kUnits;                     // rows a warp stores at a time
+    const int u = lane % kUnits;
+#pragma unroll
+    for (int i = 0; i < 32 / kRows; ++i) {
+        const int row = i * kRows + lane / kUnits;
+        const uint4 v = ld_shared_v4(stage + row * 128 + ((u ^ (row & 7)) << 4));
+        if (row < n_rows)
+            reinterpret_cast<uint4*>(static_cast<char*>(dst) + static_cast<long long>(row) * kDLatent * (kBf16 ? 2 : 4))[u] = v;
     }
 }
 
+// Thread: 32 keys of one row.  Warps w and w + 4 share tensor-memory lanes 32 (w mod 4) ..
+// and split their columns.
 __device__ void softmax(const TreeParams& p, Shared& sh, uint32_t tmem, uint32_t rank, int cluster, int tid) {
     const int lane = tid & 31, warp = tid >> 5;
-    const int row = tid & 63, half = tid >> 6;
-    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-    const uint32_t p_bar = map_to_rank(&sh.p_ready, 0), o_bar = map_to_rank(&sh.o_free, 0);
-    const uint32_t p_line = smem_u32(sh.p[half]) + row * 128;
+    const int sub = warp >> 2, half = (warp >> 1) & 1;     // keys 64 half + 32 sub ..; features 256 sub + 128 half ..
+    const int quarter = 2 * half + sub;
+    const int row = 32 * (warp & 1) + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_bar = map_to_rank(&sh.s_free[0], 0), o_bar = map_to_rank(&sh.o_free, 0);
+    const uint32_t p_line = smem_u32(sh.p[0][half]) + row * 128;
     const float c2 = p.scale_log2;
     TreeMerge merge{0, 0, 0, 0};
-    uint32_t n_v = 4;                                      // ring number of the tile's first V slot, see below
     uint32_t specials = 0;
     bool ok = true, bad = false;
     Cursor c;
@@ -441,126 +514,115 @@ __device__ void softmax(const TreeParams& p, Shared& sh, uint32_t tmem, uint32_t
         do {
             const int g = c.g, buf = g & 1;
             last = c.last();
-            bool w = mbar_wait_bounded_cluster(&sh.s_full[buf], (g >> 1) & 1, &sh.abort_flag);
-            w = __all_sync(0xffffffffu, w);
-            tc_fence_after_sync();
-            uint32_t s[2][32];
+            bool w = warp_wait(sh, &sh.s_full[buf], (g >> 1) & 1);
+            uint32_t s[32];
             if (w) {
-                tmem_ld32_async(tmem + lanes + kTmemS + 64 * buf, s[0]);
-                tmem_ld32_async(tmem + lanes + kTmemS + 64 * buf + 32, s[1]);
-                tmem_wait_ld32(s[0]);
-                tmem_wait_ld32(s[1]);
+                tmem_ld32_async(tmem + lanes + kTmemS + 64 * buf + 32 * sub, s);
+                tmem_wait_ld32(s);
             } else {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) s[0][i] = s[1][i] = 0;
+                for (int i = 0; i < 32; ++i) s[i] = 0;
             }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_relaxed(s_bar + 8 * buf);   // the score buffer is free
             const int t0 = c.tile * kTreeTileKeys;
             if (t0 + kTreeTileKeys > c.r.d_pos || t0 < c.r.lo || t0 + kTreeTileKeys > c.r.hi) {
-                const unsigned long long v = visible64(c.r, mask, t0 + 64 * half);
+                const uint32_t v = static_cast<uint32_t>(visible64(c.r, mask, t0 + 64 * half) >> (32 * sub));
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    if (!(v >> i & 1)) s[0][i] = 0xff800000u;
-                    if (!(v >> (i + 32) & 1)) s[1][i] = 0xff800000u;
-                }
+                for (int i = 0; i < 32; ++i)
+                    if (!(v >> i & 1)) s[i] = 0xff800000u;
             }
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                mx[i & 1] = fmaxf(mx[i & 1], __uint_as_float(s[0][i]));
-                mx[2 + (i & 1)] = fmaxf(mx[2 + (i & 1)], __uint_as_float(s[1][i]));
-            }
+            for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i]));
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;
             float alpha = 1.f;
             bad |= !w;
             if (named_barrier_or(kBarSoftmax, kSoftmaxThreads, bad || top > m_ref + kRescaleLog2)) {
                 // rare after the first tile: the row's maximum moves the reference
-                sh.red_max[tid] = top;
+                sh.red_max[quarter][row] = top;
                 if (named_barrier_or(kBarSoftmax, kSoftmaxThreads, bad)) {
                     ok = false;
                     break;
                 }
-                const float tm = fmaxf(top, sh.red_max[tid ^ 64]);
+                const float tm = fmaxf(fmaxf(sh.red_max[0][row], sh.red_max[1][row]),
+                                       fmaxf(sh.red_max[2][row], sh.red_max[3][row]));
                 if (tm > m_ref + kRescaleLog2) {
                     if (m_ref > -INFINITY) alpha = ex2_approx(m_ref - tm);
                     m_ref = tm;
                 }
                 l *= alpha;
             }
-            // P of the tile before has been read, O holds all tiles before
-            w = g == 0 || mbar_wait_bounded_cluster(&sh.o_done, (g - 1) & 1, &sh.abort_flag);
-            w = __all_sync(0xffffffffu, w);
-            if (w && __any_sync(0xffffffffu, alpha != 1.f)) {
-                // O of this item (tiles before this one; alpha is 1 on the first)
-                tc_fence_after_sync();
-#pragma unroll 1
-                for (int j = 0; j < 16; ++j) {
-                    float o[16];
-                    tmem_ld16(tmem + lanes + kTmemO + 16 * j, o);
+            const float base = m_ref > -INFINITY ? m_ref : 0.f;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            uint32_t pk[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) o[i] *= alpha;
-                    tmem_st16(tmem + lanes + kTmemO + 16 * j, o);
+            for (int i = 0; i < 16; ++i) {
+                const float x = ex2_approx(fmaf(__uint_as_float(s[2 * i]), c2, -base));
+                const float y = ex2_approx(fmaf(__uint_as_float(s[2 * i + 1]), c2, -base));
+                sum[i & 1] += x;
+                sum[2 + (i & 1)] += y;
+                pk[i] = pack_bf16x2(x, y);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            // this P buffer has been read (PV of tile g - 2)
+            w = g < 2 || warp_wait(sh, &sh.o_done[buf], ((g >> 1) - 1) & 1);
+            if (__any_sync(0xffffffffu, alpha != 1.f)) {
+                // (never on an item's first tile) O holds all tiles before this one
+                w = w && warp_wait(sh, &sh.o_done[buf ^ 1], ((g - 1) >> 1) & 1);
+                if (w) {
+#pragma unroll 1
+                    for (int j = 0; j < 8; ++j) {
+                        float o[16];
+                        const uint32_t at = tmem + lanes + kTmemO + 128 * sub + 16 * j;
+                        tmem_ld16(at, o);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[i] *= alpha;
+                        tmem_st16(at, o);
+                    }
                 }
             }
             // ---- probabilities, bf16, K-major lines of 64 keys
-            const float base = m_ref > -INFINITY ? m_ref : 0.f;
-            float sum[2] = {0.f, 0.f};
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    uint32_t pk[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float x = ex2_approx(fmaf(__uint_as_float(s[h][8 * u + 2 * i]), c2, -base));
-                        const float y = ex2_approx(fmaf(__uint_as_float(s[h][8 * u + 2 * i + 1]), c2, -base));
-                        sum[0] += x;
-                        sum[1] += y;
-                        pk[i] = pack_bf16x2(x, y);
-                    }
-                    st_shared_v4(p_line + (((4 * h + u) ^ (row & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
-                }
-            l += sum[0] + sum[1];
+            for (int u = 0; u < 4; ++u)
+                st_shared_v4(p_line + buf * 2 * kChunkBytes + (((4 * sub + u) ^ (row & 7)) << 4), pk[4 * u],
+                             pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
             if (c.special()) {
-                // this tile's V was loaded for this CTA's own eyes: its ring slots
-                // follow the next tile's K slots unless the item ends here
-                const uint32_t n0 = n_v + (last ? 0u : 4u);
-                bool v = w && mbar_wait_bounded(&sh.v_local[specials & 1], (specials >> 1) & 1, &sh.abort_flag);
+                // V was loaded for this CTA's own eyes
+                w = w && warp_wait(sh, &sh.v_local[specials & 1], (specials >> 1) & 1);
                 ++specials;
-                if (__all_sync(0xffffffffu, v))
-                    clean_v(sh, c, n0, tid);
-                else
-                    w = false;
+                if (w) clean_v(sh, c, tid);
             }
-            fence_proxy_async_all();
+            fence_proxy_async_smem();
             tc_fence_before_sync();
             __syncwarp();
             bad |= !w;                                     // the threads leave together at the next barrier
-            if (lane == 0 && !bad) mbar_arrive_cluster(p_bar);
+            if (lane == 0 && !bad) mbar_arrive(&sh.p_local[buf]);
             ++done;
-            n_v += 8;
             c.next(p);
         } while (!last);
         if (!ok) break;
 
-        // ---- epilogue: l of both halves, O / l, log-sum-exp
-        sh.red_sum[tid] = l;
+        // ---- epilogue: l of the four quarters, O / l, log-sum-exp
+        sh.red_sum[quarter][row] = l;
         if (named_barrier_or(kBarSoftmax, kSoftmaxThreads, bad)) {
             ok = false;
             break;
         }
-        const float lt = half == 0 ? l + sh.red_sum[tid ^ 64] : sh.red_sum[tid ^ 64] + l;
+        const float lt = (sh.red_sum[0][row] + sh.red_sum[1][row]) + (sh.red_sum[2][row] + sh.red_sum[3][row]);
         const float inv = lt == 0.f ? 0.f : 1.f / lt;
         const float lse2 = lt == 0.f ? -INFINITY : m_ref + log2f(lt);
         const bool whole = tile0 == 0 && done == n_tiles;
         const int slot = 2 * cluster + (tile0 == 0 ? 1 : 0);
-        const int block_row = static_cast<int>(rank) * 64 + row;
-        const long long out_row =
-            whole ? static_cast<long long>(b) * p.tokens * p.heads + r : static_cast<long long>(slot) * kTreeBlockRows + block_row;
-        if (half == 0 && r < live_rows) {
+        // row 0 of this CTA's 64 in the output, or in the piece
+        const long long row0 = whole ? static_cast<long long>(b) * p.tokens * p.heads + r - row
+                                     : static_cast<long long>(slot) * kTreeBlockRows + static_cast<int>(rank) * 64;
+        if (quarter == 0 && r < live_rows) {
             if (whole)
-                p.a.lse[out_row] = lse2 * kLn2;
+                p.a.lse[row0 + row] = lse2 * kLn2;
             else
-                p.lse_part[out_row] = lse2;
+                p.lse_part[row0 + row] = lse2;
         }
         if (!whole && tile0 == 0) {
             merge.b = b;
@@ -568,20 +630,28 @@ __device__ void softmax(const TreeParams& p, Shared& sh, uint32_t tmem, uint32_t
             merge.rows = min(kTreeBlockRows, live_rows - rb * kTreeBlockRows);
             merge.pieces = 1 + static_cast<int>((n_tiles - done + sh.work.per - 1) / sh.work.per);
         }
-        bool w = mbar_wait_bounded_cluster(&sh.o_done, (c.g - 1) & 1, &sh.abort_flag);
-        w = __all_sync(0xffffffffu, w);
+        const int gl = c.g - 1;
+        const bool w = warp_wait(sh, &sh.o_done[gl & 1], (gl >> 1) & 1);
         if (named_barrier_or(kBarSoftmax, kSoftmaxThreads, !w)) {
             ok = false;
             break;
         }
-        tc_fence_after_sync();
+        // (P's buffers are free: the last product is done)
+        const uint32_t stage = smem_u32(sh.p) + warp * 4096;
+        const int row_w = 32 * (warp & 1);                 // this warp's first row of the 64
+        const int n_rows = live_rows - (r - row) - row_w;
 #pragma unroll 1
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 4; ++j) {
             uint32_t o[32];
-            tmem_ld32_async(tmem + lanes + kTmemO + 32 * j, o);
+            tmem_ld32_async(tmem + lanes + kTmemO + 128 * sub + 32 * j, o);
             tmem_wait_ld32(o);
-            const int feature = 256 * (j >> 2) + 128 * half + 32 * (j & 3);
-            if (r < live_rows) store32(p, whole, out_row * kDLatent + feature, o, inv, p.part);
+            const long long at = (row0 + row_w) * kDLatent + 256 * sub + 128 * half + 32 * j;
+            if (!whole)
+                store_rows<false>(stage, o, inv, p.part + at, n_rows, lane);
+            else if (p.a.out_fp32)
+                store_rows<false>(stage, o, inv, static_cast<float*>(p.a.out) + at, n_rows, lane);
+            else
+                store_rows<true>(stage, o, inv, static_cast<uint16_t*>(p.a.out) + at, n_rows, lane);
         }
         tc_fence_before_sync();
         __syncwarp();
@@ -591,25 +661,24 @@ __device__ void softmax(const TreeParams& p, Shared& sh, uint32_t tmem, uint32_t
     if (rank == 0 && tid == 0) p.merge[cluster] = merge;
 }
 
-// Requests without rows: their tokens' outputs, by the softmax threads of all CTAs.
-__device__ void write_empty(const TreeParams& p, int cta, int ctas, int tid) {
-    for (int b = cta; b < p.batch; b += ctas) {
+// Requests without rows: their tokens' outputs, by the odd CTAs' otherwise idle warp.
+__device__ void write_empty(const TreeParams& p, int cluster, int clusters, int lane) {
+    for (int b = cluster; b < p.batch; b += clusters) {
         const TreeRequest r = load_tree_request(p, b);
         if (r.hi > 0 || r.n_tok == 0) continue;
         const long long row0 = static_cast<long long>(b) * p.tokens * p.heads;
         const int rows = r.n_tok * p.heads;
-        for (int i = tid; i < rows; i += kSoftmaxThreads) p.a.lse[row0 + i] = -INFINITY;
+        for (int i = lane; i < rows; i += 32) p.a.lse[row0 + i] = -INFINITY;
         const int per = p.a.out_fp32 ? 128 : 64;           // 16-byte units per row
         uint4* o = reinterpret_cast<uint4*>(p.a.out) + row0 * per;
-        for (int i = tid; i < rows * per; i += kSoftmaxThreads) o[i] = make_uint4(0, 0, 0, 0);
+        for (int i = lane; i < rows * per; i += 32) o[i] = make_uint4(0, 0, 0, 0);
     }
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mla_tree_attend_kernel(const __grid_constant__ TreeMaps maps, const __grid_constant__ TreeParams p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    Shared& sh = *reinterpret_cast<Shared*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                            ~static_cast<uintptr_t>(1023));
+    Shared& sh = *reinterpret_cast<Shared*>(smem_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_ctarank();
     const int cluster = blockIdx.x >> 1;
@@ -617,32 +686,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         prefetch_tensormap(&maps.kv);
         prefetch_tensormap(&maps.rope);
         prefetch_tensormap(&maps.q);
-        for (int i = 0; i < kSlots; ++i) {
-            mbar_init(&sh.ready[i], 2);
-            mbar_init(&sh.empty[i], 1);
+        for (int i = 0; i < kKSlots; ++i) {
+            mbar_init(&sh.k_ready[i], 1);
+            mbar_init(&sh.k_empty[i], 1);
         }
-        mbar_init(&sh.rope_ready, 2);
-        mbar_init(&sh.q_ready, 2);
-        mbar_init(&sh.p_ready, 8);
-        mbar_init(&sh.o_free, 8);
+        for (int i = 0; i < kVSlots; ++i) {
+            mbar_init(&sh.v_ready[i], 1);
+            mbar_init(&sh.v_empty[i], 1);
+        }
+        mbar_init(&sh.rope_ready, 1);
+        mbar_init(&sh.q_ready, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.s_free[i], 2 * kSoftmaxWarps);
+            mbar_init(&sh.p_local[i], kSoftmaxWarps);
+            mbar_init(&sh.p_peer[i], 1);
+            mbar_init(&sh.p_ready[i], 1);
+        }
+        mbar_init(&sh.o_free, 2 * kSoftmaxWarps);
         mbar_init(&sh.rope_empty, 1);
         mbar_init(&sh.q_empty, 1);
         mbar_init(&sh.s_full[0], 1);
         mbar_init(&sh.s_full[1], 1);
-        mbar_init(&sh.o_done, 1);
+        mbar_init(&sh.o_done[0], 1);
+        mbar_init(&sh.o_done[1], 1);
         mbar_init(&sh.v_local[0], 1);
         mbar_init(&sh.v_local[1], 1);
         mbar_init(&sh.stall_bar, 1);
         sh.abort_flag = 0;
         mbar_init_fence();
     }
+    __syncwarp();
+    cluster_arrive();                                      // (after this thread's barrier initialisation)
     if (warp == kMmaWarp) tmem_alloc_pair(&sh.tmem_base, kTmemCols);
     grid_dependency_wait();
     allow_dependent_launch();
     if (warp == kProducerWarp) find_work(p, cluster, lane, &sh.work);
     tc_fence_before_sync();
     __syncthreads();
-    cluster_barrier();                                     // both CTAs' barriers are initialised
+    cluster_wait();                                        // both CTAs' barriers are initialised
     tc_fence_after_sync();
     const uint32_t tmem = sh.tmem_base;
     if (p.stall_test && blockIdx.x == 0 && tid == 32 * kProducerWarp) {
@@ -650,13 +731,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         volatile int never = 0;
         if (!mbar_wait_bounded(&sh.stall_bar, 0, &never, kStallTestCycles)) raise_error(sh, p.status);
     }
+    // the dynamic window starts 1024-byte aligned (the 128-byte swizzle needs it)
+    if ((smem_u32(smem_raw) & 1023u) != 0 && tid == 0) raise_error(sh, p.status);
     if (warp == kProducerWarp) {
-        if (lane == 0) produce(maps, p, sh, rank);
+        if (lane == 0) produce(maps, p, sh, rank, false);
+    } else if (warp == kValueWarp) {
+        if (lane == 0) produce(maps, p, sh, rank, true);
+    } else if (warp == kRelayWarp) {
+        if (lane == 0) relay(p, sh, rank);
     } else if (warp == kMmaWarp) {
-        if (rank == 0 && lane == 0) issue(p, sh, tmem);
+        if (rank == 0)
+            issue(p, sh, tmem);
+        else
+            write_empty(p, cluster, p.clusters, lane);
     } else {
         softmax(p, sh, tmem, rank, cluster, tid);
-        write_empty(p, blockIdx.x, gridDim.x, tid);
     }
     __syncthreads();
     if (*static_cast<volatile int*>(&sh.abort_flag)) {
@@ -674,62 +763,160 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // ============================== merge ======================================
-// A warp per row: weights exp2(lse_i - lse) of the pieces, ascending.
-constexpr int kMergeThreads = 256;
-constexpr int kMergeRows = kMergeThreads / 32;
+// Out of the clusters' notes, block x takes the x-th row block that clusters
+// share, block y a few of its rows.  Groups of 128 threads (a float4 of the 512
+// features each): up to kFewPieces pieces a group per row, all pieces in order;
+// with more, the pieces of a row are dealt to the four groups and the four sums
+// added in order.  Pieces are weighted by exp2(lse_i - max).
+constexpr int kMergeThreads = 512;
+constexpr int kMergeGroups = kMergeThreads / 128;
+constexpr int kFewPieces = 8;
+constexpr int kMaxPieces = 1024;                           // as many clusters
 
-__global__ void __launch_bounds__(kMergeThreads) mla_tree_merge_kernel(const __grid_constant__ TreeParams p) {
-    grid_dependency_wait();
-    allow_dependent_launch();
-    const int c0 = blockIdx.x;
-    const TreeMerge m = p.merge[c0];
-    const int lane = threadIdx.x & 31;
-    const int row = blockIdx.y * kMergeRows + (threadIdx.x >> 5);
-    if (m.pieces == 0 || row >= m.rows) return;
-    // piece 0 is the owner's second slot, the others are the first slots of the clusters behind it
-    auto slot = [&](int i) { return static_cast<long long>(2 * (c0 + i) + (i == 0 ? 1 : 0)) * kTreeBlockRows + row; };
-    float top = -INFINITY;
-    for (int i = lane; i < m.pieces; i += 32) top = fmaxf(top, p.lse_part[slot(i)]);
-    top = warp_max_f32(top);
-    const float base = top > -INFINITY ? top : 0.f;
-    float sum = 0.f;
-    float4 acc[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = 0; i < m.pieces; ++i) {
-        const long long s = slot(i);
-        const float w = exp2f(p.lse_part[s] - base);       // NaN stays NaN
-        const float4* src = reinterpret_cast<const float4*>(p.part + s * kDLatent);
-        sum += w;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float4 v = src[lane + 32 * j];
-            acc[j].x = fmaf(w, v.x, acc[j].x);
-            acc[j].y = fmaf(w, v.y, acc[j].y);
-            acc[j].z = fmaf(w, v.z, acc[j].z);
-            acc[j].w = fmaf(w, v.w, acc[j].w);
-        }
-    }
+struct MergeShared {
+    float weight[kMaxPieces];
+    float4 sums[kMergeGroups][128];
+    int owner;
+    float base, sum;
+};
+
+// Piece i of a row: the owner's second slot, then the first slots of the clusters behind it.
+__device__ __forceinline__ long long piece_row(int c0, int i, int row) {
+    return static_cast<long long>(2 * (c0 + i) + (i == 0 ? 1 : 0)) * kTreeBlockRows + row;
+}
+__device__ __forceinline__ void add_scaled(float4& acc, float w, const float4 v) {
+    acc.x = fmaf(w, v.x, acc.x);
+    acc.y = fmaf(w, v.y, acc.y);
+    acc.z = fmaf(w, v.z, acc.z);
+    acc.w = fmaf(w, v.w, acc.w);
+}
+__device__ __forceinline__ void write_merged(const TreeParams& p, const TreeMerge& m, int row, int t, float4 acc,
+                                             float base, float sum) {
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const long long out_row =
         static_cast<long long>(m.b) * p.tokens * p.heads + static_cast<long long>(m.rb) * kTreeBlockRows + row;
-    if (lane == 0) p.a.lse[out_row] = sum == 0.f ? -INFINITY : (base + log2f(sum)) * kLn2;
+    if (t == 0) p.a.lse[out_row] = sum == 0.f ? -INFINITY : (base + log2f(sum)) * kLn2;
+    const float4 v = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    const long long at = out_row * kDLatent + 4 * t;
+    if (p.a.out_fp32)
+        *reinterpret_cast<float4*>(static_cast<float*>(p.a.out) + at) = v;
+    else
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.a.out) + at) =
+            make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+}
+
+__device__ void merge_few(const TreeParams& p, int c0, const TreeMerge& m, int row, int t) {
+    const float4* part = reinterpret_cast<const float4*>(p.part);
+    float l[kFewPieces];
+    float4 v[kFewPieces];
+    float top = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float4 v = make_float4(acc[j].x * inv, acc[j].y * inv, acc[j].z * inv, acc[j].w * inv);
-        const long long at = out_row * kDLatent + 4 * (lane + 32 * j);
-        if (p.a.out_fp32)
-            *reinterpret_cast<float4*>(static_cast<float*>(p.a.out) + at) = v;
-        else
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.a.out) + at) =
-                make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+    for (int i = 0; i < kFewPieces; ++i)
+        if (i < m.pieces) {
+            l[i] = p.lse_part[piece_row(c0, i, row)];
+            v[i] = part[piece_row(c0, i, row) * 128 + t];
+            top = fmaxf(top, l[i]);
+        }
+    const float base = top > -INFINITY ? top : 0.f;
+    float sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kFewPieces; ++i)
+        if (i < m.pieces) {
+            const float w = exp2f(l[i] - base);            // NaN stays NaN
+            sum += w;
+            add_scaled(acc, w, v[i]);
+        }
+    write_merged(p, m, row, t, acc, base, sum);
+}
+
+// All threads of the block.
+__device__ void merge_many(const TreeParams& p, int c0, const TreeMerge& m, int row, MergeShared& sh) {
+    const float4* part = reinterpret_cast<const float4*>(p.part);
+    const int group = threadIdx.x >> 7, t = threadIdx.x & 127, lane = threadIdx.x & 31;
+    if (threadIdx.x < 32) {
+        float top = -INFINITY;
+        for (int i = lane; i < m.pieces; i += 32) {
+            const float l = p.lse_part[piece_row(c0, i, row)];
+            sh.weight[i] = l;
+            top = fmaxf(top, l);
+        }
+        top = warp_max_f32(top);
+        const float b = top > -INFINITY ? top : 0.f;
+        float s = 0.f;
+        for (int i = lane; i < m.pieces; i += 32) {
+            const float w = exp2f(sh.weight[i] - b);
+            sh.weight[i] = w;
+            s += w;
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == 0) {
+            sh.base = b;
+            sh.sum = s;
+        }
+    }
+    __syncthreads();
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = group; i0 < m.pieces; i0 += 8 * kMergeGroups) {
+        float4 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (i0 + k * kMergeGroups < m.pieces) v[k] = part[piece_row(c0, i0 + k * kMergeGroups, row) * 128 + t];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (i0 + k * kMergeGroups < m.pieces) add_scaled(acc, sh.weight[i0 + k * kMergeGroups], v[k]);
+    }
+    sh.sums[group][t] = acc;
+    __syncthreads();
+    if (group == 0) {
+#pragma unroll
+        for (int k = 1; k < kMergeGroups; ++k) {
+            const float4 v = sh.sums[k][t];
+            acc = make_float4(acc.x + v.x, acc.y + v.y, acc.z + v.z, acc.w + v.w);
+        }
+        write_merged(p, m, row, t, acc, sh.base, sh.sum);
+    }
+}
+
+__global__ void __launch_bounds__(kMergeThreads) mla_tree_merge_kernel(const __grid_constant__ TreeParams p,
+                                                                       int rows_per_block) {
+    __shared__ MergeShared sh;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int group = tid >> 7, t = tid & 127;
+    grid_dependency_wait();
+    allow_dependent_launch();
+    if (tid < 32) {
+        int seen = 0, found = -1;
+        for (int c = 0; c < p.clusters && found < 0; c += 32) {
+            const bool has = c + lane < p.clusters && p.merge[c + lane].pieces > 0;
+            const uint32_t bal = __ballot_sync(0xffffffffu, has);
+            if (seen + __popc(bal) > static_cast<int>(blockIdx.x)) {
+                const bool mine = has && seen + __popc(bal & ((1u << lane) - 1u)) == static_cast<int>(blockIdx.x);
+                found = c + __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+            }
+            seen += __popc(bal);
+        }
+        if (lane == 0) sh.owner = found;
+    }
+    __syncthreads();
+    const int c0 = sh.owner;
+    if (c0 < 0) return;
+    const TreeMerge m = p.merge[c0];
+    const int row0 = static_cast<int>(blockIdx.y) * rows_per_block;
+    if (m.pieces <= kFewPieces) {
+        if (group < rows_per_block && row0 + group < m.rows) merge_few(p, c0, m, row0 + group, t);
+    } else {
+        for (int row = row0; row < min(row0 + rows_per_block, m.rows); ++row) {
+            merge_many(p, c0, m, row, sh);
+            __syncthreads();
+        }
     }
 }
 
 }  // namespace
 
-size_t tree_attend_smem_bytes() { return sizeof(Shared) + 1024; }
+size_t tree_attend_smem_bytes() { return sizeof(Shared); }
 
 cudaError_t tree_attend_prepare() {
     return cudaFuncSetAttribute(mla_tree_attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -749,10 +936,16 @@ cudaError_t launch_tree_attend(const TreeMaps& maps, const TreeParams& p, bool p
     cfg.numAttrs = pdl ? 1 : 0;
     cudaError_t e = cudaLaunchKernelEx(&cfg, mla_tree_attend_kernel, maps, p);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(p.clusters, kTreeBlockRows / kMergeRows);
+    // at most one shared row block per cluster, and no more than there are
+    const long long blocks =
+        static_cast<long long>(p.batch) * ((p.tokens * p.heads + kTreeBlockRows - 1) / kTreeBlockRows);
+    // a row block has about clusters / blocks pieces: few pieces, a row per group
+    const int rows = std::min(p.tokens * p.heads, kTreeBlockRows);
+    const int per = p.clusters > kFewPieces * blocks ? 1 : kMergeGroups;
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(p.clusters, blocks)), (rows + per - 1) / per);
     cfg.blockDim = dim3(kMergeThreads);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, mla_tree_merge_kernel, p);
+    return cudaLaunchKernelEx(&cfg, mla_tree_merge_kernel, p, per);
 }
 
 }  // namespace mla
