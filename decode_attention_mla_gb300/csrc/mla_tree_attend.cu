@@ -134,7 +134,11 @@ struct Cursor {
         --left;
         if (++tile < n_tiles) return;
         tile = 0;
-        if (++rb < n_rb || left <= 0) return;
+        if (left > 0) next_item(p);
+    }
+    // to the next item's first tile (b, rb, n_tiles alone; there is one)
+    __device__ __forceinline__ void next_item(const TreeParams& p) {
+        if (++rb < n_rb) return;
         rb = 0;
         do {
             ++b;
@@ -314,39 +318,55 @@ __device__ void produce(const TreeMaps& maps, const TreeParams& p, Shared& sh, u
 // ============================== MMA issue ==================================
 // One warp issues everything: the tensor pipe takes the MMAs in order, and QK and
 // PV interleaved from two warps ran at half the rate.  Its queue is short, so what
-// the warp does between two MMAs costs tensor time: the waits are on barriers of
-// its own CTA that completed long ago (P is two tiles behind: the order is QK(g),
-// PV(g - 2)), and all that crosses CTAs goes through the relay warp.  The whole
-// warp walks the tiles and waits, one lane issues (with a single thread doing all
-// of it an MMA took 100 cycles to issue, now about 36).
+// the warp does between two MMAs costs tensor time.  Hence: the whole warp walks
+// the tiles and waits, one lane issues (with a single thread doing all of it an
+// MMA took 100 cycles to issue, instead of the 32 or 64 that it runs); each
+// barrier is looked at once before the MMAs that precede its use, so a phase
+// that is over by then costs nothing; PV is two tiles behind QK, so its phases
+// are; and all that crosses CTAs goes through the relay warp.
+struct Issue {
+    Shared& sh;
+    bool lead, ok;
+
+    // after `seen` (an earlier look at the barrier): the phase is over
+    __device__ __forceinline__ void need(bool seen, uint64_t* bar, uint32_t parity) {
+        if (!seen) ok = wait_slowly(bar, parity, &sh.abort_flag) && ok;
+        tc_fence_after_sync();
+    }
+};
+
 __device__ void issue(const TreeParams& p, Shared& sh, uint32_t tmem) {
     constexpr uint32_t idesc_qk = make_idesc_bf16(128, 128, 0, 0);
     constexpr uint32_t idesc_pv = make_idesc_bf16(128, 256, 0, 1);
-    const bool lead = elect_one();
+    Issue is{sh, elect_one(), true};
     const uint64_t kd = make_sdesc(smem_u32(sh.k), 16, 1024, kLayoutSw128);
     const uint64_t vd = make_sdesc(smem_u32(sh.v), kChunkBytes, 1024, kLayoutSw128);
     const uint64_t rope = make_sdesc(smem_u32(sh.rope), 16, 1024, kLayoutSw128);
     const uint64_t q = make_sdesc(smem_u32(sh.q), 16, 1024, kLayoutSw128);
     const uint64_t pd = make_sdesc(smem_u32(sh.p), 16, 1024, kLayoutSw128);
-    uint32_t slot = 0, round = 0;                          // K ring
+    uint32_t slot = 0, k_par = 0;                          // K ring
     uint32_t firsts = 0;                                   // bit i: the tile i QKs ago was the first of its item
-    int pv_item = -1;
-    bool ok = true;
-    Cursor c;
+    int item = 0, pv_item = -1;
+    Cursor c;                                              // moves from item to item here
     c.start(p, sh.work);
     const int total = c.left;
-    for (int g = 0; g < total + 2 && ok; ++g) {
-        const int buf = g & 1;
+    int in_item = min(c.n_tiles - c.tile, total);          // tiles of the item still to come
+    bool first = true;
+    // what has been seen of the next QK's barriers, the next PV's
+    bool see_s = true, see_rope = false, see_k = false, see_p = false, see_v = false;
+    for (int g = 0; g < total + 2 && is.ok; ++g) {
+        const uint32_t buf = g & 1, par = g & 1, par2 = (g >> 1) & 1;
         firsts <<= 1;
         if (g < total) {
             const uint32_t d = tmem + kTmemS + 64 * buf;
-            const bool last = c.last();
-            firsts |= c.first ? 1u : 0u;
-            if (c.first) ok = warp_wait(sh, &sh.q_ready, c.item & 1);
-            // both CTAs have read the scores of tile g - 2
-            if (g >= 2) ok = ok && warp_wait(sh, &sh.s_free[buf], ((g >> 1) - 1) & 1);
-            ok = ok && warp_wait(sh, &sh.rope_ready, g & 1);
-            if (lead && ok) {
+            const bool last = in_item == 1;
+            if (first) {
+                firsts |= 1u;
+                is.need(false, &sh.q_ready, item & 1);
+            }
+            if (g >= 2) is.need(see_s, &sh.s_free[buf], par2 ^ 1);   // both CTAs have read the scores of tile g - 2
+            is.need(see_rope, &sh.rope_ready, par);
+            if (is.lead && is.ok) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     umma_pair_bf16(d, q + ((8 * kChunkBytes + k * 32u) >> 4), rope + (k * 32u >> 4), idesc_qk,
@@ -355,48 +375,71 @@ __device__ void issue(const TreeParams& p, Shared& sh, uint32_t tmem) {
             }
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                ok = ok && warp_wait(sh, &sh.k_ready[slot], round & 1);
-                if (lead && ok) {
-                    const uint64_t kb = kd + (slot * kSlotBytes >> 4);
+                const uint32_t at = slot, at_par = k_par;
+                is.need(see_k, &sh.k_ready[at], at_par);
+                if (++slot == kKSlots) {
+                    slot = 0;
+                    k_par ^= 1;
+                }
+                if (s < 3) {
+                    see_k = mbar_try_wait(&sh.k_ready[slot], k_par);
+                } else if (g >= 2) {
+                    see_p = mbar_try_wait(&sh.p_ready[buf], par2 ^ 1);
+                    see_v = mbar_try_wait(&sh.v_ready[0], par);
+                }
+                if (is.lead && is.ok) {
+                    const uint64_t kb = kd + (at * kSlotBytes >> 4);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
                         const uint32_t off = ((k >> 2) * kChunkBytes + (k & 3) * 32u) >> 4;
                         umma_pair_bf16(d, q + (2 * s * kChunkBytes >> 4) + off, kb + off, idesc_qk, 1u);
                     }
-                    umma_commit_pair(&sh.k_empty[slot]);
-                }
-                if (++slot == kKSlots) {
-                    slot = 0;
-                    ++round;
+                    umma_commit_pair(&sh.k_empty[at]);
                 }
             }
-            if (lead && ok) {
+            if (is.lead && is.ok) {
                 umma_commit_pair(&sh.s_full[buf]);
                 if (last) umma_commit_pair(&sh.q_empty);
             }
-            c.next(p);
+            first = last;
+            if (--in_item == 0 && g + 1 < total) {
+                c.next_item(p);
+                ++item;
+                in_item = min(c.n_tiles, total - (g + 1));
+            }
         }
         if (g >= 2) {
-            const uint32_t first = firsts >> 2 & 1u;
-            ok = ok && warp_wait(sh, &sh.p_ready[buf], ((g >> 1) - 1) & 1);
-            if (first && ++pv_item > 0) ok = ok && warp_wait(sh, &sh.o_free, (pv_item - 1) & 1);
+            const uint32_t pv_first = firsts >> 2 & 1u;
+            is.need(see_p, &sh.p_ready[buf], par2 ^ 1);
+            if (pv_first && ++pv_item > 0) is.need(false, &sh.o_free, (pv_item - 1) & 1);
             const uint64_t pb = pd + (buf * 2 * kChunkBytes >> 4);
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                ok = ok && warp_wait(sh, &sh.v_ready[s], g & 1);
-                if (lead && ok) {
+                is.need(see_v, &sh.v_ready[s], par);
+                if (s < 3) {
+                    see_v = mbar_try_wait(&sh.v_ready[s + 1], par);
+                } else {
+                    // the next step's first barriers (a false look costs a second one)
+                    see_s = g + 1 < total && mbar_try_wait(&sh.s_free[buf ^ 1], ((g + 1) >> 1 & 1) ^ 1);
+                    see_rope = g + 1 < total && mbar_try_wait(&sh.rope_ready, par ^ 1);
+                    see_k = g + 1 < total && mbar_try_wait(&sh.k_ready[slot], k_par);
+                    see_p = see_v = false;
+                }
+                if (is.lead && is.ok) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         umma_pair_bf16(tmem + kTmemO + 128 * (s >> 1), pb + (((s & 1) * kChunkBytes + k * 32u) >> 4),
                                        vd + ((s * kSlotBytes + k * 2048u) >> 4), idesc_pv,
-                                       (s & 1) == 0 && k == 0 ? first ^ 1u : 1u);
+                                       (s & 1) == 0 && k == 0 ? pv_first ^ 1u : 1u);
                     umma_commit_pair(&sh.v_empty[s]);
                 }
             }
-            if (lead && ok) umma_commit_pair(&sh.o_done[buf]);
+            if (is.lead && is.ok) umma_commit_pair(&sh.o_done[buf]);
+        } else {
+            see_s = see_rope = see_k = false;
         }
     }
-    if (!ok && lead) raise_error(sh, p.status);
+    if (!is.ok && is.lead) raise_error(sh, p.status);
 }
 
 // Carries "P of the tile is written" to the MMA warp, one thread in each CTA:
