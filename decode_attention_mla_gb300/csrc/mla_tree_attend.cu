@@ -83,9 +83,9 @@ struct __align__(1024) Shared {
     uint8_t p[2][2][kChunkBytes];                          // P of two tiles, 64 rows x 128 keys in two key atoms
     float red_max[4][64], red_sum[4][64];                  // by quarter of the tile's keys, row
     // used in the even CTA, arrivals of both
-    uint64_t k_ready[kKSlots], v_ready[kVSlots], rope_ready, q_ready, s_free[2], p_peer[2], o_free;
+    uint64_t k_ready[kKSlots], v_ready[2], q_ready, s_free[2], p_peer[2], o_free;
     // in each CTA, arrivals of the MMA thread
-    uint64_t k_empty[kKSlots], v_empty[kVSlots], rope_empty, q_empty, s_full[2], o_done[2];
+    uint64_t k_empty[kKSlots], v_empty[2], q_empty, s_full[2], o_done[2];
     // this CTA's P is written; (even CTA) both CTAs' are
     uint64_t p_local[2], p_ready[2];
     uint64_t v_local[2];                                   // V of a tile with drafted rows has landed in this CTA
@@ -253,16 +253,17 @@ struct Producer {
         tma_load_3d_pair(sh.q, &maps.q, 0, row, 0, bar, pol_q);
         return true;
     }
-    // QK operands: this CTA's 64 keys, the rope columns, then 128 columns a slot
+    // QK operands: this CTA's 64 keys, 128 columns a slot.  The rope columns come
+    // with the third slot: their place was read before the slot that this one
+    // waits for.
     __device__ bool load_k(const Cursor& c) {
         const int y = static_cast<int>(c.r.base) + c.tile * kTreeTileKeys + static_cast<int>(rank) * 64;
-        if (c.g > 0 && !mbar_wait_bounded(&sh.rope_empty, (c.g - 1) & 1, &sh.abort_flag)) return false;
-        tma_load_3d_pair(sh.rope, &maps.rope, 0, y, 8, expect(&sh.rope_ready, kChunkBytes), pol_kv);
 #pragma unroll 1
         for (int s = 0; s < 4; ++s) {
             if (round > 0 && !mbar_wait_bounded(&sh.k_empty[slot], (round - 1) & 1, &sh.abort_flag)) return false;
-            const uint32_t bar = expect(&sh.k_ready[slot], kSlotBytes);
+            const uint32_t bar = expect(&sh.k_ready[slot], kSlotBytes + (s == 2 ? kChunkBytes : 0));
             tma_load_3d_pair(sh.k[slot], &maps.kv, 0, y, 2 * s, bar, pol_kv);
+            if (s == 2) tma_load_3d_pair(sh.rope, &maps.rope, 0, y, 8, bar, pol_kv);
             if (++slot == kKSlots) {
                 slot = 0;
                 ++round;
@@ -282,18 +283,18 @@ struct Producer {
             ++specials;
         }
 #pragma unroll 1
-        for (int s = 0; s < 4; ++s) {
-            if (c.g > 0 && !mbar_wait_bounded(&sh.v_empty[s], (c.g - 1) & 1, &sh.abort_flag)) return false;
-            const int i = s >> 1, kb = s & 1;
+        for (int i = 0; i < 2; ++i) {
+            if (c.g > 0 && !mbar_wait_bounded(&sh.v_empty[i], (c.g - 1) & 1, &sh.abort_flag)) return false;
+            const int z = 4 * i + 2 * static_cast<int>(rank);
             if (special) {
                 // the softmax threads wait for these bytes and vouch for them with P
-                tma_load_3d(sh.v[s], &maps.kv, 0, y + 64 * kb, 4 * i + 2 * static_cast<int>(rank),
-                            local, pol_kv);
-                if (rank == 0) mbar_arrive(&sh.v_ready[s]);
+                tma_load_3d(sh.v[2 * i], &maps.kv, 0, y, z, local, pol_kv);
+                tma_load_3d(sh.v[2 * i + 1], &maps.kv, 0, y + 64, z, local, pol_kv);
+                if (rank == 0) mbar_arrive(&sh.v_ready[i]);
             } else {
-                const uint32_t bar = expect(&sh.v_ready[s], kSlotBytes);
-                tma_load_3d_pair(sh.v[s], &maps.kv, 0, y + 64 * kb, 4 * i + 2 * static_cast<int>(rank),
-                                 bar, pol_kv);
+                const uint32_t bar = expect(&sh.v_ready[i], 2 * kSlotBytes);
+                tma_load_3d_pair(sh.v[2 * i], &maps.kv, 0, y, z, bar, pol_kv);
+                tma_load_3d_pair(sh.v[2 * i + 1], &maps.kv, 0, y + 64, z, bar, pol_kv);
             }
         }
         return true;
@@ -331,7 +332,6 @@ struct Issue {
     // after `seen` (an earlier look at the barrier): the phase is over
     __device__ __forceinline__ void need(bool seen, uint64_t* bar, uint32_t parity) {
         if (!seen) ok = wait_slowly(bar, parity, &sh.abort_flag) && ok;
-        tc_fence_after_sync();
     }
 };
 
@@ -353,7 +353,7 @@ __device__ void issue(const TreeParams& p, Shared& sh, uint32_t tmem) {
     int in_item = min(c.n_tiles - c.tile, total);          // tiles of the item still to come
     bool first = true;
     // what has been seen of the next QK's barriers, the next PV's
-    bool see_s = true, see_rope = false, see_k = false, see_p = false, see_v = false;
+    bool see_s = true, see_k = false, see_p = false, see_v = false;
     for (int g = 0; g < total + 2 && is.ok; ++g) {
         const uint32_t buf = g & 1, par = g & 1, par2 = (g >> 1) & 1;
         firsts <<= 1;
@@ -365,18 +365,11 @@ __device__ void issue(const TreeParams& p, Shared& sh, uint32_t tmem) {
                 is.need(false, &sh.q_ready, item & 1);
             }
             if (g >= 2) is.need(see_s, &sh.s_free[buf], par2 ^ 1);   // both CTAs have read the scores of tile g - 2
-            is.need(see_rope, &sh.rope_ready, par);
-            if (is.lead && is.ok) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    umma_pair_bf16(d, q + ((8 * kChunkBytes + k * 32u) >> 4), rope + (k * 32u >> 4), idesc_qk,
-                                   k ? 1u : 0u);
-                umma_commit_pair(&sh.rope_empty);
-            }
+            tc_fence_after_sync();
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                const uint32_t at = slot, at_par = k_par;
-                is.need(see_k, &sh.k_ready[at], at_par);
+                const uint32_t at = slot;
+                is.need(see_k, &sh.k_ready[at], k_par);
                 if (++slot == kKSlots) {
                     slot = 0;
                     k_par ^= 1;
@@ -392,7 +385,13 @@ __device__ void issue(const TreeParams& p, Shared& sh, uint32_t tmem) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
                         const uint32_t off = ((k >> 2) * kChunkBytes + (k & 3) * 32u) >> 4;
-                        umma_pair_bf16(d, q + (2 * s * kChunkBytes >> 4) + off, kb + off, idesc_qk, 1u);
+                        umma_pair_bf16(d, q + (2 * s * kChunkBytes >> 4) + off, kb + off, idesc_qk, (s | k) ? 1u : 0u);
+                    }
+                    if (s == 2) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            umma_pair_bf16(d, q + ((8 * kChunkBytes + k * 32u) >> 4), rope + (k * 32u >> 4), idesc_qk,
+                                           1u);
                     }
                     umma_commit_pair(&sh.k_empty[at]);
                 }
@@ -413,30 +412,30 @@ __device__ void issue(const TreeParams& p, Shared& sh, uint32_t tmem) {
             is.need(see_p, &sh.p_ready[buf], par2 ^ 1);
             if (pv_first && ++pv_item > 0) is.need(false, &sh.o_free, (pv_item - 1) & 1);
             const uint64_t pb = pd + (buf * 2 * kChunkBytes >> 4);
+            tc_fence_after_sync();
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                is.need(see_v, &sh.v_ready[s], par);
-                if (s < 3) {
-                    see_v = mbar_try_wait(&sh.v_ready[s + 1], par);
+            for (int i = 0; i < 2; ++i) {
+                is.need(see_v, &sh.v_ready[i], par);
+                if (i == 0) {
+                    see_v = mbar_try_wait(&sh.v_ready[1], par);
                 } else {
                     // the next step's first barriers (a false look costs a second one)
-                    see_s = g + 1 < total && mbar_try_wait(&sh.s_free[buf ^ 1], ((g + 1) >> 1 & 1) ^ 1);
-                    see_rope = g + 1 < total && mbar_try_wait(&sh.rope_ready, par ^ 1);
-                    see_k = g + 1 < total && mbar_try_wait(&sh.k_ready[slot], k_par);
+                    see_s = mbar_try_wait(&sh.s_free[buf ^ 1], ((g + 1) >> 1 & 1) ^ 1);
+                    see_k = mbar_try_wait(&sh.k_ready[slot], k_par);
                     see_p = see_v = false;
                 }
                 if (is.lead && is.ok) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        umma_pair_bf16(tmem + kTmemO + 128 * (s >> 1), pb + (((s & 1) * kChunkBytes + k * 32u) >> 4),
-                                       vd + ((s * kSlotBytes + k * 2048u) >> 4), idesc_pv,
-                                       (s & 1) == 0 && k == 0 ? pv_first ^ 1u : 1u);
-                    umma_commit_pair(&sh.v_empty[s]);
+                    for (int k = 0; k < 8; ++k)
+                        umma_pair_bf16(tmem + kTmemO + 128 * i, pb + (((k >> 2) * kChunkBytes + (k & 3) * 32u) >> 4),
+                                       vd + (((2 * i + (k >> 2)) * kSlotBytes + (k & 3) * 2048u) >> 4), idesc_pv,
+                                       k == 0 ? pv_first ^ 1u : 1u);
+                    umma_commit_pair(&sh.v_empty[i]);
                 }
             }
             if (is.lead && is.ok) umma_commit_pair(&sh.o_done[buf]);
         } else {
-            see_s = see_rope = see_k = false;
+            see_s = see_k = false;
         }
     }
     if (!is.ok && is.lead) raise_error(sh, p.status);
@@ -733,11 +732,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(&sh.k_ready[i], 1);
             mbar_init(&sh.k_empty[i], 1);
         }
-        for (int i = 0; i < kVSlots; ++i) {
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.v_ready[i], 1);
             mbar_init(&sh.v_empty[i], 1);
         }
-        mbar_init(&sh.rope_ready, 1);
         mbar_init(&sh.q_ready, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.s_free[i], 2 * kSoftmaxWarps);
@@ -746,7 +744,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(&sh.p_ready[i], 1);
         }
         mbar_init(&sh.o_free, 2 * kSoftmaxWarps);
-        mbar_init(&sh.rope_empty, 1);
         mbar_init(&sh.q_empty, 1);
         mbar_init(&sh.s_full[0], 1);
         mbar_init(&sh.s_full[1], 1);
