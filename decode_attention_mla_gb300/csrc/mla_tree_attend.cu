@@ -54,14 +54,14 @@
 namespace mla {
 namespace {
 
-constexpr int kKSlots = 3, kVSlots = 4;
+constexpr int kSlots = 4;                                  // of K and of V: a tile each
 constexpr uint32_t kSlotBytes = 16384;                     // 2 column chunks of 64 rows x 128 bytes
 constexpr uint32_t kChunkBytes = 8192;
 constexpr uint32_t kQBytes = 9 * kChunkBytes;
-constexpr int kThreads = 384;
+constexpr int kThreads = 352;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
-constexpr int kProducerWarp = 8, kMmaWarp = 9, kValueWarp = 10, kRelayWarp = 11;
+constexpr int kProducerWarp = 8, kMmaWarp = 9, kValueWarp = 10;
 constexpr int kBarSoftmax = 1;                             // hardware barrier of the softmax warps
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 0, kTmemS = 256;               // O: 2 x 128 columns, S: 2 x 64 columns
@@ -76,18 +76,16 @@ struct Work {                                              // this cluster's run
 };
 
 struct __align__(1024) Shared {
-    uint8_t k[kKSlots][kSlotBytes];                        // ring: 64 keys x 128 columns, QK operand
-    uint8_t v[kVSlots][kSlotBytes];                        // (feature half i, key half kb) at 2 i + kb, PV operand
+    uint8_t k[kSlots][kSlotBytes];                         // this CTA's 64 keys x 128 columns, QK operand
+    uint8_t v[kSlots][kSlotBytes];                         // (feature half i, key half kb) at 2 i + kb, PV operand
     uint8_t rope[kChunkBytes];                             // this CTA's 64 keys, rope columns
     uint8_t q[kQBytes];                                    // 9 chunks of 64 query rows
-    uint8_t p[2][2][kChunkBytes];                          // P of two tiles, 64 rows x 128 keys in two key atoms
+    uint8_t p[2][kChunkBytes];                             // P, 64 rows x 128 keys in two key atoms
     float red_max[4][64], red_sum[4][64];                  // by quarter of the tile's keys, row
     // used in the even CTA, arrivals of both
-    uint64_t k_ready[kKSlots], v_ready[2], q_ready, s_free[2], p_peer[2], o_free;
+    uint64_t k_ready[kSlots], v_ready[2], q_ready, p_ready, o_free;
     // in each CTA, arrivals of the MMA thread
-    uint64_t k_empty[kKSlots], v_empty[2], q_empty, s_full[2], o_done[2];
-    // this CTA's P is written; (even CTA) both CTAs' are
-    uint64_t p_local[2], p_ready[2];
+    uint64_t k_empty[kSlots], v_empty[2], q_empty, s_full[2], o_done;
     uint64_t v_local[2];                                   // V of a tile with drafted rows has landed in this CTA
     uint64_t stall_bar;
     Work work;
@@ -237,7 +235,6 @@ struct Producer {
     Shared& sh;
     uint32_t rank;
     uint64_t pol_kv, pol_q;
-    uint32_t slot = 0, round = 0;                          // K ring: next slot, times around
     uint32_t specials = 0;
 
     // The even CTA's barrier of a load; that CTA announces both CTAs' bytes (the odd
@@ -253,21 +250,15 @@ struct Producer {
         tma_load_3d_pair(sh.q, &maps.q, 0, row, 0, bar, pol_q);
         return true;
     }
-    // QK operands: this CTA's 64 keys, 128 columns a slot.  The rope columns come
-    // with the third slot: their place was read before the slot that this one
-    // waits for.
+    // QK operands: this CTA's 64 keys, 128 columns a slot, the rope columns with the last
     __device__ bool load_k(const Cursor& c) {
         const int y = static_cast<int>(c.r.base) + c.tile * kTreeTileKeys + static_cast<int>(rank) * 64;
 #pragma unroll 1
-        for (int s = 0; s < 4; ++s) {
-            if (round > 0 && !mbar_wait_bounded(&sh.k_empty[slot], (round - 1) & 1, &sh.abort_flag)) return false;
-            const uint32_t bar = expect(&sh.k_ready[slot], kSlotBytes + (s == 2 ? kChunkBytes : 0));
-            tma_load_3d_pair(sh.k[slot], &maps.kv, 0, y, 2 * s, bar, pol_kv);
-            if (s == 2) tma_load_3d_pair(sh.rope, &maps.rope, 0, y, 8, bar, pol_kv);
-            if (++slot == kKSlots) {
-                slot = 0;
-                ++round;
-            }
+        for (int s = 0; s < kSlots; ++s) {
+            if (c.g > 0 && !mbar_wait_bounded(&sh.k_empty[s], (c.g - 1) & 1, &sh.abort_flag)) return false;
+            const uint32_t bar = expect(&sh.k_ready[s], kSlotBytes + (s == 3 ? kChunkBytes : 0));
+            tma_load_3d_pair(sh.k[s], &maps.kv, 0, y, 2 * s, bar, pol_kv);
+            if (s == 3) tma_load_3d_pair(sh.rope, &maps.rope, 0, y, 8, bar, pol_kv);
         }
         return true;
     }
@@ -344,121 +335,93 @@ __device__ void issue(const TreeParams& p, Shared& sh, uint32_t tmem) {
     const uint64_t rope = make_sdesc(smem_u32(sh.rope), 16, 1024, kLayoutSw128);
     const uint64_t q = make_sdesc(smem_u32(sh.q), 16, 1024, kLayoutSw128);
     const uint64_t pd = make_sdesc(smem_u32(sh.p), 16, 1024, kLayoutSw128);
-    uint32_t slot = 0, k_par = 0;                          // K ring
-    uint32_t firsts = 0;                                   // bit i: the tile i QKs ago was the first of its item
     int item = 0, pv_item = -1;
     Cursor c;                                              // moves from item to item here
     c.start(p, sh.work);
     const int total = c.left;
     int in_item = min(c.n_tiles - c.tile, total);          // tiles of the item still to come
     bool first = true;
-    // what has been seen of the next QK's barriers, the next PV's
-    bool see_s = true, see_k = false, see_p = false, see_v = false;
-    for (int g = 0; g < total + 2 && is.ok; ++g) {
-        const uint32_t buf = g & 1, par = g & 1, par2 = (g >> 1) & 1;
-        firsts <<= 1;
-        if (g < total) {
-            const uint32_t d = tmem + kTmemS + 64 * buf;
-            const bool last = in_item == 1;
-            if (first) {
-                firsts |= 1u;
-                is.need(false, &sh.q_ready, item & 1);
-            }
-            if (g >= 2) is.need(see_s, &sh.s_free[buf], par2 ^ 1);   // both CTAs have read the scores of tile g - 2
-            tc_fence_after_sync();
+    uint32_t pv_first = 0;                                 // the tile before this QK's was the first of its item
+    // what an early look has shown of the next QK's first barrier and the next PV's
+    // (false: not looked at, or not over yet)
+    bool see_k = false, see_p = false, see_v = false;
+    for (int g = 0; g <= total && is.ok; ++g) {
+        const uint32_t buf = g & 1, par = g & 1;           // of QK(g); PV(g - 1) has the other parity
+        const uint32_t qk_first = first;
+        // PV of a block's last tile goes first: the next block's QK waits for its queries
+        const int pv_turn = first ? 0 : 1;
+#pragma unroll 1
+        for (int turn = 0; turn < 2; ++turn) {
+            if (turn == pv_turn) {
+                if (g == 0) continue;
+                is.need(see_p, &sh.p_ready, par ^ 1);
+                if (pv_first && ++pv_item > 0) is.need(false, &sh.o_free, (pv_item - 1) & 1);
+                tc_fence_after_sync();
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const uint32_t at = slot;
-                is.need(see_k, &sh.k_ready[at], k_par);
-                if (++slot == kKSlots) {
-                    slot = 0;
-                    k_par ^= 1;
+                for (int i = 0; i < 2; ++i) {
+                    is.need(see_v, &sh.v_ready[i], par ^ 1);
+                    if (i == 0)
+                        see_v = mbar_try_wait(&sh.v_ready[1], par ^ 1);
+                    else
+                        see_k = mbar_try_wait(&sh.k_ready[0], par ^ pv_turn);   // of the QK that comes next
+                    if (is.lead && is.ok) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            umma_pair_bf16(tmem + kTmemO + 128 * i, pd + (((k >> 2) * kChunkBytes + (k & 3) * 32u) >> 4),
+                                           vd + (((2 * i + (k >> 2)) * kSlotBytes + (k & 3) * 2048u) >> 4), idesc_pv,
+                                           k == 0 ? pv_first ^ 1u : 1u);
+                        umma_commit_pair(&sh.v_empty[i]);
+                    }
                 }
-                if (s < 3) {
-                    see_k = mbar_try_wait(&sh.k_ready[slot], k_par);
-                } else if (g >= 2) {
-                    see_p = mbar_try_wait(&sh.p_ready[buf], par2 ^ 1);
-                    see_v = mbar_try_wait(&sh.v_ready[0], par);
+                if (is.lead && is.ok) umma_commit_pair(&sh.o_done);
+                see_p = see_v = false;
+            } else {
+                if (g == total) continue;
+                const uint32_t d = tmem + kTmemS + 64 * buf;
+                const bool last = in_item == 1;
+                if (first) is.need(false, &sh.q_ready, item & 1);
+                // (the scores of tile g - 2 have been read: PV(g - 2) waited for their P)
+#pragma unroll
+                for (int s = 0; s < kSlots; ++s) {
+                    is.need(see_k, &sh.k_ready[s], par);
+                    if (s < kSlots - 1) {
+                        see_k = mbar_try_wait(&sh.k_ready[s + 1], par);
+                    } else if (pv_turn == 1 && g >= 1) {
+                        see_p = mbar_try_wait(&sh.p_ready, par ^ 1);
+                        see_v = mbar_try_wait(&sh.v_ready[0], par ^ 1);
+                    }
+                    if (is.lead && is.ok) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const uint32_t off = ((k >> 2) * kChunkBytes + (k & 3) * 32u) >> 4;
+                            umma_pair_bf16(d, q + (2 * s * kChunkBytes >> 4) + off, kd + (s * kSlotBytes >> 4) + off,
+                                           idesc_qk, (s | k) ? 1u : 0u);
+                        }
+                        if (s == 3) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                umma_pair_bf16(d, q + ((8 * kChunkBytes + k * 32u) >> 4), rope + (k * 32u >> 4), idesc_qk,
+                                               1u);
+                        }
+                        umma_commit_pair(&sh.k_empty[s]);
+                    }
                 }
                 if (is.lead && is.ok) {
-                    const uint64_t kb = kd + (at * kSlotBytes >> 4);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const uint32_t off = ((k >> 2) * kChunkBytes + (k & 3) * 32u) >> 4;
-                        umma_pair_bf16(d, q + (2 * s * kChunkBytes >> 4) + off, kb + off, idesc_qk, (s | k) ? 1u : 0u);
-                    }
-                    if (s == 2) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            umma_pair_bf16(d, q + ((8 * kChunkBytes + k * 32u) >> 4), rope + (k * 32u >> 4), idesc_qk,
-                                           1u);
-                    }
-                    umma_commit_pair(&sh.k_empty[at]);
+                    umma_commit_pair(&sh.s_full[buf]);
+                    if (last) umma_commit_pair(&sh.q_empty);
                 }
-            }
-            if (is.lead && is.ok) {
-                umma_commit_pair(&sh.s_full[buf]);
-                if (last) umma_commit_pair(&sh.q_empty);
-            }
-            first = last;
-            if (--in_item == 0 && g + 1 < total) {
-                c.next_item(p);
-                ++item;
-                in_item = min(c.n_tiles, total - (g + 1));
+                see_k = false;
+                first = last;
+                if (--in_item == 0 && g + 1 < total) {
+                    c.next_item(p);
+                    ++item;
+                    in_item = min(c.n_tiles, total - (g + 1));
+                }
             }
         }
-        if (g >= 2) {
-            const uint32_t pv_first = firsts >> 2 & 1u;
-            is.need(see_p, &sh.p_ready[buf], par2 ^ 1);
-            if (pv_first && ++pv_item > 0) is.need(false, &sh.o_free, (pv_item - 1) & 1);
-            const uint64_t pb = pd + (buf * 2 * kChunkBytes >> 4);
-            tc_fence_after_sync();
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                is.need(see_v, &sh.v_ready[i], par);
-                if (i == 0) {
-                    see_v = mbar_try_wait(&sh.v_ready[1], par);
-                } else {
-                    // the next step's first barriers (a false look costs a second one)
-                    see_s = mbar_try_wait(&sh.s_free[buf ^ 1], ((g + 1) >> 1 & 1) ^ 1);
-                    see_k = mbar_try_wait(&sh.k_ready[slot], k_par);
-                    see_p = see_v = false;
-                }
-                if (is.lead && is.ok) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        umma_pair_bf16(tmem + kTmemO + 128 * i, pb + (((k >> 2) * kChunkBytes + (k & 3) * 32u) >> 4),
-                                       vd + (((2 * i + (k >> 2)) * kSlotBytes + (k & 3) * 2048u) >> 4), idesc_pv,
-                                       k == 0 ? pv_first ^ 1u : 1u);
-                    umma_commit_pair(&sh.v_empty[i]);
-                }
-            }
-            if (is.lead && is.ok) umma_commit_pair(&sh.o_done[buf]);
-        } else {
-            see_s = see_k = false;
-        }
+        pv_first = qk_first;
     }
     if (!is.ok && is.lead) raise_error(sh, p.status);
-}
-
-// Carries "P of the tile is written" to the MMA warp, one thread in each CTA:
-// a release that the other CTA sees takes about 1000 cycles, which neither the
-// softmax threads nor the MMA warp should spend.
-__device__ void relay(const TreeParams& p, Shared& sh, uint32_t rank) {
-    const int total = static_cast<int>(sh.work.count);
-    const uint32_t peer = map_to_rank(&sh.p_peer[0], 0);
-    bool ok = true;
-    for (int g = 0; g < total && ok; ++g) {
-        const int buf = g & 1;
-        ok = wait(sh, &sh.p_local[buf], (g >> 1) & 1);
-        if (rank != 0) {
-            if (ok) mbar_arrive_cluster(peer + 8 * buf);
-        } else {
-            ok = ok && mbar_wait_bounded_cluster(&sh.p_peer[buf], (g >> 1) & 1, &sh.abort_flag);
-            if (ok) mbar_arrive(&sh.p_ready[buf]);
-        }
-    }
-    if (!ok) raise_error(sh, p.status);
 }
 
 // ============================== softmax ====================================
@@ -495,36 +458,24 @@ __device__ void clean_v(Shared& sh, const Cursor& c, int tid) {
     }
 }
 
-// 32 features of a warp's 32 rows, through its 4 KB of shared memory so that
-// the stores of a row run along its features (16-byte units, swizzled by row:
-// 128 bytes per row in fp32, 64 in bf16).  `dst`: row 0's first feature,
-// rows 512 elements apart; rows at or past n_rows are not written.
-template <bool kBf16>
-__device__ __forceinline__ void store_rows(uint32_t stage, const uint32_t (&o)[32], float inv, void* dst, int n_rows,
-                                           int lane) {
-    constexpr int kUnits = kBf16 ? 4 : 8;                  // 16-byte units per row
+// 64 bytes of each of a warp's 32 rows (32 features in bf16, 16 in fp32),
+// through its 2 KB of shared memory so that the stores of a row run along its
+// features (16-byte units, swizzled by row pair).  `dst`: row 0's first
+// feature, rows 512 elements apart; rows at or past n_rows are not written.
+__device__ __forceinline__ void store_rows(uint32_t stage, const uint32_t (&w)[16], char* dst, int row_bytes,
+                                           int n_rows, int lane) {
     __syncwarp();                                          // the reads of the block before are done
 #pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (kBf16)
-                w[i] = pack_bf16x2(__uint_as_float(o[8 * u + 2 * i]) * inv, __uint_as_float(o[8 * u + 2 * i + 1]) * inv);
-            else
-                w[i] = __float_as_uint(__uint_as_float(o[4 * u + i]) * inv);
-        }
-        st_shared_v4(stage + lane * 128 + ((u ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
-    }
+    for (int u = 0; u < 4; ++u)
+        st_shared_v4(stage + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4), w[4 * u], w[4 * u + 1], w[4 * u + 2],
+                     w[4 * u + 3]);
     __syncwarp();
-    constexpr int kRows = 32 / kUnits;                     // rows a warp stores at a time
-    const int u = lane % kUnits;
+    const int u = lane & 3;
 #pragma unroll
-    for (int i = 0; i < 32 / kRows; ++i) {
-        const int row = i * kRows + lane / kUnits;
-        const uint4 v = ld_shared_v4(stage + row * 128 + ((u ^ (row & 7)) << 4));
-        if (row < n_rows)
-            reinterpret_cast<uint4*>(static_cast<char*>(dst) + static_cast<long long>(row) * kDLatent * (kBf16 ? 2 : 4))[u] = v;
+    for (int i = 0; i < 4; ++i) {
+        const int row = 8 * i + (lane >> 2);
+        const uint4 v = ld_shared_v4(stage + row * 64 + ((u ^ ((row >> 1) & 3)) << 4));
+        if (row < n_rows) reinterpret_cast<uint4*>(dst + static_cast<long long>(row) * row_bytes)[u] = v;
     }
 }
 
@@ -536,8 +487,8 @@ __device__ void softmax(const TreeParams& p, Shared& sh, uint32_t tmem, uint32_t
     const int quarter = 2 * half + sub;
     const int row = 32 * (warp & 1) + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t s_bar = map_to_rank(&sh.s_free[0], 0), o_bar = map_to_rank(&sh.o_free, 0);
-    const uint32_t p_line = smem_u32(sh.p[0][half]) + row * 128;
+    const uint32_t p_bar = map_to_rank(&sh.p_ready, 0), o_bar = map_to_rank(&sh.o_free, 0);
+    const uint32_t p_line = smem_u32(sh.p[half]) + row * 128;
     const float c2 = p.scale_log2;
     TreeMerge merge{0, 0, 0, 0};
     uint32_t specials = 0;
@@ -565,9 +516,6 @@ __device__ void softmax(const TreeParams& p, Shared& sh, uint32_t tmem, uint32_t
 #pragma unroll
                 for (int i = 0; i < 32; ++i) s[i] = 0;
             }
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster_relaxed(s_bar + 8 * buf);   // the score buffer is free
             const int t0 = c.tile * kTreeTileKeys;
             if (t0 + kTreeTileKeys > c.r.d_pos || t0 < c.r.lo || t0 + kTreeTileKeys > c.r.hi) {
                 const uint32_t v = static_cast<uint32_t>(visible64(c.r, mask, t0 + 64 * half) >> (32 * sub));
@@ -608,27 +556,23 @@ __device__ void softmax(const TreeParams& p, Shared& sh, uint32_t tmem, uint32_t
                 pk[i] = pack_bf16x2(x, y);
             }
             l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            // this P buffer has been read (PV of tile g - 2)
-            w = g < 2 || warp_wait(sh, &sh.o_done[buf], ((g >> 1) - 1) & 1);
-            if (__any_sync(0xffffffffu, alpha != 1.f)) {
-                // (never on an item's first tile) O holds all tiles before this one
-                w = w && warp_wait(sh, &sh.o_done[buf ^ 1], ((g - 1) >> 1) & 1);
-                if (w) {
+            // P of the tile before has been read, and O holds all tiles before this one
+            w = g == 0 || warp_wait(sh, &sh.o_done, (g - 1) & 1);
+            if (w && __any_sync(0xffffffffu, alpha != 1.f)) {   // (never on an item's first tile)
 #pragma unroll 1
-                    for (int j = 0; j < 8; ++j) {
-                        float o[16];
-                        const uint32_t at = tmem + lanes + kTmemO + 128 * sub + 16 * j;
-                        tmem_ld16(at, o);
+                for (int j = 0; j < 8; ++j) {
+                    float o[16];
+                    const uint32_t at = tmem + lanes + kTmemO + 128 * sub + 16 * j;
+                    tmem_ld16(at, o);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] *= alpha;
-                        tmem_st16(at, o);
-                    }
+                    for (int i = 0; i < 16; ++i) o[i] *= alpha;
+                    tmem_st16(at, o);
                 }
             }
             // ---- probabilities, bf16, K-major lines of 64 keys
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-                st_shared_v4(p_line + buf * 2 * kChunkBytes + (((4 * sub + u) ^ (row & 7)) << 4), pk[4 * u],
+                st_shared_v4(p_line + (((4 * sub + u) ^ (row & 7)) << 4), pk[4 * u],
                              pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
             if (c.special()) {
                 // V was loaded for this CTA's own eyes
@@ -640,7 +584,7 @@ __device__ void softmax(const TreeParams& p, Shared& sh, uint32_t tmem, uint32_t
             tc_fence_before_sync();
             __syncwarp();
             bad |= !w;                                     // the threads leave together at the next barrier
-            if (lane == 0 && !bad) mbar_arrive(&sh.p_local[buf]);
+            if (lane == 0 && !bad) mbar_arrive_peer(p_bar);
             ++done;
             c.next(p);
         } while (!last);
@@ -672,14 +616,13 @@ __device__ void softmax(const TreeParams& p, Shared& sh, uint32_t tmem, uint32_t
             merge.rows = min(kTreeBlockRows, live_rows - rb * kTreeBlockRows);
             merge.pieces = 1 + static_cast<int>((n_tiles - done + sh.work.per - 1) / sh.work.per);
         }
-        const int gl = c.g - 1;
-        const bool w = warp_wait(sh, &sh.o_done[gl & 1], (gl >> 1) & 1);
+        const bool w = warp_wait(sh, &sh.o_done, (c.g - 1) & 1);
         if (named_barrier_or(kBarSoftmax, kSoftmaxThreads, !w)) {
             ok = false;
             break;
         }
-        // (P's buffers are free: the last product is done)
-        const uint32_t stage = smem_u32(sh.p) + warp * 4096;
+        // (P's buffer is free: the last product is done)
+        const uint32_t stage = smem_u32(sh.p) + warp * 2048;
         const int row_w = 32 * (warp & 1);                 // this warp's first row of the 64
         const int n_rows = live_rows - (r - row) - row_w;
 #pragma unroll 1
@@ -688,12 +631,22 @@ __device__ void softmax(const TreeParams& p, Shared& sh, uint32_t tmem, uint32_t
             tmem_ld32_async(tmem + lanes + kTmemO + 128 * sub + 32 * j, o);
             tmem_wait_ld32(o);
             const long long at = (row0 + row_w) * kDLatent + 256 * sub + 128 * half + 32 * j;
-            if (!whole)
-                store_rows<false>(stage, o, inv, p.part + at, n_rows, lane);
-            else if (p.a.out_fp32)
-                store_rows<false>(stage, o, inv, static_cast<float*>(p.a.out) + at, n_rows, lane);
-            else
-                store_rows<true>(stage, o, inv, static_cast<uint16_t*>(p.a.out) + at, n_rows, lane);
+            uint32_t x[16];
+            if (whole && !p.a.out_fp32) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    x[i] = pack_bf16x2(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+                store_rows(stage, x, reinterpret_cast<char*>(static_cast<uint16_t*>(p.a.out) + at), 2 * kDLatent,
+                           n_rows, lane);
+            } else {
+                float* dst = (whole ? static_cast<float*>(p.a.out) : p.part) + at;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(o[16 * h + i]) * inv);
+                    store_rows(stage, x, reinterpret_cast<char*>(dst + 16 * h), 4 * kDLatent, n_rows, lane);
+                }
+            }
         }
         tc_fence_before_sync();
         __syncwarp();
@@ -728,29 +681,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         prefetch_tensormap(&maps.kv);
         prefetch_tensormap(&maps.rope);
         prefetch_tensormap(&maps.q);
-        for (int i = 0; i < kKSlots; ++i) {
+        for (int i = 0; i < kSlots; ++i) {
             mbar_init(&sh.k_ready[i], 1);
             mbar_init(&sh.k_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.v_ready[i], 1);
             mbar_init(&sh.v_empty[i], 1);
+            mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.v_local[i], 1);
         }
+        mbar_init(&sh.p_ready, 2 * kSoftmaxWarps);
+        mbar_init(&sh.o_done, 1);
         mbar_init(&sh.q_ready, 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh.s_free[i], 2 * kSoftmaxWarps);
-            mbar_init(&sh.p_local[i], kSoftmaxWarps);
-            mbar_init(&sh.p_peer[i], 1);
-            mbar_init(&sh.p_ready[i], 1);
-        }
         mbar_init(&sh.o_free, 2 * kSoftmaxWarps);
         mbar_init(&sh.q_empty, 1);
-        mbar_init(&sh.s_full[0], 1);
-        mbar_init(&sh.s_full[1], 1);
-        mbar_init(&sh.o_done[0], 1);
-        mbar_init(&sh.o_done[1], 1);
-        mbar_init(&sh.v_local[0], 1);
-        mbar_init(&sh.v_local[1], 1);
         mbar_init(&sh.stall_bar, 1);
         sh.abort_flag = 0;
         mbar_init_fence();
@@ -777,8 +722,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lane == 0) produce(maps, p, sh, rank, false);
     } else if (warp == kValueWarp) {
         if (lane == 0) produce(maps, p, sh, rank, true);
-    } else if (warp == kRelayWarp) {
-        if (lane == 0) relay(p, sh, rank);
     } else if (warp == kMmaWarp) {
         if (rank == 0)
             issue(p, sh, tmem);

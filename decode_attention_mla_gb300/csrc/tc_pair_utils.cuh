@@ -48,10 +48,13 @@ __device__ __forceinline__ uint32_t map_to_rank(const void* p, uint32_t rank) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// An arrival that orders no memory accesses (the thread's tensor-memory loads
-// are complete, and nothing else is handed over).
-__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar) {
-    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+// Arrive at an mbarrier of the other CTA with CTA-scope ordering: enough where
+// what is handed over stays in this SM (shared memory that this SM's own tensor
+// core reads, made visible to it by fence.proxy.async; tensor memory), the other
+// CTA only issuing the instruction.  A release at cluster scope waits for a round
+// trip of about 1000 cycles.
+__device__ __forceinline__ void mbar_arrive_peer(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
