@@ -343,7 +343,7 @@ __device__ void issue(const TreeParams& p, Shared& sh, uint32_t tmem) {
     bool first = true;
     uint32_t pv_first = 0;                                 // the tile before this QK's was the first of its item
     // what an early look has shown of the next QK's first barrier and the next PV's
-    // (false: not looked at, or not over yet)
+    // (false: not looked at, or not over yet; a look must not block, as try_wait may)
     bool see_k = false, see_p = false, see_v = false;
     for (int g = 0; g <= total && is.ok; ++g) {
         const uint32_t buf = g & 1, par = g & 1;           // of QK(g); PV(g - 1) has the other parity
@@ -361,9 +361,9 @@ __device__ void issue(const TreeParams& p, Shared& sh, uint32_t tmem) {
                 for (int i = 0; i < 2; ++i) {
                     is.need(see_v, &sh.v_ready[i], par ^ 1);
                     if (i == 0)
-                        see_v = mbar_try_wait(&sh.v_ready[1], par ^ 1);
+                        see_v = mbar_test(&sh.v_ready[1], par ^ 1);
                     else
-                        see_k = mbar_try_wait(&sh.k_ready[0], par ^ pv_turn);   // of the QK that comes next
+                        see_k = mbar_test(&sh.k_ready[0], par ^ pv_turn);   // of the QK that comes next
                     if (is.lead && is.ok) {
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
@@ -385,10 +385,10 @@ __device__ void issue(const TreeParams& p, Shared& sh, uint32_t tmem) {
                 for (int s = 0; s < kSlots; ++s) {
                     is.need(see_k, &sh.k_ready[s], par);
                     if (s < kSlots - 1) {
-                        see_k = mbar_try_wait(&sh.k_ready[s + 1], par);
+                        see_k = mbar_test(&sh.k_ready[s + 1], par);
                     } else if (pv_turn == 1 && g >= 1) {
-                        see_p = mbar_try_wait(&sh.p_ready, par ^ 1);
-                        see_v = mbar_try_wait(&sh.v_ready[0], par ^ 1);
+                        see_p = mbar_test(&sh.p_ready, par ^ 1);
+                        see_v = mbar_test(&sh.v_ready[0], par ^ 1);
                     }
                     if (is.lead && is.ok) {
 #pragma unroll
