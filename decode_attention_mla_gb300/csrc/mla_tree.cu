@@ -12,53 +12,6 @@ namespace {
 
 constexpr int kTreeMagic = 0x4d4c5431;                     // "MLT1"
 constexpr int kMinTiles = 1;
-constexpr int kThreads = 256;
-
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-// 18 elements of a 576-element row: 2 * lane + 64 i, + 1
-__device__ __forceinline__ void load_row(const uint16_t* row, int lane, float (&v)[18]) {
-#pragma unroll
-    for (int i = 0; i < 9; ++i) {
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(row + 2 * lane + 64 * i);
-        v[2 * i] = __uint_as_float(w << 16);
-        v[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
-    }
-}
-
-// One warp per cache row of a request.
-__global__ void __launch_bounds__(kThreads) mla_tree_weights_kernel(const TreeParams p) {
-    grid_dependency_wait();
-    const int lane = threadIdx.x & 31;
-    const int b = blockIdx.y;
-    const TreeRequest r = load_tree_request(p, b);
-    const int warps = gridDim.x * (kThreads / 32);
-    for (int t = r.lo + blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); t < r.hi; t += warps) {
-        float q[18], k[18];
-        load_row(static_cast<const uint16_t*>(p.a.kv) + (r.base + t) * p.a.row_stride, lane, k);
-        float sum = 0.f;
-        for (int i = 0; i < r.n_tok; ++i) {
-            if (t >= r.d_pos && !(tree_mask(p, b, i, r.n_tok) >> (t - r.d_pos) & 1)) continue;
-            for (int h = 0; h < p.heads; ++h) {
-                const long long w = (static_cast<long long>(b) * p.tokens + i) * p.heads + h;
-                const float lse = p.a.lse[w];
-                if (lse == -INFINITY) continue;
-                load_row(static_cast<const uint16_t*>(p.a.q) + w * kDRow, lane, q);
-                float s = 0.f;
-#pragma unroll
-                for (int j = 0; j < 18; ++j) s += q[j] * k[j];
-                sum += exp2f(warp_sum(s) * p.scale_log2 - lse * kLog2e);
-            }
-        }
-        if (lane == 0) {
-            float* dst = p.weights + r.base + t;
-            *dst = p.decay == 0.f ? sum : p.decay * *dst + sum;
-        }
-    }
-}
 
 bool off(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to != 0; }
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -131,7 +84,8 @@ int prepare(cudaStream_t st, bool may_capture) {
         if (cs != cudaStreamCaptureStatusNone) return MLA_ENOTREADY;
     }
     std::lock_guard<std::mutex> lock(g_tree_mutex);
-    if (launch_status(tree_attend_prepare()) != MLA_OK) return MLA_ECUDA;
+    if (launch_status(tree_attend_prepare()) != MLA_OK || launch_status(tree_weights_prepare()) != MLA_OK)
+        return MLA_ECUDA;
     g_tree_prepared[dev].store(1, std::memory_order_release);
     return MLA_OK;
 }
@@ -154,12 +108,9 @@ TreeParams params(const mla_tree_plan_t* pl, const mla_tree_args* a, void* scrat
     return p;
 }
 
-int encode_maps(const mla_tree_plan_t* pl, const mla_tree_args* a, TreeMaps* m) {
+int encode_q(const mla_tree_plan_t* pl, const mla_tree_args* a, CUtensorMap* map, uint32_t chunks) {
     const long long rows = static_cast<long long>(pl->shape.batch) * pl->shape.tokens * pl->shape.heads;
-    int rc = encode_bf16_row_chunks(&m->kv, a->kv, a->kv_rows, a->row_stride, 64, 2);
-    if (rc == MLA_OK) rc = encode_bf16_row_chunks(&m->rope, a->kv, a->kv_rows, a->row_stride, 64, 1);
-    if (rc == MLA_OK) rc = encode_bf16_row_chunks(&m->q, a->q, rows, MLA_D_ROW, 64, 9);
-    return rc;
+    return encode_bf16_row_chunks(map, a->q, rows, MLA_D_ROW, 64, chunks);
 }
 
 }  // namespace
@@ -196,8 +147,10 @@ int mla_tree_forward(const mla_tree_plan_t* plan, const mla_tree_args* args, voi
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     rc = mla::prepare(st, true);
     if (rc != MLA_OK) return rc;
-    mla::TreeMaps maps;
-    rc = mla::encode_maps(plan, args, &maps);
+    mla::TreeMaps maps{};
+    rc = mla::encode_bf16_row_chunks(&maps.kv, args->kv, args->kv_rows, args->row_stride, 64, 2);
+    if (rc == MLA_OK) rc = mla::encode_bf16_row_chunks(&maps.rope, args->kv, args->kv_rows, args->row_stride, 64, 1);
+    if (rc == MLA_OK) rc = mla::encode_q(plan, args, &maps.q, MLA_D_ROW / 64);
     if (rc != MLA_OK) return rc;
     return mla::launch_status(
         mla::launch_tree_attend(maps, mla::params(plan, args, scratch), plan->shape.pdl != 0, st));
@@ -211,12 +164,17 @@ int mla_tree_weights(const mla_tree_plan_t* plan, const mla_tree_args* args, flo
     if (rc == MLA_OK && mla::off(weights, 4)) rc = MLA_EALIGN;
     if (rc == MLA_OK) rc = mla::check_scratch(plan, scratch, scratch_bytes);
     if (rc != MLA_OK) return rc;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    rc = mla::prepare(st, true);
+    if (rc != MLA_OK) return rc;
+    mla::TreeMaps maps{};
+    rc = mla::encode_bf16_row_chunks(&maps.k, args->kv, args->kv_rows, args->row_stride, 128, 1);
+    if (rc == MLA_OK) rc = mla::encode_q(plan, args, &maps.q, 1);
+    if (rc != MLA_OK) return rc;
     mla::TreeParams p = mla::params(plan, args, scratch);
     p.weights = weights;
     p.decay = decay;
-    mla::mla_tree_weights_kernel<<<dim3(plan->num_sms * 4, p.batch), mla::kThreads, 0,
-                                   static_cast<cudaStream_t>(stream)>>>(p);
-    return mla::launch_status(cudaGetLastError());
+    return mla::launch_status(mla::launch_tree_weights(maps, p, plan->shape.pdl != 0, st));
 }
 
 }  // extern "C"

@@ -54,6 +54,8 @@
 namespace mla {
 namespace {
 
+using Cursor = TreeCursor<kTreeTileKeys, true>;
+
 constexpr int kSlots = 4;                                  // of K and of V: a tile each
 constexpr uint32_t kSlotBytes = 16384;                     // 2 column chunks of 64 rows x 128 bytes
 constexpr uint32_t kChunkBytes = 8192;
@@ -69,12 +71,6 @@ constexpr float kRescaleLog2 = 8.0f;                       // move the reference
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr long long kDrainCycles = 2000ll * 1000ll;        // about 1 ms: time for copies in flight after an abort
 
-struct Work {                                              // this cluster's run of units
-    long long count, per;                                  // units of the run, and of every cluster's
-    TreeRequest r;                                         // its first unit
-    int b, rb, tile;
-};
-
 struct __align__(1024) Shared {
     uint8_t k[kSlots][kSlotBytes];                         // this CTA's 64 keys x 128 columns, QK operand
     uint8_t v[kSlots][kSlotBytes];                         // (feature half i, key half kb) at 2 i + kb, PV operand
@@ -88,145 +84,11 @@ struct __align__(1024) Shared {
     uint64_t k_empty[kSlots], v_empty[2], q_empty, s_full[2], o_done;
     uint64_t v_local[2];                                   // V of a tile with drafted rows has landed in this CTA
     uint64_t stall_bar;
-    Work work;
+    TreeWork work;
     uint32_t tmem_base;
     int abort_flag;
 };
 static_assert(sizeof(Shared) <= 227 * 1024, "fits shared memory");
-
-__device__ __forceinline__ int row_blocks(const TreeParams& p, const TreeRequest& r) {
-    return (r.n_tok * p.heads + kTreeBlockRows - 1) / kTreeBlockRows;
-}
-__device__ __forceinline__ int tiles_of(const TreeRequest& r) { return (r.hi + kTreeTileKeys - 1) / kTreeTileKeys; }
-
-// Walks the tiles of a run.
-struct Cursor {
-    TreeRequest r;
-    int b, rb, n_rb, tile, n_tiles;
-    int left;                                              // tiles of the run from here on, this one included
-    int g;                                                 // tiles of the run before this one
-    int item;                                              // row blocks (or parts) before this one
-    bool first;                                            // first tile of its item
-
-    __device__ __forceinline__ void request(const TreeParams& p) {
-        r = load_tree_request(p, b);
-        n_rb = row_blocks(p, r);
-        n_tiles = tiles_of(r);
-    }
-    __device__ __forceinline__ void start(const TreeParams& p, const Work& w) {
-        b = w.b;
-        rb = w.rb;
-        tile = w.tile;
-        left = static_cast<int>(w.count);
-        g = item = 0;
-        first = true;
-        r = w.r;
-        n_rb = row_blocks(p, r);
-        n_tiles = tiles_of(r);
-    }
-    __device__ __forceinline__ bool last() const { return left == 1 || tile == n_tiles - 1; }
-    __device__ __forceinline__ void next(const TreeParams& p) {
-        first = last();
-        if (first) ++item;
-        ++g;
-        --left;
-        if (++tile < n_tiles) return;
-        tile = 0;
-        if (left > 0) next_item(p);
-    }
-    // to the next item's first tile (b, rb, n_tiles alone; there is one)
-    __device__ __forceinline__ void next_item(const TreeParams& p) {
-        if (++rb < n_rb) return;
-        rb = 0;
-        do {
-            ++b;
-            request(p);
-        } while (n_rb == 0 || n_tiles == 0);
-    }
-    // the tile holds drafted rows or rows behind them
-    __device__ __forceinline__ bool special() const { return (tile + 1) * kTreeTileKeys > r.d_pos; }
-};
-
-// Tell both CTAs of the pair to leave their loops (neither exits before both
-// have reached the closing cluster barrier).
-__device__ __forceinline__ void raise_error(Shared& sh, int* status) {
-    st_cluster_s32(map_to_rank(&sh.abort_flag, 0), 1);
-    st_cluster_s32(map_to_rank(&sh.abort_flag, 1), 1);
-    if (status) atomicCAS(status, 0, static_cast<int>(MLA_EDEVICE));
-}
-
-// Quotient of non-negative numbers; 64-bit division is a slow call.
-__device__ __forceinline__ long long quotient(long long a, long long b) {
-    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-    return a / b;
-}
-
-// One warp: this cluster's run.  All units in order of (request, row block,
-// tile); run length = ceil(units / clusters), at least min_tiles.
-__device__ void find_work(const TreeParams& p, int cluster, int lane, Work* out) {
-    auto request_of = [&](int b) {
-        TreeRequest r{};
-        if (b < p.batch) r = load_tree_request(p, b);
-        return r;
-    };
-    auto units_of = [&](const TreeRequest& r) { return static_cast<long long>(row_blocks(p, r)) * tiles_of(r); };
-    TreeRequest r = request_of(lane);                      // requests 0 .. 31 stay in registers
-    long long total = units_of(r);
-    for (int b0 = 32; b0 < p.batch; b0 += 32) total += units_of(request_of(b0 + lane));
-    if (p.batch > 1) {
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    } else {
-        total = __shfl_sync(0xffffffffu, total, 0);
-    }
-    long long per = quotient(total + p.clusters - 1, p.clusters);
-    if (per < p.min_tiles) per = p.min_tiles;
-    const long long u0 = per * cluster;
-    const long long count = u0 >= total ? 0 : (total - u0 < per ? total - u0 : per);
-    if (lane == 0) {
-        out->per = per;
-        out->count = count;
-    }
-    long long before = 0;
-    for (int b0 = 0; b0 < p.batch && count > 0; b0 += 32) {
-        if (b0 > 0) r = request_of(b0 + lane);
-        const long long u = units_of(r);
-        long long incl = u;
-        if (p.batch > 1) {
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += y;
-            }
-        }
-        const long long first = before + incl - u;         // this lane's request is units [first, first + u)
-        const bool here = u0 >= first && u0 < first + u;
-        if (here) {
-            const int n_tiles = tiles_of(r);
-            out->rb = static_cast<int>(quotient(u0 - first, n_tiles));
-            out->tile = static_cast<int>(u0 - first - static_cast<long long>(out->rb) * n_tiles);
-            out->b = b0 + lane;
-            out->r = r;
-        }
-        if (__any_sync(0xffffffffu, here)) break;
-        before += __shfl_sync(0xffffffffu, incl, 31);
-    }
-}
-
-// Bounded wait whose usual case (the phase is over) is one instruction inline.
-__device__ __noinline__ bool wait_slowly(uint64_t* bar, uint32_t parity, int* abort_flag) {
-    return mbar_wait_bounded(bar, parity, abort_flag);
-}
-__device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity) {
-    return mbar_try_wait(bar, parity) || wait_slowly(bar, parity, &sh.abort_flag);
-}
-// The same by a whole warp (every thread polls: with one lane polling for the
-// others each hand-off took longer), with one answer for all of its lanes.
-__device__ __forceinline__ bool warp_wait(Shared& sh, uint64_t* bar, uint32_t parity) {
-    const bool ok = __all_sync(0xffffffffu, wait(sh, bar, parity));
-    tc_fence_after_sync();
-    return ok;
-}
 
 // ============================== producer ==================================
 struct Producer {
@@ -304,7 +166,7 @@ __device__ void produce(const TreeMaps& maps, const TreeParams& p, Shared& sh, u
         else
             ok = (!c.first || pr.load_q(c)) && pr.load_k(c);
     }
-    if (!ok) raise_error(sh, p.status);
+    if (!ok) raise_tree_error(&sh.abort_flag, p.status);
 }
 
 // ============================== MMA issue ==================================
@@ -421,7 +283,7 @@ __device__ void issue(const TreeParams& p, Shared& sh, uint32_t tmem) {
         }
         pv_first = qk_first;
     }
-    if (!is.ok && is.lead) raise_error(sh, p.status);
+    if (!is.ok && is.lead) raise_tree_error(&sh.abort_flag, p.status);
 }
 
 // ============================== softmax ====================================
@@ -507,7 +369,7 @@ __device__ void softmax(const TreeParams& p, Shared& sh, uint32_t tmem, uint32_t
         do {
             const int g = c.g, buf = g & 1;
             last = c.last();
-            bool w = warp_wait(sh, &sh.s_full[buf], (g >> 1) & 1);
+            bool w = warp_wait(&sh.abort_flag, &sh.s_full[buf], (g >> 1) & 1);
             uint32_t s[32];
             if (w) {
                 tmem_ld32_async(tmem + lanes + kTmemS + 64 * buf + 32 * sub, s);
@@ -557,7 +419,7 @@ __device__ void softmax(const TreeParams& p, Shared& sh, uint32_t tmem, uint32_t
             }
             l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             // P of the tile before has been read, and O holds all tiles before this one
-            w = g == 0 || warp_wait(sh, &sh.o_done, (g - 1) & 1);
+            w = g == 0 || warp_wait(&sh.abort_flag, &sh.o_done, (g - 1) & 1);
             if (w && __any_sync(0xffffffffu, alpha != 1.f)) {   // (never on an item's first tile)
 #pragma unroll 1
                 for (int j = 0; j < 8; ++j) {
@@ -576,7 +438,7 @@ __device__ void softmax(const TreeParams& p, Shared& sh, uint32_t tmem, uint32_t
                              pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
             if (c.special()) {
                 // V was loaded for this CTA's own eyes
-                w = w && warp_wait(sh, &sh.v_local[specials & 1], (specials >> 1) & 1);
+                w = w && warp_wait(&sh.abort_flag, &sh.v_local[specials & 1], (specials >> 1) & 1);
                 ++specials;
                 if (w) clean_v(sh, c, tid);
             }
@@ -616,7 +478,7 @@ __device__ void softmax(const TreeParams& p, Shared& sh, uint32_t tmem, uint32_t
             merge.rows = min(kTreeBlockRows, live_rows - rb * kTreeBlockRows);
             merge.pieces = 1 + static_cast<int>((n_tiles - done + sh.work.per - 1) / sh.work.per);
         }
-        const bool w = warp_wait(sh, &sh.o_done, (c.g - 1) & 1);
+        const bool w = warp_wait(&sh.abort_flag, &sh.o_done, (c.g - 1) & 1);
         if (named_barrier_or(kBarSoftmax, kSoftmaxThreads, !w)) {
             ok = false;
             break;
@@ -652,7 +514,7 @@ __device__ void softmax(const TreeParams& p, Shared& sh, uint32_t tmem, uint32_t
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(o_bar);
     }
-    if (!ok && lane == 0) raise_error(sh, p.status);
+    if (!ok && lane == 0) raise_tree_error(&sh.abort_flag, p.status);
     if (rank == 0 && tid == 0) p.merge[cluster] = merge;
 }
 
@@ -705,7 +567,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == kMmaWarp) tmem_alloc_pair(&sh.tmem_base, kTmemCols);
     grid_dependency_wait();
     allow_dependent_launch();
-    if (warp == kProducerWarp) find_work(p, cluster, lane, &sh.work);
+    if (warp == kProducerWarp) Cursor::find_work(p, cluster, lane, &sh.work);
     tc_fence_before_sync();
     __syncthreads();
     cluster_wait();                                        // both CTAs' barriers are initialised
@@ -714,10 +576,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (p.stall_test && blockIdx.x == 0 && tid == 32 * kProducerWarp) {
         // test hook: a wait that runs out, so the abort path runs for real
         volatile int never = 0;
-        if (!mbar_wait_bounded(&sh.stall_bar, 0, &never, kStallTestCycles)) raise_error(sh, p.status);
+        if (!mbar_wait_bounded(&sh.stall_bar, 0, &never, kStallTestCycles)) raise_tree_error(&sh.abort_flag, p.status);
     }
     // the dynamic window starts 1024-byte aligned (the 128-byte swizzle needs it)
-    if ((smem_u32(smem_raw) & 1023u) != 0 && tid == 0) raise_error(sh, p.status);
+    if ((smem_u32(smem_raw) & 1023u) != 0 && tid == 0) raise_tree_error(&sh.abort_flag, p.status);
     if (warp == kProducerWarp) {
         if (lane == 0) produce(maps, p, sh, rank, false);
     } else if (warp == kValueWarp) {
@@ -899,11 +761,9 @@ __global__ void __launch_bounds__(kMergeThreads) mla_tree_merge_kernel(const __g
 
 }  // namespace
 
-size_t tree_attend_smem_bytes() { return sizeof(Shared); }
-
 cudaError_t tree_attend_prepare() {
     return cudaFuncSetAttribute(mla_tree_attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(tree_attend_smem_bytes()));
+                                static_cast<int>(sizeof(Shared)));
 }
 
 cudaError_t launch_tree_attend(const TreeMaps& maps, const TreeParams& p, bool pdl, cudaStream_t stream) {
@@ -913,7 +773,7 @@ cudaError_t launch_tree_attend(const TreeMaps& maps, const TreeParams& p, bool p
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * p.clusters);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = tree_attend_smem_bytes();
+    cfg.dynamicSmemBytes = sizeof(Shared);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;

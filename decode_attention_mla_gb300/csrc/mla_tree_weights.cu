@@ -1,0 +1,429 @@
+// mla_tree_weights.cu -- attention weight that each cache row gets from a
+// call's tokens and heads (mla_tree_weights in include/mla_tree.h):
+//   w[t] = decay w[t] + sum_r exp(s_rt - lse_r),     s = Q K^T * scale
+//
+// The log-sum-exps are known, so one pass over the cache is enough.  The scores
+// are taken with the cache rows on M, on pairs of SMs (tcgen05 cta_group::2):
+//   S^T[256 cache rows x 128 query rows] = K Q^T: 36 MMAs, 128 cache rows and
+//   64 query rows from each CTA's shared memory
+// so a cache row is one tensor-memory lane, its weight a sum over the lane's
+// columns, and no sum crosses threads but that of the two column halves.
+//
+// Bound: the cache's bytes for up to 256 query rows, the tensor cores above.
+// Staging by TMA, in one of three forms chosen by the most query rows a request
+// can have:
+//   up to 128   queries resident (72 KB), K in 9 slots of 16 KB
+//   up to 256   queries resident (144 KB), K in 4 slots
+//   more        K of the tile resident (9 slots), the query blocks streamed past
+//               it from L2 through 9 slots of 8 KB: each cache row is read once
+//               however many query rows there are
+// The units (request, tile of 256 cache rows) are cut into equal runs, one per
+// pair, from the lengths on the device.
+//
+// Warps of a CTA: 0-7 weights (warps w and w + 4 share cache rows and split the
+// columns), 8 TMA of K, 9 MMA issue (even CTA) and tensor memory, 10 TMA of Q.
+// Waits are bounded as in the attention kernel.
+#include <cmath>
+
+#include "mla_tree.cuh"
+
+namespace mla {
+namespace {
+
+constexpr int kTileKeys = 256;                             // cache rows per tile of a pair
+using Cursor = TreeCursor<kTileKeys, false>;
+
+constexpr int kChunks = 9;                                 // 64-column chunks of a row
+constexpr uint32_t kKChunkBytes = 16384;                   // 128 cache rows
+constexpr uint32_t kQChunkBytes = 8192;                    // 64 query rows
+constexpr uint32_t kQBlockBytes = kChunks * kQChunkBytes;
+constexpr int kSumWarps = 8;
+constexpr int kSumThreads = 32 * kSumWarps;
+constexpr int kKWarp = 8, kMmaWarp = 9, kQWarp = 10;
+constexpr int kThreads = 352;
+constexpr int kBarSum = 1;
+constexpr uint32_t kTmemCols = 512;
+constexpr long long kDrainCycles = 2000ll * 1000ll;
+
+// Form of the staging: kBlocks query blocks resident, or (0) streamed.
+template <int kBlocks>
+struct Cfg {
+    static constexpr bool kStream = kBlocks == 0;
+    static constexpr int kKSlots = kBlocks == 2 ? 4 : 9;
+    static constexpr int kQBuffers = kBlocks == 2 ? 2 : 1;
+    static constexpr int kScoreCols = kBlocks == 2 ? 256 : 128;   // of one of the two score buffers
+};
+
+template <int kBlocks>
+struct __align__(1024) Shared {
+    using C = Cfg<kBlocks>;
+    uint8_t k[C::kKSlots][kKChunkBytes];
+    uint8_t q[C::kQBuffers * kChunks][kQChunkBytes];       // resident blocks, or a ring of 9 chunks
+    float lse2[2][128];                                    // base 2; +inf: the row adds nothing
+    uint8_t token[2][128];
+    float half_sum[2][128];
+    // used in the even CTA
+    uint64_t k_ready[C::kKSlots], q_ready[kChunks], s_free[2];
+    // in each CTA
+    uint64_t k_empty[C::kKSlots], q_empty[kChunks], s_full[2];
+    uint64_t stall_bar;
+    TreeWork work;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+static_assert(sizeof(Shared<0>) <= 227 * 1024 && sizeof(Shared<1>) <= 227 * 1024 && sizeof(Shared<2>) <= 227 * 1024,
+              "fits shared memory");
+
+// Query blocks of a request (one, of rows that all add nothing, if it has no tokens).
+__device__ __forceinline__ int query_blocks(const TreeParams& p, const TreeRequest& r) {
+    return max(1, (r.n_tok * p.heads + kTreeBlockRows - 1) / kTreeBlockRows);
+}
+
+template <int kBlocks>
+__device__ __forceinline__ uint32_t expect(Shared<kBlocks>&, uint64_t* bar, uint32_t bytes, uint32_t rank) {
+    if (rank == 0) mbar_arrive_expect_tx(bar, 2 * bytes);
+    return map_to_rank(bar, 0);
+}
+
+template <int kBlocks>
+__device__ void produce_k(const TreeMaps& maps, const TreeParams& p, Shared<kBlocks>& sh, uint32_t rank) {
+    using C = Cfg<kBlocks>;
+    const uint64_t policy = l2_policy_evict_first();
+    uint32_t slot = 0, round = 0;
+    bool ok = true;
+    Cursor c;
+    for (c.start(p, sh.work); c.left > 0 && ok; c.next(p)) {
+        const int y = static_cast<int>(c.r.base) + c.tile * kTileKeys + static_cast<int>(rank) * 128;
+#pragma unroll 1
+        for (int s = 0; s < kChunks && ok; ++s) {
+            ok = round == 0 || mbar_wait_bounded(&sh.k_empty[slot], (round - 1) & 1, &sh.abort_flag);
+            if (ok)
+                tma_load_3d_pair(sh.k[slot], &maps.k, 0, y, s, expect(sh, &sh.k_ready[slot], kKChunkBytes, rank),
+                                 policy);
+            if (++slot == C::kKSlots) {
+                slot = 0;
+                ++round;
+            }
+        }
+    }
+    if (!ok) raise_tree_error(&sh.abort_flag, p.status);
+}
+
+template <int kBlocks>
+__device__ void produce_q(const TreeMaps& maps, const TreeParams& p, Shared<kBlocks>& sh, uint32_t rank) {
+    using C = Cfg<kBlocks>;
+    const uint64_t policy = l2_policy_evict_normal();
+    uint32_t round = 0;                                    // times the query buffers were filled
+    bool ok = true;
+    Cursor c;
+    for (c.start(p, sh.work); c.left > 0 && ok; c.next(p)) {
+        const int row = c.b * p.tokens * p.heads + static_cast<int>(rank) * 64;
+        const int blocks = query_blocks(p, c.r);
+        if constexpr (C::kStream) {
+            for (int rb = 0; rb < blocks && ok; ++rb, ++round) {
+#pragma unroll 1
+                for (int s = 0; s < kChunks && ok; ++s) {
+                    ok = round == 0 || mbar_wait_bounded(&sh.q_empty[s], (round - 1) & 1, &sh.abort_flag);
+                    if (ok)
+                        tma_load_3d_pair(sh.q[s], &maps.q, 0, row + rb * kTreeBlockRows, s,
+                                         expect(sh, &sh.q_ready[s], kQChunkBytes, rank), policy);
+                }
+            }
+        } else if (c.first) {
+            // a request's blocks stay for its part of the run
+            ok = round == 0 || mbar_wait_bounded(&sh.q_empty[0], (round - 1) & 1, &sh.abort_flag);
+            if (ok) {
+                const uint32_t bar = expect(sh, &sh.q_ready[0], blocks * kQBlockBytes, rank);
+                for (int i = 0; i < blocks * kChunks; ++i)
+                    tma_load_3d_pair(sh.q[i], &maps.q, 0, row + (i / kChunks) * kTreeBlockRows, i % kChunks, bar,
+                                     policy);
+            }
+            ++round;
+        }
+    }
+    if (!ok) raise_tree_error(&sh.abort_flag, p.status);
+}
+
+// The whole warp walks and waits, one lane issues; barriers are looked at ahead
+// of the MMAs before their use (a look never blocks).
+template <int kBlocks>
+__device__ void issue(const TreeParams& p, Shared<kBlocks>& sh, uint32_t tmem) {
+    using C = Cfg<kBlocks>;
+    constexpr uint32_t idesc = make_idesc_bf16(256, 128, 0, 0);
+    const bool lead = elect_one();
+    const uint64_t kd = make_sdesc(smem_u32(sh.k), 16, 1024, kLayoutSw128);
+    const uint64_t qd = make_sdesc(smem_u32(sh.q), 16, 1024, kLayoutSw128);
+    bool ok = true;
+    auto need = [&](bool seen, uint64_t* bar, uint32_t parity) {
+        if (!seen) ok = wait_slowly(bar, parity, &sh.abort_flag) && ok;
+    };
+    uint32_t slot = 0, k_par = 0;
+    uint32_t n = 0;                                        // score buffers filled so far
+    uint32_t q_round = 0;
+    bool see_k = false, see_q = false;
+    Cursor c;
+    for (c.start(p, sh.work); c.left > 0 && ok; c.next(p)) {
+        const int blocks = query_blocks(p, c.r);
+        if constexpr (C::kStream) {
+            for (int rb = 0; rb < blocks && ok; ++rb, ++n) {
+                const uint32_t buf = n & 1, q_par = n & 1;
+                const uint32_t d = tmem + C::kScoreCols * buf;
+                if (n >= 2) need(false, &sh.s_free[buf], ((n >> 1) - 1) & 1);
+                tc_fence_after_sync();
+#pragma unroll
+                for (int s = 0; s < kChunks; ++s) {
+                    if (rb == 0) need(false, &sh.k_ready[s], c.g & 1);
+                    need(see_q, &sh.q_ready[s], q_par);
+                    if (s + 1 < kChunks) see_q = mbar_test(&sh.q_ready[s + 1], q_par);
+                    if (lead && ok) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            umma_pair_bf16(d, kd + ((s * kKChunkBytes + k * 32u) >> 4),
+                                           qd + ((s * kQChunkBytes + k * 32u) >> 4), idesc, (s | k) ? 1u : 0u);
+                        umma_commit_pair(&sh.q_empty[s]);
+                        if (rb == blocks - 1) umma_commit_pair(&sh.k_empty[s]);
+                    }
+                }
+                see_q = false;
+                if (lead && ok) umma_commit_pair(&sh.s_full[buf]);
+            }
+        } else {
+            const uint32_t buf = n & 1;
+            const uint32_t d = tmem + C::kScoreCols * buf;
+            if (c.first) need(false, &sh.q_ready[0], q_round & 1);
+            if (n >= 2) need(false, &sh.s_free[buf], ((n >> 1) - 1) & 1);
+            tc_fence_after_sync();
+#pragma unroll
+            for (int s = 0; s < kChunks; ++s) {
+                const uint32_t at = slot;
+                need(see_k, &sh.k_ready[at], k_par);
+                if (++slot == C::kKSlots) {
+                    slot = 0;
+                    k_par ^= 1;
+                }
+                see_k = mbar_test(&sh.k_ready[slot], k_par);
+                if (lead && ok) {
+                    const uint64_t ka = kd + (at * kKChunkBytes >> 4);
+#pragma unroll
+                    for (int rb = 0; rb < kBlocks; ++rb)
+                        if (rb < blocks) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                umma_pair_bf16(d + 128 * rb, ka + (k * 32u >> 4),
+                                               qd + ((rb * kQBlockBytes + s * kQChunkBytes + k * 32u) >> 4), idesc,
+                                               (s | k) ? 1u : 0u);
+                        }
+                    umma_commit_pair(&sh.k_empty[at]);
+                }
+            }
+            if (lead && ok) {
+                umma_commit_pair(&sh.s_full[buf]);
+                if (c.last()) umma_commit_pair(&sh.q_empty[0]);
+            }
+            if (c.last()) ++q_round;
+            ++n;
+        }
+    }
+    if (!ok && lead) raise_tree_error(&sh.abort_flag, p.status);
+}
+
+template <int kBlocks>
+__device__ void add_weights(const TreeParams& p, Shared<kBlocks>& sh, uint32_t tmem, uint32_t rank, int tid) {
+    using C = Cfg<kBlocks>;
+    const int lane = tid & 31, warp = tid >> 5;
+    const int sub = warp >> 2;                             // columns 64 sub .. of a block
+    const int key = 32 * (warp & 3) + lane;                // of this CTA's 128
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_bar = map_to_rank(&sh.s_free[0], 0);
+    const float c2 = p.scale_log2;
+    uint32_t n = 0;
+    bool bad = false;
+    bool careful[2] = {false, false};                      // the block has rows that add nothing
+    Cursor c;
+    c.start(p, sh.work);
+    for (; c.left > 0; c.next(p)) {
+        const int live = c.r.n_tok * p.heads;
+        const int blocks = query_blocks(p, c.r);
+        const int t = c.tile * kTileKeys + static_cast<int>(rank) * 128 + key;
+        const bool mine = sub == 0 && t >= c.r.lo && t < c.r.hi;
+        float* dst = p.weights + c.r.base + t;
+        const float old = mine && p.decay != 0.f ? *dst : 0.f;
+        const bool special = c.special();
+        // which tokens attend a drafted row (bit per token)
+        unsigned long long seen_by = ~0ull;
+        if (special && t >= c.r.d_pos) {
+            seen_by = 0;
+            const int j = t - c.r.d_pos;
+            if (j < c.r.n_tok)
+                for (int i = 0; i < c.r.n_tok; ++i) seen_by |= (tree_mask(p, c.b, i, c.r.n_tok) >> j & 1ull) << i;
+        }
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int rb = 0; rb < blocks; ++rb) {
+            const int at = C::kStream ? (n & 1) : rb;      // place of the block's log-sum-exps
+            if (C::kStream || c.first) {
+                // (their last readers have passed a barrier since: the one of the block or
+                // tile before)
+                bool none = false;
+                if (tid < 128) {
+                    const int r = rb * kTreeBlockRows + tid;
+                    float l = -INFINITY;
+                    if (r < live) l = p.a.lse[static_cast<long long>(c.b) * p.tokens * p.heads + r];
+                    none = l == -INFINITY;
+                    sh.lse2[at][tid] = none ? INFINITY : l * kLog2e;
+                    sh.token[at][tid] = static_cast<uint8_t>(min(r / p.heads, 63));
+                }
+                careful[at] = named_barrier_or(kBarSum, kSumThreads, none);
+            }
+            const uint32_t buf = n & 1;
+            if (C::kStream || rb == 0) bad |= !warp_wait(&sh.abort_flag, &sh.s_full[buf], (n >> 1) & 1);
+            const int columns = min(kTreeBlockRows, max(live - rb * kTreeBlockRows, 0));
+            const uint32_t d = tmem + lanes + C::kScoreCols * buf + (C::kStream ? 0 : 128 * rb) + 64 * sub;
+#pragma unroll 1
+            for (int j = 0; j < 2; ++j) {
+                const int col = 64 * sub + 32 * j;
+                if (col >= columns || bad) break;          // warp-uniform
+                uint32_t s[32];
+                tmem_ld32_async(d + 32 * j, s);
+                tmem_wait_ld32(s);
+                const float4* l4 = reinterpret_cast<const float4*>(&sh.lse2[at][col]);
+                if (!special && !careful[at]) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 l = l4[i];
+                        sum[0] += ex2_approx(fmaf(__uint_as_float(s[4 * i]), c2, -l.x));
+                        sum[1] += ex2_approx(fmaf(__uint_as_float(s[4 * i + 1]), c2, -l.y));
+                        sum[2] += ex2_approx(fmaf(__uint_as_float(s[4 * i + 2]), c2, -l.z));
+                        sum[3] += ex2_approx(fmaf(__uint_as_float(s[4 * i + 3]), c2, -l.w));
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float l = sh.lse2[at][col + i];
+                        const bool adds = l != INFINITY && (seen_by >> sh.token[at][col + i] & 1ull);
+                        const float x = ex2_approx(fmaf(__uint_as_float(s[i]), c2, -l));
+                        sum[i & 3] += adds ? x : 0.f;
+                    }
+                }
+            }
+            if (C::kStream || rb == blocks - 1) {
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0 && !bad) mbar_arrive_peer(s_bar + 8 * buf);   // the score buffer is free
+                ++n;
+            }
+        }
+        const float total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        if (sub == 1) sh.half_sum[c.g & 1][key] = total;
+        if (named_barrier_or(kBarSum, kSumThreads, bad)) break;
+        if (mine) *dst = (p.decay != 0.f ? p.decay * old : 0.f) + (total + sh.half_sum[c.g & 1][key]);
+    }
+    if (bad && lane == 0) raise_tree_error(&sh.abort_flag, p.status);
+}
+
+template <int kBlocks>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    mla_tree_weights_kernel(const __grid_constant__ TreeMaps maps, const __grid_constant__ TreeParams p) {
+    using C = Cfg<kBlocks>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    Shared<kBlocks>& sh = *reinterpret_cast<Shared<kBlocks>*>(smem_raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int cluster = blockIdx.x >> 1;
+    if (tid == 0) {
+        prefetch_tensormap(&maps.k);
+        prefetch_tensormap(&maps.q);
+        for (int i = 0; i < C::kKSlots; ++i) {
+            mbar_init(&sh.k_ready[i], 1);
+            mbar_init(&sh.k_empty[i], 1);
+        }
+        for (int i = 0; i < kChunks; ++i) {
+            mbar_init(&sh.q_ready[i], 1);
+            mbar_init(&sh.q_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.s_free[i], 2 * kSumWarps);
+        }
+        mbar_init(&sh.stall_bar, 1);
+        sh.abort_flag = 0;
+        mbar_init_fence();
+    }
+    __syncwarp();
+    cluster_arrive();
+    if (warp == kMmaWarp) tmem_alloc_pair(&sh.tmem_base, kTmemCols);
+    grid_dependency_wait();
+    allow_dependent_launch();
+    if (warp == kKWarp) Cursor::find_work(p, cluster, lane, &sh.work);
+    tc_fence_before_sync();
+    __syncthreads();
+    cluster_wait();                                        // both CTAs' barriers are initialised
+    tc_fence_after_sync();
+    const uint32_t tmem = sh.tmem_base;
+    if (p.stall_test && blockIdx.x == 0 && tid == 32 * kKWarp) {
+        // test hook: a wait that runs out, so the abort path runs for real
+        volatile int never = 0;
+        if (!mbar_wait_bounded(&sh.stall_bar, 0, &never, kStallTestCycles)) raise_tree_error(&sh.abort_flag, p.status);
+    }
+    // the dynamic window starts 1024-byte aligned (the 128-byte swizzle needs it)
+    if ((smem_u32(smem_raw) & 1023u) != 0 && tid == 0) raise_tree_error(&sh.abort_flag, p.status);
+    if (warp == kKWarp) {
+        if (lane == 0) produce_k(maps, p, sh, rank);
+    } else if (warp == kQWarp) {
+        if (lane == 0) produce_q(maps, p, sh, rank);
+    } else if (warp == kMmaWarp) {
+        if (rank == 0) issue(p, sh, tmem);
+    } else {
+        add_weights(p, sh, tmem, rank, tid);
+    }
+    __syncthreads();
+    if (*static_cast<volatile int*>(&sh.abort_flag)) {
+        // nothing more is issued by this CTA: let its copies and MMAs end
+        const long long t0 = clock64();
+        while (clock64() - t0 < kDrainCycles) {
+        }
+    }
+    tc_fence_before_sync();
+    cluster_barrier();
+    if (warp == kMmaWarp) {
+        tc_fence_after_sync();
+        tmem_dealloc_pair(tmem, kTmemCols);
+    }
+}
+
+template <int kBlocks>
+cudaError_t prepare_one() {
+    return cudaFuncSetAttribute(mla_tree_weights_kernel<kBlocks>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(sizeof(Shared<kBlocks>)));
+}
+template <int kBlocks>
+cudaError_t launch_one(const TreeMaps& maps, const TreeParams& p, bool pdl, cudaStream_t stream) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * p.clusters);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = sizeof(Shared<kBlocks>);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, mla_tree_weights_kernel<kBlocks>, maps, p);
+}
+
+}  // namespace
+
+cudaError_t tree_weights_prepare() {
+    cudaError_t e = prepare_one<0>();
+    if (e == cudaSuccess) e = prepare_one<1>();
+    if (e == cudaSuccess) e = prepare_one<2>();
+    return e;
+}
+
+cudaError_t launch_tree_weights(const TreeMaps& maps, const TreeParams& p, bool pdl, cudaStream_t stream) {
+    const int blocks = (p.tokens * p.heads + kTreeBlockRows - 1) / kTreeBlockRows;
+    if (blocks == 1) return launch_one<1>(maps, p, pdl, stream);
+    if (blocks == 2) return launch_one<2>(maps, p, pdl, stream);
+    return launch_one<0>(maps, p, pdl, stream);
+}
+
+}  // namespace mla
