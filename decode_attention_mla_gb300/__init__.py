@@ -141,6 +141,8 @@ EXPORTED = ("mla_decode_abi_version", "mla_decode_plan", "mla_decode_run", "mla_
 def lib():
     """The loaded library; raises RuntimeError if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -222,9 +224,26 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr())
 
 
+_torch = None
+_raw_stream = None
+
+
+def _tc():
+    """The torch module, imported on first use (and the current stream's raw getter, where this
+    torch has it: building a Stream object costs as much as a launch)."""
+    global _torch, _raw_stream
+    if _torch is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _torch = torch
+    return _torch
+
+
 def _stream(stream):
     if stream is None:
-        import torch
+        torch = _torch or _tc()
+        if _raw_stream is not None:
+            return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
@@ -379,22 +398,22 @@ def advance(d_pos, stream=None) -> None:
 # pass them on.  The returned structures keep their tensors alive.
 
 def _need(t, name, dtypes, shape=None, contiguous=True):
-    """Check a tensor of a call: CUDA, on the current device, type, shape, layout."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    """Check a tensor of a call (CUDA, on the current device, type, shape, layout); its address."""
+    torch = _torch or _tc()
+    if not isinstance(t, torch.Tensor) or t.get_device() < 0:
         raise ValueError(f"{name}: a CUDA tensor is needed (tensors passed to the MLA decode kernels must be "
                          "CUDA tensors)")
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != torch.cuda.current_device():
         raise ValueError(f"{name} is on {t.device}, the current device is {torch.cuda.current_device()}")
-    if not isinstance(dtypes, tuple):
-        dtypes = (dtypes,)
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
-    if shape is not None and (t.dim() != len(shape) or any(e is not None and e != s for s, e in zip(t.shape, shape))):
+    if t.dtype is not dtypes and (type(dtypes) is not tuple or t.dtype not in dtypes):
+        names = " or ".join(map(str, dtypes)) if type(dtypes) is tuple else dtypes
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {names}")
+    if shape is not None and t.shape != shape and (
+            t.dim() != len(shape) or any(e is not None and e != n for n, e in zip(t.shape, shape))):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple('*' if e is None else e for e in shape)}")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _maybe(t, name, dtypes, shape):
@@ -403,9 +422,9 @@ def _maybe(t, name, dtypes, shape):
 
 def _cache(kv, kv_rows, row_stride, fp8_ok=True):
     """(pointer, rows, row stride, fp8) of a cache tensor [rows, >= 576 columns]."""
-    import torch
-    fp8 = (torch.uint8, torch.float8_e4m3fn) if fp8_ok else ()
-    p = _need(kv, "kv", (torch.bfloat16,) + fp8, contiguous=False)
+    torch = _torch or _tc()
+    p = _need(kv, "kv", (torch.bfloat16, torch.uint8, torch.float8_e4m3fn) if fp8_ok else torch.bfloat16,
+              contiguous=False)
     if kv.dim() != 2 or kv.shape[1] != D_ROW or kv.stride(1) != 1:
         raise ValueError("kv must be [rows, 576] with contiguous rows")
     if kv.shape[0] == 0:
@@ -420,7 +439,7 @@ def _cache(kv, kv_rows, row_stride, fp8_ok=True):
 
 def _strides(t, name, shape, last):
     """Pointer and leading strides of a bf16 tensor whose last dimension is contiguous."""
-    import torch
+    torch = _torch or _tc()
     p = _need(t, name, torch.bfloat16, shape, contiguous=False)
     if t.stride(-1) != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
@@ -455,7 +474,7 @@ def rope_table(rot_dim: int = D_ROPE, base: float = 10000.0, *, interleaved: boo
                amplitude: float = 1.0, device=None) -> RopeTable:
     """Rotation table on the device: pairs (2j, 2j+1) if ``interleaved``, else (j, j + rot_dim/2);
     ``scaling``: "none", "linear" or "yarn"; ``amplitude`` multiplies sines and cosines."""
-    import torch
+    torch = _torch or _tc()
     turns = rope_turns(rot_dim, base, scaling=scaling, factor=factor, original_ctx=original_ctx,
                        beta_fast=beta_fast, beta_slow=beta_slow)
     t = torch.tensor(turns, dtype=torch.int64, device=device or "cuda")       # all below 2^62
@@ -472,7 +491,7 @@ def rope_make_args(table: RopeTable, positions, *, q_rope=None, q=None, c=None, 
     bf16 [B, N, 64] go to cache row ``row_offset[b] + d_pos[b] + n`` of ``kv`` (bf16, or E4M3 bytes of
     value / ``kv_scale``); ``row_positions`` (int32 [rows]) takes the positions, ``row_weights``
     (fp32 [rows]) zeros.  Either part may be left out."""
-    import torch
+    torch = _torch or _tc()
     B, N = positions.shape
     a = RopeArgs(batch=int(B), tokens=int(N), rot_dim=table.rot_dim, interleaved=int(table.interleaved),
                  amplitude=table.amplitude, turns=_need(table.turns, "table", torch.int64),
@@ -543,7 +562,7 @@ def tree_make_args(q, kv, out, lse, *, d_pos, row_offset=None, mask=None, n_toke
 
     ``q``: bf16 [B, Q, H, 576]; ``kv``: bf16 [rows, 576]; ``out``: bf16 or fp32 [B, Q, H, 512]; ``lse``: fp32
     [B, Q, H]; ``mask``: int64 [B, Q], bit j of word i: token i attends drafted token j (None: a chain)."""
-    import torch
+    torch = _torch or _tc()
     if q.dim() != 4:
         raise ValueError("q must be [B, Q, H, 576]")
     B, Q, H, _ = q.shape
@@ -583,7 +602,7 @@ def tree_forward(p: TreePlan, q, kv, out, lse, scratch, *, stream=None, **kw) ->
 
 def tree_weights_args(p: TreePlan, a: TreeArgs, scratch, weights, *, decay: float = 1.0, stream=None) -> None:
     """``mla_tree_weights`` with prebuilt arguments: ``weights`` fp32 [rows], one entry per cache row."""
-    import torch
+    torch = _torch or _tc()
     _tree_dims(p, a)
     w = _side(weights, "weights", torch.float32, a.kv_rows)
     sp, sb = _scratch_args(scratch)
@@ -601,23 +620,22 @@ def tree_commit(kv, accept, n_accept, *, d_pos, d_pos_out=None, row_offset=None,
                 row_weights=None, kv_rows: int | None = None, row_stride: int | None = None, stream=None) -> None:
     """``mla_tree_commit``: rows ``d_pos + accept[b, k]`` move to ``d_pos + k`` for k < n_accept[b]
     (``accept``: int32 [B, Q]); ``d_pos_out`` (may be ``d_pos``) takes d_pos + n_accept."""
-    import torch
+    torch = _torch or _tc()
     B, Q = accept.shape
+    i32 = torch.int32
     kvp, rows, stride, fp8 = _cache(kv, kv_rows, row_stride)
-    a = TreeCommitArgs(kv=kvp, kv_rows=rows, row_stride=stride, kv_fp8=fp8, batch=int(B), tokens=int(Q),
-                       accept=_need(accept, "accept", torch.int32, (B, Q)),
-                       n_accept=_need(n_accept, "n_accept", torch.int32, (B,)),
-                       d_pos=_need(d_pos, "d_pos", torch.int32, (B,)),
-                       d_pos_out=_maybe(d_pos_out, "d_pos_out", torch.int32, (B,)),
-                       row_offset=_maybe(row_offset, "row_offset", torch.int64, (B,)),
-                       row_positions=_side(row_positions, "row_positions", torch.int32, rows),
-                       row_weights=_side(row_weights, "row_weights", torch.float32, rows))
+    a = TreeCommitArgs(kvp, rows, stride, fp8, B, Q, _need(accept, "accept", i32),
+                       _need(n_accept, "n_accept", i32, (B,)), _need(d_pos, "d_pos", i32, (B,)),
+                       _maybe(d_pos_out, "d_pos_out", i32, (B,)),
+                       _maybe(row_offset, "row_offset", torch.int64, (B,)),
+                       _side(row_positions, "row_positions", i32, rows),
+                       _side(row_weights, "row_weights", torch.float32, rows))
     _check(lib().mla_tree_commit(ctypes.byref(a), _stream(stream)), "mla_tree_commit")
 
 
 def evict_alloc_scratch(*, batch: int, keep: int, device=None):
     """Scratch of :func:`evict` for a batch and a budget."""
-    import torch
+    torch = _torch or _tc()
     n = int(lib().mla_evict_scratch_bytes(batch, keep))
     if n == 0:
         raise ValueError("batch must be 1 .. 65535 and keep at least 1")
@@ -630,7 +648,7 @@ def evict_make_args(kv, weights, positions, *, d_pos, next_pos, keep: int, sink:
     """Arguments of :func:`evict_args`.  ``weights`` fp32 [rows] and ``positions`` int32 [rows] have an entry
     per cache row; the ``*_out`` tensors default to the inputs (in place).  ``max_rows``: largest ``d_pos``
     expected (sizes the launch; default: the cache's rows)."""
-    import torch
+    torch = _torch or _tc()
     B = int(d_pos.shape[0])
     kvp, rows, stride, fp8 = _cache(kv, kv_rows, row_stride)
     wo = weights if weights_out is None else weights_out
