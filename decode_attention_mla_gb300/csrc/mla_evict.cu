@@ -8,14 +8,15 @@
 // of CTAs per request that read each other's histograms (distributed shared
 // memory); the keys stay in shared memory between the passes when they fit.
 // Rows above K stay, and of the rows equal to K the first so many that `keep`
-// is met; prefix counts over ballots (warp, CTA, cluster) number the evicted
-// rows below `keep` and the kept rows behind it in ascending order, which
-// pairs them up.  Integers only: no order of execution shows in the result.
+// is met; counts by ballots, summed over warps, CTA and cluster, number the
+// evicted rows below `keep` and the kept rows behind it in ascending order,
+// which pairs them up.  Integers only: no order of execution shows in the result.
 //
 // Move.  A warp copies four bf16 rows (eight E4M3 rows) at a time, nine
 // 16-byte loads in flight per lane; source rows lie at or behind `keep` and
 // destinations below it, so the copy is safe in place.  Bound: the bytes of the
 // moved rows, read and written once.
+#include <atomic>
 #include <cooperative_groups.h>
 #include <cstdint>
 
@@ -31,6 +32,7 @@ namespace {
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kLoadBatch = 8;
 constexpr int kCachedKeys = 32768;                         // keys a CTA holds in shared memory (128 KB)
 constexpr int kMaxCluster = 8;
 // One CTA up to this many rows per request, a cluster of eight above.
@@ -48,8 +50,8 @@ struct SelShared {
     uint32_t hist[2][kBins];
     uint32_t scan[kSelWarps];
     uint32_t bin, above;                                   // the chosen digit, keys with a larger one
-    uint32_t warp_eq[kSelWarps], warp_hole[kSelWarps], warp_moved[kSelWarps];
-    uint32_t total_eq, total_hole, total_moved;            // read by the other CTAs of the cluster
+    uint32_t warp_gt[2][kSelWarps], warp_eq[2][kSelWarps]; // rows above / equal to K, below keep and behind it
+    uint32_t cta_gt[2], cta_eq[2];                         // the CTA's, read by the others of the cluster
 };
 
 __device__ __forceinline__ uint32_t rank_key(float w, int pos, int sink, long long recent_from) {
@@ -90,6 +92,7 @@ __device__ __forceinline__ uint32_t warp_base(const uint32_t* counts, int warp, 
 
 template <int CL>
 __global__ void __launch_bounds__(kSelThreads) mla_evict_select_kernel(const mla_evict_args a, const EvictScratch s) {
+    constexpr int kCache = CL == 1 ? kOneCtaRows : kCachedKeys;
     extern __shared__ uint32_t cached[];
     __shared__ SelShared sh;
     cg::cluster_group cluster = cg::this_cluster();
@@ -128,8 +131,34 @@ __global__ void __launch_bounds__(kSelThreads) mla_evict_select_kernel(const mla
     auto compute_key = [&](int r) {
         return rank_key(a.weights[base + r], a.positions[base + r], a.sink, recent_from);
     };
-    auto key_of = [&](int r) { return r - r0 < kCachedKeys ? cached[r - r0] : compute_key(r); };
-    for (int r = r0 + tid; r < r1 && r - r0 < kCachedKeys; r += kSelThreads) cached[r - r0] = compute_key(r);
+    auto key_of = [&](int r) { return r - r0 < kCache ? cached[r - r0] : compute_key(r); };
+    // keys into shared memory, eight loads of each array in flight per thread; the
+    // rows below keep get their own weight and position in the outputs (the move
+    // overwrites those of the evicted ones)
+    const bool copy_w = a.weights_out != a.weights, copy_p = a.positions_out != a.positions;
+    for (int r = r0 + tid; r < r1; r += kLoadBatch * kSelThreads) {
+        float w[kLoadBatch];
+        int pos[kLoadBatch];
+#pragma unroll
+        for (int i = 0; i < kLoadBatch; ++i) {
+            const int row = r + i * kSelThreads;
+            if (row < r1) {
+                w[i] = a.weights[base + row];
+                pos[i] = a.positions[base + row];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kLoadBatch; ++i) {
+            const int row = r + i * kSelThreads;
+            if (row < r1) {
+                if (row - r0 < kCache) cached[row - r0] = rank_key(w[i], pos[i], a.sink, recent_from);
+                if (row < keep) {
+                    if (copy_w) a.weights_out[base + row] = w[i];
+                    if (copy_p) a.positions_out[base + row] = pos[i];
+                }
+            }
+        }
+    }
 
     // ---- the keep-th largest key
     uint32_t prefix = 0, need = static_cast<uint32_t>(keep);
@@ -176,61 +205,97 @@ __global__ void __launch_bounds__(kSelThreads) mla_evict_select_kernel(const mla
     }
     const uint32_t K = prefix;                             // `need` rows equal to K stay, the first ones
 
-    // ---- rows equal to K before this warp's
-    uint32_t cnt = 0;
-    for (int r = w0; r < w1; r += 32) {
-        const bool in = r + lane < w1;
-        cnt += __popc(__ballot_sync(0xffffffffu, in && key_of(r + lane) == K));
-    }
-    if (lane == 0) sh.warp_eq[warp] = cnt;
-    __syncthreads();
-    uint32_t total;
-    uint32_t eq0 = warp_base(sh.warp_eq, warp, lane, &total);
-    if (tid == 0) sh.total_eq = total;
-    everyone();
-#pragma unroll
-    for (int q = 0; q < CL; ++q)
-        if (q < rank) eq0 += *cluster.map_shared_rank(&sh.total_eq, q);
-
-    // ---- evicted rows below keep and kept rows behind it: count, then number
-    uint32_t holes = 0, moves = 0, eq = eq0;
+    // ---- this warp's rows above and equal to K, below keep and behind it
+    uint32_t gt[2] = {0, 0}, eqs[2] = {0, 0};
     for (int r = w0; r < w1; r += 32) {
         const int row = r + lane;
         const uint32_t k = row < w1 ? key_of(row) : 0u;
-        const bool is_eq = row < w1 && k == K;
-        const uint32_t bal = __ballot_sync(0xffffffffu, is_eq);
-        const bool kept = row < w1 && (k > K || (is_eq && eq + __popc(bal & ((1u << lane) - 1u)) < need));
-        eq += __popc(bal);
-        holes += __popc(__ballot_sync(0xffffffffu, row < w1 && row < keep && !kept));
-        moves += __popc(__ballot_sync(0xffffffffu, row >= keep && kept));
+        const uint32_t g = __ballot_sync(0xffffffffu, row < w1 && k > K);
+        const uint32_t e = __ballot_sync(0xffffffffu, row < w1 && k == K);
+        const uint32_t low = keep - r >= 32 ? 0xffffffffu : keep > r ? (1u << (keep - r)) - 1u : 0u;
+        gt[0] += __popc(g & low);
+        gt[1] += __popc(g & ~low);
+        eqs[0] += __popc(e & low);
+        eqs[1] += __popc(e & ~low);
     }
     if (lane == 0) {
-        sh.warp_hole[warp] = holes;
-        sh.warp_moved[warp] = moves;
+        sh.warp_gt[0][warp] = gt[0];
+        sh.warp_gt[1][warp] = gt[1];
+        sh.warp_eq[0][warp] = eqs[0];
+        sh.warp_eq[1][warp] = eqs[1];
     }
     __syncthreads();
-    uint32_t hole0 = warp_base(sh.warp_hole, warp, lane, &total);
-    if (tid == 0) sh.total_hole = total;
-    uint32_t moved0 = warp_base(sh.warp_moved, warp, lane, &total);
-    if (tid == 0) sh.total_moved = total;
-    everyone();
-    uint32_t all_holes = 0;
+    // every warp: the CTA's totals and, for lane w, what lies before warp w of the CTA
+    const uint32_t my_gt0 = sh.warp_gt[0][lane], my_gt1 = sh.warp_gt[1][lane];
+    const uint32_t my_eq0 = sh.warp_eq[0][lane], my_eq1 = sh.warp_eq[1][lane];
+    const uint32_t eq_incl = warp_incl_scan(my_eq0 + my_eq1, lane);
+    if (CL > 1) {
+        if (warp == 0) {
+            const uint32_t t[4] = {warp_incl_scan(my_gt0, lane), warp_incl_scan(my_gt1, lane),
+                                   warp_incl_scan(my_eq0, lane), warp_incl_scan(my_eq1, lane)};
+            if (lane == 31) {
+                sh.cta_gt[0] = t[0];
+                sh.cta_gt[1] = t[1];
+                sh.cta_eq[0] = t[2];
+                sh.cta_eq[1] = t[3];
+            }
+        }
+        everyone();
+    }
+    // Of `e` rows equal to K with `before` such rows in front, min(e, need - before)
+    // stay, the first ones; so the evicted rows below keep and the kept ones behind
+    // it follow from the counts.
+    auto holes_of = [&](uint32_t below, uint32_t g0, uint32_t e0, uint32_t before) {
+        const uint32_t stay = before < need ? min(e0, need - before) : 0u;
+        return below - g0 - stay;
+    };
+    auto moves_of = [&](uint32_t g1, uint32_t e0, uint32_t e1, uint32_t before) {
+        const uint32_t stay = before < need ? min(e0 + e1, need - before) : 0u;
+        return g1 + (stay > e0 ? stay - e0 : 0u);
+    };
+    auto rows_below = [&](long long from, long long to) {  // of [from, to): rows below keep
+        const long long end = to < keep ? to : keep;
+        return static_cast<uint32_t>(end > from ? end - from : 0);
+    };
+    uint32_t eq0 = 0, hole0 = 0, moved0 = 0, all_moves = 0;
+    if (CL > 1) {
+        uint32_t before = 0;
 #pragma unroll
-    for (int q = 0; q < CL; ++q) {
-        const uint32_t h = *cluster.map_shared_rank(&sh.total_hole, q);
-        all_holes += h;
-        if (q < rank) {
-            hole0 += h;
-            moved0 += *cluster.map_shared_rank(&sh.total_moved, q);
+        for (int q = 0; q < CL; ++q) {
+            const uint32_t* g = cluster.map_shared_rank(sh.cta_gt, q);
+            const uint32_t* e = cluster.map_shared_rank(sh.cta_eq, q);
+            const uint32_t e0 = e[0], e1 = e[1], mv = moves_of(g[1], e0, e1, before);
+            const long long from = min(static_cast<long long>(n), static_cast<long long>(q) * per);
+            const long long to = min(static_cast<long long>(n), from + per);
+            if (q < rank) {
+                eq0 += e0 + e1;
+                hole0 += holes_of(rows_below(from, to), g[0], e0, before);
+                moved0 += mv;
+            }
+            all_moves += mv;
+            before += e0 + e1;
         }
     }
+    {
+        // lane w: warp w's counts, then the exclusive prefix at this warp
+        const long long from = min(static_cast<long long>(r1), static_cast<long long>(r0) + lane * w_per);
+        const long long to = min(static_cast<long long>(r1), from + w_per);
+        const uint32_t before = eq0 + eq_incl - (my_eq0 + my_eq1);
+        const uint32_t h = holes_of(rows_below(from, to), my_gt0, my_eq0, before);
+        const uint32_t m = moves_of(my_gt1, my_eq0, my_eq1, before);
+        const uint32_t h_incl = warp_incl_scan(h, lane), m_incl = warp_incl_scan(m, lane);
+        if (CL == 1) all_moves = __shfl_sync(0xffffffffu, m_incl, 31);
+        eq0 = __shfl_sync(0xffffffffu, before, warp);
+        hole0 += __shfl_sync(0xffffffffu, h_incl - h, warp);
+        moved0 += __shfl_sync(0xffffffffu, m_incl - m, warp);
+    }
     if (rank == 0 && tid == 0) {
-        s.n_moves[b] = static_cast<int>(all_holes);
+        s.n_moves[b] = static_cast<int>(all_moves);        // as many as evicted rows below keep
         a.d_pos_out[b] = keep;                             // every CTA read d_pos before its first barrier
     }
     int* hole_list = s.hole + static_cast<long long>(b) * a.keep;
     int* moved_list = s.moved + static_cast<long long>(b) * a.keep;
-    eq = eq0;
+    uint32_t eq = eq0;
     const uint32_t lower = (1u << lane) - 1u;
     for (int r = w0; r < w1; r += 32) {
         const int row = r + lane;
@@ -245,10 +310,6 @@ __global__ void __launch_bounds__(kSelThreads) mla_evict_select_kernel(const mla
         if (moved) moved_list[moved0 + __popc(mb & lower)] = row;
         hole0 += __popc(hb);
         moved0 += __popc(mb);
-        if (kept && row < keep) {
-            a.weights_out[base + row] = a.weights[base + row];
-            a.positions_out[base + row] = a.positions[base + row];
-        }
     }
     allow_dependent_launch();
     everyone();                                            // no CTA leaves while others read its shared memory
@@ -299,10 +360,19 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 template <int CL>
 cudaError_t launch_select(const mla_evict_args& a, const EvictScratch& s, cudaStream_t st) {
-    const size_t smem = static_cast<size_t>(kCachedKeys) * 4;
-    cudaError_t e = cudaFuncSetAttribute(mla_evict_select_kernel<CL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
+    const size_t smem = CL == 1 ? kOneCtaRows * sizeof(uint32_t) : kCachedKeys * sizeof(uint32_t);
+    // (the attribute of the larger form is set once per device)
+    static std::atomic<int> prepared[kMaxDevices];
+    if (smem > 48 * 1024 - sizeof(SelShared)) {
+        int dev = 0;
+        if (current_device(&dev) != MLA_OK) return cudaErrorInvalidDevice;
+        if (!prepared[dev].load(std::memory_order_acquire)) {
+            const cudaError_t e = cudaFuncSetAttribute(
+                mla_evict_select_kernel<CL>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+            if (e != cudaSuccess) return e;
+            prepared[dev].store(1, std::memory_order_release);
+        }
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.batch * CL);
     cfg.blockDim = dim3(kSelThreads);
@@ -314,7 +384,7 @@ cudaError_t launch_select(const mla_evict_args& a, const EvictScratch& s, cudaSt
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = CL > 1 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, mla_evict_select_kernel<CL>, a, s);
 }
 
