@@ -4,13 +4,14 @@
 // Select.  Each row's rank is a 32-bit key that orders as (protected, weight):
 // the float's bits made monotonic, NaN as -infinity, -0 as +0, protected rows
 // above everything.  The keep-th largest key K is found exactly by a radix
-// descent over 11 + 11 + 10 bits with histograms in shared memory, by a cluster
-// of CTAs per request that read each other's histograms (distributed shared
-// memory); the keys stay in shared memory between the passes when they fit.
+// descent over four digits of eight bits, histograms in shared memory, by a
+// cluster of CTAs per request that read each other's histograms (distributed
+// shared memory is slow: 2048 bins and three digits took three times as long);
+// the keys stay in shared memory between the passes when they fit.
 // Rows above K stay, and of the rows equal to K the first so many that `keep`
-// is met; counts by ballots, summed over warps, CTA and cluster, number the
-// evicted rows below `keep` and the kept rows behind it in ascending order,
-// which pairs them up.  Integers only: no order of execution shows in the result.
+// is met; every thread counts over a contiguous run of rows, and prefix sums over
+// threads, warps and CTAs number the evicted rows below `keep` and the kept rows
+// behind it in ascending order, which pairs them up.  Integers only: no order of execution shows in the result.
 //
 // Move.  A warp copies four bf16 rows (eight E4M3 rows) at a time, nine
 // 16-byte loads in flight per lane; source rows lie at or behind `keep` and
@@ -31,13 +32,14 @@ namespace {
 
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kBins = 2048;
+constexpr int kBins = 256;
 constexpr int kLoadBatch = 8;
 constexpr int kCachedKeys = 32768;                         // keys a CTA holds in shared memory (128 KB)
 constexpr int kMaxCluster = 8;
 // One CTA up to this many rows per request, a cluster of eight above.
 constexpr int kOneCtaRows = 8192;
 constexpr int kMoveThreads = 256;
+constexpr int kMoveBlocks = 152 * 6;                       // blocks that fill the GPU twice
 constexpr int kMoveUnits = 288;                            // 16-byte units a warp moves at a time
 
 struct EvictScratch {
@@ -48,10 +50,15 @@ struct EvictScratch {
 
 struct SelShared {
     uint32_t hist[2][kBins];
-    uint32_t scan[kSelWarps];
+    uint32_t sum[kBins];                                   // over the cluster
     uint32_t bin, above;                                   // the chosen digit, keys with a larger one
-    uint32_t warp_gt[2][kSelWarps], warp_eq[2][kSelWarps]; // rows above / equal to K, below keep and behind it
-    uint32_t cta_gt[2], cta_eq[2];                         // the CTA's, read by the others of the cluster
+    unsigned long long warp_counts[kSelWarps];
+    uint32_t cta[4];                                       // the CTA's counts, read by the others of the cluster
+};
+
+// Rows above / equal to the threshold K, below `keep` and behind it.
+struct Counts {
+    uint32_t gt0, gt1, eq0, eq1;
 };
 
 __device__ __forceinline__ uint32_t rank_key(float w, int pos, int sink, long long recent_from) {
@@ -81,15 +88,6 @@ __device__ __forceinline__ uint32_t warp_incl_scan(uint32_t v, int lane) {
     return v;
 }
 
-// Exclusive prefix of this warp's count over the CTA's warps, and the CTA's
-// total (counts[] written by lane 0 of every warp before the barrier).
-__device__ __forceinline__ uint32_t warp_base(const uint32_t* counts, int warp, int lane, uint32_t* total) {
-    const uint32_t v = counts[lane];
-    const uint32_t incl = warp_incl_scan(v, lane);
-    *total = __shfl_sync(0xffffffffu, incl, 31);
-    return __shfl_sync(0xffffffffu, incl - v, warp);
-}
-
 template <int CL>
 __global__ void __launch_bounds__(kSelThreads) mla_evict_select_kernel(const mla_evict_args a, const EvictScratch s) {
     constexpr int kCache = CL == 1 ? kOneCtaRows : kCachedKeys;
@@ -109,12 +107,11 @@ __global__ void __launch_bounds__(kSelThreads) mla_evict_select_kernel(const mla
     long long base;
     const int n = request_rows(a, b, &base);
     const int keep = min(n, a.keep);
-    // this CTA's rows [r0, r1), this warp's rows [w0, w1)
-    const int per = static_cast<int>(((static_cast<long long>(n) + CL * 1024 - 1) / (CL * 1024)) * 1024);
-    const int r0 = static_cast<int>(min(static_cast<long long>(n), static_cast<long long>(rank) * per));
-    const int r1 = static_cast<int>(min(static_cast<long long>(n), static_cast<long long>(r0) + per));
-    const int w_per = per / kSelWarps;                     // a multiple of 32
-    const int w0 = min(r1, r0 + warp * w_per), w1 = min(r1, w0 + w_per);
+    // this CTA's rows [r0, r1); thread t has the `each` rows from r0 + t * each
+    const int each = static_cast<int>((static_cast<long long>(n) + CL * kSelThreads * 4 - 1) / (CL * kSelThreads * 4)) * 4;
+    const long long per = static_cast<long long>(each) * kSelThreads;
+    const int r0 = static_cast<int>(min(static_cast<long long>(n), rank * per));
+    const int r1 = static_cast<int>(min(static_cast<long long>(n), r0 + per));
     if (n <= a.keep) {                                     // uniform over the cluster
         for (int r = r0 + tid; r < r1; r += kSelThreads) {
             a.weights_out[base + r] = a.weights[base + r];
@@ -141,11 +138,9 @@ __global__ void __launch_bounds__(kSelThreads) mla_evict_select_kernel(const mla
         int pos[kLoadBatch];
 #pragma unroll
         for (int i = 0; i < kLoadBatch; ++i) {
-            const int row = r + i * kSelThreads;
-            if (row < r1) {
-                w[i] = a.weights[base + row];
-                pos[i] = a.positions[base + row];
-            }
+            const int row = min(r + i * kSelThreads, r1 - 1);   // (no branch: all loads at once)
+            w[i] = a.weights[base + row];
+            pos[i] = a.positions[base + row];
         }
 #pragma unroll
         for (int i = 0; i < kLoadBatch; ++i) {
@@ -163,131 +158,132 @@ __global__ void __launch_bounds__(kSelThreads) mla_evict_select_kernel(const mla
     // ---- the keep-th largest key
     uint32_t prefix = 0, need = static_cast<uint32_t>(keep);
 #pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-        const uint32_t digit_mask = pass == 2 ? 1023u : 2047u;
-        const uint32_t high_mask = pass == 0 ? 0u : pass == 1 ? 0xffe00000u : 0xfffffc00u;
+    for (int pass = 0; pass < 4; ++pass) {
+        const int shift = 24 - 8 * pass;
+        const uint32_t high_mask = pass == 0 ? 0u : 0xffffffffu << (shift + 8);
         uint32_t* hist = sh.hist[pass & 1];
-        hist[tid] = 0;
-        hist[tid + kSelThreads] = 0;
+        if (tid < kBins) hist[tid] = 0;
         __syncthreads();
         for (int r = r0 + tid; r < r1; r += kSelThreads) {
             const uint32_t k = key_of(r);
-            if ((k & high_mask) == prefix) atomicAdd(&hist[(k >> shift) & digit_mask], 1u);
+            if ((k & high_mask) == prefix) atomicAdd(&hist[k >> shift & 255u], 1u);
         }
         everyone();
-        // every CTA sums all histograms: thread t takes the bins 2047 - 2t, 2046 - 2t (descending)
-        uint32_t c0 = 0, c1 = 0;
-        const int bin0 = kBins - 1 - 2 * tid;
+        // every CTA sums all histograms (the next pass writes the other one; this one
+        // is written again only after every CTA has passed the next pass's barrier)
+        if (tid < kBins) {
+            uint32_t c = 0;
 #pragma unroll
-        for (int q = 0; q < CL; ++q) {
-            const uint32_t* h = CL == 1 ? hist : cluster.map_shared_rank(hist, q);
-            c0 += h[bin0];
-            c1 += h[bin0 - 1];
+            for (int q = 0; q < CL; ++q) c += (CL == 1 ? hist : cluster.map_shared_rank(hist, q))[tid];
+            sh.sum[tid] = c;
         }
-        const uint32_t incl = warp_incl_scan(c0 + c1, lane);
-        if (lane == 31) sh.scan[warp] = incl;
         __syncthreads();
-        uint32_t total;
-        const uint32_t before = warp_base(sh.scan, warp, lane, &total) + incl - (c0 + c1);
-        if (before < need && before + c0 >= need) {
-            sh.bin = bin0;
-            sh.above = before;
-        } else if (before + c0 < need && before + c0 + c1 >= need) {
-            sh.bin = bin0 - 1;
-            sh.above = before + c0;
+        if (warp == 0) {
+            // lane l: digits 255 - 8 l and the seven below it
+            uint32_t c[8], all = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                c[i] = sh.sum[kBins - 1 - 8 * lane - i];
+                all += c[i];
+            }
+            uint32_t before = warp_incl_scan(all, lane) - all;
+            if (before < need && before + all >= need) {   // one lane
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (before < need && before + c[i] >= need) {
+                        sh.bin = kBins - 1 - 8 * lane - i;
+                        sh.above = before;
+                    }
+                    before += c[i];
+                }
+            }
         }
         __syncthreads();
         prefix |= sh.bin << shift;
         need -= sh.above;
-        // the next pass writes the other histogram; this one is not written again
-        // before every CTA has passed the next pass's cluster barrier
     }
     const uint32_t K = prefix;                             // `need` rows equal to K stay, the first ones
 
-    // ---- this warp's rows above and equal to K, below keep and behind it
-    uint32_t gt[2] = {0, 0}, eqs[2] = {0, 0};
-    for (int r = w0; r < w1; r += 32) {
-        const int row = r + lane;
-        const uint32_t k = row < w1 ? key_of(row) : 0u;
-        const uint32_t g = __ballot_sync(0xffffffffu, row < w1 && k > K);
-        const uint32_t e = __ballot_sync(0xffffffffu, row < w1 && k == K);
-        const uint32_t low = keep - r >= 32 ? 0xffffffffu : keep > r ? (1u << (keep - r)) - 1u : 0u;
-        gt[0] += __popc(g & low);
-        gt[1] += __popc(g & ~low);
-        eqs[0] += __popc(e & low);
-        eqs[1] += __popc(e & ~low);
+    // ---- this thread's rows above and equal to K, below keep and behind it
+    const int t0 = static_cast<int>(min(static_cast<long long>(r1), r0 + static_cast<long long>(tid) * each));
+    const int t1 = static_cast<int>(min(static_cast<long long>(r1), static_cast<long long>(t0) + each));
+    Counts mine{0, 0, 0, 0};
+    for (int r = t0; r < t1; ++r) {
+        const uint32_t k = key_of(r);
+        const uint32_t g = k > K, e = k == K, low = r < keep;
+        mine.gt0 += g & low;
+        mine.gt1 += g & ~low;
+        mine.eq0 += e & low;
+        mine.eq1 += e & ~low;
     }
-    if (lane == 0) {
-        sh.warp_gt[0][warp] = gt[0];
-        sh.warp_gt[1][warp] = gt[1];
-        sh.warp_eq[0][warp] = eqs[0];
-        sh.warp_eq[1][warp] = eqs[1];
-    }
-    __syncthreads();
-    // every warp: the CTA's totals and, for lane w, what lies before warp w of the CTA
-    const uint32_t my_gt0 = sh.warp_gt[0][lane], my_gt1 = sh.warp_gt[1][lane];
-    const uint32_t my_eq0 = sh.warp_eq[0][lane], my_eq1 = sh.warp_eq[1][lane];
-    const uint32_t eq_incl = warp_incl_scan(my_eq0 + my_eq1, lane);
-    if (CL > 1) {
-        if (warp == 0) {
-            const uint32_t t[4] = {warp_incl_scan(my_gt0, lane), warp_incl_scan(my_gt1, lane),
-                                   warp_incl_scan(my_eq0, lane), warp_incl_scan(my_eq1, lane)};
-            if (lane == 31) {
-                sh.cta_gt[0] = t[0];
-                sh.cta_gt[1] = t[1];
-                sh.cta_eq[0] = t[2];
-                sh.cta_eq[1] = t[3];
-            }
-        }
-        everyone();
-    }
-    // Of `e` rows equal to K with `before` such rows in front, min(e, need - before)
-    // stay, the first ones; so the evicted rows below keep and the kept ones behind
-    // it follow from the counts.
-    auto holes_of = [&](uint32_t below, uint32_t g0, uint32_t e0, uint32_t before) {
-        const uint32_t stay = before < need ? min(e0, need - before) : 0u;
-        return below - g0 - stay;
+    // Of the rows equal to K that follow `before` others, min(count, need - before)
+    // stay, the first ones: from the counts follow the evicted rows below keep and
+    // the kept rows behind it, which a second prefix sum numbers.
+    auto stay_of = [&](const Counts& c, uint32_t before) {
+        return before < need ? min(c.eq0 + c.eq1, need - before) : 0u;
     };
-    auto moves_of = [&](uint32_t g1, uint32_t e0, uint32_t e1, uint32_t before) {
-        const uint32_t stay = before < need ? min(e0 + e1, need - before) : 0u;
-        return g1 + (stay > e0 ? stay - e0 : 0u);
+    auto holes_of = [&](const Counts& c, uint32_t before, uint32_t below) {
+        return below - c.gt0 - min(c.eq0, stay_of(c, before));
+    };
+    auto moves_of = [&](const Counts& c, uint32_t before) {
+        const uint32_t stay = stay_of(c, before);
+        return c.gt1 + (stay > c.eq0 ? stay - c.eq0 : 0u);
     };
     auto rows_below = [&](long long from, long long to) {  // of [from, to): rows below keep
         const long long end = to < keep ? to : keep;
         return static_cast<uint32_t>(end > from ? end - from : 0);
     };
-    uint32_t eq0 = 0, hole0 = 0, moved0 = 0, all_moves = 0;
+    // exclusive prefix over the CTA's threads of two 32-bit counts, and their totals
+    auto prefix2 = [&](uint32_t x, uint32_t y, uint32_t& px, uint32_t& py, uint32_t& tx, uint32_t& ty) {
+        const uint32_t ix = warp_incl_scan(x, lane), iy = warp_incl_scan(y, lane);
+        __syncthreads();                                   // the counts of the scan before are read
+        if (lane == 31) sh.warp_counts[warp] = static_cast<unsigned long long>(iy) << 32 | ix;
+        __syncthreads();
+        const unsigned long long v = sh.warp_counts[lane];
+        const uint32_t vx = static_cast<uint32_t>(v), vy = static_cast<uint32_t>(v >> 32);
+        const uint32_t sx = warp_incl_scan(vx, lane), sy = warp_incl_scan(vy, lane);
+        tx = __shfl_sync(0xffffffffu, sx, 31);
+        ty = __shfl_sync(0xffffffffu, sy, 31);
+        px = __shfl_sync(0xffffffffu, sx - vx, warp) + ix - x;
+        py = __shfl_sync(0xffffffffu, sy - vy, warp) + iy - y;
+    };
+    uint32_t eq = 0, hole0 = 0, moved0 = 0, all_moves = 0;
+    uint32_t eq_before, unused, eq_total, gt_total;
+    prefix2(mine.eq0 + mine.eq1, mine.gt0 + mine.gt1, eq_before, unused, eq_total, gt_total);
     if (CL > 1) {
+        // what lies in the CTAs before this one
+        uint32_t p0, p1, e0_total, g0_total;
+        prefix2(mine.eq0, mine.gt0, p0, p1, e0_total, g0_total);
+        if (tid == 0) {
+            sh.cta[0] = g0_total;
+            sh.cta[1] = gt_total - g0_total;
+            sh.cta[2] = e0_total;
+            sh.cta[3] = eq_total - e0_total;
+        }
+        everyone();
         uint32_t before = 0;
 #pragma unroll
         for (int q = 0; q < CL; ++q) {
-            const uint32_t* g = cluster.map_shared_rank(sh.cta_gt, q);
-            const uint32_t* e = cluster.map_shared_rank(sh.cta_eq, q);
-            const uint32_t e0 = e[0], e1 = e[1], mv = moves_of(g[1], e0, e1, before);
-            const long long from = min(static_cast<long long>(n), static_cast<long long>(q) * per);
-            const long long to = min(static_cast<long long>(n), from + per);
+            const uint32_t* v = cluster.map_shared_rank(sh.cta, q);
+            const Counts c{v[0], v[1], v[2], v[3]};
+            const long long from = min(static_cast<long long>(n), q * per), to = min(static_cast<long long>(n), from + per);
+            const uint32_t m = moves_of(c, before);
             if (q < rank) {
-                eq0 += e0 + e1;
-                hole0 += holes_of(rows_below(from, to), g[0], e0, before);
-                moved0 += mv;
+                eq += c.eq0 + c.eq1;
+                hole0 += holes_of(c, before, rows_below(from, to));
+                moved0 += m;
             }
-            all_moves += mv;
-            before += e0 + e1;
+            all_moves += m;
+            before += c.eq0 + c.eq1;
         }
     }
+    eq += eq_before;
     {
-        // lane w: warp w's counts, then the exclusive prefix at this warp
-        const long long from = min(static_cast<long long>(r1), static_cast<long long>(r0) + lane * w_per);
-        const long long to = min(static_cast<long long>(r1), from + w_per);
-        const uint32_t before = eq0 + eq_incl - (my_eq0 + my_eq1);
-        const uint32_t h = holes_of(rows_below(from, to), my_gt0, my_eq0, before);
-        const uint32_t m = moves_of(my_gt1, my_eq0, my_eq1, before);
-        const uint32_t h_incl = warp_incl_scan(h, lane), m_incl = warp_incl_scan(m, lane);
-        if (CL == 1) all_moves = __shfl_sync(0xffffffffu, m_incl, 31);
-        eq0 = __shfl_sync(0xffffffffu, before, warp);
-        hole0 += __shfl_sync(0xffffffffu, h_incl - h, warp);
-        moved0 += __shfl_sync(0xffffffffu, m_incl - m, warp);
+        uint32_t h, m, h_total, m_total;
+        prefix2(holes_of(mine, eq, rows_below(t0, t1)), moves_of(mine, eq), h, m, h_total, m_total);
+        hole0 += h;
+        moved0 += m;
+        if (CL == 1) all_moves = m_total;
     }
     if (rank == 0 && tid == 0) {
         s.n_moves[b] = static_cast<int>(all_moves);        // as many as evicted rows below keep
@@ -295,21 +291,12 @@ __global__ void __launch_bounds__(kSelThreads) mla_evict_select_kernel(const mla
     }
     int* hole_list = s.hole + static_cast<long long>(b) * a.keep;
     int* moved_list = s.moved + static_cast<long long>(b) * a.keep;
-    uint32_t eq = eq0;
-    const uint32_t lower = (1u << lane) - 1u;
-    for (int r = w0; r < w1; r += 32) {
-        const int row = r + lane;
-        const uint32_t k = row < w1 ? key_of(row) : 0u;
-        const bool is_eq = row < w1 && k == K;
-        const uint32_t bal = __ballot_sync(0xffffffffu, is_eq);
-        const bool kept = row < w1 && (k > K || (is_eq && eq + __popc(bal & lower) < need));
-        eq += __popc(bal);
-        const bool hole = row < w1 && row < keep && !kept, moved = row >= keep && kept;
-        const uint32_t hb = __ballot_sync(0xffffffffu, hole), mb = __ballot_sync(0xffffffffu, moved);
-        if (hole) hole_list[hole0 + __popc(hb & lower)] = row;
-        if (moved) moved_list[moved0 + __popc(mb & lower)] = row;
-        hole0 += __popc(hb);
-        moved0 += __popc(mb);
+    for (int r = t0; r < t1; ++r) {
+        const uint32_t k = key_of(r);
+        bool kept = k > K;
+        if (k == K) kept = eq++ < need;
+        if (!kept && r < keep) hole_list[hole0++] = r;
+        if (kept && r >= keep) moved_list[moved0++] = r;
     }
     allow_dependent_launch();
     everyone();                                            // no CTA leaves while others read its shared memory
@@ -328,17 +315,15 @@ __global__ void __launch_bounds__(kMoveThreads) mla_evict_move_kernel(const mla_
     const long long base = a.row_offset ? a.row_offset[b] : 0;
     const long long stride = a.row_stride * (UNITS == 72 ? 2 : 1);
     char* kv = static_cast<char*>(a.kv) + base * stride;
-    const int warps = gridDim.x * (kMoveThreads / 32);
-    const int step = warps * kRows;
-    for (long long k0 = (blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5)) * static_cast<long long>(kRows); k0 < n;
-         k0 += step) {
-        int src = 0, dst = 0;
-        if (lane < kRows && k0 + lane < n) {
-            src = moved[k0 + lane];
-            dst = hole[k0 + lane];
-            a.weights_out[base + dst] = a.weights[base + src];
-            a.positions_out[base + dst] = a.positions[base + src];
-        }
+    const int step = gridDim.x * (kMoveThreads / 32) * kRows;
+    long long k0 = (blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5)) * static_cast<long long>(kRows);
+    // the list entries of the next rows are on their way while rows move
+    int src = 0, dst = 0;
+    if (lane < kRows && k0 + lane < n) {
+        src = moved[k0 + lane];
+        dst = hole[k0 + lane];
+    }
+    for (; k0 < n; k0 += step) {
         uint4 v[kPer];
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
@@ -346,11 +331,27 @@ __global__ void __launch_bounds__(kMoveThreads) mla_evict_move_kernel(const mla_
             const int from = __shfl_sync(0xffffffffu, src, row);
             if (k0 + row < n) v[i] = reinterpret_cast<const uint4*>(kv + from * stride)[w - row * UNITS];
         }
+        const bool entry = lane < kRows && k0 + lane < n;
+        float weight = 0.f;
+        int pos = 0;
+        if (entry) {
+            weight = a.weights[base + src];
+            pos = a.positions[base + src];
+        }
+        const int to_row = dst;
+        if (lane < kRows && k0 + step + lane < n) {
+            src = moved[k0 + step + lane];
+            dst = hole[k0 + step + lane];
+        }
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int w = lane + 32 * i, row = w / UNITS;
-            const int to = __shfl_sync(0xffffffffu, dst, row);
+            const int to = __shfl_sync(0xffffffffu, to_row, row);
             if (k0 + row < n) reinterpret_cast<uint4*>(kv + to * stride)[w - row * UNITS] = v[i];
+        }
+        if (entry) {
+            a.weights_out[base + to_row] = weight;
+            a.positions_out[base + to_row] = pos;
         }
     }
 }
@@ -397,7 +398,9 @@ cudaError_t launch_move(const mla_evict_args& a, const EvictScratch& s, cudaStre
     const long long per = kMoveThreads / 32 * (kMoveUnits / UNITS);
     long long grid = (moves + per - 1) / per;
     if (grid < 1) grid = 1;
-    if (grid > 4096) grid = 4096;
+    // a few rounds per warp, so that the lists' latency is paid once
+    const long long fill = (kMoveBlocks + a.batch - 1) / a.batch;
+    if (grid > fill) grid = fill;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid), a.batch);
     cfg.blockDim = dim3(kMoveThreads);
