@@ -91,7 +91,7 @@ __device__ __forceinline__ uint32_t warp_incl_scan(uint32_t v, int lane) {
 template <int CL>
 __global__ void __launch_bounds__(kSelThreads) mla_evict_select_kernel(const mla_evict_args a, const EvictScratch s) {
     constexpr int kCache = CL == 1 ? kOneCtaRows : kCachedKeys;
-    extern __shared__ uint32_t cached[];
+    extern __shared__ __align__(16) uint32_t cached[];
     __shared__ SelShared sh;
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = CL == 1 ? 0 : static_cast<int>(cluster.block_rank());
@@ -207,15 +207,28 @@ __global__ void __launch_bounds__(kSelThreads) mla_evict_select_kernel(const mla
     // ---- this thread's rows above and equal to K, below keep and behind it
     const int t0 = static_cast<int>(min(static_cast<long long>(r1), r0 + static_cast<long long>(tid) * each));
     const int t1 = static_cast<int>(min(static_cast<long long>(r1), static_cast<long long>(t0) + each));
+    // (four keys per shared-memory load: a lane's run is 16-byte aligned)
+    auto each_key = [&](auto&& f) {
+        for (int r = t0; r < t1; r += 4) {
+            if (r - r0 + 4 <= kCache) {
+                const uint4 k = *reinterpret_cast<const uint4*>(cached + (r - r0));
+                f(r, k.x);
+                if (r + 1 < t1) f(r + 1, k.y);
+                if (r + 2 < t1) f(r + 2, k.z);
+                if (r + 3 < t1) f(r + 3, k.w);
+            } else {
+                for (int i = r; i < min(r + 4, t1); ++i) f(i, key_of(i));
+            }
+        }
+    };
     Counts mine{0, 0, 0, 0};
-    for (int r = t0; r < t1; ++r) {
-        const uint32_t k = key_of(r);
+    each_key([&](int r, uint32_t k) {
         const uint32_t g = k > K, e = k == K, low = r < keep;
         mine.gt0 += g & low;
         mine.gt1 += g & ~low;
         mine.eq0 += e & low;
         mine.eq1 += e & ~low;
-    }
+    });
     // Of the rows equal to K that follow `before` others, min(count, need - before)
     // stay, the first ones: from the counts follow the evicted rows below keep and
     // the kept rows behind it, which a second prefix sum numbers.
@@ -291,13 +304,12 @@ __global__ void __launch_bounds__(kSelThreads) mla_evict_select_kernel(const mla
     }
     int* hole_list = s.hole + static_cast<long long>(b) * a.keep;
     int* moved_list = s.moved + static_cast<long long>(b) * a.keep;
-    for (int r = t0; r < t1; ++r) {
-        const uint32_t k = key_of(r);
+    each_key([&](int r, uint32_t k) {
         bool kept = k > K;
         if (k == K) kept = eq++ < need;
         if (!kept && r < keep) hole_list[hole0++] = r;
         if (kept && r >= keep) moved_list[moved0++] = r;
-    }
+    });
     allow_dependent_launch();
     everyone();                                            // no CTA leaves while others read its shared memory
 }
