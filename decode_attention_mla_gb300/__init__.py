@@ -416,25 +416,40 @@ def _need(t, name, dtypes, shape=None, contiguous=True):
     return t.data_ptr()
 
 
+def _quick(t, name, dtype, shape, device):
+    """As _need, for the calls that check their tensors every time: the usual case first."""
+    try:
+        if t.get_device() == device and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _need(t, name, dtype, shape)
+
+
 def _maybe(t, name, dtypes, shape):
     return None if t is None else _need(t, name, dtypes, shape)
 
 
 def _cache(kv, kv_rows, row_stride, fp8_ok=True):
-    """(pointer, rows, row stride, fp8) of a cache tensor [rows, >= 576 columns]."""
+    """(pointer, rows, row stride, fp8) of a cache tensor [rows, 576] with contiguous rows."""
     torch = _torch or _tc()
     p = _need(kv, "kv", (torch.bfloat16, torch.uint8, torch.float8_e4m3fn) if fp8_ok else torch.bfloat16,
               contiguous=False)
-    if kv.dim() != 2 or kv.shape[1] != D_ROW or kv.stride(1) != 1:
+    shape = kv.shape
+    if len(shape) != 2 or shape[1] != D_ROW or kv.stride(1) != 1:
         raise ValueError("kv must be [rows, 576] with contiguous rows")
-    if kv.shape[0] == 0:
-        raise ValueError("kv has no rows")
-    stride = int(kv.stride(0)) if kv.shape[0] > 1 else max(int(kv.stride(0)), D_ROW)
-    if kv_rows is not None and not 1 <= kv_rows <= kv.shape[0]:
-        raise ValueError("kv_rows is outside the tensor")
+    rows, stride = shape[0], kv.stride(0)
+    if rows < 2:
+        if rows == 0:
+            raise ValueError("kv has no rows")
+        stride = max(stride, D_ROW)
+    if kv_rows is not None:
+        if not 1 <= kv_rows <= rows:
+            raise ValueError("kv_rows is outside the tensor")
+        rows = int(kv_rows)
     if row_stride is not None and row_stride != stride:
         raise ValueError("row_stride differs from the tensor's")
-    return p, int(kv_rows if kv_rows is not None else kv.shape[0]), stride, int(kv.dtype != torch.bfloat16)
+    return p, rows, stride, 0 if kv.dtype is torch.bfloat16 else 1
 
 
 def _strides(t, name, shape, last):
@@ -622,12 +637,12 @@ def tree_commit(kv, accept, n_accept, *, d_pos, d_pos_out=None, row_offset=None,
     (``accept``: int32 [B, Q]); ``d_pos_out`` (may be ``d_pos``) takes d_pos + n_accept."""
     torch = _torch or _tc()
     B, Q = accept.shape
-    i32 = torch.int32
+    i32, dev = torch.int32, torch.cuda.current_device()
     kvp, rows, stride, fp8 = _cache(kv, kv_rows, row_stride)
-    a = TreeCommitArgs(kvp, rows, stride, fp8, B, Q, _need(accept, "accept", i32),
-                       _need(n_accept, "n_accept", i32, (B,)), _need(d_pos, "d_pos", i32, (B,)),
-                       _maybe(d_pos_out, "d_pos_out", i32, (B,)),
-                       _maybe(row_offset, "row_offset", torch.int64, (B,)),
+    a = TreeCommitArgs(kvp, rows, stride, fp8, B, Q, _quick(accept, "accept", i32, (B, Q), dev),
+                       _quick(n_accept, "n_accept", i32, (B,), dev), _quick(d_pos, "d_pos", i32, (B,), dev),
+                       None if d_pos_out is None else _quick(d_pos_out, "d_pos_out", i32, (B,), dev),
+                       None if row_offset is None else _quick(row_offset, "row_offset", torch.int64, (B,), dev),
                        _side(row_positions, "row_positions", i32, rows),
                        _side(row_weights, "row_weights", torch.float32, rows))
     _check(lib().mla_tree_commit(ctypes.byref(a), _stream(stream)), "mla_tree_commit")
