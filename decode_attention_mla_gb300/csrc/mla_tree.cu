@@ -11,7 +11,6 @@ namespace mla {
 namespace {
 
 constexpr int kTreeMagic = 0x4d4c5431;                     // "MLT1"
-constexpr int kMinTiles = 1;
 
 bool off(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to != 0; }
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -29,8 +28,8 @@ int check_shape(const mla_tree_shape* s) {
 // Scratch: status word, the pairs' merge notes, their pieces (two each) and
 // the pieces' log-sum-exps, each region 256-byte aligned.
 constexpr size_t kMergeOffset = 256;
-// Pairs of SMs to use; the merge holds the weights of at most so many pieces.
-int tree_pairs(int num_sms) { return num_sms < 2 ? 1 : num_sms > 2048 ? 1024 : num_sms / 2; }
+// Pairs of SMs to use.
+int tree_pairs(int num_sms) { return num_sms < 2 ? 1 : num_sms / 2; }
 void layout(mla_tree_plan_t* pl) {
     const size_t pairs = static_cast<size_t>(tree_pairs(pl->num_sms));
     pl->grid = static_cast<int>(2 * pairs);
@@ -98,7 +97,6 @@ TreeParams params(const mla_tree_plan_t* pl, const mla_tree_args* a, void* scrat
     p.tokens = pl->shape.tokens;
     p.heads = pl->shape.heads;
     p.clusters = pl->grid / 2;
-    p.min_tiles = kMinTiles;
     p.scale_log2 = pl->shape.scale * kLog2e;
     p.merge = reinterpret_cast<TreeMerge*>(base + kMergeOffset);
     p.part = reinterpret_cast<float*>(base + pl->part_offset);

@@ -24,7 +24,7 @@ struct TreeMerge {
 struct TreeParams {
     mla_tree_args a;
     int batch, tokens, heads;
-    int clusters, min_tiles;
+    int clusters;
     float scale_log2;                                      // scale * log2(e): scores in base-2 units
     float* part;                                           // fp32 [clusters][2][128][512], normalised
     float* lse_part;                                       // fp32 [clusters][2][128], base 2
@@ -148,7 +148,7 @@ struct TreeCursor {
     __device__ __forceinline__ bool special() const { return (tile + 1) * kKeys > r.d_pos; }
 
     // One warp: this cluster's run.  All units in order of (request, row block,
-    // tile); run length = ceil(units / clusters), at least min_tiles.
+    // tile); run length = ceil(units / clusters).
     static __device__ void find_work(const TreeParams& p, int cluster, int lane, TreeWork* out) {
         auto request_of = [&](int b) {
             TreeRequest r{};
@@ -166,7 +166,7 @@ struct TreeCursor {
             total = __shfl_sync(0xffffffffu, total, 0);
         }
         long long per = quotient(total + p.clusters - 1, p.clusters);
-        if (per < p.min_tiles) per = p.min_tiles;
+        if (per < 1) per = 1;
         const long long u0 = per * cluster;
         const long long count = u0 >= total ? 0 : (total - u0 < per ? total - u0 : per);
         if (lane == 0) {

@@ -320,6 +320,13 @@ __device__ void clean_v(Shared& sh, const Cursor& c, int tid) {
     }
 }
 
+// Place of a piece's feature quad: [piece][32-row group][quad][row], so that the
+// epilogue's and the merge's warps (a row per lane) touch 512 consecutive bytes.
+// (Rows of 2 KB, staged through shared memory, took 6300 cycles per row block.)
+__device__ __forceinline__ long long piece_quad(int slot, int row, int quad) {
+    return ((static_cast<long long>(slot) * (kTreeBlockRows / 32) + (row >> 5)) * (kDLatent / 4) + quad) * 32 + (row & 31);
+}
+
 // 64 bytes of each of a warp's 32 rows (32 features in bf16, 16 in fp32),
 // through its 2 KB of shared memory so that the stores of a row run along its
 // features (16-byte units, swizzled by row pair).  `dst`: row 0's first
@@ -463,14 +470,11 @@ __device__ void softmax(const TreeParams& p, Shared& sh, uint32_t tmem, uint32_t
         const float lse2 = lt == 0.f ? -INFINITY : m_ref + log2f(lt);
         const bool whole = tile0 == 0 && done == n_tiles;
         const int slot = 2 * cluster + (tile0 == 0 ? 1 : 0);
-        // row 0 of this CTA's 64 in the output, or in the piece
-        const long long row0 = whole ? static_cast<long long>(b) * p.tokens * p.heads + r - row
-                                     : static_cast<long long>(slot) * kTreeBlockRows + static_cast<int>(rank) * 64;
         if (quarter == 0 && r < live_rows) {
             if (whole)
-                p.a.lse[row0 + row] = lse2 * kLn2;
+                p.a.lse[static_cast<long long>(b) * p.tokens * p.heads + r] = lse2 * kLn2;
             else
-                p.lse_part[row0 + row] = lse2;
+                p.lse_part[slot * kTreeBlockRows + static_cast<int>(rank) * 64 + row] = lse2;
         }
         if (!whole && tile0 == 0) {
             merge.b = b;
@@ -487,32 +491,45 @@ __device__ void softmax(const TreeParams& p, Shared& sh, uint32_t tmem, uint32_t
         const uint32_t stage = smem_u32(sh.p) + warp * 2048;
         const int row_w = 32 * (warp & 1);                 // this warp's first row of the 64
         const int n_rows = live_rows - (r - row) - row_w;
+        const int f0 = 256 * sub + 128 * half;             // its first feature
+        float4* piece = reinterpret_cast<float4*>(p.part) +
+                        piece_quad(slot, static_cast<int>(rank) * 64 + row_w, f0 / 4) + lane;
+        char* out = static_cast<char*>(p.a.out) +
+                    ((static_cast<long long>(b) * p.tokens * p.heads + r - row + row_w) * kDLatent + f0) *
+                        (p.a.out_fp32 ? 4 : 2);
 #pragma unroll 1
         for (int j = 0; j < 4; ++j) {
             uint32_t o[32];
             tmem_ld32_async(tmem + lanes + kTmemO + 128 * sub + 32 * j, o);
             tmem_wait_ld32(o);
-            const long long at = (row0 + row_w) * kDLatent + 256 * sub + 128 * half + 32 * j;
+            if (!whole) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    piece[(8 * j + i) * 32] =
+                        make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
+                                    __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
+                continue;
+            }
             uint32_t x[16];
-            if (whole && !p.a.out_fp32) {
+            if (!p.a.out_fp32) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     x[i] = pack_bf16x2(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
-                store_rows(stage, x, reinterpret_cast<char*>(static_cast<uint16_t*>(p.a.out) + at), 2 * kDLatent,
-                           n_rows, lane);
+                store_rows(stage, x, out + 64 * j, 2 * kDLatent, n_rows, lane);
             } else {
-                float* dst = (whole ? static_cast<float*>(p.a.out) : p.part) + at;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(o[16 * h + i]) * inv);
-                    store_rows(stage, x, reinterpret_cast<char*>(dst + 16 * h), 4 * kDLatent, n_rows, lane);
+                    store_rows(stage, x, out + 128 * j + 64 * h, 4 * kDLatent, n_rows, lane);
                 }
             }
         }
         tc_fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(o_bar);
+        // O may be overwritten.  (Only if something will wait for it: no arrival may be on
+        // its way to a CTA that has left, and the closing barrier orders none.)
+        if (lane == 0 && c.left > 0) mbar_arrive_peer(o_bar);
     }
     if (!ok && lane == 0) raise_tree_error(&sh.abort_flag, p.status);
     if (rank == 0 && tid == 0) p.merge[cluster] = merge;
@@ -600,7 +617,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     }
     tc_fence_before_sync();
-    cluster_barrier();
+    cluster_barrier_relaxed();                             // neither CTA's shared memory goes before both are done
     if (warp == kMmaWarp) {
         tc_fence_after_sync();
         tmem_dealloc_pair(tmem, kTmemCols);
@@ -609,153 +626,152 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 // ============================== merge ======================================
 // Out of the clusters' notes, block x takes the x-th row block that clusters
-// share, block y a few of its rows.  Groups of 128 threads (a float4 of the 512
-// features each): up to kFewPieces pieces a group per row, all pieces in order;
-// with more, the pieces of a row are dealt to the four groups and the four sums
-// added in order.  Pieces are weighted by exp2(lse_i - max).
-constexpr int kMergeThreads = 512;
-constexpr int kMergeGroups = kMergeThreads / 128;
-constexpr int kFewPieces = 8;
-constexpr int kMaxPieces = 1024;                           // as many clusters
+// share.  A warp: 32 rows (one per lane) and QUADS feature quads; the pieces in
+// ascending order, a batch of loads in flight at a time, with a running maximum of
+// their log-sum-exps.  With few pieces a warp takes four quads (a lane's output is
+// a whole sector); with many, one quad, and four warps share the pieces and join
+// their sums in order (the pieces come from L2: 76 of them in one warp's hands
+// took three times as long).
+constexpr int kMergeWarps = 8;
+constexpr int kFewPieces = 8;                              // up to about so many per block: four quads per warp
 
-struct MergeShared {
-    float weight[kMaxPieces];
-    float4 sums[kMergeGroups][128];
-    int owner;
-    float base, sum;
-};
-
-// Piece i of a row: the owner's second slot, then the first slots of the clusters behind it.
-__device__ __forceinline__ long long piece_row(int c0, int i, int row) {
-    return static_cast<long long>(2 * (c0 + i) + (i == 0 ? 1 : 0)) * kTreeBlockRows + row;
-}
-__device__ __forceinline__ void add_scaled(float4& acc, float w, const float4 v) {
-    acc.x = fmaf(w, v.x, acc.x);
-    acc.y = fmaf(w, v.y, acc.y);
-    acc.z = fmaf(w, v.z, acc.z);
-    acc.w = fmaf(w, v.w, acc.w);
-}
-__device__ __forceinline__ void write_merged(const TreeParams& p, const TreeMerge& m, int row, int t, float4 acc,
-                                             float base, float sum) {
+template <int QUADS, int PARTS>
+__global__ void __launch_bounds__(32 * kMergeWarps) mla_tree_merge_kernel(const __grid_constant__ TreeParams p) {
+    constexpr int kBatch = QUADS == 1 ? 10 : 4;
+    __shared__ TreeMerge note;
+    __shared__ int owner;
+    __shared__ float joined[PARTS > 1 ? kMergeWarps : 1][6][32];   // maximum, sum, four features
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    grid_dependency_wait();
+    allow_dependent_launch();
+    if (warp == 0) {
+        int seen = 0;
+        bool found = false;
+        for (int c = 0; c < p.clusters && !found; c += 128) {
+            TreeMerge n[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int at = c + 32 * i + lane;
+                n[i] = p.merge[min(at, p.clusters - 1)];
+                if (at >= p.clusters) n[i].pieces = 0;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t bal = __ballot_sync(0xffffffffu, n[i].pieces > 0);
+                const int rank = seen + __popc(bal & ((1u << lane) - 1u));
+                if (n[i].pieces > 0 && rank == static_cast<int>(blockIdx.x)) {
+                    note = n[i];
+                    owner = c + 32 * i + lane;
+                }
+                seen += __popc(bal);
+            }
+            found = seen > static_cast<int>(blockIdx.x);
+        }
+        if (!found && lane == 0) owner = -1;
+    }
+    __syncthreads();
+    const int c0 = owner;
+    if (c0 < 0) return;
+    const TreeMerge m = note;
+    constexpr int kQuadWarps = kMergeWarps / PARTS;        // warps of a block with quads of their own
+    constexpr int kTasks = kDLatent / 4 / QUADS / kQuadWarps;   // blocks per 32 rows
+    const int group = static_cast<int>(blockIdx.y) / kTasks;
+    const int part_of = warp / kQuadWarps;                 // share of the pieces
+    const int quad = ((static_cast<int>(blockIdx.y) % kTasks) * kQuadWarps + warp % kQuadWarps) * QUADS;
+    const int row = 32 * group + lane;
+    const bool live = row < m.rows;
+    if (32 * group >= m.rows) return;                      // uniform over the block
+    // piece 0 is the owner's second slot, the others are the first slots of the clusters behind it
+    auto slot = [&](int i) { return 2 * (c0 + i) + (i == 0 ? 1 : 0); };
+    const float4* part = reinterpret_cast<const float4*>(p.part);
+    float4 acc[QUADS];
+#pragma unroll
+    for (int k = 0; k < QUADS; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f, top = -INFINITY, base = 0.f;
+    const int share = (m.pieces + PARTS - 1) / PARTS;
+    const int end = min(m.pieces, (part_of + 1) * share);
+    for (int i0 = part_of * share; i0 < end; i0 += kBatch) {
+        float l[kBatch];
+        float4 v[kBatch][QUADS];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int at = slot(min(i0 + i, end - 1));     // (no branch: all loads at once)
+            l[i] = live ? p.lse_part[at * kTreeBlockRows + row] : -INFINITY;
+            const float4* src = part + piece_quad(at, row, quad);
+#pragma unroll
+            for (int k = 0; k < QUADS; ++k) v[i][k] = src[32 * k];
+        }
+        const float before = top;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) top = fmaxf(top, l[i]);   // (the repeated last piece changes nothing)
+        if (top > before) {
+            const float scale = before > -INFINITY ? exp2f(before - top) : 0.f;
+            base = top;
+            // (a NaN stays: a product with 0 only drops sums of nothing)
+            if (before > -INFINITY || sum != 0.f) {
+                sum *= scale;
+#pragma unroll
+                for (int k = 0; k < QUADS; ++k)
+                    acc[k] = make_float4(acc[k].x * scale, acc[k].y * scale, acc[k].z * scale, acc[k].w * scale);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (i0 + i < end) {
+                const float w = exp2f(l[i] - base);        // NaN stays NaN
+                sum += w;
+#pragma unroll
+                for (int k = 0; k < QUADS; ++k) {
+                    acc[k].x = fmaf(w, v[i][k].x, acc[k].x);
+                    acc[k].y = fmaf(w, v[i][k].y, acc[k].y);
+                    acc[k].z = fmaf(w, v[i][k].z, acc[k].z);
+                    acc[k].w = fmaf(w, v[i][k].w, acc[k].w);
+                }
+            }
+    }
+    if constexpr (PARTS > 1) {
+        static_assert(QUADS == 1, "one quad per warp where warps share pieces");
+        const float mine[6] = {top, sum, acc[0].x, acc[0].y, acc[0].z, acc[0].w};
+#pragma unroll
+        for (int k = 0; k < 6; ++k) joined[warp][k][lane] = mine[k];
+        __syncthreads();
+        if (part_of != 0) return;
+        float t[PARTS];
+        top = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < PARTS; ++q) {
+            t[q] = joined[warp + q * kQuadWarps][0][lane];
+            top = fmaxf(top, t[q]);
+        }
+        base = top > -INFINITY ? top : 0.f;
+        sum = 0.f;
+        acc[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int q = 0; q < PARTS; ++q) {
+            const float(&from)[6][32] = joined[warp + q * kQuadWarps];
+            // (a share whose maximum is -infinity has the sum 0, or a NaN)
+            const float w = t[q] > -INFINITY ? exp2f(t[q] - base) : 1.f;
+            sum = fmaf(w, from[1][lane], sum);
+            acc[0].x = fmaf(w, from[2][lane], acc[0].x);
+            acc[0].y = fmaf(w, from[3][lane], acc[0].y);
+            acc[0].z = fmaf(w, from[4][lane], acc[0].z);
+            acc[0].w = fmaf(w, from[5][lane], acc[0].w);
+        }
+    }
+    if (!live) return;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const long long out_row =
         static_cast<long long>(m.b) * p.tokens * p.heads + static_cast<long long>(m.rb) * kTreeBlockRows + row;
-    if (t == 0) p.a.lse[out_row] = sum == 0.f ? -INFINITY : (base + log2f(sum)) * kLn2;
-    const float4 v = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-    const long long at = out_row * kDLatent + 4 * t;
-    if (p.a.out_fp32)
-        *reinterpret_cast<float4*>(static_cast<float*>(p.a.out) + at) = v;
-    else
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.a.out) + at) =
-            make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-}
-
-__device__ void merge_few(const TreeParams& p, int c0, const TreeMerge& m, int row, int t) {
-    const float4* part = reinterpret_cast<const float4*>(p.part);
-    float l[kFewPieces];
-    float4 v[kFewPieces];
-    float top = -INFINITY;
+    if (quad == 0) p.a.lse[out_row] = sum == 0.f ? -INFINITY : (base + log2f(sum)) * kLn2;
 #pragma unroll
-    for (int i = 0; i < kFewPieces; ++i)
-        if (i < m.pieces) {
-            l[i] = p.lse_part[piece_row(c0, i, row)];
-            v[i] = part[piece_row(c0, i, row) * 128 + t];
-            top = fmaxf(top, l[i]);
-        }
-    const float base = top > -INFINITY ? top : 0.f;
-    float sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < kFewPieces; ++i)
-        if (i < m.pieces) {
-            const float w = exp2f(l[i] - base);            // NaN stays NaN
-            sum += w;
-            add_scaled(acc, w, v[i]);
-        }
-    write_merged(p, m, row, t, acc, base, sum);
-}
-
-// All threads of the block.
-__device__ void merge_many(const TreeParams& p, int c0, const TreeMerge& m, int row, MergeShared& sh) {
-    const float4* part = reinterpret_cast<const float4*>(p.part);
-    const int group = threadIdx.x >> 7, t = threadIdx.x & 127, lane = threadIdx.x & 31;
-    if (threadIdx.x < 32) {
-        float top = -INFINITY;
-        for (int i = lane; i < m.pieces; i += 32) {
-            const float l = p.lse_part[piece_row(c0, i, row)];
-            sh.weight[i] = l;
-            top = fmaxf(top, l);
-        }
-        top = warp_max_f32(top);
-        const float b = top > -INFINITY ? top : 0.f;
-        float s = 0.f;
-        for (int i = lane; i < m.pieces; i += 32) {
-            const float w = exp2f(sh.weight[i] - b);
-            sh.weight[i] = w;
-            s += w;
-        }
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (lane == 0) {
-            sh.base = b;
-            sh.sum = s;
-        }
-    }
-    __syncthreads();
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = group; i0 < m.pieces; i0 += 8 * kMergeGroups) {
-        float4 v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (i0 + k * kMergeGroups < m.pieces) v[k] = part[piece_row(c0, i0 + k * kMergeGroups, row) * 128 + t];
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (i0 + k * kMergeGroups < m.pieces) add_scaled(acc, sh.weight[i0 + k * kMergeGroups], v[k]);
-    }
-    sh.sums[group][t] = acc;
-    __syncthreads();
-    if (group == 0) {
-#pragma unroll
-        for (int k = 1; k < kMergeGroups; ++k) {
-            const float4 v = sh.sums[k][t];
-            acc = make_float4(acc.x + v.x, acc.y + v.y, acc.z + v.z, acc.w + v.w);
-        }
-        write_merged(p, m, row, t, acc, sh.base, sh.sum);
-    }
-}
-
-__global__ void __launch_bounds__(kMergeThreads) mla_tree_merge_kernel(const __grid_constant__ TreeParams p,
-                                                                       int rows_per_block) {
-    __shared__ MergeShared sh;
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int group = tid >> 7, t = tid & 127;
-    grid_dependency_wait();
-    allow_dependent_launch();
-    if (tid < 32) {
-        int seen = 0, found = -1;
-        for (int c = 0; c < p.clusters && found < 0; c += 32) {
-            const bool has = c + lane < p.clusters && p.merge[c + lane].pieces > 0;
-            const uint32_t bal = __ballot_sync(0xffffffffu, has);
-            if (seen + __popc(bal) > static_cast<int>(blockIdx.x)) {
-                const bool mine = has && seen + __popc(bal & ((1u << lane) - 1u)) == static_cast<int>(blockIdx.x);
-                found = c + __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
-            }
-            seen += __popc(bal);
-        }
-        if (lane == 0) sh.owner = found;
-    }
-    __syncthreads();
-    const int c0 = sh.owner;
-    if (c0 < 0) return;
-    const TreeMerge m = p.merge[c0];
-    const int row0 = static_cast<int>(blockIdx.y) * rows_per_block;
-    if (m.pieces <= kFewPieces) {
-        if (group < rows_per_block && row0 + group < m.rows) merge_few(p, c0, m, row0 + group, t);
-    } else {
-        for (int row = row0; row < min(row0 + rows_per_block, m.rows); ++row) {
-            merge_many(p, c0, m, row, sh);
-            __syncthreads();
-        }
+    for (int k = 0; k < QUADS; ++k) {
+        const float4 v = make_float4(acc[k].x * inv, acc[k].y * inv, acc[k].z * inv, acc[k].w * inv);
+        const long long at = out_row * kDLatent + 4 * (quad + k);
+        if (p.a.out_fp32)
+            *reinterpret_cast<float4*>(static_cast<float*>(p.a.out) + at) = v;
+        else
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.a.out) + at) =
+                make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
     }
 }
 
@@ -782,13 +798,17 @@ cudaError_t launch_tree_attend(const TreeMaps& maps, const TreeParams& p, bool p
     // at most one shared row block per cluster, and no more than there are
     const long long blocks =
         static_cast<long long>(p.batch) * ((p.tokens * p.heads + kTreeBlockRows - 1) / kTreeBlockRows);
-    // a row block has about clusters / blocks pieces: few pieces, a row per group
-    const int rows = std::min(p.tokens * p.heads, kTreeBlockRows);
-    const int per = p.clusters > kFewPieces * blocks ? 1 : kMergeGroups;
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(p.clusters, blocks)), (rows + per - 1) / per);
-    cfg.blockDim = dim3(kMergeThreads);
+    const unsigned items = static_cast<unsigned>(std::min<long long>(p.clusters, blocks));
+    const int groups = (std::min(p.tokens * p.heads, kTreeBlockRows) + 31) / 32;
+    cfg.blockDim = dim3(32 * kMergeWarps);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, mla_tree_merge_kernel, p, per);
+    // a row block has about clusters / blocks pieces
+    if (p.clusters > kFewPieces * blocks) {
+        cfg.gridDim = dim3(items, groups * (kDLatent / 4 / (kMergeWarps / 4)));
+        return cudaLaunchKernelEx(&cfg, mla_tree_merge_kernel<1, 4>, p);
+    }
+    cfg.gridDim = dim3(items, groups * (kDLatent / 16 / kMergeWarps));
+    return cudaLaunchKernelEx(&cfg, mla_tree_merge_kernel<4, 1>, p);
 }
 
 }  // namespace mla

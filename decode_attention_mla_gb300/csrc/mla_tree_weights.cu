@@ -383,7 +383,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     }
     tc_fence_before_sync();
-    cluster_barrier();
+    cluster_barrier();                                     // orders the last arrivals at the other CTA, too
     if (warp == kMmaWarp) {
         tc_fence_after_sync();
         tmem_dealloc_pair(tmem, kTmemCols);

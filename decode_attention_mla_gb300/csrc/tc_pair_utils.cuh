@@ -29,6 +29,10 @@ __device__ __forceinline__ bool elect_one() {
         : "=r"(r));
     return r != 0;
 }
+// The same without ordering memory accesses.
+__device__ __forceinline__ void cluster_barrier_relaxed() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
 // The two halves of cluster_barrier: what a thread did before its arrival is
 // visible after the others' wait.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
