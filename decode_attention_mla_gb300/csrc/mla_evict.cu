@@ -39,7 +39,7 @@ constexpr int kMaxCluster = 8;
 // One CTA up to this many rows per request, a cluster of eight above.
 constexpr int kOneCtaRows = 8192;
 constexpr int kMoveThreads = 256;
-constexpr int kMoveBlocks = 152 * 6;                       // blocks that fill the GPU twice
+constexpr int kMoveBlocks = 152 * 12;                      // about four times what fits the GPU at once
 constexpr int kMoveUnits = 288;                            // 16-byte units a warp moves at a time
 
 struct EvictScratch {

@@ -315,3 +315,146 @@ def test_long_cache_weights_sum_to_the_tokens_and_heads():
     mla.tree_weights(p, c.d["q"], c.d["kv"], lse, mla.tree_alloc_scratch(p), w, **c.kw())
     assert abs(float(w.double().sum()) - 3 * 128) <= 3 * 128 * 1e-4
     c.check(out, lse)
+
+
+@pytest.mark.parametrize("num_sms", [0, 10])
+def test_many_requests_of_all_lengths(num_sms):
+    rnd = random.Random(4)
+    lens = [rnd.choice([-1, 0, 1, 63, 127, 128, 129, 200, 300]) for _ in range(70)]
+    n = [rnd.randint(0, 3) for _ in range(70)]
+    c = Case(40, lens, 3, 16, n_tokens=n)
+    out, lse = c.run(num_sms=num_sms)
+    c.check(out, lse)
+    old = torch.rand(c.kv.shape[0])
+    w = old.cuda()
+    p = c.plan(num_sms=num_sms)
+    mla.tree_weights(p, c.d["q"], c.d["kv"], lse, mla.tree_alloc_scratch(p), w, decay=0.25, **c.kw())
+    new, tol = ref.weights(c.q, c.kv, lse.cpu(), old, d_pos=c.lens, row_offset=c.offs, n_tokens=c.n, bits=c.bits,
+                           scale=SCALE, decay=0.25)
+    assert ((w.double().cpu() - new).abs() <= tol).all()
+
+
+def test_a_batch_with_nothing_to_attend():
+    c = Case(41, [-1, 0, -1], 2, 16, n_tokens=[2, 0, 1])
+    out, lse = c.run()
+    c.check(out, lse)
+
+
+@pytest.mark.parametrize("Q,H", [(1, 16), (2, 128), (3, 128), (9, 128)])
+@pytest.mark.parametrize("num_sms", [2, 4, 0])
+def test_weights_of_several_requests_in_one_run(Q, H, num_sms):
+    """All forms of the staging (one and two resident query blocks, streamed ones) across requests."""
+    c = Case(50 + Q, [600, 0, 257, 1000, 255, 1, 511], Q, H, n_tokens=[Q, Q, 1, Q, 0, Q, max(1, Q - 1)])
+    out, lse = c.run(num_sms=num_sms)
+    old = torch.rand(c.kv.shape[0])
+    results = []
+    for pdl in (False, True):
+        w = old.cuda()
+        p = c.plan(num_sms=num_sms, pdl=pdl)
+        scratch = mla.tree_alloc_scratch(p)
+        mla.tree_weights(p, c.d["q"], c.d["kv"], lse, scratch, w, decay=0.75, **c.kw())
+        torch.cuda.synchronize()
+        assert mla.status_word(p, scratch) == 0
+        results.append(w)
+    new, tol = ref.weights(c.q, c.kv, lse.cpu(), old, d_pos=c.lens, row_offset=c.offs, n_tokens=c.n, bits=c.bits,
+                           scale=SCALE, decay=0.75)
+    assert ((results[0].double().cpu() - new).abs() <= tol).all()
+    assert torch.equal(results[0], results[1])
+
+
+def test_rows_past_4_gigabytes():
+    """The same requests at the front of a cache and behind its first 4 GiB give the same bits."""
+    far = (1 << 32) // 1152 + 1000
+    rows = far + 1200
+    kv = torch.empty(rows, 576, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    kv[:1200] = torch.randn(1200, 576, generator=g, device="cuda").bfloat16()
+    kv[far:] = kv[:1200]
+    c = Case(60, [1000], 7, 16)
+    d_pos = torch.tensor([1000], dtype=torch.int32, device="cuda")
+    weights, positions = torch.zeros(rows, device="cuda"), torch.zeros(rows, dtype=torch.int32, device="cuda")
+    seen = []
+    for at in (0, far):
+        off = torch.tensor([at], dtype=torch.int64, device="cuda")
+        p = c.plan()
+        scratch = mla.tree_alloc_scratch(p)
+        new = torch.randn(1, 7, 576, generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+        pos = torch.arange(1000, 1007, dtype=torch.int32, device="cuda")[None]
+        mla.rope_append(mla.rope_table(64), pos, c=new[..., :512], k_rope=new[..., 512:], kv=kv, d_pos=d_pos,
+                        row_offset=off, row_positions=positions, row_weights=weights)
+        out, lse = c.outputs()
+        kw = dict(d_pos=d_pos, row_offset=off, mask=c.d["mask"])
+        mla.tree_forward(p, c.d["q"], kv, out, lse, scratch, **kw)
+        mla.tree_weights(p, c.d["q"], kv, lse, scratch, weights, decay=0.0, **kw)
+        mla.tree_commit(kv, torch.tensor([[3, 5, 6]], dtype=torch.int32, device="cuda"),
+                        torch.tensor([3], dtype=torch.int32, device="cuda"), d_pos=d_pos, row_offset=off,
+                        row_weights=weights)
+        d = d_pos + 3
+        mla.evict(kv, weights, positions, mla.evict_alloc_scratch(batch=1, keep=600), d_pos=d,
+                  next_pos=torch.tensor([1007], dtype=torch.int32, device="cuda"), keep=600, row_offset=off)
+        seen.append((out, lse, weights[at:at + 1200].clone(), kv[at:at + 1200].clone(), d.clone()))
+    for x, y in zip(*seen):
+        assert torch.equal(x.view(torch.int16) if x.dtype == torch.bfloat16 else x,
+                           y.view(torch.int16) if y.dtype == torch.bfloat16 else y)
+
+
+def test_a_wait_that_runs_out_is_reported_and_the_context_stays_usable():
+    c = Case(61, [3000, 50], 8, 16)
+    want = c.reference()
+    p = c.plan(stall_test=True)
+    good = c.plan()
+    scratch = mla.tree_alloc_scratch(p)
+    out, lse = c.outputs()
+    args = mla.tree_make_args(c.d["q"], c.d["kv"], out, lse, **c.kw())
+    w = torch.zeros(c.kv.shape[0], device="cuda")
+    for call in (lambda q: mla.tree_forward_args(q, args, scratch),
+                 lambda q: mla.tree_weights_args(q, args, scratch, w, decay=0.0)):
+        mla.scratch_init(scratch)
+        call(p)
+        torch.cuda.synchronize()
+        assert mla.status_word(p, scratch) == mla.EDEVICE
+    mla.scratch_init(scratch)
+    mla.tree_forward_args(good, args, scratch)
+    torch.cuda.synchronize()
+    assert mla.status_word(good, scratch) == 0
+    c.check(out, lse, want)
+
+
+def test_two_host_threads():
+    import threading
+    cases = [Case(70 + i, [500 + 300 * i, 40], 6, 16) for i in range(2)]
+    got, failed = [None, None], []
+
+    def work(i):
+        try:
+            c, s = cases[i], torch.cuda.Stream()
+            p = c.plan(pdl=True)
+            scratch, (out, lse) = mla.tree_alloc_scratch(p), c.outputs()
+            torch.cuda.synchronize()
+            for _ in range(20):
+                mla.tree_forward(p, c.d["q"], c.d["kv"], out, lse, scratch, stream=s, **c.kw())
+            s.synchronize()
+            got[i] = (out, lse)
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not failed
+    for c, r in zip(cases, got):
+        c.check(*r)
+
+
+def test_arguments_of_another_shape_than_the_plan_are_refused():
+    c = Case(62, [30], 4, 16)
+    p = mla.tree_plan(batch=1, tokens=5, heads=16, scale=SCALE)
+    out, lse = c.outputs()
+    with pytest.raises(ValueError, match="plan"):
+        mla.tree_forward(p, c.d["q"], c.d["kv"], out, lse, mla.tree_alloc_scratch(p), **c.kw())
+    with pytest.raises(ValueError):
+        mla.tree_make_args(c.d["q"], c.d["kv"].to(torch.float16), out, lse, **c.kw())
+    with pytest.raises(ValueError):
+        mla.tree_make_args(c.d["q"].transpose(1, 2), c.d["kv"], out, lse, **c.kw())
+    with pytest.raises(ValueError):
+        mla.tree_make_args(c.d["q"], c.d["kv"], out, lse, **{**c.kw(), "d_pos": c.d["d_pos"].long()})
