@@ -133,25 +133,41 @@ __global__ void __launch_bounds__(kSelThreads) mla_evict_select_kernel(const mla
     // rows below keep get their own weight and position in the outputs (the move
     // overwrites those of the evicted ones)
     const bool copy_w = a.weights_out != a.weights, copy_p = a.positions_out != a.positions;
-    for (int r = r0 + tid; r < r1; r += kLoadBatch * kSelThreads) {
-        float w[kLoadBatch];
-        int pos[kLoadBatch];
+    auto load = [&](int r, int end, float (&w)[kLoadBatch], int (&pos)[kLoadBatch]) {
 #pragma unroll
         for (int i = 0; i < kLoadBatch; ++i) {
-            const int row = min(r + i * kSelThreads, r1 - 1);   // (no branch: all loads at once)
+            const int row = min(r + i * kSelThreads, end - 1);   // (no branch: all loads at once)
             w[i] = a.weights[base + row];
             pos[i] = a.positions[base + row];
         }
+    };
+    auto copy = [&](int r, int end, const float (&w)[kLoadBatch], const int (&pos)[kLoadBatch]) {
 #pragma unroll
         for (int i = 0; i < kLoadBatch; ++i) {
             const int row = r + i * kSelThreads;
-            if (row < r1) {
-                if (row - r0 < kCache) cached[row - r0] = rank_key(w[i], pos[i], a.sink, recent_from);
-                if (row < keep) {
-                    if (copy_w) a.weights_out[base + row] = w[i];
-                    if (copy_p) a.positions_out[base + row] = pos[i];
-                }
+            if (row < end) {
+                if (copy_w) a.weights_out[base + row] = w[i];
+                if (copy_p) a.positions_out[base + row] = pos[i];
             }
+        }
+    };
+    float w[kLoadBatch];
+    int pos[kLoadBatch];
+    for (int r = r0 + tid; r < r1; r += kLoadBatch * kSelThreads) {
+        load(r, r1, w, pos);
+#pragma unroll
+        for (int i = 0; i < kLoadBatch; ++i) {
+            const int row = r + i * kSelThreads;
+            if (row < r1 && row - r0 < kCache) cached[row - r0] = rank_key(w[i], pos[i], a.sink, recent_from);
+        }
+        if (CL == 1) copy(r, min(r1, keep), w, pos);
+    }
+    if (CL > 1 && (copy_w || copy_p)) {
+        // (the first CTAs have all the rows below keep: shared out over the cluster)
+        const int per_cta = (keep + CL - 1) / CL, c0 = min(keep, rank * per_cta), c1 = min(keep, c0 + per_cta);
+        for (int r = c0 + tid; r < c1; r += kLoadBatch * kSelThreads) {
+            load(r, c1, w, pos);
+            copy(r, c1, w, pos);
         }
     }
 
@@ -304,12 +320,28 @@ __global__ void __launch_bounds__(kSelThreads) mla_evict_select_kernel(const mla
     }
     int* hole_list = s.hole + static_cast<long long>(b) * a.keep;
     int* moved_list = s.moved + static_cast<long long>(b) * a.keep;
-    each_key([&](int r, uint32_t k) {
-        bool kept = k > K;
-        if (k == K) kept = eq++ < need;
-        if (!kept && r < keep) hole_list[hole0++] = r;
-        if (kept && r >= keep) moved_list[moved0++] = r;
-    });
+    // the warp's rows again, now 32 at a time, so that the lists are written in runs
+    // (a thread's own rows one by one: scattered stores, three times the time)
+    eq = __shfl_sync(0xffffffffu, eq, 0);
+    hole0 = __shfl_sync(0xffffffffu, hole0, 0);
+    moved0 = __shfl_sync(0xffffffffu, moved0, 0);
+    const uint32_t lower = (1u << lane) - 1u;
+    const int warp_from = static_cast<int>(min(static_cast<long long>(r1), r0 + static_cast<long long>(warp) * 32 * each));
+    const int warp_to = static_cast<int>(min(static_cast<long long>(r1), warp_from + 32ll * each));
+    for (int r = warp_from; r < warp_to; r += 32) {
+        const int row = r + lane;
+        const bool in = row < warp_to;
+        const uint32_t k = in ? key_of(row) : 0u;
+        const uint32_t e = __ballot_sync(0xffffffffu, in && k == K);
+        const bool kept = in && (k > K || (k == K && eq + __popc(e & lower) < need));
+        const bool hole = in && row < keep && !kept, moved = row >= keep && kept;
+        const uint32_t hb = __ballot_sync(0xffffffffu, hole), mb = __ballot_sync(0xffffffffu, moved);
+        if (hole) hole_list[hole0 + __popc(hb & lower)] = row;
+        if (moved) moved_list[moved0 + __popc(mb & lower)] = row;
+        eq += __popc(e);
+        hole0 += __popc(hb);
+        moved0 += __popc(mb);
+    }
     allow_dependent_launch();
     everyone();                                            // no CTA leaves while others read its shared memory
 }

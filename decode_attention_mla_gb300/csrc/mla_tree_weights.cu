@@ -13,7 +13,7 @@
 // Staging by TMA, in one of three forms chosen by the most query rows a request
 // can have:
 //   up to 128   queries resident (72 KB), K in 9 slots of 16 KB
-//   up to 256   queries resident (144 KB), K in 4 slots
+//   up to 256   queries resident (144 KB), K in 5 slots (with 4, 7% slower)
 //   more        K of the tile resident (9 slots), the query blocks streamed past
 //               it from L2 through 9 slots of 8 KB: each cache row is read once
 //               however many query rows there are
@@ -49,7 +49,7 @@ constexpr long long kDrainCycles = 2000ll * 1000ll;
 template <int kBlocks>
 struct Cfg {
     static constexpr bool kStream = kBlocks == 0;
-    static constexpr int kKSlots = kBlocks == 2 ? 4 : 9;
+    static constexpr int kKSlots = kBlocks == 2 ? 5 : 9;
     static constexpr int kQBuffers = kBlocks == 2 ? 2 : 1;
     static constexpr int kScoreCols = kBlocks == 2 ? 256 : 128;   // of one of the two score buffers
 };
