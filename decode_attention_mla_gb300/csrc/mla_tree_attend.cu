@@ -97,13 +97,17 @@ struct Producer {
     Shared& sh;
     uint32_t rank;
     uint64_t pol_kv, pol_q;
+    uint32_t leader;                                       // what turns this CTA's addresses into the even CTA's
     uint32_t specials = 0;
 
     // The even CTA's barrier of a load; that CTA announces both CTAs' bytes (the odd
     // CTA's may land first: the phase is open until the announcement arrives).
     __device__ __forceinline__ uint32_t expect(uint64_t* bar, uint32_t bytes) {
         if (rank == 0) mbar_arrive_expect_tx(bar, 2 * bytes);
-        return map_to_rank(bar, 0);
+        return smem_u32(bar) + leader;
+    }
+    __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
+        return mbar_try_wait(bar, parity) || wait_slowly(bar, parity, &sh.abort_flag);
     }
     __device__ bool load_q(const Cursor& c) {
         if (c.item > 0 && !mbar_wait_bounded(&sh.q_empty, (c.item - 1) & 1, &sh.abort_flag)) return false;
@@ -115,9 +119,9 @@ struct Producer {
     // QK operands: this CTA's 64 keys, 128 columns a slot, the rope columns with the last
     __device__ bool load_k(const Cursor& c) {
         const int y = static_cast<int>(c.r.base) + c.tile * kTreeTileKeys + static_cast<int>(rank) * 64;
-#pragma unroll 1
+#pragma unroll
         for (int s = 0; s < kSlots; ++s) {
-            if (c.g > 0 && !mbar_wait_bounded(&sh.k_empty[s], (c.g - 1) & 1, &sh.abort_flag)) return false;
+            if (c.g > 0 && !wait(&sh.k_empty[s], (c.g - 1) & 1)) return false;
             const uint32_t bar = expect(&sh.k_ready[s], kSlotBytes + (s == 3 ? kChunkBytes : 0));
             tma_load_3d_pair(sh.k[s], &maps.kv, 0, y, 2 * s, bar, pol_kv);
             if (s == 3) tma_load_3d_pair(sh.rope, &maps.rope, 0, y, 8, bar, pol_kv);
@@ -135,9 +139,9 @@ struct Producer {
             mbar_arrive_expect_tx(local, 4 * kSlotBytes);
             ++specials;
         }
-#pragma unroll 1
+#pragma unroll
         for (int i = 0; i < 2; ++i) {
-            if (c.g > 0 && !mbar_wait_bounded(&sh.v_empty[i], (c.g - 1) & 1, &sh.abort_flag)) return false;
+            if (c.g > 0 && !wait(&sh.v_empty[i], (c.g - 1) & 1)) return false;
             const int z = 4 * i + 2 * static_cast<int>(rank);
             if (special) {
                 // the softmax threads wait for these bytes and vouch for them with P
@@ -157,7 +161,8 @@ struct Producer {
 // One thread for the query rows and K, one for V: K of a tile is taken before V
 // of the tile before it, so neither waits in the other's queue.
 __device__ void produce(const TreeMaps& maps, const TreeParams& p, Shared& sh, uint32_t rank, bool values) {
-    Producer pr{maps, p, sh, rank, l2_policy_evict_normal(), l2_policy_evict_normal()};
+    Producer pr{maps, p, sh, rank, l2_policy_evict_normal(), l2_policy_evict_normal(),
+                map_to_rank(&sh, 0) - smem_u32(&sh)};
     Cursor c;
     bool ok = true;
     for (c.start(p, sh.work); c.left > 0 && ok; c.next(p)) {
