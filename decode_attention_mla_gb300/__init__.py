@@ -523,6 +523,8 @@ def rope_make_args(table: RopeTable, positions, *, q_rope=None, q=None, c=None, 
         a.q_out, a.q_out_batch, a.q_out_token, a.q_out_head = _strides(part, "q", (B, N, H, D_ROPE), 3)
     if not (c is None) == (k_rope is None) == (kv is None) == (d_pos is None):
         raise ValueError("c, k_rope, kv and d_pos go together")
+    if kv is None and not (row_positions is None and row_weights is None):
+        raise ValueError("row_positions and row_weights belong to the rows of kv")
     if kv is not None:
         a.c, a.c_batch, a.c_token = _strides(c, "c", (B, N, D_LATENT), 2)
         a.k_rope, a.k_rope_batch, a.k_rope_token = _strides(k_rope, "k_rope", (B, N, D_ROPE), 2)

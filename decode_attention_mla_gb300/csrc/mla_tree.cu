@@ -18,7 +18,7 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 int check_shape(const mla_tree_shape* s) {
     if (!s) return MLA_EINVAL;
     if (s->batch < 1 || s->batch > 4096 || s->tokens < 1 || s->tokens > MLA_TREE_MAX_TOKENS) return MLA_EINVAL;
-    if (!(s->scale > 0.f) || !std::isfinite(s->scale)) return MLA_EINVAL;
+    if (!(s->scale > 0.f) || !std::isfinite(s->scale * kLog2e)) return MLA_EINVAL;
     if (s->num_sms < 0 || (s->pdl != 0 && s->pdl != 1) || (s->stall_test != 0 && s->stall_test != 1))
         return MLA_EINVAL;
     if (s->heads < 1 || s->heads > 128) return MLA_EUNSUPPORTED;

@@ -14,6 +14,7 @@ namespace mla {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTreeTileKeys = 128;                         // cache rows per tile of a CTA pair
 constexpr int kTreeBlockRows = 128;                        // (token, head) rows per CTA pair
+constexpr long long kTreeMaxRow = 0x7fffff00;              // rows of a request from here on are not attended
 
 // What a cluster leaves for the merge: its last piece is the first one of a row
 // block that `pieces` consecutive clusters share (0: nothing to merge).
@@ -43,14 +44,15 @@ struct TreeRequest {
 
 __device__ __forceinline__ TreeRequest load_tree_request(const TreeParams& p, int b) {
     TreeRequest r;
-    r.base = p.a.row_offset ? p.a.row_offset[b] : 0;
+    // (an offset at which no row can lie inside is as good as any other such)
+    r.base = p.a.row_offset ? max(p.a.row_offset[b], -(1ll << 40)) : 0;
     r.d_pos = p.a.d_pos[b];
     r.n_tok = p.a.n_tokens ? min(max(p.a.n_tokens[b], 0), p.tokens) : p.tokens;
     const long long rows = r.d_pos < 0 ? 0 : static_cast<long long>(r.d_pos) + r.n_tok;
     const long long lo = r.base < 0 ? -r.base : 0, end = p.a.kv_rows - r.base;
-    const long long hi = end < rows ? end : rows;
-    // base > kv_rows or base <= -rows: none of the rows is inside (and base + t
-    // fits 32 bits for every t < hi otherwise)
+    const long long hi = min(min(end, rows), kTreeMaxRow);
+    // hi <= lo: none of the rows is inside (otherwise base + t fits 32 bits for
+    // every t < hi, and so does the last tile's end)
     r.hi = hi > lo ? static_cast<int>(hi) : 0;
     r.lo = hi > lo ? static_cast<int>(lo) : 0;
     return r;

@@ -55,7 +55,7 @@ MLA_API int mla_rope_table(const mla_rope_spec *spec, unsigned long long *turns)
 
 typedef struct {
     int batch;                  /* B: 1 .. 65535 requests */
-    int tokens;                 /* N: new tokens per request (the largest), 1 .. 2^30 */
+    int tokens;                 /* N: new tokens per request (the largest), 1 .. 2^28 */
     int heads;                  /* 0 .. 128; 0 = no queries */
     int rot_dim;                /* as in the table */
     int interleaved;            /* 1 = pairs (2j, 2j + 1); 0 = pairs (j, j + rot_dim / 2) */

@@ -15,8 +15,10 @@
  *
  * What a token does not attend does not reach its result, whatever it holds
  * (NaN and infinities too): rows behind the drafts, drafted rows its mask
- * leaves out, rows outside [0, kv_rows).  An attended row with a NaN, or whose
- * score is NaN or +infinity, makes the whole result of the (token, head) NaN.
+ * leaves out, rows outside [0, kv_rows), rows t >= 2^31 - 256 of a request.
+ * An attended row with a NaN, or whose score is NaN or +infinity, makes the
+ * whole result of the (token, head) NaN; one whose score is -infinity adds
+ * nothing, or a NaN to those elements of the result where its latent is infinite.
  * A token that attends no row gets out = 0 and lse = -infinity.  Outputs of
  * the tokens behind n_tokens[b] are left as they were.
  *
@@ -37,7 +39,7 @@ typedef struct {
     int batch;            /* 1 .. 4096 requests */
     int tokens;           /* Q: largest number of drafted tokens per request, 1 .. 64 */
     int heads;            /* 1 .. 128 */
-    float scale;          /* softmax scale, finite and > 0 */
+    float scale;          /* softmax scale, > 0 and below 2.3e38 */
     int num_sms;          /* SMs to plan for; 0 = query the current device and prepare the kernels there */
     int pdl;              /* 1 = launch with programmatic dependent launch */
     int stall_test;       /* test hook, as in mla_decode_shape */
@@ -51,8 +53,8 @@ typedef struct {
     int grid;                  /* CTAs of the attention kernel */
     size_t scratch_bytes;
     size_t status_offset;      /* int32 status word: 0 healthy, else an mla_status */
-    size_t part_offset;        /* fp32 slice outputs */
-    size_t lse_part_offset;    /* fp32 slice log-sum-exps */
+    size_t part_offset;        /* fp32 pieces of outputs */
+    size_t lse_part_offset;    /* fp32 log-sum-exps of the pieces */
 } mla_tree_plan_t;
 
 typedef struct {

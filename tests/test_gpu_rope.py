@@ -132,3 +132,11 @@ def test_many_tokens_linear_scaling():
     want = ref.rotate(qp[..., 128:], pos[..., None], ref.inv_freq(64, 1e6, "linear", 4.0), 64, True, 1.0)
     # the 64-bit reference's own product p f is exact to 2^-52 of 120000 radians
     assert ((q[..., 512:].double().cpu() - want).abs() <= bound(qp[..., 128:], want, pos, 1.0)).all()
+
+
+def test_side_arrays_without_rows_are_refused():
+    x = torch.zeros(1, 1, 16, 64, dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros(1, 1, 16, 576, dtype=torch.bfloat16, device="cuda")
+    pos = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="belong"):
+        mla.rope_append(mla.rope_table(), pos, q_rope=x, q=q, row_weights=torch.zeros(4, device="cuda"))

@@ -4,6 +4,9 @@ evict when the cache outgrows its budget, and decode on with the dense kernels.
 Each step is checked against the plain form on the cache as it stood."""
 import math
 import random
+import subprocess
+import sys
+from pathlib import Path
 
 import pytest
 import torch
@@ -182,3 +185,59 @@ def test_serving_loop_as_one_graph():
             assert torch.equal(x.view(torch.int32), y.view(torch.int32))
         assert torch.equal(a.positions, b.positions)
     assert max(a.d_pos.tolist()) == a.KEEP
+
+
+FIRST_USE = """
+import torch, decode_attention_mla_gb300 as mla
+N, KEEP = 20000, 7000
+g = torch.Generator(device="cuda").manual_seed(3)
+i32 = dict(dtype=torch.int32, device="cuda")
+kv = torch.randn(N + 8, 576, device="cuda", generator=g).bfloat16()
+w = torch.rand(N + 8, device="cuda", generator=g)
+pos = torch.arange(N + 8, **i32)
+table = mla.rope_table()
+state = dict(kv=kv, w=w, pos=pos, d=torch.tensor([N], **i32), q=torch.zeros(1, 4, 16, 576, device="cuda").bfloat16())
+start = {k: v.clone() for k, v in state.items()}
+x = torch.randn(1, 4, 16, 64, device="cuda", generator=g).bfloat16()
+rows = torch.randn(1, 4, 576, device="cuda", generator=g).bfloat16()
+at = torch.arange(N, N + 4, **i32)[None].contiguous()
+accept, n_accept, nxt = torch.tensor([[0, 2, 3, 0]], **i32), torch.tensor([3], **i32), torch.tensor([N + 3], **i32)
+scratch = mla.evict_alloc_scratch(batch=1, keep=KEEP)
+plan = mla.tree_plan(batch=1, tokens=4, heads=16, scale=0.04, num_sms=152)
+tree_scratch = mla.tree_alloc_scratch(plan)
+lse = torch.zeros(1, 4, 16, device="cuda")
+out = torch.zeros(1, 4, 16, 512, device="cuda")
+
+def step(s):
+    mla.rope_append(table, at, q_rope=x, q=s["q"], c=rows[..., :512], k_rope=rows[..., 512:], kv=s["kv"],
+                    d_pos=s["d"], row_positions=s["pos"], row_weights=s["w"])
+    mla.tree_commit(s["kv"], accept, n_accept, d_pos=s["d"], d_pos_out=s["d"], row_positions=s["pos"],
+                    row_weights=s["w"])
+    mla.evict(s["kv"], s["w"], s["pos"], scratch, d_pos=s["d"], next_pos=nxt, keep=KEEP, sink=4, recent=64)
+
+torch.cuda.synchronize()
+refused = False
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    step(state)                                   # the library's first launches
+    try:
+        mla.tree_forward(plan, state["q"], state["kv"], out, lse, tree_scratch, d_pos=state["d"])
+    except mla.MLADecodeError as e:
+        refused = e.status == mla.ENOTREADY
+assert refused
+for _ in range(2):
+    for k, v in start.items():
+        state[k].copy_(v)
+    graph.replay()
+torch.cuda.synchronize()
+step(start)
+for k, v in start.items():
+    assert torch.equal(state[k], v), k
+print("same")
+"""
+
+
+def test_first_use_inside_a_capture():
+    run = subprocess.run([sys.executable, "-c", FIRST_USE], cwd=Path(mla.__file__).parents[1], capture_output=True,
+                         text=True, timeout=300)
+    assert run.returncode == 0 and "same" in run.stdout, run.stderr[-2000:]

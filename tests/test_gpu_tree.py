@@ -143,6 +143,21 @@ def test_negative_row_offset_starts_inside_the_request():
     c.check(*c.run())
 
 
+def test_offsets_at_which_no_row_can_lie_inside():
+    c = Case(12, [30, 30, 30, 100], 4, 16)
+    c.d["d_pos"] = torch.tensor([2**31 - 1, 50, 2**31 - 1, 100], dtype=torch.int32, device="cuda")
+    c.d["row_offset"] = torch.tensor([-2**31, 2**62, -2**63, c.offs[3]], dtype=torch.int64, device="cuda")
+    out, lse = c.run()
+    assert (out[:3] == 0).all() and torch.isneginf(lse[:3]).all()
+    c.check(out, lse, {**{(b, i): (torch.zeros(16, 512), torch.full((16,), -math.inf), torch.zeros(16, 512),
+                                   torch.zeros(16)) for b in range(3) for i in range(4)},
+                       **{k: v for k, v in c.reference().items() if k[0] == 3}})
+    w = torch.full((c.kv.shape[0],), 5.0, device="cuda")
+    p = c.plan()
+    mla.tree_weights(p, c.d["q"], c.d["kv"], lse, mla.tree_alloc_scratch(p), w, decay=0.0, **c.kw())
+    assert (w[:c.offs[3]] == 5).all() and abs(float(w[c.offs[3]:c.offs[3] + 104].sum()) - 64) < 0.1
+
+
 @pytest.mark.parametrize("stride", [584, 640, 1152])
 def test_row_strides(stride):
     c = Case(10, [200, 77], 5, 16, stride=stride)

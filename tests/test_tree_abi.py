@@ -73,6 +73,7 @@ def rope_args(**kw):
     (dict(q_rope_head=66), mla.EALIGN), (dict(q_out_token=9220), mla.EALIGN), (dict(c_token=577), mla.EALIGN),
     (dict(k_rope_batch=4), mla.EALIGN), (dict(d_pos=PTR + 2), mla.EALIGN), (dict(turns=PTR + 4), mla.EALIGN),
     (dict(heads=0, kv=None, c=None, k_rope=None), mla.EINVAL), (dict(row_weights=PTR + 1), mla.EALIGN),
+    (dict(tokens=(1 << 28) + 1), mla.EINVAL),
 ])
 def test_rope_refusals(kw, status):
     assert refused("mla_rope_append", ctypes.byref(rope_args(**kw)), None) == status
@@ -92,7 +93,7 @@ def tree_plan(**kw):
     (dict(batch=0), mla.EINVAL), (dict(batch=4097), mla.EINVAL), (dict(tokens=0), mla.EINVAL),
     (dict(tokens=65), mla.EINVAL), (dict(heads=0), mla.EUNSUPPORTED), (dict(heads=129), mla.EUNSUPPORTED),
     (dict(scale=0.0), mla.EINVAL), (dict(scale=math.inf), mla.EINVAL), (dict(scale=math.nan), mla.EINVAL),
-    (dict(num_sms=-1), mla.EINVAL),
+    (dict(num_sms=-1), mla.EINVAL), (dict(scale=3e38), mla.EINVAL),
 ])
 def test_tree_plan_refusals(kw, status):
     with pytest.raises(mla.MLADecodeError) as e:
