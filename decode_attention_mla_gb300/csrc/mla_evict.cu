@@ -11,12 +11,15 @@
 // Rows above K stay, and of the rows equal to K the first so many that `keep`
 // is met; every thread counts over a contiguous run of rows, and prefix sums over
 // threads, warps and CTAs number the evicted rows below `keep` and the kept rows
-// behind it in ascending order, which pairs them up.  Integers only: no order of execution shows in the result.
+// behind it in ascending order, which pairs them up.  Integers only: no order of
+// execution shows in the result.  Bound: latency (barriers and passes over shared
+// memory); 35 us for 16 requests of up to 131072 rows, 9 for one of 8192.
 //
 // Move.  A warp copies four bf16 rows (eight E4M3 rows) at a time, nine
 // 16-byte loads in flight per lane; source rows lie at or behind `keep` and
 // destinations below it, so the copy is safe in place.  Bound: the bytes of the
-// moved rows, read and written once.
+// moved rows, read and written once, in rows of 1152 bytes from anywhere: 116 us
+// for 16 requests (0.58 GB in and out, 5 TB/s).
 #include <atomic>
 #include <cooperative_groups.h>
 #include <cstdint>

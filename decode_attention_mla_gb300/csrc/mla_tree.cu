@@ -25,8 +25,8 @@ int check_shape(const mla_tree_shape* s) {
     return MLA_OK;
 }
 
-// Scratch: status word, the pairs' merge notes, their pieces (two each) and
-// the pieces' log-sum-exps, each region 256-byte aligned.
+// Scratch: status word, the pairs' merge notes, their pieces and the pieces'
+// log-sum-exps, each region 256-byte aligned.
 constexpr size_t kMergeOffset = 256;
 // Pairs of SMs to use.
 int tree_pairs(int num_sms) { return num_sms < 2 ? 1 : num_sms / 2; }
@@ -34,9 +34,9 @@ void layout(mla_tree_plan_t* pl) {
     const size_t pairs = static_cast<size_t>(tree_pairs(pl->num_sms));
     pl->grid = static_cast<int>(2 * pairs);
     pl->status_offset = 0;
-    pl->part_offset = up256(kMergeOffset + pairs * sizeof(TreeMerge));
-    pl->lse_part_offset = pl->part_offset + pairs * 2 * kTreeBlockRows * kDLatent * sizeof(float);
-    pl->scratch_bytes = up256(pl->lse_part_offset + pairs * 2 * kTreeBlockRows * sizeof(float));
+    pl->part_offset = up256(kMergeOffset + pairs * kTreePieces * (sizeof(TreeMerge) + sizeof(TreeCut)));
+    pl->lse_part_offset = pl->part_offset + pairs * kTreePieces * kTreeBlockRows * kDLatent * sizeof(float);
+    pl->scratch_bytes = up256(pl->lse_part_offset + pairs * kTreePieces * kTreeBlockRows * sizeof(float));
 }
 
 int check_plan(const mla_tree_plan_t* pl) {
@@ -99,6 +99,7 @@ TreeParams params(const mla_tree_plan_t* pl, const mla_tree_args* a, void* scrat
     p.clusters = pl->grid / 2;
     p.scale_log2 = pl->shape.scale * kLog2e;
     p.merge = reinterpret_cast<TreeMerge*>(base + kMergeOffset);
+    p.cut = reinterpret_cast<TreeCut*>(p.merge + kTreePieces * p.clusters);
     p.part = reinterpret_cast<float*>(base + pl->part_offset);
     p.lse_part = reinterpret_cast<float*>(base + pl->lse_part_offset);
     p.status = reinterpret_cast<int*>(base + pl->status_offset);

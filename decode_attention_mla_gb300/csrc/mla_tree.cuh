@@ -14,12 +14,22 @@ namespace mla {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTreeTileKeys = 128;                         // cache rows per tile of a CTA pair
 constexpr int kTreeBlockRows = 128;                        // (token, head) rows per CTA pair
+constexpr int kTreeCutTiles = 96;                          // tiles per run from which row blocks are cut
 constexpr long long kTreeMaxRow = 0x7fffff00;              // rows of a request from here on are not attended
 
-// What a cluster leaves for the merge: its last piece is the first one of a row
-// block that `pieces` consecutive clusters share (0: nothing to merge).
-struct TreeMerge {
-    int b, rb, pieces, rows;
+// Pieces that a cluster's run can leave: the run's first item, its last one, and at
+// most one between them (see TreeSegments).
+constexpr int kTreePieces = 3;
+// Note of a piece that opens a row block shared by several runs.
+struct __align__(16) TreeMerge {
+    int b, rb;
+    int rows;                                              // of the row block; the piece's place in its run << 16
+    int pieces;                                            // the piece and the first ones of the runs behind it
+                                                           // (0: no note, -1: in segments, see TreeCut)
+};
+struct __align__(16) TreeCut {
+    int n_rb, n_tiles, per;                                // as in the cursor
+    int begin;                                             // the request's first unit, relative to the run's
 };
 
 struct TreeParams {
@@ -27,9 +37,10 @@ struct TreeParams {
     int batch, tokens, heads;
     int clusters;
     float scale_log2;                                      // scale * log2(e): scores in base-2 units
-    float* part;                                           // fp32 [clusters][2][128][512], normalised
-    float* lse_part;                                       // fp32 [clusters][2][128], base 2
-    TreeMerge* merge;                                      // [clusters]
+    float* part;                                           // fp32 [clusters][3][128 x 512], normalised, by feature quads
+    float* lse_part;                                       // fp32 [clusters][3][128], base 2
+    TreeMerge* merge;                                      // [3][clusters] (without segments the first row alone)
+    TreeCut* cut;                                          // [3][clusters]
     int* status;
     int stall_test;
     float* weights;
@@ -81,12 +92,54 @@ __device__ __forceinline__ unsigned long long visible64(const TreeRequest& r, un
 
 
 // ---- runs of tiles -------------------------------------------------------------
-// The units (request, row block, tile of cache rows), in this order, are cut into
+// A request's work is a list of jobs, in units of a tile: its row blocks (over all
+// of its cache), one after the other.  All requests' units, in order, are cut into
 // equal runs, one per pair of CTAs, from the lengths on the device.
+//
+// The row blocks of a request read the same cache rows, at about the same time
+// if run lengths and cache lengths happen to fit; otherwise, with more cache than L2
+// holds, each reads them from DRAM again (16 requests of 5 row blocks: 1.35 GB for
+// 0.38 GB of rows).  Hence
+//   - tiles go by the clock: a job done whole by one run starts at the tile that it
+//     would have reached if it had begun with the run, and goes round; of a job cut
+//     between two runs, the first takes the far tiles, so that the second begins
+//     at the near ones with the others.  At any time the pairs of a request then
+//     are at one of two places;
+//   - row blocks longer than a run are cut into segments of a run's length, and the
+//     jobs are (segment, row block).  The last one or two segments are 0.5 to 1.25
+//     runs long, so that a run has at most one whole job between its first and its
+//     last item, and a job is in three runs at most.
+// Measured (5 tokens x 128 heads): 16 requests of 4096 .. 32768 rows 285 -> 262 us,
+// by the clock alone; one of 300000 rows 330 -> 316 by the clock, 279 with
+// segments.  Segments leave more pieces to merge: with runs of 14 tiles (8 requests
+// of 16384 rows, 16 x 16) 48 us where uncut row blocks take 43, with 120 tiles 203
+// and 205 us, so they are made from kTreeCutTiles per run on.
+struct TreeSegments {
+    int full, len, a, b;                                   // `full` segments of len tiles, one of a, one of b (0: none)
+
+    __device__ __forceinline__ void set(int n_tiles, int n_rb, int seg_tiles) {
+        full = 0;
+        len = seg_tiles;
+        a = n_tiles;
+        b = 0;
+        if (n_rb > 1 && n_tiles > seg_tiles) {
+            full = n_tiles / seg_tiles - 1;
+            const int rest = n_tiles - full * seg_tiles;   // one length or more, below two
+            a = rest - seg_tiles <= seg_tiles / 4 ? rest : (rest + 1) / 2;
+            b = rest - a;
+        }
+    }
+    __device__ __forceinline__ int count() const { return full + (b > 0 ? 2 : 1); }
+    __device__ __forceinline__ int start(int seg) const { return seg <= full ? seg * len : full * len + a; }
+    __device__ __forceinline__ int tiles(int seg) const { return seg < full ? len : seg == full ? a : b; }
+};
+
 struct TreeWork {                                          // a cluster's run
     long long count, per;                                  // units of the run, and of every cluster's
-    TreeRequest r;                                         // its first unit
-    int b, rb, tile;
+    TreeRequest r;                                         // of its first unit
+    int b, seg, rb, at;                                    // the first unit's job, and its place in it
+    int begin;                                             // the request's first unit, relative to the run's
+    int seg_tiles;                                         // tiles per segment
 };
 
 // Quotient of non-negative numbers; 64-bit division is a slow call.
@@ -95,15 +148,19 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
     return a / b;
 }
 
-// Walks the tiles of a run.  kByBlocks: one unit per row block and tile of a
-// request; otherwise one per tile.
+// Walks the tiles of a run.  kByBlocks: a request's jobs are its row blocks;
+// otherwise it has one job, its tiles.  An item is what one run does of a job.
 template <int kKeys, bool kByBlocks>
 struct TreeCursor {
     TreeRequest r;
-    int b, rb, n_rb, tile, n_tiles;
-    int left;                                              // tiles of the run from here on, this one included
+    TreeSegments sg;
+    int b, seg, rb, n_rb, n_tiles, seg_tiles;
+    int begin;                                             // place of the request's first unit in the run (may be < 0)
+    int tile, lo, hi;                                      // the item's tiles, and the one at hand
+    int item_left;                                         // tiles of the item from here on, this one included
+    int left;                                              // ... of the run
     int g;                                                 // tiles of the run before this one
-    int item;                                              // row blocks (or parts) before this one
+    int item;                                              // items before this one
     bool first;                                            // first tile of its item
 
     static __device__ __forceinline__ int blocks_of(const TreeParams& p, const TreeRequest& r) {
@@ -112,45 +169,68 @@ struct TreeCursor {
     static __device__ __forceinline__ int tiles_of(const TreeRequest& r) { return (r.hi + kKeys - 1) / kKeys; }
 
     __device__ __forceinline__ void request(const TreeParams& p) {
-        r = load_tree_request(p, b);
         n_rb = blocks_of(p, r);
         n_tiles = tiles_of(r);
+        if constexpr (kByBlocks)
+            sg.set(n_tiles, n_rb, seg_tiles);
+        else
+            sg = TreeSegments{0, 0, n_tiles, 0};
+    }
+    // the item that begins with unit `at` of the job
+    __device__ __forceinline__ void enter(int at) {
+        const int len = sg.tiles(seg);
+        item_left = min(len - at, left);
+        hi = sg.start(seg) + len - at;                     // (of a cut job the first run takes the far tiles)
+        lo = hi - item_left;
+        tile = kByBlocks && g > 0 && item_left == len ? lo + g % len : lo;
     }
     __device__ __forceinline__ void start(const TreeParams& p, const TreeWork& w) {
         b = w.b;
+        seg = w.seg;
         rb = w.rb;
-        tile = w.tile;
+        seg_tiles = w.seg_tiles;
+        begin = w.begin;
         left = static_cast<int>(w.count);
         g = item = 0;
         first = true;
         r = w.r;
-        n_rb = blocks_of(p, r);
-        n_tiles = tiles_of(r);
+        request(p);
+        enter(w.at);
     }
-    __device__ __forceinline__ bool last() const { return left == 1 || tile == n_tiles - 1; }
+    __device__ __forceinline__ bool last() const { return item_left == 1; }
+    // the item has its job's first unit; is all of the request's tiles
+    __device__ __forceinline__ bool opens() const { return hi == sg.start(seg) + sg.tiles(seg); }
+    __device__ __forceinline__ bool whole() const { return hi - lo == n_tiles; }
     __device__ __forceinline__ void next(const TreeParams& p) {
-        first = last();
-        if (first) ++item;
         ++g;
         --left;
-        if (++tile < n_tiles) return;
-        tile = 0;
+        first = --item_left == 0;
+        if (!first) {
+            if (++tile == hi) tile = lo;
+            return;
+        }
+        ++item;
         if (left > 0) next_item(p);
     }
-    // to the next item's first tile (b, rb, n_tiles alone; there is one)
+    // to the next item's first tile, the g-th of the run (there is one)
     __device__ __forceinline__ void next_item(const TreeParams& p) {
-        if (++rb < n_rb) return;
-        rb = 0;
-        do {
-            ++b;
-            request(p);
-        } while (n_rb == 0 || n_tiles == 0);
+        if (++rb == n_rb) {
+            rb = 0;
+            if (++seg == sg.count()) {
+                seg = 0;
+                do {
+                    r = load_tree_request(p, ++b);
+                    request(p);
+                } while (n_rb == 0 || n_tiles == 0);
+                begin = g;
+            }
+        }
+        enter(0);
     }
     // the tile holds drafted rows or rows behind them
     __device__ __forceinline__ bool special() const { return (tile + 1) * kKeys > r.d_pos; }
 
-    // One warp: this cluster's run.  All units in order of (request, row block,
-    // tile); run length = ceil(units / clusters).
+    // One warp: this cluster's run; run length = ceil(units / clusters).
     static __device__ void find_work(const TreeParams& p, int cluster, int lane, TreeWork* out) {
         auto request_of = [&](int b) {
             TreeRequest r{};
@@ -171,9 +251,11 @@ struct TreeCursor {
         if (per < 1) per = 1;
         const long long u0 = per * cluster;
         const long long count = u0 >= total ? 0 : (total - u0 < per ? total - u0 : per);
+        const int seg_tiles = static_cast<int>(kByBlocks && per >= kTreeCutTiles ? min(per, kTreeMaxRow) : kTreeMaxRow);
         if (lane == 0) {
             out->per = per;
             out->count = count;
+            out->seg_tiles = seg_tiles;
         }
         long long before = 0;
         for (int b0 = 0; b0 < p.batch && count > 0; b0 += 32) {
@@ -190,9 +272,24 @@ struct TreeCursor {
             const long long first = before + incl - u;         // this lane's request is units [first, first + u)
             const bool here = u0 >= first && u0 < first + u;
             if (here) {
-                const int n_tiles = tiles_of(r);
-                out->rb = static_cast<int>(quotient(u0 - first, n_tiles));
-                out->tile = static_cast<int>(u0 - first - static_cast<long long>(out->rb) * n_tiles);
+                const int n_tiles = tiles_of(r), n_rb = blocks_of(p, r);
+                TreeSegments sg;
+                sg.set(n_tiles, n_rb, seg_tiles);
+                long long at = u0 - first;                     // in the request, then in the segment
+                int seg = 0;
+                if (sg.full > 0) {
+                    const long long each = static_cast<long long>(n_rb) * seg_tiles;
+                    seg = static_cast<int>(min(quotient(at, each), static_cast<long long>(sg.full)));
+                    at -= seg * each;
+                }
+                if (seg == sg.full && sg.b > 0 && at >= static_cast<long long>(n_rb) * sg.a) {
+                    at -= static_cast<long long>(n_rb) * sg.a;
+                    ++seg;
+                }
+                out->rb = static_cast<int>(quotient(at, sg.tiles(seg)));
+                out->at = static_cast<int>(at - static_cast<long long>(out->rb) * sg.tiles(seg));
+                out->seg = seg;
+                out->begin = static_cast<int>(first - u0);
                 out->b = b0 + lane;
                 out->r = r;
             }

@@ -17,21 +17,31 @@
 // In tensor memory a row's 128 scores lie in two lanes (row, row + 64), 64 keys
 // each; O likewise, so two threads own a row and share only its reference m.
 //
-// Work split.  The units (request, row block, tile), in this order, are cut
-// into equal runs, one per pair, from the lengths on the device: no pair idles
-// however ragged the batch.  A run that holds a whole row block writes the
+// Work split.  The units (request, row block, tile) are cut into equal runs, one
+// per pair, from the lengths on the device: no pair idles however ragged the batch.
+// Tiles of a run go in an order that keeps the pairs of a request at the same cache
+// rows at the same time (TreeCursor).  A run that holds a whole row block writes the
 // result; otherwise it leaves a normalised fp32 piece and its log-sum-exp, and
-// a second kernel merges the pieces of a block in ascending order.
+// a second kernel merges the pieces of a block in a fixed order.
 //
-// Staging.  Ring of eight 16 KB slots (64 keys x 128 columns) filled by TMA in
-// the order the MMAs take them: four slots with this CTA's 64 keys for QK, four
-// with its 256 features of all 128 keys for PV (keys of the other CTA's half are
-// L2 hits).  QK of tile g + 1 is issued before PV of tile g, so the softmax of a
-// tile runs under the next tile's QK.
+// Staging, all by TMA: the queries of the row block (72 KB per CTA); K of a tile
+// whole (this CTA's 64 keys: four slots of 128 columns, the rope columns beside the
+// last), V of a tile whole (this CTA's 256 features of all 128 keys: two halves of
+// two slots; the keys of the other CTA's half are L2 hits); P 16 KB.  QK of tile g
+// goes before PV of tile g - 1, so the softmax of a tile runs under the next
+// tile's QK and the PV before it; at a block's end PV goes first, since the next
+// block's QK waits for its queries.
+//
+// Bound: the tensor cores (an M128 N128 K16 MMA of a pair takes 32 cycles, N256 64;
+// a tile 2200), fed at 140 KB per tile and CTA.  Measured: 64 drafts x 128 heads over
+// 65536 rows 635 us, 1840 TFLOP/s or 0.95 of cuBLAS's burst rate, while the clock
+// holds; 16 ragged requests of 5 x 128 262 us, 1460 TFLOP/s (DRAM re-reads
+// of row blocks that drift apart); 16 x 16 over 131072 rows 61 us; 8 x 16 over 248
+// rows 11.5 us, of which the two kernels' launches, set-up and merge are 10.
 //
 // Warps of a CTA: 0-7 softmax and epilogue, 8 TMA of Q and K, 9 MMA issue (even
-// CTA only) and tensor memory, 10 TMA of V, 11 relay of P's readiness.  Barriers that
-// the MMA thread waits on live in the even CTA and take arrivals of both.
+// CTA; the odd one's writes empty requests) and tensor memory, 10 TMA of V.
+// Barriers that the MMA warp waits on live in the even CTA and take arrivals of both.
 //
 // Rounding: P is rounded to bf16 for the product (relative 2^-8 at most per
 // probability, sums use the unrounded values), O and the statistics are fp32.
@@ -181,8 +191,8 @@ __device__ void produce(const TreeMaps& maps, const TreeParams& p, Shared& sh, u
 // the tiles and waits, one lane issues (with a single thread doing all of it an
 // MMA took 100 cycles to issue, instead of the 32 or 64 that it runs); each
 // barrier is looked at once before the MMAs that precede its use, so a phase
-// that is over by then costs nothing; PV is two tiles behind QK, so its phases
-// are; and all that crosses CTAs goes through the relay warp.
+// that is over by then costs nothing; and PV is a tile behind QK, so its
+// probabilities have had a tile's time.
 struct Issue {
     Shared& sh;
     bool lead, ok;
@@ -206,7 +216,7 @@ __device__ void issue(const TreeParams& p, Shared& sh, uint32_t tmem) {
     Cursor c;                                              // moves from item to item here
     c.start(p, sh.work);
     const int total = c.left;
-    int in_item = min(c.n_tiles - c.tile, total);          // tiles of the item still to come
+    int in_item = c.item_left;                             // tiles of the item still to come
     bool first = true;
     uint32_t pv_first = 0;                                 // the tile before this QK's was the first of its item
     // what an early look has shown of the next QK's first barrier and the next PV's
@@ -280,9 +290,11 @@ __device__ void issue(const TreeParams& p, Shared& sh, uint32_t tmem) {
                 see_k = false;
                 first = last;
                 if (--in_item == 0 && g + 1 < total) {
+                    c.g = g + 1;
+                    c.left = total - c.g;
                     c.next_item(p);
                     ++item;
-                    in_item = min(c.n_tiles, total - (g + 1));
+                    in_item = c.item_left;
                 }
             }
         }
@@ -325,7 +337,7 @@ __device__ void clean_v(Shared& sh, const Cursor& c, int tid) {
     }
 }
 
-// Place of a piece's feature quad: [piece][32-row group][quad][row], so that the
+// Place of a piece's feature quad: [slot][32-row group][quad][row], so that the
 // epilogue's and the merge's warps (a row per lane) touch 512 consecutive bytes.
 // (Rows of 2 KB, staged through shared memory, took 6300 cycles per row block.)
 __device__ __forceinline__ long long piece_quad(int slot, int row, int quad) {
@@ -364,9 +376,11 @@ __device__ void softmax(const TreeParams& p, Shared& sh, uint32_t tmem, uint32_t
     const uint32_t p_bar = map_to_rank(&sh.p_ready, 0), o_bar = map_to_rank(&sh.o_free, 0);
     const uint32_t p_line = smem_u32(sh.p[half]) + row * 128;
     const float c2 = p.scale_log2;
-    TreeMerge merge{0, 0, 0, 0};
     uint32_t specials = 0;
     bool ok = true, bad = false;
+    const bool notes = rank == 0 && tid == 0;
+    if (notes)
+        for (int i = 0; i < kTreePieces; ++i) p.merge[i * p.clusters + cluster].pieces = 0;
     Cursor c;
     c.start(p, sh.work);
     while (c.left > 0 && ok) {
@@ -374,9 +388,11 @@ __device__ void softmax(const TreeParams& p, Shared& sh, uint32_t tmem, uint32_t
         const int r = c.rb * kTreeBlockRows + static_cast<int>(rank) * 64 + row;
         const int live_rows = c.r.n_tok * p.heads;
         const unsigned long long mask = r < live_rows ? tree_mask(p, c.b, r / p.heads, c.r.n_tok) : 0ull;
-        const int b = c.b, rb = c.rb, tile0 = c.tile, n_tiles = c.n_tiles;
+        const int b = c.b, rb = c.rb;
+        const bool whole = c.whole(), run_first = c.g == 0;
+        const bool opens = !whole && c.seg == 0 && c.opens(), cut = c.sg.count() > 1;
+        const TreeCut of{c.n_rb, c.n_tiles, static_cast<int>(sh.work.per), c.begin};
         float m_ref = -INFINITY, l = 0.f;
-        int done = 0;
         bool last;
         do {
             const int g = c.g, buf = g & 1;
@@ -459,7 +475,6 @@ __device__ void softmax(const TreeParams& p, Shared& sh, uint32_t tmem, uint32_t
             __syncwarp();
             bad |= !w;                                     // the threads leave together at the next barrier
             if (lane == 0 && !bad) mbar_arrive_peer(p_bar);
-            ++done;
             c.next(p);
         } while (!last);
         if (!ok) break;
@@ -473,19 +488,21 @@ __device__ void softmax(const TreeParams& p, Shared& sh, uint32_t tmem, uint32_t
         const float lt = (sh.red_sum[0][row] + sh.red_sum[1][row]) + (sh.red_sum[2][row] + sh.red_sum[3][row]);
         const float inv = lt == 0.f ? 0.f : 1.f / lt;
         const float lse2 = lt == 0.f ? -INFINITY : m_ref + log2f(lt);
-        const bool whole = tile0 == 0 && done == n_tiles;
-        const int slot = 2 * cluster + (tile0 == 0 ? 1 : 0);
+        // place of the piece: the run's first item, one that ends with the run's length, another
+        const int place = run_first ? 0 : c.g == sh.work.per ? 2 : 1, slot = kTreePieces * cluster + place;
         if (quarter == 0 && r < live_rows) {
             if (whole)
                 p.a.lse[static_cast<long long>(b) * p.tokens * p.heads + r] = lse2 * kLn2;
             else
                 p.lse_part[slot * kTreeBlockRows + static_cast<int>(rank) * 64 + row] = lse2;
         }
-        if (!whole && tile0 == 0) {
-            merge.b = b;
-            merge.rb = rb;
-            merge.rows = min(kTreeBlockRows, live_rows - rb * kTreeBlockRows);
-            merge.pieces = 1 + static_cast<int>((n_tiles - done + sh.work.per - 1) / sh.work.per);
+        if (notes && opens) {
+            const int rows = min(kTreeBlockRows, live_rows - rb * kTreeBlockRows);
+            // (an uncut job's pieces lie in the runs from this one to that of its last unit)
+            const int pieces = cut ? -1 : (of.begin + (rb + 1) * of.n_tiles - 1) / of.per + 1;
+            const int at = (cut ? place : 0) * p.clusters + cluster;
+            p.merge[at] = TreeMerge{b, rb, rows | place << 16, pieces};
+            if (cut) p.cut[at] = of;
         }
         const bool w = warp_wait(&sh.abort_flag, &sh.o_done, (c.g - 1) & 1);
         if (named_barrier_or(kBarSoftmax, kSoftmaxThreads, !w)) {
@@ -537,7 +554,6 @@ __device__ void softmax(const TreeParams& p, Shared& sh, uint32_t tmem, uint32_t
         if (lane == 0 && c.left > 0) mbar_arrive_peer(o_bar);
     }
     if (!ok && lane == 0) raise_tree_error(&sh.abort_flag, p.status);
-    if (rank == 0 && tid == 0) p.merge[cluster] = merge;
 }
 
 // Requests without rows: their tokens' outputs, by the odd CTAs' otherwise idle warp.
@@ -630,9 +646,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // ============================== merge ======================================
-// Out of the clusters' notes, block x takes the x-th row block that clusters
-// share.  A warp: 32 rows (one per lane) and QUADS feature quads; the pieces in
-// ascending order, a batch of loads in flight at a time, with a running maximum of
+// Out of the clusters' notes, block x takes the x-th row block that several runs
+// share.  A warp: 32 rows (one per lane) and QUADS feature quads; the pieces in a
+// fixed order, a batch of loads in flight at a time, with a running maximum of
 // their log-sum-exps.  With few pieces a warp takes four quads (a lane's output is
 // a whole sector); with many, one quad, and four warps share the pieces and join
 // their sums in order (the pieces come from L2: 76 of them in one warp's hands
@@ -640,31 +656,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 constexpr int kMergeWarps = 8;
 constexpr int kFewPieces = 8;                              // up to about so many per block: four quads per warp
 
+constexpr int kMergeList = 256;
+
+// Candidates for the pieces of row block rb in segments: part c mod 3 of segment c / 3.
+__device__ __forceinline__ int cut_candidates(const TreeCut& m) {
+    TreeSegments sg;
+    sg.set(m.n_tiles, m.n_rb, m.per);
+    return 3 * sg.count();
+}
+// One warp: the slots of the pieces among candidates c0 .. c0 + kMergeList - 1.
+__device__ __noinline__ int list_cut_pieces(const TreeCut& m, int rb, int cluster, int c0, int lane, int* list) {
+    TreeSegments sg;
+    sg.set(m.n_tiles, m.n_rb, m.per);
+    const int all = min(3 * sg.count(), c0 + kMergeList);
+    int n = 0;
+    for (int c = c0; c < all; c += 32) {
+        const int at = c + lane, seg = at / 3, part = at - 3 * seg;
+        // units of the job, relative to the first of the run that opens the row block
+        const int s0 = m.begin + m.n_rb * sg.start(seg) + rb * sg.tiles(seg), s1 = s0 + sg.tiles(seg);
+        const int run = s0 / m.per, run_end = (run + 1) * m.per;
+        const bool is = at < all && s1 > run_end + (part - 1) * m.per;
+        const uint32_t bal = __ballot_sync(0xffffffffu, is);
+        if (is)
+            list[n + __popc(bal & ((1u << lane) - 1u))] =
+                kTreePieces * (cluster + run + part) + (part > 0 || s0 == run * m.per ? 0 : s1 >= run_end ? 2 : 1);
+        n += __popc(bal);
+    }
+    return n;
+}
+
 template <int QUADS, int PARTS>
 __global__ void __launch_bounds__(32 * kMergeWarps) mla_tree_merge_kernel(const __grid_constant__ TreeParams p) {
     constexpr int kBatch = QUADS == 1 ? 10 : 4;
     __shared__ TreeMerge note;
     __shared__ int owner;
+    __shared__ int list[kMergeList];                       // slots of pieces in segments, in order
+    __shared__ int listed;
     __shared__ float joined[PARTS > 1 ? kMergeWarps : 1][6][32];   // maximum, sum, four features
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     grid_dependency_wait();
     allow_dependent_launch();
     if (warp == 0) {
+        const int notes = kTreePieces * p.clusters;
         int seen = 0;
         bool found = false;
-        for (int c = 0; c < p.clusters && !found; c += 128) {
+        for (int c = 0; c < notes && !found; c += 128) {
             TreeMerge n[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int at = c + 32 * i + lane;
-                n[i] = p.merge[min(at, p.clusters - 1)];
-                if (at >= p.clusters) n[i].pieces = 0;
+                n[i] = p.merge[min(at, notes - 1)];
+                if (at >= notes) n[i].pieces = 0;
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint32_t bal = __ballot_sync(0xffffffffu, n[i].pieces > 0);
+                const uint32_t bal = __ballot_sync(0xffffffffu, n[i].pieces != 0);
                 const int rank = seen + __popc(bal & ((1u << lane) - 1u));
-                if (n[i].pieces > 0 && rank == static_cast<int>(blockIdx.x)) {
+                if (n[i].pieces != 0 && rank == static_cast<int>(blockIdx.x)) {
                     note = n[i];
                     owner = c + 32 * i + lane;
                 }
@@ -675,64 +723,84 @@ __global__ void __launch_bounds__(32 * kMergeWarps) mla_tree_merge_kernel(const 
         if (!found && lane == 0) owner = -1;
     }
     __syncthreads();
-    const int c0 = owner;
-    if (c0 < 0) return;
+    if (owner < 0) return;
     const TreeMerge m = note;
+    const int rows = m.rows & 0xffff;
+    const bool cut = m.pieces < 0;
+    int cluster = owner;                                   // whose run opens the row block
+    while (cluster >= p.clusters) cluster -= p.clusters;
+    // slot of a piece; pieces in segments are listed, kMergeList candidates at a time
+    auto slot = [&](int i) {
+        return cut ? list[i] : kTreePieces * (cluster + i) + (i == 0 ? m.rows >> 16 : 0);
+    };
+    auto list_pieces = [&](int c0) {
+        if (warp == 0) {
+            const int n = list_cut_pieces(p.cut[owner], m.rb, cluster, c0, lane, list);
+            if (lane == 0) listed = n;
+        }
+        __syncthreads();
+    };
+    const int candidates = cut ? cut_candidates(p.cut[owner]) : 0;
+    if (cut) list_pieces(0);
     constexpr int kQuadWarps = kMergeWarps / PARTS;        // warps of a block with quads of their own
     constexpr int kTasks = kDLatent / 4 / QUADS / kQuadWarps;   // blocks per 32 rows
     const int group = static_cast<int>(blockIdx.y) / kTasks;
     const int part_of = warp / kQuadWarps;                 // share of the pieces
     const int quad = ((static_cast<int>(blockIdx.y) % kTasks) * kQuadWarps + warp % kQuadWarps) * QUADS;
     const int row = 32 * group + lane;
-    const bool live = row < m.rows;
-    if (32 * group >= m.rows) return;                      // uniform over the block
-    // piece 0 is the owner's second slot, the others are the first slots of the clusters behind it
-    auto slot = [&](int i) { return 2 * (c0 + i) + (i == 0 ? 1 : 0); };
+    const bool live = row < rows;
+    if (32 * group >= rows) return;                      // uniform over the block
     const float4* part = reinterpret_cast<const float4*>(p.part);
     float4 acc[QUADS];
 #pragma unroll
     for (int k = 0; k < QUADS; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     float sum = 0.f, top = -INFINITY, base = 0.f;
-    const int share = (m.pieces + PARTS - 1) / PARTS;
-    const int end = min(m.pieces, (part_of + 1) * share);
-    for (int i0 = part_of * share; i0 < end; i0 += kBatch) {
-        float l[kBatch];
-        float4 v[kBatch][QUADS];
+    for (int c0 = 0;; c0 += kMergeList) {
+        const int n = cut ? listed : m.pieces;
+        const int share = (n + PARTS - 1) / PARTS;
+        const int end = min(n, (part_of + 1) * share);
+        for (int i0 = part_of * share; i0 < end; i0 += kBatch) {
+            float l[kBatch];
+            float4 v[kBatch][QUADS];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int at = slot(min(i0 + i, end - 1));     // (no branch: all loads at once)
-            l[i] = live ? p.lse_part[at * kTreeBlockRows + row] : -INFINITY;
-            const float4* src = part + piece_quad(at, row, quad);
+            for (int i = 0; i < kBatch; ++i) {
+                const int at = slot(min(i0 + i, end - 1));     // (no branch: all loads at once)
+                l[i] = live ? p.lse_part[at * kTreeBlockRows + row] : -INFINITY;
+                const float4* src = part + piece_quad(at, row, quad);
 #pragma unroll
-            for (int k = 0; k < QUADS; ++k) v[i][k] = src[32 * k];
-        }
-        const float before = top;
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) top = fmaxf(top, l[i]);   // (the repeated last piece changes nothing)
-        if (top > before) {
-            const float scale = before > -INFINITY ? exp2f(before - top) : 0.f;
-            base = top;
-            // (a NaN stays: a product with 0 only drops sums of nothing)
-            if (before > -INFINITY || sum != 0.f) {
-                sum *= scale;
-#pragma unroll
-                for (int k = 0; k < QUADS; ++k)
-                    acc[k] = make_float4(acc[k].x * scale, acc[k].y * scale, acc[k].z * scale, acc[k].w * scale);
+                for (int k = 0; k < QUADS; ++k) v[i][k] = src[32 * k];
             }
-        }
+            const float before = top;
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-            if (i0 + i < end) {
-                const float w = exp2f(l[i] - base);        // NaN stays NaN
-                sum += w;
+            for (int i = 0; i < kBatch; ++i) top = fmaxf(top, l[i]);   // (the repeated last piece changes nothing)
+            if (top > before) {
+                const float scale = before > -INFINITY ? exp2f(before - top) : 0.f;
+                base = top;
+                // (a NaN stays: a product with 0 only drops sums of nothing)
+                if (before > -INFINITY || sum != 0.f) {
+                    sum *= scale;
 #pragma unroll
-                for (int k = 0; k < QUADS; ++k) {
-                    acc[k].x = fmaf(w, v[i][k].x, acc[k].x);
-                    acc[k].y = fmaf(w, v[i][k].y, acc[k].y);
-                    acc[k].z = fmaf(w, v[i][k].z, acc[k].z);
-                    acc[k].w = fmaf(w, v[i][k].w, acc[k].w);
+                    for (int k = 0; k < QUADS; ++k)
+                        acc[k] = make_float4(acc[k].x * scale, acc[k].y * scale, acc[k].z * scale, acc[k].w * scale);
                 }
             }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                if (i0 + i < end) {
+                    const float w = exp2f(l[i] - base);        // NaN stays NaN
+                    sum += w;
+#pragma unroll
+                    for (int k = 0; k < QUADS; ++k) {
+                        acc[k].x = fmaf(w, v[i][k].x, acc[k].x);
+                        acc[k].y = fmaf(w, v[i][k].y, acc[k].y);
+                        acc[k].z = fmaf(w, v[i][k].z, acc[k].z);
+                        acc[k].w = fmaf(w, v[i][k].w, acc[k].w);
+                    }
+                }
+        }
+        if (c0 + kMergeList >= candidates) break;          // (uniform)
+        __syncthreads();
+        list_pieces(c0 + kMergeList);
     }
     if constexpr (PARTS > 1) {
         static_assert(QUADS == 1, "one quad per warp where warps share pieces");
@@ -800,10 +868,12 @@ cudaError_t launch_tree_attend(const TreeMaps& maps, const TreeParams& p, bool p
     cfg.numAttrs = pdl ? 1 : 0;
     cudaError_t e = cudaLaunchKernelEx(&cfg, mla_tree_attend_kernel, maps, p);
     if (e != cudaSuccess) return e;
-    // at most one shared row block per cluster, and no more than there are
-    const long long blocks =
-        static_cast<long long>(p.batch) * ((p.tokens * p.heads + kTreeBlockRows - 1) / kTreeBlockRows);
-    const unsigned items = static_cast<unsigned>(std::min<long long>(p.clusters, blocks));
+    // shared row blocks: no more than there are row blocks or notes, and without
+    // segments (one block per request) at most one per run
+    const int per_request = (p.tokens * p.heads + kTreeBlockRows - 1) / kTreeBlockRows;
+    const long long blocks = static_cast<long long>(p.batch) * per_request;
+    const unsigned items =
+        static_cast<unsigned>(std::min<long long>((per_request > 1 ? kTreePieces : 1) * p.clusters, blocks));
     const int groups = (std::min(p.tokens * p.heads, kTreeBlockRows) + 31) / 32;
     cfg.blockDim = dim3(32 * kMergeWarps);
     cfg.dynamicSmemBytes = 0;

@@ -112,6 +112,60 @@ def test_trees_against_the_64_bit_form(lens, Q, H, dtype):
     c.check(*c.run(dtype))
 
 
+# Runs of 96 tiles and more, on few pairs: a request's row blocks are cut along the
+# cache, and their pieces lie in several runs.
+@pytest.mark.parametrize("num_sms", [0, 2, 10, 20, 24])
+@pytest.mark.parametrize("lens,Q,H", [
+    ([50000], 2, 65), ([24000, 0, 9000, 130, 20000], 3, 100), ([13000] * 4, 5, 64), ([49100, 30], 64, 6),
+])
+def test_long_caches_of_several_row_blocks(lens, Q, H, num_sms):
+    c = Case(13 + Q, lens, Q, H, gain=0.5)
+    out, lse = c.run(num_sms=num_sms)
+    c.check(out, lse, long_reference(c))
+
+
+def long_reference(c):
+    """Case.reference, once per case."""
+    key = (tuple(c.lens), c.Q, c.H)
+    if key not in LONG:
+        LONG[key] = c.reference()
+    return LONG[key]
+
+
+LONG = {}
+
+
+# Queries of zero weigh all rows alike, and sums of latents of 0 and 1 are exact: a row
+# left out or taken twice shows in the mean and in the log of the count.  Bound: the
+# merge's weights are within 2^-22, each product and sum of a piece within 2^-24.
+@pytest.mark.parametrize("num_sms,lens,Q,H", [
+    (0, [1000], 1, 1), (1200, [50000], 1, 5), (1200, [60000], 2, 65), (400, [1300000], 2, 65),
+    (2, [20000, 5000], 3, 128), (6, [20000, 5000, 0, 30000], 3, 128), (10, [9000] * 7, 4, 128),
+    (14, [12288 + 64 * i for i in range(9)], 2, 128), (0, [30000 + 7777 * i for i in range(12)], 5, 128),
+    (0, [300000, 250000], 5, 128), (38, [100, 150000, 37, 60000, 1], 9, 50), (24, [200000], 64, 8),
+])
+def test_every_row_counts_once(num_sms, lens, Q, H):
+    g = torch.Generator(device="cuda").manual_seed(len(lens) + Q)
+    offs = [sum(lens[:b]) + b * Q for b in range(len(lens))]
+    rows = sum(lens) + len(lens) * Q
+    kv = torch.randint(0, 2, (rows, 576), generator=g, device="cuda", dtype=torch.int8).bfloat16()
+    B, i32 = len(lens), dict(dtype=torch.int32, device="cuda")
+    q = torch.zeros(B, Q, H, 576, dtype=torch.bfloat16, device="cuda")
+    out, lse = torch.empty(B, Q, H, 512, device="cuda"), torch.empty(B, Q, H, device="cuda")
+    p = mla.tree_plan(batch=B, tokens=Q, heads=H, scale=SCALE, num_sms=num_sms)
+    scratch = mla.tree_alloc_scratch(p)
+    mla.tree_forward(p, q, kv, out, lse, scratch, d_pos=torch.tensor(lens, **i32),
+                     row_offset=torch.tensor(offs, dtype=torch.int64, device="cuda"))
+    assert mla.status_word(p, scratch) == 0
+    tol = 2.0 ** -21 + 2 * p.grid * 2.0 ** -23
+    for b, (o, n) in enumerate(zip(offs, lens)):
+        whole = kv[o:o + n, :512].sum(0, dtype=torch.float64)
+        for i in range(Q):
+            want = (whole + kv[o + n:o + n + i + 1, :512].double().sum(0)) / (n + i + 1)
+            assert (out[b, i].double() - want).abs().max() <= tol, (b, i)
+            assert (lse[b, i].double() - math.log(n + i + 1)).abs().max() <= 2.0 ** -20 * 8, (b, i)
+
+
 @pytest.mark.parametrize("mask", ["chain", "random", "none"])
 @pytest.mark.parametrize("lens,n", [([0, 40, 0], [4, 9, 0]), ([130, 257, 5], [9, 1, 6])])
 def test_masks_chains_empty_rows_and_ragged_drafts(mask, lens, n):
