@@ -9,8 +9,8 @@
 // shared memory is slow: 2048 bins and three digits took three times as long);
 // the keys stay in shared memory between the passes when they fit.
 // Rows above K stay, and of the rows equal to K the first so many that `keep`
-// is met; every thread counts over a contiguous run of rows, and prefix sums over
-// threads, warps and CTAs number the evicted rows below `keep` and the kept rows
+// is met; every warp counts over a contiguous run of rows, and prefix sums over
+// warps and CTAs number the evicted rows below `keep` and the kept rows
 // behind it in ascending order, which pairs them up.  Integers only: no order of
 // execution shows in the result.  Bound: latency (barriers and passes over shared
 // memory); 35 us for 16 requests of up to 131072 rows, 9 for one of 8192.
@@ -51,17 +51,17 @@ struct EvictScratch {
     int* moved;                                            // [B][keep] kept rows behind keep, ascending
 };
 
+// Rows above / equal to the threshold K, below `keep` and behind it.
+struct __align__(16) Counts {
+    uint32_t gt0, gt1, eq0, eq1;
+};
+
 struct SelShared {
     uint32_t hist[2][kBins];
     uint32_t sum[kBins];                                   // over the cluster
     uint32_t bin, above;                                   // the chosen digit, keys with a larger one
-    unsigned long long warp_counts[kSelWarps];
-    uint32_t cta[4];                                       // the CTA's counts, read by the others of the cluster
-};
-
-// Rows above / equal to the threshold K, below `keep` and behind it.
-struct Counts {
-    uint32_t gt0, gt1, eq0, eq1;
+    Counts warp_counts[kSelWarps];
+    Counts cta;                                            // the CTA's, read by the others of the cluster
 };
 
 __device__ __forceinline__ uint32_t rank_key(float w, int pos, int sink, long long recent_from) {
@@ -110,9 +110,9 @@ __global__ void __launch_bounds__(kSelThreads) mla_evict_select_kernel(const mla
     long long base;
     const int n = request_rows(a, b, &base);
     const int keep = min(n, a.keep);
-    // this CTA's rows [r0, r1); thread t has the `each` rows from r0 + t * each
-    const int each = static_cast<int>((static_cast<long long>(n) + CL * kSelThreads * 4 - 1) / (CL * kSelThreads * 4)) * 4;
-    const long long per = static_cast<long long>(each) * kSelThreads;
+    // this CTA's rows [r0, r1), in runs of `run` rows (a multiple of 32) per warp
+    const int run = static_cast<int>((static_cast<long long>(n) + CL * kSelThreads - 1) / (CL * kSelThreads)) * 32;
+    const long long per = static_cast<long long>(run) * kSelWarps;
     const int r0 = static_cast<int>(min(static_cast<long long>(n), rank * per));
     const int r1 = static_cast<int>(min(static_cast<long long>(n), r0 + per));
     if (n <= a.keep) {                                     // uniform over the cluster
@@ -183,9 +183,14 @@ __global__ void __launch_bounds__(kSelThreads) mla_evict_select_kernel(const mla
         uint32_t* hist = sh.hist[pass & 1];
         if (tid < kBins) hist[tid] = 0;
         __syncthreads();
-        for (int r = r0 + tid; r < r1; r += kSelThreads) {
-            const uint32_t k = key_of(r);
+        auto count_key = [&](uint32_t k) {
             if ((k & high_mask) == prefix) atomicAdd(&hist[k >> shift & 255u], 1u);
+        };
+        if (r1 - r0 <= kCache) {
+#pragma unroll 4
+            for (int i = tid; i < r1 - r0; i += kSelThreads) count_key(cached[i]);
+        } else {
+            for (int r = r0 + tid; r < r1; r += kSelThreads) count_key(key_of(r));
         }
         everyone();
         // every CTA sums all histograms (the next pass writes the other one; this one
@@ -223,34 +228,30 @@ __global__ void __launch_bounds__(kSelThreads) mla_evict_select_kernel(const mla
     }
     const uint32_t K = prefix;                             // `need` rows equal to K stay, the first ones
 
-    // ---- this thread's rows above and equal to K, below keep and behind it
-    const int t0 = static_cast<int>(min(static_cast<long long>(r1), r0 + static_cast<long long>(tid) * each));
-    const int t1 = static_cast<int>(min(static_cast<long long>(r1), static_cast<long long>(t0) + each));
-    // (four keys per shared-memory load: a lane's run is 16-byte aligned)
-    auto each_key = [&](auto&& f) {
-        for (int r = t0; r < t1; r += 4) {
-            if (r - r0 + 4 <= kCache) {
-                const uint4 k = *reinterpret_cast<const uint4*>(cached + (r - r0));
-                f(r, k.x);
-                if (r + 1 < t1) f(r + 1, k.y);
-                if (r + 2 < t1) f(r + 2, k.z);
-                if (r + 3 < t1) f(r + 3, k.w);
-            } else {
-                for (int i = r; i < min(r + 4, t1); ++i) f(i, key_of(i));
+    // ---- the warp's rows above and equal to K, below keep and behind it
+    auto run_from = [&](int w) { return static_cast<int>(min(static_cast<long long>(r1), r0 + static_cast<long long>(w) * run)); };
+    const int from = run_from(warp), to = run_from(warp + 1);
+    {
+        uint32_t gt = 0, eq = 0;
+        auto count_rows = [&](int r0, int r1) {
+#pragma unroll 4
+            for (int r = r0 + lane; r < r1; r += 32) {
+                const uint32_t k = key_of(r);
+                gt += k > K;
+                eq += k == K;
             }
-        }
-    };
-    Counts mine{0, 0, 0, 0};
-    each_key([&](int r, uint32_t k) {
-        const uint32_t g = k > K, e = k == K, low = r < keep;
-        mine.gt0 += g & low;
-        mine.gt1 += g & ~low;
-        mine.eq0 += e & low;
-        mine.eq1 += e & ~low;
-    });
+        };
+        const int low_to = min(max(keep, from), to);       // rows below keep, then the others
+        count_rows(from, low_to);
+        const uint32_t gt0 = gt, eq0 = eq;
+        count_rows(low_to, to);
+        const Counts c{__reduce_add_sync(0xffffffffu, gt0), __reduce_add_sync(0xffffffffu, gt - gt0),
+                       __reduce_add_sync(0xffffffffu, eq0), __reduce_add_sync(0xffffffffu, eq - eq0)};
+        if (lane == 0) sh.warp_counts[warp] = c;
+    }
     // Of the rows equal to K that follow `before` others, min(count, need - before)
     // stay, the first ones: from the counts follow the evicted rows below keep and
-    // the kept rows behind it, which a second prefix sum numbers.
+    // the kept rows behind it, which prefix sums number.
     auto stay_of = [&](const Counts& c, uint32_t before) {
         return before < need ? min(c.eq0 + c.eq1, need - before) : 0u;
     };
@@ -265,57 +266,37 @@ __global__ void __launch_bounds__(kSelThreads) mla_evict_select_kernel(const mla
         const long long end = to < keep ? to : keep;
         return static_cast<uint32_t>(end > from ? end - from : 0);
     };
-    // exclusive prefix over the CTA's threads of two 32-bit counts, and their totals
-    auto prefix2 = [&](uint32_t x, uint32_t y, uint32_t& px, uint32_t& py, uint32_t& tx, uint32_t& ty) {
-        const uint32_t ix = warp_incl_scan(x, lane), iy = warp_incl_scan(y, lane);
-        __syncthreads();                                   // the counts of the scan before are read
-        if (lane == 31) sh.warp_counts[warp] = static_cast<unsigned long long>(iy) << 32 | ix;
-        __syncthreads();
-        const unsigned long long v = sh.warp_counts[lane];
-        const uint32_t vx = static_cast<uint32_t>(v), vy = static_cast<uint32_t>(v >> 32);
-        const uint32_t sx = warp_incl_scan(vx, lane), sy = warp_incl_scan(vy, lane);
-        tx = __shfl_sync(0xffffffffu, sx, 31);
-        ty = __shfl_sync(0xffffffffu, sy, 31);
-        px = __shfl_sync(0xffffffffu, sx - vx, warp) + ix - x;
-        py = __shfl_sync(0xffffffffu, sy - vy, warp) + iy - y;
-    };
+    __syncthreads();
+    // every warp: lane l has warp l's counts, of this CTA
+    const Counts mine = sh.warp_counts[lane];
+    const uint32_t eq_mine = mine.eq0 + mine.eq1;
+    const uint32_t eq_incl = warp_incl_scan(eq_mine, lane);
     uint32_t eq = 0, hole0 = 0, moved0 = 0, all_moves = 0;
-    uint32_t eq_before, unused, eq_total, gt_total;
-    prefix2(mine.eq0 + mine.eq1, mine.gt0 + mine.gt1, eq_before, unused, eq_total, gt_total);
     if (CL > 1) {
-        // what lies in the CTAs before this one
-        uint32_t p0, p1, e0_total, g0_total;
-        prefix2(mine.eq0, mine.gt0, p0, p1, e0_total, g0_total);
-        if (tid == 0) {
-            sh.cta[0] = g0_total;
-            sh.cta[1] = gt_total - g0_total;
-            sh.cta[2] = e0_total;
-            sh.cta[3] = eq_total - e0_total;
-        }
+        // what lies in the CTAs before this one: lane q has CTA q's counts
+        const Counts sum{__reduce_add_sync(0xffffffffu, mine.gt0), __reduce_add_sync(0xffffffffu, mine.gt1),
+                         __reduce_add_sync(0xffffffffu, mine.eq0), __reduce_add_sync(0xffffffffu, mine.eq1)};
+        if (tid == 0) sh.cta = sum;
         everyone();
-        uint32_t before = 0;
-#pragma unroll
-        for (int q = 0; q < CL; ++q) {
-            const uint32_t* v = cluster.map_shared_rank(sh.cta, q);
-            const Counts c{v[0], v[1], v[2], v[3]};
-            const long long from = min(static_cast<long long>(n), q * per), to = min(static_cast<long long>(n), from + per);
-            const uint32_t m = moves_of(c, before);
-            if (q < rank) {
-                eq += c.eq0 + c.eq1;
-                hole0 += holes_of(c, before, rows_below(from, to));
-                moved0 += m;
-            }
-            all_moves += m;
-            before += c.eq0 + c.eq1;
-        }
+        Counts c{0, 0, 0, 0};
+        if (lane < CL) c = *cluster.map_shared_rank(&sh.cta, lane);
+        const uint32_t before = warp_incl_scan(c.eq0 + c.eq1, lane) - (c.eq0 + c.eq1);
+        const long long c0 = min(static_cast<long long>(n), lane * per), c1 = min(static_cast<long long>(n), c0 + per);
+        const uint32_t m = moves_of(c, before), h = lane < CL ? holes_of(c, before, rows_below(c0, c1)) : 0u;
+        eq = __shfl_sync(0xffffffffu, before, rank);
+        hole0 = __reduce_add_sync(0xffffffffu, lane < rank ? h : 0u);
+        moved0 = __reduce_add_sync(0xffffffffu, lane < rank ? m : 0u);
+        all_moves = __reduce_add_sync(0xffffffffu, m);
     }
-    eq += eq_before;
     {
-        uint32_t h, m, h_total, m_total;
-        prefix2(holes_of(mine, eq, rows_below(t0, t1)), moves_of(mine, eq), h, m, h_total, m_total);
-        hole0 += h;
-        moved0 += m;
-        if (CL == 1) all_moves = m_total;
+        const uint32_t before = eq + eq_incl - eq_mine;
+        const uint32_t h = holes_of(mine, before, rows_below(run_from(lane), run_from(lane + 1)));
+        const uint32_t m = moves_of(mine, before);
+        const uint32_t hi = warp_incl_scan(h, lane), mi = warp_incl_scan(m, lane);
+        eq = __shfl_sync(0xffffffffu, before, warp);
+        hole0 += __shfl_sync(0xffffffffu, hi - h, warp);
+        moved0 += __shfl_sync(0xffffffffu, mi - m, warp);
+        if (CL == 1) all_moves = __shfl_sync(0xffffffffu, mi, 31);
     }
     if (rank == 0 && tid == 0) {
         s.n_moves[b] = static_cast<int>(all_moves);        // as many as evicted rows below keep
@@ -323,27 +304,28 @@ __global__ void __launch_bounds__(kSelThreads) mla_evict_select_kernel(const mla
     }
     int* hole_list = s.hole + static_cast<long long>(b) * a.keep;
     int* moved_list = s.moved + static_cast<long long>(b) * a.keep;
-    // the warp's rows again, now 32 at a time, so that the lists are written in runs
+    // the warp's rows again, 32 at a time, so that the lists are written in runs
     // (a thread's own rows one by one: scattered stores, three times the time)
-    eq = __shfl_sync(0xffffffffu, eq, 0);
-    hole0 = __shfl_sync(0xffffffffu, hole0, 0);
-    moved0 = __shfl_sync(0xffffffffu, moved0, 0);
     const uint32_t lower = (1u << lane) - 1u;
-    const int warp_from = static_cast<int>(min(static_cast<long long>(r1), r0 + static_cast<long long>(warp) * 32 * each));
-    const int warp_to = static_cast<int>(min(static_cast<long long>(r1), warp_from + 32ll * each));
-    for (int r = warp_from; r < warp_to; r += 32) {
+    for (int r = from; r < to; r += 32) {
         const int row = r + lane;
-        const bool in = row < warp_to;
+        const bool in = row < to;
         const uint32_t k = in ? key_of(row) : 0u;
         const uint32_t e = __ballot_sync(0xffffffffu, in && k == K);
         const bool kept = in && (k > K || (k == K && eq + __popc(e & lower) < need));
-        const bool hole = in && row < keep && !kept, moved = row >= keep && kept;
-        const uint32_t hb = __ballot_sync(0xffffffffu, hole), mb = __ballot_sync(0xffffffffu, moved);
-        if (hole) hole_list[hole0 + __popc(hb & lower)] = row;
-        if (moved) moved_list[moved0 + __popc(mb & lower)] = row;
         eq += __popc(e);
-        hole0 += __popc(hb);
-        moved0 += __popc(mb);
+        if (r < keep) {
+            const bool hole = in && row < keep && !kept;
+            const uint32_t hb = __ballot_sync(0xffffffffu, hole);
+            if (hole) hole_list[hole0 + __popc(hb & lower)] = row;
+            hole0 += __popc(hb);
+        }
+        if (r + 32 > keep) {
+            const bool moved = row >= keep && kept;
+            const uint32_t mb = __ballot_sync(0xffffffffu, moved);
+            if (moved) moved_list[moved0 + __popc(mb & lower)] = row;
+            moved0 += __popc(mb);
+        }
     }
     allow_dependent_launch();
     everyone();                                            // no CTA leaves while others read its shared memory
