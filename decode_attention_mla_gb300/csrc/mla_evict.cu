@@ -132,6 +132,12 @@ __global__ void __launch_bounds__(kSelThreads) mla_evict_select_kernel(const mla
         return rank_key(a.weights[base + r], a.positions[base + r], a.sink, recent_from);
     };
     auto key_of = [&](int r) { return r - r0 < kCache ? cached[r - r0] : compute_key(r); };
+    auto with_keys = [&](auto&& f) {
+        if (r1 - r0 <= kCache)
+            f([&](int r) { return cached[r - r0]; });
+        else
+            f(key_of);
+    };
     // keys into shared memory, eight loads of each array in flight per thread; the
     // rows below keep get their own weight and position in the outputs (the move
     // overwrites those of the evicted ones)
@@ -186,12 +192,10 @@ __global__ void __launch_bounds__(kSelThreads) mla_evict_select_kernel(const mla
         auto count_key = [&](uint32_t k) {
             if ((k & high_mask) == prefix) atomicAdd(&hist[k >> shift & 255u], 1u);
         };
-        if (r1 - r0 <= kCache) {
+        with_keys([&](auto key) {
 #pragma unroll 4
-            for (int i = tid; i < r1 - r0; i += kSelThreads) count_key(cached[i]);
-        } else {
-            for (int r = r0 + tid; r < r1; r += kSelThreads) count_key(key_of(r));
-        }
+            for (int r = r0 + tid; r < r1; r += kSelThreads) count_key(key(r));
+        });
         everyone();
         // every CTA sums all histograms (the next pass writes the other one; this one
         // is written again only after every CTA has passed the next pass's barrier)
@@ -231,17 +235,19 @@ __global__ void __launch_bounds__(kSelThreads) mla_evict_select_kernel(const mla
     // ---- the warp's rows above and equal to K, below keep and behind it
     auto run_from = [&](int w) { return static_cast<int>(min(static_cast<long long>(r1), r0 + static_cast<long long>(w) * run)); };
     const int from = run_from(warp), to = run_from(warp + 1);
+    const int low_to = min(max(keep, from), to);           // rows below keep, then the others
     {
         uint32_t gt = 0, eq = 0;
         auto count_rows = [&](int r0, int r1) {
+            with_keys([&](auto key) {
 #pragma unroll 4
-            for (int r = r0 + lane; r < r1; r += 32) {
-                const uint32_t k = key_of(r);
-                gt += k > K;
-                eq += k == K;
-            }
+                for (int r = r0 + lane; r < r1; r += 32) {
+                    const uint32_t k = key(r);
+                    gt += k > K;
+                    eq += k == K;
+                }
+            });
         };
-        const int low_to = min(max(keep, from), to);       // rows below keep, then the others
         count_rows(from, low_to);
         const uint32_t gt0 = gt, eq0 = eq;
         count_rows(low_to, to);
@@ -307,25 +313,34 @@ __global__ void __launch_bounds__(kSelThreads) mla_evict_select_kernel(const mla
     // the warp's rows again, 32 at a time, so that the lists are written in runs
     // (a thread's own rows one by one: scattered stores, three times the time)
     const uint32_t lower = (1u << lane) - 1u;
-    for (int r = from; r < to; r += 32) {
-        const int row = r + lane;
-        const bool in = row < to;
-        const uint32_t k = in ? key_of(row) : 0u;
-        const uint32_t e = __ballot_sync(0xffffffffu, in && k == K);
-        const bool kept = in && (k > K || (k == K && eq + __popc(e & lower) < need));
-        eq += __popc(e);
-        if (r < keep) {
-            const bool hole = in && row < keep && !kept;
-            const uint32_t hb = __ballot_sync(0xffffffffu, hole);
-            if (hole) hole_list[hole0 + __popc(hb & lower)] = row;
-            hole0 += __popc(hb);
+    const uint32_t eq_warp = __shfl_sync(0xffffffffu, eq_mine, warp);
+    auto list_rows = [&](int r0, int r1, bool kept_ones, int* list, uint32_t at, auto&& kept) {
+#pragma unroll 4
+        for (int r = r0; r < r1; r += 32) {
+            const int row = r + lane;
+            const bool listed = kept(row, r1) == kept_ones && row < r1;
+            const uint32_t who = __ballot_sync(0xffffffffu, listed);
+            if (listed) list[at + __popc(who & lower)] = row;
+            at += __popc(who);
         }
-        if (r + 32 > keep) {
-            const bool moved = row >= keep && kept;
-            const uint32_t mb = __ballot_sync(0xffffffffu, moved);
-            if (moved) moved_list[moved0 + __popc(mb & lower)] = row;
-            moved0 += __popc(mb);
-        }
+    };
+    auto list_both = [&](auto&& kept) {
+        list_rows(from, low_to, false, hole_list, hole0, kept);
+        list_rows(low_to, to, true, moved_list, moved0, kept);
+    };
+    if (eq + eq_warp <= need || (eq >= need && K != 0xffffffffu)) {
+        // all or none of the warp's rows equal to K stay
+        const uint32_t least = eq + eq_warp <= need ? K : K + 1;
+        with_keys([&](auto key) { list_both([&](int row, int end) { return row < end && key(row) >= least; }); });
+    } else {
+        list_both([&](int row, int end) {
+            const uint32_t k = row < end ? key_of(row) : 0u;
+            const bool equal = row < end && k == K;
+            const uint32_t e = __ballot_sync(0xffffffffu, equal);
+            const bool stays = (row < end && k > K) || (equal && eq + __popc(e & lower) < need);
+            eq += __popc(e);
+            return stays;
+        });
     }
     allow_dependent_launch();
     everyone();                                            // no CTA leaves while others read its shared memory
