@@ -180,8 +180,9 @@ struct TreeCursor {
     __device__ __forceinline__ void enter(int at) {
         const int len = sg.tiles(seg);
         item_left = min(len - at, left);
-        hi = sg.start(seg) + len - at;                     // (of a cut job the first run takes the far tiles)
-        lo = hi - item_left;
+        // (of a cut row block the first run takes the far tiles)
+        lo = sg.start(seg) + (kByBlocks ? len - at - item_left : at);
+        hi = lo + item_left;
         tile = kByBlocks && g > 0 && item_left == len ? lo + g % len : lo;
     }
     __device__ __forceinline__ void start(const TreeParams& p, const TreeWork& w) {

@@ -63,7 +63,7 @@ struct __align__(1024) Shared {
     uint8_t k[C::kKSlots][kKChunkBytes];
     uint8_t q[C::kQBuffers * kChunks][kQChunkBytes];       // resident blocks, or a ring of 9 chunks
     float lse2[2][128];                                    // base 2; +inf: the row adds nothing
-    uint8_t token[2][128];
+    uint32_t adds[2][4];                                   // bit per row: it adds something
     float half_sum[2][128];
     // used in the even CTA
     uint64_t k_ready[C::kKSlots], q_ready[kChunks], s_free[2];
@@ -253,9 +253,9 @@ __device__ void add_weights(const TreeParams& p, Shared<kBlocks>& sh, uint32_t t
         const float old = mine && p.decay != 0.f ? *dst : 0.f;
         const bool special = c.special();
         // which tokens attend a drafted row (bit per token)
-        unsigned long long seen_by = ~0ull;
-        if (special && t >= c.r.d_pos) {
-            seen_by = 0;
+        const bool draft = special && t >= c.r.d_pos;
+        unsigned long long seen_by = 0;
+        if (draft) {
             const int j = t - c.r.d_pos;
             if (j < c.r.n_tok)
                 for (int i = 0; i < c.r.n_tok; ++i) seen_by |= (tree_mask(p, c.b, i, c.r.n_tok) >> j & 1ull) << i;
@@ -273,7 +273,8 @@ __device__ void add_weights(const TreeParams& p, Shared<kBlocks>& sh, uint32_t t
                     if (r < live) l = p.a.lse[static_cast<long long>(c.b) * p.tokens * p.heads + r];
                     none = l == -INFINITY;
                     sh.lse2[at][tid] = none ? INFINITY : l * kLog2e;
-                    sh.token[at][tid] = static_cast<uint8_t>(min(r / p.heads, 63));
+                    const uint32_t adds = __ballot_sync(0xffffffffu, !none);
+                    if (lane == 0) sh.adds[at][warp] = adds;
                 }
                 careful[at] = named_barrier_or(kBarSum, kSumThreads, none);
             }
@@ -281,6 +282,18 @@ __device__ void add_weights(const TreeParams& p, Shared<kBlocks>& sh, uint32_t t
             if (C::kStream || rb == 0) bad |= !warp_wait(&sh.abort_flag, &sh.s_full[buf], (n >> 1) & 1);
             const int columns = min(kTreeBlockRows, max(live - rb * kTreeBlockRows, 0));
             const uint32_t d = tmem + lanes + C::kScoreCols * buf + (C::kStream ? 0 : 128 * rb) + 64 * sub;
+            // this row's columns that count (bit per column, of 64)
+            unsigned long long counts = 0;
+            if (special || careful[at]) {
+                counts = sh.adds[at][2 * sub] | static_cast<unsigned long long>(sh.adds[at][2 * sub + 1]) << 32;
+                if (draft) {
+                    const int c0 = rb * kTreeBlockRows + 64 * sub;
+                    unsigned long long seen = 0;
+                    for (int i = c0 / p.heads; i < c.r.n_tok && i * p.heads < c0 + 64; ++i)
+                        if (seen_by >> i & 1ull) seen |= low_bits((i + 1) * p.heads - c0) & ~low_bits(i * p.heads - c0);
+                    counts &= seen;
+                }
+            }
 #pragma unroll 1
             for (int j = 0; j < 2; ++j) {
                 const int col = 64 * sub + 32 * j;
@@ -301,10 +314,8 @@ __device__ void add_weights(const TreeParams& p, Shared<kBlocks>& sh, uint32_t t
                 } else {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
-                        const float l = sh.lse2[at][col + i];
-                        const bool adds = l != INFINITY && (seen_by >> sh.token[at][col + i] & 1ull);
-                        const float x = ex2_approx(fmaf(__uint_as_float(s[i]), c2, -l));
-                        sum[i & 3] += adds ? x : 0.f;
+                        const float x = ex2_approx(fmaf(__uint_as_float(s[i]), c2, -sh.lse2[at][col + i]));
+                        sum[i & 3] += static_cast<uint32_t>(counts >> (32 * j)) >> i & 1u ? x : 0.f;
                     }
                 }
             }

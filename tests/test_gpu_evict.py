@@ -137,6 +137,22 @@ def test_evict_keeps_the_heaviest_rows(lens, keep, sink, recent, kind, fp8, stri
         assert torch.equal(p[o:o + k], wp[o:o + k])
 
 
+@pytest.mark.parametrize("n,keep", [(3000, 1100), (20000, 9000), (700, 800)])
+@pytest.mark.parametrize("own_weights", [True, False])
+def test_one_side_array_in_place_and_the_other_not(n, keep, own_weights):
+    kv = cache(n + 2, False, 576)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    w, p = torch.rand(n + 2, generator=g, device="cuda"), torch.randperm(n + 2, device="cuda").int()
+    want, ww, wp = reference(kv, w, p, [n], [2], keep, 3, 20, [n])
+    wo, po = (torch.full_like(w, 9), p) if own_weights else (w, torch.full_like(p, 9))
+    d = ints([n])
+    mla.evict(kv, w, p, mla.evict_alloc_scratch(batch=1, keep=keep), d_pos=d, next_pos=ints([n]), keep=keep, sink=3,
+              recent=20, row_offset=ints([2], torch.int64), weights_out=wo, positions_out=po)
+    k = min(n, keep)
+    assert torch.equal(raw(kv), want) and d.tolist() == [k]
+    assert torch.equal(wo[2:2 + k], ww[2:2 + k]) and torch.equal(po[2:2 + k], wp[2:2 + k])
+
+
 def test_rows_behind_the_cache_are_no_rows():
     kv = cache(100, False, 576)
     w, p = torch.rand(100, device="cuda"), ints(list(range(100)))
