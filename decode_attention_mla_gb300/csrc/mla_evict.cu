@@ -13,7 +13,7 @@
 // warps and CTAs number the evicted rows below `keep` and the kept rows
 // behind it in ascending order, which pairs them up.  Integers only: no order of
 // execution shows in the result.  Bound: latency (barriers and passes over shared
-// memory); 35 us for 16 requests of up to 131072 rows, 9 for one of 8192.
+// memory); 25 us for 16 requests of up to 131072 rows, 8 for one of 8192.
 //
 // Move.  A warp copies four bf16 rows (eight E4M3 rows) at a time, nine
 // 16-byte loads in flight per lane; source rows lie at or behind `keep` and

@@ -99,7 +99,7 @@ __device__ __forceinline__ unsigned long long visible64(const TreeRequest& r, un
 // The row blocks of a request read the same cache rows, at about the same time
 // if run lengths and cache lengths happen to fit; otherwise, with more cache than L2
 // holds, each reads them from DRAM again (16 requests of 5 row blocks: 1.35 GB for
-// 0.38 GB of rows).  Hence
+// 0.38 GB of rows; 0.61 in the order below).  Hence
 //   - tiles go by the clock: a job done whole by one run starts at the tile that it
 //     would have reached if it had begun with the run, and goes round; of a job cut
 //     between two runs, the first takes the far tiles, so that the second begins

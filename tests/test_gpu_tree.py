@@ -327,7 +327,8 @@ def test_two_calls_at_once_with_their_own_scratch():
 @pytest.mark.parametrize("lens,Q,H,n,mask", [
     ([0], 1, 1, None, "tree"), ([1], 1, 16, None, "tree"), ([127], 1, 16, None, "chain"), ([128], 2, 64, None, "tree"),
     ([129], 2, 128, None, "tree"), ([500], 8, 33, None, "tree"), ([260, 0, -1, 64, 1000], 5, 16, [5, 5, 5, 0, 3], "random"),
-    ([100], 64, 16, None, "tree"), ([300], 6, 16, None, "none"),
+    ([100], 64, 16, None, "tree"), ([300], 6, 16, None, "none"), ([100], 64, 1, None, "random"),
+    ([70, 9], 30, 7, None, "random"), ([40], 5, 127, None, "tree"),
 ])
 def test_weights_against_the_64_bit_form(lens, Q, H, n, mask, decay):
     c = Case(21 + Q + H, lens, Q, H, n_tokens=n, mask=mask)
