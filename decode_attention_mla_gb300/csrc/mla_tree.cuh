@@ -14,6 +14,8 @@ namespace mla {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTreeTileKeys = 128;                         // cache rows per tile of a CTA pair
 constexpr int kTreeBlockRows = 128;                        // (token, head) rows per CTA pair
+constexpr int kTreePieceRate = 14;                         // pieces written and merged in a tile's time ...
+constexpr int kTreeFewPieces = 16;                         // ... fewer cost next to nothing
 constexpr int kTreeCutTiles = 96;                          // tiles per run from which row blocks are cut
 constexpr long long kTreeMaxRow = 0x7fffff00;              // rows of a request from here on are not attended
 
@@ -231,6 +233,33 @@ struct TreeCursor {
     // the tile holds drafted rows or rows behind them
     __device__ __forceinline__ bool special() const { return (tile + 1) * kKeys > r.d_pos; }
 
+    // Run length, made a whole number of row blocks where they have one length and that
+    // costs no more tiles than writing and merging the pieces (64 x 128 rows over 4096:
+    // 32 tiles for 27, 56 us for 63; 64 requests of 1 x 128 over 4000 70 for 83).
+    // `tiles`: of every request with rows among the first 32.
+    static __device__ __forceinline__ long long whole_blocks(const TreeParams& p, const TreeRequest& r, int tiles,
+                                                             int lane, uint32_t total, long long per) {
+        uint32_t blocks = r.hi > 0 ? blocks_of(p, r) : 0;
+        if (p.batch > 1) {
+            bool alike = true;
+            for (int b = 32 + lane; b < p.batch; b += 32) {
+                const TreeRequest next = load_tree_request(p, b);
+                const int rb = next.hi > 0 ? blocks_of(p, next) : 0;
+                alike &= rb == 0 || tiles_of(next) == tiles;
+                blocks += rb;
+            }
+            if (!__all_sync(0xffffffffu, alike)) return per;
+            blocks = __reduce_add_sync(0xffffffffu, blocks);
+        }
+        const uint32_t clusters = p.clusters;
+        const long long whole = static_cast<long long>(blocks <= clusters ? 1 : (blocks + clusters - 1) / clusters) * tiles;
+        if (whole == per || whole > per + 1 + (clusters + blocks) / kTreePieceRate) return per;
+        // one piece per run, and one more where a run ends inside a block
+        const uint32_t run = static_cast<uint32_t>(per);
+        const uint32_t pieces = total / run + (tiles % run ? blocks : 0);
+        return pieces >= kTreeFewPieces && whole <= per + 1 + pieces / kTreePieceRate ? whole : per;
+    }
+
     // One warp: this cluster's run; run length = ceil(units / clusters).
     static __device__ void find_work(const TreeParams& p, int cluster, int lane, TreeWork* out) {
         auto request_of = [&](int b) {
@@ -239,17 +268,22 @@ struct TreeCursor {
             return r;
         };
         auto units_of = [&](const TreeRequest& r) { return static_cast<long long>(blocks_of(p, r)) * tiles_of(r); };
-        TreeRequest r = request_of(lane);                      // requests 0 .. 31 stay in registers
+        const bool one = p.batch == 1;                         // every lane has the one request
+        TreeRequest r = request_of(one ? 0 : lane);            // requests 0 .. 31 stay in registers
         long long total = units_of(r);
         for (int b0 = 32; b0 < p.batch; b0 += 32) total += units_of(request_of(b0 + lane));
-        if (p.batch > 1) {
+        if (!one) {
 #pragma unroll
             for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-        } else {
-            total = __shfl_sync(0xffffffffu, total, 0);
         }
         long long per = quotient(total + p.clusters - 1, p.clusters);
         if (per < 1) per = 1;
+        if (kByBlocks && total >= kTreeFewPieces && total < kTreeMaxRow) {
+            const int own = units_of(r) > 0 ? tiles_of(r) : 0;
+            const int tiles = one ? own : __reduce_max_sync(0xffffffffu, own);
+            if (tiles > 0 && (one || __all_sync(0xffffffffu, own == 0 || own == tiles)))
+                per = whole_blocks(p, r, tiles, lane, static_cast<uint32_t>(total), per);
+        }
         const long long u0 = per * cluster;
         const long long count = u0 >= total ? 0 : (total - u0 < per ? total - u0 : per);
         const int seg_tiles = static_cast<int>(kByBlocks && per >= kTreeCutTiles ? min(per, kTreeMaxRow) : kTreeMaxRow);
@@ -263,7 +297,7 @@ struct TreeCursor {
             if (b0 > 0) r = request_of(b0 + lane);
             const long long u = units_of(r);
             long long incl = u;
-            if (p.batch > 1) {
+            if (!one) {
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const long long y = __shfl_up_sync(0xffffffffu, incl, o);
@@ -271,7 +305,7 @@ struct TreeCursor {
                 }
             }
             const long long first = before + incl - u;         // this lane's request is units [first, first + u)
-            const bool here = u0 >= first && u0 < first + u;
+            const bool here = u0 >= first && u0 < first + u && (lane == 0 || !one);
             if (here) {
                 const int n_tiles = tiles_of(r), n_rb = blocks_of(p, r);
                 TreeSegments sg;

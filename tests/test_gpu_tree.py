@@ -143,6 +143,9 @@ LONG = {}
     (2, [20000, 5000], 3, 128), (6, [20000, 5000, 0, 30000], 3, 128), (10, [9000] * 7, 4, 128),
     (14, [12288 + 64 * i for i in range(9)], 2, 128), (0, [30000 + 7777 * i for i in range(12)], 5, 128),
     (0, [300000, 250000], 5, 128), (38, [100, 150000, 37, 60000, 1], 9, 50), (24, [200000], 64, 8),
+    # row blocks of one length, a whole number of them per run
+    (0, [1000], 64, 128), (0, [4000] * 64, 1, 128), (6, [900] * 5, 2, 128), (0, [500] * 40, 1, 16),
+    (0, [500] * 39 + [700], 1, 16), (0, [500, 0, 500, 500], 30, 128), (10, [600] * 12, 3, 128),
 ])
 def test_every_row_counts_once(num_sms, lens, Q, H):
     g = torch.Generator(device="cuda").manual_seed(len(lens) + Q)
