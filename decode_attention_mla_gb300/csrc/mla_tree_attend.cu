@@ -654,7 +654,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // their sums in order (the pieces come from L2: 76 of them in one warp's hands
 // took three times as long).
 constexpr int kMergeWarps = 8;
-constexpr int kFewPieces = 8;                              // up to about so many per block: four quads per warp
+// Up to about so many pieces per block: four quads per warp.  Measured on whole calls,
+// four quads / shared pieces: 8 blocks (10 pieces) 22.5 / 27.1 us, 6 blocks (13) 28.6 /
+// 30.2, 5 blocks (15) 40.8 / 40.6, 4 blocks (19) 27.8 / 26.0, 2 blocks (38) 28.9 / 20.8.
+constexpr int kFewPieces = 15;
 
 constexpr int kMergeList = 256;
 
