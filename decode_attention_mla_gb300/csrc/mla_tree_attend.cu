@@ -520,7 +520,7 @@ __device__ void softmax(const TreeParams& p, Shared& sh, uint32_t tmem, uint32_t
                     ((static_cast<long long>(b) * p.tokens * p.heads + r - row + row_w) * kDLatent + f0) *
                         (p.a.out_fp32 ? 4 : 2);
 #pragma unroll 1
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 4 && n_rows > 0; ++j) {        // (the merge reads groups with live rows only)
             uint32_t o[32];
             tmem_ld32_async(tmem + lanes + kTmemO + 128 * sub + 32 * j, o);
             tmem_wait_ld32(o);
