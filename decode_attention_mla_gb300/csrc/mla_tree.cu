@@ -89,6 +89,12 @@ int prepare(cudaStream_t st, bool may_capture) {
     return MLA_OK;
 }
 
+// Height of the boxes that a row block's last query rows come in (64: none needed).
+int q_tail(const mla_tree_plan_t* pl) {
+    const int rest = (pl->shape.tokens * pl->shape.heads + 7) / 8 * 8 % 64;
+    return rest ? rest : 64;
+}
+
 // The tensor cores' sums over 576 products are fp32, but each addition drops what
 // does not fit, towards zero: a score comes out smaller by 4.4e-7 of itself on average
 // (4.1e-7 .. 4.5e-7 for scores of deviation 0.5 .. 2; a score of 9 is off by 3.5e-6, an
@@ -102,6 +108,7 @@ TreeParams params(const mla_tree_plan_t* pl, const mla_tree_args* a, void* scrat
     p.batch = pl->shape.batch;
     p.tokens = pl->shape.tokens;
     p.heads = pl->shape.heads;
+    p.q_tail = q_tail(pl);
     p.clusters = pl->grid / 2;
     p.scale_log2 = static_cast<float>(pl->shape.scale * 1.4426950408889634 * (1 + kScoreLoss));
     p.merge = reinterpret_cast<TreeMerge*>(base + kMergeOffset);
@@ -113,9 +120,11 @@ TreeParams params(const mla_tree_plan_t* pl, const mla_tree_args* a, void* scrat
     return p;
 }
 
-int encode_q(const mla_tree_plan_t* pl, const mla_tree_args* a, CUtensorMap* map, uint32_t chunks) {
+int encode_q(const mla_tree_plan_t* pl, const mla_tree_args* a, TreeMaps* maps, uint32_t chunks) {
     const long long rows = static_cast<long long>(pl->shape.batch) * pl->shape.tokens * pl->shape.heads;
-    return encode_bf16_row_chunks(map, a->q, rows, MLA_D_ROW, 64, chunks);
+    const int rc = encode_bf16_row_chunks(&maps->q, a->q, rows, MLA_D_ROW, 64, chunks);
+    if (rc != MLA_OK || q_tail(pl) == 64) return rc;
+    return encode_bf16_row_chunks(&maps->q_tail, a->q, rows, MLA_D_ROW, q_tail(pl), 1);
 }
 
 }  // namespace
@@ -155,7 +164,7 @@ int mla_tree_forward(const mla_tree_plan_t* plan, const mla_tree_args* args, voi
     mla::TreeMaps maps{};
     rc = mla::encode_bf16_row_chunks(&maps.kv, args->kv, args->kv_rows, args->row_stride, 64, 2);
     if (rc == MLA_OK) rc = mla::encode_bf16_row_chunks(&maps.rope, args->kv, args->kv_rows, args->row_stride, 64, 1);
-    if (rc == MLA_OK) rc = mla::encode_q(plan, args, &maps.q, MLA_D_ROW / 64);
+    if (rc == MLA_OK) rc = mla::encode_q(plan, args, &maps, MLA_D_ROW / 64);
     if (rc != MLA_OK) return rc;
     return mla::launch_status(
         mla::launch_tree_attend(maps, mla::params(plan, args, scratch), plan->shape.pdl != 0, st));
@@ -174,7 +183,7 @@ int mla_tree_weights(const mla_tree_plan_t* plan, const mla_tree_args* args, flo
     if (rc != MLA_OK) return rc;
     mla::TreeMaps maps{};
     rc = mla::encode_bf16_row_chunks(&maps.k, args->kv, args->kv_rows, args->row_stride, 128, 1);
-    if (rc == MLA_OK) rc = mla::encode_q(plan, args, &maps.q, 1);
+    if (rc == MLA_OK) rc = mla::encode_q(plan, args, &maps, 1);
     if (rc != MLA_OK) return rc;
     mla::TreeParams p = mla::params(plan, args, scratch);
     p.weights = weights;

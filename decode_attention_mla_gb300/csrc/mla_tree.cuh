@@ -37,6 +37,7 @@ struct __align__(16) TreeCut {
 struct TreeParams {
     mla_tree_args a;
     int batch, tokens, heads;
+    int q_tail;                                            // tokens * heads mod 64, rounded up to 8 (64: no rest)
     int clusters;
     float scale_log2;                                      // scale * log2(e): scores in base-2 units
     float* part;                                           // fp32 [clusters][3][128 x 512], normalised, by feature quads
@@ -360,7 +361,31 @@ struct TreeMaps {                                          // boxes of 64-column
     CUtensorMap rope;                                      // attention: cache, 64 rows x 1 chunk
     CUtensorMap k;                                         // weights: cache, 128 rows x 1 chunk
     CUtensorMap q;                                         // attention: queries, 64 rows x 9 chunks; weights: x 1
+    CUtensorMap q_tail;                                    // queries, q_tail rows x 1 chunk
 };
+
+// Of the 64 query rows from `row` on, how many are loaded: those in the tensor, if boxes
+// of q_tail rows make them up, and otherwise all.  (Rows that TMA fills with zeros cost
+// nothing in one CTA, but 5 us where all of them ask for some at once: one token of 16
+// heads over 16384 rows 22 us, without such rows 17.)  Rows that are not loaded hold
+// anything; they are dead, and no row's result depends on another's.
+__device__ __forceinline__ int query_rows(const TreeParams& p, int row) {
+    const int there = min(max((p.batch * p.tokens * p.heads - row + 7) & ~7, 0), 64);
+    return there % p.q_tail == 0 ? there : 64;
+}
+// `n` of them: kQChunks 64-column chunks from `chunk` on.
+template <int kQChunks>
+__device__ __forceinline__ void load_query_rows(uint8_t* dst, const TreeMaps& maps, int row, int n, int tail, int chunk,
+                                                uint32_t bar, uint64_t policy) {
+    if (n == 64) {
+        tma_load_3d_pair(dst, &maps.q, 0, row, chunk, bar, policy);
+        return;
+    }
+    for (int i = 0; i < n; i += tail)
+#pragma unroll
+        for (int k = 0; k < kQChunks; ++k)
+            tma_load_3d_pair(dst + k * 8192 + i * 128, &maps.q_tail, 0, row + i, chunk + k, bar, policy);
+}
 cudaError_t tree_attend_prepare();
 cudaError_t launch_tree_attend(const TreeMaps& maps, const TreeParams& p, bool pdl, cudaStream_t stream);
 cudaError_t tree_weights_prepare();

@@ -121,9 +121,11 @@ struct Producer {
     }
     __device__ bool load_q(const Cursor& c) {
         if (c.item > 0 && !mbar_wait_bounded(&sh.q_empty, (c.item - 1) & 1, &sh.abort_flag)) return false;
-        const uint32_t bar = expect(&sh.q_ready, kQBytes);
-        const int row = c.b * p.tokens * p.heads + c.rb * kTreeBlockRows + static_cast<int>(rank) * 64;
-        tma_load_3d_pair(sh.q, &maps.q, 0, row, 0, bar, pol_q);
+        const int row = c.b * p.tokens * p.heads + c.rb * kTreeBlockRows;
+        const int n0 = query_rows(p, row), n1 = query_rows(p, row + 64);
+        if (rank == 0) mbar_arrive_expect_tx(&sh.q_ready, (n0 + n1) * (kQBytes / 64));
+        load_query_rows<9>(sh.q, maps, row + 64 * static_cast<int>(rank), rank == 0 ? n0 : n1, p.q_tail, 0,
+                           smem_u32(&sh.q_ready) + leader, pol_q);
         return true;
     }
     // QK operands: this CTA's 64 keys, 128 columns a slot, the rope columns with the last
@@ -581,6 +583,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         prefetch_tensormap(&maps.kv);
         prefetch_tensormap(&maps.rope);
         prefetch_tensormap(&maps.q);
+        if (p.q_tail < 64) prefetch_tensormap(&maps.q_tail);
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(&sh.k_ready[i], 1);
             mbar_init(&sh.k_empty[i], 1);

@@ -121,10 +121,15 @@ __device__ void produce_q(const TreeMaps& maps, const TreeParams& p, Shared<kBlo
     bool ok = true;
     Cursor c;
     for (c.start(p, sh.work); c.left > 0 && ok; c.next(p)) {
-        const int row = c.b * p.tokens * p.heads + static_cast<int>(rank) * 64;
+        const int row0 = c.b * p.tokens * p.heads, row = row0 + static_cast<int>(rank) * 64;
         const int blocks = query_blocks(p, c.r);
+        const int last0 = query_rows(p, row0 + (blocks - 1) * kTreeBlockRows),
+                  last1 = query_rows(p, row0 + (blocks - 1) * kTreeBlockRows + 64);   // (the blocks before it are whole)
         if constexpr (C::kStream) {
-            for (int rb = 0; rb < blocks && ok; ++rb, ++round) {
+            // (a loop of its own for a last block that is not loaded whole: this one keeps
+            // pace with the MMAs only while it is short)
+            const int whole = last0 + last1 == kTreeBlockRows ? blocks : blocks - 1;
+            for (int rb = 0; rb < whole && ok; ++rb, ++round) {
 #pragma unroll 1
                 for (int s = 0; s < kChunks && ok; ++s) {
                     ok = round == 0 || mbar_wait_bounded(&sh.q_empty[s], (round - 1) & 1, &sh.abort_flag);
@@ -133,14 +138,29 @@ __device__ void produce_q(const TreeMaps& maps, const TreeParams& p, Shared<kBlo
                                          expect(sh, &sh.q_ready[s], kQChunkBytes, rank), policy);
                 }
             }
+            if (whole < blocks && ok) {
+#pragma unroll 1
+                for (int s = 0; s < kChunks && ok; ++s) {
+                    ok = round == 0 || mbar_wait_bounded(&sh.q_empty[s], (round - 1) & 1, &sh.abort_flag);
+                    if (!ok) break;
+                    if (rank == 0) mbar_arrive_expect_tx(&sh.q_ready[s], (last0 + last1) * 128);
+                    load_query_rows<1>(sh.q[s], maps, row + whole * kTreeBlockRows, rank == 0 ? last0 : last1, p.q_tail,
+                                       s, map_to_rank(&sh.q_ready[s], 0), policy);
+                }
+                ++round;
+            }
         } else if (c.first) {
             // a request's blocks stay for its part of the run
             ok = round == 0 || mbar_wait_bounded(&sh.q_empty[0], (round - 1) & 1, &sh.abort_flag);
             if (ok) {
-                const uint32_t bar = expect(sh, &sh.q_ready[0], blocks * kQBlockBytes, rank);
-                for (int i = 0; i < blocks * kChunks; ++i)
-                    tma_load_3d_pair(sh.q[i], &maps.q, 0, row + (i / kChunks) * kTreeBlockRows, i % kChunks, bar,
-                                     policy);
+                if (rank == 0)
+                    mbar_arrive_expect_tx(&sh.q_ready[0], ((blocks - 1) * kTreeBlockRows + last0 + last1) * (kChunks * 128));
+                for (int i = 0; i < blocks * kChunks; ++i) {
+                    const int rb = i / kChunks;
+                    load_query_rows<1>(sh.q[i], maps, row + rb * kTreeBlockRows,
+                                       rb < blocks - 1 ? 64 : rank == 0 ? last0 : last1, p.q_tail, i % kChunks,
+                                       map_to_rank(&sh.q_ready[0], 0), policy);
+                }
             }
             ++round;
         }
@@ -347,6 +367,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         prefetch_tensormap(&maps.k);
         prefetch_tensormap(&maps.q);
+        if (p.q_tail < 64) prefetch_tensormap(&maps.q_tail);
         for (int i = 0; i < C::kKSlots; ++i) {
             mbar_init(&sh.k_ready[i], 1);
             mbar_init(&sh.k_empty[i], 1);

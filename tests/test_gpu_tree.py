@@ -106,6 +106,8 @@ class Case:
     ([0], 1, 1), ([1], 1, 16), ([0], 5, 16), ([63], 1, 16), ([64], 2, 16), ([127], 1, 128), ([128], 4, 32),
     ([120], 8, 16), ([121], 8, 16), ([255], 3, 5), ([300], 7, 48), ([1000], 64, 16), ([513], 64, 128),
     ([2000], 13, 17), ([700, 0, 129, 64, 3], 6, 16), ([200] * 9, 3, 64),
+    # query rows that are not a whole number of boxes, in several requests
+    ([3000], 1, 16), ([200] * 5, 1, 5), ([300] * 6, 3, 7), ([500, 300], 5, 70), ([90, 400, 7], 12, 33),
 ])
 def test_trees_against_the_64_bit_form(lens, Q, H, dtype):
     c = Case(11 * len(lens) + Q + H, lens, Q, H)
@@ -331,7 +333,8 @@ def test_two_calls_at_once_with_their_own_scratch():
     ([0], 1, 1, None, "tree"), ([1], 1, 16, None, "tree"), ([127], 1, 16, None, "chain"), ([128], 2, 64, None, "tree"),
     ([129], 2, 128, None, "tree"), ([500], 8, 33, None, "tree"), ([260, 0, -1, 64, 1000], 5, 16, [5, 5, 5, 0, 3], "random"),
     ([100], 64, 16, None, "tree"), ([300], 6, 16, None, "none"), ([100], 64, 1, None, "random"),
-    ([70, 9], 30, 7, None, "random"), ([40], 5, 127, None, "tree"),
+    ([70, 9], 30, 7, None, "random"), ([40], 5, 127, None, "tree"), ([500, 300], 5, 70, None, "tree"),
+    ([200] * 5, 1, 5, None, "tree"), ([300] * 6, 3, 7, None, "chain"), ([90, 400, 7], 12, 33, [12, 1, 7], "random"),
 ])
 def test_weights_against_the_64_bit_form(lens, Q, H, n, mask, decay):
     c = Case(21 + Q + H, lens, Q, H, n_tokens=n, mask=mask)
