@@ -234,31 +234,79 @@ struct TreeCursor {
     // the tile holds drafted rows or rows behind them
     __device__ __forceinline__ bool special() const { return (tile + 1) * kKeys > r.d_pos; }
 
-    // Run length, made a whole number of row blocks where they have one length and that
-    // costs no more tiles than writing and merging the pieces (64 x 128 rows over 4096:
-    // 32 tiles for 27, 56 us for 63; 64 requests of 1 x 128 over 4000 70 for 83).
-    // `tiles`: of every request with rows among the first 32.
-    static __device__ __forceinline__ long long whole_blocks(const TreeParams& p, const TreeRequest& r, int tiles,
-                                                             int lane, uint32_t total, long long per) {
+    // Whether row blocks go whole into the run that their first unit falls into: some runs
+    // then are longer, but no pieces are written and merged.  (64 x 128 rows over 4096: 32
+    // tiles for 27, 56 us for 63; 64 requests of 1 x 128 over 4000 70 for 83; 16 of 8 x 128
+    // over 500 .. 1400 47 for 57; but 8 of 4 x 64 over 1000, 8 tiles for 2, 20 for 17.)
+    // `longest`, `alike`: of the lengths of the first 32 requests.
+    static __device__ __forceinline__ bool keep_whole(const TreeParams& p, const TreeRequest& r, int longest,
+                                                      bool alike, int lane, uint32_t total, uint32_t per) {
         uint32_t blocks = r.hi > 0 ? blocks_of(p, r) : 0;
         if (p.batch > 1) {
-            bool alike = true;
+            const int first = longest;
             for (int b = 32 + lane; b < p.batch; b += 32) {
                 const TreeRequest next = load_tree_request(p, b);
-                const int rb = next.hi > 0 ? blocks_of(p, next) : 0;
-                alike &= rb == 0 || tiles_of(next) == tiles;
-                blocks += rb;
+                const int n = next.hi > 0 ? blocks_of(p, next) : 0;
+                blocks += n;
+                alike &= n == 0 || tiles_of(next) == first;
+                longest = max(longest, n == 0 ? 0 : tiles_of(next));
             }
-            if (!__all_sync(0xffffffffu, alike)) return per;
+            longest = __reduce_max_sync(0xffffffffu, longest);
+            alike = __all_sync(0xffffffffu, alike);
             blocks = __reduce_add_sync(0xffffffffu, blocks);
         }
-        const uint32_t clusters = p.clusters;
-        const long long whole = static_cast<long long>(blocks <= clusters ? 1 : (blocks + clusters - 1) / clusters) * tiles;
-        if (whole == per || whole > per + 1 + (clusters + blocks) / kTreePieceRate) return per;
-        // one piece per run, and one more where a run ends inside a block
-        const uint32_t run = static_cast<uint32_t>(per);
-        const uint32_t pieces = total / run + (tiles % run ? blocks : 0);
-        return pieces >= kTreeFewPieces && whole <= per + 1 + pieces / kTreePieceRate ? whole : per;
+        const uint32_t more = alike ? (per + longest - 1) / longest * longest - per : longest - 1;
+        if (more > 1 + 2u * p.clusters / kTreePieceRate) return false;
+        // pieces: one per run and one more where a run ends inside a block, two at most
+        const uint32_t runs = total / per;
+        const uint32_t pieces = min(runs + (alike && longest % per == 0 ? 0 : blocks), 2 * runs);
+        return pieces >= kTreeFewPieces && more <= 1 + pieces / kTreePieceRate;
+    }
+
+    // The run of the row blocks whose first unit lies in [u0, u1).
+    static __device__ __forceinline__ void find_whole(const TreeParams& p, TreeRequest r, bool one, long long u0,
+                                                      long long u1, long long total, int lane, TreeWork* out) {
+        long long before = 0, s0 = -1, s1 = total;
+        for (int b0 = 0; b0 < p.batch; b0 += 32) {
+            if (b0 > 0) r = b0 + lane < p.batch ? load_tree_request(p, b0 + lane) : TreeRequest{};
+            const int len = max(tiles_of(r), 1), n_rb = r.hi > 0 ? blocks_of(p, r) : 0;
+            const long long u = static_cast<long long>(n_rb) * len;
+            long long incl = u;
+            if (!one) {
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += y;
+                }
+            }
+            const long long first = before + incl - u;
+            // this lane's request's first block that begins at or behind a unit
+            auto block = [&](long long at) { return at <= first ? 0ll : quotient(at - first + len - 1, len); };
+            const long long j0 = block(u0), j1 = block(u1);
+            const bool mine = lane == 0 || !one;
+            const uint32_t has0 = __ballot_sync(0xffffffffu, mine && j0 < n_rb);
+            const uint32_t has1 = __ballot_sync(0xffffffffu, mine && j1 < n_rb);
+            if (s0 < 0 && has0 != 0) {
+                const int src = __ffs(has0) - 1;
+                s0 = __shfl_sync(0xffffffffu, first + j0 * len, src);
+                if (lane == src) {
+                    out->b = b0 + lane;
+                    out->r = r;
+                    out->seg = out->at = 0;
+                    out->rb = static_cast<int>(j0);
+                    out->begin = static_cast<int>(first - s0);
+                }
+            }
+            if (has1 != 0) {
+                s1 = __shfl_sync(0xffffffffu, first + j1 * len, __ffs(has1) - 1);
+                break;
+            }
+            before += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (lane == 0) {
+            out->count = s0 < 0 ? 0 : s1 - s0;
+            out->seg_tiles = static_cast<int>(kTreeMaxRow);
+        }
     }
 
     // One warp: this cluster's run; run length = ceil(units / clusters).
@@ -279,11 +327,13 @@ struct TreeCursor {
         }
         long long per = quotient(total + p.clusters - 1, p.clusters);
         if (per < 1) per = 1;
+        bool whole = false;
         if (kByBlocks && total >= kTreeFewPieces && total < kTreeMaxRow) {
             const int own = units_of(r) > 0 ? tiles_of(r) : 0;
-            const int tiles = one ? own : __reduce_max_sync(0xffffffffu, own);
-            if (tiles > 0 && (one || __all_sync(0xffffffffu, own == 0 || own == tiles)))
-                per = whole_blocks(p, r, tiles, lane, static_cast<uint32_t>(total), per);
+            const int longest = one ? own : __reduce_max_sync(0xffffffffu, own);
+            const bool alike = one || __all_sync(0xffffffffu, own == 0 || own == longest);
+            if (longest > 0 && (alike || longest <= 2 + 2 * p.clusters / kTreePieceRate))
+                whole = keep_whole(p, r, longest, alike, lane, static_cast<uint32_t>(total), static_cast<uint32_t>(per));
         }
         const long long u0 = per * cluster;
         const long long count = u0 >= total ? 0 : (total - u0 < per ? total - u0 : per);
@@ -292,6 +342,10 @@ struct TreeCursor {
             out->per = per;
             out->count = count;
             out->seg_tiles = seg_tiles;
+        }
+        if (whole) {
+            find_whole(p, r, one, u0, u0 + per, total, lane, out);
+            return;
         }
         long long before = 0;
         for (int b0 = 0; b0 < p.batch && count > 0; b0 += 32) {

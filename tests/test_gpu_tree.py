@@ -148,6 +148,9 @@ LONG = {}
     # row blocks of one length, a whole number of them per run
     (0, [1000], 64, 128), (0, [4000] * 64, 1, 128), (6, [900] * 5, 2, 128), (0, [500] * 40, 1, 16),
     (0, [500] * 39 + [700], 1, 16), (0, [500, 0, 500, 500], 30, 128), (10, [600] * 12, 3, 128),
+    # short ones of several lengths, whole as well
+    (0, [357, 567], 45, 128), (0, [300 + 97 * (i % 11) for i in range(100)], 1, 128),
+    (0, [20, 0, 900, 4, 130, 1, 400], 40, 64), (0, [(i * 37) % 140 for i in range(70)], 6, 128), (8, [700, 300], 20, 100),
 ])
 def test_every_row_counts_once(num_sms, lens, Q, H):
     g = torch.Generator(device="cuda").manual_seed(len(lens) + Q)
