@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -112,6 +113,10 @@ class TreeCommitArgs(ctypes.Structure):
                 ("row_positions", ctypes.c_void_p), ("row_weights", ctypes.c_void_p)]
 
 
+# The same layout, packed in one go: tree_commit fills its arguments on every call.
+_COMMIT_ARGS = struct.Struct("Pqqiii0P7P")
+
+
 class EvictArgs(ctypes.Structure):
     _fields_ = [("kv", ctypes.c_void_p), ("kv_rows", ctypes.c_longlong), ("row_stride", ctypes.c_longlong),
                 ("kv_fp8", ctypes.c_int), ("batch", ctypes.c_int), ("keep", ctypes.c_int), ("sink", ctypes.c_int),
@@ -195,7 +200,7 @@ def lib():
         L.mla_tree_weights.restype = I
         L.mla_tree_weights.argtypes = [ctypes.POINTER(TreePlan), ctypes.POINTER(TreeArgs), P, F, P, SZ, P]
         L.mla_tree_commit.restype = I
-        L.mla_tree_commit.argtypes = [ctypes.POINTER(TreeCommitArgs), P]
+        L.mla_tree_commit.argtypes = [P, P]
         L.mla_evict_scratch_bytes.restype = SZ
         L.mla_evict_scratch_bytes.argtypes = [I, I]
         L.mla_evict.restype = I
@@ -243,7 +248,7 @@ def _stream(stream):
     if stream is None:
         torch = _torch or _tc()
         if _raw_stream is not None:
-            return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
+            return _raw_stream(torch.cuda.current_device())    # (every entry point declares the pointer type)
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
@@ -299,6 +304,8 @@ def make_args(q, kv, out, lse, *, d_pos=None, row_offset=None, cache_len=None, i
 
 
 def _scratch_args(scratch):
+    if getattr(scratch, "is_cuda", False):
+        return scratch.data_ptr(), scratch.nbytes
     return _ptr(scratch), scratch.numel() * scratch.element_size()
 
 
@@ -452,6 +459,18 @@ def _cache(kv, kv_rows, row_stride, fp8_ok=True):
     return p, rows, stride, 0 if kv.dtype is torch.bfloat16 else 1
 
 
+def _quick_cache(kv, device, torch):
+    """As _cache(kv, None, None) for the usual cache; None if it is not one."""
+    try:
+        dt, shape, strides = kv.dtype, kv.shape, kv.stride()
+        if (kv.get_device() == device and len(shape) == 2 and shape[1] == D_ROW and strides[1] == 1 and shape[0] > 1
+                and (dt is torch.bfloat16 or dt is torch.uint8 or dt is torch.float8_e4m3fn)):
+            return kv.data_ptr(), shape[0], strides[0], 0 if dt is torch.bfloat16 else 1
+    except AttributeError:
+        pass
+    return None
+
+
 def _strides(t, name, shape, last):
     """Pointer and leading strides of a bf16 tensor whose last dimension is contiguous."""
     torch = _torch or _tc()
@@ -541,6 +560,9 @@ def _side(t, name, dtype, rows):
     """A per-row array: at least one entry for every cache row."""
     if t is None:
         return None
+    if getattr(t, "dtype", None) is dtype and t.dim() == 1 and t.shape[0] >= rows and t.is_contiguous() and (
+            t.get_device() == _torch.cuda.current_device()):
+        return t.data_ptr()
     p = _need(t, name, dtype, (None,))
     if t.shape[0] < rows:
         raise ValueError(f"{name} needs an entry for each of the {rows} cache rows")
@@ -640,14 +662,17 @@ def tree_commit(kv, accept, n_accept, *, d_pos, d_pos_out=None, row_offset=None,
     torch = _torch or _tc()
     B, Q = accept.shape
     i32, dev = torch.int32, torch.cuda.current_device()
-    kvp, rows, stride, fp8 = _cache(kv, kv_rows, row_stride)
-    a = TreeCommitArgs(kvp, rows, stride, fp8, B, Q, _quick(accept, "accept", i32, (B, Q), dev),
-                       _quick(n_accept, "n_accept", i32, (B,), dev), _quick(d_pos, "d_pos", i32, (B,), dev),
-                       None if d_pos_out is None else _quick(d_pos_out, "d_pos_out", i32, (B,), dev),
-                       None if row_offset is None else _quick(row_offset, "row_offset", torch.int64, (B,), dev),
-                       _side(row_positions, "row_positions", i32, rows),
-                       _side(row_weights, "row_weights", torch.float32, rows))
-    _check(lib().mla_tree_commit(ctypes.byref(a), _stream(stream)), "mla_tree_commit")
+    kvp, rows, stride, fp8 = _quick_cache(kv, dev, torch) or _cache(kv, None, None)
+    if kv_rows is not None or row_stride is not None:
+        kvp, rows, stride, fp8 = _cache(kv, kv_rows, row_stride)
+    args = _COMMIT_ARGS.pack(
+        kvp, rows, stride, fp8, B, Q, _quick(accept, "accept", i32, (B, Q), dev),
+        _quick(n_accept, "n_accept", i32, (B,), dev), _quick(d_pos, "d_pos", i32, (B,), dev),
+        0 if d_pos_out is None else _quick(d_pos_out, "d_pos_out", i32, (B,), dev),
+        0 if row_offset is None else _quick(row_offset, "row_offset", torch.int64, (B,), dev),
+        0 if row_positions is None else _side(row_positions, "row_positions", i32, rows),
+        0 if row_weights is None else _side(row_weights, "row_weights", torch.float32, rows))
+    _check(lib().mla_tree_commit(args, _stream(stream)), "mla_tree_commit")
 
 
 def evict_alloc_scratch(*, batch: int, keep: int, device=None):

@@ -151,6 +151,7 @@ LONG = {}
     # short ones of several lengths, whole as well
     (0, [357, 567], 45, 128), (0, [300 + 97 * (i % 11) for i in range(100)], 1, 128),
     (0, [20, 0, 900, 4, 130, 1, 400], 40, 64), (0, [(i * 37) % 140 for i in range(70)], 6, 128), (8, [700, 300], 20, 100),
+    (0, [(i * 7) % 23 for i in range(4096)], 1, 1),
 ])
 def test_every_row_counts_once(num_sms, lens, Q, H):
     g = torch.Generator(device="cuda").manual_seed(len(lens) + Q)

@@ -224,3 +224,9 @@ def test_python_side_wants_cuda_tensors():
         mla.rope_turns(scaling="other")
     with pytest.raises(ValueError):
         mla.evict_alloc_scratch(batch=1, keep=0)
+
+
+def test_packed_commit_arguments_have_the_structures_layout():
+    v = list(range(1, 14))
+    a = mla.TreeCommitArgs(*v)
+    assert mla._COMMIT_ARGS.size == ctypes.sizeof(a) and mla._COMMIT_ARGS.pack(*v) == bytes(a)
