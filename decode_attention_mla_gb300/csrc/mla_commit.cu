@@ -76,6 +76,14 @@ extern "C" int mla_tree_commit(const mla_tree_commit_args* a, void* stream) {
         mla::off(a->n_accept, 4) || mla::off(a->d_pos, 4) || mla::off(a->d_pos_out, 4) ||
         mla::off(a->row_offset, 8) || mla::off(a->row_positions, 4) || mla::off(a->row_weights, 4))
         return MLA_EALIGN;
-    mla::mla_commit_kernel<<<a->batch, mla::kCommitThreads, 0, static_cast<cudaStream_t>(stream)>>>(*a);
-    return mla::launch_status(cudaGetLastError());
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a->batch);
+    cfg.blockDim = dim3(mla::kCommitThreads);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return mla::launch_status(cudaLaunchKernelEx(&cfg, mla::mla_commit_kernel, *a));
 }

@@ -274,7 +274,14 @@ extern "C" int mla_rope_append(const mla_rope_args* args, void* stream) {
     const int units = (args->heads + 4 * mla::kHeadPasses - 1) / (4 * mla::kHeadPasses) + (args->kv ? 1 : 0);
     const long long warps = static_cast<long long>(args->tokens) * units;
     const long long per = mla::kRopeThreads / 32;
-    mla::mla_rope_kernel<<<dim3(static_cast<unsigned>((warps + per - 1) / per), args->batch), mla::kRopeThreads, 0,
-                           static_cast<cudaStream_t>(stream)>>>(*args, units);
-    return mla::launch_status(cudaGetLastError());
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((warps + per - 1) / per), args->batch);
+    cfg.blockDim = dim3(mla::kRopeThreads);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return mla::launch_status(cudaLaunchKernelEx(&cfg, mla::mla_rope_kernel, *args, units));
 }

@@ -175,3 +175,32 @@ def test_more_rows_than_the_select_holds_in_shared_memory():
         mla.evict(k, wk, pk, mla.evict_alloc_scratch(batch=1, keep=70001), d_pos=d, next_pos=ints([n]), keep=70001,
                   sink=4, recent=1000, max_rows=expect)
         assert torch.equal(raw(k), want) and torch.equal(wk[:70001], ww[:70001]) and torch.equal(pk[:70001], wp[:70001])
+
+
+@pytest.mark.parametrize("n,keep", [(3000, 1100), (20000, 9000)])
+def test_captured_behind_copies(n, keep):
+    # the launches may begin before the work ahead of them has ended: here copies that bring their inputs
+    kv = cache(n, False, 576)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    w, p = torch.rand(n, generator=g, device="cuda"), torch.randperm(n, device="cuda").int()
+    want, ww, wp = reference(kv, w, p, [n - 2], [0], keep, 3, 20, [n])
+    start = [t.clone() for t in (raw(kv), w, p)]
+    d, path, two = ints([n - 2]), ints([[1, 0]]), ints([2])
+    d0, nxt, scratch = ints([n - 2]), ints([n]), mla.evict_alloc_scratch(batch=1, keep=keep)
+    side = dict(row_positions=p, row_weights=w)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        for t, s in zip((raw(kv), w, p), start):
+            t.copy_(s)
+        d.copy_(d0)
+        mla.evict(kv, w, p, scratch, d_pos=d, next_pos=nxt, keep=keep, sink=3, recent=20)
+        d -= 2
+        mla.tree_commit(kv, path, two, d_pos=d, d_pos_out=d, **side)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    want[keep - 2:keep] = want[keep - 2:keep].flip(0)
+    ww[keep - 2:keep], wp[keep - 2:keep] = ww[keep - 2:keep].flip(0), wp[keep - 2:keep].flip(0)
+    assert torch.equal(raw(kv)[:keep], want[:keep]) and d.tolist() == [keep]
+    assert torch.equal(w[:keep], ww[:keep]) and torch.equal(p[:keep], wp[:keep])
