@@ -34,10 +34,10 @@
 //
 // Bound: the tensor cores (an M128 N128 K16 MMA of a pair takes 32 cycles, N256 64;
 // a tile 2200), fed at 140 KB per tile and CTA.  Measured: 64 drafts x 128 heads over
-// 65536 rows 635 us, 1840 TFLOP/s or 0.95 of cuBLAS's burst rate, while the clock
-// holds; 16 ragged requests of 5 x 128 262 us, 1460 TFLOP/s (DRAM re-reads
+// 65536 rows 630 us, 1860 TFLOP/s or 0.95 of cuBLAS's burst rate, while the clock
+// holds; 16 ragged requests of 5 x 128 262 us, 1470 TFLOP/s (DRAM re-reads
 // of row blocks that drift apart); 16 x 16 over 131072 rows 61 us; 8 x 16 over 248
-// rows 11.5 us, of which the two kernels' launches, set-up and merge are 10.
+// rows 11.8 us, of which the two kernels' launches, set-up and merge are 10.
 //
 // Warps of a CTA: 0-7 softmax and epilogue, 8 TMA of Q and K, 9 MMA issue (even
 // CTA; the odd one's writes empty requests) and tensor memory, 10 TMA of V.

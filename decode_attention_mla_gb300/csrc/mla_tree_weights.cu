@@ -22,7 +22,7 @@
 // Measured: one query block over 131072 rows 26 us, 5.8 TB/s of cache; 8 requests
 // of 8192 .. 131072 rows with 256 query rows 122 us, 6.1 TB/s and 1550 TFLOP/s at
 // once; 1024 query rows over 131072 105 us, 1470 TFLOP/s; 16 query rows over 8192
-// rows 8.6 us, most of it launch and set-up.
+// rows 7.0 us, most of it launch and set-up.
 //
 // Warps of a CTA: 0-7 weights (warps w and w + 4 share cache rows and split the
 // columns), 8 TMA of K, 9 MMA issue (even CTA) and tensor memory, 10 TMA of Q.
