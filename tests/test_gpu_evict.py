@@ -204,3 +204,21 @@ def test_captured_behind_copies(n, keep):
     ww[keep - 2:keep], wp[keep - 2:keep] = ww[keep - 2:keep].flip(0), wp[keep - 2:keep].flip(0)
     assert torch.equal(raw(kv)[:keep], want[:keep]) and d.tolist() == [keep]
     assert torch.equal(w[:keep], ww[:keep]) and torch.equal(p[:keep], wp[:keep])
+
+
+def test_two_evictions_at_once():
+    runs = []
+    for n, keep in ((30000, 9000), (12000, 5000)):
+        kv = cache(n, False, 576, seed=n)
+        g = torch.Generator(device="cuda").manual_seed(n)
+        w, p = torch.rand(n, generator=g, device="cuda"), torch.randperm(n, device="cuda").int()
+        want, ww, wp = reference(kv, w, p, [n], [0], keep, 4, 64, [n])
+        runs.append((kv, w, p, ints([n]), ints([n]), keep, mla.evict_alloc_scratch(batch=1, keep=keep),
+                     torch.cuda.Stream(), want, ww, wp))
+    torch.cuda.synchronize()
+    for kv, w, p, d, nxt, keep, scratch, s, *_ in runs:
+        mla.evict(kv, w, p, scratch, d_pos=d, next_pos=nxt, keep=keep, sink=4, recent=64, stream=s)
+    torch.cuda.synchronize()
+    for kv, w, p, d, _, keep, _, _, want, ww, wp in runs:
+        assert torch.equal(raw(kv), want) and d.tolist() == [keep]
+        assert torch.equal(w[:keep], ww[:keep]) and torch.equal(p[:keep], wp[:keep])

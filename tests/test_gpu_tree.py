@@ -206,6 +206,14 @@ def test_negative_row_offset_starts_inside_the_request():
     c.check(*c.run())
 
 
+def test_requests_over_the_same_rows():
+    # reading only, so requests may share cache rows: one prefix, two of their own lengths
+    c = Case(20, [700, 700, 260], 5, 16, offsets=[3, 3, 3])
+    c.kv = c.kv.nan_to_num(0.25)
+    c.d["kv"].copy_(c.kv)
+    c.check(*c.run())
+
+
 def test_offsets_at_which_no_row_can_lie_inside():
     c = Case(12, [30, 30, 30, 100], 4, 16)
     c.d["d_pos"] = torch.tensor([2**31 - 1, 50, 2**31 - 1, 100], dtype=torch.int32, device="cuda")
