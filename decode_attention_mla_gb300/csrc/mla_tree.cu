@@ -15,10 +15,13 @@ constexpr int kTreeMagic = 0x4d4c5431;                     // "MLT1"
 bool off(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to != 0; }
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
+// The caller's scale in base-2 units, as the kernels take it.
+float scale_log2(float scale) { return static_cast<float>(scale * 1.4426950408889634); }
+
 int check_shape(const mla_tree_shape* s) {
     if (!s) return MLA_EINVAL;
     if (s->batch < 1 || s->batch > 4096 || s->tokens < 1 || s->tokens > MLA_TREE_MAX_TOKENS) return MLA_EINVAL;
-    if (!(s->scale > 0.f) || !std::isfinite(s->scale * kLog2e)) return MLA_EINVAL;
+    if (!(s->scale > 0.f) || !std::isfinite(scale_log2(s->scale))) return MLA_EINVAL;
     if (s->num_sms < 0 || (s->pdl != 0 && s->pdl != 1) || (s->stall_test != 0 && s->stall_test != 1))
         return MLA_EINVAL;
     if (s->heads < 1 || s->heads > 128) return MLA_EUNSUPPORTED;
@@ -95,12 +98,6 @@ int q_tail(const mla_tree_plan_t* pl) {
     return rest ? rest : 64;
 }
 
-// The tensor cores' sums over 576 products are fp32, but each addition drops what
-// does not fit, towards zero: a score comes out smaller by 4.4e-7 of itself on average
-// (4.1e-7 .. 4.5e-7 for scores of deviation 0.5 .. 2; a score of 9 is off by 3.5e-6, an
-// fp32 product by 0.4e-6).  The scale gives it back: 1.1e-6 is left.
-constexpr double kScoreLoss = 4.4e-7;
-
 TreeParams params(const mla_tree_plan_t* pl, const mla_tree_args* a, void* scratch) {
     char* base = static_cast<char*>(scratch);
     TreeParams p{};
@@ -110,7 +107,7 @@ TreeParams params(const mla_tree_plan_t* pl, const mla_tree_args* a, void* scrat
     p.heads = pl->shape.heads;
     p.q_tail = q_tail(pl);
     p.clusters = pl->grid / 2;
-    p.scale_log2 = static_cast<float>(pl->shape.scale * 1.4426950408889634 * (1 + kScoreLoss));
+    p.scale_log2 = scale_log2(pl->shape.scale);
     p.merge = reinterpret_cast<TreeMerge*>(base + kMergeOffset);
     p.cut = reinterpret_cast<TreeCut*>(p.merge + kTreePieces * p.clusters);
     p.part = reinterpret_cast<float*>(base + pl->part_offset);

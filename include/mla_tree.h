@@ -13,6 +13,11 @@
  *
  * With one token and mask 1 this is mla_decode_forward's dense decode.
  *
+ * Products of q and k are exact; their fp32 sums (the tensor cores') drop what
+ * does not fit, towards zero: a score is within 2^-13 of the sum of its
+ * products' magnitudes, and exact where nothing is dropped.  With normal
+ * queries and rows scores come out smaller by about 4e-7 of themselves.
+ *
  * What a token does not attend does not reach its result, whatever it holds
  * (NaN and infinities too): rows behind the drafts, drafted rows its mask
  * leaves out, rows outside [0, kv_rows), rows t >= 2^31 - 256 of a request.

@@ -3,6 +3,7 @@ every call here is refused before anything is launched, or needs no device."""
 import ctypes
 import math
 
+import numpy as np
 import pytest
 
 import decode_attention_mla_gb300 as mla
@@ -99,6 +100,23 @@ def test_tree_plan_refusals(kw, status):
     with pytest.raises(mla.MLADecodeError) as e:
         tree_plan(**kw)
     assert e.value.status == status
+
+
+def test_every_scale_that_a_plan_takes_is_a_number_in_base_2():
+    """The kernels scale by float32(scale * log2 e): finite for the largest scale taken, infinite for the next."""
+    def taken(bits):
+        try:
+            tree_plan(scale=float(np.int32(bits).view(np.float32)))
+            return True
+        except mla.MLADecodeError:
+            return False
+    lo, hi = int(np.float32(2e38).view(np.int32)), int(np.float32(3e38).view(np.int32))
+    while hi - lo > 1:
+        mid = (lo + hi) // 2
+        lo, hi = (mid, hi) if taken(mid) else (lo, mid)
+    with np.errstate(over="ignore"):
+        in_base_2 = [np.float32(np.float64(np.int32(b).view(np.float32)) * math.log2(math.e)) for b in (lo, hi)]
+    assert np.isfinite(in_base_2[0]) and np.isinf(in_base_2[1])
 
 
 def test_tree_plan_layout():
