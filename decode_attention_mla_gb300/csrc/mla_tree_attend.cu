@@ -15,7 +15,9 @@
 //   PV: M = 128,                   N = 256 features (128 per CTA), K = 128 keys: 2 x 8 MMAs
 //
 // In tensor memory a row's 128 scores lie in two lanes (row, row + 64), 64 keys
-// each; O likewise, so two threads own a row and share only its reference m.
+// each, and warps w and w + 4 share lanes: four threads own a row, 32 keys each.  They
+// share the row's reference m (its maximum goes through shared memory when it moves)
+// and, at a block's end, its sum.
 //
 // Work split.  The units (request, row block, tile) are cut into equal runs, one
 // per pair, from the lengths on the device: no pair idles however ragged the batch.
@@ -43,8 +45,15 @@
 // CTA; the odd one's writes empty requests) and tensor memory, 10 TMA of V.
 // Barriers that the MMA warp waits on live in the even CTA and take arrivals of both.
 //
-// Rounding: P is rounded to bf16 for the product (relative 2^-8 at most per
-// probability, sums use the unrounded values), O and the statistics are fp32.
+// Rounding: O and the statistics are fp32, sums use the unrounded probabilities.  For
+// bf16 outputs P enters the product as one bf16: 2^-8 of a probability at most, and on
+// average over a row's keys no more than the rounding of the output.  For fp32 outputs
+// (kFp32) it enters as a pair, P_hi + P_lo, within 2^-16, as in the decode: a single bf16
+// leaves errors of up to 4e-3 over 2 .. 16 rows of normal values.  There is no room for a
+// second P, so P_lo takes the buffer once the product with P_hi has read it, and V stays
+// until both are done (bf16 / fp32 outputs: 8 x 16 query rows over 248 cache rows 11.9 / 12.8
+// us, 1 x 16 over 16384 16.9 / 18.8, 16 x 16 over 131072 63.5 / 82, 16 requests of 5 x 128
+// over 16384 240 / 367, 64 x 128 over 65536 650 / 1090).
 //
 // What a token does not attend must not reach it although the product runs over
 // whole tiles: masked scores become -infinity and P = 0, and in the tiles that
@@ -195,6 +204,11 @@ __device__ void produce(const TreeMaps& maps, const TreeParams& p, Shared& sh, u
 // barrier is looked at once before the MMAs that precede its use, so a phase
 // that is over by then costs nothing; and PV is a tile behind QK, so its
 // probabilities have had a tile's time.
+//
+// Phases of p_ready and o_done: one per tile, or (kFp32) two, of which P_hi's has
+// parity 0 and P_lo's parity 1.
+template <bool kFp32>
+constexpr int kParts = kFp32 ? 2 : 1;
 struct Issue {
     Shared& sh;
     bool lead, ok;
@@ -205,6 +219,7 @@ struct Issue {
     }
 };
 
+template <bool kFp32>
 __device__ void issue(const TreeParams& p, Shared& sh, uint32_t tmem) {
     constexpr uint32_t idesc_qk = make_idesc_bf16(128, 128, 0, 0);
     constexpr uint32_t idesc_pv = make_idesc_bf16(128, 256, 0, 1);
@@ -233,27 +248,33 @@ __device__ void issue(const TreeParams& p, Shared& sh, uint32_t tmem) {
         for (int turn = 0; turn < 2; ++turn) {
             if (turn == pv_turn) {
                 if (g == 0) continue;
-                is.need(see_p, &sh.p_ready, par ^ 1);
-                if (pv_first && ++pv_item > 0) is.need(false, &sh.o_free, (pv_item - 1) & 1);
-                tc_fence_after_sync();
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    is.need(see_v, &sh.v_ready[i], par ^ 1);
-                    if (i == 0)
-                        see_v = mbar_test(&sh.v_ready[1], par ^ 1);
-                    else
-                        see_k = mbar_test(&sh.k_ready[0], par ^ pv_turn);   // of the QK that comes next
-                    if (is.lead && is.ok) {
+                for (int part = 0; part < kParts<kFp32>; ++part) {   // P, or P_hi and P_lo
+                    constexpr int kLast = kParts<kFp32> - 1;
+                    is.need(see_p, &sh.p_ready, kFp32 ? part : par ^ 1);
+                    if (part == 0 && pv_first && ++pv_item > 0) is.need(false, &sh.o_free, (pv_item - 1) & 1);
+                    tc_fence_after_sync();
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            umma_pair_bf16(tmem + kTmemO + 128 * i, pd + (((k >> 2) * kChunkBytes + (k & 3) * 32u) >> 4),
-                                           vd + (((2 * i + (k >> 2)) * kSlotBytes + (k & 3) * 2048u) >> 4), idesc_pv,
-                                           k == 0 ? pv_first ^ 1u : 1u);
-                        umma_commit_pair(&sh.v_empty[i]);
+                    for (int i = 0; i < 2; ++i) {
+                        if (part == 0) is.need(see_v, &sh.v_ready[i], par ^ 1);
+                        if (part == 0 && i == 0)
+                            see_v = mbar_test(&sh.v_ready[1], par ^ 1);
+                        else if (part == kLast && i == 1)
+                            see_k = mbar_test(&sh.k_ready[0], par ^ pv_turn);   // of the QK that comes next
+                        if (is.lead && is.ok) {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                umma_pair_bf16(tmem + kTmemO + 128 * i,
+                                               pd + (((k >> 2) * kChunkBytes + (k & 3) * 32u) >> 4),
+                                               vd + (((2 * i + (k >> 2)) * kSlotBytes + (k & 3) * 2048u) >> 4), idesc_pv,
+                                               part == 0 && k == 0 ? pv_first ^ 1u : 1u);
+                            if (part == kLast) umma_commit_pair(&sh.v_empty[i]);
+                        }
                     }
+                    if (is.lead && is.ok) umma_commit_pair(&sh.o_done);
+                    see_p = false;
                 }
-                if (is.lead && is.ok) umma_commit_pair(&sh.o_done);
-                see_p = see_v = false;
+                see_v = false;
             } else {
                 if (g == total) continue;
                 const uint32_t d = tmem + kTmemS + 64 * buf;
@@ -266,7 +287,7 @@ __device__ void issue(const TreeParams& p, Shared& sh, uint32_t tmem) {
                     if (s < kSlots - 1) {
                         see_k = mbar_test(&sh.k_ready[s + 1], par);
                     } else if (pv_turn == 1 && g >= 1) {
-                        see_p = mbar_test(&sh.p_ready, par ^ 1);
+                        see_p = mbar_test(&sh.p_ready, kFp32 ? 0 : par ^ 1);
                         see_v = mbar_test(&sh.v_ready[0], par ^ 1);
                     }
                     if (is.lead && is.ok) {
@@ -369,6 +390,7 @@ __device__ __forceinline__ void store_rows(uint32_t stage, const uint32_t (&w)[1
 
 // Thread: 32 keys of one row.  Warps w and w + 4 share tensor-memory lanes 32 (w mod 4) ..
 // and split their columns.
+template <bool kFp32>
 __device__ void softmax(const TreeParams& p, Shared& sh, uint32_t tmem, uint32_t rank, int cluster, int tid) {
     const int lane = tid & 31, warp = tid >> 5;
     const int sub = warp >> 2, half = (warp >> 1) & 1;     // keys 64 half + 32 sub ..; features 256 sub + 128 half ..
@@ -438,18 +460,21 @@ __device__ void softmax(const TreeParams& p, Shared& sh, uint32_t tmem, uint32_t
             }
             const float base = m_ref > -INFINITY ? m_ref : 0.f;
             float sum[4] = {0.f, 0.f, 0.f, 0.f};
-            uint32_t pk[16];
+            uint32_t pk[16], rest[16];                     // (rest: kFp32 alone)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const float x = ex2_approx(fmaf(__uint_as_float(s[2 * i]), c2, -base));
                 const float y = ex2_approx(fmaf(__uint_as_float(s[2 * i + 1]), c2, -base));
                 sum[i & 1] += x;
                 sum[2 + (i & 1)] += y;
-                pk[i] = pack_bf16x2(x, y);
+                if constexpr (kFp32)
+                    split_bf16x2(x, y, pk[i], rest[i]);
+                else
+                    pk[i] = pack_bf16x2(x, y);
             }
             l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             // P of the tile before has been read, and O holds all tiles before this one
-            w = g == 0 || warp_wait(&sh.abort_flag, &sh.o_done, (g - 1) & 1);
+            w = g == 0 || warp_wait(&sh.abort_flag, &sh.o_done, kFp32 ? 1 : (g - 1) & 1);
             if (w && __any_sync(0xffffffffu, alpha != 1.f)) {   // (never on an item's first tile)
 #pragma unroll 1
                 for (int j = 0; j < 8; ++j) {
@@ -462,21 +487,32 @@ __device__ void softmax(const TreeParams& p, Shared& sh, uint32_t tmem, uint32_t
                 }
             }
             // ---- probabilities, bf16, K-major lines of 64 keys
+            auto store_p = [&](const uint32_t (&v)[16]) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-                st_shared_v4(p_line + (((4 * sub + u) ^ (row & 7)) << 4), pk[4 * u],
-                             pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
+                for (int u = 0; u < 4; ++u)
+                    st_shared_v4(p_line + (((4 * sub + u) ^ (row & 7)) << 4), v[4 * u], v[4 * u + 1], v[4 * u + 2],
+                                 v[4 * u + 3]);
+            };
+            auto hand_over = [&] {
+                fence_proxy_async_smem();
+                tc_fence_before_sync();
+                __syncwarp();
+                bad |= !w;                                 // the threads leave together at the next barrier
+                if (lane == 0 && !bad) mbar_arrive_peer(p_bar);
+            };
+            store_p(pk);
             if (c.special()) {
                 // V was loaded for this CTA's own eyes
                 w = w && warp_wait(&sh.abort_flag, &sh.v_local[specials & 1], (specials >> 1) & 1);
                 ++specials;
                 if (w) clean_v(sh, c, tid);
             }
-            fence_proxy_async_smem();
-            tc_fence_before_sync();
-            __syncwarp();
-            bad |= !w;                                     // the threads leave together at the next barrier
-            if (lane == 0 && !bad) mbar_arrive_peer(p_bar);
+            hand_over();
+            if (kFp32 && !bad) {
+                w = warp_wait(&sh.abort_flag, &sh.o_done, 0);   // P_hi has been read
+                store_p(rest);
+                hand_over();
+            }
             c.next(p);
         } while (!last);
         if (!ok) break;
@@ -506,7 +542,7 @@ __device__ void softmax(const TreeParams& p, Shared& sh, uint32_t tmem, uint32_t
             p.merge[at] = TreeMerge{b, rb, rows | place << 16, pieces};
             if (cut) p.cut[at] = of;
         }
-        const bool w = warp_wait(&sh.abort_flag, &sh.o_done, (c.g - 1) & 1);
+        const bool w = warp_wait(&sh.abort_flag, &sh.o_done, kFp32 ? 1 : (c.g - 1) & 1);
         if (named_barrier_or(kBarSoftmax, kSoftmaxThreads, !w)) {
             ok = false;
             break;
@@ -520,7 +556,7 @@ __device__ void softmax(const TreeParams& p, Shared& sh, uint32_t tmem, uint32_t
                         piece_quad(slot, static_cast<int>(rank) * 64 + row_w, f0 / 4) + lane;
         char* out = static_cast<char*>(p.a.out) +
                     ((static_cast<long long>(b) * p.tokens * p.heads + r - row + row_w) * kDLatent + f0) *
-                        (p.a.out_fp32 ? 4 : 2);
+                        (kFp32 ? 4 : 2);
 #pragma unroll 1
         for (int j = 0; j < 4 && n_rows > 0; ++j) {        // (the merge reads groups with live rows only)
             uint32_t o[32];
@@ -535,7 +571,7 @@ __device__ void softmax(const TreeParams& p, Shared& sh, uint32_t tmem, uint32_t
                 continue;
             }
             uint32_t x[16];
-            if (!p.a.out_fp32) {
+            if constexpr (!kFp32) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     x[i] = pack_bf16x2(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
@@ -572,6 +608,7 @@ __device__ void write_empty(const TreeParams& p, int cluster, int clusters, int 
     }
 }
 
+template <bool kFp32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mla_tree_attend_kernel(const __grid_constant__ TreeMaps maps, const __grid_constant__ TreeParams p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -627,11 +664,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lane == 0) produce(maps, p, sh, rank, true);
     } else if (warp == kMmaWarp) {
         if (rank == 0)
-            issue(p, sh, tmem);
+            issue<kFp32>(p, sh, tmem);
         else
             write_empty(p, cluster, p.clusters, lane);
     } else {
-        softmax(p, sh, tmem, rank, cluster, tid);
+        softmax<kFp32>(p, sh, tmem, rank, cluster, tid);
     }
     __syncthreads();
     if (*static_cast<volatile int*>(&sh.abort_flag)) {
@@ -857,8 +894,12 @@ __global__ void __launch_bounds__(32 * kMergeWarps) mla_tree_merge_kernel(const 
 }  // namespace
 
 cudaError_t tree_attend_prepare() {
-    return cudaFuncSetAttribute(mla_tree_attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(sizeof(Shared)));
+    for (auto kernel : {mla_tree_attend_kernel<false>, mla_tree_attend_kernel<true>}) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sizeof(Shared)));
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 cudaError_t launch_tree_attend(const TreeMaps& maps, const TreeParams& p, bool pdl, cudaStream_t stream) {
@@ -872,7 +913,8 @@ cudaError_t launch_tree_attend(const TreeMaps& maps, const TreeParams& p, bool p
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, mla_tree_attend_kernel, maps, p);
+    cudaError_t e =
+        cudaLaunchKernelEx(&cfg, p.a.out_fp32 ? mla_tree_attend_kernel<true> : mla_tree_attend_kernel<false>, maps, p);
     if (e != cudaSuccess) return e;
     // shared row blocks: no more than there are row blocks or notes, and without
     // segments (one block per request) at most one per run

@@ -11,7 +11,8 @@
  *     s_t = (q_lat . c_t + q_rope . k_rope_t) * scale
  *     lse = ln sum_t exp(s_t),     out = sum_t exp(s_t - lse) c_t
  *
- * With one token and mask 1 this is mla_decode_forward's dense decode.
+ * With one token and mask 1 this is mla_decode_forward's dense decode (with
+ * fp32 outputs within its error, too).
  *
  * Products of q and k are exact; their fp32 sums (the tensor cores') drop what
  * does not fit, towards zero: a score is within 2^-13 of the sum of its
@@ -74,9 +75,9 @@ typedef struct {
                                     n_tokens[b] are ignored */
     const int *n_tokens;         /* (device) int32 [B], clamped to 0 .. Q; NULL = Q for every request */
     void *out;                   /* (device) bf16 or fp32 [B][Q][heads][512], 16-byte aligned */
-    int out_fp32;                /* 1 = fp32 outputs (e.g. for mla_decode_project).  Probabilities enter the
-                                    product as bf16 either way: relative error up to 2^-8 before the rounding
-                                    of a bf16 output */
+    int out_fp32;                /* 1 = fp32 outputs (e.g. for mla_decode_project): probabilities enter the product
+                                    in 16 bits and more, as in the decode.  0 = bf16 outputs: they enter as one
+                                    bf16 each (2^-8), which over few rows can show beside the output's own rounding */
     float *lse;                  /* (device) fp32 [B][Q][heads], natural log */
 } mla_tree_args;
 

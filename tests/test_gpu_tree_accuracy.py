@@ -12,6 +12,8 @@ import torch
 
 import decode_attention_mla_gb300 as mla
 import _tree_ref as ref
+import workloads
+from _gpu import assert_parity, oracle_dense
 
 pytestmark = pytest.mark.gpu
 U = 2.0 ** -24
@@ -117,3 +119,51 @@ def test_the_largest_scale_is_a_number():
         assert (lse[0, i].double() - math.log(18 + i)).abs().max() <= 2.0 ** -20
     assert (out - 1).abs().max() <= 2.0 ** -20
     assert abs(float(w.double().sum()) - 15) <= 15 * 2.0 ** -18
+
+
+# ---- fp32 outputs ---------------------------------------------------------------
+@pytest.mark.parametrize("H", [16, 128])
+@pytest.mark.parametrize("T", [1, 2, 3, 5, 16, 64, 129, 256, 1000])
+def test_one_token_meets_the_dense_decodes_bar(T, H):
+    """One drafted token is the dense decode: the same inputs, oracle and bar."""
+    for seed in range(3):
+        x = workloads.dense(1, H, T, seed=100 * T + seed)
+        p = mla.tree_plan(batch=1, tokens=1, heads=H, scale=x.scale)
+        scratch = mla.tree_alloc_scratch(p)
+        out, lse = torch.empty(1, 1, H, 512, device="cuda"), torch.empty(1, 1, H, device="cuda")
+        mla.tree_forward(p, x.q.cuda()[:, None].contiguous(), x.kv.cuda(), out, lse, scratch, d_pos=x.d_pos.int().cuda())
+        assert_parity(out[:, 0], lse[:, 0], *oracle_dense(x), what=f"T={T}, H={H}, seed {seed}")
+
+
+@pytest.mark.parametrize("num_sms", [0, 2, 6])
+@pytest.mark.parametrize("lens,Q,H", [([3], 2, 16), ([0, 40, 7], 9, 16), ([300, 1, 128], 5, 33), ([500], 64, 16),
+                                      ([700, 90], 3, 128)])
+def test_fp32_outputs_of_exact_scores(lens, Q, H, num_sms):
+    """Probabilities enter the product with V in 16 bits and more."""
+    g = torch.Generator().manual_seed(Q + H)
+    B, offs = len(lens), [sum(lens[:b]) + b * Q for b in range(len(lens))]
+    rows = sum(lens) + B * Q
+    kv = torch.randn(rows, 576, generator=g).bfloat16()
+    kv[:, 570] = torch.randint(-40, 41, (rows,), generator=g).bfloat16()
+    q = torch.zeros(B, Q, H, 576, dtype=torch.bfloat16)
+    q[..., 570] = torch.tensor([2.0 ** -(h % 3) for h in range(H)]).bfloat16()
+    p = mla.tree_plan(batch=B, tokens=Q, heads=H, scale=0.1, num_sms=num_sms)
+    scratch = mla.tree_alloc_scratch(p)
+    out, lse = torch.empty(B, Q, H, 512, device="cuda"), torch.empty(B, Q, H, device="cuda")
+    mla.tree_forward(p, q.cuda(), kv.cuda(), out, lse, scratch, d_pos=ints(lens), row_offset=ints(offs, torch.int64))
+    assert mla.status_word(p, scratch) == 0
+    for b in range(B):
+        for i in range(Q):
+            n = lens[b] + i + 1
+            k = kv[offs[b]:offs[b] + n].double()
+            s = q[b, i].double() @ k.T * f32(0.1)
+            rl = torch.logsumexp(s, 1)
+            prob = torch.exp(s - rl[:, None])
+            want, spread = prob @ k[:, :512], prob @ k[:, :512].abs()
+            # a probability: its exponent (5 U of the largest |s|), exponential and reference 2^-20, the
+            # pair of bf16 numbers 2^-16; sums over 2 n products drop 2^-23 each; l likewise over n; pieces
+            # are joined with weights within 2^-20
+            rel = 2 * (5 * U * s.abs().amax(1) + 2.0 ** -20) + 2.0 ** -16 + 3 * n * 2.0 ** -23 + 2.0 ** -20
+            err = (out[b, i].double().cpu() - want).abs()
+            assert (err <= rel[:, None] * spread).all(), (b, i, float((err / spread).max()), float(rel.max()))
+            assert ((lse[b, i].double().cpu() - rl).abs() <= 5 * U * s.abs().amax(1) + 2.0 ** -19 + n * U).all()
