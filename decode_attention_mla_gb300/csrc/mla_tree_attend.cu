@@ -203,7 +203,8 @@ __device__ void produce(const TreeMaps& maps, const TreeParams& p, Shared& sh, u
 // MMA took 100 cycles to issue, instead of the 32 or 64 that it runs); each
 // barrier is looked at once before the MMAs that precede its use, so a phase
 // that is over by then costs nothing; and PV is a tile behind QK, so its
-// probabilities have had a tile's time.
+// probabilities have had a tile's time.  A buffer is announced as free only to a load that
+// will wait for it: no barrier orders the arrival of a commit with the end of the other CTA.
 //
 // Phases of p_ready and o_done: one per tile, or (kFp32) two, of which P_hi's has
 // parity 0 and P_lo's parity 1.
@@ -268,7 +269,7 @@ __device__ void issue(const TreeParams& p, Shared& sh, uint32_t tmem) {
                                                pd + (((k >> 2) * kChunkBytes + (k & 3) * 32u) >> 4),
                                                vd + (((2 * i + (k >> 2)) * kSlotBytes + (k & 3) * 2048u) >> 4), idesc_pv,
                                                part == 0 && k == 0 ? pv_first ^ 1u : 1u);
-                            if (part == kLast) umma_commit_pair(&sh.v_empty[i]);
+                            if (part == kLast && g < total) umma_commit_pair(&sh.v_empty[i]);
                         }
                     }
                     if (is.lead && is.ok) umma_commit_pair(&sh.o_done);
@@ -303,12 +304,12 @@ __device__ void issue(const TreeParams& p, Shared& sh, uint32_t tmem) {
                                 umma_pair_bf16(d, q + ((8 * kChunkBytes + k * 32u) >> 4), rope + (k * 32u >> 4), idesc_qk,
                                                1u);
                         }
-                        umma_commit_pair(&sh.k_empty[s]);
+                        if (g + 1 < total) umma_commit_pair(&sh.k_empty[s]);
                     }
                 }
                 if (is.lead && is.ok) {
                     umma_commit_pair(&sh.s_full[buf]);
-                    if (last) umma_commit_pair(&sh.q_empty);
+                    if (last && g + 1 < total) umma_commit_pair(&sh.q_empty);
                 }
                 see_k = false;
                 first = last;
@@ -587,8 +588,8 @@ __device__ void softmax(const TreeParams& p, Shared& sh, uint32_t tmem, uint32_t
         }
         tc_fence_before_sync();
         __syncwarp();
-        // O may be overwritten.  (Only if something will wait for it: no arrival may be on
-        // its way to a CTA that has left, and the closing barrier orders none.)
+        // O may be overwritten.  (Only if something will wait for it, as for the buffers: the
+        // closing barrier orders no arrival.)
         if (lane == 0 && c.left > 0) mbar_arrive_peer(o_bar);
     }
     if (!ok && lane == 0) raise_tree_error(&sh.abort_flag, p.status);

@@ -169,7 +169,9 @@ __device__ void produce_q(const TreeMaps& maps, const TreeParams& p, Shared<kBlo
 }
 
 // The whole warp walks and waits, one lane issues; barriers are looked at ahead
-// of the MMAs before their use (a look never blocks).
+// of the MMAs before their use (a look never blocks).  A buffer is announced as free only
+// to a load that will wait for it: the closing barrier orders what threads did, not the
+// arrival of a commit, and the odd CTA may be gone by then.
 template <int kBlocks>
 __device__ void issue(const TreeParams& p, Shared<kBlocks>& sh, uint32_t tmem) {
     using C = Cfg<kBlocks>;
@@ -188,6 +190,7 @@ __device__ void issue(const TreeParams& p, Shared<kBlocks>& sh, uint32_t tmem) {
     Cursor c;
     for (c.start(p, sh.work); c.left > 0 && ok; c.next(p)) {
         const int blocks = query_blocks(p, c.r);
+        const bool more = c.left > 1;                      // tiles of the run
         if constexpr (C::kStream) {
             for (int rb = 0; rb < blocks && ok; ++rb, ++n) {
                 const uint32_t buf = n & 1, q_par = n & 1;
@@ -204,8 +207,8 @@ __device__ void issue(const TreeParams& p, Shared<kBlocks>& sh, uint32_t tmem) {
                         for (int k = 0; k < 4; ++k)
                             umma_pair_bf16(d, kd + ((s * kKChunkBytes + k * 32u) >> 4),
                                            qd + ((s * kQChunkBytes + k * 32u) >> 4), idesc, (s | k) ? 1u : 0u);
-                        umma_commit_pair(&sh.q_empty[s]);
-                        if (rb == blocks - 1) umma_commit_pair(&sh.k_empty[s]);
+                        if (more || rb < blocks - 1) umma_commit_pair(&sh.q_empty[s]);
+                        if (more && rb == blocks - 1) umma_commit_pair(&sh.k_empty[s]);
                     }
                 }
                 see_q = false;
@@ -237,12 +240,13 @@ __device__ void issue(const TreeParams& p, Shared<kBlocks>& sh, uint32_t tmem) {
                                                qd + ((rb * kQBlockBytes + s * kQChunkBytes + k * 32u) >> 4), idesc,
                                                (s | k) ? 1u : 0u);
                         }
-                    umma_commit_pair(&sh.k_empty[at]);
+                    // (the slot's next load is kKSlots loads on)
+                    if (kChunks * c.left - 1 - s >= C::kKSlots) umma_commit_pair(&sh.k_empty[at]);
                 }
             }
             if (lead && ok) {
                 umma_commit_pair(&sh.s_full[buf]);
-                if (c.last()) umma_commit_pair(&sh.q_empty[0]);
+                if (c.last() && more) umma_commit_pair(&sh.q_empty[0]);
             }
             if (c.last()) ++q_round;
             ++n;
@@ -419,7 +423,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     }
     tc_fence_before_sync();
-    cluster_barrier();                                     // orders the last arrivals at the other CTA, too
+    cluster_barrier();                                     // orders the threads' last arrivals (s_free), too
     if (warp == kMmaWarp) {
         tc_fence_after_sync();
         tmem_dealloc_pair(tmem, kTmemCols);
