@@ -63,7 +63,7 @@ def tree(q, kv, *, d_pos, row_offset, n_tokens, bits, scale, kv_rows=None):
 
 
 def weights(q, kv, lse, old, *, d_pos, row_offset, n_tokens, bits, scale, decay, kv_rows=None):
-    """New weights and their bounds (entries that are not touched: old, bound 0)."""
+    """New weights and their bounds (entries that are not touched: old, and a bound all the same)."""
     B, Q, H, _ = q.shape
     kv_rows = kv_rows or kv.shape[0]
     new, tol = old.double().clone(), torch.zeros(old.shape, dtype=torch.float64)

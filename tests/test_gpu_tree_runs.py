@@ -7,7 +7,7 @@ import torch
 
 import decode_attention_mla_gb300 as mla
 import _tree_ref as ref
-from test_gpu_tree import Case
+from test_gpu_tree import SCALE, Case
 
 pytestmark = pytest.mark.gpu
 NAN = float("nan")
@@ -48,3 +48,68 @@ def test_calls_one_behind_the_other(lens, Q, H, num_sms, dtype):
     assert mla.status_word(p, scratch) == 0
     for a, b in zip(first, (out, lse, w)):
         assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+def touched_rows(c):
+    """Entries of the weights that a call writes (its rows inside the cache), from the definition."""
+    touched = torch.zeros(c.kv.shape[0], dtype=torch.bool)
+    for b in range(c.B):
+        if c.lens[b] >= 0:
+            lo, hi = max(c.offs[b], 0), min(c.offs[b] + c.lens[b] + c.n[b], c.kv_rows)
+            touched[lo:hi] = True
+    return touched
+
+
+@pytest.mark.parametrize("decay", [0.0, 0.5, 1.0])
+@pytest.mark.parametrize("lens,Q,H,n", [([600], 8, 33, [5]), ([260, 0, -1, 64, 1000], 5, 16, [5, 5, 5, 0, 3]),
+                                        ([300, 128], 2, 128, [1, 2]), ([255, 400], 5, 128, [5, 4])])
+def test_entries_of_other_rows_keep_their_bits(lens, Q, H, n, decay):
+    c = Case(90 + Q + H, lens, Q, H, n_tokens=n, mask="random")
+    c.kv_rows -= 2 if n[-1] == Q else 0                     # the last request's last rows lie outside
+    touched = touched_rows(c)
+    assert not touched.all() and (~touched).sum() >= 3
+    old = torch.rand(c.kv.shape[0], generator=torch.Generator().manual_seed(1))
+    old[~touched] = torch.tensor([NAN, -0.0, math.inf, -3.0]).repeat(old.numel())[:int((~touched).sum())]
+    out, lse = c.run()
+    w = old.cuda()
+    p = c.plan()
+    mla.tree_weights(p, c.d["q"], c.d["kv"], lse, mla.tree_alloc_scratch(p), w, decay=decay, **c.kw())
+    w = w.cpu()
+    assert torch.equal(w[~touched].view(torch.int32), old[~touched].view(torch.int32))
+    new, tol = ref.weights(c.q, c.kv, lse.cpu(), old.nan_to_num(0, 0, 0), d_pos=c.lens, row_offset=c.offs, n_tokens=c.n,
+                           bits=c.bits, scale=SCALE, decay=decay, kv_rows=c.kv_rows)
+    assert ((w.double() - new).abs() <= tol)[touched].all()
+
+
+def test_a_wait_that_runs_out_with_fp32_outputs():
+    c = Case(61, [3000, 50], 8, 16)
+    bad, good = c.plan(stall_test=True), c.plan()
+    scratch = mla.tree_alloc_scratch(bad)
+    out, lse = c.outputs(torch.float32)
+    args = mla.tree_make_args(c.d["q"], c.d["kv"], out, lse, **c.kw())
+    mla.tree_forward_args(bad, args, scratch)
+    torch.cuda.synchronize()
+    assert mla.status_word(bad, scratch) == mla.EDEVICE
+    mla.scratch_init(scratch)
+    mla.tree_forward_args(good, args, scratch)
+    torch.cuda.synchronize()
+    assert mla.status_word(good, scratch) == 0
+    c.check(out, lse)
+
+
+@pytest.mark.parametrize("bad", [NAN, math.inf])
+def test_non_finite_drafts_with_fp32_outputs(bad):
+    """Only token 3 attends the broken draft 3; committed rows fill part of the drafts' tile and all of it."""
+    for rows in (140, 256, 0):
+        c = Case(12, [rows], 8, 16, mask="none")
+        c.bits = [[1 << i for i in range(8)]]
+        c.d["mask"] = torch.tensor(c.bits, dtype=torch.int64, device="cuda")
+        c.d["kv"][c.offs[0] + rows + 3, 100:140] = bad
+        c.d["q"][:, :, :, 100:140] = abs(c.d["q"][:, :, :, 100:140])
+        c.q = c.d["q"].cpu()
+        want = c.reference()
+        del want[0, 3]
+        out, lse = c.run(torch.float32)
+        assert torch.isnan(out[0, 3]).all()
+        out[0, 3], lse[0, 3] = 7, 7
+        c.check(out, lse, want)
