@@ -433,6 +433,14 @@ def _quick(t, name, dtype, shape, device):
     return _need(t, name, dtype, shape)
 
 
+def _int(v, name):
+    """An int argument: a C int would take a larger one modulo 2^32."""
+    v = int(v)
+    if not -2 ** 31 <= v < 2 ** 31:
+        raise ValueError(f"{name} = {v} is no 32-bit integer")
+    return v
+
+
 def _maybe(t, name, dtypes, shape):
     return None if t is None else _need(t, name, dtypes, shape)
 
@@ -496,7 +504,7 @@ def rope_turns(rot_dim: int = D_ROPE, base: float = 10000.0, *, scaling: str = "
     """``mla_rope_table``: angle per position of each pair, as 64-bit fractions of a turn (host integers)."""
     if scaling not in ROPE_SCALING:
         raise ValueError(f"scaling must be one of {sorted(ROPE_SCALING)}")
-    spec = RopeSpec(rot_dim=rot_dim, scaling=ROPE_SCALING[scaling], base=base, factor=factor,
+    spec = RopeSpec(rot_dim=_int(rot_dim, "rot_dim"), scaling=ROPE_SCALING[scaling], base=base, factor=factor,
                     original_ctx=original_ctx, beta_fast=beta_fast, beta_slow=beta_slow)
     buf = (ctypes.c_ulonglong * 32)()
     _check(lib().mla_rope_table(ctypes.byref(spec), buf), "mla_rope_table")
@@ -583,8 +591,8 @@ def rope_append(table: RopeTable, positions, *, stream=None, **kw) -> None:
 def tree_plan(*, batch: int, tokens: int, heads: int, scale: float, num_sms: int = 0, pdl: bool = False,
               stall_test: bool = False) -> TreePlan:
     """``mla_tree_plan``: up to ``tokens`` (<= 64) drafted tokens per request."""
-    s = TreeShape(batch=batch, tokens=tokens, heads=heads, scale=scale, num_sms=num_sms, pdl=int(bool(pdl)),
-                  stall_test=int(bool(stall_test)))
+    s = TreeShape(batch=_int(batch, "batch"), tokens=_int(tokens, "tokens"), heads=_int(heads, "heads"), scale=scale,
+                  num_sms=_int(num_sms, "num_sms"), pdl=int(bool(pdl)), stall_test=int(bool(stall_test)))
     p = TreePlan()
     _check(lib().mla_tree_plan(ctypes.byref(s), ctypes.byref(p)), "mla_tree_plan")
     return p
@@ -678,7 +686,7 @@ def tree_commit(kv, accept, n_accept, *, d_pos, d_pos_out=None, row_offset=None,
 def evict_alloc_scratch(*, batch: int, keep: int, device=None):
     """Scratch of :func:`evict` for a batch and a budget."""
     torch = _torch or _tc()
-    n = int(lib().mla_evict_scratch_bytes(batch, keep))
+    n = int(lib().mla_evict_scratch_bytes(_int(batch, "batch"), _int(keep, "keep")))
     if n == 0:
         raise ValueError("batch must be 1 .. 65535 and keep at least 1")
     return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
@@ -696,8 +704,9 @@ def evict_make_args(kv, weights, positions, *, d_pos, next_pos, keep: int, sink:
     wo = weights if weights_out is None else weights_out
     po = positions if positions_out is None else positions_out
     do = d_pos if d_pos_out is None else d_pos_out
-    a = EvictArgs(kv=kvp, kv_rows=rows, row_stride=stride, kv_fp8=fp8, batch=B, keep=int(keep), sink=int(sink),
-                  recent=int(recent), max_rows=int(min(rows, 0x7fffffff) if max_rows is None else max_rows),
+    a = EvictArgs(kv=kvp, kv_rows=rows, row_stride=stride, kv_fp8=fp8, batch=B, keep=_int(keep, "keep"),
+                  sink=_int(sink, "sink"), recent=_int(recent, "recent"),
+                  max_rows=min(rows, 0x7fffffff) if max_rows is None else _int(max_rows, "max_rows"),
                   weights=_side(weights, "weights", torch.float32, rows),
                   positions=_side(positions, "positions", torch.int32, rows),
                   d_pos=_need(d_pos, "d_pos", torch.int32, (B,)),

@@ -34,12 +34,12 @@ typedef struct {
     const int *positions;        /* (device) int32 [kv_rows] */
     const int *d_pos;            /* (device) int32 [B] rows of each request (clamped to the rows inside
                                     [0, kv_rows); negative = none) */
-    const int *next_pos;         /* (device) int32 [B]: position of the next token */
+    const int *next_pos;         /* (device) int32 [B]: position of the next token; may be d_pos */
     const long long *row_offset; /* (device) int64 [B], >= 0; may be NULL for a batch of 1 */
     float *weights_out;          /* (device) fp32 [kv_rows]: may be `weights`, else no overlap with it; the
                                     first min(n, keep) entries of each request are written */
     int *positions_out;          /* (device) int32 [kv_rows], likewise */
-    int *d_pos_out;              /* (device) int32 [B]: min(n, keep); may be d_pos */
+    int *d_pos_out;              /* (device) int32 [B]: min(n, keep), 0 for a negative d_pos; may be d_pos */
 } mla_evict_args;
 
 /* Scratch bytes of a call (256-byte aligned device memory, no initial value;

@@ -222,3 +222,24 @@ def test_two_evictions_at_once():
     for kv, w, p, d, _, keep, _, _, want, ww, wp in runs:
         assert torch.equal(raw(kv), want) and d.tolist() == [keep]
         assert torch.equal(w[:keep], ww[:keep]) and torch.equal(p[:keep], wp[:keep])
+
+
+@pytest.mark.parametrize("name", ["keep", "sink", "recent", "max_rows"])
+def test_integers_past_32_bits_are_refused(name):
+    kv, w, p, d = cache(40, False, 576), torch.rand(40, device="cuda"), ints(list(range(40))), ints([30])
+    with pytest.raises(ValueError, match="32-bit"):
+        mla.evict_make_args(kv, w, p, d_pos=d, next_pos=ints([30]), **{"keep": 20, name: 2 ** 32 + 5})
+
+
+@pytest.mark.parametrize("n,keep", [(3000, 1100), (20000, 9000), (60, 90)])
+def test_next_positions_in_the_tensor_that_is_rewritten(n, keep):
+    """Before the first eviction the next position is the number of rows: one tensor may be both, in place."""
+    kv = cache(n, False, 576)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    w, p = torch.rand(n, generator=g, device="cuda"), torch.arange(n, dtype=torch.int32, device="cuda")
+    want, ww, wp = reference(kv, w, p, [n], [0], keep, 4, 50, [n])
+    d = ints([n])
+    mla.evict(kv, w, p, mla.evict_alloc_scratch(batch=1, keep=keep), d_pos=d, next_pos=d, keep=keep, sink=4, recent=50)
+    k = min(n, keep)
+    assert torch.equal(raw(kv), want) and d.tolist() == [k]
+    assert torch.equal(w[:k], ww[:k]) and torch.equal(p[:k], wp[:k])

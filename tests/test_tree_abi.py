@@ -248,3 +248,14 @@ def test_packed_commit_arguments_have_the_structures_layout():
     v = list(range(1, 14))
     a = mla.TreeCommitArgs(*v)
     assert mla._COMMIT_ARGS.size == ctypes.sizeof(a) and mla._COMMIT_ARGS.pack(*v) == bytes(a)
+
+
+@pytest.mark.parametrize("call", [
+    lambda big: tree_plan(batch=big), lambda big: tree_plan(tokens=big), lambda big: tree_plan(heads=big),
+    lambda big: tree_plan(num_sms=big), lambda big: mla.rope_turns(big), lambda big: mla._int(-big, "x"),
+    lambda big: mla.evict_alloc_scratch(batch=big, keep=4), lambda big: mla.evict_alloc_scratch(batch=1, keep=big),
+])
+def test_integers_past_32_bits_are_refused(call):
+    """A C int would take them modulo 2^32: 2^32 + 8 rows to keep would be 8."""
+    with pytest.raises(ValueError, match="32-bit"):
+        call(2 ** 32 + 8)
