@@ -72,6 +72,7 @@ class RopeSpec(ctypes.Structure):
 
 
 class RopeArgs(ctypes.Structure):
+    _device = None                     # device of the tensors, where a *_make_args call has checked them
     _fields_ = [("batch", ctypes.c_int), ("tokens", ctypes.c_int), ("heads", ctypes.c_int), ("rot_dim", ctypes.c_int),
                 ("interleaved", ctypes.c_int), ("amplitude", ctypes.c_float), ("turns", ctypes.c_void_p),
                 ("positions", ctypes.c_void_p), ("n_tokens", ctypes.c_void_p),
@@ -99,6 +100,7 @@ class TreePlan(ctypes.Structure):
 
 
 class TreeArgs(ctypes.Structure):
+    _device = None                     # device of the tensors, where a *_make_args call has checked them
     _fields_ = [("q", ctypes.c_void_p), ("kv", ctypes.c_void_p), ("kv_rows", ctypes.c_longlong),
                 ("row_stride", ctypes.c_longlong), ("d_pos", ctypes.c_void_p), ("row_offset", ctypes.c_void_p),
                 ("mask", ctypes.c_void_p), ("n_tokens", ctypes.c_void_p), ("out", ctypes.c_void_p),
@@ -118,6 +120,7 @@ _COMMIT_ARGS = struct.Struct("Pqqiii0P7P")
 
 
 class EvictArgs(ctypes.Structure):
+    _device = None                     # device of the tensors, where a *_make_args call has checked them
     _fields_ = [("kv", ctypes.c_void_p), ("kv_rows", ctypes.c_longlong), ("row_stride", ctypes.c_longlong),
                 ("kv_fp8", ctypes.c_int), ("batch", ctypes.c_int), ("keep", ctypes.c_int), ("sink", ctypes.c_int),
                 ("recent", ctypes.c_int), ("max_rows", ctypes.c_int), ("weights", ctypes.c_void_p),
@@ -433,6 +436,22 @@ def _quick(t, name, dtype, shape, device):
     return _need(t, name, dtype, shape)
 
 
+def _scratch_here(scratch):
+    """Address and bytes of a call's scratch (CUDA, on the current device, contiguous)."""
+    torch = _torch or _tc()
+    if getattr(scratch, "is_cuda", False) and scratch.get_device() == torch.cuda.current_device() and (
+            scratch.is_contiguous()):
+        return scratch.data_ptr(), scratch.nbytes
+    return _need(scratch, "scratch", scratch.dtype if isinstance(scratch, torch.Tensor) else None), scratch.nbytes
+
+
+def _same_device(a):
+    """Arguments were checked against the device that was current when they were laid out."""
+    device = (_torch or _tc()).cuda.current_device()
+    if a._device is not None and a._device != device:
+        raise ValueError(f"arguments for device {a._device}, the current device is {device}")
+
+
 def _int(v, name):
     """An int argument: a C int would take a larger one modulo 2^32."""
     v = int(v)
@@ -560,6 +579,7 @@ def rope_make_args(table: RopeTable, positions, *, q_rope=None, q=None, c=None, 
         a.row_offset = _maybe(row_offset, "row_offset", torch.int64, (B,))
         a.row_positions = _side(row_positions, "row_positions", torch.int32, a.kv_rows)
         a.row_weights = _side(row_weights, "row_weights", torch.float32, a.kv_rows)
+    a._device = torch.cuda.current_device()
     a._keep = (table, positions, q_rope, q, c, k_rope, kv, d_pos, row_offset, n_tokens, row_positions, row_weights)
     return a
 
@@ -579,6 +599,7 @@ def _side(t, name, dtype, rows):
 
 def rope_append_args(a: RopeArgs, stream=None) -> None:
     """``mla_rope_append`` with prebuilt arguments."""
+    _same_device(a)
     _check(lib().mla_rope_append(ctypes.byref(a), _stream(stream)), "mla_rope_append")
 
 
@@ -622,13 +643,15 @@ def tree_make_args(q, kv, out, lse, *, d_pos, row_offset=None, mask=None, n_toke
                  out=_maybe(out, "out", (torch.bfloat16, torch.float32), (B, Q, H, D_LATENT)),
                  out_fp32=int(out is not None and out.dtype == torch.float32),
                  lse=_need(lse, "lse", torch.float32, (B, Q, H)))
+    a._device = torch.cuda.current_device()
     a._keep = (q, kv, d_pos, row_offset, mask, n_tokens, out, lse)
     a._dims = (int(B), int(Q), int(H))
     return a
 
 
 def _tree_dims(p: TreePlan, a: TreeArgs):
-    """The arguments' [B, Q, H] must be the plan's: the kernels index by the plan."""
+    """The arguments' [B, Q, H] must be the plan's (the kernels index by the plan), and on this device."""
+    _same_device(a)
     if a._dims != (p.shape.batch, p.shape.tokens, p.shape.heads):
         raise ValueError(f"arguments of shape {a._dims} for a plan of "
                          f"{(p.shape.batch, p.shape.tokens, p.shape.heads)}")
@@ -637,7 +660,7 @@ def _tree_dims(p: TreePlan, a: TreeArgs):
 def tree_forward_args(p: TreePlan, a: TreeArgs, scratch, stream=None) -> None:
     """``mla_tree_forward`` with prebuilt arguments."""
     _tree_dims(p, a)
-    sp, sb = _scratch_args(scratch)
+    sp, sb = _scratch_here(scratch)
     _check(lib().mla_tree_forward(ctypes.byref(p), ctypes.byref(a), sp, sb, _stream(stream)), "mla_tree_forward")
 
 
@@ -652,7 +675,7 @@ def tree_weights_args(p: TreePlan, a: TreeArgs, scratch, weights, *, decay: floa
     torch = _torch or _tc()
     _tree_dims(p, a)
     w = _side(weights, "weights", torch.float32, a.kv_rows)
-    sp, sb = _scratch_args(scratch)
+    sp, sb = _scratch_here(scratch)
     _check(lib().mla_tree_weights(ctypes.byref(p), ctypes.byref(a), w, float(decay), sp, sb, _stream(stream)),
            "mla_tree_weights")
 
@@ -715,13 +738,15 @@ def evict_make_args(kv, weights, positions, *, d_pos, next_pos, keep: int, sink:
                   weights_out=_side(wo, "weights_out", torch.float32, rows),
                   positions_out=_side(po, "positions_out", torch.int32, rows),
                   d_pos_out=_need(do, "d_pos_out", torch.int32, (B,)))
+    a._device = torch.cuda.current_device()
     a._keep = (kv, weights, positions, d_pos, next_pos, row_offset, wo, po, do)
     return a
 
 
 def evict_args(a: EvictArgs, scratch, stream=None) -> None:
     """``mla_evict`` with prebuilt arguments."""
-    sp, sb = _scratch_args(scratch)
+    _same_device(a)
+    sp, sb = _scratch_here(scratch)
     _check(lib().mla_evict(ctypes.byref(a), sp, sb, _stream(stream)), "mla_evict")
 
 

@@ -113,3 +113,51 @@ def test_non_finite_drafts_with_fp32_outputs(bad):
         assert torch.isnan(out[0, 3]).all()
         out[0, 3], lse[0, 3] = 7, 7
         c.check(out, lse, want)
+
+
+class Elsewhere:
+    """A tensor that says it is on another device."""
+
+    def __init__(self, t):
+        self.t, self.is_cuda, self.dtype, self.nbytes = t, True, t.dtype, t.nbytes
+
+    def get_device(self):
+        return self.t.get_device() + 1
+
+    def is_contiguous(self):
+        return True
+
+
+def test_scratch_and_arguments_of_another_device_are_refused():
+    """Refused before anything is launched: scratch elsewhere, or with fewer bytes behind it than it
+    counts (a broadcast one); arguments laid out while another device was current."""
+    c = Case(63, [30], 4, 16)
+    p = c.plan()
+    scratch = mla.tree_alloc_scratch(p)
+    out, lse = c.outputs()
+    a = mla.tree_make_args(c.d["q"], c.d["kv"], out, lse, **c.kw())
+    n = c.kv.shape[0]
+    w, pos = torch.zeros(n, device="cuda"), torch.zeros(n, dtype=torch.int32, device="cuda")
+    kv = torch.zeros(n, 576, dtype=torch.bfloat16, device="cuda")
+    e = mla.evict_make_args(kv, w, pos, d_pos=c.d["d_pos"].clone(), next_pos=c.d["d_pos"], keep=8,
+                            row_offset=c.d["row_offset"])
+    r = mla.rope_make_args(mla.rope_table(), torch.zeros(1, 4, dtype=torch.int32, device="cuda"),
+                           q_rope=c.d["q"][..., 512:], q=c.d["q"])
+    ev = mla.evict_alloc_scratch(batch=1, keep=8)
+    wide = torch.zeros(1, 256, dtype=torch.uint8, device="cuda").expand(p.scratch_bytes // 256 + 1, 256)
+    for bad in (Elsewhere(scratch), wide, scratch.cpu()):
+        for call in (lambda: mla.tree_forward_args(p, a, bad), lambda: mla.tree_weights_args(p, a, bad, w),
+                     lambda: mla.evict_args(e, bad)):
+            with pytest.raises(ValueError):
+                call()
+    for args, call in ((a, lambda: mla.tree_forward_args(p, a, scratch)),
+                       (a, lambda: mla.tree_weights_args(p, a, scratch, w)),
+                       (e, lambda: mla.evict_args(e, ev)), (r, lambda: mla.rope_append_args(r))):
+        assert args._device == 0
+        args._device = 1
+        with pytest.raises(ValueError, match="device"):
+            call()
+        args._device = 0
+    mla.tree_forward_args(p, a, scratch)
+    torch.cuda.synchronize()
+    c.check(out, lse)
