@@ -21,6 +21,7 @@ decode_attention_mla_gb300.
 """
 import math
 import random
+from operator import is_not
 
 import torch
 
@@ -326,20 +327,35 @@ def _run_evict(s):
     return s["kv"], s["weights_out"], s["positions_out"], keep[:, 0]
 
 
+# The state's tensors whose addresses are in a call's arguments.
+LAID_OUT = dict(
+    rope=("positions", "q_proj", "q", "kv_proj", "kv", "n_tokens", "d_pos", "row_offset"),
+    tree=("q", "kv", "out", "lse", "mask", "n_tokens", "d_pos", "row_offset"),
+    weights=("q", "kv", "lse", "mask", "n_tokens", "d_pos", "row_offset"),
+    evict=("kv", "weights", "positions", "next_pos", "weights_out", "positions_out", "d_pos_out", "d_pos", "row_offset"))
+
+
 def _own(s):
-    """The calls a serving loop makes: arguments that stay the same are laid out once."""
+    """The calls a serving loop makes: arguments that stay the same are laid out once, and
+    again if one of the state's tensors has been replaced by another."""
     import decode_attention_mla_gb300 as mla
-    case, op, h = s["case"], s["case"]["op"], s.get("handle")
+    case, op, h = s["case"], s["case"]["op"], None
+    if op != "commit":
+        laid_out, h = s.get("handle", ((), None))
+        tensors = [s[k] for k in LAID_OUT[op]]
+        if len(laid_out) != len(tensors) or any(map(is_not, laid_out, tensors)):
+            h = None
     common = dict(d_pos=s["d_pos"], row_offset=s["row_offset"])
     if op == "rope":
         if h is None:
             yarn = dict(scaling="yarn", factor=40.0, original_ctx=4096, amplitude=s["amplitude"])
             table = mla.rope_table(rot_dim=case["rot"], base=10000.0, interleaved=case["interleaved"],
                                    **(yarn if case["yarn"] else {}))
-            h = s["handle"] = mla.rope_make_args(
+            h = mla.rope_make_args(
                 table, s["positions"], q_rope=s["q_proj"][..., 128:], q=s["q"], c=s["kv_proj"][..., :LATENT],
                 k_rope=s["kv_proj"][..., LATENT:], kv=s["kv"], n_tokens=s["n_tokens"], kv_scale=s["kv_scale"],
                 **common)
+            s["handle"] = tensors, h
         mla.rope_append_args(h)
         return None
     if op in ("tree", "weights"):
@@ -347,7 +363,8 @@ def _own(s):
             plan = mla.tree_plan(batch=case["B"], tokens=case["Q"], heads=case["H"], scale=SCALE, pdl=True)
             args = mla.tree_make_args(s["q"], s["kv"], s.get("out"), s["lse"], mask=s["mask"],
                                       n_tokens=s["n_tokens"], **common)
-            h = s["handle"] = (plan, args, mla.tree_alloc_scratch(plan))
+            h = plan, args, mla.tree_alloc_scratch(plan)
+            s["handle"] = tensors, h
         if op == "tree":
             mla.tree_forward_args(*h)
             return s["out"], s["lse"]
@@ -361,7 +378,8 @@ def _own(s):
             s["kv"], s["weights"], s["positions"], next_pos=s["next_pos"], keep=case["keep"], sink=case["sink"],
             recent=case["recent"], max_rows=case["hi"], weights_out=s["weights_out"],
             positions_out=s["positions_out"], d_pos_out=s["d_pos_out"], **common)
-        h = s["handle"] = (args, mla.evict_alloc_scratch(batch=case["B"], keep=case["keep"]))
+        h = args, mla.evict_alloc_scratch(batch=case["B"], keep=case["keep"])
+        s["handle"] = tensors, h
     mla.evict_args(*h)
     return s["kv"], s["weights_out"], s["positions_out"], s["d_pos_out"]
 
