@@ -236,12 +236,18 @@ _torch = None
 _raw_stream = None
 
 
+def _device():
+    """The current device (replaced by torch's own getter on first use)."""
+    return _tc().cuda.current_device()
+
+
 def _tc():
-    """The torch module, imported on first use (and the current stream's raw getter, where this
-    torch has it: building a Stream object costs as much as a launch)."""
-    global _torch, _raw_stream
+    """The torch module, imported on first use (and the getters of the current stream's address and
+    device, where this torch has them: building a Stream object costs as much as a launch)."""
+    global _torch, _raw_stream, _device
     if _torch is None:
         import torch
+        _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         _torch = torch
     return _torch
@@ -251,7 +257,7 @@ def _stream(stream):
     if stream is None:
         torch = _torch or _tc()
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())    # (every entry point declares the pointer type)
+            return _raw_stream(_device())                      # (every entry point declares the pointer type)
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
@@ -413,8 +419,8 @@ def _need(t, name, dtypes, shape=None, contiguous=True):
     if not isinstance(t, torch.Tensor) or t.get_device() < 0:
         raise ValueError(f"{name}: a CUDA tensor is needed (tensors passed to the MLA decode kernels must be "
                          "CUDA tensors)")
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is {torch.cuda.current_device()}")
+    if t.get_device() != _device():
+        raise ValueError(f"{name} is on {t.device}, the current device is {_device()}")
     if t.dtype is not dtypes and (type(dtypes) is not tuple or t.dtype not in dtypes):
         names = " or ".join(map(str, dtypes)) if type(dtypes) is tuple else dtypes
         raise ValueError(f"{name}: dtype {t.dtype}, expected {names}")
@@ -438,18 +444,20 @@ def _quick(t, name, dtype, shape, device):
 
 def _scratch_here(scratch):
     """Address and bytes of a call's scratch (CUDA, on the current device, contiguous)."""
-    torch = _torch or _tc()
-    if getattr(scratch, "is_cuda", False) and scratch.get_device() == torch.cuda.current_device() and (
-            scratch.is_contiguous()):
-        return scratch.data_ptr(), scratch.nbytes
-    return _need(scratch, "scratch", scratch.dtype if isinstance(scratch, torch.Tensor) else None), scratch.nbytes
+    try:
+        if scratch.get_device() == _device() and scratch.is_contiguous():
+            return scratch.data_ptr(), scratch.nbytes
+    except AttributeError:
+        pass
+    return _need(scratch, "scratch", getattr(scratch, "dtype", None)), scratch.nbytes
 
 
-def _same_device(a):
-    """Arguments were checked against the device that was current when they were laid out."""
-    device = (_torch or _tc()).cuda.current_device()
+def _stream_of(a, stream):
+    """Stream of a call with prebuilt arguments, which were checked against the device that was current then."""
+    device = _device()
     if a._device is not None and a._device != device:
         raise ValueError(f"arguments for device {a._device}, the current device is {device}")
+    return _raw_stream(device) if stream is None and _raw_stream is not None else _stream(stream)
 
 
 def _int(v, name):
@@ -579,7 +587,7 @@ def rope_make_args(table: RopeTable, positions, *, q_rope=None, q=None, c=None, 
         a.row_offset = _maybe(row_offset, "row_offset", torch.int64, (B,))
         a.row_positions = _side(row_positions, "row_positions", torch.int32, a.kv_rows)
         a.row_weights = _side(row_weights, "row_weights", torch.float32, a.kv_rows)
-    a._device = torch.cuda.current_device()
+    a._device = _device()
     a._keep = (table, positions, q_rope, q, c, k_rope, kv, d_pos, row_offset, n_tokens, row_positions, row_weights)
     return a
 
@@ -589,7 +597,7 @@ def _side(t, name, dtype, rows):
     if t is None:
         return None
     if getattr(t, "dtype", None) is dtype and t.dim() == 1 and t.shape[0] >= rows and t.is_contiguous() and (
-            t.get_device() == _torch.cuda.current_device()):
+            t.get_device() == _device()):
         return t.data_ptr()
     p = _need(t, name, dtype, (None,))
     if t.shape[0] < rows:
@@ -599,8 +607,7 @@ def _side(t, name, dtype, rows):
 
 def rope_append_args(a: RopeArgs, stream=None) -> None:
     """``mla_rope_append`` with prebuilt arguments."""
-    _same_device(a)
-    _check(lib().mla_rope_append(ctypes.byref(a), _stream(stream)), "mla_rope_append")
+    _check(lib().mla_rope_append(ctypes.byref(a), _stream_of(a, stream)), "mla_rope_append")
 
 
 def rope_append(table: RopeTable, positions, *, stream=None, **kw) -> None:
@@ -643,15 +650,14 @@ def tree_make_args(q, kv, out, lse, *, d_pos, row_offset=None, mask=None, n_toke
                  out=_maybe(out, "out", (torch.bfloat16, torch.float32), (B, Q, H, D_LATENT)),
                  out_fp32=int(out is not None and out.dtype == torch.float32),
                  lse=_need(lse, "lse", torch.float32, (B, Q, H)))
-    a._device = torch.cuda.current_device()
+    a._device = _device()
     a._keep = (q, kv, d_pos, row_offset, mask, n_tokens, out, lse)
     a._dims = (int(B), int(Q), int(H))
     return a
 
 
 def _tree_dims(p: TreePlan, a: TreeArgs):
-    """The arguments' [B, Q, H] must be the plan's (the kernels index by the plan), and on this device."""
-    _same_device(a)
+    """The arguments' [B, Q, H] must be the plan's: the kernels index by the plan."""
     if a._dims != (p.shape.batch, p.shape.tokens, p.shape.heads):
         raise ValueError(f"arguments of shape {a._dims} for a plan of "
                          f"{(p.shape.batch, p.shape.tokens, p.shape.heads)}")
@@ -661,7 +667,7 @@ def tree_forward_args(p: TreePlan, a: TreeArgs, scratch, stream=None) -> None:
     """``mla_tree_forward`` with prebuilt arguments."""
     _tree_dims(p, a)
     sp, sb = _scratch_here(scratch)
-    _check(lib().mla_tree_forward(ctypes.byref(p), ctypes.byref(a), sp, sb, _stream(stream)), "mla_tree_forward")
+    _check(lib().mla_tree_forward(ctypes.byref(p), ctypes.byref(a), sp, sb, _stream_of(a, stream)), "mla_tree_forward")
 
 
 def tree_forward(p: TreePlan, q, kv, out, lse, scratch, *, stream=None, **kw) -> None:
@@ -676,7 +682,7 @@ def tree_weights_args(p: TreePlan, a: TreeArgs, scratch, weights, *, decay: floa
     _tree_dims(p, a)
     w = _side(weights, "weights", torch.float32, a.kv_rows)
     sp, sb = _scratch_here(scratch)
-    _check(lib().mla_tree_weights(ctypes.byref(p), ctypes.byref(a), w, float(decay), sp, sb, _stream(stream)),
+    _check(lib().mla_tree_weights(ctypes.byref(p), ctypes.byref(a), w, float(decay), sp, sb, _stream_of(a, stream)),
            "mla_tree_weights")
 
 
@@ -692,7 +698,7 @@ def tree_commit(kv, accept, n_accept, *, d_pos, d_pos_out=None, row_offset=None,
     (``accept``: int32 [B, Q]); ``d_pos_out`` (may be ``d_pos``) takes d_pos + n_accept."""
     torch = _torch or _tc()
     B, Q = accept.shape
-    i32, dev = torch.int32, torch.cuda.current_device()
+    i32, dev = torch.int32, _device()
     kvp, rows, stride, fp8 = _quick_cache(kv, dev, torch) or _cache(kv, None, None)
     if kv_rows is not None or row_stride is not None:
         kvp, rows, stride, fp8 = _cache(kv, kv_rows, row_stride)
@@ -738,16 +744,15 @@ def evict_make_args(kv, weights, positions, *, d_pos, next_pos, keep: int, sink:
                   weights_out=_side(wo, "weights_out", torch.float32, rows),
                   positions_out=_side(po, "positions_out", torch.int32, rows),
                   d_pos_out=_need(do, "d_pos_out", torch.int32, (B,)))
-    a._device = torch.cuda.current_device()
+    a._device = _device()
     a._keep = (kv, weights, positions, d_pos, next_pos, row_offset, wo, po, do)
     return a
 
 
 def evict_args(a: EvictArgs, scratch, stream=None) -> None:
     """``mla_evict`` with prebuilt arguments."""
-    _same_device(a)
     sp, sb = _scratch_here(scratch)
-    _check(lib().mla_evict(ctypes.byref(a), sp, sb, _stream(stream)), "mla_evict")
+    _check(lib().mla_evict(ctypes.byref(a), sp, sb, _stream_of(a, stream)), "mla_evict")
 
 
 def evict(kv, weights, positions, scratch, *, stream=None, **kw) -> None:
