@@ -21,7 +21,7 @@ decode_attention_mla_gb300.
 """
 import math
 import random
-from operator import is_not
+from operator import is_not, itemgetter
 
 import torch
 
@@ -329,10 +329,11 @@ def _run_evict(s):
 
 # The state's tensors whose addresses are in a call's arguments.
 LAID_OUT = dict(
-    rope=("positions", "q_proj", "q", "kv_proj", "kv", "n_tokens", "d_pos", "row_offset"),
-    tree=("q", "kv", "out", "lse", "mask", "n_tokens", "d_pos", "row_offset"),
-    weights=("q", "kv", "lse", "mask", "n_tokens", "d_pos", "row_offset"),
-    evict=("kv", "weights", "positions", "next_pos", "weights_out", "positions_out", "d_pos_out", "d_pos", "row_offset"))
+    rope=itemgetter("positions", "q_proj", "q", "kv_proj", "kv", "n_tokens", "d_pos", "row_offset"),
+    tree=itemgetter("q", "kv", "out", "lse", "mask", "n_tokens", "d_pos", "row_offset"),
+    weights=itemgetter("q", "kv", "lse", "mask", "n_tokens", "d_pos", "row_offset"),
+    evict=itemgetter("kv", "weights", "positions", "next_pos", "weights_out", "positions_out", "d_pos_out", "d_pos",
+                     "row_offset"))
 
 
 def _own(s):
@@ -341,9 +342,9 @@ def _own(s):
     import decode_attention_mla_gb300 as mla
     case, op, h = s["case"], s["case"]["op"], None
     if op != "commit":
-        laid_out, h = s.get("handle", ((), None))
-        tensors = [s[k] for k in LAID_OUT[op]]
-        if len(laid_out) != len(tensors) or any(map(is_not, laid_out, tensors)):
+        tensors = LAID_OUT[op](s)
+        laid_out, h = s.get("handle", (tensors, None))
+        if any(map(is_not, laid_out, tensors)):
             h = None
     common = dict(d_pos=s["d_pos"], row_offset=s["row_offset"])
     if op == "rope":
