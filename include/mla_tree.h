@@ -17,7 +17,8 @@
  * Products of q and k are exact; their fp32 sums (the tensor cores') drop what
  * does not fit, towards zero: a score is within 2^-13 of the sum of its
  * products' magnitudes, and exact where nothing is dropped.  With normal
- * queries and rows scores come out smaller by about 4e-7 of themselves.
+ * queries and rows scores come out smaller by about 4e-7 of themselves (in
+ * mla_tree_weights, which adds two sums of half the length, by 1e-7).
  *
  * What a token does not attend does not reach its result, whatever it holds
  * (NaN and infinities too): rows behind the drafts, drafted rows its mask

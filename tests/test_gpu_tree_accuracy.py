@@ -167,3 +167,24 @@ def test_fp32_outputs_of_exact_scores(lens, Q, H, num_sms):
             err = (out[b, i].double().cpu() - want).abs()
             assert (err <= rel[:, None] * spread).all(), (b, i, float((err / spread).max()), float(rel.max()))
             assert ((lse[b, i].double().cpu() - rl).abs() <= 5 * U * s.abs().amax(1) + 2.0 ** -19 + n * U).all()
+
+
+@pytest.mark.parametrize("Q,H,rows,num_sms", [(1, 16, 300, 0), (1, 128, 300, 2), (2, 128, 300, 2), (2, 100, 900, 2),
+                                              (2, 128, 300, 0), (5, 64, 300, 2)])
+def test_weights_keep_half_of_what_one_chain_of_sums_drops(Q, H, rows, num_sms):
+    """A score of 64 and 35 addends of 2^-24 of it, one in each of the other 16-column products that
+    an MMA sums: towards zero, each is dropped where it is added to the large one.  Half a chain's are not."""
+    kv = torch.zeros(rows + Q, 576, dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros(1, Q, H, 576, dtype=torch.bfloat16, device="cuda")
+    for t in (kv, q):
+        t[..., 0] = 8
+        t[..., 24::16] = 2.0 ** -9
+    s = 64 + 35 * 2.0 ** -18
+    lse = torch.full((1, Q, H), 64.0, device="cuda")
+    w = torch.empty(rows + Q, device="cuda")
+    p = mla.tree_plan(batch=1, tokens=Q, heads=H, scale=1.0, num_sms=num_sms)
+    mla.tree_weights(p, q, kv, lse, mla.tree_alloc_scratch(p), w, decay=0.0, d_pos=ints([rows]))
+    # the first half, 20 MMAs, drops 19 of the addends at most; roundings as in test_weights_of_exact_scores
+    rel = 19 * 2.0 ** -18 + 3 * U * 64 + 2.0 ** -21 + Q * H * U
+    want = Q * H * math.exp(s - 64)
+    assert ((w[:rows].double() - want).abs() <= rel * want).all(), float((w[:rows].double() / want - 1).abs().max())
