@@ -542,7 +542,8 @@ def rope_table(rot_dim: int = D_ROPE, base: float = 10000.0, *, interleaved: boo
                factor: float = 1.0, original_ctx: float = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0,
                amplitude: float = 1.0, device=None) -> RopeTable:
     """Rotation table on the device: pairs (2j, 2j+1) if ``interleaved``, else (j, j + rot_dim/2);
-    ``scaling``: "none", "linear" or "yarn"; ``amplitude`` multiplies sines and cosines."""
+    ``scaling``: "none", "linear" or "yarn" (the angles); ``amplitude`` multiplies sines and cosines and is
+    the caller's to give: 1 whatever the scaling, where YaRN's usual one is 0.1 ln(factor) + 1."""
     torch = _torch or _tc()
     turns = rope_turns(rot_dim, base, scaling=scaling, factor=factor, original_ctx=original_ctx,
                        beta_fast=beta_fast, beta_slow=beta_slow)
@@ -635,8 +636,8 @@ def tree_make_args(q, kv, out, lse, *, d_pos, row_offset=None, mask=None, n_toke
                    kv_rows: int | None = None, row_stride: int | None = None) -> TreeArgs:
     """Arguments of :func:`tree_forward_args` and :func:`tree_weights_args` (which needs no ``out``).
 
-    ``q``: bf16 [B, Q, H, 576]; ``kv``: bf16 [rows, 576]; ``out``: bf16 or fp32 [B, Q, H, 512]; ``lse``: fp32
-    [B, Q, H]; ``mask``: int64 [B, Q], bit j of word i: token i attends drafted token j (None: a chain)."""
+    ``q``: bf16 [B, Q, H, 576]; ``kv``: bf16 [rows, 576]; ``out``: bf16 or fp32 [B, Q, H, 512] (fp32 also takes
+    probabilities in 16 bits instead of 8, as the decode does, for up to 1.6 times the time); ``lse``: fp32 [B, Q, H]; ``mask``: int64 [B, Q], bit j of word i: token i attends drafted token j (None: a chain)."""
     torch = _torch or _tc()
     if q.dim() != 4:
         raise ValueError("q must be [B, Q, H, 576]")

@@ -6,8 +6,8 @@
 // 72 16-byte units, five units a thread) and writes after a barrier, so any
 // order of the path is right although source and destination rows overlap.
 // Bound: latency (a path is at most 74 KB); a row already in place is skipped.
-// Measured in a graph: 3.0 us a call for a path of up to 8 rows, 4.8 for 64 of up to 64
-// (a direct call takes the host 7 us).
+// Measured in a graph: 2.6 us a call for a path of up to 8 rows, 4.3 for 64 of up to 64
+// (a direct call takes the host 6.6 us).
 #include <cstdint>
 
 #include "device_utils.cuh"

@@ -35,11 +35,12 @@
 // block's QK waits for its queries.
 //
 // Bound: the tensor cores (an M128 N128 K16 MMA of a pair takes 32 cycles, N256 64;
-// a tile 2200), fed at 140 KB per tile and CTA.  Measured: 64 drafts x 128 heads over
-// 65536 rows 630 us, 1860 TFLOP/s or 0.95 of cuBLAS's burst rate, while the clock
-// holds; 16 ragged requests of 5 x 128 262 us, 1470 TFLOP/s (DRAM re-reads
-// of row blocks that drift apart); 16 x 16 over 131072 rows 61 us; 8 x 16 over 248
-// rows 11.8 us, of which the two kernels' launches, set-up and merge are 10.
+// a tile 2200), fed at 140 KB per tile and CTA.  Measured in long rows of calls, bf16
+// outputs: 64 drafts x 128 heads over 65536 rows 740 us, 1590 TFLOP/s, under the power cap
+// (in short rows 647 us, 1810 TFLOP/s or 0.93 of cuBLAS's burst rate); 16 ragged requests
+// of 5 x 128 281 us, 1310 TFLOP/s (251 us; DRAM re-reads of row blocks that drift apart);
+// 16 x 16 over 131072 rows 65 us; 8 x 16 over 248 rows 11.7 us, of which the two
+// kernels' launches, set-up and merge are 10.
 //
 // Warps of a CTA: 0-7 softmax and epilogue, 8 TMA of Q and K, 9 MMA issue (even
 // CTA; the odd one's writes empty requests) and tensor memory, 10 TMA of V.

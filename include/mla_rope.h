@@ -59,7 +59,7 @@ typedef struct {
     int heads;                  /* 0 .. 128; 0 = no queries */
     int rot_dim;                /* as in the table */
     int interleaved;            /* 1 = pairs (2j, 2j + 1); 0 = pairs (j, j + rot_dim / 2) */
-    float amplitude;            /* A: finite and > 0; 1 unless the scaling asks for another */
+    float amplitude;            /* A: finite and > 0; the caller's to give (YaRN's usual one: 0.1 ln(factor) + 1) */
     const unsigned long long *turns; /* (device) mla_rope_table's values */
     const int *positions;       /* (device) int32 [B][N], >= 0 */
     const int *n_tokens;        /* (device) int32 [B], new tokens of each request (clamped to 0 .. N);
