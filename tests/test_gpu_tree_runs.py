@@ -7,6 +7,7 @@ import torch
 
 import decode_attention_mla_gb300 as mla
 import _tree_ref as ref
+import test_gpu_tree
 from test_gpu_tree import SCALE, Case
 
 pytestmark = pytest.mark.gpu
@@ -161,3 +162,31 @@ def test_scratch_and_arguments_of_another_device_are_refused():
     mla.tree_forward_args(p, a, scratch)
     torch.cuda.synchronize()
     c.check(out, lse)
+
+
+ROWS_ONCE = next(m.args[1] for m in test_gpu_tree.test_every_row_counts_once.pytestmark if m.name == "parametrize")
+
+
+@pytest.mark.parametrize("num_sms,lens,Q,H", ROWS_ONCE)
+def test_every_row_counts_once_with_bf16_outputs(num_sms, lens, Q, H):
+    """All splits of the work, in the other form of the kernel: queries of zero, so the log-sum-exp is the
+    log of the count, and the means of latents of 0 and 1 differ from the fp32 ones by their rounding."""
+    B, i32 = len(lens), dict(dtype=torch.int32, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(B + Q)
+    offs = [sum(lens[:b]) + b * Q for b in range(B)]
+    kv = torch.randint(0, 2, (sum(lens) + B * Q, 576), generator=g, device="cuda", dtype=torch.int8).bfloat16()
+    q = torch.zeros(B, Q, H, 576, dtype=torch.bfloat16, device="cuda")
+    p = mla.tree_plan(batch=B, tokens=Q, heads=H, scale=SCALE, num_sms=num_sms)
+    scratch = mla.tree_alloc_scratch(p)
+    got = []
+    for dtype in (torch.bfloat16, torch.float32):
+        out, lse = torch.empty(B, Q, H, 512, dtype=dtype, device="cuda"), torch.empty(B, Q, H, device="cuda")
+        mla.tree_forward(p, q, kv, out, lse, scratch, d_pos=torch.tensor(lens, **i32),
+                         row_offset=torch.tensor(offs, dtype=torch.int64, device="cuda"))
+        got.append((out, lse))
+    assert mla.status_word(p, scratch) == 0
+    count = torch.tensor(lens, dtype=torch.float64, device="cuda")[:, None] + torch.arange(1, Q + 1, device="cuda")
+    assert (got[0][1].double() - torch.log(count)[:, :, None]).abs().max() <= 2.0 ** -20 * 8
+    # probabilities of one are exact in bf16: half a step of the output, and the fp32 sums' 2^-18
+    out, exact = got[0][0].float(), got[1][0]
+    assert ((out - exact).abs() <= ref.BF16 * exact.abs() + 2.0 ** -18).all()
