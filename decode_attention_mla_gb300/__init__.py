@@ -26,6 +26,7 @@ LIB_PATH = os.path.join(_HERE, "libmla_decode.so")
 D_LATENT = 512
 D_ROPE = 64
 D_ROW = 576
+Q4_ROW = 416                           # bytes of a row of the 4-bit cache
 MAX_SPLITS = 256
 
 OK, EINVAL, EUNSUPPORTED, ESCRATCH, EALIGN, ECUDA, EDEVICE, ENOTREADY = 0, -1, -2, -3, -4, -5, -6, -7
@@ -129,6 +130,68 @@ class EvictArgs(ctypes.Structure):
                 ("d_pos_out", ctypes.c_void_p)]
 
 
+class PagedCache(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("page_stride", ctypes.c_longlong), ("n_pages", ctypes.c_int),
+                ("page_rows", ctypes.c_int), ("page_table", ctypes.c_void_p), ("columns", ctypes.c_int),
+                ("kv_scale", ctypes.c_float)]
+
+
+class PagedAppendArgs(ctypes.Structure):
+    _device = None                     # device of the tensors, where a *_make_args call has checked them
+    _fields_ = [("cache", PagedCache), ("batch", ctypes.c_int), ("tokens", ctypes.c_int), ("heads", ctypes.c_int),
+                ("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("amplitude", ctypes.c_float),
+                ("turns", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("n_tokens", ctypes.c_void_p),
+                ("q_rope", ctypes.c_void_p), ("q_rope_batch", ctypes.c_longlong), ("q_rope_token", ctypes.c_longlong),
+                ("q_rope_head", ctypes.c_longlong),
+                ("q_out", ctypes.c_void_p), ("q_out_batch", ctypes.c_longlong), ("q_out_token", ctypes.c_longlong),
+                ("q_out_head", ctypes.c_longlong),
+                ("c", ctypes.c_void_p), ("c_batch", ctypes.c_longlong), ("c_token", ctypes.c_longlong),
+                ("k_rope", ctypes.c_void_p), ("k_rope_batch", ctypes.c_longlong), ("k_rope_token", ctypes.c_longlong),
+                ("c_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p), ("q_norm", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("d_pos", ctypes.c_void_p)]
+
+
+class PagedReadArgs(ctypes.Structure):
+    _device = None                     # device of the tensors, where a *_make_args call has checked them
+    _fields_ = [("cache", PagedCache), ("batch", ctypes.c_int), ("rows", ctypes.c_int), ("first", ctypes.c_void_p),
+                ("n_rows", ctypes.c_void_p), ("out", ctypes.c_void_p), ("out_batch", ctypes.c_longlong),
+                ("out_row", ctypes.c_longlong)]
+
+
+class PagedShape(ctypes.Structure):
+    _fields_ = TreeShape._fields_
+
+
+class PagedPlan(ctypes.Structure):
+    _fields_ = [("shape", PagedShape)] + TreePlan._fields_[1:]
+
+
+class PagedArgs(ctypes.Structure):
+    _device = None                     # device of the tensors, where a *_make_args call has checked them
+    _fields_ = [("cache", PagedCache), ("q", ctypes.c_void_p), ("d_pos", ctypes.c_void_p), ("n_tokens", ctypes.c_void_p),
+                ("window", ctypes.c_int), ("sink", ctypes.c_int), ("out", ctypes.c_void_p), ("out_fp32", ctypes.c_int),
+                ("lse", ctypes.c_void_p)]
+
+
+_POOL_FIELDS = [("pages", ctypes.c_void_p), ("page_stride", ctypes.c_longlong), ("n_pages", ctypes.c_int),
+                ("page_rows", ctypes.c_int), ("row_bytes", ctypes.c_int), ("batch", ctypes.c_int),
+                ("columns", ctypes.c_int), ("page_table", ctypes.c_void_p)]
+
+
+class PagesForkArgs(ctypes.Structure):
+    _device = None                     # device of the tensors, where a *_make_args call has checked them
+    _fields_ = _POOL_FIELDS + [
+        ("d_pos", ctypes.c_void_p), ("parent", ctypes.c_void_p), ("rows", ctypes.c_void_p), ("reserve", ctypes.c_int),
+        ("window", ctypes.c_int), ("sink", ctypes.c_int), ("page_table_out", ctypes.c_void_p),
+        ("d_pos_out", ctypes.c_void_p), ("refs", ctypes.c_void_p), ("missing", ctypes.c_void_p)]
+
+
+class PagesCompactArgs(ctypes.Structure):
+    _device = None                     # device of the tensors, where a *_make_args call has checked them
+    _fields_ = _POOL_FIELDS + [("refs", ctypes.c_void_p), ("page_table_out", ctypes.c_void_p),
+                               ("refs_out", ctypes.c_void_p), ("used", ctypes.c_void_p)]
+
+
 class MLADecodeError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -143,7 +206,8 @@ EXPORTED = ("mla_decode_abi_version", "mla_decode_plan", "mla_decode_run", "mla_
             "mla_decode_strerror", "mla_decode_forward_static", "mla_decode_project", "mla_decode_forward_step",
             "mla_floor_empty_pair", "mla_floor_read", "mla_floor_gather", "mla_decode_static_status", "mla_decode_static_reset",
             "mla_rope_table", "mla_rope_append", "mla_tree_plan", "mla_tree_forward", "mla_tree_weights",
-            "mla_tree_commit", "mla_evict_scratch_bytes", "mla_evict")
+            "mla_tree_commit", "mla_evict_scratch_bytes", "mla_evict", "mla_paged_append", "mla_paged_read",
+            "mla_paged_plan", "mla_paged_forward", "mla_pages_scratch_bytes", "mla_pages_fork", "mla_pages_compact")
 
 
 def lib():
@@ -208,6 +272,20 @@ def lib():
         L.mla_evict_scratch_bytes.argtypes = [I, I]
         L.mla_evict.restype = I
         L.mla_evict.argtypes = [ctypes.POINTER(EvictArgs), P, SZ, P]
+        L.mla_paged_append.restype = I
+        L.mla_paged_append.argtypes = [ctypes.POINTER(PagedAppendArgs), P]
+        L.mla_paged_read.restype = I
+        L.mla_paged_read.argtypes = [ctypes.POINTER(PagedReadArgs), P]
+        L.mla_paged_plan.restype = I
+        L.mla_paged_plan.argtypes = [ctypes.POINTER(PagedShape), ctypes.POINTER(PagedPlan)]
+        L.mla_paged_forward.restype = I
+        L.mla_paged_forward.argtypes = [ctypes.POINTER(PagedPlan), ctypes.POINTER(PagedArgs), P, SZ, P]
+        L.mla_pages_scratch_bytes.restype = SZ
+        L.mla_pages_scratch_bytes.argtypes = [I, I, I]
+        L.mla_pages_fork.restype = I
+        L.mla_pages_fork.argtypes = [ctypes.POINTER(PagesForkArgs), P, SZ, P]
+        L.mla_pages_compact.restype = I
+        L.mla_pages_compact.argtypes = [ctypes.POINTER(PagesCompactArgs), P, SZ, P]
         _lib = L
         return L
 
@@ -760,6 +838,254 @@ def evict(kv, weights, positions, scratch, *, stream=None, **kw) -> None:
     """Keep each request's ``keep`` rows of largest weight (the first ``sink`` and the last ``recent``
     positions before all others), compacted in place (arguments as for :func:`evict_make_args`)."""
     evict_args(evict_make_args(kv, weights, positions, **kw), scratch, stream)
+
+
+# ---- a latent cache in 4 bits, in pages --------------------------------------
+
+def paged_alloc(n_pages: int, page_rows: int, device=None):
+    """Pages of a 4-bit cache: uint8 [n_pages, page_rows, 416], zeros (every row then stands for zeros)."""
+    torch = _torch or _tc()
+    return torch.zeros(n_pages, page_rows, Q4_ROW, dtype=torch.uint8, device=device or "cuda")
+
+
+def _pool(pages, row_bytes=None):
+    """(pointer, page stride in bytes, pages, rows per page, bytes per row) of pages [n, page_rows, ..] whose
+    rows are contiguous within a page."""
+    torch = _torch or _tc()
+    if not isinstance(pages, torch.Tensor) or pages.dim() != 3:
+        raise ValueError("pages must be a tensor [n_pages, page_rows, row]")
+    p = _need(pages, "pages", pages.dtype, contiguous=False)
+    n, rows, width = pages.shape
+    size = pages.element_size()
+    if n < 1 or rows < 1 or width < 1:
+        raise ValueError("pages has no rows")
+    if row_bytes is not None and (pages.dtype is not torch.uint8 or width != row_bytes):
+        raise ValueError(f"pages: {tuple(pages.shape)} of {pages.dtype}, expected [*, *, {row_bytes}] of torch.uint8")
+    if pages.stride(2) != 1 and width > 1 or pages.stride(1) != width and rows > 1:
+        raise ValueError("the rows of a page must be contiguous")
+    return p, (pages.stride(0) if n > 1 else rows * width) * size, _int(n, "n_pages"), rows, width * size
+
+
+def _paged_cache(pages, page_table, kv_scale, batch) -> PagedCache:
+    torch = _torch or _tc()
+    p, stride, n, rows, _ = _pool(pages, Q4_ROW)
+    table = _need(page_table, "page_table", torch.int32, (batch, None))
+    return PagedCache(pages=p, page_stride=stride, n_pages=n, page_rows=rows, page_table=table,
+                      columns=_int(page_table.shape[1], "columns"), kv_scale=float(kv_scale))
+
+
+def paged_append_make_args(table: RopeTable, positions, *, q_rope=None, q=None, c=None, k_rope=None, pages=None,
+                           page_table=None, d_pos=None, n_tokens=None, c_norm=None, k_norm=None, q_norm=None,
+                           eps: float = 1e-6, kv_scale: float = 1.0) -> PagedAppendArgs:
+    """Arguments of :func:`paged_append_args`.
+
+    ``positions``: int32 [B, N].  Queries: ``q_rope`` bf16 [B, N, H, 64] (any strides, multiples of 8),
+    normalised with ``q_norm`` (bf16 [64]) if given, is rotated into ``q[..., 512:]`` of bf16 [B, N, H, 576].
+    Rows: ``c`` bf16 [B, N, 512], normalised with ``c_norm`` (bf16 [512]) if given, goes in 4 bits, and ``k_rope``
+    bf16 [B, N, 64], normalised with ``k_norm`` if given and rotated, in bf16 to row ``d_pos[b] + n`` of request b
+    in ``pages`` (uint8 [n_pages, page_rows, 416]) by ``page_table`` (int32 [B, columns]).  ``kv_scale``: a power
+    of two.  Either part may be left out."""
+    torch = _torch or _tc()
+    B, N = positions.shape
+    a = PagedAppendArgs(batch=int(B), tokens=int(N), rot_dim=table.rot_dim, interleaved=int(table.interleaved),
+                        amplitude=table.amplitude, turns=_need(table.turns, "table", torch.int64),
+                        positions=_need(positions, "positions", torch.int32, (B, N)),
+                        n_tokens=_maybe(n_tokens, "n_tokens", torch.int32, (B,)), eps=float(eps))
+    if (q_rope is None) != (q is None):
+        raise ValueError("q_rope and q go together")
+    if q is not None:
+        H = q.shape[2] if q.dim() == 4 else -1
+        a.heads = int(H)
+        a.q_rope, a.q_rope_batch, a.q_rope_token, a.q_rope_head = _strides(q_rope, "q_rope", (B, N, H, D_ROPE), 3)
+        _need(q, "q", torch.bfloat16, (B, N, H, D_ROW), contiguous=False)
+        part = q[..., D_LATENT:]
+        a.q_out, a.q_out_batch, a.q_out_token, a.q_out_head = _strides(part, "q", (B, N, H, D_ROPE), 3)
+    elif q_norm is not None:
+        raise ValueError("q_norm belongs to q_rope and q")
+    rows = (c, k_rope, pages, page_table, d_pos)
+    if any(t is None for t in rows) != all(t is None for t in rows):
+        raise ValueError("c, k_rope, pages, page_table and d_pos go together")
+    if pages is None and not (c_norm is None and k_norm is None):
+        raise ValueError("c_norm and k_norm belong to the rows")
+    if pages is not None:
+        a.c, a.c_batch, a.c_token = _strides(c, "c", (B, N, D_LATENT), 2)
+        a.k_rope, a.k_rope_batch, a.k_rope_token = _strides(k_rope, "k_rope", (B, N, D_ROPE), 2)
+        a.cache = _paged_cache(pages, page_table, kv_scale, B)
+        a.d_pos = _need(d_pos, "d_pos", torch.int32, (B,))
+    a.c_norm = _maybe(c_norm, "c_norm", torch.bfloat16, (D_LATENT,))
+    a.k_norm = _maybe(k_norm, "k_norm", torch.bfloat16, (D_ROPE,))
+    a.q_norm = _maybe(q_norm, "q_norm", torch.bfloat16, (D_ROPE,))
+    a._device = _device()
+    a._keep = (table, positions, q_rope, q, c, k_rope, pages, page_table, d_pos, n_tokens, c_norm, k_norm, q_norm)
+    return a
+
+
+def paged_append_args(a: PagedAppendArgs, stream=None) -> None:
+    """``mla_paged_append`` with prebuilt arguments."""
+    _check(lib().mla_paged_append(ctypes.byref(a), _stream_of(a, stream)), "mla_paged_append")
+
+
+def paged_append(table: RopeTable, positions, *, stream=None, **kw) -> None:
+    """Normalise and rotate the new tokens' queries and keys, normalise and quantise their latents, and write
+    their rows (arguments as for :func:`paged_append_make_args`)."""
+    paged_append_args(paged_append_make_args(table, positions, **kw), stream)
+
+
+def paged_read_make_args(out, pages, page_table, *, first=None, n_rows=None, kv_scale: float = 1.0) -> PagedReadArgs:
+    """Arguments of :func:`paged_read_args`.  ``out``: bf16 [B, N, 576], any strides that are multiples of 8;
+    ``first``, ``n_rows``: int32 [B] (None: 0, N)."""
+    torch = _torch or _tc()
+    if out.dim() != 3:
+        raise ValueError("out must be [B, N, 576]")
+    B, N, _ = out.shape
+    a = PagedReadArgs(cache=_paged_cache(pages, page_table, kv_scale, B), batch=int(B), rows=int(N),
+                      first=_maybe(first, "first", torch.int32, (B,)), n_rows=_maybe(n_rows, "n_rows", torch.int32, (B,)))
+    a.out, a.out_batch, a.out_row = _strides(out, "out", (B, N, D_ROW), 2)
+    a.out_row = a.out_row or D_ROW
+    a._device = _device()
+    a._keep = (out, pages, page_table, first, n_rows)
+    return a
+
+
+def paged_read_args(a: PagedReadArgs, stream=None) -> None:
+    """``mla_paged_read`` with prebuilt arguments."""
+    _check(lib().mla_paged_read(ctypes.byref(a), _stream_of(a, stream)), "mla_paged_read")
+
+
+def paged_read(out, pages, page_table, *, stream=None, **kw) -> None:
+    """``out[b, n] =`` row ``first[b] + n`` of request b as bf16 values, for n < n_rows[b] (arguments as for
+    :func:`paged_read_make_args`)."""
+    paged_read_args(paged_read_make_args(out, pages, page_table, **kw), stream)
+
+
+def paged_plan(*, batch: int, tokens: int, heads: int, scale: float, num_sms: int = 0, pdl: bool = False,
+               stall_test: bool = False) -> PagedPlan:
+    """``mla_paged_plan``: up to ``tokens`` (<= 64) new tokens per request."""
+    s = PagedShape(batch=_int(batch, "batch"), tokens=_int(tokens, "tokens"), heads=_int(heads, "heads"), scale=scale,
+                   num_sms=_int(num_sms, "num_sms"), pdl=int(bool(pdl)), stall_test=int(bool(stall_test)))
+    p = PagedPlan()
+    _check(lib().mla_paged_plan(ctypes.byref(s), ctypes.byref(p)), "mla_paged_plan")
+    return p
+
+
+def paged_alloc_scratch(p: PagedPlan, device=None):
+    """Allocate and zero the scratch of a paged plan (outside capture); :func:`status_word` reads its status."""
+    return alloc_scratch(p, device)
+
+
+def paged_make_args(q, pages, page_table, out, lse, *, d_pos, n_tokens=None, window: int = 0, sink: int = 0,
+                    kv_scale: float = 1.0) -> PagedArgs:
+    """Arguments of :func:`paged_forward_args`.
+
+    ``q``: bf16 [B, Q, H, 576]; ``pages``: uint8 [n_pages, page_rows, 416]; ``page_table``: int32 [B, columns];
+    ``out``: bf16 or fp32 [B, Q, H, 512]; ``lse``: fp32 [B, Q, H].  Token i stands in row ``d_pos[b] + i`` and
+    attends the rows up to it: all of them, or with a ``window`` the last ``window`` and the first ``sink``."""
+    torch = _torch or _tc()
+    if q.dim() != 4:
+        raise ValueError("q must be [B, Q, H, 576]")
+    B, Q, H, _ = q.shape
+    a = PagedArgs(cache=_paged_cache(pages, page_table, kv_scale, B),
+                  q=_need(q, "q", torch.bfloat16, (B, Q, H, D_ROW)), d_pos=_need(d_pos, "d_pos", torch.int32, (B,)),
+                  n_tokens=_maybe(n_tokens, "n_tokens", torch.int32, (B,)), window=_int(window, "window"),
+                  sink=_int(sink, "sink"),
+                  out=_need(out, "out", (torch.bfloat16, torch.float32), (B, Q, H, D_LATENT)),
+                  out_fp32=int(out.dtype == torch.float32), lse=_need(lse, "lse", torch.float32, (B, Q, H)))
+    a._device = _device()
+    a._keep = (q, pages, page_table, out, lse, d_pos, n_tokens)
+    a._dims = (int(B), int(Q), int(H))
+    return a
+
+
+def paged_forward_args(p: PagedPlan, a: PagedArgs, scratch, stream=None) -> None:
+    """``mla_paged_forward`` with prebuilt arguments."""
+    _tree_dims(p, a)
+    sp, sb = _scratch_here(scratch)
+    _check(lib().mla_paged_forward(ctypes.byref(p), ctypes.byref(a), sp, sb, _stream_of(a, stream)),
+           "mla_paged_forward")
+
+
+def paged_forward(p: PagedPlan, q, pages, page_table, out, lse, scratch, *, stream=None, **kw) -> None:
+    """Attention of each request's new tokens over its rows in the 4-bit cache (arguments as for
+    :func:`paged_make_args`)."""
+    paged_forward_args(p, paged_make_args(q, pages, page_table, out, lse, **kw), scratch, stream)
+
+
+def pages_alloc_scratch(pages, page_table, device=None):
+    """Scratch of :func:`pages_fork` and :func:`pages_compact` for a pool and a table."""
+    torch = _torch or _tc()
+    B, columns = page_table.shape
+    n = int(lib().mla_pages_scratch_bytes(_int(B, "batch"), _int(columns, "columns"), _int(pages.shape[0], "n_pages")))
+    if n == 0:
+        raise ValueError("batch must be 1 .. 4096, and the table and the pool below 2^30 entries")
+    return torch.empty(n, dtype=torch.uint8, device=device or pages.device)
+
+
+def _pool_args(cls, pages, page_table, page_table_out, **kw):
+    torch = _torch or _tc()
+    p, stride, n, rows, row_bytes = _pool(pages)
+    t = _need(page_table, "page_table", torch.int32, (None, None))
+    B, columns = page_table.shape
+    to = t if page_table_out is None else _need(page_table_out, "page_table_out", torch.int32, (B, columns))
+    return cls(pages=p, page_stride=stride, n_pages=n, page_rows=rows, row_bytes=_int(row_bytes, "row bytes"),
+               batch=_int(B, "batch"), columns=_int(columns, "columns"), page_table=t, page_table_out=to, **kw), B, n
+
+
+def pages_fork_make_args(pages, page_table, d_pos, refs, *, parent=None, rows=None, reserve: int = 0, window: int = 0,
+                         sink: int = 0, page_table_out=None, d_pos_out=None, missing) -> PagesForkArgs:
+    """Arguments of :func:`pages_fork_args`.  ``pages``: [n_pages, page_rows, row] of any type, rows of a multiple of
+    16 bytes; ``page_table``: int32 [B, columns]; ``d_pos``, ``parent``, ``rows``: int32 [B]; ``refs``: int32
+    [n_pages], written; ``missing``: int32 [1], written.  The ``*_out`` tensors default to the inputs (in place)."""
+    torch = _torch or _tc()
+    a, B, n = _pool_args(PagesForkArgs, pages, page_table, page_table_out, reserve=_int(reserve, "reserve"),
+                         window=_int(window, "window"), sink=_int(sink, "sink"))
+    a.d_pos = _need(d_pos, "d_pos", torch.int32, (B,))
+    a.d_pos_out = a.d_pos if d_pos_out is None else _need(d_pos_out, "d_pos_out", torch.int32, (B,))
+    a.parent = _maybe(parent, "parent", torch.int32, (B,))
+    a.rows = _maybe(rows, "rows", torch.int32, (B,))
+    a.refs = _need(refs, "refs", torch.int32, (n,))
+    a.missing = _need(missing, "missing", torch.int32, (1,))
+    a._device = _device()
+    a._keep = (pages, page_table, page_table_out, d_pos, d_pos_out, parent, rows, refs, missing)
+    return a
+
+
+def pages_fork_args(a: PagesForkArgs, scratch, stream=None) -> None:
+    """``mla_pages_fork`` with prebuilt arguments."""
+    sp, sb = _scratch_here(scratch)
+    _check(lib().mla_pages_fork(ctypes.byref(a), sp, sb, _stream_of(a, stream)), "mla_pages_fork")
+
+
+def pages_fork(pages, page_table, d_pos, refs, scratch, *, stream=None, **kw) -> None:
+    """Every request goes on from the first ``rows[b]`` rows of request ``parent[b]`` (its own rows, all of them, where
+    not given; a parent outside 0 .. B - 1 ends it): full pages are shared, a last page that others need is copied,
+    pages for ``reserve`` rows more are taken, and all others are free (arguments as for
+    :func:`pages_fork_make_args`)."""
+    pages_fork_args(pages_fork_make_args(pages, page_table, d_pos, refs, **kw), scratch, stream)
+
+
+def pages_compact_make_args(pages, page_table, refs, *, page_table_out=None, refs_out=None, used) -> PagesCompactArgs:
+    """Arguments of :func:`pages_compact_args` (tensors as for :func:`pages_fork_make_args`; ``used``: int32 [1],
+    written).  The ``*_out`` tensors default to the inputs (in place)."""
+    torch = _torch or _tc()
+    a, _, n = _pool_args(PagesCompactArgs, pages, page_table, page_table_out)
+    a.refs = _need(refs, "refs", torch.int32, (n,))
+    a.refs_out = a.refs if refs_out is None else _need(refs_out, "refs_out", torch.int32, (n,))
+    a.used = _need(used, "used", torch.int32, (1,))
+    a._device = _device()
+    a._keep = (pages, page_table, page_table_out, refs, refs_out, used)
+    return a
+
+
+def pages_compact_args(a: PagesCompactArgs, scratch, stream=None) -> None:
+    """``mla_pages_compact`` with prebuilt arguments."""
+    sp, sb = _scratch_here(scratch)
+    _check(lib().mla_pages_compact(ctypes.byref(a), sp, sb, _stream_of(a, stream)), "mla_pages_compact")
+
+
+def pages_compact(pages, page_table, refs, scratch, *, stream=None, **kw) -> None:
+    """Move the pages in use (``refs`` above 0) to the front of the pool (arguments as for
+    :func:`pages_compact_make_args`)."""
+    pages_compact_args(pages_compact_make_args(pages, page_table, refs, **kw), scratch, stream)
 
 
 def floor_empty_pair(a, b, *, pdl: bool = True, stream=None) -> None:

@@ -1,0 +1,150 @@
+// mla_paged.cu -- attention over the 4-bit paged cache: plan, checks and launch
+// (include/mla_paged.h).
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+
+#include "mla_paged.cuh"
+
+namespace mla {
+namespace {
+
+constexpr int kPagedMagic = 0x4d4c5034;                    // "MLP4"
+
+bool off(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to != 0; }
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+float scale_log2(float scale) { return static_cast<float>(scale * 1.4426950408889634); }
+
+int check_shape(const mla_paged_shape* s) {
+    if (!s) return MLA_EINVAL;
+    if (s->batch < 1 || s->batch > 4096 || s->tokens < 1 || s->tokens > MLA_PAGED_MAX_TOKENS) return MLA_EINVAL;
+    if (!(s->scale > 0.f) || !(s->scale < 0x1p60f)) return MLA_EINVAL;
+    if (s->num_sms < 0 || (s->pdl != 0 && s->pdl != 1) || (s->stall_test != 0 && s->stall_test != 1))
+        return MLA_EINVAL;
+    if (s->heads < 1 || s->heads > 128) return MLA_EUNSUPPORTED;
+    return MLA_OK;
+}
+
+// Scratch as of a tree plan: status word, the pairs' merge notes, their pieces and the pieces'
+// log-sum-exps, each region 256-byte aligned.
+constexpr size_t kMergeOffset = 256;
+int pairs_of(int num_sms) { return num_sms < 2 ? 1 : num_sms / 2; }
+void layout(mla_paged_plan_t* pl) {
+    const size_t pairs = static_cast<size_t>(pairs_of(pl->num_sms));
+    pl->grid = static_cast<int>(2 * pairs);
+    pl->status_offset = 0;
+    pl->part_offset = up256(kMergeOffset + pairs * kTreePieces * (sizeof(TreeMerge) + sizeof(TreeCut)));
+    pl->lse_part_offset = pl->part_offset + pairs * kTreePieces * kTreeBlockRows * kDLatent * sizeof(float);
+    pl->scratch_bytes = up256(pl->lse_part_offset + pairs * kTreePieces * kTreeBlockRows * sizeof(float));
+}
+
+int check_plan(const mla_paged_plan_t* pl) {
+    if (!pl || pl->magic != kPagedMagic || check_shape(&pl->shape) != MLA_OK || pl->num_sms < 1) return MLA_EINVAL;
+    mla_paged_plan_t want = *pl;
+    layout(&want);
+    if (pl->grid != want.grid || pl->status_offset != want.status_offset || pl->part_offset != want.part_offset ||
+        pl->lse_part_offset != want.lse_part_offset || pl->scratch_bytes != want.scratch_bytes)
+        return MLA_EINVAL;
+    return MLA_OK;
+}
+
+int check_args(const mla_paged_args* a) {
+    if (!a || !a->q || !a->d_pos || !a->lse || !a->out) return MLA_EINVAL;
+    if (a->window < 0 || a->sink < 0 || (a->out_fp32 != 0 && a->out_fp32 != 1)) return MLA_EINVAL;
+    const int rc = check_cache(&a->cache);
+    if (rc != MLA_OK) return rc;
+    return off(a->q, 16) || off(a->out, 16) || off(a->lse, 4) || off(a->d_pos, 4) || off(a->n_tokens, 4) ? MLA_EALIGN
+                                                                                                         : MLA_OK;
+}
+
+std::atomic<int> g_paged_prepared[kMaxDevices];
+std::mutex g_paged_mutex;
+
+// Kernel attributes, once per device, outside any capture.
+int prepare(cudaStream_t st, bool may_capture) {
+    int dev = 0;
+    const int rc = current_device(&dev);
+    if (rc != MLA_OK) return rc;
+    if (g_paged_prepared[dev].load(std::memory_order_acquire)) return MLA_OK;
+    if (may_capture) {
+        cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+        if (cudaStreamIsCapturing(st, &cs) != cudaSuccess) {
+            cudaGetLastError();
+            return MLA_ECUDA;
+        }
+        if (cs != cudaStreamCaptureStatusNone) return MLA_ENOTREADY;
+    }
+    std::lock_guard<std::mutex> lock(g_paged_mutex);
+    if (launch_status(paged_attend_prepare()) != MLA_OK) return MLA_ECUDA;
+    g_paged_prepared[dev].store(1, std::memory_order_release);
+    return MLA_OK;
+}
+
+PagedParams params(const mla_paged_plan_t* pl, const mla_paged_args* a, void* scratch) {
+    char* base = static_cast<char*>(scratch);
+    PagedParams p{};
+    p.t.a.d_pos = a->d_pos;
+    p.t.a.n_tokens = a->n_tokens;
+    p.t.a.out = a->out;
+    p.t.a.out_fp32 = a->out_fp32;
+    p.t.a.lse = a->lse;
+    p.t.batch = pl->shape.batch;
+    p.t.tokens = pl->shape.tokens;
+    p.t.heads = pl->shape.heads;
+    p.t.clusters = pl->grid / 2;
+    p.t.scale_log2 = scale_log2(pl->shape.scale);
+    p.t.merge = reinterpret_cast<TreeMerge*>(base + kMergeOffset);
+    p.t.cut = reinterpret_cast<TreeCut*>(p.t.merge + kTreePieces * p.t.clusters);
+    p.t.part = reinterpret_cast<float*>(base + pl->part_offset);
+    p.t.lse_part = reinterpret_cast<float*>(base + pl->lse_part_offset);
+    p.t.status = reinterpret_cast<int*>(base + pl->status_offset);
+    p.t.stall_test = pl->shape.stall_test;
+    p.cache = paged_cache(&a->cache);
+    p.q = static_cast<const uint16_t*>(a->q);
+    p.kv_scale = a->cache.kv_scale;
+    p.window = a->window;
+    p.sink = a->sink;
+    return p;
+}
+
+}  // namespace
+}  // namespace mla
+
+extern "C" {
+
+int mla_paged_plan(const mla_paged_shape* shape, mla_paged_plan_t* plan) {
+    if (!plan) return MLA_EINVAL;
+    int rc = mla::check_shape(shape);
+    if (rc != MLA_OK) return rc;
+    mla_paged_plan_t pl{};
+    pl.shape = *shape;
+    pl.magic = mla::kPagedMagic;
+    pl.num_sms = shape->num_sms;
+    if (pl.num_sms == 0) {
+        int dev = 0;
+        rc = mla::current_device(&dev);
+        if (rc == MLA_OK) rc = mla::device_sm_count(dev, &pl.num_sms);
+        if (rc == MLA_OK) rc = mla::prepare(nullptr, false);
+        if (rc != MLA_OK) return rc;
+    }
+    mla::layout(&pl);
+    *plan = pl;
+    return MLA_OK;
+}
+
+int mla_paged_forward(const mla_paged_plan_t* plan, const mla_paged_args* args, void* scratch, size_t scratch_bytes,
+                      void* stream) {
+    int rc = mla::check_plan(plan);
+    if (rc == MLA_OK) rc = mla::check_args(args);
+    if (rc == MLA_OK && (!scratch || mla::off(scratch, 256) || scratch_bytes < plan->scratch_bytes)) rc = MLA_ESCRATCH;
+    if (rc != MLA_OK) return rc;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    rc = mla::prepare(st, true);
+    if (rc != MLA_OK) return rc;
+    return mla::launch_status(
+        mla::launch_paged_attend(mla::params(plan, args, scratch), plan->shape.pdl != 0, st));
+}
+
+}  // extern "C"

@@ -1,0 +1,361 @@
+// mla_paged_append.cu -- new rows of the 4-bit cache and the queries beside them:
+// norms, rotation, quantisation and the write, in one pass; and rows read back
+// (include/mla_paged.h).
+//
+//   x' = x * rstd * w,   rstd = (mean(x^2) + eps)^(-1/2)
+//   block of 16: s = E4M3(max|x'| / (6 kv_scale)),  code = E2M1(x' / (s kv_scale))
+//
+// A value next to a border between two codes falls to the side that the last bit of
+// rstd says, and one code more or less is a third of the value.  So rstd is the fp32
+// number next to the exact one: the sum of squares is kept as a pair of fp32
+// numbers (squares of bf16 values are exact in fp32; the pair's sums, Knuth's two-sum,
+// lose 2^-48), and the reciprocal root is corrected once with the residual 1 - m r^2,
+// taken exactly with fma.  The products x * rstd * w are rounded one after the other.
+//
+// Bound: bytes (128 in and 128 out per query head; 1152 in and 416 out per row).  Warps work
+// alone, as in mla_rope.cu: a warp takes up to 32 heads of one token, eight lanes a head, or
+// the token's row, of which a lane has 16 consecutive latent values: a block with its scale.
+#include <cmath>
+#include <cstdint>
+
+#include <cuda_fp8.h>
+
+#include "device_utils.cuh"
+#include "mla_q4.cuh"
+#include "mla_rope.cuh"
+
+namespace mla {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kHeadPasses = 8;                             // of four heads each, per warp
+
+// (hi, lo) += x, hi + lo exact but for what leaves lo.
+__device__ __forceinline__ void two_add(float& hi, float& lo, float x) {
+    const float s = __fadd_rn(hi, x);
+    const float t = __fsub_rn(s, hi);
+    lo += __fadd_rn(__fsub_rn(hi, __fsub_rn(s, t)), __fsub_rn(x, t));
+    hi = s;
+}
+// The fp32 number next to (hi + lo)^(-1/2).
+__device__ __forceinline__ float rsqrt_pair(float hi, float lo) {
+    const float r = rsqrtf(hi);
+    if (!(hi > 0x1p-120f && hi < 0x1p120f)) return r;      // (0, infinity, NaN: as rsqrt; no bits to win at the ends)
+    const float p = __fmul_rn(r, r), pe = fmaf(r, r, -p);
+    const float h = __fmul_rn(hi, p), he = fmaf(hi, p, -h);
+    const float e = __fsub_rn(1.f, h) - he - fmaf(hi, pe, __fmul_rn(lo, p));
+    return fmaf(0.5f * r, e, r);
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+// Eight values as E2M1, the first in the low bits.
+__device__ __forceinline__ uint32_t narrow_e2m1(const float* v) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(r)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return r;
+}
+
+// Norm of 64 elements in eight lanes (each lane its unit's eight; the sum is that of all lanes
+// with the same lane / 8).
+__device__ __forceinline__ void norm_unit(float (&f)[8], const float (&w)[8], float eps) {
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum = fmaf(f[i], f[i], sum);
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float r = rsqrtf(fmaf(sum, 1.f / kDRope, eps));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = f[i] * r * w[i];
+}
+
+struct AppendParams4 {
+    mla_paged_append_args a;
+    PagedCache cache;
+    float kv_scale, sixth;                                 // 1 / (6 kv_scale)
+};
+
+__global__ void __launch_bounds__(kThreads) mla_paged_append_kernel(const __grid_constant__ AppendParams4 p,
+                                                                    int units_per_token) {
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const mla_paged_append_args& a = p.a;
+    const int lane = threadIdx.x & 31;
+    const int w = static_cast<int>(blockIdx.x) * (kThreads / 32) + static_cast<int>(threadIdx.x >> 5);
+    const int n = w / units_per_token, part = w - n * units_per_token;
+    const int b = blockIdx.y;
+    if (n >= a.tokens || (a.n_tokens && n >= a.n_tokens[b])) return;
+    const int half = a.rot_dim >> 1;
+    const int u = lane & 7;
+    const int pos = a.positions[static_cast<long long>(b) * a.tokens + n];
+    const bool rotated = 4 * u < half;                     // half is a multiple of 4: a unit whole or not at all
+    int lo, hi;
+    unit_offsets(u, half, a.interleaved, lo, hi);
+    if (p.cache.pages && part == units_per_token - 1) {
+        // ---- the row
+        const int d = a.d_pos[b];
+        const long long t = static_cast<long long>(d) + n;
+        if (d < 0 || t >= paged_rows(p.cache)) return;     // uniform over the warp, as the next
+        const int page = page_of(p.cache, b, static_cast<int>(t));
+        if (page < 0) return;
+        uint8_t* row = row_in(p.cache, page, static_cast<int>(t));
+        const uint4* c = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.c) + b * a.c_batch +
+                                                        n * a.c_token) + 2 * lane;
+        const uint4 v0 = c[0], v1 = c[1];
+        uint4 k = make_uint4(0, 0, 0, 0);
+        if (lane < 8)
+            k = load_unit(static_cast<const uint16_t*>(a.k_rope) + b * a.k_rope_batch + n * a.k_rope_token, lo, hi);
+        float sn0, cs0, cs[4], sn[4];
+        pair_angle(pos, a.turns, half, a.amplitude, lane, sn0, cs0);
+        unit_angles(u, sn0, cs0, cs, sn);
+        float f[16];
+        {
+            float x[8];
+            widen8(v0, x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = x[i];
+            widen8(v1, x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[8 + i] = x[i];
+        }
+        if (a.c_norm) {
+            float sum = 0.f, low = 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) two_add(sum, low, __fmul_rn(f[i], f[i]));
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                // (each pair of lanes adds the larger lane's numbers to the smaller's: the same in both)
+                const float s = __shfl_xor_sync(0xffffffffu, sum, o), l = __shfl_xor_sync(0xffffffffu, low, o);
+                const bool up = lane & o;
+                float x = up ? s : sum, xl = up ? l : low;
+                two_add(x, xl, up ? sum : s);
+                sum = x;
+                low = xl + (up ? low : l);
+            }
+            sum *= 1.f / kDLatent;
+            low *= 1.f / kDLatent;
+            two_add(sum, low, a.eps);
+            const float r = rsqrt_pair(sum, low);
+            const uint4* g = static_cast<const uint4*>(a.c_norm) + 2 * lane;
+            const uint4 g0 = g[0], g1 = g[1];
+            float x[8];
+            widen8(g0, x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = __fmul_rn(__fmul_rn(f[i], r), x[i]);
+            widen8(g1, x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[8 + i] = __fmul_rn(__fmul_rn(f[8 + i], r), x[i]);
+        }
+        float top = fabsf(f[0]);
+#pragma unroll
+        for (int i = 1; i < 16; ++i) top = max_nan(top, fabsf(f[i]));
+        const uint8_t scale =
+            __nv_cvt_float_to_fp8(__fmul_rn(top, p.sixth), __NV_SATFINITE, __NV_E4M3);   // NaN stays NaN
+        const float step = __fmul_rn(__low2float(__half2(__nv_cvt_fp8_to_halfraw(scale, __NV_E4M3), __half())), p.kv_scale);
+        const float inv = step > 0.f ? __frcp_rn(step) : 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f[i] = __fmul_rn(f[i], inv);
+        reinterpret_cast<uint2*>(row)[lane] = make_uint2(narrow_e2m1(f), narrow_e2m1(f + 8));
+        row[kQ4Scales + lane] = scale;
+        float x[8];
+        widen8(k, x);
+        if (a.k_norm) {
+            float g[8];
+            widen8(load_unit(static_cast<const uint16_t*>(a.k_norm), lo, hi), g);
+            norm_unit(x, g, a.eps);
+        }
+        if (rotated) rotate_unit(x, a.interleaved, cs, sn);
+        if (lane < 8) {
+            const uint4 o = narrow8(x);
+            uint16_t* dst = reinterpret_cast<uint16_t*>(row + kQ4Rope);
+            *reinterpret_cast<uint2*>(dst + lo) = make_uint2(o.x, o.y);
+            *reinterpret_cast<uint2*>(dst + hi) = make_uint2(o.z, o.w);
+        }
+        return;
+    }
+    // ---- up to 32 heads of the token: all loads before the angles
+    uint4 v[kHeadPasses];
+    const int h0 = kHeadPasses * 4 * part + (lane >> 3);
+    const uint16_t* src = static_cast<const uint16_t*>(a.q_rope) + b * a.q_rope_batch + n * a.q_rope_token;
+#pragma unroll
+    for (int j = 0; j < kHeadPasses; ++j) {
+        v[j] = make_uint4(0, 0, 0, 0);
+        if (h0 + 4 * j < a.heads) {
+            const uint16_t* q = src + (h0 + 4 * j) * a.q_rope_head;
+            v[j] = a.interleaved ? *reinterpret_cast<const uint4*>(q + lo) : load_unit(q, lo, hi);
+        }
+    }
+    float sn0, cs0, cs[4], sn[4], g[8];
+    pair_angle(pos, a.turns, half, a.amplitude, lane, sn0, cs0);
+    unit_angles(u, sn0, cs0, cs, sn);
+    if (a.q_norm) widen8(load_unit(static_cast<const uint16_t*>(a.q_norm), lo, hi), g);
+    uint16_t* dst = static_cast<uint16_t*>(a.q_out) + b * a.q_out_batch + n * a.q_out_token;
+#pragma unroll
+    for (int j = 0; j < kHeadPasses; ++j) {
+        if (kHeadPasses * 4 * part + 4 * j >= a.heads) break;   // uniform over the warp
+        float f[8];
+        widen8(v[j], f);
+        if (a.q_norm) norm_unit(f, g, a.eps);
+        if (rotated) rotate_unit(f, a.interleaved, cs, sn);
+        if (h0 + 4 * j < a.heads) {
+            const uint4 o = narrow8(f);
+            uint16_t* q = dst + (h0 + 4 * j) * a.q_out_head;
+            if (a.interleaved) {
+                *reinterpret_cast<uint4*>(q + lo) = o;
+            } else {
+                *reinterpret_cast<uint2*>(q + lo) = make_uint2(o.x, o.y);
+                *reinterpret_cast<uint2*>(q + hi) = make_uint2(o.z, o.w);
+            }
+        }
+    }
+}
+
+struct ReadParams {
+    mla_paged_read_args a;
+    PagedCache cache;
+    float kv_scale;
+};
+
+// A warp per row: a lane has a block of 16 values, and two of the 64 key values.
+__global__ void __launch_bounds__(kThreads) mla_paged_read_kernel(const __grid_constant__ ReadParams p) {
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const int lane = threadIdx.x & 31;
+    const int n = static_cast<int>(blockIdx.x) * (kThreads / 32) + static_cast<int>(threadIdx.x >> 5);
+    const int b = blockIdx.y;
+    if (n >= p.a.rows || (p.a.n_rows && n >= p.a.n_rows[b])) return;
+    const long long t = static_cast<long long>(p.a.first ? p.a.first[b] : 0) + n;
+    const int page = t >= 0 && t < paged_rows(p.cache) ? page_of(p.cache, b, static_cast<int>(t)) : -1;
+    uint16_t* out = static_cast<uint16_t*>(p.a.out) + b * p.a.out_batch + n * p.a.out_row;
+    uint32_t o[8], key = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = 0;
+    if (page >= 0) {
+        const uint8_t* row = row_in(p.cache, page, static_cast<int>(t));
+        const uint2 w = reinterpret_cast<const uint2*>(row)[lane];
+        const uint8_t scale = row[kQ4Scales + lane];
+        key = reinterpret_cast<const uint32_t*>(row + kQ4Rope)[lane];
+        const uint32_t s = widen_e4m3(static_cast<uint16_t>(scale | scale << 8));
+        uint32_t h[8];
+        widen_e2m1(w.x, reinterpret_cast<uint32_t(&)[4]>(h[0]));
+        widen_e2m1(w.y, reinterpret_cast<uint32_t(&)[4]>(h[4]));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 v = f16x2_to_float2(mul_f16x2(h[i], s));   // exact
+            o[i] = pack_bf16x2(v.x * p.kv_scale, v.y * p.kv_scale);
+        }
+    }
+    uint4* dst = reinterpret_cast<uint4*>(out) + 2 * lane;
+    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    reinterpret_cast<uint32_t*>(out + kDLatent)[lane] = key;
+}
+
+bool off(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to != 0; }
+bool off8(long long stride) { return stride % 8 != 0; }
+
+int check(const mla_paged_append_args* a) {
+    if (!a || a->batch < 1 || a->batch > 65535 || a->tokens < 1 || a->tokens > (1 << 28)) return MLA_EINVAL;
+    if (a->heads < 0 || a->heads > 128) return MLA_EUNSUPPORTED;
+    if (a->rot_dim < 8 || a->rot_dim > 64 || a->rot_dim % 8 != 0) return MLA_EUNSUPPORTED;
+    if (a->interleaved != 0 && a->interleaved != 1) return MLA_EINVAL;
+    if (!(a->amplitude > 0.f) || !std::isfinite(a->amplitude)) return MLA_EINVAL;
+    if (!(a->eps >= 0.f) || !std::isfinite(a->eps)) return MLA_EINVAL;
+    if (!a->turns || !a->positions) return MLA_EINVAL;
+    const bool rows = a->cache.pages != nullptr;
+    if (rows ? (!a->c || !a->k_rope || !a->d_pos) : (a->c || a->k_rope || a->d_pos || a->c_norm || a->k_norm))
+        return MLA_EINVAL;
+    if (!rows && a->heads == 0) return MLA_EINVAL;
+    if (a->heads > 0 ? (!a->q_rope || !a->q_out) : (a->q_rope || a->q_out || a->q_norm)) return MLA_EINVAL;
+    if (rows) {
+        const int rc = check_cache(&a->cache);
+        if (rc != MLA_OK) return rc;
+        if (off(a->c, 16) || off(a->k_rope, 16) || off8(a->c_batch) || off8(a->c_token) || off8(a->k_rope_batch) ||
+            off8(a->k_rope_token) || off(a->d_pos, 4) || off(a->c_norm, 16) || off(a->k_norm, 16))
+            return MLA_EALIGN;
+    }
+    if (a->heads > 0 &&
+        (off(a->q_rope, 16) || off(a->q_out, 16) || off8(a->q_rope_batch) || off8(a->q_rope_token) ||
+         off8(a->q_rope_head) || off8(a->q_out_batch) || off8(a->q_out_token) || off8(a->q_out_head) ||
+         off(a->q_norm, 16)))
+        return MLA_EALIGN;
+    if (off(a->turns, 8) || off(a->positions, 4) || off(a->n_tokens, 4)) return MLA_EALIGN;
+    return MLA_OK;
+}
+
+int launch_blocks(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, long long warps, int batch, void* stream) {
+    const long long per = kThreads / 32, blocks = (warps + per - 1) / per;
+    if (blocks > 0x7fffffffLL) return MLA_EINVAL;
+    attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr->val.programmaticStreamSerializationAllowed = 1;
+    cfg->gridDim = dim3(static_cast<unsigned>(blocks), batch);
+    cfg->blockDim = dim3(kThreads);
+    cfg->stream = static_cast<cudaStream_t>(stream);
+    cfg->attrs = attr;
+    cfg->numAttrs = 1;
+    return MLA_OK;
+}
+
+}  // namespace
+
+int check_cache(const mla_paged_cache* c) {
+    if (!c->pages || !c->page_table || c->n_pages < 1 || c->columns < 1) return MLA_EINVAL;
+    if (c->page_rows < 8 || c->page_rows > 1024 || (c->page_rows & (c->page_rows - 1)) != 0) return MLA_EINVAL;
+    if (static_cast<long long>(c->columns) * c->page_rows > 0x7fffff00LL) return MLA_EINVAL;
+    if (c->page_stride < static_cast<long long>(c->page_rows) * MLA_Q4_ROW) return MLA_EINVAL;
+    int e = 0;
+    if (!(c->kv_scale >= 0x1p-64f) || !(c->kv_scale <= 0x1p64f) || std::frexp(c->kv_scale, &e) != 0.5f) return MLA_EINVAL;
+    if (c->page_stride % 16 != 0 || off(c->pages, 16) || off(c->page_table, 4)) return MLA_EALIGN;
+    return MLA_OK;
+}
+
+PagedCache paged_cache(const mla_paged_cache* c) {
+    PagedCache p{static_cast<uint8_t*>(c->pages), c->page_stride, c->page_table, c->n_pages, c->columns, 0};
+    while ((1 << p.row_shift) < c->page_rows) ++p.row_shift;
+    return p;
+}
+
+}  // namespace mla
+
+extern "C" int mla_paged_append(const mla_paged_append_args* args, void* stream) {
+    int rc = mla::check(args);
+    if (rc != MLA_OK) return rc;
+    mla::AppendParams4 p{*args, {}, 1.f, 1.f};
+    if (args->cache.pages) {
+        p.cache = mla::paged_cache(&args->cache);
+        p.kv_scale = args->cache.kv_scale;
+        p.sixth = static_cast<float>(1.0 / 6.0 / args->cache.kv_scale);
+    }
+    const int units = (args->heads + 4 * mla::kHeadPasses - 1) / (4 * mla::kHeadPasses) + (args->cache.pages ? 1 : 0);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    rc = mla::launch_blocks(&cfg, &attr, static_cast<long long>(args->tokens) * units, args->batch, stream);
+    if (rc != MLA_OK) return rc;
+    return mla::launch_status(cudaLaunchKernelEx(&cfg, mla::mla_paged_append_kernel, p, units));
+}
+
+extern "C" int mla_paged_read(const mla_paged_read_args* args, void* stream) {
+    if (!args || args->batch < 1 || args->batch > 65535 || args->rows < 1 || args->rows > (1 << 28) || !args->out)
+        return MLA_EINVAL;
+    int rc = mla::check_cache(&args->cache);
+    if (rc != MLA_OK) return rc;
+    if (args->out_row < MLA_D_ROW) return MLA_EINVAL;
+    if (mla::off(args->out, 16) || mla::off8(args->out_batch) || mla::off8(args->out_row) || mla::off(args->first, 4) ||
+        mla::off(args->n_rows, 4))
+        return MLA_EALIGN;
+    const mla::ReadParams p{*args, mla::paged_cache(&args->cache), args->cache.kv_scale};
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    rc = mla::launch_blocks(&cfg, &attr, args->rows, args->batch, stream);
+    if (rc != MLA_OK) return rc;
+    return mla::launch_status(cudaLaunchKernelEx(&cfg, mla::mla_paged_read_kernel, p));
+}

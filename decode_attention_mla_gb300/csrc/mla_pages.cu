@@ -1,0 +1,496 @@
+// mla_pages.cu -- the pages of a cache: forked, copied, reserved, freed and
+// compacted on the device (include/mla_paged.h).
+//
+// fork.  A page's references follow from the new tables alone, so there is no list of
+// free pages to keep: refs are counted anew, and the free pages are those without
+// any.  Three launches: clear; every request's entries, counted with atomics (sums and
+// minima of integers: the same in any order), by whose last block the pages are handed
+// out (one block: its scan of refs ends as soon as it has found enough free pages);
+// then the tables written and the shared last pages copied.  The new table waits in
+// scratch, since a request's row may be another's parent.
+//
+// compact.  Ranks of the pages in use by a two-level count; the k-th page in use
+// behind the front goes to the k-th hole in it.  Three launches: counts per 4096 pages;
+// lists of holes and moving pages; moves, tables and references.
+//
+// Bound: bytes (tables and references, and the rows that are copied), below that the
+// launches.
+#include <algorithm>
+#include <cstdint>
+
+#include "device_utils.cuh"
+#include "mla_internal.h"
+#include "mla_paged.h"
+
+namespace mla {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kPlaceThreads = 1024;
+constexpr int kChunk = 4096;                               // pages per block of the counts
+constexpr int kNobody = 0x7fffffff;
+
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+struct ForkParams {
+    mla_pages_fork_args a;
+    int shift;                                             // log2(page_rows)
+    int blocks;                                            // of the counting launch
+    int* table;                                            // [B][columns] the new table
+    int* keeper;                                           // [n_pages] first request that ends in the page
+    int* rows;                                             // [B] n
+    int* first;                                            // [B] pages taken by the requests before
+    int* src;                                              // [B] page to copy, or -1
+    int* dst;                                              // [B]
+    int* free;                                             // pages taken, in order
+    int* ticket;
+};
+
+// Rows that request b goes on with, and its parent (-1: it ends).
+__device__ __forceinline__ int fork_rows(const ForkParams& p, int b, int& parent) {
+    parent = p.a.parent ? p.a.parent[b] : b;
+    if (parent < 0 || parent >= p.a.batch) {
+        parent = -1;
+        return 0;
+    }
+    const int n = max(p.a.d_pos[parent], 0);
+    return min(min(n, p.a.rows ? max(p.a.rows[b], 0) : n), p.a.columns << p.shift);
+}
+// Column behind the last one that request b reserves, n rows kept.
+__device__ __forceinline__ int fork_end(const ForkParams& p, int n) {
+    const long long rows = static_cast<long long>(n) + p.a.reserve + (1 << p.shift) - 1;
+    return static_cast<int>(min(rows >> p.shift, static_cast<long long>(p.a.columns)));
+}
+
+__global__ void __launch_bounds__(kThreads) mla_fork_clear_kernel(const __grid_constant__ ForkParams p) {
+    grid_dependency_wait();
+    allow_dependent_launch();
+    for (int i = blockIdx.x * kThreads + threadIdx.x; i < p.a.n_pages; i += gridDim.x * kThreads) {
+        p.a.refs[i] = 0;
+        p.keeper[i] = kNobody;
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0;
+}
+
+// Inclusive sum over the block; `total`: of all.
+__device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+    }
+    __syncthreads();                                       // (the sums of the scan before have been read)
+    if (lane == 31) warp_sums[warp] = v;
+    __syncthreads();
+    int before = 0;
+    total = 0;
+    for (int w = 0; w < warps; ++w) {
+        if (w < warp) before += warp_sums[w];
+        total += warp_sums[w];
+    }
+    return v + before;
+}
+
+// Hand out pages (one block).
+__device__ void fork_place(const ForkParams& p) {
+    __shared__ int sums[32];
+    const int batch = p.a.batch, columns = p.a.columns;
+    // ---- what each request needs: a copy of its last page, pages behind it
+    int needed = 0;
+    for (int b0 = 0; b0 < batch; b0 += kPlaceThreads) {
+        const int b = b0 + threadIdx.x;
+        int need = 0, from = -1;
+        if (b < batch) {
+            int parent;
+            const int n = __ldcg(p.rows + b);
+            fork_rows(p, b, parent);
+            const int end = parent < 0 ? 0 : fork_end(p, n);
+            const int part = n & ((1 << p.shift) - 1), last = n >> p.shift;
+            need = max(0, end - last);
+            if (part) {
+                const int page = __ldcg(p.table + static_cast<long long>(b) * columns + last);
+                if (page >= 0) {
+                    if (__ldcg(p.a.refs + page) > 0 || __ldcg(p.keeper + page) != b)
+                        from = page;
+                    else
+                        --need;                            // it stays
+                }
+            }
+            p.src[b] = from;
+        }
+        int total;
+        const int incl = block_scan(need, sums, total);
+        if (b < batch) p.first[b] = needed + incl - need;
+        needed += total;
+    }
+    __syncthreads();
+    // ---- last pages that stay
+    for (int b = threadIdx.x; b < batch; b += kPlaceThreads) {
+        const int n = __ldcg(p.rows + b), part = n & ((1 << p.shift) - 1);
+        if (part == 0 || p.src[b] >= 0) continue;
+        const int page = __ldcg(p.table + static_cast<long long>(b) * columns + (n >> p.shift));
+        if (page >= 0) p.a.refs[page] = 1;
+    }
+    __syncthreads();
+    // ---- the first free pages
+    int found = 0;
+    for (int i0 = 0; i0 < p.a.n_pages && found < needed; i0 += 4 * kPlaceThreads) {
+        const int i = i0 + 4 * threadIdx.x;
+        bool is[4];
+        int mine = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            is[k] = i + k < p.a.n_pages && __ldcg(p.a.refs + i + k) == 0;
+            mine += is[k];
+        }
+        int total;
+        int at = found + block_scan(mine, sums, total) - mine;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (is[k]) {
+                if (at < needed) p.free[at] = i + k;
+                ++at;
+            }
+        found += total;
+    }
+    const int have = min(found, needed);
+    __syncthreads();
+    // ---- and who gets them
+    for (int b = threadIdx.x; b < batch; b += kPlaceThreads) {
+        int parent;
+        const int n = __ldcg(p.rows + b);
+        fork_rows(p, b, parent);
+        const int end = parent < 0 ? 0 : fork_end(p, n);
+        const int part = n & ((1 << p.shift) - 1), last = n >> p.shift;
+        int* row = p.table + static_cast<long long>(b) * columns;
+        int at = p.first[b], to = -1, rows = n;
+        for (int c = last; c < end; ++c) {
+            if (c == last && part && p.src[b] < 0 && __ldcg(row + c) >= 0) continue;   // it stays
+            const int page = at < have ? p.free[at] : -1;
+            ++at;
+            if (page >= 0) p.a.refs[page] = 1;
+            row[c] = page;
+            if (c == last && p.src[b] >= 0) {
+                to = page;
+                if (page < 0) rows = n - part;
+            }
+        }
+        p.dst[b] = to;
+        p.rows[b] = rows;
+    }
+    if (threadIdx.x == 0) *p.a.missing = needed - have;
+}
+
+// A request's entries, kThreads * 4 columns a block; the last block hands out pages.
+__global__ void __launch_bounds__(kPlaceThreads) mla_fork_count_kernel(const __grid_constant__ ForkParams p) {
+    __shared__ int is_last;
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const int b = blockIdx.y, ps = 1 << p.shift;
+    int parent;
+    const int n = fork_rows(p, b, parent);
+    for (int c = blockIdx.x * kPlaceThreads + threadIdx.x; c < p.a.columns; c += gridDim.x * kPlaceThreads) {
+        int page = -1;
+        const long long t0 = static_cast<long long>(c) << p.shift, t1 = t0 + ps;
+        if (t0 < n) {
+            page = p.a.page_table[static_cast<long long>(parent) * p.a.columns + c];
+            if (page < 0 || page >= p.a.n_pages) page = -1;
+            // (no later token attends rows up to n - window)
+            if (p.a.window > 0 && t0 >= p.a.sink && t1 <= static_cast<long long>(n) + 1 - p.a.window) page = -1;
+            if (page >= 0) {
+                if (t1 <= n)
+                    atomicAdd(p.a.refs + page, 1);
+                else
+                    atomicMin(p.keeper + page, b);
+            }
+        }
+        p.table[static_cast<long long>(b) * p.a.columns + c] = page;
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.rows[b] = n;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) is_last = atomicAdd(p.ticket, 1) == p.blocks - 1;
+    __syncthreads();
+    if (!is_last) return;
+    __threadfence();
+    fork_place(p);
+}
+
+__device__ __forceinline__ void copy_units(uint4* dst, const uint4* src, long long units) {
+    long long i = threadIdx.x;
+    for (; i + 3 * kThreads < units; i += 4 * kThreads) {
+        uint4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = src[i + k * kThreads];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) dst[i + k * kThreads] = v[k];
+    }
+    for (; i < units; i += kThreads) dst[i] = src[i];
+}
+
+// A block per request: its table, its rows, its copied page.
+__global__ void __launch_bounds__(kThreads) mla_fork_write_kernel(const __grid_constant__ ForkParams p) {
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const int b = blockIdx.x;
+    const int n = p.rows[b], from = p.src[b], to = p.dst[b];
+    const long long row = static_cast<long long>(b) * p.a.columns;
+    for (int c = threadIdx.x; c < p.a.columns; c += kThreads) p.a.page_table_out[row + c] = p.table[row + c];
+    if (threadIdx.x == 0) p.a.d_pos_out[b] = n;
+    if (to < 0) return;
+    char* pages = static_cast<char*>(p.a.pages);
+    const int rows = n & ((1 << p.shift) - 1);
+    copy_units(reinterpret_cast<uint4*>(pages + to * p.a.page_stride),
+               reinterpret_cast<const uint4*>(pages + from * p.a.page_stride),
+               static_cast<long long>(rows) * p.a.row_bytes / 16);
+}
+
+// ---- compact --------------------------------------------------------------------
+struct CompactParams {
+    mla_pages_compact_args a;
+    int chunks;
+    int* counts;                                           // [chunks] pages in use
+    int* place;                                            // [n_pages] -1: not in use; its rank among the moving
+                                                           // pages, if it moves
+    int* hole;                                             // [..] by rank: page to fill
+    int* mover;                                            // ... and the page that goes there
+    int* mover_refs;                                       // ... and its references
+    int* moves;                                            // number of them
+};
+
+__global__ void __launch_bounds__(kThreads) mla_compact_count_kernel(const __grid_constant__ CompactParams p) {
+    __shared__ int sums[32];
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const int i0 = blockIdx.x * kChunk;
+    int mine = 0;
+#pragma unroll
+    for (int k = 0; k < kChunk / kThreads; ++k) {
+        const int i = i0 + k * kThreads + threadIdx.x;
+        if (i < p.a.n_pages) mine += p.a.refs[i] > 0;
+    }
+    int total;
+    block_scan(mine, sums, total);
+    if (threadIdx.x == 0) p.counts[blockIdx.x] = total;
+}
+
+__global__ void __launch_bounds__(kThreads) mla_compact_list_kernel(const __grid_constant__ CompactParams p) {
+    __shared__ int sums[32];
+    grid_dependency_wait();
+    allow_dependent_launch();
+    int live = 0, before = 0;                              // pages in use: all, and in the chunks before
+    for (int c0 = 0; c0 < p.chunks; c0 += kThreads) {
+        const int c = c0 + threadIdx.x;
+        const int v = c < p.chunks ? p.counts[c] : 0;
+        int t;
+        block_scan(v, sums, t);
+        live += t;
+        block_scan(c < static_cast<int>(blockIdx.x) ? v : 0, sums, t);
+        before += t;
+    }
+    // pages in use among the first `live`
+    int front = 0;
+    const int edge = live / kChunk;                        // (the chunk that the front ends in)
+    for (int c0 = 0; c0 < edge; c0 += kThreads) {
+        int t;
+        block_scan(c0 + static_cast<int>(threadIdx.x) < edge ? p.counts[c0 + threadIdx.x] : 0, sums, t);
+        front += t;
+    }
+    {
+        int mine = 0, t;
+        for (int i = edge * kChunk + threadIdx.x; i < live; i += kThreads) mine += p.a.refs[i] > 0;
+        block_scan(mine, sums, t);
+        front += t;
+    }
+    // this chunk's pages, sixteen a thread
+    constexpr int kEach = kChunk / kThreads;
+    const int i0 = blockIdx.x * kChunk + threadIdx.x * kEach;
+    int refs[kEach], mine = 0, t;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+        refs[k] = i0 + k < p.a.n_pages ? p.a.refs[i0 + k] : 0;
+        mine += refs[k] > 0;
+    }
+    int rank = before + block_scan(mine, sums, t) - mine;  // pages in use before i
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+        const int i = i0 + k;
+        if (i >= p.a.n_pages) break;
+        if (refs[k] > 0) {
+            p.place[i] = rank - front;                     // (used for i >= live alone)
+            if (i >= live) {
+                p.mover[rank - front] = i;
+                p.mover_refs[rank - front] = refs[k];
+            } else {
+                p.place[i] = 0;
+            }
+            ++rank;
+        } else {
+            p.place[i] = -1;
+            if (i < live) p.hole[i - rank] = i;
+        }
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        *p.a.used = live;
+        *p.moves = live - front;
+    }
+}
+
+__global__ void __launch_bounds__(kThreads) mla_compact_move_kernel(const __grid_constant__ CompactParams p) {
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const int moves = *p.moves, live = *p.a.used;
+    const long long page = static_cast<long long>(p.a.page_rows) * p.a.row_bytes / 16;
+    char* pages = static_cast<char*>(p.a.pages);
+    for (int k = blockIdx.x; k < moves; k += gridDim.x)
+        copy_units(reinterpret_cast<uint4*>(pages + p.hole[k] * p.a.page_stride),
+                   reinterpret_cast<const uint4*>(pages + p.mover[k] * p.a.page_stride), page);
+    const long long at = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
+    const long long step = static_cast<long long>(gridDim.x) * kThreads;
+    const long long entries = static_cast<long long>(p.a.batch) * p.a.columns;
+    for (long long e = at; e < entries; e += step) {
+        int v = p.a.page_table[e];
+        if (v < 0 || v >= p.a.n_pages) {
+            v = -1;
+        } else {
+            const int place = p.place[v];
+            if (place < 0)
+                v = -1;
+            else if (v >= live)
+                v = p.hole[place];
+        }
+        p.a.page_table_out[e] = v;
+    }
+    // references: of a page that stays its own, of the k-th hole the k-th moving page's
+    for (long long i = at; i < p.a.n_pages; i += step) {
+        if (i >= live)
+            p.a.refs_out[i] = 0;
+        else if (p.place[i] >= 0 && p.a.refs_out != p.a.refs)
+            p.a.refs_out[i] = p.a.refs[i];
+    }
+    for (long long k = at; k < moves; k += step) p.a.refs_out[p.hole[k]] = p.mover_refs[k];
+}
+
+bool off(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to != 0; }
+
+bool sizes_ok(int batch, int columns, int n_pages) {
+    return batch >= 1 && batch <= 4096 && columns >= 1 && n_pages >= 1 && n_pages <= (1 << 30) &&
+           static_cast<long long>(batch) * columns < (1ll << 30);
+}
+
+int check(const void* pages, long long page_stride, int n_pages, int page_rows, int row_bytes, int batch, int columns) {
+    if (!pages || !sizes_ok(batch, columns, n_pages)) return MLA_EINVAL;
+    if (page_rows < 8 || page_rows > 1024 || (page_rows & (page_rows - 1)) != 0) return MLA_EINVAL;
+    if (static_cast<long long>(columns) * page_rows > 0x7fffff00LL) return MLA_EINVAL;
+    if (row_bytes < 16 || row_bytes > 65536 || page_stride < static_cast<long long>(page_rows) * row_bytes)
+        return MLA_EINVAL;
+    return row_bytes % 16 != 0 || page_stride % 16 != 0 || off(pages, 16) ? MLA_EALIGN : MLA_OK;
+}
+
+// Scratch: fork's and compact's arrays, whichever are more.
+size_t fork_bytes(int batch, int columns, int n_pages) {
+    const size_t entries = static_cast<size_t>(batch) * columns;
+    return 256 + up256(4 * entries) + 2 * up256(4 * static_cast<size_t>(n_pages)) + 4 * up256(4 * static_cast<size_t>(batch));
+}
+size_t compact_bytes(int n_pages) {
+    const size_t n = static_cast<size_t>(n_pages);
+    return 256 + up256(4 * ((n + kChunk - 1) / kChunk)) + 4 * up256(4 * n);
+}
+
+struct Carver {
+    char* at;
+    int* take(size_t ints) {
+        int* p = reinterpret_cast<int*>(at);
+        at += up256(4 * ints);
+        return p;
+    }
+};
+
+template <class Params>
+cudaError_t launch(void (*kernel)(Params), dim3 grid, int threads, const Params& p, void* stream) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+}  // namespace
+}  // namespace mla
+
+extern "C" {
+
+size_t mla_pages_scratch_bytes(int batch, int columns, int n_pages) {
+    if (!mla::sizes_ok(batch, columns, n_pages)) return 0;
+    return std::max(mla::fork_bytes(batch, columns, n_pages), mla::compact_bytes(n_pages));
+}
+
+int mla_pages_fork(const mla_pages_fork_args* args, void* scratch, size_t scratch_bytes, void* stream) {
+    using namespace mla;
+    if (!args) return MLA_EINVAL;
+    int rc = check(args->pages, args->page_stride, args->n_pages, args->page_rows, args->row_bytes, args->batch,
+                   args->columns);
+    if (rc != MLA_OK) return rc;
+    if (!args->page_table || !args->d_pos || !args->page_table_out || !args->d_pos_out || !args->refs || !args->missing ||
+        args->reserve < 0 || args->window < 0 || args->sink < 0)
+        return MLA_EINVAL;
+    if (off(args->page_table, 4) || off(args->d_pos, 4) || off(args->parent, 4) || off(args->rows, 4) ||
+        off(args->page_table_out, 4) || off(args->d_pos_out, 4) || off(args->refs, 4) || off(args->missing, 4))
+        return MLA_EALIGN;
+    if (!scratch || off(scratch, 256) || scratch_bytes < fork_bytes(args->batch, args->columns, args->n_pages))
+        return MLA_ESCRATCH;
+    ForkParams p{};
+    p.a = *args;
+    while ((1 << p.shift) < args->page_rows) ++p.shift;
+    Carver c{static_cast<char*>(scratch)};
+    p.ticket = c.take(64);
+    p.table = c.take(static_cast<size_t>(args->batch) * args->columns);
+    p.keeper = c.take(args->n_pages);
+    p.free = c.take(args->n_pages);
+    p.rows = c.take(args->batch);
+    p.first = c.take(args->batch);
+    p.src = c.take(args->batch);
+    p.dst = c.take(args->batch);
+    const dim3 count((args->columns + kPlaceThreads - 1) / kPlaceThreads, args->batch);
+    p.blocks = static_cast<int>(count.x * count.y);
+    const int clear = std::min((args->n_pages + kThreads - 1) / kThreads, 1024);
+    cudaError_t e = launch(mla_fork_clear_kernel, dim3(clear), kThreads, p, stream);
+    if (e == cudaSuccess) e = launch(mla_fork_count_kernel, count, kPlaceThreads, p, stream);
+    if (e == cudaSuccess) e = launch(mla_fork_write_kernel, dim3(args->batch), kThreads, p, stream);
+    return launch_status(e);
+}
+
+int mla_pages_compact(const mla_pages_compact_args* args, void* scratch, size_t scratch_bytes, void* stream) {
+    using namespace mla;
+    if (!args) return MLA_EINVAL;
+    int rc = check(args->pages, args->page_stride, args->n_pages, args->page_rows, args->row_bytes, args->batch,
+                   args->columns);
+    if (rc != MLA_OK) return rc;
+    if (!args->page_table || !args->refs || !args->page_table_out || !args->refs_out || !args->used) return MLA_EINVAL;
+    if (off(args->page_table, 4) || off(args->refs, 4) || off(args->page_table_out, 4) || off(args->refs_out, 4) ||
+        off(args->used, 4))
+        return MLA_EALIGN;
+    if (!scratch || off(scratch, 256) || scratch_bytes < compact_bytes(args->n_pages)) return MLA_ESCRATCH;
+    CompactParams p{};
+    p.a = *args;
+    p.chunks = (args->n_pages + kChunk - 1) / kChunk;
+    Carver c{static_cast<char*>(scratch)};
+    p.moves = c.take(64);
+    p.counts = c.take(p.chunks);
+    p.place = c.take(args->n_pages);
+    p.hole = c.take(args->n_pages);
+    p.mover = c.take(args->n_pages);
+    p.mover_refs = c.take(args->n_pages);
+    cudaError_t e = launch(mla_compact_count_kernel, dim3(p.chunks), kThreads, p, stream);
+    if (e == cudaSuccess) e = launch(mla_compact_list_kernel, dim3(p.chunks), kThreads, p, stream);
+    if (e == cudaSuccess) e = launch(mla_compact_move_kernel, dim3(1216), kThreads, p, stream);
+    return launch_status(e);
+}
+
+}  // extern "C"
