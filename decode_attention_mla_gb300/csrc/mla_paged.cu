@@ -85,22 +85,22 @@ int prepare(cudaStream_t st, bool may_capture) {
 PagedParams params(const mla_paged_plan_t* pl, const mla_paged_args* a, void* scratch) {
     char* base = static_cast<char*>(scratch);
     PagedParams p{};
-    p.t.a.d_pos = a->d_pos;
-    p.t.a.n_tokens = a->n_tokens;
-    p.t.a.out = a->out;
-    p.t.a.out_fp32 = a->out_fp32;
-    p.t.a.lse = a->lse;
-    p.t.batch = pl->shape.batch;
-    p.t.tokens = pl->shape.tokens;
-    p.t.heads = pl->shape.heads;
-    p.t.clusters = pl->grid / 2;
-    p.t.scale_log2 = scale_log2(pl->shape.scale);
-    p.t.merge = reinterpret_cast<TreeMerge*>(base + kMergeOffset);
-    p.t.cut = reinterpret_cast<TreeCut*>(p.t.merge + kTreePieces * p.t.clusters);
-    p.t.part = reinterpret_cast<float*>(base + pl->part_offset);
-    p.t.lse_part = reinterpret_cast<float*>(base + pl->lse_part_offset);
-    p.t.status = reinterpret_cast<int*>(base + pl->status_offset);
-    p.t.stall_test = pl->shape.stall_test;
+    p.a.d_pos = a->d_pos;
+    p.a.n_tokens = a->n_tokens;
+    p.a.out = a->out;
+    p.a.out_fp32 = a->out_fp32;
+    p.a.lse = a->lse;
+    p.batch = pl->shape.batch;
+    p.tokens = pl->shape.tokens;
+    p.heads = pl->shape.heads;
+    p.clusters = pl->grid / 2;
+    p.scale_log2 = scale_log2(pl->shape.scale);
+    p.merge = reinterpret_cast<TreeMerge*>(base + kMergeOffset);
+    p.cut = reinterpret_cast<TreeCut*>(p.merge + kTreePieces * p.clusters);
+    p.part = reinterpret_cast<float*>(base + pl->part_offset);
+    p.lse_part = reinterpret_cast<float*>(base + pl->lse_part_offset);
+    p.status = reinterpret_cast<int*>(base + pl->status_offset);
+    p.stall_test = pl->shape.stall_test;
     p.cache = paged_cache(&a->cache);
     p.q = static_cast<const uint16_t*>(a->q);
     p.kv_scale = a->cache.kv_scale;

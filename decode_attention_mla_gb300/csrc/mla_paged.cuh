@@ -1,4 +1,4 @@
-// mla_paged.cuh -- what the host side and the kernel of the attention over the
+// mla_paged.cuh -- what the host side and the kernels of the attention over the
 // 4-bit paged cache share.
 #pragma once
 
@@ -7,13 +7,37 @@
 
 namespace mla {
 
-struct PagedParams {
-    TreeParams t;                                          // outputs, sizes, pieces and their notes
+struct PagedParams : TreeParams {                          // (of a.*: d_pos, n_tokens, out, out_fp32, lse)
     PagedCache cache;
     const uint16_t* q;
     float kv_scale;
     int window, sink;
 };
+
+// A request's rows, in tiles of kTreeTileKeys, those that no token attends left out: the
+// first `lo` tiles (the rows before `sink`), then those `base` further on; hi: tiles * kTreeTileKeys.
+__device__ __forceinline__ TreeRequest load_tree_request(const PagedParams& p, int b) {
+    TreeRequest r;
+    r.d_pos = p.a.d_pos[b];
+    r.n_tok = p.a.n_tokens ? min(max(p.a.n_tokens[b], 0), p.tokens) : p.tokens;
+    r.base = 0;
+    r.lo = r.hi = 0;
+    if (r.d_pos < 0 || r.n_tok == 0) return r;
+    const int end = static_cast<int>(min(static_cast<long long>(r.d_pos) + r.n_tok, static_cast<long long>(paged_rows(p.cache))));
+    int tiles = (end + kTreeTileKeys - 1) / kTreeTileKeys;
+    if (p.window > 0) {
+        r.lo = min(p.sink / kTreeTileKeys + (p.sink % kTreeTileKeys != 0), tiles);
+        const int first = min(max(max(r.d_pos - p.window + 1, 0) / kTreeTileKeys, r.lo), tiles);
+        r.base = first - r.lo;
+        tiles -= first - r.lo;
+    }
+    r.hi = tiles * kTreeTileKeys;
+    return r;
+}
+// First row of the request's tile.
+__device__ __forceinline__ int tile_row(const TreeRequest& r, int tile) {
+    return (tile < r.lo ? tile : tile + static_cast<int>(r.base)) * kTreeTileKeys;
+}
 
 cudaError_t paged_attend_prepare();
 cudaError_t launch_paged_attend(const PagedParams& p, bool pdl, cudaStream_t stream);

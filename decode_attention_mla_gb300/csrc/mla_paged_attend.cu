@@ -1,105 +1,757 @@
-// mla_paged_attend.cu -- attention over the 4-bit paged cache (include/mla_paged.h).
+// mla_paged_attend.cu -- attention over the 4-bit paged cache on pairs of SMs
+// (tcgen05 cta_group::2, tensor memory), rows widened on their way to the tensor
+// cores (include/mla_paged.h).
 //
-// A warp per query row: a lane has sixteen features (one block of a row) and two of the
-// 64 rotated ones; rows one after the other, a running maximum and sum.
+// The matrices, the split into runs of tiles, the pieces and their merge are those of
+// mla_tree_attend.cu: query rows (token * heads + head) in blocks of 128, 64 per CTA
+// of a pair; tiles of 128 cache rows; S = Q K^T in two tensor-memory buffers, O (64 x
+// 512 fp32 per CTA) in 256 columns; a run of tiles per pair.  What differs:
+//
+// Operands.  A latent value is code * scale * kv_scale; code * scale has six
+// significant bits and lies between 2^-10 and 2688, so it is exact in f16.  Eight warps
+// per CTA take raw bytes from the pages to registers a tile ahead, widen them (one conversion
+// and one product per two values) and write the tiles' operands in the swizzled layout: a warp
+// per slot of K (this CTA's 64 rows, 128 columns) and per slot of V (64 rows, 128 of this CTA's
+// 256 features).  The key values stay bf16 and are multiplied with bf16 queries, into the same
+// accumulators.
+// q_lat goes to f16, the whole query row times a power of two that brings its largest value to
+// 2^14 .. 2^15 (values down to 2^-32 of it stay exact); the scores' factor takes it back.
+//
+// Rounding: P enters the product as one f16 of 2^7 times the probability (relative to the reference,
+// which lags the maximum by 2^8 at most: at most 2^15), 2^-12 each, so bf16 and fp32 outputs are the
+// same product; O and the statistics are fp32, sums use the unrounded probabilities.
+//
+// What a token does not attend must not reach it: masked scores become -infinity and P = 0; the
+// only value of V that is not finite, an E4M3 scale's NaN, becomes 0 there (a token that attends such
+// a row has a NaN score from K, where it stays).  Rows without a page are zeros, and masked: the
+// softmax warps read the tile's page numbers themselves.
+//
+// Bound: the tensor cores (2200 cycles a tile at best), whatever the number of query rows.
+//
+// Every wait is bounded; a wait that runs out raises MLA_EDEVICE in the status word, both CTAs
+// leave their loops and meet at a cluster barrier.
+//
+// Warps of a CTA: 0-7 softmax and epilogue, 8-11 K, 12-15 V (all eight: queries), 16 MMA issue
+// (even CTA; the odd one's writes empty requests) and tensor memory, 17-18 key values.  Barriers that the MMA warp waits
+// on live in the even CTA and take arrivals of both.
+#include <cmath>
+
 #include "mla_paged.cuh"
+#include "tc_pair_utils.cuh"
 
 namespace mla {
 namespace {
 
-constexpr int kThreads = 128;
+using Cursor = TreeCursor<kTreeTileKeys, true, PagedParams>;
 
-__global__ void __launch_bounds__(kThreads) mla_paged_attend_kernel(const __grid_constant__ PagedParams p) {
+constexpr int kSlots = 4;                                  // of K and of V: a tile each
+constexpr uint32_t kSlotBytes = 16384;                     // 2 column chunks of 64 rows x 128 bytes
+constexpr uint32_t kChunkBytes = 8192;
+constexpr uint32_t kQBytes = 9 * kChunkBytes;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
+constexpr int kKeyWarp = 8, kValueWarp = 12, kFillWarps = 8, kMmaWarp = 16;
+constexpr int kRopeWarp = 17, kRopeWarps = 2;
+constexpr int kThreads = 608;
+constexpr int kBarSoftmax = 1;                             // hardware barrier of the softmax warps
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTmemO = 0, kTmemS = 256;               // O: 2 x 128 columns, S: 2 x 64 columns
+constexpr float kRescaleLog2 = 8.0f;                       // move the reference when a max grows past 2^8
+constexpr float kProbLog2 = 7.0f;                          // P is held times 2^7
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr long long kDrainCycles = 2000ll * 1000ll;        // about 1 ms: time for MMAs in flight after an abort
+
+struct __align__(1024) Shared {
+    uint8_t k[kSlots][kSlotBytes];                         // this CTA's 64 keys x 128 columns, QK operand
+    uint8_t v[kSlots][kSlotBytes];                         // (feature half i, key half kb) at 2 i + kb, PV operand
+    uint8_t rope[kChunkBytes];                             // this CTA's 64 keys, rope columns (bf16)
+    uint8_t q[kQBytes];                                    // 9 chunks of 64 query rows (f16, the last bf16)
+    uint8_t p[2][kChunkBytes];                             // P, 64 rows x 128 keys in two key atoms
+    float red_max[4][64], red_sum[4][64];                  // by quarter of the tile's keys, row
+    int8_t q_exp[4][64];                                   // by item mod 4: a query row is held times 2^-q_exp
+    // used in the even CTA, arrivals of both
+    uint64_t k_ready[kSlots], rope_ready, v_ready[2], q_ready, p_ready, o_free;
+    // in each CTA, arrivals of the MMA thread
+    uint64_t k_empty[kSlots], v_empty[2], q_empty, s_full[2], o_done;
+    // this CTA's query rows are there, by item mod 2 (those of an item may be there before the softmax
+    // warps have come to the one before)
+    uint64_t q_local[2];
+    uint64_t stall_bar;
+    TreeWork work;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+static_assert(sizeof(Shared) <= 227 * 1024, "fits shared memory");
+
+// ============================== operands ==================================
+__device__ __forceinline__ uint4 ld_once_v4(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint32_t low_half_twice(uint32_t v) { return __byte_perm(v, v, 0x1010); }
+__device__ __forceinline__ uint32_t high_half_twice(uint32_t v) { return __byte_perm(v, v, 0x3232); }
+
+// One warp's slot: 64 rows (key half `half` of a tile) x 128 features, from byte `from` of the rows'
+// codes on.  Eight rows (one page) at a time: lane = row + 8 * unit, unit = 32 features.
+struct Slot {
+    uint4 raw[8];
+    uint32_t scales[4];                                    // of two such groups each
+
+    // pg: page number of the eight rows 8 (lane & 7) .. of the half
+    __device__ __forceinline__ void load(const PagedCache& c, int t0, int pg, int from, int lane) {
+        const int unit = lane >> 3, mask = (1 << c.row_shift) - 1;
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            const int page = __shfl_sync(0xffffffffu, pg, n);
+            raw[n] = make_uint4(0, 0, 0, 0);
+            uint32_t two = 0;
+            if (page >= 0) {
+                const uint8_t* row = c.pages + page * c.page_stride + ((t0 + 8 * n + (lane & 7)) & mask) * MLA_Q4_ROW;
+                raw[n] = ld_once_v4(row + from + 16 * unit);
+                two = *reinterpret_cast<const uint16_t*>(row + kQ4Scales + (from >> 3) + 2 * unit);
+            }
+            scales[n >> 1] = n & 1 ? scales[n >> 1] | two << 16 : two;
+        }
+    }
+    // kClean: NaN scales become 0
+    template <bool kClean>
+    __device__ __forceinline__ void store(uint32_t dst, int lane) const {
+        const int unit = lane >> 3, key = lane & 7;
+        const uint32_t line = dst + (unit >> 1) * kChunkBytes + key * 128;
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            uint32_t s = widen_e4m3(static_cast<uint16_t>(scales[n >> 1] >> (16 * (n & 1))));
+            if (kClean) s &= __heq2_mask(*reinterpret_cast<__half2*>(&s), *reinterpret_cast<__half2*>(&s));
+            const uint32_t lo = low_half_twice(s), hi = high_half_twice(s);
+            const uint32_t w[4] = {raw[n].x, raw[n].y, raw[n].z, raw[n].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t h[4];
+                widen_e2m1(w[i], h);
+                const uint32_t f = i < 2 ? lo : hi;
+                st_shared_v4(line + n * 1024 + (((4 * (unit & 1) + i) ^ key) << 4), mul_f16x2(h[0], f), mul_f16x2(h[1], f),
+                             mul_f16x2(h[2], f), mul_f16x2(h[3], f));
+            }
+        }
+    }
+};
+
+// Page number of rows t0 + 8 (lane & 7) .., or -1.
+__device__ __forceinline__ int half_pages(const PagedCache& c, int b, int t0, int lane) {
+    return page_of(c, b, t0 + 8 * (lane & 7));
+}
+
+// Writes that the tensor cores of this SM read: announced to the even CTA's barrier.
+__device__ __forceinline__ void hand_over(uint32_t bar, int lane) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_peer(bar);
+}
+
+// This warp's eight query rows (of the CTA's 64): times a power of two, latents in f16.
+// (A call: its registers are not those of the rows that wait to be stored.)  row0: the first of them, `live`
+// how many there are, at b's queries.
+__device__ __noinline__ void fill_queries(const PagedParams& p, Shared& sh, int b, int row0, int live, int item, int fill,
+                                          int lane) {
+    const uint4* src = reinterpret_cast<const uint4*>(p.q + (static_cast<long long>(b) * p.tokens * p.heads + row0) * kDRow);
+    const float inv_kv = 1.f / p.kv_scale;                 // a power of two
+#pragma unroll 1
+    for (int i0 = 0; i0 < live; i0 += 2) {
+        uint4 x[2][3];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                x[i][k] = make_uint4(0, 0, 0, 0);
+                if (i0 + i < live && (k < 2 || lane < 8)) x[i][k] = src[(i0 + i) * 72 + 32 * k + lane];
+            }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (i0 + i >= live) break;
+            float top = 0.f;
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                const uint32_t w[4] = {x[i][k].x, x[i][k].y, x[i][k].z, x[i][k].w};
+                float m = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
+                top = fmaxf(top, k < 2 ? m : m * inv_kv);
+            }
+            top = warp_max_f32(top);
+            const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127 - 14, -126), 126);
+            const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+            const int row = 8 * fill + i0 + i;
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                if (k == 2 && lane >= 8) break;
+                const uint32_t w[4] = {x[i][k].x, x[i][k].y, x[i][k].z, x[i][k].w};
+                uint32_t o[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float a = __uint_as_float(w[j] << 16) * f, b = __uint_as_float(w[j] & 0xffff0000u) * f;
+                    if (k < 2) {
+                        const __half2 h = __floats2half2_rn(a, b);
+                        o[j] = *reinterpret_cast<const uint32_t*>(&h);
+                    } else {
+                        o[j] = pack_bf16x2(a * inv_kv, b * inv_kv);
+                    }
+                }
+                const int unit = 32 * k + lane;
+                st_shared_v4(smem_u32(sh.q) + (unit >> 3) * kChunkBytes + sw128_offset(row, (unit & 7) * 16), o[0], o[1],
+                             o[2], o[3]);
+            }
+            if (lane == 0) sh.q_exp[item & 3][row] = static_cast<int8_t>(e);
+        }
+    }
+}
+
+// The warps that write operands: kKeys the K slots, the others the V slots.
+template <bool kKeys>
+__device__ void fill(const PagedParams& p, Shared& sh, uint32_t rank, int warp, int lane) {
+    const int slot = warp & 3, nth = warp - kKeyWarp;
+    const int half = kKeys ? static_cast<int>(rank) : slot & 1;
+    const int from = kKeys ? 64 * slot : 128 * (slot >> 1) + 64 * static_cast<int>(rank);
+    const uint32_t leader = map_to_rank(&sh, 0) - smem_u32(&sh);
+    const uint32_t ready = smem_u32(kKeys ? &sh.k_ready[slot] : &sh.v_ready[slot >> 1]) + leader;
+    uint64_t* empty = kKeys ? &sh.k_empty[slot] : &sh.v_empty[slot >> 1];
+    const uint32_t dst = smem_u32(kKeys ? sh.k[slot] : sh.v[slot]);
+    const PagedCache& cache = p.cache;
+    Cursor c;
+    c.start(p, sh.work);
+    if (c.left <= 0) return;
+    Slot s;
+    int t0 = tile_row(c.r, c.tile) + 64 * half;
+    int pg = half_pages(cache, c.b, t0, lane);
+    s.load(cache, t0, pg, from, lane);
+    while (true) {
+        const int g = c.g;
+        if (c.first) {
+            if (c.item > 0 && !warp_wait(&sh.abort_flag, &sh.q_empty, (c.item - 1) & 1)) break;
+            const int row0 = c.rb * kTreeBlockRows + static_cast<int>(rank) * 64 + 8 * nth;
+            fill_queries(p, sh, c.b, row0, min(c.r.n_tok * p.heads - row0, 8), c.item, nth, lane);
+            hand_over(smem_u32(&sh.q_ready) + leader, lane);
+            if (lane == 0) mbar_arrive(&sh.q_local[c.item & 1]);
+        }
+        // the next tile's pages, looked up ahead
+        c.next(p);
+        const bool more = c.left > 0;
+        if (more) {
+            t0 = tile_row(c.r, c.tile) + 64 * half;
+            pg = half_pages(cache, c.b, t0, lane);
+        }
+        if (g > 0 && !warp_wait(&sh.abort_flag, empty, (g - 1) & 1)) break;
+        s.store<!kKeys>(dst, lane);
+        hand_over(ready, lane);
+        if (more) s.load(cache, t0, pg, from, lane);
+        if (!more) return;
+    }
+    if (lane == 0) raise_tree_error(&sh.abort_flag, p.status);
+}
+
+// The key values of this CTA's 64 rows, 32 a warp: as they are, a tile ahead in registers.
+__device__ void fill_rope(const PagedParams& p, Shared& sh, uint32_t rank, int nth, int lane) {
+    const PagedCache& cache = p.cache;
+    const uint32_t ready = map_to_rank(&sh.rope_ready, 0);
+    const int unit = lane & 7, row0 = 32 * nth + (lane >> 3);
+    Cursor c;
+    c.start(p, sh.work);
+    if (c.left <= 0) return;
+    uint4 rope[8];
+    auto load = [&] {
+        const int t0 = tile_row(c.r, c.tile) + 64 * static_cast<int>(rank);
+        const int pg = half_pages(cache, c.b, t0, lane);
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            const int page = __shfl_sync(0xffffffffu, pg, 4 * nth + (n >> 1)), t = t0 + row0 + 4 * n;
+            rope[n] = make_uint4(0, 0, 0, 0);
+            if (page >= 0)
+                rope[n] = ld_once_v4(cache.pages + page * cache.page_stride +
+                                     (t & ((1 << cache.row_shift) - 1)) * MLA_Q4_ROW + kQ4Rope + 16 * unit);
+        }
+    };
+    load();
+    while (true) {
+        const int g = c.g;
+        if (g > 0 && !warp_wait(&sh.abort_flag, &sh.k_empty[kSlots - 1], (g - 1) & 1)) break;
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+            st_shared_v4(smem_u32(sh.rope) + sw128_offset(row0 + 4 * n, unit * 16), rope[n].x, rope[n].y, rope[n].z,
+                         rope[n].w);
+        hand_over(ready, lane);
+        c.next(p);
+        if (c.left <= 0) return;
+        load();
+    }
+    if (lane == 0) raise_tree_error(&sh.abort_flag, p.status);
+}
+
+// ============================== MMA issue ==================================
+// As in mla_tree_attend.cu: one warp issues everything, QK of a tile before PV of the tile
+// before it (after it at an item's first tile), each barrier looked at ahead of its use.
+struct Issue {
+    Shared& sh;
+    bool lead, ok;
+
+    // after `seen` (an earlier look at the barrier): the phase is over
+    __device__ __forceinline__ void need(bool seen, uint64_t* bar, uint32_t parity) {
+        if (!seen) ok = wait_slowly(bar, parity, &sh.abort_flag) && ok;
+    }
+};
+
+__device__ void issue(const PagedParams& p, Shared& sh, uint32_t tmem) {
+    constexpr uint32_t idesc_qk = make_idesc_f16(128, 128, 0, 0), idesc_rope = make_idesc_bf16(128, 128, 0, 0);
+    constexpr uint32_t idesc_pv = make_idesc_f16(128, 256, 0, 1);
+    Issue is{sh, elect_one(), true};
+    const uint64_t kd = make_sdesc(smem_u32(sh.k), 16, 1024, kLayoutSw128);
+    const uint64_t vd = make_sdesc(smem_u32(sh.v), kChunkBytes, 1024, kLayoutSw128);
+    const uint64_t rope = make_sdesc(smem_u32(sh.rope), 16, 1024, kLayoutSw128);
+    const uint64_t q = make_sdesc(smem_u32(sh.q), 16, 1024, kLayoutSw128);
+    const uint64_t pd = make_sdesc(smem_u32(sh.p), 16, 1024, kLayoutSw128);
+    int item = 0, pv_item = -1;
+    Cursor c;                                              // moves from item to item here
+    c.start(p, sh.work);
+    const int total = c.left;
+    int in_item = c.item_left;                             // tiles of the item still to come
+    bool first = true;
+    uint32_t pv_first = 0;                                 // the tile before this QK's was the first of its item
+    bool see_k = false, see_p = false, see_v = false;
+    for (int g = 0; g <= total && is.ok; ++g) {
+        const uint32_t buf = g & 1, par = g & 1;           // of QK(g); PV(g - 1) has the other parity
+        const uint32_t qk_first = first;
+        const int pv_turn = first ? 0 : 1;
+#pragma unroll 1
+        for (int turn = 0; turn < 2; ++turn) {
+            if (turn == pv_turn) {
+                if (g == 0) continue;
+                is.need(see_p, &sh.p_ready, par ^ 1);
+                if (pv_first && ++pv_item > 0) is.need(false, &sh.o_free, (pv_item - 1) & 1);
+                tc_fence_after_sync();
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    is.need(see_v, &sh.v_ready[i], par ^ 1);
+                    if (i == 0)
+                        see_v = mbar_test(&sh.v_ready[1], par ^ 1);
+                    else
+                        see_k = mbar_test(&sh.k_ready[0], par ^ pv_turn);   // of the QK that comes next
+                    if (is.lead && is.ok) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            umma_pair_bf16(tmem + kTmemO + 128 * i, pd + (((k >> 2) * kChunkBytes + (k & 3) * 32u) >> 4),
+                                           vd + (((2 * i + (k >> 2)) * kSlotBytes + (k & 3) * 2048u) >> 4), idesc_pv,
+                                           k == 0 ? pv_first ^ 1u : 1u);
+                        if (g < total) umma_commit_pair(&sh.v_empty[i]);
+                    }
+                }
+                if (is.lead && is.ok) umma_commit_pair(&sh.o_done);
+                see_p = see_v = false;
+            } else {
+                if (g == total) continue;
+                const uint32_t d = tmem + kTmemS + 64 * buf;
+                const bool last = in_item == 1;
+                if (first) is.need(false, &sh.q_ready, item & 1);
+                // (the scores of tile g - 2 have been read: PV(g - 2) waited for their P)
+#pragma unroll
+                for (int s = 0; s < kSlots; ++s) {
+                    is.need(see_k, &sh.k_ready[s], par);
+                    if (s < kSlots - 1) {
+                        see_k = mbar_test(&sh.k_ready[s + 1], par);
+                    } else {
+                        is.need(false, &sh.rope_ready, par);
+                        if (pv_turn == 1 && g >= 1) {
+                            see_p = mbar_test(&sh.p_ready, par ^ 1);
+                            see_v = mbar_test(&sh.v_ready[0], par ^ 1);
+                        }
+                    }
+                    if (s == 0) tc_fence_after_sync();
+                    if (is.lead && is.ok) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const uint32_t off = ((k >> 2) * kChunkBytes + (k & 3) * 32u) >> 4;
+                            umma_pair_bf16(d, q + (2 * s * kChunkBytes >> 4) + off, kd + (s * kSlotBytes >> 4) + off,
+                                           idesc_qk, (s | k) ? 1u : 0u);
+                        }
+                        if (s == 3) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                umma_pair_bf16(d, q + ((8 * kChunkBytes + k * 32u) >> 4), rope + (k * 32u >> 4),
+                                               idesc_rope, 1u);
+                        }
+                        if (g + 1 < total) umma_commit_pair(&sh.k_empty[s]);
+                    }
+                }
+                if (is.lead && is.ok) {
+                    umma_commit_pair(&sh.s_full[buf]);
+                    if (last && g + 1 < total) umma_commit_pair(&sh.q_empty);
+                }
+                see_k = false;
+                first = last;
+                if (--in_item == 0 && g + 1 < total) {
+                    c.g = g + 1;
+                    c.left = total - c.g;
+                    c.next_item(p);
+                    ++item;
+                    in_item = c.item_left;
+                }
+            }
+        }
+        pv_first = qk_first;
+    }
+    if (!is.ok && is.lead) raise_tree_error(&sh.abort_flag, p.status);
+}
+
+// ============================== softmax ====================================
+// Place of a piece's feature quad, as the merge reads it: [slot][32-row group][quad][row].
+__device__ __forceinline__ long long piece_quad(int slot, int row, int quad) {
+    return ((static_cast<long long>(slot) * (kTreeBlockRows / 32) + (row >> 5)) * (kDLatent / 4) + quad) * 32 + (row & 31);
+}
+
+// 64 bytes of each of a warp's 32 rows, through its 2 KB of shared memory so that the stores of a
+// row run along its features (16-byte units, swizzled by row pair).
+__device__ __forceinline__ void store_rows(uint32_t stage, const uint32_t (&w)[16], char* dst, int row_bytes,
+                                           int n_rows, int lane) {
+    __syncwarp();                                          // the reads of the block before are done
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+        st_shared_v4(stage + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4), w[4 * u], w[4 * u + 1], w[4 * u + 2],
+                     w[4 * u + 3]);
+    __syncwarp();
+    const int u = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = 8 * i + (lane >> 2);
+        const uint4 v = ld_shared_v4(stage + row * 64 + ((u ^ ((row >> 1) & 3)) << 4));
+        if (row < n_rows) reinterpret_cast<uint4*>(dst + static_cast<long long>(row) * row_bytes)[u] = v;
+    }
+}
+
+__device__ __forceinline__ uint32_t low_bits32(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; }
+__device__ __forceinline__ int row_int(long long t) { return static_cast<int>(min(max(t, 0ll), 0x7fffffffll)); }
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Thread: 32 keys of one row.  Warps w and w + 4 share tensor-memory lanes 32 (w mod 4) ..
+// and split their columns.
+__device__ void softmax(const PagedParams& p, Shared& sh, uint32_t tmem, uint32_t rank, int cluster, int tid) {
+    const int lane = tid & 31, warp = tid >> 5;
+    const int sub = warp >> 2, half = (warp >> 1) & 1;     // keys 64 half + 32 sub ..; features 256 sub + 128 half ..
+    const int quarter = 2 * half + sub;
+    const int row = 32 * (warp & 1) + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t p_bar = map_to_rank(&sh.p_ready, 0), o_bar = map_to_rank(&sh.o_free, 0);
+    const uint32_t p_line = smem_u32(sh.p[half]) + row * 128;
+    bool ok = true, bad = false;
+    const bool notes = rank == 0 && tid == 0;
+    if (notes)
+        for (int i = 0; i < kTreePieces; ++i) p.merge[i * p.clusters + cluster].pieces = 0;
+    Cursor c;
+    c.start(p, sh.work);
+    // whether rows 8 (lane & 15) .. of the tile have a page, looked up a tile ahead
+    int pages = 0;
+    if (c.left > 0) pages = page_of(p.cache, c.b, tile_row(c.r, c.tile) + 8 * (lane & 15));
+    while (c.left > 0 && ok) {
+        // ---- one item: tiles of one row block
+        const int r = c.rb * kTreeBlockRows + static_cast<int>(rank) * 64 + row;
+        const int live_rows = c.r.n_tok * p.heads;
+        const int b = c.b, rb = c.rb;
+        // this row's token attends rows [from, to) and those before sink
+        const long long own = static_cast<long long>(c.r.d_pos) + r / p.heads;
+        const int to = r < live_rows ? row_int(own + 1) : 0;
+        const int from = p.window > 0 ? row_int(own + 1 - p.window) : 0;
+        // tiles whose rows every token attends: up to all_to, from all_from on or before sink
+        const int all_to = row_int(static_cast<long long>(c.r.d_pos) + 1);
+        const int all_from = p.window > 0 ? row_int(static_cast<long long>(c.r.d_pos) + c.r.n_tok - p.window) : 0;
+        const bool whole = c.whole(), run_first = c.g == 0;
+        const bool opens = !whole && c.seg == 0 && c.opens(), cut = c.sg.count() > 1;
+        const TreeCut of{c.n_rb, c.n_tiles, static_cast<int>(sh.work.per), c.begin};
+        bad |= !warp_wait(&sh.abort_flag, &sh.q_local[c.item & 1], (c.item >> 1) & 1);
+        const float c2 = p.scale_log2 * p.kv_scale *
+                         (r < live_rows ? __uint_as_float(static_cast<uint32_t>(127 + sh.q_exp[c.item & 3][row]) << 23) : 1.f);
+        float m_ref = -INFINITY, l = 0.f;
+        bool last;
+        do {
+            const int g = c.g, buf = g & 1;
+            last = c.last();
+            bool w = warp_wait(&sh.abort_flag, &sh.s_full[buf], (g >> 1) & 1);
+            uint32_t s[32];
+            if (w) {
+                tmem_ld32_async(tmem + lanes + kTmemS + 64 * buf + 32 * sub, s);
+                tmem_wait_ld32(s);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) s[i] = 0;
+            }
+            const int t0 = tile_row(c.r, c.tile);
+            const uint32_t here = __ballot_sync(0xffffffffu, pages >= 0);
+            if (here != 0xffffffffu || t0 + kTreeTileKeys > all_to || (t0 < all_from && t0 + kTreeTileKeys > p.sink)) {
+                const int t = t0 + 64 * half + 32 * sub;
+                const uint32_t four = here >> (8 * half + 4 * sub) & 15;   // of eight rows each
+                const uint32_t v = low_bits32(to - t) & (~low_bits32(from - t) | low_bits32(p.sink - t)) &
+                                   ((four * 0x00204081u & 0x01010101u) * 0xffu);
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (!(v >> i & 1)) s[i] = 0xff800000u;
+            }
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i]));
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;
+            float alpha = 1.f;
+            bad |= !w;
+            if (named_barrier_or(kBarSoftmax, kSoftmaxThreads, bad || top > m_ref + kRescaleLog2)) {
+                // rare after the first tile: the row's maximum moves the reference
+                sh.red_max[quarter][row] = top;
+                if (named_barrier_or(kBarSoftmax, kSoftmaxThreads, bad)) {
+                    ok = false;
+                    break;
+                }
+                const float tm = fmaxf(fmaxf(sh.red_max[0][row], sh.red_max[1][row]),
+                                       fmaxf(sh.red_max[2][row], sh.red_max[3][row]));
+                if (tm > m_ref + kRescaleLog2) {
+                    if (m_ref > -INFINITY) alpha = ex2_approx(m_ref - tm);
+                    m_ref = tm;
+                }
+                l *= alpha;
+            }
+            const float base = (m_ref > -INFINITY ? m_ref : 0.f) - kProbLog2;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float x = ex2_approx(fmaf(__uint_as_float(s[2 * i]), c2, -base));
+                const float y = ex2_approx(fmaf(__uint_as_float(s[2 * i + 1]), c2, -base));
+                sum[i & 1] += x;
+                sum[2 + (i & 1)] += y;
+                pk[i] = pack_f16x2(x, y);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            // P of the tile before has been read, and O holds all tiles before this one
+            w = g == 0 || warp_wait(&sh.abort_flag, &sh.o_done, (g - 1) & 1);
+            if (w && __any_sync(0xffffffffu, alpha != 1.f)) {   // (never on an item's first tile)
+#pragma unroll 1
+                for (int j = 0; j < 8; ++j) {
+                    float o[16];
+                    const uint32_t at = tmem + lanes + kTmemO + 128 * sub + 16 * j;
+                    tmem_ld16(at, o);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[i] *= alpha;
+                    tmem_st16(at, o);
+                }
+            }
+            // ---- probabilities, f16, K-major lines of 64 keys
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                st_shared_v4(p_line + (((4 * sub + u) ^ (row & 7)) << 4), pk[4 * u], pk[4 * u + 1], pk[4 * u + 2],
+                             pk[4 * u + 3]);
+            fence_proxy_async_smem();
+            tc_fence_before_sync();
+            __syncwarp();
+            bad |= !w;                                     // the threads leave together at the next barrier
+            if (lane == 0 && !bad) mbar_arrive_peer(p_bar);
+            c.next(p);
+            if (c.left > 0) pages = page_of(p.cache, c.b, tile_row(c.r, c.tile) + 8 * (lane & 15));
+        } while (!last);
+        if (!ok) break;
+
+        // ---- epilogue: l of the four quarters, O / l, log-sum-exp
+        sh.red_sum[quarter][row] = l;
+        if (named_barrier_or(kBarSoftmax, kSoftmaxThreads, bad)) {
+            ok = false;
+            break;
+        }
+        const float lt = (sh.red_sum[0][row] + sh.red_sum[1][row]) + (sh.red_sum[2][row] + sh.red_sum[3][row]);
+        const float inv = lt == 0.f ? 0.f : p.kv_scale / lt;
+        const float lse2 = lt == 0.f ? -INFINITY : (m_ref - kProbLog2) + log2f(lt);
+        // place of the piece: the run's first item, one that ends with the run's length, another
+        const int place = run_first ? 0 : c.g == sh.work.per ? 2 : 1, slot = kTreePieces * cluster + place;
+        if (quarter == 0 && r < live_rows) {
+            if (whole)
+                p.a.lse[static_cast<long long>(b) * p.tokens * p.heads + r] = lse2 * kLn2;
+            else
+                p.lse_part[slot * kTreeBlockRows + static_cast<int>(rank) * 64 + row] = lse2;
+        }
+        if (notes && opens) {
+            const int rows = min(kTreeBlockRows, live_rows - rb * kTreeBlockRows);
+            // (an uncut job's pieces lie in the runs from this one to that of its last unit)
+            const int pieces = cut ? -1 : (of.begin + (rb + 1) * of.n_tiles - 1) / of.per + 1;
+            const int at = (cut ? place : 0) * p.clusters + cluster;
+            p.merge[at] = TreeMerge{b, rb, rows | place << 16, pieces};
+            if (cut) p.cut[at] = of;
+        }
+        const bool w = warp_wait(&sh.abort_flag, &sh.o_done, (c.g - 1) & 1);
+        if (named_barrier_or(kBarSoftmax, kSoftmaxThreads, !w)) {
+            ok = false;
+            break;
+        }
+        // (P's buffer is free: the last product is done)
+        const uint32_t stage = smem_u32(sh.p) + warp * 2048;
+        const int row_w = 32 * (warp & 1);                 // this warp's first row of the 64
+        const int n_rows = live_rows - (r - row) - row_w;
+        const int f0 = 256 * sub + 128 * half;             // its first feature
+        float4* piece = reinterpret_cast<float4*>(p.part) +
+                        piece_quad(slot, static_cast<int>(rank) * 64 + row_w, f0 / 4) + lane;
+        const int bytes = p.a.out_fp32 ? 4 : 2;
+        char* out = static_cast<char*>(p.a.out) +
+                    ((static_cast<long long>(b) * p.tokens * p.heads + r - row + row_w) * kDLatent + f0) * bytes;
+#pragma unroll 1
+        for (int j = 0; j < 4 && n_rows > 0; ++j) {        // (the merge reads groups with live rows only)
+            uint32_t o[32];
+            tmem_ld32_async(tmem + lanes + kTmemO + 128 * sub + 32 * j, o);
+            tmem_wait_ld32(o);
+            if (!whole) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    piece[(8 * j + i) * 32] =
+                        make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
+                                    __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
+                continue;
+            }
+            uint32_t x[16];
+            if (!p.a.out_fp32) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    x[i] = pack_bf16x2(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+                store_rows(stage, x, out + 64 * j, 2 * kDLatent, n_rows, lane);
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(o[16 * h + i]) * inv);
+                    store_rows(stage, x, out + 128 * j + 64 * h, 4 * kDLatent, n_rows, lane);
+                }
+            }
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        // O may be overwritten.  (Only if something will wait for it: the closing barrier orders no arrival.)
+        if (lane == 0 && c.left > 0) mbar_arrive_peer(o_bar);
+    }
+    if (!ok && lane == 0) raise_tree_error(&sh.abort_flag, p.status);
+}
+
+// Requests without rows: their tokens' outputs, by the odd CTAs' otherwise idle warp.
+__device__ void write_empty(const PagedParams& p, int cluster, int clusters, int lane) {
+    for (int b = cluster; b < p.batch; b += clusters) {
+        const TreeRequest r = load_tree_request(p, b);
+        if (r.hi > 0 || r.n_tok == 0) continue;
+        const long long row0 = static_cast<long long>(b) * p.tokens * p.heads;
+        const int rows = r.n_tok * p.heads;
+        for (int i = lane; i < rows; i += 32) p.a.lse[row0 + i] = -INFINITY;
+        const int per = p.a.out_fp32 ? 128 : 64;           // 16-byte units per row
+        uint4* o = reinterpret_cast<uint4*>(p.a.out) + row0 * per;
+        for (int i = lane; i < rows * per; i += 32) o[i] = make_uint4(0, 0, 0, 0);
+    }
+}
+
+__device__ __noinline__ void find_work(const PagedParams& p, int cluster, int lane, TreeWork* work) {
+    Cursor::find_work(p, cluster, lane, work);
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    mla_paged_attend_kernel(const __grid_constant__ PagedParams p) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    Shared& sh = *reinterpret_cast<Shared*>(smem_raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int cluster = blockIdx.x >> 1;
+    if (tid == 0) {
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(&sh.k_ready[i], 2);
+            mbar_init(&sh.k_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.v_ready[i], 4);
+            mbar_init(&sh.v_empty[i], 1);
+            mbar_init(&sh.s_full[i], 1);
+        }
+        mbar_init(&sh.rope_ready, 2 * kRopeWarps);
+        mbar_init(&sh.p_ready, 2 * kSoftmaxWarps);
+        mbar_init(&sh.o_done, 1);
+        mbar_init(&sh.q_ready, 2 * kFillWarps);
+        for (int i = 0; i < 2; ++i) mbar_init(&sh.q_local[i], kFillWarps);
+        mbar_init(&sh.o_free, 2 * kSoftmaxWarps);
+        mbar_init(&sh.q_empty, 1);
+        mbar_init(&sh.stall_bar, 1);
+        sh.abort_flag = 0;
+        mbar_init_fence();
+    }
+    __syncwarp();
+    cluster_arrive();                                      // (after this thread's barrier initialisation)
+    if (warp == kMmaWarp) tmem_alloc_pair(&sh.tmem_base, kTmemCols);
     grid_dependency_wait();
     allow_dependent_launch();
-    const int lane = threadIdx.x & 31;
-    const long long row = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-    const int per = p.t.tokens * p.t.heads;
-    const int b = static_cast<int>(row / per), i = static_cast<int>(row - static_cast<long long>(b) * per) / p.t.heads;
-    if (b >= p.t.batch) return;
-    if (p.t.a.n_tokens && i >= p.t.a.n_tokens[b]) return;
-    float q[16], o[16];
-    const uint16_t* src = p.q + row * kDRow;
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-        q[k] = __uint_as_float(static_cast<uint32_t>(src[16 * lane + k]) << 16);
-        o[k] = 0.f;
+    if (warp == kKeyWarp) {
+        find_work(p, cluster, lane, &sh.work);
+    } else if (warp > kKeyWarp && warp < kMmaWarp) {
+        // query rows behind the last one: zeros, so that their scores are finite
+        for (int i = (warp - kKeyWarp - 1) * 32 + lane; i < static_cast<int>(kQBytes / 16); i += 7 * 32)
+            reinterpret_cast<uint4*>(sh.q)[i] = make_uint4(0, 0, 0, 0);
     }
-    const float q0 = __uint_as_float(static_cast<uint32_t>(src[kDLatent + 2 * lane]) << 16);
-    const float q1 = __uint_as_float(static_cast<uint32_t>(src[kDLatent + 2 * lane + 1]) << 16);
-    float m = -INFINITY, l = 0.f;
-    const int d = p.t.a.d_pos[b];
-    const long long last = d < 0 ? -1 : static_cast<long long>(d) + i;
-    const long long recent = p.window > 0 ? last - p.window + 1 : 0;
-    const long long end = min(last + 1, static_cast<long long>(paged_rows(p.cache)));
-    for (long long t = 0; t < end; ++t) {
-        if (t >= p.sink && t < recent) {
-            t = recent - 1;
-            continue;
-        }
-        const int page = page_of(p.cache, b, static_cast<int>(t));
-        if (page < 0) continue;
-        const uint8_t* kv = row_in(p.cache, page, static_cast<int>(t));
-        const uint2 w = reinterpret_cast<const uint2*>(kv)[lane];
-        const uint8_t scale = kv[kQ4Scales + lane];
-        const uint32_t key = reinterpret_cast<const uint32_t*>(kv + kQ4Rope)[lane];
-        const uint32_t s2 = widen_e4m3(static_cast<uint16_t>(scale | scale << 8));
-        uint32_t h[8];
-        widen_e2m1(w.x, reinterpret_cast<uint32_t(&)[4]>(h[0]));
-        widen_e2m1(w.y, reinterpret_cast<uint32_t(&)[4]>(h[4]));
-        float c[16], s = 0.f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float2 v = f16x2_to_float2(mul_f16x2(h[k], s2));
-            c[2 * k] = v.x * p.kv_scale;
-            c[2 * k + 1] = v.y * p.kv_scale;
-            s = fmaf(q[2 * k], c[2 * k], fmaf(q[2 * k + 1], c[2 * k + 1], s));
-        }
-        s = fmaf(q0, __uint_as_float(key << 16), fmaf(q1, __uint_as_float(key & 0xffff0000u), s));
-#pragma unroll
-        for (int x = 16; x >= 1; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        s *= p.t.scale_log2;
-        const float top = fmaxf(m, s);
-        if (s == -INFINITY) continue;
-        const float a = exp2f(m - top), e = exp2f(s - top);
-        m = top;
-        l = l * a + e;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) o[k] = fmaf(e, c[k], o[k] * a);
+    tc_fence_before_sync();
+    __syncthreads();
+    cluster_wait();                                        // both CTAs' barriers are initialised
+    tc_fence_after_sync();
+    const uint32_t tmem = sh.tmem_base;
+    if (p.stall_test && blockIdx.x == 0 && tid == 32 * kKeyWarp) {
+        // test hook: a wait that runs out, so the abort path runs for real
+        volatile int never = 0;
+        if (!mbar_wait_bounded(&sh.stall_bar, 0, &never, kStallTestCycles)) raise_tree_error(&sh.abort_flag, p.status);
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    if (lane == 0) p.t.a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-#pragma unroll
-    for (int k = 0; k < 16; ++k) o[k] *= inv;
-    if (p.t.a.out_fp32) {
-        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.t.a.out) + row * kDLatent) + 4 * lane;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+    __syncwarp();
+    // the dynamic window starts 1024-byte aligned (the 128-byte swizzle needs it)
+    if ((smem_u32(smem_raw) & 1023u) != 0 && tid == 0) raise_tree_error(&sh.abort_flag, p.status);
+    if (warp >= kRopeWarp) {
+        fill_rope(p, sh, rank, warp - kRopeWarp, lane);
+    } else if (warp == kMmaWarp) {
+        if (rank == 0)
+            issue(p, sh, tmem);
+        else
+            write_empty(p, cluster, p.clusters, lane);
+    } else if (warp >= kValueWarp) {
+        fill<false>(p, sh, rank, warp, lane);
+    } else if (warp >= kKeyWarp) {
+        fill<true>(p, sh, rank, warp, lane);
     } else {
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.t.a.out) + row * kDLatent) + 2 * lane;
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-            dst[k] = make_uint4(pack_bf16x2(o[8 * k], o[8 * k + 1]), pack_bf16x2(o[8 * k + 2], o[8 * k + 3]),
-                                pack_bf16x2(o[8 * k + 4], o[8 * k + 5]), pack_bf16x2(o[8 * k + 6], o[8 * k + 7]));
+        softmax(p, sh, tmem, rank, cluster, tid);
+    }
+    __syncthreads();
+    if (*static_cast<volatile int*>(&sh.abort_flag)) {
+        // nothing more is issued by this CTA: let its MMAs end
+        const long long t0 = clock64();
+        while (clock64() - t0 < kDrainCycles) {
+        }
+    }
+    tc_fence_before_sync();
+    cluster_barrier_relaxed();                             // neither CTA's shared memory goes before both are done
+    if (warp == kMmaWarp) {
+        tc_fence_after_sync();
+        tmem_dealloc_pair(tmem, kTmemCols);
     }
 }
 
 }  // namespace
 
-cudaError_t paged_attend_prepare() { return cudaSuccess; }
+cudaError_t paged_attend_prepare() {
+    return cudaFuncSetAttribute(mla_paged_attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(sizeof(Shared)));
+}
 
 cudaError_t launch_paged_attend(const PagedParams& p, bool pdl, cudaStream_t stream) {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    const long long rows = static_cast<long long>(p.t.batch) * p.t.tokens * p.t.heads;
-    cfg.gridDim = dim3(static_cast<unsigned>((rows + kThreads / 32 - 1) / (kThreads / 32)));
+    cfg.gridDim = dim3(2 * p.clusters);
     cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = sizeof(Shared);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, mla_paged_attend_kernel, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, mla_paged_attend_kernel, p);
+    return e != cudaSuccess ? e : launch_tree_merge(p, pdl, stream);
 }
 
 }  // namespace mla

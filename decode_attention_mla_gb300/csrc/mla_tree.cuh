@@ -153,7 +153,8 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
 
 // Walks the tiles of a run.  kByBlocks: a request's jobs are its row blocks;
 // otherwise it has one job, its tiles.  An item is what one run does of a job.
-template <int kKeys, bool kByBlocks>
+// Params: TreeParams, or what is derived from it with a load_tree_request of its own.
+template <int kKeys, bool kByBlocks, class Params = TreeParams>
 struct TreeCursor {
     TreeRequest r;
     TreeSegments sg;
@@ -166,12 +167,12 @@ struct TreeCursor {
     int item;                                              // items before this one
     bool first;                                            // first tile of its item
 
-    static __device__ __forceinline__ int blocks_of(const TreeParams& p, const TreeRequest& r) {
+    static __device__ __forceinline__ int blocks_of(const Params& p, const TreeRequest& r) {
         return kByBlocks ? (r.n_tok * p.heads + kTreeBlockRows - 1) / kTreeBlockRows : 1;
     }
     static __device__ __forceinline__ int tiles_of(const TreeRequest& r) { return (r.hi + kKeys - 1) / kKeys; }
 
-    __device__ __forceinline__ void request(const TreeParams& p) {
+    __device__ __forceinline__ void request(const Params& p) {
         n_rb = blocks_of(p, r);
         n_tiles = tiles_of(r);
         if constexpr (kByBlocks)
@@ -188,7 +189,7 @@ struct TreeCursor {
         hi = lo + item_left;
         tile = kByBlocks && g > 0 && item_left == len ? lo + g % len : lo;
     }
-    __device__ __forceinline__ void start(const TreeParams& p, const TreeWork& w) {
+    __device__ __forceinline__ void start(const Params& p, const TreeWork& w) {
         b = w.b;
         seg = w.seg;
         rb = w.rb;
@@ -205,7 +206,7 @@ struct TreeCursor {
     // the item has its job's first unit; is all of the request's tiles
     __device__ __forceinline__ bool opens() const { return hi == sg.start(seg) + sg.tiles(seg); }
     __device__ __forceinline__ bool whole() const { return hi - lo == n_tiles; }
-    __device__ __forceinline__ void next(const TreeParams& p) {
+    __device__ __forceinline__ void next(const Params& p) {
         ++g;
         --left;
         first = --item_left == 0;
@@ -217,7 +218,7 @@ struct TreeCursor {
         if (left > 0) next_item(p);
     }
     // to the next item's first tile, the g-th of the run (there is one)
-    __device__ __forceinline__ void next_item(const TreeParams& p) {
+    __device__ __forceinline__ void next_item(const Params& p) {
         if (++rb == n_rb) {
             rb = 0;
             if (++seg == sg.count()) {
@@ -239,7 +240,7 @@ struct TreeCursor {
     // tiles for 27, 56 us for 63; 64 requests of 1 x 128 over 4000 70 for 83; 16 of 8 x 128
     // over 500 .. 1400 47 for 57; but 8 of 4 x 64 over 1000, 8 tiles for 2, 20 for 17.)
     // `longest`, `alike`: of the lengths of the first 32 requests.
-    static __device__ __forceinline__ bool keep_whole(const TreeParams& p, const TreeRequest& r, int longest,
+    static __device__ __forceinline__ bool keep_whole(const Params& p, const TreeRequest& r, int longest,
                                                       bool alike, int lane, uint32_t total, uint32_t per) {
         uint32_t blocks = r.hi > 0 ? blocks_of(p, r) : 0;
         if (p.batch > 1) {
@@ -264,7 +265,7 @@ struct TreeCursor {
     }
 
     // The run of the row blocks whose first unit lies in [u0, u1).
-    static __device__ __forceinline__ void find_whole(const TreeParams& p, TreeRequest r, bool one, long long u0,
+    static __device__ __forceinline__ void find_whole(const Params& p, TreeRequest r, bool one, long long u0,
                                                       long long u1, long long total, int lane, TreeWork* out) {
         long long before = 0, s0 = -1, s1 = total;
         for (int b0 = 0; b0 < p.batch; b0 += 32) {
@@ -310,7 +311,7 @@ struct TreeCursor {
     }
 
     // One warp: this cluster's run; run length = ceil(units / clusters).
-    static __device__ void find_work(const TreeParams& p, int cluster, int lane, TreeWork* out) {
+    static __device__ void find_work(const Params& p, int cluster, int lane, TreeWork* out) {
         auto request_of = [&](int b) {
             TreeRequest r{};
             if (b < p.batch) r = load_tree_request(p, b);
@@ -442,6 +443,8 @@ __device__ __forceinline__ void load_query_rows(uint8_t* dst, const TreeMaps& ma
 }
 cudaError_t tree_attend_prepare();
 cudaError_t launch_tree_attend(const TreeMaps& maps, const TreeParams& p, bool pdl, cudaStream_t stream);
+// The pieces of row blocks that several runs share, joined.
+cudaError_t launch_tree_merge(const TreeParams& p, bool pdl, cudaStream_t stream);
 cudaError_t tree_weights_prepare();
 cudaError_t launch_tree_weights(const TreeMaps& maps, const TreeParams& p, bool pdl, cudaStream_t stream);
 

@@ -918,6 +918,17 @@ cudaError_t launch_tree_attend(const TreeMaps& maps, const TreeParams& p, bool p
     cudaError_t e =
         cudaLaunchKernelEx(&cfg, p.a.out_fp32 ? mla_tree_attend_kernel<true> : mla_tree_attend_kernel<false>, maps, p);
     if (e != cudaSuccess) return e;
+    return launch_tree_merge(p, pdl, stream);
+}
+
+cudaError_t launch_tree_merge(const TreeParams& p, bool pdl, cudaStream_t stream) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 1 : 0;
     // shared row blocks: no more than there are row blocks or notes, and without
     // segments (one block per request) at most one per run
     const int per_request = (p.tokens * p.heads + kTreeBlockRows - 1) / kTreeBlockRows;
@@ -926,7 +937,6 @@ cudaError_t launch_tree_attend(const TreeMaps& maps, const TreeParams& p, bool p
         static_cast<unsigned>(std::min<long long>((per_request > 1 ? kTreePieces : 1) * p.clusters, blocks));
     const int groups = (std::min(p.tokens * p.heads, kTreeBlockRows) + 31) / 32;
     cfg.blockDim = dim3(32 * kMergeWarps);
-    cfg.dynamicSmemBytes = 0;
     // a row block has about clusters / blocks pieces
     if (p.clusters > kFewPieces * blocks) {
         cfg.gridDim = dim3(items, groups * (kDLatent / 4 / (kMergeWarps / 4)));

@@ -304,6 +304,16 @@ def test_two_streams_with_scratch_of_their_own():
     b.check()
 
 
+def test_a_wait_that_runs_out_is_reported():
+    c = Case([300], H=16).on_gpu()
+    plan = mla.paged_plan(batch=1, tokens=1, heads=16, scale=c.scale, stall_test=True)
+    _, scratch = c.forward(plan=plan)
+    torch.cuda.synchronize()
+    assert mla.status_word(plan, scratch) == mla.EDEVICE
+    c.forward()
+    c.check()
+
+
 def test_arguments_of_another_shape_are_refused():
     c = Case([30], H=16).on_gpu()
     plan = mla.paged_plan(batch=1, tokens=1, heads=32, scale=1.0)
