@@ -10,9 +10,8 @@
 // Operands.  A latent value is code * scale * kv_scale; code * scale has six
 // significant bits and lies between 2^-10 and 2688, so it is exact in f16.  Eight warps
 // per CTA take raw bytes from the pages to registers a tile ahead, widen them (one conversion
-// and one product per two values) and write the tiles' operands in the swizzled layout: a warp
-// per slot of K (this CTA's 64 rows, 128 columns) and per slot of V (64 rows, 128 of this CTA's
-// 256 features).  The key values stay bf16 and are multiplied with bf16 queries, into the same
+// and one product per two values) and write the tiles' operands in the swizzled layout: K (this CTA's
+// 64 rows, 512 columns) and V (128 rows, this CTA's 256 features), 32 rows x 256 columns a warp.  The key values stay bf16 and are multiplied with bf16 queries, into the same
 // accumulators.
 // q_lat goes to f16, the whole query row times a power of two that brings its largest value to
 // 2^14 .. 2^15 (values down to 2^-32 of it stay exact); the scores' factor takes it back.
@@ -32,7 +31,8 @@
 // leave their loops and meet at a cluster barrier.
 //
 // Warps of a CTA: 0-7 softmax and epilogue, 8-11 K, 12-15 V (all eight: queries), 16 MMA issue
-// (even CTA; the odd one's writes empty requests) and tensor memory, 17-18 key values.  Barriers that the MMA warp waits
+// (even CTA; the odd one's writes empty requests) and tensor memory, 17-18 key values,
+// 19 the items of the run.  Barriers that the MMA warp waits
 // on live in the even CTA and take arrivals of both.
 #include <cmath>
 
@@ -51,8 +51,9 @@ constexpr uint32_t kQBytes = 9 * kChunkBytes;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
 constexpr int kKeyWarp = 8, kValueWarp = 12, kFillWarps = 8, kMmaWarp = 16;
-constexpr int kRopeWarp = 17, kRopeWarps = 2;
-constexpr int kThreads = 608;
+constexpr int kRopeWarp = 17, kRopeWarps = 2, kScoutWarp = 19;
+constexpr int kItemReaders = kSoftmaxWarps + kFillWarps + kRopeWarps;   // and the even CTA's MMA warp
+constexpr int kThreads = 640;
 constexpr int kBarSoftmax = 1;                             // hardware barrier of the softmax warps
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 0, kTmemS = 256;               // O: 2 x 128 columns, S: 2 x 64 columns
@@ -61,6 +62,16 @@ constexpr float kProbLog2 = 7.0f;                          // P is held times 2^
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr long long kDrainCycles = 2000ll * 1000ll;        // about 1 ms: time for MMAs in flight after an abort
 
+// What one run does of a job (see TreeCursor), for the warps that work on it.
+struct __align__(16) Item {
+    int b, lo, hi, tile;                                   // tiles lo .. hi - 1, from `tile` on and round
+    int near, skip, d_pos, n_tok;                          // as r.lo, r.base of the request, and its own
+    int rb, flags, n_rb, n_tiles;
+    int begin, item, unused[2];
+};
+constexpr int kWhole = 1, kOpens = 2, kCut = 4;
+constexpr int kItems = 4;
+
 struct __align__(1024) Shared {
     uint8_t k[kSlots][kSlotBytes];                         // this CTA's 64 keys x 128 columns, QK operand
     uint8_t v[kSlots][kSlotBytes];                         // (feature half i, key half kb) at 2 i + kb, PV operand
@@ -68,14 +79,16 @@ struct __align__(1024) Shared {
     uint8_t q[kQBytes];                                    // 9 chunks of 64 query rows (f16, the last bf16)
     uint8_t p[2][kChunkBytes];                             // P, 64 rows x 128 keys in two key atoms
     float red_max[4][64], red_sum[4][64];                  // by quarter of the tile's keys, row
+    Item items[kItems];                                    // by item mod kItems
     int8_t q_exp[4][64];                                   // by item mod 4: a query row is held times 2^-q_exp
     // used in the even CTA, arrivals of both
-    uint64_t k_ready[kSlots], rope_ready, v_ready[2], q_ready, p_ready, o_free;
+    uint64_t k_ready[2], rope_ready, v_ready, q_ready, p_ready, o_free;   // (K by pairs of slots)
     // in each CTA, arrivals of the MMA thread
-    uint64_t k_empty[kSlots], v_empty[2], q_empty, s_full[2], o_done;
+    uint64_t k_empty[2], v_empty, q_empty, s_full[2], o_done;
     // this CTA's query rows are there, by item mod 2 (those of an item may be there before the softmax
     // warps have come to the one before)
     uint64_t q_local[2];
+    uint64_t item_full[kItems], item_empty[kItems];
     uint64_t stall_bar;
     TreeWork work;
     uint32_t tmem_base;
@@ -83,42 +96,135 @@ struct __align__(1024) Shared {
 };
 static_assert(sizeof(Shared) <= 227 * 1024, "fits shared memory");
 
+// ============================== items ====================================
+// One warp walks the run and lays its items out, a few ahead; the others need
+// few registers for their place in it.
+__device__ void scout(const PagedParams& p, Shared& sh, int lane) {
+    Cursor c;
+    c.start(p, sh.work);
+    while (c.left > 0) {
+        if (c.item >= kItems &&
+            !warp_wait(&sh.abort_flag, &sh.item_empty[c.item % kItems], (c.item / kItems - 1) & 1)) {
+            if (lane == 0) raise_tree_error(&sh.abort_flag, p.status);
+            return;
+        }
+        if (lane == 0) {
+            Item& i = sh.items[c.item % kItems];
+            i.b = c.b;
+            i.lo = c.lo;
+            i.hi = c.hi;
+            i.tile = c.tile;
+            i.near = c.r.lo;
+            i.skip = static_cast<int>(c.r.base);
+            i.d_pos = c.r.d_pos;
+            i.n_tok = c.r.n_tok;
+            i.rb = c.rb;
+            i.flags = (c.whole() ? kWhole : 0) | (!c.whole() && c.seg == 0 && c.opens() ? kOpens : 0) |
+                      (c.sg.count() > 1 ? kCut : 0);
+            i.n_rb = c.n_rb;
+            i.n_tiles = c.n_tiles;
+            i.begin = c.begin;
+            i.item = c.item;
+            mbar_arrive(&sh.item_full[c.item % kItems]);
+        }
+        __syncwarp();
+        const int n = c.item_left;
+        c.g += n;
+        c.left -= n;
+        ++c.item;
+        if (c.left > 0) c.next_item(p);
+    }
+}
+
+// A warp's place in the run: tile `tile` of item `item`, the g-th of the run.
+struct Walk {
+    int g, left;                                           // tiles before it, and from it on
+    int item, in_item;                                     // tiles of the item from it on
+    int tile, lo, hi, near, skip, b;
+    bool first;                                            // first tile of its item
+
+    __device__ __forceinline__ bool enter(Shared& sh) {
+        first = true;
+        if (!warp_wait(&sh.abort_flag, &sh.item_full[item % kItems], (item / kItems) & 1)) return false;
+        const Item& i = sh.items[item % kItems];
+        b = i.b;
+        lo = i.lo;
+        hi = i.hi;
+        tile = i.tile;
+        near = i.near;
+        skip = i.skip;
+        in_item = hi - lo;
+        return true;
+    }
+    // false: a wait ran out
+    __device__ __forceinline__ bool start(Shared& sh) {
+        g = item = 0;
+        left = static_cast<int>(sh.work.count);
+        return left <= 0 || enter(sh);
+    }
+    __device__ __forceinline__ bool next(Shared& sh) {
+        ++g;
+        --left;
+        first = --in_item == 0;
+        if (!first) {
+            if (++tile == hi) tile = lo;
+            return true;
+        }
+        ++item;
+        return left <= 0 || enter(sh);
+    }
+    // first row of the tile
+    __device__ __forceinline__ int row() const { return (tile < near ? tile : tile + skip) * kTreeTileKeys; }
+    // this warp needs nothing more of the item's description
+    static __device__ __forceinline__ void release(Shared& sh, int item, int lane) {
+        if (lane == 0) mbar_arrive(&sh.item_empty[item % kItems]);
+    }
+};
+
 // ============================== operands ==================================
 __device__ __forceinline__ uint4 ld_once_v4(const void* p) {
     uint4 v;
     asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
     return v;
 }
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
 __device__ __forceinline__ uint32_t low_half_twice(uint32_t v) { return __byte_perm(v, v, 0x1010); }
 __device__ __forceinline__ uint32_t high_half_twice(uint32_t v) { return __byte_perm(v, v, 0x3232); }
 
-// One warp's slot: 64 rows (key half `half` of a tile) x 128 features, from byte `from` of the rows'
-// codes on.  Eight rows (one page) at a time: lane = row + 8 * unit, unit = 32 features.
-struct Slot {
+// One warp's share of an operand: 32 rows x 256 features (two slots), from byte `from` of the rows'
+// codes on.  Four rows at a time: lane = row mod 4 + 4 * unit, a unit being 32 features (so a load
+// touches few lines, and eight lanes that store together hit all banks).
+struct Share {
     uint4 raw[8];
-    uint32_t scales[4];                                    // of two such groups each
+    uint32_t scales[4];                                    // of two such loads each
 
-    // pg: page number of the eight rows 8 (lane & 7) .. of the half
+    // pg: page number of the eight rows t0 + 8 (lane & 3) ..
     __device__ __forceinline__ void load(const PagedCache& c, int t0, int pg, int from, int lane) {
-        const int unit = lane >> 3, mask = (1 << c.row_shift) - 1;
+        const int unit = lane >> 2, at = t0 & ((1 << c.row_shift) - 1);
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
-            const int page = __shfl_sync(0xffffffffu, pg, n);
+            const int page = __shfl_sync(0xffffffffu, pg, n >> 1);
             raw[n] = make_uint4(0, 0, 0, 0);
             uint32_t two = 0;
             if (page >= 0) {
-                const uint8_t* row = c.pages + page * c.page_stride + ((t0 + 8 * n + (lane & 7)) & mask) * MLA_Q4_ROW;
-                raw[n] = ld_once_v4(row + from + 16 * unit);
-                two = *reinterpret_cast<const uint16_t*>(row + kQ4Scales + (from >> 3) + 2 * unit);
+                // (t0 is a multiple of 32, and a page of fewer rows is 8 or 16)
+                const int row = (at + 4 * n + (lane & 3)) & ((1 << c.row_shift) - 1);
+                const uint8_t* src = c.pages + page * c.page_stride + row * MLA_Q4_ROW;
+                raw[n] = ld_once_v4(src + from + 16 * unit);
+                two = *reinterpret_cast<const uint16_t*>(src + kQ4Scales + (from >> 3) + 2 * unit);
             }
             scales[n >> 1] = n & 1 ? scales[n >> 1] | two << 16 : two;
         }
     }
-    // kClean: NaN scales become 0
+    // dst: the first row's line in the first slot; `step`: bytes from slot to slot.  kClean: NaN scales become 0.
     template <bool kClean>
-    __device__ __forceinline__ void store(uint32_t dst, int lane) const {
-        const int unit = lane >> 3, key = lane & 7;
-        const uint32_t line = dst + (unit >> 1) * kChunkBytes + key * 128;
+    __device__ __forceinline__ void store(uint32_t dst, uint32_t step, int lane) const {
+        const int unit = lane >> 2;
+        // row & 7 is lane & 3, plus 4 in every other load
+        const uint32_t line = dst + (unit >> 2) * step + ((unit >> 1) & 1) * kChunkBytes + (lane & 3) * 128;
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
             uint32_t s = widen_e4m3(static_cast<uint16_t>(scales[n >> 1] >> (16 * (n & 1))));
@@ -130,17 +236,12 @@ struct Slot {
                 uint32_t h[4];
                 widen_e2m1(w[i], h);
                 const uint32_t f = i < 2 ? lo : hi;
-                st_shared_v4(line + n * 1024 + (((4 * (unit & 1) + i) ^ key) << 4), mul_f16x2(h[0], f), mul_f16x2(h[1], f),
-                             mul_f16x2(h[2], f), mul_f16x2(h[3], f));
+                st_shared_v4(line + n * 512 + (((4 * (unit & 1) + i) ^ ((lane & 3) + 4 * (n & 1))) << 4),
+                             mul_f16x2(h[0], f), mul_f16x2(h[1], f), mul_f16x2(h[2], f), mul_f16x2(h[3], f));
             }
         }
     }
 };
-
-// Page number of rows t0 + 8 (lane & 7) .., or -1.
-__device__ __forceinline__ int half_pages(const PagedCache& c, int b, int t0, int lane) {
-    return page_of(c, b, t0 + 8 * (lane & 7));
-}
 
 // Writes that the tensor cores of this SM read: announced to the even CTA's barrier.
 __device__ __forceinline__ void hand_over(uint32_t bar, int lane) {
@@ -149,103 +250,103 @@ __device__ __forceinline__ void hand_over(uint32_t bar, int lane) {
     if (lane == 0) mbar_arrive_peer(bar);
 }
 
-// This warp's eight query rows (of the CTA's 64): times a power of two, latents in f16.
-// (A call: its registers are not those of the rows that wait to be stored.)  row0: the first of them, `live`
-// how many there are, at b's queries.
-__device__ __noinline__ void fill_queries(const PagedParams& p, Shared& sh, int b, int row0, int live, int item, int fill,
-                                          int lane) {
-    const uint4* src = reinterpret_cast<const uint4*>(p.q + (static_cast<long long>(b) * p.tokens * p.heads + row0) * kDRow);
+// This warp's eight query rows (of the CTA's 64): copied, then times a power of two in place,
+// latents in f16.  `live` of them, from row0 of the tensor on.
+__device__ __forceinline__ void fill_queries(const PagedParams& p, Shared& sh, long long row0, int live, int item, int fill,
+                                             int lane) {
+    const uint4* src = reinterpret_cast<const uint4*>(p.q + row0 * kDRow) + lane;
+    const uint32_t q = smem_u32(sh.q);
+    // unit 32 k + lane of a row: chunk 4 k + lane / 8
+    const uint32_t dst = q + (lane >> 3) * kChunkBytes;
+#pragma unroll 1
+    for (int i = 0; i < live; ++i) {
+        const uint32_t at = dst + sw128_offset(8 * fill + i, (lane & 7) * 16);
+        cp_async_16(at, src + i * 72);
+        cp_async_16(at + 4 * kChunkBytes, src + i * 72 + 32);
+        if (lane < 8) cp_async_16(at + 8 * kChunkBytes, src + i * 72 + 64);
+    }
+    cp_async_commit();
+    cp_async_wait_group<0>();
     const float inv_kv = 1.f / p.kv_scale;                 // a power of two
 #pragma unroll 1
-    for (int i0 = 0; i0 < live; i0 += 2) {
-        uint4 x[2][3];
+    for (int i = 0; i < live; ++i) {
+        const uint32_t at = dst + sw128_offset(8 * fill + i, (lane & 7) * 16);   // (this lane's own copies)
+        uint4 x[3];
+        x[0] = ld_shared_v4(at);
+        x[1] = ld_shared_v4(at + 4 * kChunkBytes);
+        x[2] = lane < 8 ? ld_shared_v4(at + 8 * kChunkBytes) : make_uint4(0, 0, 0, 0);
+        float top = 0.f;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int k = 0; k < 3; ++k) {
+            const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+            float m = 0.f;
 #pragma unroll
-            for (int k = 0; k < 3; ++k) {
-                x[i][k] = make_uint4(0, 0, 0, 0);
-                if (i0 + i < live && (k < 2 || lane < 8)) x[i][k] = src[(i0 + i) * 72 + 32 * k + lane];
-            }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (i0 + i >= live) break;
-            float top = 0.f;
-#pragma unroll
-            for (int k = 0; k < 3; ++k) {
-                const uint32_t w[4] = {x[i][k].x, x[i][k].y, x[i][k].z, x[i][k].w};
-                float m = 0.f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
-                top = fmaxf(top, k < 2 ? m : m * inv_kv);
-            }
-            top = warp_max_f32(top);
-            const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127 - 14, -126), 126);
-            const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-            const int row = 8 * fill + i0 + i;
-#pragma unroll
-            for (int k = 0; k < 3; ++k) {
-                if (k == 2 && lane >= 8) break;
-                const uint32_t w[4] = {x[i][k].x, x[i][k].y, x[i][k].z, x[i][k].w};
-                uint32_t o[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float a = __uint_as_float(w[j] << 16) * f, b = __uint_as_float(w[j] & 0xffff0000u) * f;
-                    if (k < 2) {
-                        const __half2 h = __floats2half2_rn(a, b);
-                        o[j] = *reinterpret_cast<const uint32_t*>(&h);
-                    } else {
-                        o[j] = pack_bf16x2(a * inv_kv, b * inv_kv);
-                    }
-                }
-                const int unit = 32 * k + lane;
-                st_shared_v4(smem_u32(sh.q) + (unit >> 3) * kChunkBytes + sw128_offset(row, (unit & 7) * 16), o[0], o[1],
-                             o[2], o[3]);
-            }
-            if (lane == 0) sh.q_exp[item & 3][row] = static_cast<int8_t>(e);
+            for (int e = 0; e < 4; ++e)
+                m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
+            top = fmaxf(top, k < 2 ? m : m * inv_kv);
         }
+        top = warp_max_f32(top);
+        const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127 - 14, -126), 126);
+        const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+            uint32_t o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float a = __uint_as_float(w[j] << 16) * f, b = __uint_as_float(w[j] & 0xffff0000u) * f;
+                o[j] = k < 2 ? pack_f16x2(a, b) : pack_bf16x2(a * inv_kv, b * inv_kv);
+            }
+            if (k < 2 || lane < 8) st_shared_v4(at + 4 * k * kChunkBytes, o[0], o[1], o[2], o[3]);
+        }
+        if (lane == 0) sh.q_exp[item & 3][8 * fill + i] = static_cast<int8_t>(e);
     }
 }
 
-// The warps that write operands: kKeys the K slots, the others the V slots.
+// The warps that write operands.  K: 32 of this CTA's 64 rows, the slots 2 pair and 2 pair + 1; V: 32 of the
+// tile's 128 rows, this CTA's 256 features.
 template <bool kKeys>
 __device__ void fill(const PagedParams& p, Shared& sh, uint32_t rank, int warp, int lane) {
-    const int slot = warp & 3, nth = warp - kKeyWarp;
-    const int half = kKeys ? static_cast<int>(rank) : slot & 1;
-    const int from = kKeys ? 64 * slot : 128 * (slot >> 1) + 64 * static_cast<int>(rank);
+    const int nth = warp - kKeyWarp, pair = nth >> 1;      // (pair: kKeys)
+    const int row0 = kKeys ? 64 * static_cast<int>(rank) + 32 * (nth & 1) : 32 * (nth & 3);
+    const int from = 128 * (kKeys ? pair : static_cast<int>(rank));
     const uint32_t leader = map_to_rank(&sh, 0) - smem_u32(&sh);
-    const uint32_t ready = smem_u32(kKeys ? &sh.k_ready[slot] : &sh.v_ready[slot >> 1]) + leader;
-    uint64_t* empty = kKeys ? &sh.k_empty[slot] : &sh.v_empty[slot >> 1];
-    const uint32_t dst = smem_u32(kKeys ? sh.k[slot] : sh.v[slot]);
-    const PagedCache& cache = p.cache;
-    Cursor c;
-    c.start(p, sh.work);
+    uint64_t* empty = kKeys ? &sh.k_empty[pair] : &sh.v_empty;
+    const uint32_t ready = smem_u32(kKeys ? &sh.k_ready[pair] : &sh.v_ready) + leader;
+    // (V: half i of the features and kb of the keys at slot 2 i + kb)
+    const uint32_t dst = smem_u32(kKeys ? sh.k[2 * pair] : sh.v[(nth & 3) >> 1]) + 32 * (nth & 1) * 128;
+    const uint32_t step = kKeys ? kSlotBytes : 2 * kSlotBytes;
+    Walk c;
+    bool ok = c.start(sh);
     if (c.left <= 0) return;
-    Slot s;
-    int t0 = tile_row(c.r, c.tile) + 64 * half;
-    int pg = half_pages(cache, c.b, t0, lane);
-    s.load(cache, t0, pg, from, lane);
-    while (true) {
+    Share s;
+    int t0 = c.row() + row0;
+    int pg = page_of(p.cache, c.b, t0 + 8 * (lane & 3));
+    s.load(p.cache, t0, pg, from, lane);
+    while (ok) {
         const int g = c.g;
         if (c.first) {
             if (c.item > 0 && !warp_wait(&sh.abort_flag, &sh.q_empty, (c.item - 1) & 1)) break;
-            const int row0 = c.rb * kTreeBlockRows + static_cast<int>(rank) * 64 + 8 * nth;
-            fill_queries(p, sh, c.b, row0, min(c.r.n_tok * p.heads - row0, 8), c.item, nth, lane);
+            const Item& i = sh.items[c.item % kItems];
+            const int r0 = i.rb * kTreeBlockRows + static_cast<int>(rank) * 64 + 8 * nth;
+            fill_queries(p, sh, static_cast<long long>(i.b) * p.tokens * p.heads + r0, min(i.n_tok * p.heads - r0, 8),
+                         c.item, nth, lane);
             hand_over(smem_u32(&sh.q_ready) + leader, lane);
             if (lane == 0) mbar_arrive(&sh.q_local[c.item & 1]);
+            Walk::release(sh, c.item, lane);
         }
         // the next tile's pages, looked up ahead
-        c.next(p);
-        const bool more = c.left > 0;
+        ok = c.next(sh);
+        const bool more = c.left > 0 && ok;
         if (more) {
-            t0 = tile_row(c.r, c.tile) + 64 * half;
-            pg = half_pages(cache, c.b, t0, lane);
+            t0 = c.row() + row0;
+            pg = page_of(p.cache, c.b, t0 + 8 * (lane & 3));
         }
         if (g > 0 && !warp_wait(&sh.abort_flag, empty, (g - 1) & 1)) break;
-        s.store<!kKeys>(dst, lane);
+        s.store<!kKeys>(dst, step, lane);
         hand_over(ready, lane);
-        if (more) s.load(cache, t0, pg, from, lane);
-        if (!more) return;
+        if (c.left <= 0) return;
+        if (more) s.load(p.cache, t0, pg, from, lane);
     }
     if (lane == 0) raise_tree_error(&sh.abort_flag, p.status);
 }
@@ -255,13 +356,13 @@ __device__ void fill_rope(const PagedParams& p, Shared& sh, uint32_t rank, int n
     const PagedCache& cache = p.cache;
     const uint32_t ready = map_to_rank(&sh.rope_ready, 0);
     const int unit = lane & 7, row0 = 32 * nth + (lane >> 3);
-    Cursor c;
-    c.start(p, sh.work);
+    Walk c;
+    bool ok = c.start(sh);
     if (c.left <= 0) return;
     uint4 rope[8];
     auto load = [&] {
-        const int t0 = tile_row(c.r, c.tile) + 64 * static_cast<int>(rank);
-        const int pg = half_pages(cache, c.b, t0, lane);
+        const int t0 = c.row() + 64 * static_cast<int>(rank);
+        const int pg = page_of(cache, c.b, t0 + 8 * (lane & 7));
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
             const int page = __shfl_sync(0xffffffffu, pg, 4 * nth + (n >> 1)), t = t0 + row0 + 4 * n;
@@ -271,18 +372,19 @@ __device__ void fill_rope(const PagedParams& p, Shared& sh, uint32_t rank, int n
                                      (t & ((1 << cache.row_shift) - 1)) * MLA_Q4_ROW + kQ4Rope + 16 * unit);
         }
     };
-    load();
-    while (true) {
+    if (ok) load();
+    while (ok) {
         const int g = c.g;
-        if (g > 0 && !warp_wait(&sh.abort_flag, &sh.k_empty[kSlots - 1], (g - 1) & 1)) break;
+        if (c.first) Walk::release(sh, c.item, lane);
+        if (g > 0 && !warp_wait(&sh.abort_flag, &sh.k_empty[1], (g - 1) & 1)) break;
 #pragma unroll
         for (int n = 0; n < 8; ++n)
             st_shared_v4(smem_u32(sh.rope) + sw128_offset(row0 + 4 * n, unit * 16), rope[n].x, rope[n].y, rope[n].z,
                          rope[n].w);
         hand_over(ready, lane);
-        c.next(p);
+        ok = c.next(sh);
         if (c.left <= 0) return;
-        load();
+        if (ok) load();
     }
     if (lane == 0) raise_tree_error(&sh.abort_flag, p.status);
 }
@@ -310,10 +412,15 @@ __device__ void issue(const PagedParams& p, Shared& sh, uint32_t tmem) {
     const uint64_t q = make_sdesc(smem_u32(sh.q), 16, 1024, kLayoutSw128);
     const uint64_t pd = make_sdesc(smem_u32(sh.p), 16, 1024, kLayoutSw128);
     int item = 0, pv_item = -1;
-    Cursor c;                                              // moves from item to item here
-    c.start(p, sh.work);
-    const int total = c.left;
-    int in_item = c.item_left;                             // tiles of the item still to come
+    const int total = static_cast<int>(sh.work.count), lane = threadIdx.x & 31;
+    int in_item = 0;                                       // tiles of the item still to come
+    auto enter = [&] {
+        is.need(false, &sh.item_full[item % kItems], (item / kItems) & 1);
+        in_item = sh.items[item % kItems].hi - sh.items[item % kItems].lo;
+        __syncwarp();
+        Walk::release(sh, item, lane);
+    };
+    if (total > 0) enter();
     bool first = true;
     uint32_t pv_first = 0;                                 // the tile before this QK's was the first of its item
     bool see_k = false, see_p = false, see_v = false;
@@ -328,21 +435,17 @@ __device__ void issue(const PagedParams& p, Shared& sh, uint32_t tmem) {
                 is.need(see_p, &sh.p_ready, par ^ 1);
                 if (pv_first && ++pv_item > 0) is.need(false, &sh.o_free, (pv_item - 1) & 1);
                 tc_fence_after_sync();
+                is.need(see_v, &sh.v_ready, par ^ 1);
+                see_k = mbar_test(&sh.k_ready[0], par ^ pv_turn);   // of the QK that comes next
+                if (is.lead && is.ok) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    is.need(see_v, &sh.v_ready[i], par ^ 1);
-                    if (i == 0)
-                        see_v = mbar_test(&sh.v_ready[1], par ^ 1);
-                    else
-                        see_k = mbar_test(&sh.k_ready[0], par ^ pv_turn);   // of the QK that comes next
-                    if (is.lead && is.ok) {
+                    for (int i = 0; i < 2; ++i)
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
                             umma_pair_bf16(tmem + kTmemO + 128 * i, pd + (((k >> 2) * kChunkBytes + (k & 3) * 32u) >> 4),
                                            vd + (((2 * i + (k >> 2)) * kSlotBytes + (k & 3) * 2048u) >> 4), idesc_pv,
                                            k == 0 ? pv_first ^ 1u : 1u);
-                        if (g < total) umma_commit_pair(&sh.v_empty[i]);
-                    }
+                    if (g < total) umma_commit_pair(&sh.v_empty);
                 }
                 if (is.lead && is.ok) umma_commit_pair(&sh.o_done);
                 see_p = see_v = false;
@@ -353,32 +456,31 @@ __device__ void issue(const PagedParams& p, Shared& sh, uint32_t tmem) {
                 if (first) is.need(false, &sh.q_ready, item & 1);
                 // (the scores of tile g - 2 have been read: PV(g - 2) waited for their P)
 #pragma unroll
-                for (int s = 0; s < kSlots; ++s) {
-                    is.need(see_k, &sh.k_ready[s], par);
-                    if (s < kSlots - 1) {
-                        see_k = mbar_test(&sh.k_ready[s + 1], par);
+                for (int pair = 0; pair < 2; ++pair) {
+                    is.need(see_k, &sh.k_ready[pair], par);
+                    if (pair == 0) {
+                        see_k = mbar_test(&sh.k_ready[1], par);
+                        tc_fence_after_sync();
                     } else {
                         is.need(false, &sh.rope_ready, par);
                         if (pv_turn == 1 && g >= 1) {
                             see_p = mbar_test(&sh.p_ready, par ^ 1);
-                            see_v = mbar_test(&sh.v_ready[0], par ^ 1);
+                            see_v = mbar_test(&sh.v_ready, par ^ 1);
                         }
                     }
-                    if (s == 0) tc_fence_after_sync();
                     if (is.lead && is.ok) {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const uint32_t off = ((k >> 2) * kChunkBytes + (k & 3) * 32u) >> 4;
-                            umma_pair_bf16(d, q + (2 * s * kChunkBytes >> 4) + off, kd + (s * kSlotBytes >> 4) + off,
-                                           idesc_qk, (s | k) ? 1u : 0u);
+                        for (int k = 0; k < 16; ++k) {
+                            const uint32_t off = ((4 * pair + (k >> 2)) * kChunkBytes + (k & 3) * 32u) >> 4;
+                            umma_pair_bf16(d, q + off, kd + off, idesc_qk, (pair | k) ? 1u : 0u);
                         }
-                        if (s == 3) {
+                        if (pair == 1) {
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 umma_pair_bf16(d, q + ((8 * kChunkBytes + k * 32u) >> 4), rope + (k * 32u >> 4),
                                                idesc_rope, 1u);
                         }
-                        if (g + 1 < total) umma_commit_pair(&sh.k_empty[s]);
+                        if (g + 1 < total) umma_commit_pair(&sh.k_empty[pair]);
                     }
                 }
                 if (is.lead && is.ok) {
@@ -388,11 +490,8 @@ __device__ void issue(const PagedParams& p, Shared& sh, uint32_t tmem) {
                 see_k = false;
                 first = last;
                 if (--in_item == 0 && g + 1 < total) {
-                    c.g = g + 1;
-                    c.left = total - c.g;
-                    c.next_item(p);
                     ++item;
-                    in_item = c.item_left;
+                    enter();
                 }
             }
         }
@@ -428,16 +527,12 @@ __device__ __forceinline__ void store_rows(uint32_t stage, const uint32_t (&w)[1
 
 __device__ __forceinline__ uint32_t low_bits32(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; }
 __device__ __forceinline__ int row_int(long long t) { return static_cast<int>(min(max(t, 0ll), 0x7fffffffll)); }
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
 
 // Thread: 32 keys of one row.  Warps w and w + 4 share tensor-memory lanes 32 (w mod 4) ..
 // and split their columns.
 __device__ void softmax(const PagedParams& p, Shared& sh, uint32_t tmem, uint32_t rank, int cluster, int tid) {
     const int lane = tid & 31, warp = tid >> 5;
-    const int sub = warp >> 2, half = (warp >> 1) & 1;     // keys 64 half + 32 sub ..; features 256 sub + 128 half ..
+    const int sub = warp >> 2, half = (warp >> 1) & 1;     // keys 64 half + 32 sub ..; features 256 half + 128 sub ..
     const int quarter = 2 * half + sub;
     const int row = 32 * (warp & 1) + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -447,34 +542,32 @@ __device__ void softmax(const PagedParams& p, Shared& sh, uint32_t tmem, uint32_
     const bool notes = rank == 0 && tid == 0;
     if (notes)
         for (int i = 0; i < kTreePieces; ++i) p.merge[i * p.clusters + cluster].pieces = 0;
-    Cursor c;
-    c.start(p, sh.work);
+    Walk c;
+    ok = c.start(sh);
     // whether rows 8 (lane & 15) .. of the tile have a page, looked up a tile ahead
     int pages = 0;
-    if (c.left > 0) pages = page_of(p.cache, c.b, tile_row(c.r, c.tile) + 8 * (lane & 15));
+    if (c.left > 0 && ok) pages = page_of(p.cache, c.b, c.row() + 8 * (lane & 15));
     while (c.left > 0 && ok) {
         // ---- one item: tiles of one row block
-        const int r = c.rb * kTreeBlockRows + static_cast<int>(rank) * 64 + row;
-        const int live_rows = c.r.n_tok * p.heads;
-        const int b = c.b, rb = c.rb;
+        const int item = c.item, g0 = c.g;
+        const Item& it = sh.items[item % kItems];
+        const int r = it.rb * kTreeBlockRows + static_cast<int>(rank) * 64 + row;
+        const bool live = r < it.n_tok * p.heads;
         // this row's token attends rows [from, to) and those before sink
-        const long long own = static_cast<long long>(c.r.d_pos) + r / p.heads;
-        const int to = r < live_rows ? row_int(own + 1) : 0;
+        const long long own = static_cast<long long>(it.d_pos) + r / p.heads;
+        const int to = live ? row_int(own + 1) : 0;
         const int from = p.window > 0 ? row_int(own + 1 - p.window) : 0;
         // tiles whose rows every token attends: up to all_to, from all_from on or before sink
-        const int all_to = row_int(static_cast<long long>(c.r.d_pos) + 1);
-        const int all_from = p.window > 0 ? row_int(static_cast<long long>(c.r.d_pos) + c.r.n_tok - p.window) : 0;
-        const bool whole = c.whole(), run_first = c.g == 0;
-        const bool opens = !whole && c.seg == 0 && c.opens(), cut = c.sg.count() > 1;
-        const TreeCut of{c.n_rb, c.n_tiles, static_cast<int>(sh.work.per), c.begin};
-        bad |= !warp_wait(&sh.abort_flag, &sh.q_local[c.item & 1], (c.item >> 1) & 1);
+        const int all_to = row_int(static_cast<long long>(it.d_pos) + 1);
+        const int all_from = p.window > 0 ? row_int(static_cast<long long>(it.d_pos) + it.n_tok - p.window) : 0;
+        bad |= !warp_wait(&sh.abort_flag, &sh.q_local[item & 1], (item >> 1) & 1);
         const float c2 = p.scale_log2 * p.kv_scale *
-                         (r < live_rows ? __uint_as_float(static_cast<uint32_t>(127 + sh.q_exp[c.item & 3][row]) << 23) : 1.f);
+                         (live ? __uint_as_float(static_cast<uint32_t>(127 + sh.q_exp[item & 3][row]) << 23) : 1.f);
         float m_ref = -INFINITY, l = 0.f;
         bool last;
         do {
             const int g = c.g, buf = g & 1;
-            last = c.last();
+            last = c.in_item == 1;
             bool w = warp_wait(&sh.abort_flag, &sh.s_full[buf], (g >> 1) & 1);
             uint32_t s[32];
             if (w) {
@@ -484,7 +577,7 @@ __device__ void softmax(const PagedParams& p, Shared& sh, uint32_t tmem, uint32_
 #pragma unroll
                 for (int i = 0; i < 32; ++i) s[i] = 0;
             }
-            const int t0 = tile_row(c.r, c.tile);
+            const int t0 = c.row();
             const uint32_t here = __ballot_sync(0xffffffffu, pages >= 0);
             if (here != 0xffffffffu || t0 + kTreeTileKeys > all_to || (t0 < all_from && t0 + kTreeTileKeys > p.sink)) {
                 const int t = t0 + 64 * half + 32 * sub;
@@ -551,8 +644,9 @@ __device__ void softmax(const PagedParams& p, Shared& sh, uint32_t tmem, uint32_
             __syncwarp();
             bad |= !w;                                     // the threads leave together at the next barrier
             if (lane == 0 && !bad) mbar_arrive_peer(p_bar);
-            c.next(p);
-            if (c.left > 0) pages = page_of(p.cache, c.b, tile_row(c.r, c.tile) + 8 * (lane & 15));
+            const bool entered = c.next(sh);
+            bad |= !entered;
+            if (c.left > 0 && entered) pages = page_of(p.cache, c.b, c.row() + 8 * (lane & 15));
         } while (!last);
         if (!ok) break;
 
@@ -565,15 +659,19 @@ __device__ void softmax(const PagedParams& p, Shared& sh, uint32_t tmem, uint32_
         const float lt = (sh.red_sum[0][row] + sh.red_sum[1][row]) + (sh.red_sum[2][row] + sh.red_sum[3][row]);
         const float inv = lt == 0.f ? 0.f : p.kv_scale / lt;
         const float lse2 = lt == 0.f ? -INFINITY : (m_ref - kProbLog2) + log2f(lt);
+        const int b = it.b, rb = it.rb, live_rows = it.n_tok * p.heads;
+        const bool whole = it.flags & kWhole;
         // place of the piece: the run's first item, one that ends with the run's length, another
-        const int place = run_first ? 0 : c.g == sh.work.per ? 2 : 1, slot = kTreePieces * cluster + place;
-        if (quarter == 0 && r < live_rows) {
+        const int place = g0 == 0 ? 0 : c.g == sh.work.per ? 2 : 1, slot = kTreePieces * cluster + place;
+        if (quarter == 0 && live) {
             if (whole)
                 p.a.lse[static_cast<long long>(b) * p.tokens * p.heads + r] = lse2 * kLn2;
             else
                 p.lse_part[slot * kTreeBlockRows + static_cast<int>(rank) * 64 + row] = lse2;
         }
-        if (notes && opens) {
+        if (notes && it.flags & kOpens) {
+            const bool cut = it.flags & kCut;
+            const TreeCut of{it.n_rb, it.n_tiles, static_cast<int>(sh.work.per), it.begin};
             const int rows = min(kTreeBlockRows, live_rows - rb * kTreeBlockRows);
             // (an uncut job's pieces lie in the runs from this one to that of its last unit)
             const int pieces = cut ? -1 : (of.begin + (rb + 1) * of.n_tiles - 1) / of.per + 1;
@@ -590,7 +688,7 @@ __device__ void softmax(const PagedParams& p, Shared& sh, uint32_t tmem, uint32_
         const uint32_t stage = smem_u32(sh.p) + warp * 2048;
         const int row_w = 32 * (warp & 1);                 // this warp's first row of the 64
         const int n_rows = live_rows - (r - row) - row_w;
-        const int f0 = 256 * sub + 128 * half;             // its first feature
+        const int f0 = 256 * half + 128 * sub;             // its first feature
         float4* piece = reinterpret_cast<float4*>(p.part) +
                         piece_quad(slot, static_cast<int>(rank) * 64 + row_w, f0 / 4) + lane;
         const int bytes = p.a.out_fp32 ? 4 : 2;
@@ -624,6 +722,7 @@ __device__ void softmax(const PagedParams& p, Shared& sh, uint32_t tmem, uint32_
                 }
             }
         }
+        Walk::release(sh, item, lane);
         tc_fence_before_sync();
         __syncwarp();
         // O may be overwritten.  (Only if something will wait for it: the closing barrier orders no arrival.)
@@ -658,15 +757,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t rank = cluster_ctarank();
     const int cluster = blockIdx.x >> 1;
     if (tid == 0) {
-        for (int i = 0; i < kSlots; ++i) {
-            mbar_init(&sh.k_ready[i], 2);
-            mbar_init(&sh.k_empty[i], 1);
-        }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh.v_ready[i], 4);
-            mbar_init(&sh.v_empty[i], 1);
+            mbar_init(&sh.k_ready[i], 4);
+            mbar_init(&sh.k_empty[i], 1);
             mbar_init(&sh.s_full[i], 1);
         }
+        mbar_init(&sh.v_ready, 8);
+        mbar_init(&sh.v_empty, 1);
         mbar_init(&sh.rope_ready, 2 * kRopeWarps);
         mbar_init(&sh.p_ready, 2 * kSoftmaxWarps);
         mbar_init(&sh.o_done, 1);
@@ -674,6 +771,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 2; ++i) mbar_init(&sh.q_local[i], kFillWarps);
         mbar_init(&sh.o_free, 2 * kSoftmaxWarps);
         mbar_init(&sh.q_empty, 1);
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&sh.item_full[i], 1);
+            mbar_init(&sh.item_empty[i], kItemReaders + (rank == 0 ? 1 : 0));
+        }
         mbar_init(&sh.stall_bar, 1);
         sh.abort_flag = 0;
         mbar_init_fence();
@@ -703,7 +804,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
     // the dynamic window starts 1024-byte aligned (the 128-byte swizzle needs it)
     if ((smem_u32(smem_raw) & 1023u) != 0 && tid == 0) raise_tree_error(&sh.abort_flag, p.status);
-    if (warp >= kRopeWarp) {
+    if (warp == kScoutWarp) {
+        scout(p, sh, lane);
+    } else if (warp >= kRopeWarp) {
         fill_rope(p, sh, rank, warp - kRopeWarp, lane);
     } else if (warp == kMmaWarp) {
         if (rank == 0)
