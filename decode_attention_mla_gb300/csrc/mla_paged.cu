@@ -143,8 +143,13 @@ int mla_paged_forward(const mla_paged_plan_t* plan, const mla_paged_args* args, 
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     rc = mla::prepare(st, true);
     if (rc != MLA_OK) return rc;
+    mla::PagedMaps maps;
+    rc = mla::encode_q4_boxes(&maps.codes, &args->cache, 64, CU_TENSOR_MAP_SWIZZLE_64B);
+    if (rc == MLA_OK) rc = mla::encode_q4_boxes(&maps.scales, &args->cache, 16, CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (rc == MLA_OK) rc = mla::encode_q4_boxes(&maps.rope, &args->cache, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (rc != MLA_OK) return rc;
     return mla::launch_status(
-        mla::launch_paged_attend(mla::params(plan, args, scratch), plan->shape.pdl != 0, st));
+        mla::launch_paged_attend(maps, mla::params(plan, args, scratch), plan->shape.pdl != 0, st));
 }
 
 }  // extern "C"

@@ -39,7 +39,14 @@ __device__ __forceinline__ int tile_row(const TreeRequest& r, int tile) {
     return (tile < r.lo ? tile : tile + static_cast<int>(r.base)) * kTreeTileKeys;
 }
 
+// Views {416 bytes, page_rows, n_pages} of the pages; boxes of min(page_rows, 64) rows.
+struct PagedMaps {
+    CUtensorMap codes;                                     // 64 bytes of a row, 64-byte swizzled
+    CUtensorMap scales;                                    // 16 bytes
+    CUtensorMap rope;                                      // 128 bytes, 128-byte swizzled
+};
+
 cudaError_t paged_attend_prepare();
-cudaError_t launch_paged_attend(const PagedParams& p, bool pdl, cudaStream_t stream);
+cudaError_t launch_paged_attend(const PagedMaps& maps, const PagedParams& p, bool pdl, cudaStream_t stream);
 
 }  // namespace mla

@@ -9,10 +9,13 @@
 //
 // Operands.  A latent value is code * scale * kv_scale; code * scale has six
 // significant bits and lies between 2^-10 and 2688, so it is exact in f16.  Eight warps
-// per CTA take raw bytes from the pages to registers a tile ahead, widen them (one conversion
-// and one product per two values) and write the tiles' operands in the swizzled layout: K (this CTA's
-// 64 rows, 512 columns) and V (128 rows, this CTA's 256 features), 32 rows x 256 columns a warp.  The key values stay bf16 and are multiplied with bf16 queries, into the same
-// accumulators.
+// per CTA write the tiles' operands in the swizzled layout, a slot each: K (this CTA's 64 rows, 128 of 512
+// columns) and V (64 of the tile's rows, 128 of this CTA's 256 features).  The rows' bytes come by TMA
+// into the slot itself, pass through registers, and go back widened (one conversion and one product per two
+// values): there is no room for them beside the operands.  (Through registers alone, by loads of 16 bytes a
+// lane a tile ahead: 507 us where this form takes 326 for 16 requests of 4 x 128; the loads in flight do not
+// fit what shared memory leaves of L1.)  The key values stay bf16 and are multiplied with bf16
+// queries, into the same accumulators; they land in their place, and rows are called to L2 three tiles ahead.
 // q_lat goes to f16, the whole query row times a power of two that brings its largest value to
 // 2^14 .. 2^15 (values down to 2^-32 of it stay exact); the scores' factor takes it back.
 //
@@ -31,8 +34,8 @@
 // leave their loops and meet at a cluster barrier.
 //
 // Warps of a CTA: 0-7 softmax and epilogue, 8-11 K, 12-15 V (all eight: queries), 16 MMA issue
-// (even CTA; the odd one's writes empty requests) and tensor memory, 17-18 key values,
-// 19 the items of the run.  Barriers that the MMA warp waits
+// (even CTA; the odd one's writes empty requests) and tensor memory, 17 key values,
+// 18 the items of the run, 19 idle.  Barriers that the MMA warp waits
 // on live in the even CTA and take arrivals of both.
 #include <cmath>
 
@@ -51,8 +54,8 @@ constexpr uint32_t kQBytes = 9 * kChunkBytes;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
 constexpr int kKeyWarp = 8, kValueWarp = 12, kFillWarps = 8, kMmaWarp = 16;
-constexpr int kRopeWarp = 17, kRopeWarps = 2, kScoutWarp = 19;
-constexpr int kItemReaders = kSoftmaxWarps + kFillWarps + kRopeWarps;   // and the even CTA's MMA warp
+constexpr int kRopeWarp = 17, kScoutWarp = 18;
+constexpr int kItemReaders = kSoftmaxWarps + kFillWarps + 1;   // and the even CTA's MMA warp
 constexpr int kThreads = 640;
 constexpr int kBarSoftmax = 1;                             // hardware barrier of the softmax warps
 constexpr uint32_t kTmemCols = 512;
@@ -60,7 +63,7 @@ constexpr uint32_t kTmemO = 0, kTmemS = 256;               // O: 2 x 128 columns
 constexpr float kRescaleLog2 = 8.0f;                       // move the reference when a max grows past 2^8
 constexpr float kProbLog2 = 7.0f;                          // P is held times 2^7
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr long long kDrainCycles = 2000ll * 1000ll;        // about 1 ms: time for MMAs in flight after an abort
+constexpr long long kDrainCycles = 2000ll * 1000ll;        // about 1 ms: time for copies and MMAs in flight after an abort
 
 // What one run does of a job (see TreeCursor), for the warps that work on it.
 struct __align__(16) Item {
@@ -82,9 +85,10 @@ struct __align__(1024) Shared {
     Item items[kItems];                                    // by item mod kItems
     int8_t q_exp[4][64];                                   // by item mod 4: a query row is held times 2^-q_exp
     // used in the even CTA, arrivals of both
-    uint64_t k_ready[2], rope_ready, v_ready, q_ready, p_ready, o_free;   // (K by pairs of slots)
+    uint64_t k_ready[kSlots], rope_ready, v_ready[2], q_ready, p_ready, o_free;
     // in each CTA, arrivals of the MMA thread
-    uint64_t k_empty[2], v_empty, q_empty, s_full[2], o_done;
+    uint64_t k_empty[kSlots], v_empty[2], q_empty, s_full[2], o_done;
+    uint64_t raw[kFillWarps];                              // a slot's bytes have landed in it
     // this CTA's query rows are there, by item mod 2 (those of an item may be there before the softmax
     // warps have come to the one before)
     uint64_t q_local[2];
@@ -182,9 +186,9 @@ struct Walk {
 };
 
 // ============================== operands ==================================
-__device__ __forceinline__ uint4 ld_once_v4(const void* p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+__device__ __forceinline__ uint32_t ld_shared_u16(uint32_t addr) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
     return v;
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -194,54 +198,45 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 __device__ __forceinline__ uint32_t low_half_twice(uint32_t v) { return __byte_perm(v, v, 0x1010); }
 __device__ __forceinline__ uint32_t high_half_twice(uint32_t v) { return __byte_perm(v, v, 0x3232); }
 
-// One warp's share of an operand: 32 rows x 256 features (two slots), from byte `from` of the rows'
-// codes on.  Four rows at a time: lane = row mod 4 + 4 * unit, a unit being 32 features (so a load
-// touches few lines, and eight lanes that store together hit all banks).
-struct Share {
-    uint4 raw[8];
-    uint32_t scales[4];                                    // of two such loads each
+// Rows per box: a page's, 64 at most.
+__device__ __forceinline__ int box_rows(const PagedCache& c) { return min(1 << c.row_shift, 64); }
 
-    // pg: page number of the eight rows t0 + 8 (lane & 3) ..
-    __device__ __forceinline__ void load(const PagedCache& c, int t0, int pg, int from, int lane) {
-        const int unit = lane >> 2, at = t0 & ((1 << c.row_shift) - 1);
+// One slot: 64 rows (half a tile) x 128 features.  The rows' bytes land in the slot itself, 64 bytes of codes a
+// row (64-byte swizzled) and behind them 16 bytes of scales, of which eight are the slot's; they are taken to registers, all
+// of them, and the widened values written over them.
+constexpr int kRawScales = 64 * 64;                        // where the scales land
+constexpr uint32_t kRawBytes = 64 * (64 + 16);
+
+__device__ __forceinline__ void widen_slot(uint32_t slot, int scale_byte, bool clean, int lane) {
+    const int row = lane & 7, unit = lane >> 3;            // of eight rows; 32 features
+    uint4 raw[8];
+    uint32_t scales[8];
+    // (64-byte swizzle: 16-byte unit u of row r lies at u ^ (r / 2 mod 4))
+    const uint32_t from = slot + row * 64 + ((unit ^ ((row >> 1) & 3)) << 4);
+    const uint32_t scale_from = slot + kRawScales + row * 16 + scale_byte + 2 * unit;
 #pragma unroll
-        for (int n = 0; n < 8; ++n) {
-            const int page = __shfl_sync(0xffffffffu, pg, n >> 1);
-            raw[n] = make_uint4(0, 0, 0, 0);
-            uint32_t two = 0;
-            if (page >= 0) {
-                // (t0 is a multiple of 32, and a page of fewer rows is 8 or 16)
-                const int row = (at + 4 * n + (lane & 3)) & ((1 << c.row_shift) - 1);
-                const uint8_t* src = c.pages + page * c.page_stride + row * MLA_Q4_ROW;
-                raw[n] = ld_once_v4(src + from + 16 * unit);
-                two = *reinterpret_cast<const uint16_t*>(src + kQ4Scales + (from >> 3) + 2 * unit);
-            }
-            scales[n >> 1] = n & 1 ? scales[n >> 1] | two << 16 : two;
+    for (int n = 0; n < 8; ++n) {
+        raw[n] = ld_shared_v4(from + n * 512);
+        scales[n] = ld_shared_u16(scale_from + n * 128);
+    }
+    __syncwarp();                                          // every lane has its bytes: they may be overwritten
+    const uint32_t line = slot + (unit >> 1) * kChunkBytes + row * 128;
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+        uint32_t s = widen_e4m3(static_cast<uint16_t>(scales[n]));
+        if (clean) s &= __heq2_mask(*reinterpret_cast<__half2*>(&s), *reinterpret_cast<__half2*>(&s));
+        const uint32_t lo = low_half_twice(s), hi = high_half_twice(s);
+        const uint32_t w[4] = {raw[n].x, raw[n].y, raw[n].z, raw[n].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t h[4];
+            widen_e2m1(w[i], h);
+            const uint32_t f = i < 2 ? lo : hi;
+            st_shared_v4(line + n * 1024 + (((4 * (unit & 1) + i) ^ row) << 4), mul_f16x2(h[0], f), mul_f16x2(h[1], f),
+                         mul_f16x2(h[2], f), mul_f16x2(h[3], f));
         }
     }
-    // dst: the first row's line in the first slot; `step`: bytes from slot to slot.  kClean: NaN scales become 0.
-    template <bool kClean>
-    __device__ __forceinline__ void store(uint32_t dst, uint32_t step, int lane) const {
-        const int unit = lane >> 2;
-        // row & 7 is lane & 3, plus 4 in every other load
-        const uint32_t line = dst + (unit >> 2) * step + ((unit >> 1) & 1) * kChunkBytes + (lane & 3) * 128;
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-            uint32_t s = widen_e4m3(static_cast<uint16_t>(scales[n >> 1] >> (16 * (n & 1))));
-            if (kClean) s &= __heq2_mask(*reinterpret_cast<__half2*>(&s), *reinterpret_cast<__half2*>(&s));
-            const uint32_t lo = low_half_twice(s), hi = high_half_twice(s);
-            const uint32_t w[4] = {raw[n].x, raw[n].y, raw[n].z, raw[n].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t h[4];
-                widen_e2m1(w[i], h);
-                const uint32_t f = i < 2 ? lo : hi;
-                st_shared_v4(line + n * 512 + (((4 * (unit & 1) + i) ^ ((lane & 3) + 4 * (n & 1))) << 4),
-                             mul_f16x2(h[0], f), mul_f16x2(h[1], f), mul_f16x2(h[2], f), mul_f16x2(h[3], f));
-            }
-        }
-    }
-};
+}
 
 // Writes that the tensor cores of this SM read: announced to the even CTA's barrier.
 __device__ __forceinline__ void hand_over(uint32_t bar, int lane) {
@@ -303,28 +298,45 @@ __device__ __forceinline__ void fill_queries(const PagedParams& p, Shared& sh, l
     }
 }
 
-// The warps that write operands.  K: 32 of this CTA's 64 rows, the slots 2 pair and 2 pair + 1; V: 32 of the
-// tile's 128 rows, this CTA's 256 features.
-template <bool kKeys>
-__device__ void fill(const PagedParams& p, Shared& sh, uint32_t rank, int warp, int lane) {
-    const int nth = warp - kKeyWarp, pair = nth >> 1;      // (pair: kKeys)
-    const int row0 = kKeys ? 64 * static_cast<int>(rank) + 32 * (nth & 1) : 32 * (nth & 3);
-    const int from = 128 * (kKeys ? pair : static_cast<int>(rank));
+// Where a box of the tile's rows lies: page and row in it (a page behind the last one: the box is zeros).
+struct Place {
+    int page, row;
+    __device__ __forceinline__ void find(const PagedCache& c, int b, int t) {
+        page = page_of(c, b, t);
+        if (page < 0) page = c.n_pages;
+        row = t & ((1 << c.row_shift) - 1);
+    }
+};
+
+// The warps that write operands: a slot of K (this CTA's 64 rows) or of V (half kb of the tile's rows, 128 of this
+// CTA's 256 features).  A slot's bytes are asked for when the products with the tile before are done; that, their way
+// from L2 and the widening take place while the other product runs.
+__device__ void fill(const PagedMaps& maps, const PagedParams& p, Shared& sh, uint32_t rank, int warp, int lane) {
+    const bool keys = warp < kValueWarp;
+    const int nth = warp - kKeyWarp, slot = nth & 3;
+    const int row0 = 64 * (keys ? static_cast<int>(rank) : slot & 1);
+    const int from = keys ? 64 * slot : 128 * static_cast<int>(rank) + 64 * (slot >> 1);   // byte of the rows' codes
     const uint32_t leader = map_to_rank(&sh, 0) - smem_u32(&sh);
-    uint64_t* empty = kKeys ? &sh.k_empty[pair] : &sh.v_empty;
-    const uint32_t ready = smem_u32(kKeys ? &sh.k_ready[pair] : &sh.v_ready) + leader;
-    // (V: half i of the features and kb of the keys at slot 2 i + kb)
-    const uint32_t dst = smem_u32(kKeys ? sh.k[2 * pair] : sh.v[(nth & 3) >> 1]) + 32 * (nth & 1) * 128;
-    const uint32_t step = kKeys ? kSlotBytes : 2 * kSlotBytes;
+    uint64_t* empty = keys ? &sh.k_empty[slot] : &sh.v_empty[slot >> 1];
+    const uint32_t ready = smem_u32(keys ? &sh.k_ready[slot] : &sh.v_ready[slot >> 1]) + leader;
+    uint8_t* dst = keys ? sh.k[slot] : sh.v[slot];
+    const uint64_t policy = l2_policy_evict_normal();
+    const int box = box_rows(p.cache), boxes = 64 / box;
     Walk c;
     bool ok = c.start(sh);
     if (c.left <= 0) return;
-    Share s;
-    int t0 = c.row() + row0;
-    int pg = page_of(p.cache, c.b, t0 + 8 * (lane & 3));
-    s.load(p.cache, t0, pg, from, lane);
+    Place at;
+    at.find(p.cache, c.b, c.row() + row0 + box * (lane & (boxes - 1)));
     while (ok) {
         const int g = c.g;
+        if (g > 0 && !warp_wait(&sh.abort_flag, empty, (g - 1) & 1)) break;
+        if (lane == 0) mbar_arrive_expect_tx(&sh.raw[nth], kRawBytes);
+        __syncwarp();
+        if (lane < boxes) {
+            tma_load_3d(dst + lane * box * 64, &maps.codes, from, at.row, at.page, &sh.raw[nth], policy);
+            tma_load_3d(dst + kRawScales + lane * box * 16, &maps.scales, kQ4Scales + 16 * (from >> 7), at.row, at.page,
+                        &sh.raw[nth], policy);
+        }
         if (c.first) {
             if (c.item > 0 && !warp_wait(&sh.abort_flag, &sh.q_empty, (c.item - 1) & 1)) break;
             const Item& i = sh.items[c.item % kItems];
@@ -335,56 +347,52 @@ __device__ void fill(const PagedParams& p, Shared& sh, uint32_t rank, int warp, 
             if (lane == 0) mbar_arrive(&sh.q_local[c.item & 1]);
             Walk::release(sh, c.item, lane);
         }
-        // the next tile's pages, looked up ahead
         ok = c.next(sh);
-        const bool more = c.left > 0 && ok;
-        if (more) {
-            t0 = c.row() + row0;
-            pg = page_of(p.cache, c.b, t0 + 8 * (lane & 3));
-        }
-        if (g > 0 && !warp_wait(&sh.abort_flag, empty, (g - 1) & 1)) break;
-        s.store<!kKeys>(dst, step, lane);
+        if (c.left > 0 && ok) at.find(p.cache, c.b, c.row() + row0 + box * (lane & (boxes - 1)));
+        if (!warp_wait(&sh.abort_flag, &sh.raw[nth], g & 1)) break;
+        widen_slot(smem_u32(dst), from >> 3 & 8, !keys, lane);
         hand_over(ready, lane);
         if (c.left <= 0) return;
-        if (more) s.load(p.cache, t0, pg, from, lane);
     }
     if (lane == 0) raise_tree_error(&sh.abort_flag, p.status);
 }
 
-// The key values of this CTA's 64 rows, 32 a warp: as they are, a tile ahead in registers.
-__device__ void fill_rope(const PagedParams& p, Shared& sh, uint32_t rank, int nth, int lane) {
-    const PagedCache& cache = p.cache;
-    const uint32_t ready = map_to_rank(&sh.rope_ready, 0);
-    const int unit = lane & 7, row0 = 32 * nth + (lane >> 3);
+// The key values of this CTA's 64 rows, as they are, and the rows of a later tile on their way to L2.
+constexpr int kAhead = 3;                                  // tiles
+__device__ void fill_rope(const PagedMaps& maps, const PagedParams& p, Shared& sh, uint32_t rank, int lane) {
+    const uint32_t bar = map_to_rank(&sh.rope_ready, 0);
+    const uint64_t policy = l2_policy_evict_normal();
+    const int box = box_rows(p.cache), boxes = 64 / box;
+    const int row0 = 64 * static_cast<int>(rank) + box * (lane & (boxes - 1));
     Walk c;
     bool ok = c.start(sh);
     if (c.left <= 0) return;
-    uint4 rope[8];
-    auto load = [&] {
-        const int t0 = c.row() + 64 * static_cast<int>(rank);
-        const int pg = page_of(cache, c.b, t0 + 8 * (lane & 7));
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-            const int page = __shfl_sync(0xffffffffu, pg, 4 * nth + (n >> 1)), t = t0 + row0 + 4 * n;
-            rope[n] = make_uint4(0, 0, 0, 0);
-            if (page >= 0)
-                rope[n] = ld_once_v4(cache.pages + page * cache.page_stride +
-                                     (t & ((1 << cache.row_shift) - 1)) * MLA_Q4_ROW + kQ4Rope + 16 * unit);
-        }
-    };
-    if (ok) load();
+    Walk ahead = c;
     while (ok) {
         const int g = c.g;
+        Place at;
+        at.find(p.cache, c.b, c.row() + row0);
+        if (g > 0 && !warp_wait(&sh.abort_flag, &sh.k_empty[kSlots - 1], (g - 1) & 1)) break;
+        // (the even CTA announces both CTAs' bytes; the odd one's may land first: the phase is open until then)
+        if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&sh.rope_ready, 2 * kChunkBytes);
+        __syncwarp();
+        if (lane < boxes)
+            tma_load_3d_pair(sh.rope + lane * box * 128, &maps.rope, kQ4Rope, at.row, at.page, bar, policy);
         if (c.first) Walk::release(sh, c.item, lane);
-        if (g > 0 && !warp_wait(&sh.abort_flag, &sh.k_empty[1], (g - 1) & 1)) break;
-#pragma unroll
-        for (int n = 0; n < 8; ++n)
-            st_shared_v4(smem_u32(sh.rope) + sw128_offset(row0 + 4 * n, unit * 16), rope[n].x, rope[n].y, rope[n].z,
-                         rope[n].w);
-        hand_over(ready, lane);
+        if (ahead.g < g) ahead = c;
+        while (ahead.g < g + kAhead && ahead.left > 1) {
+            // (an item that is not laid out yet is not waited for)
+            if (ahead.in_item == 1 &&
+                !__all_sync(0xffffffffu, mbar_test(&sh.item_full[(ahead.item + 1) % kItems], ((ahead.item + 1) / kItems) & 1)))
+                break;
+            if (!ahead.next(sh)) break;
+            if (lane < boxes) {
+                const int page = page_of(p.cache, ahead.b, ahead.row() + row0);
+                if (page >= 0) bulk_prefetch_l2(row_in(p.cache, page, ahead.row() + row0), box * MLA_Q4_ROW);
+            }
+        }
         ok = c.next(sh);
         if (c.left <= 0) return;
-        if (ok) load();
     }
     if (lane == 0) raise_tree_error(&sh.abort_flag, p.status);
 }
@@ -435,17 +443,21 @@ __device__ void issue(const PagedParams& p, Shared& sh, uint32_t tmem) {
                 is.need(see_p, &sh.p_ready, par ^ 1);
                 if (pv_first && ++pv_item > 0) is.need(false, &sh.o_free, (pv_item - 1) & 1);
                 tc_fence_after_sync();
-                is.need(see_v, &sh.v_ready, par ^ 1);
-                see_k = mbar_test(&sh.k_ready[0], par ^ pv_turn);   // of the QK that comes next
-                if (is.lead && is.ok) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < 2; ++i) {
+                    is.need(see_v, &sh.v_ready[i], par ^ 1);
+                    if (i == 0)
+                        see_v = mbar_test(&sh.v_ready[1], par ^ 1);
+                    else
+                        see_k = mbar_test(&sh.k_ready[0], par ^ pv_turn);   // of the QK that comes next
+                    if (is.lead && is.ok) {
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
                             umma_pair_bf16(tmem + kTmemO + 128 * i, pd + (((k >> 2) * kChunkBytes + (k & 3) * 32u) >> 4),
                                            vd + (((2 * i + (k >> 2)) * kSlotBytes + (k & 3) * 2048u) >> 4), idesc_pv,
                                            k == 0 ? pv_first ^ 1u : 1u);
-                    if (g < total) umma_commit_pair(&sh.v_empty);
+                        if (g < total) umma_commit_pair(&sh.v_empty[i]);
+                    }
                 }
                 if (is.lead && is.ok) umma_commit_pair(&sh.o_done);
                 see_p = see_v = false;
@@ -456,31 +468,31 @@ __device__ void issue(const PagedParams& p, Shared& sh, uint32_t tmem) {
                 if (first) is.need(false, &sh.q_ready, item & 1);
                 // (the scores of tile g - 2 have been read: PV(g - 2) waited for their P)
 #pragma unroll
-                for (int pair = 0; pair < 2; ++pair) {
-                    is.need(see_k, &sh.k_ready[pair], par);
-                    if (pair == 0) {
-                        see_k = mbar_test(&sh.k_ready[1], par);
-                        tc_fence_after_sync();
+                for (int s = 0; s < kSlots; ++s) {
+                    is.need(see_k, &sh.k_ready[s], par);
+                    if (s < kSlots - 1) {
+                        see_k = mbar_test(&sh.k_ready[s + 1], par);
                     } else {
                         is.need(false, &sh.rope_ready, par);
                         if (pv_turn == 1 && g >= 1) {
                             see_p = mbar_test(&sh.p_ready, par ^ 1);
-                            see_v = mbar_test(&sh.v_ready, par ^ 1);
+                            see_v = mbar_test(&sh.v_ready[0], par ^ 1);
                         }
                     }
+                    if (s == 0) tc_fence_after_sync();
                     if (is.lead && is.ok) {
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const uint32_t off = ((4 * pair + (k >> 2)) * kChunkBytes + (k & 3) * 32u) >> 4;
-                            umma_pair_bf16(d, q + off, kd + off, idesc_qk, (pair | k) ? 1u : 0u);
+                        for (int k = 0; k < 8; ++k) {
+                            const uint32_t off = ((2 * s + (k >> 2)) * kChunkBytes + (k & 3) * 32u) >> 4;
+                            umma_pair_bf16(d, q + off, kd + off, idesc_qk, (s | k) ? 1u : 0u);
                         }
-                        if (pair == 1) {
+                        if (s == kSlots - 1) {
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 umma_pair_bf16(d, q + ((8 * kChunkBytes + k * 32u) >> 4), rope + (k * 32u >> 4),
                                                idesc_rope, 1u);
                         }
-                        if (g + 1 < total) umma_commit_pair(&sh.k_empty[pair]);
+                        if (g + 1 < total) umma_commit_pair(&sh.k_empty[s]);
                     }
                 }
                 if (is.lead && is.ok) {
@@ -750,21 +762,27 @@ __device__ __noinline__ void find_work(const PagedParams& p, int cluster, int la
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    mla_paged_attend_kernel(const __grid_constant__ PagedParams p) {
+    mla_paged_attend_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant__ PagedParams p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     Shared& sh = *reinterpret_cast<Shared*>(smem_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_ctarank();
     const int cluster = blockIdx.x >> 1;
     if (tid == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh.k_ready[i], 4);
+        prefetch_tensormap(&maps.codes);
+        prefetch_tensormap(&maps.scales);
+        prefetch_tensormap(&maps.rope);
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(&sh.k_ready[i], 2);
             mbar_init(&sh.k_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.v_ready[i], 4);
+            mbar_init(&sh.v_empty[i], 1);
             mbar_init(&sh.s_full[i], 1);
         }
-        mbar_init(&sh.v_ready, 8);
-        mbar_init(&sh.v_empty, 1);
-        mbar_init(&sh.rope_ready, 2 * kRopeWarps);
+        for (int i = 0; i < kFillWarps; ++i) mbar_init(&sh.raw[i], 1);
+        mbar_init(&sh.rope_ready, 1);
         mbar_init(&sh.p_ready, 2 * kSoftmaxWarps);
         mbar_init(&sh.o_done, 1);
         mbar_init(&sh.q_ready, 2 * kFillWarps);
@@ -806,23 +824,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if ((smem_u32(smem_raw) & 1023u) != 0 && tid == 0) raise_tree_error(&sh.abort_flag, p.status);
     if (warp == kScoutWarp) {
         scout(p, sh, lane);
-    } else if (warp >= kRopeWarp) {
-        fill_rope(p, sh, rank, warp - kRopeWarp, lane);
+    } else if (warp == kRopeWarp) {
+        fill_rope(maps, p, sh, rank, lane);
     } else if (warp == kMmaWarp) {
         if (rank == 0)
             issue(p, sh, tmem);
         else
             write_empty(p, cluster, p.clusters, lane);
-    } else if (warp >= kValueWarp) {
-        fill<false>(p, sh, rank, warp, lane);
-    } else if (warp >= kKeyWarp) {
-        fill<true>(p, sh, rank, warp, lane);
-    } else {
+    } else if (warp >= kKeyWarp && warp < kMmaWarp) {
+        fill(maps, p, sh, rank, warp, lane);
+    } else if (warp < kSoftmaxWarps) {
         softmax(p, sh, tmem, rank, cluster, tid);
     }
     __syncthreads();
     if (*static_cast<volatile int*>(&sh.abort_flag)) {
-        // nothing more is issued by this CTA: let its MMAs end
+        // nothing more is issued by this CTA: let its copies and MMAs end
         const long long t0 = clock64();
         while (clock64() - t0 < kDrainCycles) {
         }
@@ -842,7 +858,7 @@ cudaError_t paged_attend_prepare() {
                                 static_cast<int>(sizeof(Shared)));
 }
 
-cudaError_t launch_paged_attend(const PagedParams& p, bool pdl, cudaStream_t stream) {
+cudaError_t launch_paged_attend(const PagedMaps& maps, const PagedParams& p, bool pdl, cudaStream_t stream) {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -853,7 +869,7 @@ cudaError_t launch_paged_attend(const PagedParams& p, bool pdl, cudaStream_t str
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, mla_paged_attend_kernel, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, mla_paged_attend_kernel, maps, p);
     return e != cudaSuccess ? e : launch_tree_merge(p, pdl, stream);
 }
 

@@ -63,6 +63,7 @@ __device__ __forceinline__ float2 f16x2_to_float2(uint32_t v) { return __half22f
 
 // Host: the cache's fields as the kernels take them, checked.
 int check_cache(const mla_paged_cache* c);
+int encode_q4_boxes(CUtensorMap* map, const mla_paged_cache* c, uint32_t box_bytes, CUtensorMapSwizzle swizzle);
 PagedCache paged_cache(const mla_paged_cache* c);
 
 }  // namespace mla
