@@ -77,13 +77,13 @@ int encode_bf16_row_chunks(CUtensorMap* map, const void* base, long long rows, l
     return r == CUDA_SUCCESS ? MLA_OK : MLA_ECUDA;
 }
 
-// View {416 bytes, page_rows, n_pages} of a 4-bit cache's pages; boxes of `box_bytes` of up to 64 rows of a page.
+// View {416 bytes, page_rows, n_pages} of a 4-bit cache's pages; boxes of `box_bytes` of up to 32 rows of a page.
 int encode_q4_boxes(CUtensorMap* map, const mla_paged_cache* c, uint32_t box_bytes, CUtensorMapSwizzle swizzle) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (!enc) return MLA_ECUDA;
     const cuuint64_t dims[3] = {MLA_Q4_ROW, static_cast<cuuint64_t>(c->page_rows), static_cast<cuuint64_t>(c->n_pages)};
     const cuuint64_t strides[2] = {MLA_Q4_ROW, static_cast<cuuint64_t>(c->page_stride)};
-    const cuuint32_t box[3] = {box_bytes, static_cast<cuuint32_t>(c->page_rows < 64 ? c->page_rows : 64), 1u};
+    const cuuint32_t box[3] = {box_bytes, static_cast<cuuint32_t>(c->page_rows < 32 ? c->page_rows : 32), 1u};
     const cuuint32_t elem_strides[3] = {1u, 1u, 1u};
     const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, c->pages, dims, strides, box, elem_strides,
                            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_NONE,

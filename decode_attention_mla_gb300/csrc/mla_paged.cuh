@@ -39,7 +39,7 @@ __device__ __forceinline__ int tile_row(const TreeRequest& r, int tile) {
     return (tile < r.lo ? tile : tile + static_cast<int>(r.base)) * kTreeTileKeys;
 }
 
-// Views {416 bytes, page_rows, n_pages} of the pages; boxes of min(page_rows, 64) rows.
+// Views {416 bytes, page_rows, n_pages} of the pages; boxes of min(page_rows, 32) rows.
 struct PagedMaps {
     CUtensorMap codes;                                     // 64 bytes of a row, 64-byte swizzled
     CUtensorMap scales;                                    // 16 bytes

@@ -9,8 +9,8 @@
 //
 // Operands.  A latent value is code * scale * kv_scale; code * scale has six
 // significant bits and lies between 2^-10 and 2688, so it is exact in f16.  Eight warps
-// per CTA write the tiles' operands in the swizzled layout, a slot each: K (this CTA's 64 rows, 128 of 512
-// columns) and V (64 of the tile's rows, 128 of this CTA's 256 features).  The rows' bytes come by TMA
+// per CTA write the tiles' operands in the swizzled layout, slots of 64 rows x 128 columns: K (this CTA's rows,
+// four slots) and V (the tile's rows, this CTA's 256 features, four slots).  The rows' bytes come by TMA
 // into the slot itself, pass through registers, and go back widened (one conversion and one product per two
 // values): there is no room for them beside the operands.  (Through registers alone, by loads of 16 bytes a
 // lane a tile ahead: 507 us where this form takes 326 for 16 requests of 4 x 128; the loads in flight do not
@@ -33,9 +33,8 @@
 // Every wait is bounded; a wait that runs out raises MLA_EDEVICE in the status word, both CTAs
 // leave their loops and meet at a cluster barrier.
 //
-// Warps of a CTA: 0-7 softmax and epilogue, 8-11 K, 12-15 V (all eight: queries), 16 MMA issue
-// (even CTA; the odd one's writes empty requests) and tensor memory, 17 key values,
-// 18 the items of the run, 19 idle.  Barriers that the MMA warp waits
+// Warps of a CTA: 0 MMA issue (even CTA; the odd one's writes empty requests) and tensor memory, 1 TMA of K, 2 TMA of V,
+// 3 the items of the run, 4-11 softmax and epilogue, 12-19 operands and queries.  Barriers that the MMA warp waits
 // on live in the even CTA and take arrivals of both.
 #include <cmath>
 
@@ -53,9 +52,9 @@ constexpr uint32_t kChunkBytes = 8192;
 constexpr uint32_t kQBytes = 9 * kChunkBytes;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
-constexpr int kKeyWarp = 8, kValueWarp = 12, kFillWarps = 8, kMmaWarp = 16;
-constexpr int kRopeWarp = 17, kScoutWarp = 18;
-constexpr int kItemReaders = kSoftmaxWarps + kFillWarps + 1;   // and the even CTA's MMA warp
+constexpr int kMmaWarp = 0, kKeyWarp = 1, kValueWarp = 2, kScoutWarp = 3;
+constexpr int kSoftmaxWarp = 4, kFillWarp = 12, kFillWarps = 8;
+constexpr int kItemReaders = kSoftmaxWarps + kFillWarps + 2;   // and the even CTA's MMA warp
 constexpr int kThreads = 640;
 constexpr int kBarSoftmax = 1;                             // hardware barrier of the softmax warps
 constexpr uint32_t kTmemCols = 512;
@@ -88,7 +87,7 @@ struct __align__(1024) Shared {
     uint64_t k_ready[kSlots], rope_ready, v_ready[2], q_ready, p_ready, o_free;
     // in each CTA, arrivals of the MMA thread
     uint64_t k_empty[kSlots], v_empty[2], q_empty, s_full[2], o_done;
-    uint64_t raw[kFillWarps];                              // a slot's bytes have landed in it
+    uint64_t k_raw[kSlots], v_raw[kSlots];                 // a slot's bytes have landed in it
     // this CTA's query rows are there, by item mod 2 (those of an item may be there before the softmax
     // warps have come to the one before)
     uint64_t q_local[2];
@@ -198,31 +197,32 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 __device__ __forceinline__ uint32_t low_half_twice(uint32_t v) { return __byte_perm(v, v, 0x1010); }
 __device__ __forceinline__ uint32_t high_half_twice(uint32_t v) { return __byte_perm(v, v, 0x3232); }
 
-// Rows per box: a page's, 64 at most.
-__device__ __forceinline__ int box_rows(const PagedCache& c) { return min(1 << c.row_shift, 64); }
+// Rows per box: a page's, 32 at most.
+__device__ __forceinline__ int box_rows(const PagedCache& c) { return min(1 << c.row_shift, 32); }
 
-// One slot: 64 rows (half a tile) x 128 features.  The rows' bytes land in the slot itself, 64 bytes of codes a
-// row (64-byte swizzled) and behind them 16 bytes of scales, of which eight are the slot's; they are taken to registers, all
-// of them, and the widened values written over them.
-constexpr int kRawScales = 64 * 64;                        // where the scales land
+// One slot: 64 rows (half a tile) x 128 features.  The rows' bytes land in the slot itself, where 32 rows' widened
+// values go to: their codes, 64 bytes a row (64-byte swizzled), in the first of their two 4 KB pieces, 16 bytes of scales
+// a row, of which eight are the slot's, in the second.  One warp takes these to registers, all of them, and writes
+// the widened values over them.
+constexpr uint32_t kHalfBytes = 4096;                      // 32 rows of a chunk
 constexpr uint32_t kRawBytes = 64 * (64 + 16);
 
-__device__ __forceinline__ void widen_slot(uint32_t slot, int scale_byte, bool clean, int lane) {
+__device__ __forceinline__ void widen_half(uint32_t piece, int scale_byte, bool clean, int lane) {
     const int row = lane & 7, unit = lane >> 3;            // of eight rows; 32 features
-    uint4 raw[8];
-    uint32_t scales[8];
+    uint4 raw[4];
+    uint32_t scales[4];
     // (64-byte swizzle: 16-byte unit u of row r lies at u ^ (r / 2 mod 4))
-    const uint32_t from = slot + row * 64 + ((unit ^ ((row >> 1) & 3)) << 4);
-    const uint32_t scale_from = slot + kRawScales + row * 16 + scale_byte + 2 * unit;
+    const uint32_t from = piece + row * 64 + ((unit ^ ((row >> 1) & 3)) << 4);
+    const uint32_t scale_from = piece + kChunkBytes + row * 16 + scale_byte + 2 * unit;
 #pragma unroll
-    for (int n = 0; n < 8; ++n) {
+    for (int n = 0; n < 4; ++n) {
         raw[n] = ld_shared_v4(from + n * 512);
         scales[n] = ld_shared_u16(scale_from + n * 128);
     }
     __syncwarp();                                          // every lane has its bytes: they may be overwritten
-    const uint32_t line = slot + (unit >> 1) * kChunkBytes + row * 128;
+    const uint32_t line = piece + (unit >> 1) * kChunkBytes + row * 128;
 #pragma unroll
-    for (int n = 0; n < 8; ++n) {
+    for (int n = 0; n < 4; ++n) {
         uint32_t s = widen_e4m3(static_cast<uint16_t>(scales[n]));
         if (clean) s &= __heq2_mask(*reinterpret_cast<__half2*>(&s), *reinterpret_cast<__half2*>(&s));
         const uint32_t lo = low_half_twice(s), hi = high_half_twice(s);
@@ -298,87 +298,142 @@ __device__ __forceinline__ void fill_queries(const PagedParams& p, Shared& sh, l
     }
 }
 
-// Where a box of the tile's rows lies: page and row in it (a page behind the last one: the box is zeros).
-struct Place {
-    int page, row;
-    __device__ __forceinline__ void find(const PagedCache& c, int b, int t) {
-        page = page_of(c, b, t);
-        if (page < 0) page = c.n_pages;
-        row = t & ((1 << c.row_shift) - 1);
+// The warps that write operands, all of them those of K, then those of V: 32 rows of a slot each.  K of a tile goes before
+// V of the tile before it, as the products do.
+__device__ void fill(const PagedParams& p, Shared& sh, uint32_t rank, int nth, int lane) {
+    const int slot = nth >> 1;
+    const uint32_t leader = map_to_rank(&sh, 0) - smem_u32(&sh);
+    const uint32_t k_ready = smem_u32(&sh.k_ready[slot]) + leader, v_ready = smem_u32(&sh.v_ready[slot >> 1]) + leader;
+    const uint32_t k_piece = smem_u32(sh.k[slot]) + (nth & 1) * kHalfBytes, v_piece = smem_u32(sh.v[slot]) + (nth & 1) * kHalfBytes;
+    // (which eight of the sixteen scale bytes are the slot's)
+    const int k_scale = 8 * (slot & 1), v_scale = 8 * (slot >> 1);
+    const int total = static_cast<int>(sh.work.count);
+    int item = 0, in_item = 0;                             // of the K at hand; its tiles still to come
+    for (int g = 0; g <= total && total > 0; ++g) {
+        if (g < total) {
+            if (in_item == 0) {
+                if (!warp_wait(&sh.abort_flag, &sh.item_full[item % kItems], (item / kItems) & 1)) break;
+                const Item& i = sh.items[item % kItems];
+                in_item = i.hi - i.lo;
+                if (item > 0 && !warp_wait(&sh.abort_flag, &sh.q_empty, (item - 1) & 1)) break;
+                const int r0 = i.rb * kTreeBlockRows + static_cast<int>(rank) * 64 + 8 * nth;
+                fill_queries(p, sh, static_cast<long long>(i.b) * p.tokens * p.heads + r0,
+                             min(i.n_tok * p.heads - r0, 8), item, nth, lane);
+                hand_over(smem_u32(&sh.q_ready) + leader, lane);
+                if (lane == 0) mbar_arrive(&sh.q_local[item & 1]);
+                Walk::release(sh, item, lane);
+                ++item;
+            }
+            --in_item;
+            if (!warp_wait(&sh.abort_flag, &sh.k_raw[slot], g & 1)) break;
+            widen_half(k_piece, k_scale, false, lane);
+            hand_over(k_ready, lane);
+        }
+        if (g > 0) {
+            if (!warp_wait(&sh.abort_flag, &sh.v_raw[slot], (g - 1) & 1)) break;
+            widen_half(v_piece, v_scale, true, lane);
+            hand_over(v_ready, lane);
+        }
+        if (g == total) return;
+    }
+    if (total > 0 && lane == 0) raise_tree_error(&sh.abort_flag, p.status);
+}
+
+// The warps that ask for the bytes: a slot's when the products with the tile before are done.
+struct Producer {
+    const PagedMaps& maps;
+    const PagedParams& p;
+    Shared& sh;
+    const uint32_t rank;
+    const int lane, box;                                   // rows per box; a lane has one of those of 64 rows
+    const uint64_t policy;
+
+    __device__ __forceinline__ int row() const { return box * (lane & (64 / box - 1)); }
+    // page of this lane's box of the 64 rows from t0 on (one behind the last one: the box is zeros), and its row there
+    __device__ __forceinline__ int page(int b, int t0) const {
+        const int page = page_of(p.cache, b, t0 + row());
+        return page < 0 ? p.cache.n_pages : page;
+    }
+    __device__ __forceinline__ int row_in_page(int t0) const { return (t0 + row()) & ((1 << p.cache.row_shift) - 1); }
+    // 64 rows of a slot: 64 bytes of codes from byte `from` on
+    __device__ __forceinline__ void slot(uint8_t* dst, uint64_t* bar, int from, int page, int in_page) const {
+        if (lane == 0) mbar_arrive_expect_tx(bar, kRawBytes);
+        __syncwarp();
+        if (lane < 64 / box) {
+            uint8_t* piece = dst + (row() >> 5) * kHalfBytes;
+            tma_load_3d(piece + (row() & 31) * 64, &maps.codes, from, in_page, page, bar, policy);
+            tma_load_3d(piece + kChunkBytes + (row() & 31) * 16, &maps.scales, kQ4Scales + 16 * (from >> 7), in_page, page,
+                        bar, policy);
+        }
     }
 };
 
-// The warps that write operands: a slot of K (this CTA's 64 rows) or of V (half kb of the tile's rows, 128 of this
-// CTA's 256 features).  A slot's bytes are asked for when the products with the tile before are done; that, their way
-// from L2 and the widening take place while the other product runs.
-__device__ void fill(const PagedMaps& maps, const PagedParams& p, Shared& sh, uint32_t rank, int warp, int lane) {
-    const bool keys = warp < kValueWarp;
-    const int nth = warp - kKeyWarp, slot = nth & 3;
-    const int row0 = 64 * (keys ? static_cast<int>(rank) : slot & 1);
-    const int from = keys ? 64 * slot : 128 * static_cast<int>(rank) + 64 * (slot >> 1);   // byte of the rows' codes
-    const uint32_t leader = map_to_rank(&sh, 0) - smem_u32(&sh);
-    uint64_t* empty = keys ? &sh.k_empty[slot] : &sh.v_empty[slot >> 1];
-    const uint32_t ready = smem_u32(keys ? &sh.k_ready[slot] : &sh.v_ready[slot >> 1]) + leader;
-    uint8_t* dst = keys ? sh.k[slot] : sh.v[slot];
-    const uint64_t policy = l2_policy_evict_normal();
-    const int box = box_rows(p.cache), boxes = 64 / box;
+// K and the key values of this CTA's 64 rows.
+__device__ void produce_keys(const PagedMaps& maps, const PagedParams& p, Shared& sh, uint32_t rank, int lane) {
+    const Producer pr{maps, p, sh, rank, lane, box_rows(p.cache), l2_policy_evict_normal()};
+    const uint32_t rope_bar = map_to_rank(&sh.rope_ready, 0);
+    const int mine = 64 * static_cast<int>(rank);
     Walk c;
     bool ok = c.start(sh);
     if (c.left <= 0) return;
-    Place at;
-    at.find(p.cache, c.b, c.row() + row0 + box * (lane & (boxes - 1)));
+    int page = 0, at = 0;
+    if (ok) {
+        page = pr.page(c.b, c.row() + mine);
+        at = pr.row_in_page(c.row() + mine);
+    }
     while (ok) {
         const int g = c.g;
-        if (g > 0 && !warp_wait(&sh.abort_flag, empty, (g - 1) & 1)) break;
-        if (lane == 0) mbar_arrive_expect_tx(&sh.raw[nth], kRawBytes);
+        if (c.first) Walk::release(sh, c.item, lane);
+#pragma unroll 1
+        for (int s = 0; s < kSlots && ok; ++s) {
+            ok = g == 0 || warp_wait(&sh.abort_flag, &sh.k_empty[s], (g - 1) & 1);
+            if (ok) pr.slot(sh.k[s], &sh.k_raw[s], 64 * s, page, at);
+        }
+        if (!ok) break;
+        // (the even CTA announces both CTAs' bytes; the odd one's may land first: the phase is open until then)
+        if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&sh.rope_ready, 2 * kChunkBytes);
         __syncwarp();
-        if (lane < boxes) {
-            tma_load_3d(dst + lane * box * 64, &maps.codes, from, at.row, at.page, &sh.raw[nth], policy);
-            tma_load_3d(dst + kRawScales + lane * box * 16, &maps.scales, kQ4Scales + 16 * (from >> 7), at.row, at.page,
-                        &sh.raw[nth], policy);
-        }
-        if (c.first) {
-            if (c.item > 0 && !warp_wait(&sh.abort_flag, &sh.q_empty, (c.item - 1) & 1)) break;
-            const Item& i = sh.items[c.item % kItems];
-            const int r0 = i.rb * kTreeBlockRows + static_cast<int>(rank) * 64 + 8 * nth;
-            fill_queries(p, sh, static_cast<long long>(i.b) * p.tokens * p.heads + r0, min(i.n_tok * p.heads - r0, 8),
-                         c.item, nth, lane);
-            hand_over(smem_u32(&sh.q_ready) + leader, lane);
-            if (lane == 0) mbar_arrive(&sh.q_local[c.item & 1]);
-            Walk::release(sh, c.item, lane);
-        }
+        if (lane < 64 / pr.box)
+            tma_load_3d_pair(sh.rope + pr.row() * 128, &maps.rope, kQ4Rope, at, page, rope_bar, pr.policy);
         ok = c.next(sh);
-        if (c.left > 0 && ok) at.find(p.cache, c.b, c.row() + row0 + box * (lane & (boxes - 1)));
-        if (!warp_wait(&sh.abort_flag, &sh.raw[nth], g & 1)) break;
-        widen_slot(smem_u32(dst), from >> 3 & 8, !keys, lane);
-        hand_over(ready, lane);
         if (c.left <= 0) return;
+        if (ok) {                                          // the next tile's place, looked up ahead
+            page = pr.page(c.b, c.row() + mine);
+            at = pr.row_in_page(c.row() + mine);
+        }
     }
     if (lane == 0) raise_tree_error(&sh.abort_flag, p.status);
 }
 
-// The key values of this CTA's 64 rows, as they are, and the rows of a later tile on their way to L2.
+// V of the tile's rows, this CTA's 256 features; and this CTA's 64 rows of a later tile on their way to L2.
 constexpr int kAhead = 3;                                  // tiles
-__device__ void fill_rope(const PagedMaps& maps, const PagedParams& p, Shared& sh, uint32_t rank, int lane) {
-    const uint32_t bar = map_to_rank(&sh.rope_ready, 0);
-    const uint64_t policy = l2_policy_evict_normal();
-    const int box = box_rows(p.cache), boxes = 64 / box;
-    const int row0 = 64 * static_cast<int>(rank) + box * (lane & (boxes - 1));
+__device__ void produce_values(const PagedMaps& maps, const PagedParams& p, Shared& sh, uint32_t rank, int lane) {
+    const Producer pr{maps, p, sh, rank, lane, box_rows(p.cache), l2_policy_evict_normal()};
     Walk c;
     bool ok = c.start(sh);
     if (c.left <= 0) return;
     Walk ahead = c;
+    int page[2] = {}, at[2] = {};
+    auto find = [&] {
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            page[kb] = pr.page(c.b, c.row() + 64 * kb);
+            at[kb] = pr.row_in_page(c.row() + 64 * kb);
+        }
+    };
+    if (ok) find();
     while (ok) {
         const int g = c.g;
-        Place at;
-        at.find(p.cache, c.b, c.row() + row0);
-        if (g > 0 && !warp_wait(&sh.abort_flag, &sh.k_empty[kSlots - 1], (g - 1) & 1)) break;
-        // (the even CTA announces both CTAs' bytes; the odd one's may land first: the phase is open until then)
-        if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&sh.rope_ready, 2 * kChunkBytes);
-        __syncwarp();
-        if (lane < boxes)
-            tma_load_3d_pair(sh.rope + lane * box * 128, &maps.rope, kQ4Rope, at.row, at.page, bar, policy);
         if (c.first) Walk::release(sh, c.item, lane);
+#pragma unroll 1
+        for (int i = 0; i < 2 && ok; ++i) {
+            ok = g == 0 || warp_wait(&sh.abort_flag, &sh.v_empty[i], (g - 1) & 1);
+            if (!ok) break;
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+                pr.slot(sh.v[2 * i + kb], &sh.v_raw[2 * i + kb], 128 * static_cast<int>(rank) + 64 * i, page[kb], at[kb]);
+        }
+        if (!ok) break;
         if (ahead.g < g) ahead = c;
         while (ahead.g < g + kAhead && ahead.left > 1) {
             // (an item that is not laid out yet is not waited for)
@@ -386,13 +441,14 @@ __device__ void fill_rope(const PagedMaps& maps, const PagedParams& p, Shared& s
                 !__all_sync(0xffffffffu, mbar_test(&sh.item_full[(ahead.item + 1) % kItems], ((ahead.item + 1) / kItems) & 1)))
                 break;
             if (!ahead.next(sh)) break;
-            if (lane < boxes) {
-                const int page = page_of(p.cache, ahead.b, ahead.row() + row0);
-                if (page >= 0) bulk_prefetch_l2(row_in(p.cache, page, ahead.row() + row0), box * MLA_Q4_ROW);
+            if (lane < 64 / pr.box) {
+                const int t = ahead.row() + 64 * static_cast<int>(rank) + pr.row(), far = page_of(p.cache, ahead.b, t);
+                if (far >= 0) bulk_prefetch_l2(row_in(p.cache, far, t), pr.box * MLA_Q4_ROW);
             }
         }
         ok = c.next(sh);
         if (c.left <= 0) return;
+        if (ok) find();
     }
     if (lane == 0) raise_tree_error(&sh.abort_flag, p.status);
 }
@@ -773,15 +829,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         prefetch_tensormap(&maps.scales);
         prefetch_tensormap(&maps.rope);
         for (int i = 0; i < kSlots; ++i) {
-            mbar_init(&sh.k_ready[i], 2);
+            mbar_init(&sh.k_ready[i], 4);
             mbar_init(&sh.k_empty[i], 1);
+            mbar_init(&sh.k_raw[i], 1);
+            mbar_init(&sh.v_raw[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh.v_ready[i], 4);
+            mbar_init(&sh.v_ready[i], 8);
             mbar_init(&sh.v_empty[i], 1);
             mbar_init(&sh.s_full[i], 1);
         }
-        for (int i = 0; i < kFillWarps; ++i) mbar_init(&sh.raw[i], 1);
         mbar_init(&sh.rope_ready, 1);
         mbar_init(&sh.p_ready, 2 * kSoftmaxWarps);
         mbar_init(&sh.o_done, 1);
@@ -802,11 +859,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == kMmaWarp) tmem_alloc_pair(&sh.tmem_base, kTmemCols);
     grid_dependency_wait();
     allow_dependent_launch();
-    if (warp == kKeyWarp) {
+    if (warp == kScoutWarp) {
         find_work(p, cluster, lane, &sh.work);
-    } else if (warp > kKeyWarp && warp < kMmaWarp) {
+    } else if (warp >= kFillWarp) {
         // query rows behind the last one: zeros, so that their scores are finite
-        for (int i = (warp - kKeyWarp - 1) * 32 + lane; i < static_cast<int>(kQBytes / 16); i += 7 * 32)
+        for (int i = tid - 32 * kFillWarp; i < static_cast<int>(kQBytes / 16); i += 32 * kFillWarps)
             reinterpret_cast<uint4*>(sh.q)[i] = make_uint4(0, 0, 0, 0);
     }
     tc_fence_before_sync();
@@ -814,7 +871,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_wait();                                        // both CTAs' barriers are initialised
     tc_fence_after_sync();
     const uint32_t tmem = sh.tmem_base;
-    if (p.stall_test && blockIdx.x == 0 && tid == 32 * kKeyWarp) {
+    if (p.stall_test && blockIdx.x == 0 && tid == 32 * kScoutWarp) {
         // test hook: a wait that runs out, so the abort path runs for real
         volatile int never = 0;
         if (!mbar_wait_bounded(&sh.stall_bar, 0, &never, kStallTestCycles)) raise_tree_error(&sh.abort_flag, p.status);
@@ -822,19 +879,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
     // the dynamic window starts 1024-byte aligned (the 128-byte swizzle needs it)
     if ((smem_u32(smem_raw) & 1023u) != 0 && tid == 0) raise_tree_error(&sh.abort_flag, p.status);
-    if (warp == kScoutWarp) {
-        scout(p, sh, lane);
-    } else if (warp == kRopeWarp) {
-        fill_rope(maps, p, sh, rank, lane);
+    if (warp >= kFillWarp) {
+        fill(p, sh, rank, warp - kFillWarp, lane);
+    } else if (warp >= kSoftmaxWarp) {
+        softmax(p, sh, tmem, rank, cluster, tid - 32 * kSoftmaxWarp);
     } else if (warp == kMmaWarp) {
         if (rank == 0)
             issue(p, sh, tmem);
         else
             write_empty(p, cluster, p.clusters, lane);
-    } else if (warp >= kKeyWarp && warp < kMmaWarp) {
-        fill(maps, p, sh, rank, warp, lane);
-    } else if (warp < kSoftmaxWarps) {
-        softmax(p, sh, tmem, rank, cluster, tid);
+    } else if (warp == kKeyWarp) {
+        produce_keys(maps, p, sh, rank, lane);
+    } else if (warp == kValueWarp) {
+        produce_values(maps, p, sh, rank, lane);
+    } else {
+        scout(p, sh, lane);
     }
     __syncthreads();
     if (*static_cast<volatile int*>(&sh.abort_flag)) {
