@@ -27,15 +27,16 @@ int check_shape(const mla_paged_shape* s) {
     return MLA_OK;
 }
 
-// Scratch as of a tree plan: status word, the pairs' merge notes, their pieces and the pieces'
-// log-sum-exps, each region 256-byte aligned.
+// Scratch as of a tree plan: status word, the runs' merge notes, their pieces and the pieces'
+// log-sum-exps, each region 256-byte aligned.  A run is a pair's (pieces of 128 query rows) or, with few
+// query rows, an SM's (pieces of 16, in the place of 32): twice as many notes, fewer bytes.
 constexpr size_t kMergeOffset = 256;
 int pairs_of(int num_sms) { return num_sms < 2 ? 1 : num_sms / 2; }
 void layout(mla_paged_plan_t* pl) {
     const size_t pairs = static_cast<size_t>(pairs_of(pl->num_sms));
     pl->grid = static_cast<int>(2 * pairs);
     pl->status_offset = 0;
-    pl->part_offset = up256(kMergeOffset + pairs * kTreePieces * (sizeof(TreeMerge) + sizeof(TreeCut)));
+    pl->part_offset = up256(kMergeOffset + 2 * pairs * kTreePieces * (sizeof(TreeMerge) + sizeof(TreeCut)));
     pl->lse_part_offset = pl->part_offset + pairs * kTreePieces * kTreeBlockRows * kDLatent * sizeof(float);
     pl->scratch_bytes = up256(pl->lse_part_offset + pairs * kTreePieces * kTreeBlockRows * sizeof(float));
 }
@@ -77,12 +78,22 @@ int prepare(cudaStream_t st, bool may_capture) {
         if (cs != cudaStreamCaptureStatusNone) return MLA_ENOTREADY;
     }
     std::lock_guard<std::mutex> lock(g_paged_mutex);
-    if (launch_status(paged_attend_prepare()) != MLA_OK) return MLA_ECUDA;
+    if (launch_status(paged_attend_prepare()) != MLA_OK || launch_status(paged_decode_prepare()) != MLA_OK)
+        return MLA_ECUDA;
     g_paged_prepared[dev].store(1, std::memory_order_release);
     return MLA_OK;
 }
 
-PagedParams params(const mla_paged_plan_t* pl, const mla_paged_args* a, void* scratch) {
+// Few query rows: on warp-level MMAs, an SM's run each.  (It counts units of 64 rows in an int.)
+constexpr int kFewRows = 32;
+bool few_rows(const mla_paged_plan_t* pl, const mla_paged_args* a) {
+    const long long rows = static_cast<long long>(pl->shape.tokens) * pl->shape.heads;
+    const long long blocks = (rows + kDecodeBlockRows - 1) / kDecodeBlockRows;
+    const long long units = static_cast<long long>(a->cache.columns) * a->cache.page_rows / 64 + 1;
+    return rows <= kFewRows && pl->shape.batch * blocks * units < (1ll << 30);
+}
+
+PagedParams params(const mla_paged_plan_t* pl, const mla_paged_args* a, void* scratch, bool few) {
     char* base = static_cast<char*>(scratch);
     PagedParams p{};
     p.a.d_pos = a->d_pos;
@@ -93,7 +104,8 @@ PagedParams params(const mla_paged_plan_t* pl, const mla_paged_args* a, void* sc
     p.batch = pl->shape.batch;
     p.tokens = pl->shape.tokens;
     p.heads = pl->shape.heads;
-    p.clusters = pl->grid / 2;
+    p.clusters = few ? pl->grid : pl->grid / 2;
+    p.block_rows = few ? kDecodeBlockRows : kTreeBlockRows;
     p.scale_log2 = scale_log2(pl->shape.scale);
     p.merge = reinterpret_cast<TreeMerge*>(base + kMergeOffset);
     p.cut = reinterpret_cast<TreeCut*>(p.merge + kTreePieces * p.clusters);
@@ -143,13 +155,16 @@ int mla_paged_forward(const mla_paged_plan_t* plan, const mla_paged_args* args, 
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     rc = mla::prepare(st, true);
     if (rc != MLA_OK) return rc;
+    const bool few = mla::few_rows(plan, args);
+    const mla::PagedParams p = mla::params(plan, args, scratch, few);
+    if (few) return mla::launch_status(mla::launch_paged_decode(p, plan->shape.pdl != 0, st));
     mla::PagedMaps maps;
     rc = mla::encode_q4_boxes(&maps.codes, &args->cache, 64, CU_TENSOR_MAP_SWIZZLE_64B);
     if (rc == MLA_OK) rc = mla::encode_q4_boxes(&maps.scales, &args->cache, 16, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (rc == MLA_OK) rc = mla::encode_q4_boxes(&maps.rope, &args->cache, 128, CU_TENSOR_MAP_SWIZZLE_128B);
     if (rc != MLA_OK) return rc;
     return mla::launch_status(
-        mla::launch_paged_attend(maps, mla::params(plan, args, scratch), plan->shape.pdl != 0, st));
+        mla::launch_paged_attend(maps, p, plan->shape.pdl != 0, st));
 }
 
 }  // extern "C"

@@ -14,9 +14,12 @@ struct PagedParams : TreeParams {                          // (of a.*: d_pos, n_
     int window, sink;
 };
 
-// A request's rows, in tiles of kTreeTileKeys, those that no token attends left out: the
-// first `lo` tiles (the rows before `sink`), then those `base` further on; hi: tiles * kTreeTileKeys.
-__device__ __forceinline__ TreeRequest load_tree_request(const PagedParams& p, int b) {
+constexpr int kDecodeBlockRows = 16;                       // query rows per block of the kernel for few of them
+
+// A request's rows, in tiles of kRows, those that no token attends left out: the first `lo` tiles (the
+// rows before `sink`), then those `base` further on; hi: tiles * kRows.
+template <int kRows>
+__device__ __forceinline__ TreeRequest load_paged_request(const PagedParams& p, int b) {
     TreeRequest r;
     r.d_pos = p.a.d_pos[b];
     r.n_tok = p.a.n_tokens ? min(max(p.a.n_tokens[b], 0), p.tokens) : p.tokens;
@@ -24,21 +27,19 @@ __device__ __forceinline__ TreeRequest load_tree_request(const PagedParams& p, i
     r.lo = r.hi = 0;
     if (r.d_pos < 0 || r.n_tok == 0) return r;
     const int end = static_cast<int>(min(static_cast<long long>(r.d_pos) + r.n_tok, static_cast<long long>(paged_rows(p.cache))));
-    int tiles = (end + kTreeTileKeys - 1) / kTreeTileKeys;
+    int tiles = (end + kRows - 1) / kRows;
     if (p.window > 0) {
-        r.lo = min(p.sink / kTreeTileKeys + (p.sink % kTreeTileKeys != 0), tiles);
-        const int first = min(max(max(r.d_pos - p.window + 1, 0) / kTreeTileKeys, r.lo), tiles);
+        r.lo = min(p.sink / kRows + (p.sink % kRows != 0), tiles);
+        const int first = min(max(max(r.d_pos - p.window + 1, 0) / kRows, r.lo), tiles);
         r.base = first - r.lo;
         tiles -= first - r.lo;
     }
-    r.hi = tiles * kTreeTileKeys;
+    r.hi = tiles * kRows;
     return r;
 }
-// First row of the request's tile.
-__device__ __forceinline__ int tile_row(const TreeRequest& r, int tile) {
-    return (tile < r.lo ? tile : tile + static_cast<int>(r.base)) * kTreeTileKeys;
+__device__ __forceinline__ TreeRequest load_tree_request(const PagedParams& p, int b) {
+    return load_paged_request<kTreeTileKeys>(p, b);
 }
-
 // Views {416 bytes, page_rows, n_pages} of the pages; boxes of min(page_rows, 32) rows.
 struct PagedMaps {
     CUtensorMap codes;                                     // 64 bytes of a row, 64-byte swizzled
@@ -46,6 +47,8 @@ struct PagedMaps {
     CUtensorMap rope;                                      // 128 bytes, 128-byte swizzled
 };
 
+cudaError_t paged_decode_prepare();
+cudaError_t launch_paged_decode(const PagedParams& p, bool pdl, cudaStream_t stream);
 cudaError_t paged_attend_prepare();
 cudaError_t launch_paged_attend(const PagedMaps& maps, const PagedParams& p, bool pdl, cudaStream_t stream);
 

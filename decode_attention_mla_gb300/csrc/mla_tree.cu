@@ -107,6 +107,7 @@ TreeParams params(const mla_tree_plan_t* pl, const mla_tree_args* a, void* scrat
     p.heads = pl->shape.heads;
     p.q_tail = q_tail(pl);
     p.clusters = pl->grid / 2;
+    p.block_rows = kTreeBlockRows;
     p.scale_log2 = scale_log2(pl->shape.scale);
     p.merge = reinterpret_cast<TreeMerge*>(base + kMergeOffset);
     p.cut = reinterpret_cast<TreeCut*>(p.merge + kTreePieces * p.clusters);

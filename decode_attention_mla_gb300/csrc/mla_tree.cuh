@@ -39,6 +39,8 @@ struct TreeParams {
     int batch, tokens, heads;
     int q_tail;                                            // tokens * heads mod 64, rounded up to 8 (64: no rest)
     int clusters;
+    int block_rows;                                        // query rows per block: kTreeBlockRows, or what a kernel that
+                                                           // leaves pieces of fewer takes
     float scale_log2;                                      // scale * log2(e): scores in base-2 units
     float* part;                                           // fp32 [clusters][3][128 x 512], normalised, by feature quads
     float* lse_part;                                       // fp32 [clusters][3][128], base 2

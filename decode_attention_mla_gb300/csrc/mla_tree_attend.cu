@@ -365,8 +365,8 @@ __device__ void clean_v(Shared& sh, const Cursor& c, int tid) {
 // Place of a piece's feature quad: [slot][32-row group][quad][row], so that the
 // epilogue's and the merge's warps (a row per lane) touch 512 consecutive bytes.
 // (Rows of 2 KB, staged through shared memory, took 6300 cycles per row block.)
-__device__ __forceinline__ long long piece_quad(int slot, int row, int quad) {
-    return ((static_cast<long long>(slot) * (kTreeBlockRows / 32) + (row >> 5)) * (kDLatent / 4) + quad) * 32 + (row & 31);
+__device__ __forceinline__ long long piece_quad(int slot, int row, int quad, int groups = kTreeBlockRows / 32) {
+    return ((static_cast<long long>(slot) * groups + (row >> 5)) * (kDLatent / 4) + quad) * 32 + (row & 31);
 }
 
 // 64 bytes of each of a warp's 32 rows (32 features in bf16, 16 in fp32),
@@ -794,6 +794,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) mla_tree_merge_kernel(const 
     const int quad = ((static_cast<int>(blockIdx.y) % kTasks) * kQuadWarps + warp % kQuadWarps) * QUADS;
     const int row = 32 * group + lane;
     const bool live = row < rows;
+    const int groups = (p.block_rows + 31) >> 5;           // of 32 rows, per piece
     if (32 * group >= rows) return;                      // uniform over the block
     const float4* part = reinterpret_cast<const float4*>(p.part);
     float4 acc[QUADS];
@@ -810,8 +811,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps) mla_tree_merge_kernel(const 
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
                 const int at = slot(min(i0 + i, end - 1));     // (no branch: all loads at once)
-                l[i] = live ? p.lse_part[at * kTreeBlockRows + row] : -INFINITY;
-                const float4* src = part + piece_quad(at, row, quad);
+                l[i] = live ? p.lse_part[at * (32 * groups) + row] : -INFINITY;
+                const float4* src = part + piece_quad(at, row, quad, groups);
 #pragma unroll
                 for (int k = 0; k < QUADS; ++k) v[i][k] = src[32 * k];
             }
@@ -879,7 +880,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) mla_tree_merge_kernel(const 
     if (!live) return;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const long long out_row =
-        static_cast<long long>(m.b) * p.tokens * p.heads + static_cast<long long>(m.rb) * kTreeBlockRows + row;
+        static_cast<long long>(m.b) * p.tokens * p.heads + static_cast<long long>(m.rb) * p.block_rows + row;
     if (quad == 0) p.a.lse[out_row] = sum == 0.f ? -INFINITY : (base + log2f(sum)) * kLn2;
 #pragma unroll
     for (int k = 0; k < QUADS; ++k) {
@@ -931,11 +932,11 @@ cudaError_t launch_tree_merge(const TreeParams& p, bool pdl, cudaStream_t stream
     cfg.numAttrs = pdl ? 1 : 0;
     // shared row blocks: no more than there are row blocks or notes, and without
     // segments (one block per request) at most one per run
-    const int per_request = (p.tokens * p.heads + kTreeBlockRows - 1) / kTreeBlockRows;
+    const int per_request = (p.tokens * p.heads + p.block_rows - 1) / p.block_rows;
     const long long blocks = static_cast<long long>(p.batch) * per_request;
     const unsigned items =
         static_cast<unsigned>(std::min<long long>((per_request > 1 ? kTreePieces : 1) * p.clusters, blocks));
-    const int groups = (std::min(p.tokens * p.heads, kTreeBlockRows) + 31) / 32;
+    const int groups = (std::min(p.tokens * p.heads, p.block_rows) + 31) / 32;
     cfg.blockDim = dim3(32 * kMergeWarps);
     // a row block has about clusters / blocks pieces
     if (p.clusters > kFewPieces * blocks) {
