@@ -7,30 +7,31 @@
 // are in shared memory (416 bytes), and each warp takes its bytes from there twice, into the fragments
 // of Q K^T and of P V.
 //
-// A group of four warps shares the 32 rows of a slot.  Warp w has features 128 w .. + 127 (and 16 of the 64 key
-// values): its scores are partial sums, which the warps exchange through shared memory; warp w then has the whole
-// scores of rows 8 w .. + 7, and hands their probabilities to the others; and its part of O, 16 x 128 fp32, stays
-// in registers.  Two groups take alternate slots, each with a running maximum and sum of its own, and are joined at
-// an item's end.
+// A group of eight warps shares the 64 rows of a slot.  Warp w has features 64 w .. + 63 (and 16 of the 64 key
+// values of half of the rows): its scores are partial sums, which the warps exchange through shared memory; warp w then
+// has the whole scores of rows 8 w .. + 7, and hands their probabilities to the others; and its part of O, 16 x 64
+// fp32, stays in registers.  Two groups take alternate slots, each with a running maximum and sum of its own, and are
+// joined at an item's end.  (Groups of four warps with 128 features: 204 us where eight take XX for 32 requests of 16
+// heads: two warps per scheduler leave it idle two cycles of three.)
 //
-// Orders.  The contraction over features may go in any order: lane 4 g + j has, of row g of eight, features 32 j ..
-// 32 j + 31 (16 bytes of codes), four to a k-step.  Rows of a slot lie 416 bytes apart, eight banks on: with rows
-// (0, 2, 1, 3, 4, 6, 5, 7) as columns g eight lanes read 32 banks.  For P V lane 4 g + j has features 16 g .. 16 g + 15 (a block,
-// eight bytes) of rows j, 4 + j, 8 + j, 12 + j of sixteen: again all banks.  Two rows' codes are brought
-// together in bytes (low and high half), so one conversion gives the pair of values that a fragment wants.
+// Orders.  The contraction over features may go in any order: lane 4 g + j has, of row g of eight, features 16 j ..
+// 16 j + 15 (a block: eight bytes of codes), four to a k-step.  Rows of a slot lie 416 bytes apart, eight banks on, so four
+// rows' eight banks each are all 32.  For P V lane 4 g + j has features 8 g .. 8 g + 7 (four bytes) of rows j, 4 + j, 8 + j,
+// 12 + j of sixteen: again all banks.  Two rows' codes are brought together in bytes (low and high half), so one
+// conversion gives the pair of values that a fragment wants.
 //
 // A code times its scale is exact in f16 (six bits, 2^-10 .. 2688).  Queries are f16 times a power of two per row, probabilities
 // f16 times 2^7, key values and their queries bf16, as in mla_paged_attend.cu; sums are fp32.  Codes are finite whatever
 // the bytes, and a scale's NaN becomes 0 in P V (in Q K^T it stays: the row's scores are NaN); so rows that nobody
 // attends need no clearing: their scores are masked, their probabilities 0.
 //
-// Work split: units of 64 rows (a slot per group) of all requests' blocks of sixteen query rows, one equal run per SM; pieces and
+// Work split: units of 128 rows (a slot per group) of all requests' blocks of sixteen query rows, one equal run per SM; pieces and
 // their merge as in mla_tree_attend.cu.
 //
 // Bound: 16 MMAs and about 66 other instructions of a warp per row and SM, 17 cycles each way, beside 19 for its bytes from
 // HBM.
 //
-// Warps: 0-3 and 4-7 the groups, 8 bulk copies and the run's items, 9 empty requests.
+// Warps: 0-7 and 8-15 the groups, 16 bulk copies and the run's items, 17 empty requests.
 #include <cmath>
 
 #include "mla_paged.cuh"
@@ -38,18 +39,20 @@
 namespace mla {
 namespace {
 
-constexpr int kUnitRows = 64, kSlotRows = 32;
+constexpr int kUnitRows = 128, kSlotRows = 64;
 constexpr int kSlotBytes = kSlotRows * MLA_Q4_ROW;
-constexpr int kRing = 12;
-constexpr int kGroupThreads = 128, kComputeThreads = 256;
-constexpr int kProducerWarp = 8, kEmptyWarp = 9;
-constexpr int kThreads = 320;
+constexpr int kRing = 6;
+constexpr int kWarps = 8;                                  // of a group
+constexpr int kGroupThreads = 32 * kWarps, kComputeThreads = 2 * kGroupThreads;
+constexpr int kProducerWarp = 2 * kWarps, kEmptyWarp = kProducerWarp + 1;
+constexpr int kThreads = 32 * (kEmptyWarp + 1);
 constexpr int kBarGroup = 1, kBarBoth = 3;                 // hardware barriers: of each group, of both
 constexpr int kBlockRows = kDecodeBlockRows;
 constexpr float kRescaleLog2 = 8.0f;                       // move the reference when a max grows past 2^8
 constexpr float kProbLog2 = 7.0f;                          // P is held times 2^7
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kItems = 8;
+constexpr int kItems = 4;
+constexpr int kSide = 2;                                   // chains of score products side by side
 
 // What this run does of a row block: units lo .. hi - 1 of its n_units.
 struct __align__(16) Item {
@@ -60,12 +63,11 @@ struct __align__(16) Item {
 
 struct __align__(128) Shared {
     uint8_t ring[kRing][kSlotBytes];
-    float4 part[2][4][4][32];                              // per group: partial scores by warp, eight rows, lane
-    float o[4][16][32][4];                                 // group 1's O at an item's end: by warp, tile, lane
-    uint16_t p[2][16][40];                                 // per group: probabilities, row by row (padded), see place_of
-    float red[2][4][16];                                   // per group: maxima or sums by warp, row
+    // per group: partial scores by warp, eight rows, lane; at an item's end group 1's O by warp, tile, lane
+    float4 part[2][kWarps][8][32];
+    uint16_t p[2][16][80];                                 // per group: probabilities, row by row (padded), see place_of
+    float red[2][kWarps][16];                              // per group: maxima or sums by warp, row
     float ml[2][16];                                       // group 1's maximum and sum
-    float q_top[2][4][16];                                 // per group: largest |q| by warp, row
     Item items[kItems];
     uint64_t full[kRing], empty[kRing];
     uint64_t item_full[kItems], item_empty[kItems];
@@ -188,7 +190,7 @@ __device__ void produce(const PagedParams& p, Shared& sh, int lane) {
                     if (lane == 0) {
                         // eight rows a bit
                         uint32_t v = 0;
-                        for (int k = 0; k < 4; ++k) v |= (here >> (8 * k / box) & 1) << k;
+                        for (int k = 0; k < 8; ++k) v |= (here >> (8 * k / box) & 1) << k;
                         sh.valid[ring] = v;
                         mbar_arrive_expect_tx(&sh.full[ring], __popc(here) * box * MLA_Q4_ROW);
                     }
@@ -238,39 +240,34 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 __device__ __forceinline__ uint32_t clean_nan(uint32_t v) {
     return v & __heq2_mask(*reinterpret_cast<__half2*>(&v), *reinterpret_cast<__half2*>(&v));
 }
-__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
-    return v;
+// (Not volatile: with two warps per scheduler the order of loads, conversions and products counts.)
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    return v;
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint2 lds_v2(uint32_t addr) {
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
-    return v;
-}
+
 __device__ __forceinline__ int row_int(long long t) { return static_cast<int>(min(max(t, 0ll), 0x7fffffffll)); }
 
-// Row of a slot's eight that column n of a score tile stands for.
-__device__ __forceinline__ int row_of_column(int n) { return (n & 4) | (n & 1) << 1 | (n >> 1 & 1); }
 // Place in a row of P of slot row t: the four of 16 rows that a lane's fragment wants lie together.
-__device__ __forceinline__ int place_of(int t) { return (t & 16) | (t & 3) << 2 | (t >> 2 & 3); }
+__device__ __forceinline__ int place_of(int t) { return (t & 48) | (t & 3) << 2 | (t >> 2 & 3); }
 
 struct Fragments {
-    uint32_t q[8][4];                                      // f16, by k-step
+    uint32_t q[4][4];                                      // f16, by k-step
     uint32_t rope[4];                                      // bf16
 };
 
-// This lane's query values: rows g and g + 8 of the block, features 128 w + 32 j .. + 31, key values 16 w + 4 j .. + 3;
-// returns the rows' exponents.
+// This lane's query values: rows g and g + 8 of the block, features 64 w + 16 j .. + 15, key values 16 (w mod 4) + 4 j .. + 3,
+// and what the rows were divided by.
 __device__ __forceinline__ void load_queries(const PagedParams& p, Shared& sh, int group, int w, int lane, long long row0, int live,
                                              Fragments& f, float (&factor)[2]) {
     const int g = lane >> 2, j = lane & 3;
-    uint4 x[2][4];
+    uint4 x[2][2];
     uint2 y[2];
     const float inv_kv = 1.f / p.kv_scale;                 // a power of two
 #pragma unroll
@@ -278,15 +275,15 @@ __device__ __forceinline__ void load_queries(const PagedParams& p, Shared& sh, i
         const uint16_t* src = p.q + (row0 + g + 8 * h) * kDRow;
         const bool there = g + 8 * h < live;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            x[h][k] = there ? reinterpret_cast<const uint4*>(src + 128 * w + 32 * j)[k] : make_uint4(0, 0, 0, 0);
-        y[h] = there ? *reinterpret_cast<const uint2*>(src + kDLatent + 16 * w + 4 * j) : make_uint2(0, 0);
+        for (int k = 0; k < 2; ++k)
+            x[h][k] = there ? reinterpret_cast<const uint4*>(src + 64 * w + 16 * j)[k] : make_uint4(0, 0, 0, 0);
+        y[h] = there ? *reinterpret_cast<const uint2*>(src + kDLatent + 16 * (w & 3) + 4 * j) : make_uint2(0, 0);
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         float top = 0.f, rope = 0.f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 2; ++k) {
             const uint32_t v[4] = {x[h][k].x, x[h][k].y, x[h][k].z, x[h][k].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -299,7 +296,7 @@ __device__ __forceinline__ void load_queries(const PagedParams& p, Shared& sh, i
         top = fmaxf(top, rope * inv_kv);
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        if (j == 0) sh.q_top[group][w][g + 8 * h] = top;
+        if (j == 0) sh.red[group][w][g + 8 * h] = top;
     }
     named_barrier_sync(kBarGroup + group, kGroupThreads);
     float scale[2];
@@ -307,16 +304,16 @@ __device__ __forceinline__ void load_queries(const PagedParams& p, Shared& sh, i
     for (int h = 0; h < 2; ++h) {
         float top = 0.f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) top = fmaxf(top, sh.q_top[group][k][g + 8 * h]);
+        for (int k = 0; k < kWarps; ++k) top = fmaxf(top, sh.red[group][k][g + 8 * h]);
         const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127 - 14, -126), 126);
         scale[h] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
         factor[h] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
     }
-    // k-step s: features 32 j + 4 s, + 1 (registers 0, 1) and + 2, + 3 (2, 3); rows g (0, 2) and g + 8 (1, 3)
+    // k-step s: features 16 j + 4 s, + 1 (registers 0, 1) and + 2, + 3 (2, 3); rows g (0, 2) and g + 8 (1, 3)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 2; ++k) {
             const uint32_t v[4] = {x[h][k].x, x[h][k].y, x[h][k].z, x[h][k].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -329,16 +326,15 @@ __device__ __forceinline__ void load_queries(const PagedParams& p, Shared& sh, i
             f.rope[2 * e + h] = pack_bf16x2(__uint_as_float(v[e] << 16) * scale[h] * inv_kv,
                                             __uint_as_float(v[e] & 0xffff0000u) * scale[h] * inv_kv);
     }
-    // (q_top is written again after many barriers of the group)
+    // (`red` is written again after the next barrier of the group)
 }
 
 __device__ void compute(const PagedParams& p, Shared& sh, int group, int w, int lane) {
     const int g = lane >> 2, j = lane & 3;
     const int bar = kBarGroup + group;
     bool bad = false;
-    // this lane's scores: rows g and g + 8, slot rows 8 w + key[0], key[1]
-    const int key[2] = {8 * w + row_of_column(2 * j), 8 * w + row_of_column(2 * j + 1)};
-    const int key_place[2] = {place_of(key[0]), place_of(key[1])};
+    // this lane's scores: rows g and g + 8, slot rows 8 w + 2 j, + 1
+    const int key_place = place_of(8 * w + 2 * j);         // (of the next row four places on)
     int ring = group, turn = 0;
     // A hardware barrier has no time limit, so nobody leaves one alone: a group leaves together (its barriers tell
     // whether one of its waits ran out), and after the run or in the middle of it, it meets the other once more.
@@ -348,62 +344,65 @@ __device__ void compute(const PagedParams& p, Shared& sh, int group, int w, int 
             bad = true;
             break;
         }
-        const Item it = sh.items[item % kItems];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.item_empty[item % kItems]);
+        const Item& it = sh.items[item % kItems];
         if (it.b < 0) break;
         const int live = min(it.n_tok * p.heads - it.rb * kBlockRows, kBlockRows);
         const long long row0 = static_cast<long long>(it.b) * p.tokens * p.heads + it.rb * kBlockRows;
         Fragments f;
         float c2[2];
         load_queries(p, sh, group, w, lane, row0, live, f, c2);
-        int to[2], from[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            c2[h] *= p.scale_log2 * p.kv_scale;
-            const long long own = static_cast<long long>(it.d_pos) + (it.rb * kBlockRows + g + 8 * h) / p.heads;
-            to[h] = g + 8 * h < live ? row_int(own + 1) : 0;
-            from[h] = p.window > 0 ? row_int(own + 1 - p.window) : 0;
-        }
+        c2[0] *= p.scale_log2 * p.kv_scale;
+        c2[1] *= p.scale_log2 * p.kv_scale;
         // slots whose rows every token attends: up to all_to, from all_from on or before sink
         const int all_to = row_int(static_cast<long long>(it.d_pos) + 1);
         const int all_from = p.window > 0 ? row_int(static_cast<long long>(it.d_pos) + it.n_tok - p.window) : 0;
-        float o[16][4];
+        const int units = it.hi, near = it.near, skip = it.skip;
+        float o[8][4];
 #pragma unroll
-        for (int m = 0; m < 16; ++m)
+        for (int m = 0; m < 8; ++m)
 #pragma unroll
             for (int k = 0; k < 4; ++k) o[m][k] = 0.f;
         float m_ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-        for (int unit = it.lo; unit < it.hi; ++unit) {
-            const int t0 = (unit < it.near ? unit : unit + it.skip) * kUnitRows + kSlotRows * group;
+        for (int unit = it.lo; unit < units; ++unit) {
+            const int t0 = (unit < near ? unit : unit + skip) * kUnitRows + kSlotRows * group;
             bad |= !wait(sh, &sh.full[ring], turn & 1);
-            const uint32_t slot = smem_u32(sh.ring[ring]);
+            const uint8_t* slot = sh.ring[ring];
             const uint32_t valid = sh.valid[ring];
-            // ---- partial scores of this warp's features
-            float acc[4][4];
+            // ---- partial scores of this warp's features: chains of products side by side
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t at = slot + (8 * e + row_of_column(g)) * MLA_Q4_ROW;
-                const uint4 raw = ld_shared_v4(at + 64 * w + 16 * j);
-                const uint32_t s = widen_e4m3(static_cast<uint16_t>(lds_u16(at + kQ4Scales + 8 * w + 2 * j)));
-                const uint2 rope = lds_v2(at + kQ4Rope + 32 * w + 8 * j);
-                const uint32_t lo = __byte_perm(s, s, 0x1010), hi = __byte_perm(s, s, 0x3232);
+            for (int e0 = 0; e0 < 8; e0 += kSide) {
+                float acc[kSide][4];
+                uint2 raw[kSide];
+                uint32_t by[kSide];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) acc[e][k] = 0.f;
-                mma_bf16_16816(acc[e], f.rope, rope.x, rope.y);
-                const uint32_t words[4] = {raw.x, raw.y, raw.z, raw.w};
+                for (int e = 0; e < kSide; ++e) {
+                    const uint8_t* at = slot + (8 * (e0 + e) + g) * MLA_Q4_ROW;
+                    raw[e] = *reinterpret_cast<const uint2*>(at + 32 * w + 8 * j);
+                    const uint32_t s = at[kQ4Scales + 4 * w + j];
+                    by[e] = widen_e4m3(static_cast<uint16_t>(s | s << 8));
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t h[4];
-                    widen_e2m1(words[i], h);
-                    const uint32_t by = i < 2 ? lo : hi;
-                    mma_f16_16816(acc[e], f.q[2 * i], mul_f16x2(h[0], by), mul_f16x2(h[1], by));
-                    mma_f16_16816(acc[e], f.q[2 * i + 1], mul_f16x2(h[2], by), mul_f16x2(h[3], by));
+                    for (int k = 0; k < 4; ++k) acc[e][k] = 0.f;
+                    if (w >> 2 == e0 >> 2) {               // (the key values of 32 rows are four warps', of the others the others')
+                        const uint2 rope = *reinterpret_cast<const uint2*>(at + kQ4Rope + 32 * (w & 3) + 8 * j);
+                        mma_bf16(acc[e], f.rope, rope.x, rope.y);
+                    }
                 }
-            }
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                sh.part[group][w][e][lane] = make_float4(acc[e][0], acc[e][1], acc[e][2], acc[e][3]);
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t h[kSide][4];
+#pragma unroll
+                    for (int e = 0; e < kSide; ++e) {
+                        widen_e2m1(i == 0 ? raw[e].x : raw[e].y, h[e]);
+                        mma_f16(acc[e], f.q[2 * i], mul_f16x2(h[e][0], by[e]), mul_f16x2(h[e][1], by[e]));
+                    }
+#pragma unroll
+                    for (int e = 0; e < kSide; ++e)
+                        mma_f16(acc[e], f.q[2 * i + 1], mul_f16x2(h[e][2], by[e]), mul_f16x2(h[e][3], by[e]));
+                }
+#pragma unroll
+                for (int e = 0; e < kSide; ++e)
+                    sh.part[group][w][e0 + e][lane] = make_float4(acc[e][0], acc[e][1], acc[e][2], acc[e][3]);
+            }
             if (named_barrier_or(bar, kGroupThreads, bad)) {
                 bad = true;
                 break;
@@ -411,7 +410,7 @@ __device__ void compute(const PagedParams& p, Shared& sh, int group, int w, int 
             // ---- whole scores of rows 8 w .. + 7
             float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < kWarps; ++k) {
                 const float4 v = sh.part[group][k][w][lane];
                 s[0] += v.x;
                 s[1] += v.y;
@@ -421,9 +420,16 @@ __device__ void compute(const PagedParams& p, Shared& sh, int group, int w, int 
             const bool here = valid >> w & 1;
             if (!here || t0 + kSlotRows > all_to || (t0 < all_from && t0 + kSlotRows > p.sink)) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int t = t0 + key[k & 1], h = k >> 1;
-                    if (!(here && t < to[h] && (t >= from[h] || t < p.sink))) s[k] = -INFINITY;
+                for (int h = 0; h < 2; ++h) {
+                    // the row's token attends rows [from, to) and those before sink
+                    const long long own = static_cast<long long>(it.d_pos) + (it.rb * kBlockRows + g + 8 * h) / p.heads;
+                    const int to = g + 8 * h < live ? row_int(own + 1) : 0;
+                    const int from = p.window > 0 ? row_int(own + 1 - p.window) : 0;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int t = t0 + 8 * w + 2 * j + k;
+                        if (!(here && t < to && (t >= from || t < p.sink))) s[2 * h + k] = -INFINITY;
+                    }
                 }
             }
             float top[2], base[2];
@@ -440,7 +446,7 @@ __device__ void compute(const PagedParams& p, Shared& sh, int group, int w, int 
                 for (int k = 0; k < 4; ++k) {
                     e[k] = ex2_approx(s[k] - base[k >> 1]);
                     const __half v = __float2half_rn(e[k]);
-                    sh.p[group][g + 8 * (k >> 1)][key_place[k & 1]] = *reinterpret_cast<const uint16_t*>(&v);
+                    sh.p[group][g + 8 * (k >> 1)][key_place + 4 * (k & 1)] = *reinterpret_cast<const uint16_t*>(&v);
                 }
             };
             publish();
@@ -456,15 +462,16 @@ __device__ void compute(const PagedParams& p, Shared& sh, int group, int w, int 
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int r = g + 8 * h;
-                    const float t = fmaxf(fmaxf(sh.red[group][0][r], sh.red[group][1][r]),
-                                          fmaxf(sh.red[group][2][r], sh.red[group][3][r]));
+                    float t = sh.red[group][0][r];
+#pragma unroll
+                    for (int k = 1; k < kWarps; ++k) t = fmaxf(t, sh.red[group][k][r]);
                     if (t > m_ref[h] + kRescaleLog2) {
                         const float alpha = m_ref[h] > -INFINITY ? ex2_approx(m_ref[h] - t) : 1.f;
                         m_ref[h] = t;
                         base[h] = t - kProbLog2;
                         l[h] *= alpha;
 #pragma unroll
-                        for (int m = 0; m < 16; ++m) {
+                        for (int m = 0; m < 8; ++m) {
                             o[m][2 * h] *= alpha;
                             o[m][2 * h + 1] *= alpha;
                         }
@@ -475,41 +482,31 @@ __device__ void compute(const PagedParams& p, Shared& sh, int group, int w, int 
             }
             l[0] += e[0] + e[1];
             l[1] += e[2] + e[3];
-            // ---- P V, this warp's features
+            // ---- P V, this warp's features, 16 rows at a time
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint32_t a[4];
-                const uint2 a0 = lds_v2(smem_u32(&sh.p[group][g][16 * half + 4 * j]));
-                const uint2 a1 = lds_v2(smem_u32(&sh.p[group][g + 8][16 * half + 4 * j]));
-                a[0] = a0.x;
-                a[1] = a1.x;
-                a[2] = a0.y;
-                a[3] = a1.y;
-                const uint32_t at = slot + (16 * half + j) * MLA_Q4_ROW;
-                uint2 v[4];
-                uint32_t sc[4];
+            for (int step = 0; step < 4; ++step) {
+                const uint2 a0 = *reinterpret_cast<const uint2*>(&sh.p[group][g][16 * step + 4 * j]);
+                const uint2 a1 = *reinterpret_cast<const uint2*>(&sh.p[group][g + 8][16 * step + 4 * j]);
+                const uint32_t a[4] = {a0.x, a1.x, a0.y, a1.y};
+                uint32_t x[4], by[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    v[i] = lds_v2(at + 4 * i * MLA_Q4_ROW + 64 * w + 8 * g);
-                    sc[i] = lds_u8(at + 4 * i * MLA_Q4_ROW + kQ4Scales + 8 * w + g);
+                    const uint8_t* at = slot + (16 * step + 4 * i + j) * MLA_Q4_ROW;
+                    x[i] = *reinterpret_cast<const uint32_t*>(at + 32 * w + 4 * g);
+                    by[i] = at[kQ4Scales + 4 * w + (g >> 1)];
                 }
-                const uint32_t s01 = clean_nan(widen_e4m3(static_cast<uint16_t>(sc[0] | sc[1] << 8)));
-                const uint32_t s23 = clean_nan(widen_e4m3(static_cast<uint16_t>(sc[2] | sc[3] << 8)));
+                const uint32_t s01 = clean_nan(widen_e4m3(static_cast<uint16_t>(by[0] | by[1] << 8)));
+                const uint32_t s23 = clean_nan(widen_e4m3(static_cast<uint16_t>(by[2] | by[3] << 8)));
+                constexpr uint32_t kLow = 0x0f0f0f0fu;
+                uint32_t even01[4], odd01[4], even23[4], odd23[4];
+                widen_e2m1((x[0] & kLow) | (x[1] << 4 & ~kLow), even01);
+                widen_e2m1((x[2] & kLow) | (x[3] << 4 & ~kLow), even23);
+                widen_e2m1((x[0] >> 4 & kLow) | (x[1] & ~kLow), odd01);
+                widen_e2m1((x[2] >> 4 & kLow) | (x[3] & ~kLow), odd23);
 #pragma unroll
-                for (int word = 0; word < 2; ++word) {
-                    const uint32_t x0 = word ? v[0].y : v[0].x, x1 = word ? v[1].y : v[1].x;
-                    const uint32_t x2 = word ? v[2].y : v[2].x, x3 = word ? v[3].y : v[3].x;
-                    constexpr uint32_t kLow = 0x0f0f0f0fu;
-                    uint32_t even01[4], odd01[4], even23[4], odd23[4];
-                    widen_e2m1((x0 & kLow) | (x1 << 4 & ~kLow), even01);
-                    widen_e2m1((x0 >> 4 & kLow) | (x1 & ~kLow), odd01);
-                    widen_e2m1((x2 & kLow) | (x3 << 4 & ~kLow), even23);
-                    widen_e2m1((x2 >> 4 & kLow) | (x3 & ~kLow), odd23);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        mma_f16_16816(o[8 * word + 2 * i], a, mul_f16x2(even01[i], s01), mul_f16x2(even23[i], s23));
-                        mma_f16_16816(o[8 * word + 2 * i + 1], a, mul_f16x2(odd01[i], s01), mul_f16x2(odd23[i], s23));
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    mma_f16(o[2 * i], a, mul_f16x2(even01[i], s01), mul_f16x2(even23[i], s23));
+                    mma_f16(o[2 * i + 1], a, mul_f16x2(odd01[i], s01), mul_f16x2(odd23[i], s23));
                 }
             }
             __syncwarp();
@@ -532,12 +529,13 @@ __device__ void compute(const PagedParams& p, Shared& sh, int group, int w, int 
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int r = g + 8 * h;
-            l[h] = (sh.red[group][0][r] + sh.red[group][1][r]) + (sh.red[group][2][r] + sh.red[group][3][r]);
+            l[h] = 0.f;
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) l[h] += sh.red[group][k][r];
         }
         if (group == 1) {
 #pragma unroll
-            for (int m = 0; m < 16; ++m)
-                *reinterpret_cast<float4*>(sh.o[w][m][lane]) = make_float4(o[m][0], o[m][1], o[m][2], o[m][3]);
+            for (int m = 0; m < 8; ++m) sh.part[1][w][m][lane] = make_float4(o[m][0], o[m][1], o[m][2], o[m][3]);
             if (w == 0 && j == 0) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -577,45 +575,41 @@ __device__ void compute(const PagedParams& p, Shared& sh, int group, int w, int 
             if (w == 0 && lane == 0 && !whole && it.lo == 0)
                 p.merge[blockIdx.x] = TreeMerge{it.b, it.rb, live | (item == 0 ? 0 : 1) << 16, it.runs};
 #pragma unroll
-            for (int m = 0; m < 16; ++m) {
-                const float4 v = *reinterpret_cast<const float4*>(sh.o[w][m][lane]);
+            for (int m = 0; m < 8; ++m) {
+                const float4 v = sh.part[1][w][m][lane];
                 o[m][0] = o[m][0] * by0[0] + v.x * by1[0];
                 o[m][1] = o[m][1] * by0[0] + v.y * by1[0];
                 o[m][2] = o[m][2] * by0[1] + v.z * by1[1];
                 o[m][3] = o[m][3] * by0[1] + v.w * by1[1];
             }
-            // rows g, g + 8; features 128 w + 32 j + m (register 0) and + 16 (register 1)
+            // rows g, g + 8; features 64 w + 16 j + m (register 0) and + 8 (register 1)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int r = g + 8 * h;
                 if (r >= live) continue;
-                if (!whole) {
-                    float4* piece = reinterpret_cast<float4*>(p.part) +
-                                    (static_cast<long long>(slot) * (kDLatent / 4) + 32 * w + 8 * j) * 32 + r;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int m = 4 * (k & 3), c = 2 * h + (k >> 2);
-                        piece[32 * k] = make_float4(o[m][c], o[m + 1][c], o[m + 2][c], o[m + 3][c]);
-                    }
-                } else if (p.a.out_fp32) {
-                    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.a.out) + (row0 + r) * kDLatent + 128 * w + 32 * j);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int m = 4 * (k & 3), c = 2 * h + (k >> 2);
-                        dst[k] = make_float4(o[m][c], o[m + 1][c], o[m + 2][c], o[m + 3][c]);
-                    }
-                } else {
-                    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.a.out) + (row0 + r) * kDLatent + 128 * w + 32 * j);
+                if (!whole || p.a.out_fp32) {
+                    float4* dst = whole ? reinterpret_cast<float4*>(static_cast<float*>(p.a.out) + (row0 + r) * kDLatent + 64 * w + 16 * j)
+                                        : reinterpret_cast<float4*>(p.part) +
+                                              (static_cast<long long>(slot) * (kDLatent / 4) + 16 * w + 4 * j) * 32 + r;
+                    const int step = whole ? 1 : 32;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const int m = 8 * (k & 1), c = 2 * h + (k >> 1);
-                        dst[k] = make_uint4(pack_bf16x2(o[m][c], o[m + 1][c]), pack_bf16x2(o[m + 2][c], o[m + 3][c]),
-                                            pack_bf16x2(o[m + 4][c], o[m + 5][c]), pack_bf16x2(o[m + 6][c], o[m + 7][c]));
+                        const int m = 4 * (k & 1), c = 2 * h + (k >> 1);
+                        dst[step * k] = make_float4(o[m][c], o[m + 1][c], o[m + 2][c], o[m + 3][c]);
+                    }
+                } else {
+                    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.a.out) + (row0 + r) * kDLatent + 64 * w + 16 * j);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int c = 2 * h + k;
+                        dst[k] = make_uint4(pack_bf16x2(o[0][c], o[1][c]), pack_bf16x2(o[2][c], o[3][c]),
+                                            pack_bf16x2(o[4][c], o[5][c]), pack_bf16x2(o[6][c], o[7][c]));
                     }
                 }
             }
         }
         named_barrier_sync(kBarBoth, kComputeThreads);     // group 1's O has been read
+        if (lane == 0) mbar_arrive(&sh.item_empty[item % kItems]);
     }
     named_barrier_or(kBarBoth, kComputeThreads, true);
     if (bad && lane == 0) raise(p, sh);
@@ -628,11 +622,11 @@ __global__ void __launch_bounds__(kThreads, 1) mla_paged_decode_kernel(const __g
     if (tid == 0) {
         for (int i = 0; i < kRing; ++i) {
             mbar_init(&sh.full[i], 1);
-            mbar_init(&sh.empty[i], 4);
+            mbar_init(&sh.empty[i], kWarps);
         }
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&sh.item_full[i], 1);
-            mbar_init(&sh.item_empty[i], 8);
+            mbar_init(&sh.item_empty[i], 2 * kWarps);
         }
         mbar_init(&sh.stall_bar, 1);
         sh.abort_flag = 0;
@@ -665,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_paged_decode_kernel(const __g
             for (int i = lane; i < rows * per; i += 32) o[i] = make_uint4(0, 0, 0, 0);
         }
     } else {
-        compute(p, sh, warp >> 2, warp & 3, lane);
+        compute(p, sh, warp / kWarps, warp % kWarps, lane);
     }
     __syncthreads();
     if (*static_cast<volatile int*>(&sh.abort_flag)) {
