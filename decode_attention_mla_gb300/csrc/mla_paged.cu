@@ -84,12 +84,12 @@ int prepare(cudaStream_t st, bool may_capture) {
     return MLA_OK;
 }
 
-// Few query rows: on warp-level MMAs, an SM's run each.  (It counts units of 128 rows in an int.)
+// Few query rows: on warp-level MMAs, an SM's run each.  (It counts units of 64 rows in an int.)
 constexpr int kFewRows = 32;
 bool few_rows(const mla_paged_plan_t* pl, const mla_paged_args* a) {
     const long long rows = static_cast<long long>(pl->shape.tokens) * pl->shape.heads;
     const long long blocks = (rows + kDecodeBlockRows - 1) / kDecodeBlockRows;
-    const long long units = static_cast<long long>(a->cache.columns) * a->cache.page_rows / 128 + 2;
+    const long long units = static_cast<long long>(a->cache.columns) * a->cache.page_rows / 64 + 2;
     return rows <= kFewRows && pl->shape.batch * blocks * units < (1ll << 30);
 }
 

@@ -4,34 +4,34 @@
 // Sixteen query rows (token * heads + head) are one MMA tile, and rows need be widened for nobody
 // else, so nothing is gained by operands in shared memory: the tcgen05 kernel (mla_paged_attend.cu) writes
 // and reads them there, 390 KB per 128 rows of a pair, whatever the number of query rows.  Here rows stay as they
-// are in shared memory (416 bytes), and each warp takes its bytes from there twice, into the fragments
-// of Q K^T and of P V.
+// are in shared memory (416 bytes), and are widened on their way from there to the MMAs.
 //
-// A group of eight warps shares the 64 rows of a slot.  Warp w has features 64 w .. + 63 (and 16 of the 64 key
-// values of half of the rows): its scores are partial sums, which the warps exchange through shared memory; warp w then
-// has the whole scores of rows 8 w .. + 7, and hands their probabilities to the others; and its part of O, 16 x 64
-// fp32, stays in registers.  Two groups take alternate slots, each with a running maximum and sum of its own, and are
-// joined at an item's end.  (Groups of four warps with 128 features: 204 us where eight take XX for 32 requests of 16
-// heads: two warps per scheduler leave it idle two cycles of three.)
+// A group of four warps shares the 32 rows of a slot.  Warp w has features 128 w .. + 127 (and 16 of the 64 key
+// values): it widens them once, into the fragments of Q K^T and to shared memory of its own, from where ldmatrix
+// brings them back transposed for P V.  Its scores are partial sums, which the warps exchange through shared memory;
+// warp w then has the whole scores of rows 8 w .. + 7, and hands their probabilities to the others; and its part of O,
+// 16 x 128 fp32, stays in registers.  Two groups take slots in turn, each with a running maximum and sum of its own,
+// and are joined at an item's end.  (Measured on 32 requests of 16 heads, 168 us now: values widened a second time from the
+// bytes for P V, 186; two chains of products beside each other in the place of four, 183; transposed by movmatrix instead of
+// through shared memory, 180; three groups, which have 144 registers a thread, 187.)
 //
 // Orders.  The contraction over features may go in any order: lane 4 g + j has, of row g of eight, features 16 j ..
-// 16 j + 15 (a block: eight bytes of codes), four to a k-step.  Rows of a slot lie 416 bytes apart, eight banks on, so four
-// rows' eight banks each are all 32.  For P V lane 4 g + j has features 8 g .. 8 g + 7 (four bytes) of rows j, 4 + j, 8 + j,
-// 12 + j of sixteen: again all banks.  Two rows' codes are brought together in bytes (low and high half), so one
-// conversion gives the pair of values that a fragment wants.
+// 16 j + 15 of 64 (a block: eight bytes of codes), four to a k-step.  Rows of a slot lie 416 bytes apart, eight banks on, so
+// four rows' eight banks each are all 32.
 //
 // A code times its scale is exact in f16 (six bits, 2^-10 .. 2688).  Queries are f16 times a power of two per row, probabilities
 // f16 times 2^7, key values and their queries bf16, as in mla_paged_attend.cu; sums are fp32.  Codes are finite whatever
 // the bytes, and a scale's NaN becomes 0 in P V (in Q K^T it stays: the row's scores are NaN); so rows that nobody
 // attends need no clearing: their scores are masked, their probabilities 0.
 //
-// Work split: units of 128 rows (a slot per group) of all requests' blocks of sixteen query rows, one equal run per SM; pieces and
+// Work split: units of 64 rows (a slot per group) of all requests' blocks of sixteen query rows, one equal run per SM; pieces and
 // their merge as in mla_tree_attend.cu.
 //
-// Bound: 16 MMAs and about 66 other instructions of a warp per row and SM, 17 cycles each way, beside 19 for its bytes from
-// HBM.
+// Bound: 30 cycles of shared memory per row and SM (16 of them the widened values' way there and back, 4 the queries'
+// fragments), beside 17 of MMAs and 19 for its bytes from HBM; what is measured is 42, the rest being the chain from a
+// slot's bytes to its P V, which two warps a scheduler hide in part.  Bytes alone, nothing computed: 87 us of those 168.
 //
-// Warps: 0-7 and 8-15 the groups, 16 bulk copies and the run's items, 17 empty requests.
+// Warps: 0-3 and 4-7 the groups, 8 bulk copies and the run's items, 9 empty requests.
 #include <cmath>
 
 #include "mla_paged.cuh"
@@ -39,20 +39,20 @@
 namespace mla {
 namespace {
 
-constexpr int kUnitRows = 128, kSlotRows = 64;
+constexpr int kGroups = 2;
+constexpr int kSlotRows = 32, kUnitRows = kGroups * kSlotRows;
 constexpr int kSlotBytes = kSlotRows * MLA_Q4_ROW;
-constexpr int kRing = 6;
-constexpr int kWarps = 8;                                  // of a group
-constexpr int kGroupThreads = 32 * kWarps, kComputeThreads = 2 * kGroupThreads;
-constexpr int kProducerWarp = 2 * kWarps, kEmptyWarp = kProducerWarp + 1;
+constexpr int kRing = 4 * kGroups;
+constexpr int kWarps = 4;                                  // of a group
+constexpr int kGroupThreads = 32 * kWarps, kComputeThreads = kGroups * kGroupThreads;
+constexpr int kProducerWarp = kGroups * kWarps, kEmptyWarp = kProducerWarp + 1;
 constexpr int kThreads = 32 * (kEmptyWarp + 1);
-constexpr int kBarGroup = 1, kBarBoth = 3;                 // hardware barriers: of each group, of both
+constexpr int kBarAll = 1, kBarGroup = 2;                  // hardware barriers: of all groups, of each
 constexpr int kBlockRows = kDecodeBlockRows;
 constexpr float kRescaleLog2 = 8.0f;                       // move the reference when a max grows past 2^8
 constexpr float kProbLog2 = 7.0f;                          // P is held times 2^7
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kItems = 4;
-constexpr int kSide = 2;                                   // chains of score products side by side
 
 // What this run does of a row block: units lo .. hi - 1 of its n_units.
 struct __align__(16) Item {
@@ -63,11 +63,15 @@ struct __align__(16) Item {
 
 struct __align__(128) Shared {
     uint8_t ring[kRing][kSlotBytes];
-    // per group: partial scores by warp, eight rows, lane; at an item's end group 1's O by warp, tile, lane
-    float4 part[2][kWarps][8][32];
-    uint16_t p[2][16][80];                                 // per group: probabilities, row by row (padded), see place_of
-    float red[2][kWarps][16];                              // per group: maxima or sums by warp, row
-    float ml[2][16];                                       // group 1's maximum and sum
+    float4 part[kGroups][kWarps][4][32];                         // per group: partial scores by warp, eight rows, lane
+    // per group and warp: a slot's values of the warp's features in f16, 256 bytes a row, 16-byte unit u of row r at u ^
+    // (r mod 8); at an item's end the O of all groups but the first
+    float4 v[kGroups][kWarps][kSlotRows * 16];
+    uint4 q[9][kWarps][32];                                // query fragments by k-step (the last: key values), warp, lane
+    uint16_t p[kGroups][16][40];                                 // per group: probabilities, row by row (padded)
+    float red[kGroups][kWarps][16];                        // per group: maxima or sums by warp, row
+    float top[kGroups][16], sum[kGroups][16];              // ... at an item's end
+    float factor[16];                                      // what the query rows were divided by
     Item items[kItems];
     uint64_t full[kRing], empty[kRing];
     uint64_t item_full[kItems], item_empty[kItems];
@@ -133,7 +137,7 @@ __device__ __forceinline__ void raise(const PagedParams& p, Shared& sh) {
 
 // ============================== producer ==================================
 // One warp: the run's items, and the bytes of its slots.  A lane has a box (the rows of a page that lie in a
-// slot) of one of a unit's two slots.
+// slot) of one of a unit's slots.
 __device__ void produce(const PagedParams& p, Shared& sh, int lane) {
     const int total = count_units(p, lane);
     const int per = (total + p.clusters - 1) / p.clusters, cta = blockIdx.x;
@@ -141,8 +145,8 @@ __device__ void produce(const PagedParams& p, Shared& sh, int lane) {
     const int u1 = min(u0 + per, total);
     const uint64_t policy = l2_policy_evict_normal();
     const int box = min(1 << p.cache.row_shift, kSlotRows), boxes = kSlotRows / box;   // of a slot
-    const bool mine = lane < 2 * boxes;
-    const int row = (lane & (boxes - 1)) * box + (lane >= boxes ? kSlotRows : 0);     // of the unit
+    const bool mine = lane < kGroups * boxes;
+    const int row = lane * box;                            // of the unit
     if (u0 < u1) {
         Start s = find_start(p, u0, lane);
         TreeRequest r = load_paged_request<kUnitRows>(p, s.b);
@@ -181,7 +185,7 @@ __device__ void produce(const PagedParams& p, Shared& sh, int lane) {
                 if (at + 1 < hi) page = place(at + 1, t);
                 const uint32_t have = __ballot_sync(0xffffffffu, now >= 0);
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
+                for (int q = 0; q < kGroups; ++q) {
                     if (turn > 0 && !wait(sh, &sh.empty[ring], (turn - 1) & 1)) {
                         ok = false;
                         break;
@@ -190,12 +194,12 @@ __device__ void produce(const PagedParams& p, Shared& sh, int lane) {
                     if (lane == 0) {
                         // eight rows a bit
                         uint32_t v = 0;
-                        for (int k = 0; k < 8; ++k) v |= (here >> (8 * k / box) & 1) << k;
+                        for (int k = 0; k < 4; ++k) v |= (here >> (8 * k / box) & 1) << k;
                         sh.valid[ring] = v;
                         mbar_arrive_expect_tx(&sh.full[ring], __popc(here) * box * MLA_Q4_ROW);
                     }
                     __syncwarp();
-                    if (mine && (lane >= boxes) == (q == 1) && src)
+                    if (lane >= q * boxes && lane < (q + 1) * boxes && src)
                         bulk_copy_g2s(sh.ring[ring] + (row & (kSlotRows - 1)) * MLA_Q4_ROW, src, box * MLA_Q4_ROW,
                                       &sh.full[ring], policy);
                     if (++ring == kRing) {
@@ -254,20 +258,16 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
 
 __device__ __forceinline__ int row_int(long long t) { return static_cast<int>(min(max(t, 0ll), 0x7fffffffll)); }
 
-// Place in a row of P of slot row t: the four of 16 rows that a lane's fragment wants lie together.
-__device__ __forceinline__ int place_of(int t) { return (t & 48) | (t & 3) << 2 | (t >> 2 & 3); }
+// (Orders no other access: what it writes is read behind the group's next barrier.)
+__device__ __forceinline__ void store_values(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d));
+}
 
-struct Fragments {
-    uint32_t q[4][4];                                      // f16, by k-step
-    uint32_t rope[4];                                      // bf16
-};
-
-// This lane's query values: rows g and g + 8 of the block, features 64 w + 16 j .. + 15, key values 16 (w mod 4) + 4 j .. + 3,
-// and what the rows were divided by.
-__device__ __forceinline__ void load_queries(const PagedParams& p, Shared& sh, int group, int w, int lane, long long row0, int live,
-                                             Fragments& f, float (&factor)[2]) {
+// The first group: the block's query rows as fragments.  A lane has rows g and g + 8, features 128 w + 64 k + 16 j .. + 15
+// (k = 0, 1), key values 16 w + 4 j .. + 3.
+__device__ __forceinline__ void load_queries(const PagedParams& p, Shared& sh, int w, int lane, long long row0, int live) {
     const int g = lane >> 2, j = lane & 3;
-    uint4 x[2][2];
+    uint4 x[2][4];
     uint2 y[2];
     const float inv_kv = 1.f / p.kv_scale;                 // a power of two
 #pragma unroll
@@ -275,15 +275,15 @@ __device__ __forceinline__ void load_queries(const PagedParams& p, Shared& sh, i
         const uint16_t* src = p.q + (row0 + g + 8 * h) * kDRow;
         const bool there = g + 8 * h < live;
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-            x[h][k] = there ? reinterpret_cast<const uint4*>(src + 64 * w + 16 * j)[k] : make_uint4(0, 0, 0, 0);
-        y[h] = there ? *reinterpret_cast<const uint2*>(src + kDLatent + 16 * (w & 3) + 4 * j) : make_uint2(0, 0);
+        for (int k = 0; k < 4; ++k)
+            x[h][k] = there ? reinterpret_cast<const uint4*>(src + 128 * w + 64 * (k >> 1) + 16 * j)[k & 1] : make_uint4(0, 0, 0, 0);
+        y[h] = there ? *reinterpret_cast<const uint2*>(src + kDLatent + 16 * w + 4 * j) : make_uint2(0, 0);
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         float top = 0.f, rope = 0.f;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < 4; ++k) {
             const uint32_t v[4] = {x[h][k].x, x[h][k].y, x[h][k].z, x[h][k].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -296,116 +296,125 @@ __device__ __forceinline__ void load_queries(const PagedParams& p, Shared& sh, i
         top = fmaxf(top, rope * inv_kv);
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        if (j == 0) sh.red[group][w][g + 8 * h] = top;
+        if (j == 0) sh.red[0][w][g + 8 * h] = top;
     }
-    named_barrier_sync(kBarGroup + group, kGroupThreads);
+    named_barrier_sync(kBarGroup, kGroupThreads);
     float scale[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         float top = 0.f;
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k) top = fmaxf(top, sh.red[group][k][g + 8 * h]);
+        for (int k = 0; k < kWarps; ++k) top = fmaxf(top, sh.red[0][k][g + 8 * h]);
         const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127 - 14, -126), 126);
         scale[h] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        factor[h] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        if (w == 0 && j == 0) sh.factor[g + 8 * h] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
     }
-    // k-step s: features 16 j + 4 s, + 1 (registers 0, 1) and + 2, + 3 (2, 3); rows g (0, 2) and g + 8 (1, 3)
+    // k-step 2 k + s: features 64 (k / 2) + 16 j + 8 (k mod 2) + 4 s, + 1 (registers 0, 1) and + 2, + 3 (2, 3); rows g (0, 2)
+    // and g + 8 (1, 3)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t a[4] = {x[0][k].x, x[0][k].y, x[0][k].z, x[0][k].w}, b[4] = {x[1][k].x, x[1][k].y, x[1][k].z, x[1][k].w};
+        auto f16 = [](uint32_t v, float by) {
+            return pack_f16x2(__uint_as_float(v << 16) * by, __uint_as_float(v & 0xffff0000u) * by);
+        };
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const uint32_t v[4] = {x[h][k].x, x[h][k].y, x[h][k].z, x[h][k].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                f.q[2 * k + (e >> 1)][2 * (e & 1) + h] =
-                    pack_f16x2(__uint_as_float(v[e] << 16) * scale[h], __uint_as_float(v[e] & 0xffff0000u) * scale[h]);
-        }
-        const uint32_t v[2] = {y[h].x, y[h].y};
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-            f.rope[2 * e + h] = pack_bf16x2(__uint_as_float(v[e] << 16) * scale[h] * inv_kv,
-                                            __uint_as_float(v[e] & 0xffff0000u) * scale[h] * inv_kv);
+        for (int s = 0; s < 2; ++s)
+            sh.q[2 * k + s][w][lane] = make_uint4(f16(a[2 * s], scale[0]), f16(b[2 * s], scale[1]), f16(a[2 * s + 1], scale[0]),
+                                                  f16(b[2 * s + 1], scale[1]));
     }
-    // (`red` is written again after the next barrier of the group)
+    auto bf16 = [&](uint32_t v, float by) {
+        return pack_bf16x2(__uint_as_float(v << 16) * by * inv_kv, __uint_as_float(v & 0xffff0000u) * by * inv_kv);
+    };
+    sh.q[8][w][lane] = make_uint4(bf16(y[0].x, scale[0]), bf16(y[1].x, scale[1]), bf16(y[0].y, scale[0]), bf16(y[1].y, scale[1]));
 }
 
 __device__ void compute(const PagedParams& p, Shared& sh, int group, int w, int lane) {
     const int g = lane >> 2, j = lane & 3;
     const int bar = kBarGroup + group;
-    bool bad = false;
-    // this lane's scores: rows g and g + 8, slot rows 8 w + 2 j, + 1
-    const int key_place = place_of(8 * w + 2 * j);         // (of the next row four places on)
+    // addresses: values written (unit 2 j of row g), values read (transposed), P read
+    const uint32_t values = smem_u32(sh.v[group][w]);
+    const uint32_t v_write = values + g * 256, v_read = values + (8 * (lane >> 3 & 1) + (lane & 7)) * 256;
+    const uint32_t p_read = smem_u32(&sh.p[group][(lane & 7) + 8 * (lane >> 3 & 1)][8 * (lane >> 4)]);
     int ring = group, turn = 0;
-    // A hardware barrier has no time limit, so nobody leaves one alone: a group leaves together (its barriers tell
-    // whether one of its waits ran out), and after the run or in the middle of it, it meets the other once more.
+    // A hardware barrier has no time limit, so nobody leaves one alone: all leave together at an item's beginning; a group
+    // whose wait runs out in the middle meets the others at the item's end, and all leave there.
     for (int item = 0;; ++item) {
-        bad = !wait(sh, &sh.item_full[item % kItems], (item / kItems) & 1);
-        if (named_barrier_or(bar, kGroupThreads, bad)) {
-            bad = true;
-            break;
+        const bool there = wait(sh, &sh.item_full[item % kItems], (item / kItems) & 1);
+        if (named_barrier_or(kBarAll, kComputeThreads, !there)) {
+            if (lane == 0) raise(p, sh);
+            return;
         }
         const Item& it = sh.items[item % kItems];
-        if (it.b < 0) break;
+        if (it.b < 0) return;
         const int live = min(it.n_tok * p.heads - it.rb * kBlockRows, kBlockRows);
         const long long row0 = static_cast<long long>(it.b) * p.tokens * p.heads + it.rb * kBlockRows;
-        Fragments f;
-        float c2[2];
-        load_queries(p, sh, group, w, lane, row0, live, f, c2);
-        c2[0] *= p.scale_log2 * p.kv_scale;
-        c2[1] *= p.scale_log2 * p.kv_scale;
+        if (group == 0) load_queries(p, sh, w, lane, row0, live);
+        named_barrier_sync(kBarAll, kComputeThreads);
+        const float c2[2] = {sh.factor[g] * p.scale_log2 * p.kv_scale, sh.factor[g + 8] * p.scale_log2 * p.kv_scale};
         // slots whose rows every token attends: up to all_to, from all_from on or before sink
         const int all_to = row_int(static_cast<long long>(it.d_pos) + 1);
         const int all_from = p.window > 0 ? row_int(static_cast<long long>(it.d_pos) + it.n_tok - p.window) : 0;
         const int units = it.hi, near = it.near, skip = it.skip;
-        float o[8][4];
+        float o[16][4];
 #pragma unroll
-        for (int m = 0; m < 8; ++m)
+        for (int m = 0; m < 16; ++m)
 #pragma unroll
             for (int k = 0; k < 4; ++k) o[m][k] = 0.f;
         float m_ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
         for (int unit = it.lo; unit < units; ++unit) {
             const int t0 = (unit < near ? unit : unit + skip) * kUnitRows + kSlotRows * group;
-            bad |= !wait(sh, &sh.full[ring], turn & 1);
+            const bool bad = !wait(sh, &sh.full[ring], turn & 1);
             const uint8_t* slot = sh.ring[ring];
             const uint32_t valid = sh.valid[ring];
-            // ---- partial scores of this warp's features: chains of products side by side
+            // ---- the slot's values of this warp's features, widened once: into the fragments of its partial scores, and
+            // to shared memory for P V.  Eight rows of each of four chains of products side by side
+            float acc[4][4];
+            const uint8_t* at = slot + g * MLA_Q4_ROW;
 #pragma unroll
-            for (int e0 = 0; e0 < 8; e0 += kSide) {
-                float acc[kSide][4];
-                uint2 raw[kSide];
-                uint32_t by[kSide];
+            for (int e = 0; e < 4; ++e) {
+                const uint2 rope = *reinterpret_cast<const uint2*>(at + 8 * e * MLA_Q4_ROW + kQ4Rope + 32 * w + 8 * j);
+                const uint4 q = sh.q[8][w][lane];
 #pragma unroll
-                for (int e = 0; e < kSide; ++e) {
-                    const uint8_t* at = slot + (8 * (e0 + e) + g) * MLA_Q4_ROW;
-                    raw[e] = *reinterpret_cast<const uint2*>(at + 32 * w + 8 * j);
-                    const uint32_t s = at[kQ4Scales + 4 * w + j];
+                for (int k = 0; k < 4; ++k) acc[e][k] = 0.f;
+                mma_bf16(acc[e], {q.x, q.y, q.z, q.w}, rope.x, rope.y);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint2 raw[4];
+                uint32_t by[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    raw[e] = *reinterpret_cast<const uint2*>(at + 8 * e * MLA_Q4_ROW + 64 * w + 32 * k + 8 * j);
+                    const uint32_t s = at[8 * e * MLA_Q4_ROW + kQ4Scales + 8 * w + 4 * k + j];
                     by[e] = widen_e4m3(static_cast<uint16_t>(s | s << 8));
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) acc[e][k] = 0.f;
-                    if (w >> 2 == e0 >> 2) {               // (the key values of 32 rows are four warps', of the others the others')
-                        const uint2 rope = *reinterpret_cast<const uint2*>(at + kQ4Rope + 32 * (w & 3) + 8 * j);
-                        mma_bf16(acc[e], f.rope, rope.x, rope.y);
-                    }
                 }
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    uint32_t h[kSide][4];
+                    uint32_t h[4][4];
+                    const uint4 q0 = sh.q[4 * k + 2 * i][w][lane], q1 = sh.q[4 * k + 2 * i + 1][w][lane];
 #pragma unroll
-                    for (int e = 0; e < kSide; ++e) {
+                    for (int e = 0; e < 4; ++e) {
                         widen_e2m1(i == 0 ? raw[e].x : raw[e].y, h[e]);
-                        mma_f16(acc[e], f.q[2 * i], mul_f16x2(h[e][0], by[e]), mul_f16x2(h[e][1], by[e]));
+                        const uint32_t finite = clean_nan(by[e]);
+                        // (a scale's NaN makes the row's scores NaN, through one of its products, but no value of V)
+                        const uint32_t first = i == 0 ? mul_f16x2(h[e][0], by[e]) : 0u;
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) h[e][n] = mul_f16x2(h[e][n], finite);
+                        mma_f16(acc[e], {q0.x, q0.y, q0.z, q0.w}, i == 0 ? first : h[e][0], h[e][1]);
+                        store_values(v_write + 2048 * e + (((8 * k + 2 * j + i) ^ g) << 4), h[e][0], h[e][1], h[e][2],
+                                     h[e][3]);
                     }
 #pragma unroll
-                    for (int e = 0; e < kSide; ++e)
-                        mma_f16(acc[e], f.q[2 * i + 1], mul_f16x2(h[e][2], by[e]), mul_f16x2(h[e][3], by[e]));
+                    for (int e = 0; e < 4; ++e) mma_f16(acc[e], {q1.x, q1.y, q1.z, q1.w}, h[e][2], h[e][3]);
                 }
-#pragma unroll
-                for (int e = 0; e < kSide; ++e)
-                    sh.part[group][w][e0 + e][lane] = make_float4(acc[e][0], acc[e][1], acc[e][2], acc[e][3]);
             }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                sh.part[group][w][e][lane] = make_float4(acc[e][0], acc[e][1], acc[e][2], acc[e][3]);
             if (named_barrier_or(bar, kGroupThreads, bad)) {
-                bad = true;
-                break;
+                if (lane == 0) raise(p, sh);
+                named_barrier_or(kBarAll, kComputeThreads, true);
+                return;
             }
             // ---- whole scores of rows 8 w .. + 7
             float s[4] = {0.f, 0.f, 0.f, 0.f};
@@ -443,11 +452,10 @@ __device__ void compute(const PagedParams& p, Shared& sh, int group, int w, int 
             float e[4];
             auto publish = [&] {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    e[k] = ex2_approx(s[k] - base[k >> 1]);
-                    const __half v = __float2half_rn(e[k]);
-                    sh.p[group][g + 8 * (k >> 1)][key_place + 4 * (k & 1)] = *reinterpret_cast<const uint16_t*>(&v);
-                }
+                for (int k = 0; k < 4; ++k) e[k] = ex2_approx(s[k] - base[k >> 1]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    *reinterpret_cast<uint32_t*>(&sh.p[group][g + 8 * h][8 * w + 2 * j]) = pack_f16x2(e[2 * h], e[2 * h + 1]);
             };
             publish();
             if (named_barrier_or(bar, kGroupThreads, top[0] > m_ref[0] + kRescaleLog2 || top[1] > m_ref[1] + kRescaleLog2)) {
@@ -471,7 +479,7 @@ __device__ void compute(const PagedParams& p, Shared& sh, int group, int w, int 
                         base[h] = t - kProbLog2;
                         l[h] *= alpha;
 #pragma unroll
-                        for (int m = 0; m < 8; ++m) {
+                        for (int m = 0; m < 16; ++m) {
                             o[m][2 * h] *= alpha;
                             o[m][2 * h + 1] *= alpha;
                         }
@@ -484,40 +492,25 @@ __device__ void compute(const PagedParams& p, Shared& sh, int group, int w, int 
             l[1] += e[2] + e[3];
             // ---- P V, this warp's features, 16 rows at a time
 #pragma unroll
-            for (int step = 0; step < 4; ++step) {
-                const uint2 a0 = *reinterpret_cast<const uint2*>(&sh.p[group][g][16 * step + 4 * j]);
-                const uint2 a1 = *reinterpret_cast<const uint2*>(&sh.p[group][g + 8][16 * step + 4 * j]);
-                const uint32_t a[4] = {a0.x, a1.x, a0.y, a1.y};
-                uint32_t x[4], by[4];
+            for (int step = 0; step < 2; ++step) {
+                uint32_t a[4];
+                ldmatrix_x4(a, p_read + 32 * step);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint8_t* at = slot + (16 * step + 4 * i + j) * MLA_Q4_ROW;
-                    x[i] = *reinterpret_cast<const uint32_t*>(at + 32 * w + 4 * g);
-                    by[i] = at[kQ4Scales + 4 * w + (g >> 1)];
-                }
-                const uint32_t s01 = clean_nan(widen_e4m3(static_cast<uint16_t>(by[0] | by[1] << 8)));
-                const uint32_t s23 = clean_nan(widen_e4m3(static_cast<uint16_t>(by[2] | by[3] << 8)));
-                constexpr uint32_t kLow = 0x0f0f0f0fu;
-                uint32_t even01[4], odd01[4], even23[4], odd23[4];
-                widen_e2m1((x[0] & kLow) | (x[1] << 4 & ~kLow), even01);
-                widen_e2m1((x[2] & kLow) | (x[3] << 4 & ~kLow), even23);
-                widen_e2m1((x[0] >> 4 & kLow) | (x[1] & ~kLow), odd01);
-                widen_e2m1((x[2] >> 4 & kLow) | (x[3] & ~kLow), odd23);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    mma_f16(o[2 * i], a, mul_f16x2(even01[i], s01), mul_f16x2(even23[i], s23));
-                    mma_f16(o[2 * i + 1], a, mul_f16x2(odd01[i], s01), mul_f16x2(odd23[i], s23));
+                for (int m = 0; m < 16; m += 2) {
+                    uint32_t b[4];
+                    ldmatrix_x4_trans(b, v_read + 4096 * step + (((m + (lane >> 4)) ^ (lane & 7)) << 4));
+                    mma_f16(o[m], a, b[0], b[1]);
+                    mma_f16(o[m + 1], a, b[2], b[3]);
                 }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.empty[ring]);
-            ring += 2;
+            ring += kGroups;
             if (ring >= kRing) {
                 ring -= kRing;
                 ++turn;
             }
         }
-        if (bad) break;
         // ---- the item's end: sums over the group's rows, then both groups
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -533,32 +526,36 @@ __device__ void compute(const PagedParams& p, Shared& sh, int group, int w, int 
 #pragma unroll
             for (int k = 0; k < kWarps; ++k) l[h] += sh.red[group][k][r];
         }
-        if (group == 1) {
-#pragma unroll
-            for (int m = 0; m < 8; ++m) sh.part[1][w][m][lane] = make_float4(o[m][0], o[m][1], o[m][2], o[m][3]);
-            if (w == 0 && j == 0) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    sh.ml[0][g + 8 * h] = m_ref[h];
-                    sh.ml[1][g + 8 * h] = l[h];
-                }
-            }
-        }
-        if (named_barrier_or(kBarBoth, kComputeThreads, false)) return;   // the other group has left
-        if (group == 0) {
-            float by0[2], by1[2], lse2[2];
+        if (w == 0 && j == 0) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const float m1 = sh.ml[0][g + 8 * h], l1 = sh.ml[1][g + 8 * h];
-                const float m = fmaxf(m_ref[h], m1);
-                // (a group without rows has the sum 0 and O = 0; a NaN stays one)
-                by0[h] = m_ref[h] > -INFINITY ? ex2_approx(m_ref[h] - m) : 1.f;
-                by1[h] = m1 > -INFINITY ? ex2_approx(m1 - m) : 1.f;
-                const float sum = l[h] * by0[h] + l1 * by1[h];
+                sh.top[group][g + 8 * h] = m_ref[h];
+                sh.sum[group][g + 8 * h] = l[h];
+            }
+        }
+        if (group > 0) {
+#pragma unroll
+            for (int m = 0; m < 16; ++m) sh.v[group][w][32 * m + lane] = make_float4(o[m][0], o[m][1], o[m][2], o[m][3]);
+        }
+        if (named_barrier_or(kBarAll, kComputeThreads, false)) return;   // a group has left
+        if (group == 0) {
+            float by[kGroups][2], lse2[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float m = m_ref[h], sum = 0.f;
+#pragma unroll
+                for (int k = 1; k < kGroups; ++k) m = fmaxf(m, sh.top[k][g + 8 * h]);
+#pragma unroll
+                for (int k = 0; k < kGroups; ++k) {
+                    // (a group without rows has the sum 0 and O = 0; a NaN stays one)
+                    const float t = sh.top[k][g + 8 * h];
+                    by[k][h] = t > -INFINITY ? ex2_approx(t - m) : 1.f;
+                    sum = fmaf(sh.sum[k][g + 8 * h], by[k][h], sum);
+                }
                 const float inv = sum == 0.f ? 0.f : p.kv_scale / sum;
                 lse2[h] = sum == 0.f ? -INFINITY : (m - kProbLog2) + log2f(sum);
-                by0[h] *= inv;
-                by1[h] *= inv;
+#pragma unroll
+                for (int k = 0; k < kGroups; ++k) by[k][h] *= inv;
             }
             const bool whole = it.hi - it.lo == it.n_units;
             const int slot = kTreePieces * static_cast<int>(blockIdx.x) + (item == 0 ? 0 : 1);
@@ -575,44 +572,44 @@ __device__ void compute(const PagedParams& p, Shared& sh, int group, int w, int 
             if (w == 0 && lane == 0 && !whole && it.lo == 0)
                 p.merge[blockIdx.x] = TreeMerge{it.b, it.rb, live | (item == 0 ? 0 : 1) << 16, it.runs};
 #pragma unroll
-            for (int m = 0; m < 8; ++m) {
-                const float4 v = sh.part[1][w][m][lane];
-                o[m][0] = o[m][0] * by0[0] + v.x * by1[0];
-                o[m][1] = o[m][1] * by0[0] + v.y * by1[0];
-                o[m][2] = o[m][2] * by0[1] + v.z * by1[1];
-                o[m][3] = o[m][3] * by0[1] + v.w * by1[1];
-            }
-            // rows g, g + 8; features 64 w + 16 j + m (register 0) and + 8 (register 1)
+            for (int m = 0; m < 16; ++m)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[m][k] *= by[0][k >> 1];
+#pragma unroll
+            for (int k = 1; k < kGroups; ++k)
+#pragma unroll
+                for (int m = 0; m < 16; ++m) {
+                    const float4 v = sh.v[k][w][32 * m + lane];
+                    o[m][0] = fmaf(v.x, by[k][0], o[m][0]);
+                    o[m][1] = fmaf(v.y, by[k][0], o[m][1]);
+                    o[m][2] = fmaf(v.z, by[k][1], o[m][2]);
+                    o[m][3] = fmaf(v.w, by[k][1], o[m][3]);
+                }
+            // rows g, g + 8; features 128 w + 8 m + 2 j, + 1
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int r = g + 8 * h;
                 if (r >= live) continue;
-                if (!whole || p.a.out_fp32) {
-                    float4* dst = whole ? reinterpret_cast<float4*>(static_cast<float*>(p.a.out) + (row0 + r) * kDLatent + 64 * w + 16 * j)
-                                        : reinterpret_cast<float4*>(p.part) +
-                                              (static_cast<long long>(slot) * (kDLatent / 4) + 16 * w + 4 * j) * 32 + r;
-                    const int step = whole ? 1 : 32;
+                const int from = 128 * w + 2 * j;
+                if (!whole) {
+                    float* piece = p.part + (static_cast<long long>(slot) * (kDLatent / 4) * 32 + r) * 4 + (j & 1) * 2;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int m = 4 * (k & 1), c = 2 * h + (k >> 1);
-                        dst[step * k] = make_float4(o[m][c], o[m + 1][c], o[m + 2][c], o[m + 3][c]);
-                    }
+                    for (int m = 0; m < 16; ++m)
+                        *reinterpret_cast<float2*>(piece + (32 * w + 2 * m + (j >> 1)) * 128) = make_float2(o[m][2 * h], o[m][2 * h + 1]);
+                } else if (p.a.out_fp32) {
+                    float* dst = static_cast<float*>(p.a.out) + (row0 + r) * kDLatent + from;
+#pragma unroll
+                    for (int m = 0; m < 16; ++m) *reinterpret_cast<float2*>(dst + 8 * m) = make_float2(o[m][2 * h], o[m][2 * h + 1]);
                 } else {
-                    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.a.out) + (row0 + r) * kDLatent + 64 * w + 16 * j);
+                    uint16_t* dst = static_cast<uint16_t*>(p.a.out) + (row0 + r) * kDLatent + from;
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const int c = 2 * h + k;
-                        dst[k] = make_uint4(pack_bf16x2(o[0][c], o[1][c]), pack_bf16x2(o[2][c], o[3][c]),
-                                            pack_bf16x2(o[4][c], o[5][c]), pack_bf16x2(o[6][c], o[7][c]));
-                    }
+                    for (int m = 0; m < 16; ++m) *reinterpret_cast<uint32_t*>(dst + 8 * m) = pack_bf16x2(o[m][2 * h], o[m][2 * h + 1]);
                 }
             }
         }
-        named_barrier_sync(kBarBoth, kComputeThreads);     // group 1's O has been read
+        // (the others' O has been read when all meet at the next item's beginning)
         if (lane == 0) mbar_arrive(&sh.item_empty[item % kItems]);
     }
-    named_barrier_or(kBarBoth, kComputeThreads, true);
-    if (bad && lane == 0) raise(p, sh);
 }
 
 __global__ void __launch_bounds__(kThreads, 1) mla_paged_decode_kernel(const __grid_constant__ PagedParams p) {
@@ -626,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_paged_decode_kernel(const __g
         }
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&sh.item_full[i], 1);
-            mbar_init(&sh.item_empty[i], 2 * kWarps);
+            mbar_init(&sh.item_empty[i], kGroups * kWarps);
         }
         mbar_init(&sh.stall_bar, 1);
         sh.abort_flag = 0;
