@@ -84,7 +84,10 @@ int prepare(cudaStream_t st, bool may_capture) {
     return MLA_OK;
 }
 
-// Few query rows: on warp-level MMAs, an SM's run each.  (It counts units of 64 rows in an int.)
+// Few query rows: on warp-level MMAs, an SM's run each.  Measured against the tcgen05 kernel, us (requests x cache rows), for
+// 16 query rows per request: 14.5 and 16.7 (1 x 255), 24.7 and 30.9 (8 x 4096), 26.8 and 38.0 (32 x 2000), 154 and 253
+// (32 x 32768); for 32: 15.4 and 18.1, 27.6 and 30.9, 35.0 and 38.2, 287 and 253; for 48: 16.5 and 20.6, 30.9 and 34.5,
+// 45.8 and 41.2, 421 and 257.  (How long the requests are, the host does not know.  It counts units of 64 rows in an int.)
 constexpr int kFewRows = 32;
 bool few_rows(const mla_paged_plan_t* pl, const mla_paged_args* a) {
     const long long rows = static_cast<long long>(pl->shape.tokens) * pl->shape.heads;

@@ -27,7 +27,10 @@
 namespace mla {
 namespace {
 
-constexpr int kThreads = 256;
+// Registers held to 72, seven blocks per SM: 4696 tokens of 128 heads 32 us; with 80 and six blocks 35, blocks of 256 threads
+// 36 (a warp's 32 heads are 4 KB on their way: with 28 warps, seven eighths of what hides the memory's latency).
+constexpr int kThreads = 128;
+constexpr int kBlocksPerSm = 7;
 constexpr int kHeadPasses = 8;                             // of four heads each, per warp
 
 // (hi, lo) += x, hi + lo exact but for what leaves lo.
@@ -78,13 +81,54 @@ __device__ __forceinline__ void norm_unit(float (&f)[8], const float (&w)[8], fl
     for (int i = 0; i < 8; ++i) f[i] = f[i] * r * w[i];
 }
 
+// Two fp32 numbers in a 64-bit register, and products of both.
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+// A unit's four pairs (x, y): x of pairs 0, 1 and of 2, 3, then y.
+template <bool kInterleaved>
+__device__ __forceinline__ void widen_pairs(const uint4 v, uint64_t (&x)[2], uint64_t (&y)[2]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    auto lo = [&](int i) { return __uint_as_float(w[i] << 16); };
+    auto hi = [&](int i) { return __uint_as_float(w[i] & 0xffff0000u); };
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        x[i] = kInterleaved ? pack2(lo(2 * i), lo(2 * i + 1)) : pack2(lo(i), hi(i));
+        y[i] = kInterleaved ? pack2(hi(2 * i), hi(2 * i + 1)) : pack2(lo(2 + i), hi(2 + i));
+    }
+}
+template <bool kInterleaved>
+__device__ __forceinline__ uint4 narrow_pairs(const uint64_t (&x)[2], const uint64_t (&y)[2]) {
+    const float2 a = unpack2(x[0]), b = unpack2(x[1]), c = unpack2(y[0]), d = unpack2(y[1]);
+    if (kInterleaved) return make_uint4(pack_bf16x2(a.x, c.x), pack_bf16x2(a.y, c.y), pack_bf16x2(b.x, d.x), pack_bf16x2(b.y, d.y));
+    return make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(b.x, b.y), pack_bf16x2(c.x, c.y), pack_bf16x2(d.x, d.y));
+}
+
 struct AppendParams4 {
     mla_paged_append_args a;
     PagedCache cache;
     float kv_scale, sixth;                                 // 1 / (6 kv_scale)
 };
 
-__global__ void __launch_bounds__(kThreads) mla_paged_append_kernel(const __grid_constant__ AppendParams4 p,
+template <bool kInterleaved>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) mla_paged_append_kernel(const __grid_constant__ AppendParams4 p,
                                                                     int units_per_token) {
     grid_dependency_wait();
     allow_dependent_launch();
@@ -99,7 +143,7 @@ __global__ void __launch_bounds__(kThreads) mla_paged_append_kernel(const __grid
     const int pos = a.positions[static_cast<long long>(b) * a.tokens + n];
     const bool rotated = 4 * u < half;                     // half is a multiple of 4: a unit whole or not at all
     int lo, hi;
-    unit_offsets(u, half, a.interleaved, lo, hi);
+    unit_offsets(u, half, kInterleaved, lo, hi);
     if (p.cache.pages && part == units_per_token - 1) {
         // ---- the row
         const int d = a.d_pos[b];
@@ -173,7 +217,7 @@ __global__ void __launch_bounds__(kThreads) mla_paged_append_kernel(const __grid
             widen8(load_unit(static_cast<const uint16_t*>(a.k_norm), lo, hi), g);
             norm_unit(x, g, a.eps);
         }
-        if (rotated) rotate_unit(x, a.interleaved, cs, sn);
+        if (rotated) rotate_unit(x, kInterleaved, cs, sn);
         if (lane < 8) {
             const uint4 o = narrow8(x);
             uint16_t* dst = reinterpret_cast<uint16_t*>(row + kQ4Rope);
@@ -191,25 +235,77 @@ __global__ void __launch_bounds__(kThreads) mla_paged_append_kernel(const __grid
         v[j] = make_uint4(0, 0, 0, 0);
         if (h0 + 4 * j < a.heads) {
             const uint16_t* q = src + (h0 + 4 * j) * a.q_rope_head;
-            v[j] = a.interleaved ? *reinterpret_cast<const uint4*>(q + lo) : load_unit(q, lo, hi);
+            v[j] = kInterleaved ? *reinterpret_cast<const uint4*>(q + lo) : load_unit(q, lo, hi);
         }
     }
-    float sn0, cs0, cs[4], sn[4], g[8];
+    float sn0, cs0, cs[4], sn[4];
     pair_angle(pos, a.turns, half, a.amplitude, lane, sn0, cs0);
     unit_angles(u, sn0, cs0, cs, sn);
-    if (a.q_norm) widen8(load_unit(static_cast<const uint16_t*>(a.q_norm), lo, hi), g);
+    // x' = x r wx cos - y r wy sin,  y' = y r wy cos + x r wx sin (a pair that is not rotated: x r wx, y r wy): the weights
+    // go into the angles
+    uint64_t wx[2] = {pack2(1.f, 1.f), pack2(1.f, 1.f)}, wy[2] = {wx[0], wx[0]};
+    if (a.q_norm) widen_pairs<kInterleaved>(load_unit(static_cast<const uint16_t*>(a.q_norm), lo, hi), wx, wy);
+    uint64_t xx[2], yx[2], yy[2], xy[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint64_t c = rotated ? pack2(cs[2 * i], cs[2 * i + 1]) : pack2(1.f, 1.f);
+        xx[i] = mul2(wx[i], c);
+        yy[i] = mul2(wy[i], c);
+        xy[i] = mul2(wx[i], pack2(sn[2 * i], sn[2 * i + 1]));
+        yx[i] = mul2(wy[i], pack2(-sn[2 * i], -sn[2 * i + 1]));
+    }
+    float r = 1.f;
+    if (a.q_norm) {
+        // sums of squares of all eight passes' heads; lane u of eight ends with those of pass u
+        float sum[kHeadPasses];
+#pragma unroll
+        for (int j = 0; j < kHeadPasses; ++j) {
+            uint64_t x[2], y[2];
+            widen_pairs<kInterleaved>(v[j], x, y);
+            const float2 t = unpack2(fma2(y[1], y[1], fma2(y[0], y[0], fma2(x[1], x[1], mul2(x[0], x[0])))));
+            sum[j] = t.x + t.y;
+        }
+        static_assert(kHeadPasses == 8, "as many passes as a head has lanes");
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) {
+            const bool up = lane & o;
+#pragma unroll
+            for (int j = 0; j < o; ++j) {
+                const float mine = up ? sum[j + o] : sum[j], other = up ? sum[j] : sum[j + o];
+                sum[j] = mine + __shfl_xor_sync(0xffffffffu, other, o);
+            }
+        }
+        r = rsqrtf(fmaf(sum[0], 1.f / kDRope, a.eps));
+    }
     uint16_t* dst = static_cast<uint16_t*>(a.q_out) + b * a.q_out_batch + n * a.q_out_token;
 #pragma unroll
     for (int j = 0; j < kHeadPasses; ++j) {
         if (kHeadPasses * 4 * part + 4 * j >= a.heads) break;   // uniform over the warp
-        float f[8];
-        widen8(v[j], f);
-        if (a.q_norm) norm_unit(f, g, a.eps);
-        if (rotated) rotate_unit(f, a.interleaved, cs, sn);
+        uint64_t x[2], y[2];
+        widen_pairs<kInterleaved>(v[j], x, y);
+        if (a.q_norm) {
+            const float f = __shfl_sync(0xffffffffu, r, (lane & 24) | j);
+            const uint64_t by = pack2(f, f);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                x[i] = mul2(x[i], by);
+                y[i] = mul2(y[i], by);
+            }
+        }
+        uint64_t rx[2], ry[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            rx[i] = mul2(x[i], xx[i]);
+            ry[i] = mul2(y[i], yy[i]);
+            if (rotated) {
+                rx[i] = fma2(y[i], yx[i], rx[i]);
+                ry[i] = fma2(x[i], xy[i], ry[i]);
+            }
+        }
         if (h0 + 4 * j < a.heads) {
-            const uint4 o = narrow8(f);
+            const uint4 o = narrow_pairs<kInterleaved>(rx, ry);
             uint16_t* q = dst + (h0 + 4 * j) * a.q_out_head;
-            if (a.interleaved) {
+            if (kInterleaved) {
                 *reinterpret_cast<uint4*>(q + lo) = o;
             } else {
                 *reinterpret_cast<uint2*>(q + lo) = make_uint2(o.x, o.y);
@@ -340,7 +436,8 @@ extern "C" int mla_paged_append(const mla_paged_append_args* args, void* stream)
     cudaLaunchAttribute attr;
     rc = mla::launch_blocks(&cfg, &attr, static_cast<long long>(args->tokens) * units, args->batch, stream);
     if (rc != MLA_OK) return rc;
-    return mla::launch_status(cudaLaunchKernelEx(&cfg, mla::mla_paged_append_kernel, p, units));
+    return mla::launch_status(cudaLaunchKernelEx(
+        &cfg, args->interleaved ? mla::mla_paged_append_kernel<true> : mla::mla_paged_append_kernel<false>, p, units));
 }
 
 extern "C" int mla_paged_read(const mla_paged_read_args* args, void* stream) {

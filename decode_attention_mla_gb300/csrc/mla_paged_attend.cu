@@ -280,7 +280,8 @@ __device__ __forceinline__ void fill_queries(const PagedParams& p, Shared& sh, l
                 m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
             top = fmaxf(top, k < 2 ? m : m * inv_kv);
         }
-        top = warp_max_f32(top);
+        // (magnitudes as fp32 bits are in the order of integers)
+        top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
         const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127 - 14, -126), 126);
         const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll
@@ -929,7 +930,8 @@ cudaError_t launch_paged_attend(const PagedMaps& maps, const PagedParams& p, boo
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, mla_paged_attend_kernel, maps, p);
-    return e != cudaSuccess ? e : launch_tree_merge(p, pdl, stream);
+    // (it waits for this kernel's end before it reads: it may always be launched ahead)
+    return e != cudaSuccess ? e : launch_tree_merge(p, true, stream);
 }
 
 }  // namespace mla

@@ -686,7 +686,8 @@ cudaError_t launch_paged_decode(const PagedParams& p, bool pdl, cudaStream_t str
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, mla_paged_decode_kernel, p);
-    return e != cudaSuccess ? e : launch_tree_merge(p, pdl, stream);
+    // (it waits for this kernel's end before it reads: it may always be launched ahead)
+    return e != cudaSuccess ? e : launch_tree_merge(p, true, stream);
 }
 
 }  // namespace mla
