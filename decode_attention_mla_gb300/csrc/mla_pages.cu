@@ -7,15 +7,19 @@
 // minima of integers: the same in any order), by whose last block the pages are handed
 // out (one block: its scan of refs ends as soon as it has found enough free pages);
 // then the tables written and the shared last pages copied.  The new table waits in
-// scratch, since a request's row may be another's parent.
+// scratch, since a request's row may be another's parent.  A small fork is one block's.
 //
-// compact.  Ranks of the pages in use by a two-level count; the k-th page in use
-// behind the front goes to the k-th hole in it.  Three launches: counts per 4096 pages;
-// lists of holes and moving pages; moves, tables and references.
+// compact.  The k-th page in use behind the front goes to the k-th hole in it.  Pools of up to
+// kBitsPages pages take one launch: every block counts all of them itself, which costs it
+// less than a launch whose counts it would wait for (512 pages 4.3 us for 8.7, 65536
+// 9.9 for 13.7); references in place take a second.  Larger pools, three: counts
+// per 4096 pages; lists of holes and moving pages; moves, tables and references.
 //
 // Bound: bytes (tables and references, and the rows that are copied), below that the
-// launches.
+// launches, each a chain of a few loads.  256 requests with 65300 entries, a pool of 65536: 14.4 us.
+// 7700 pages of 26 KB moved by bulk copies: 74 us, 5.6 TB/s (by loads and stores of a thread's own, 82).
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 
 #include "device_utils.cuh"
@@ -92,7 +96,7 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
     return v + before;
 }
 
-// Hand out pages (one block).
+// Hand out pages (one block).  All of its threads have passed a barrier behind the counts.
 __device__ void fork_place(const ForkParams& p) {
     __shared__ int sums[32];
     const int batch = p.a.batch, columns = p.a.columns;
@@ -182,31 +186,35 @@ __device__ void fork_place(const ForkParams& p) {
     if (threadIdx.x == 0) *p.a.missing = needed - have;
 }
 
+// Entry c of request b, which has n rows: into the new table, and counted.
+__device__ __forceinline__ void fork_entry(const ForkParams& p, int b, int c, int parent, int n) {
+    int page = -1;
+    const long long t0 = static_cast<long long>(c) << p.shift, t1 = t0 + (1 << p.shift);
+    if (t0 < n) {
+        page = p.a.page_table[static_cast<long long>(parent) * p.a.columns + c];
+        if (page < 0 || page >= p.a.n_pages) page = -1;
+        // (no later token attends rows up to n - window)
+        if (p.a.window > 0 && t0 >= p.a.sink && t1 <= static_cast<long long>(n) + 1 - p.a.window) page = -1;
+        if (page >= 0) {
+            if (t1 <= n)
+                atomicAdd(p.a.refs + page, 1);
+            else
+                atomicMin(p.keeper + page, b);
+        }
+    }
+    p.table[static_cast<long long>(b) * p.a.columns + c] = page;
+}
+
 // A request's entries, kThreads * 4 columns a block; the last block hands out pages.
 __global__ void __launch_bounds__(kPlaceThreads) mla_fork_count_kernel(const __grid_constant__ ForkParams p) {
     __shared__ int is_last;
     grid_dependency_wait();
     allow_dependent_launch();
-    const int b = blockIdx.y, ps = 1 << p.shift;
+    const int b = blockIdx.y;
     int parent;
     const int n = fork_rows(p, b, parent);
-    for (int c = blockIdx.x * kPlaceThreads + threadIdx.x; c < p.a.columns; c += gridDim.x * kPlaceThreads) {
-        int page = -1;
-        const long long t0 = static_cast<long long>(c) << p.shift, t1 = t0 + ps;
-        if (t0 < n) {
-            page = p.a.page_table[static_cast<long long>(parent) * p.a.columns + c];
-            if (page < 0 || page >= p.a.n_pages) page = -1;
-            // (no later token attends rows up to n - window)
-            if (p.a.window > 0 && t0 >= p.a.sink && t1 <= static_cast<long long>(n) + 1 - p.a.window) page = -1;
-            if (page >= 0) {
-                if (t1 <= n)
-                    atomicAdd(p.a.refs + page, 1);
-                else
-                    atomicMin(p.keeper + page, b);
-            }
-        }
-        p.table[static_cast<long long>(b) * p.a.columns + c] = page;
-    }
+    for (int c = blockIdx.x * kPlaceThreads + threadIdx.x; c < p.a.columns; c += gridDim.x * kPlaceThreads)
+        fork_entry(p, b, c, parent, n);
     if (blockIdx.x == 0 && threadIdx.x == 0) p.rows[b] = n;
     __threadfence();
     __syncthreads();
@@ -217,16 +225,27 @@ __global__ void __launch_bounds__(kPlaceThreads) mla_fork_count_kernel(const __g
     fork_place(p);
 }
 
-__device__ __forceinline__ void copy_units(uint4* dst, const uint4* src, long long units) {
-    long long i = threadIdx.x;
-    for (; i + 3 * kThreads < units; i += 4 * kThreads) {
-        uint4 v[4];
+// Eight loads a thread on their way; thread `at` of `threads`.
+__device__ __forceinline__ void copy_units(uint4* dst, const uint4* src, int units, int at, int threads) {
+    for (int i = at; i < units; i += 8 * threads) {
+        uint4 v[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = src[i + k * kThreads];
+        for (int k = 0; k < 8; ++k)
+            if (i + k * threads < units) v[k] = src[i + k * threads];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) dst[i + k * kThreads] = v[k];
+        for (int k = 0; k < 8; ++k)
+            if (i + k * threads < units) dst[i + k * threads] = v[k];
     }
-    for (; i < units; i += kThreads) dst[i] = src[i];
+}
+// Request b's copied page, if it has one.
+__device__ __forceinline__ void fork_copy(const ForkParams& p, int b, int at, int threads) {
+    const int n = p.rows[b], from = p.src[b], to = p.dst[b];
+    if (to < 0) return;
+    char* pages = static_cast<char*>(p.a.pages);
+    const int rows = n & ((1 << p.shift) - 1);
+    copy_units(reinterpret_cast<uint4*>(pages + to * p.a.page_stride),
+               reinterpret_cast<const uint4*>(pages + from * p.a.page_stride),
+               rows * (p.a.row_bytes / 16), at, threads);
 }
 
 // A block per request: its table, its rows, its copied page.
@@ -234,16 +253,38 @@ __global__ void __launch_bounds__(kThreads) mla_fork_write_kernel(const __grid_c
     grid_dependency_wait();
     allow_dependent_launch();
     const int b = blockIdx.x;
-    const int n = p.rows[b], from = p.src[b], to = p.dst[b];
     const long long row = static_cast<long long>(b) * p.a.columns;
     for (int c = threadIdx.x; c < p.a.columns; c += kThreads) p.a.page_table_out[row + c] = p.table[row + c];
-    if (threadIdx.x == 0) p.a.d_pos_out[b] = n;
-    if (to < 0) return;
-    char* pages = static_cast<char*>(p.a.pages);
-    const int rows = n & ((1 << p.shift) - 1);
-    copy_units(reinterpret_cast<uint4*>(pages + to * p.a.page_stride),
-               reinterpret_cast<const uint4*>(pages + from * p.a.page_stride),
-               static_cast<long long>(rows) * p.a.row_bytes / 16);
+    if (threadIdx.x == 0) p.a.d_pos_out[b] = p.rows[b];
+    fork_copy(p, b, threadIdx.x, kThreads);
+}
+
+// All of it in one block, one launch for three.
+__global__ void __launch_bounds__(kPlaceThreads) mla_fork_small_kernel(const __grid_constant__ ForkParams p) {
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const int entries = p.a.batch * p.a.columns;
+    for (int i = threadIdx.x; i < p.a.n_pages; i += kPlaceThreads) {
+        p.a.refs[i] = 0;
+        p.keeper[i] = kNobody;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < entries; e += kPlaceThreads) {
+        const int b = e / p.a.columns, c = e - b * p.a.columns;
+        int parent;
+        const int n = fork_rows(p, b, parent);
+        fork_entry(p, b, c, parent, n);
+        if (c == 0) p.rows[b] = n;
+    }
+    __threadfence();
+    __syncthreads();
+    fork_place(p);
+    __syncthreads();
+    for (int e = threadIdx.x; e < entries; e += kPlaceThreads) p.a.page_table_out[e] = p.table[e];
+    for (int b = threadIdx.x; b < p.a.batch; b += kPlaceThreads) p.a.d_pos_out[b] = p.rows[b];
+    // copies, kThreads threads a request
+    for (int b = threadIdx.x / kThreads; b < p.a.batch; b += kPlaceThreads / kThreads)
+        fork_copy(p, b, threadIdx.x % kThreads, kThreads);
 }
 
 // ---- compact --------------------------------------------------------------------
@@ -256,8 +297,230 @@ struct CompactParams {
     int* hole;                                             // [..] by rank: page to fill
     int* mover;                                            // ... and the page that goes there
     int* mover_refs;                                       // ... and its references
-    int* moves;                                            // number of them
+    int* moves;                                            // number of them; of pages in use
+    uint32_t* bits;                                        // kept for the references in place: which pages are in use
 };
+
+// Whole pages moved by bulk copies through shared memory: one warp keeps kPartsAhead parts of pages on their way in and the
+// rest of the ring on its way out.
+constexpr int kPartBytes = 16384, kParts = 12, kPartsAhead = 7;
+constexpr int kMoveThreads = 1024;
+struct __align__(128) MoveRing {
+    uint8_t part[kParts][kPartBytes];
+    uint64_t full[kParts];
+    char* to[kParts];
+    int bytes[kParts];
+};
+
+__device__ __forceinline__ void bulk_copy_s2g(void* dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void init_ring(MoveRing& r) {
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kParts; ++i) mbar_init(&r.full[i], 1);
+        mbar_init_fence();
+    }
+    __syncthreads();
+}
+// One warp.  places(k, from, to): the k-th moving page and where it goes.  A copy that does not arrive: `used` is -1.
+template <class Places>
+__device__ void move_pages(const CompactParams& p, MoveRing& r, int moves, int lane, const Places& places) {
+    char* pages = static_cast<char*>(p.a.pages);
+    const int page = p.a.page_rows * p.a.row_bytes, per = (page + kPartBytes - 1) / kPartBytes;
+    const long long all = static_cast<long long>(moves) * per, first = blockIdx.x, step = gridDim.x;
+    const long long mine = first < all ? (all - first + step - 1) / step : 0;
+    const uint64_t policy = l2_policy_evict_first();
+    volatile int never = 0;
+    bool ok = true;
+    int in = 0, out = 0;                                   // ring slots of the next part in and out
+    uint32_t phase = 0;                                    // of `out`
+    auto send = [&] {
+        const bool there = mbar_wait_bounded(&r.full[out], phase, &never);
+        if (there) bulk_copy_s2g(r.to[out], r.part[out], r.bytes[out]);
+        if (++out == kParts) {
+            out = 0;
+            phase ^= 1;
+        }
+        return there;
+    };
+    for (long long base = 0; base < mine && ok; base += 32) {
+        int from = 0, to = 0, offset = 0;
+        if (base + lane < mine) {
+            const long long t = first + (base + lane) * step;
+            const int k = static_cast<int>(t / per);
+            offset = static_cast<int>(t - static_cast<long long>(k) * per) * kPartBytes;
+            places(k, from, to);
+        }
+        const int n = static_cast<int>(min(mine - base, 32ll));
+        for (int j = 0; j < n; ++j) {
+            const int f = __shfl_sync(0xffffffffu, from, j), t = __shfl_sync(0xffffffffu, to, j);
+            const int o = __shfl_sync(0xffffffffu, offset, j);
+            if (lane == 0 && ok) {
+                if (base + j >= kPartsAhead) ok = send();
+                // the part that was in this slot has left it
+                asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kParts - kPartsAhead) : "memory");
+                const int bytes = min(page - o, kPartBytes);
+                r.to[in] = pages + t * p.a.page_stride + o;
+                r.bytes[in] = bytes;
+                if (ok) {
+                    mbar_arrive_expect_tx(&r.full[in], bytes);
+                    bulk_copy_g2s(r.part[in], pages + f * p.a.page_stride + o, bytes, &r.full[in], policy);
+                }
+                if (++in == kParts) in = 0;
+            }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+    if (lane == 0) {
+        for (long long i = min(mine, static_cast<long long>(kPartsAhead)); i > 0 && ok; --i) ok = send();
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        if (!ok) {
+            // copies in flight get time to land before shared memory is given up
+            const long long t0 = clock64();
+            while (clock64() - t0 < 2000ll * 1000ll) {
+            }
+            *p.a.used = -1;
+        }
+    }
+}
+
+// Pools of up to kBitsPages pages: every block counts all of them itself, as bits in its shared memory with the set bits
+// before each word, and finds the k-th hole and the k-th moving page there.
+constexpr int kBitsPages = 65536, kBitsWords = kBitsPages / 32, kBitsThreads = kMoveThreads;
+struct PageBits {
+    uint32_t word[kBitsWords];
+    int before[kBitsWords];
+    int sums[32];
+};
+
+// Bits of the block's words to their ranks; returns the number of pages in use.  (words: up to kBitsWords.)
+__device__ int rank_bits(PageBits& s, int words) {
+    constexpr int kEach = kBitsWords / kBitsThreads;
+    int mine[kEach], sum = 0, live;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+        const int w = kEach * threadIdx.x + k;
+        mine[k] = w < words ? __popc(s.word[w]) : 0;
+        sum += mine[k];
+    }
+    int at = block_scan(sum, s.sums, live) - sum;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+        s.before[kEach * threadIdx.x + k] = at;            // (behind the last word: all)
+        at += mine[k];
+    }
+    __syncthreads();
+    return live;
+}
+__device__ __forceinline__ int bit_rank(const PageBits& s, int i) {
+    return s.before[i >> 5] + __popc(s.word[i >> 5] & ((1u << (i & 31)) - 1));
+}
+// The n-th bit (from 0) that is set, or with kZero that is not.
+template <bool kZero>
+__device__ __noinline__ int nth_bit(const PageBits& s, int words, int n) {
+    int lo = 0, hi = words;                                // the word lies in [lo, hi)
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if ((kZero ? 32 * mid - s.before[mid] : s.before[mid]) <= n)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    n -= kZero ? 32 * lo - s.before[lo] : s.before[lo];
+    uint32_t v = kZero ? ~s.word[lo] : s.word[lo];
+    int bit = 0;
+#pragma unroll
+    for (int step = 16; step > 0; step >>= 1) {
+        const int c = __popc(v & ((1u << step) - 1));
+        if (n >= c) {
+            n -= c;
+            v >>= step;
+            bit += step;
+        }
+    }
+    return 32 * lo + bit;
+}
+
+__global__ void __launch_bounds__(kBitsThreads) mla_compact_bits_kernel(const __grid_constant__ CompactParams p) {
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    MoveRing& ring = *reinterpret_cast<MoveRing*>(smem_raw);
+    PageBits& s = *reinterpret_cast<PageBits*>(smem_raw + sizeof(MoveRing));
+    init_ring(ring);
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const int lane = threadIdx.x & 31, words = (p.a.n_pages + 31) >> 5;
+    constexpr int kWarps = kBitsThreads / 32, kAhead = 8;
+    for (int w0 = threadIdx.x >> 5; w0 < words; w0 += kAhead * kWarps) {
+        int refs[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int i = 32 * (w0 + k * kWarps) + lane;
+            refs[k] = i < p.a.n_pages ? p.a.refs[i] : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const uint32_t word = __ballot_sync(0xffffffffu, refs[k] > 0);
+            if (lane == 0 && w0 + k * kWarps < words) s.word[w0 + k * kWarps] = word;
+        }
+    }
+    const int live = rank_bits(s, words);
+    const int front = live < 32 * words ? bit_rank(s, live) : live;   // pages in use among the first `live`
+    const int moves = live - front;
+    const bool in_place = p.a.refs_out == p.a.refs;
+    if (blockIdx.x == 0) {
+        if (threadIdx.x == 0) {
+            *p.a.used = live;
+            p.moves[1] = live;
+        }
+        if (in_place)
+            for (int w = threadIdx.x; w < words; w += kBitsThreads) p.bits[w] = s.word[w];
+    }
+    // ---- the pages, by one warp; the table and the references by the others
+    if (threadIdx.x < 32) {
+        move_pages(p, ring, moves, lane, [&](int k, int& from, int& to) {
+            from = nth_bit<false>(s, words, front + k);
+            to = nth_bit<true>(s, words, k);
+        });
+        return;
+    }
+    // ---- the table
+    const long long at = static_cast<long long>(blockIdx.x) * (kBitsThreads - 32) + threadIdx.x - 32;
+    const long long step = static_cast<long long>(gridDim.x) * (kBitsThreads - 32);
+    const long long entries = static_cast<long long>(p.a.batch) * p.a.columns;
+    for (long long e = at; e < entries; e += step) {
+        int v = p.a.page_table[e];
+        if (v < 0 || v >= p.a.n_pages || !(s.word[v >> 5] >> (v & 31) & 1))
+            v = -1;
+        else if (v >= live)
+            v = nth_bit<true>(s, words, bit_rank(s, v) - front);
+        p.a.page_table_out[e] = v;
+    }
+    if (in_place) return;                                  // (other blocks may still read the references)
+    for (long long i = at; i < p.a.n_pages; i += step) {
+        const int from = i >= live ? -1 : s.word[i >> 5] >> (i & 31) & 1 ? static_cast<int>(i)
+                         : nth_bit<false>(s, words, front + static_cast<int>(i) - bit_rank(s, static_cast<int>(i)));
+        p.a.refs_out[i] = from < 0 ? 0 : p.a.refs[from];
+    }
+}
+
+// The references in place: the k-th moving page's go to the k-th hole.
+__global__ void __launch_bounds__(kBitsThreads) mla_compact_refs_kernel(const __grid_constant__ CompactParams p) {
+    __shared__ PageBits s;
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const int words = (p.a.n_pages + 31) >> 5, live = p.moves[1];
+    for (int w = threadIdx.x; w < words; w += kBitsThreads) s.word[w] = p.bits[w];
+    rank_bits(s, words);
+    const int front = live < 32 * words ? bit_rank(s, live) : live;
+    for (int i = live + blockIdx.x * kBitsThreads + threadIdx.x; i < p.a.n_pages; i += gridDim.x * kBitsThreads) {
+        if (s.word[i >> 5] >> (i & 31) & 1)
+            p.a.refs_out[nth_bit<true>(s, words, bit_rank(s, i) - front)] = p.a.refs_out[i];
+        p.a.refs_out[i] = 0;
+    }
+}
 
 __global__ void __launch_bounds__(kThreads) mla_compact_count_kernel(const __grid_constant__ CompactParams p) {
     __shared__ int sums[32];
@@ -333,21 +596,27 @@ __global__ void __launch_bounds__(kThreads) mla_compact_list_kernel(const __grid
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         *p.a.used = live;
-        *p.moves = live - front;
+        p.moves[0] = live - front;
+        p.moves[1] = live;
     }
 }
 
-__global__ void __launch_bounds__(kThreads) mla_compact_move_kernel(const __grid_constant__ CompactParams p) {
+__global__ void __launch_bounds__(kMoveThreads) mla_compact_move_kernel(const __grid_constant__ CompactParams p) {
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    MoveRing& ring = *reinterpret_cast<MoveRing*>(smem_raw);
+    init_ring(ring);
     grid_dependency_wait();
     allow_dependent_launch();
-    const int moves = *p.moves, live = *p.a.used;
-    const long long page = static_cast<long long>(p.a.page_rows) * p.a.row_bytes / 16;
-    char* pages = static_cast<char*>(p.a.pages);
-    for (int k = blockIdx.x; k < moves; k += gridDim.x)
-        copy_units(reinterpret_cast<uint4*>(pages + p.hole[k] * p.a.page_stride),
-                   reinterpret_cast<const uint4*>(pages + p.mover[k] * p.a.page_stride), page);
-    const long long at = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
-    const long long step = static_cast<long long>(gridDim.x) * kThreads;
+    const int moves = p.moves[0], live = p.moves[1];
+    if (threadIdx.x < 32) {
+        move_pages(p, ring, moves, threadIdx.x, [&](int k, int& from, int& to) {
+            from = p.mover[k];
+            to = p.hole[k];
+        });
+        return;
+    }
+    const long long at = static_cast<long long>(blockIdx.x) * (kMoveThreads - 32) + threadIdx.x - 32;
+    const long long step = static_cast<long long>(gridDim.x) * (kMoveThreads - 32);
     const long long entries = static_cast<long long>(p.a.batch) * p.a.columns;
     for (long long e = at; e < entries; e += step) {
         int v = p.a.page_table[e];
@@ -398,6 +667,14 @@ size_t compact_bytes(int n_pages) {
     return 256 + up256(4 * ((n + kChunk - 1) / kChunk)) + 4 * up256(4 * n);
 }
 
+// One block does all of a small fork, in one launch for three.  Measured, us (requests x pages named, pages of the pool;
+// each request with a copy of 64 rows of 416 bytes): 6.9 for 9.0 (1 x 40, 512), 10.5 for 11.7 (4 x 40, 512); but 13.9 for
+// 11.6 (16 x 256, 4096; copies of 16 rows) and 19.1 for 13.2 (8 x 1000, 8192).
+bool fork_is_small(const mla_pages_fork_args* a) {
+    return a->n_pages <= 1024 && static_cast<long long>(a->batch) * a->columns <= 1024 &&
+           static_cast<long long>(a->batch) * a->page_rows * a->row_bytes <= 128 << 10;
+}
+
 struct Carver {
     char* at;
     int* take(size_t ints) {
@@ -408,17 +685,37 @@ struct Carver {
 };
 
 template <class Params>
-cudaError_t launch(void (*kernel)(Params), dim3 grid, int threads, const Params& p, void* stream) {
+cudaError_t launch(void (*kernel)(Params), dim3 grid, int threads, const Params& p, void* stream, size_t smem = 0) {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = static_cast<cudaStream_t>(stream);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+constexpr size_t kBitsSmem = sizeof(MoveRing) + sizeof(PageBits);
+static_assert(kBitsSmem <= 227 * 1024, "fits shared memory");
+std::atomic<int> g_moves_prepared[kMaxDevices];
+
+// The device's SMs, and once per device the kernels' shared memory.
+int prepare_moves(int* sms) {
+    int dev = 0;
+    int rc = current_device(&dev);
+    if (rc == MLA_OK) rc = device_sm_count(dev, sms);
+    if (rc != MLA_OK || g_moves_prepared[dev].load(std::memory_order_acquire)) return rc;
+    cudaError_t e = cudaFuncSetAttribute(mla_compact_bits_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(kBitsSmem));
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(mla_compact_move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(sizeof(MoveRing)));
+    if (e == cudaSuccess) g_moves_prepared[dev].store(1, std::memory_order_release);
+    return launch_status(e);
 }
 
 }  // namespace
@@ -457,6 +754,7 @@ int mla_pages_fork(const mla_pages_fork_args* args, void* scratch, size_t scratc
     p.first = c.take(args->batch);
     p.src = c.take(args->batch);
     p.dst = c.take(args->batch);
+    if (fork_is_small(args)) return launch_status(launch(mla_fork_small_kernel, dim3(1), kPlaceThreads, p, stream));
     const dim3 count((args->columns + kPlaceThreads - 1) / kPlaceThreads, args->batch);
     p.blocks = static_cast<int>(count.x * count.y);
     const int clear = std::min((args->n_pages + kThreads - 1) / kThreads, 1024);
@@ -487,9 +785,20 @@ int mla_pages_compact(const mla_pages_compact_args* args, void* scratch, size_t 
     p.hole = c.take(args->n_pages);
     p.mover = c.take(args->n_pages);
     p.mover_refs = c.take(args->n_pages);
+    int sms = 0;
+    rc = prepare_moves(&sms);
+    if (rc != MLA_OK) return rc;
+    if (args->n_pages <= kBitsPages) {
+        p.bits = reinterpret_cast<uint32_t*>(p.hole);
+        cudaError_t e = launch(mla_compact_bits_kernel, dim3(sms), kBitsThreads, p, stream, kBitsSmem);
+        if (e == cudaSuccess && args->refs_out == args->refs)
+            e = launch(mla_compact_refs_kernel, dim3(std::min((args->n_pages + kBitsThreads - 1) / kBitsThreads, sms)),
+                       kBitsThreads, p, stream);
+        return launch_status(e);
+    }
     cudaError_t e = launch(mla_compact_count_kernel, dim3(p.chunks), kThreads, p, stream);
     if (e == cudaSuccess) e = launch(mla_compact_list_kernel, dim3(p.chunks), kThreads, p, stream);
-    if (e == cudaSuccess) e = launch(mla_compact_move_kernel, dim3(1216), kThreads, p, stream);
+    if (e == cudaSuccess) e = launch(mla_compact_move_kernel, dim3(sms), kMoveThreads, p, stream, sizeof(MoveRing));
     return launch_status(e);
 }
 

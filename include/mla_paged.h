@@ -213,7 +213,7 @@ typedef struct {
     const int *refs;            /* (device) int32 [n_pages]: a page is in use where this is above 0 */
     int *page_table_out;        /* (device) int32 [B][columns]; may be page_table */
     int *refs_out;              /* (device) int32 [n_pages]; may be refs */
-    int *used;                  /* (device) int32 [1]: pages in use */
+    int *used;                  /* (device) int32 [1]: pages in use (-1: a copy did not arrive in time) */
 } mla_pages_compact_args;
 
 /* Move the pages in use to the pages 0 .. used - 1: those behind `used`, in ascending order, to the
