@@ -137,27 +137,37 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) mla_paged_append_kerne
     const int w = static_cast<int>(blockIdx.x) * (kThreads / 32) + static_cast<int>(threadIdx.x >> 5);
     const int n = w / units_per_token, part = w - n * units_per_token;
     const int b = blockIdx.y;
-    if (n >= a.tokens || (a.n_tokens && n >= a.n_tokens[b])) return;
+    if (n >= a.tokens) return;
+    const bool is_row = p.cache.pages && part == units_per_token - 1;
+    // (loads that wait for nothing, side by side)
+    const int n_tok = a.n_tokens ? a.n_tokens[b] : a.tokens;
+    const int pos = a.positions[static_cast<long long>(b) * a.tokens + n];
+    const int d = is_row ? a.d_pos[b] : 0;
+    if (n >= n_tok) return;
     const int half = a.rot_dim >> 1;
     const int u = lane & 7;
-    const int pos = a.positions[static_cast<long long>(b) * a.tokens + n];
     const bool rotated = 4 * u < half;                     // half is a multiple of 4: a unit whole or not at all
     int lo, hi;
     unit_offsets(u, half, kInterleaved, lo, hi);
-    if (p.cache.pages && part == units_per_token - 1) {
+    if (is_row) {
         // ---- the row
-        const int d = a.d_pos[b];
         const long long t = static_cast<long long>(d) + n;
-        if (d < 0 || t >= paged_rows(p.cache)) return;     // uniform over the warp, as the next
+        if (d < 0 || t >= paged_rows(p.cache)) return;     // uniform over the warp, as below
         const int page = page_of(p.cache, b, static_cast<int>(t));
-        if (page < 0) return;
-        uint8_t* row = row_in(p.cache, page, static_cast<int>(t));
         const uint4* c = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.c) + b * a.c_batch +
                                                         n * a.c_token) + 2 * lane;
         const uint4 v0 = c[0], v1 = c[1];
         uint4 k = make_uint4(0, 0, 0, 0);
         if (lane < 8)
             k = load_unit(static_cast<const uint16_t*>(a.k_rope) + b * a.k_rope_batch + n * a.k_rope_token, lo, hi);
+        uint4 g0 = make_uint4(0, 0, 0, 0), g1 = g0, gk = g0;
+        if (a.c_norm) {
+            g0 = static_cast<const uint4*>(a.c_norm)[2 * lane];
+            g1 = static_cast<const uint4*>(a.c_norm)[2 * lane + 1];
+        }
+        if (a.k_norm) gk = load_unit(static_cast<const uint16_t*>(a.k_norm), lo, hi);
+        if (page < 0) return;
+        uint8_t* row = row_in(p.cache, page, static_cast<int>(t));
         float sn0, cs0, cs[4], sn[4];
         pair_angle(pos, a.turns, half, a.amplitude, lane, sn0, cs0);
         unit_angles(u, sn0, cs0, cs, sn);
@@ -189,8 +199,6 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) mla_paged_append_kerne
             low *= 1.f / kDLatent;
             two_add(sum, low, a.eps);
             const float r = rsqrt_pair(sum, low);
-            const uint4* g = static_cast<const uint4*>(a.c_norm) + 2 * lane;
-            const uint4 g0 = g[0], g1 = g[1];
             float x[8];
             widen8(g0, x);
 #pragma unroll
@@ -214,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) mla_paged_append_kerne
         widen8(k, x);
         if (a.k_norm) {
             float g[8];
-            widen8(load_unit(static_cast<const uint16_t*>(a.k_norm), lo, hi), g);
+            widen8(gk, g);
             norm_unit(x, g, a.eps);
         }
         if (rotated) rotate_unit(x, kInterleaved, cs, sn);
@@ -328,8 +336,10 @@ __global__ void __launch_bounds__(kThreads) mla_paged_read_kernel(const __grid_c
     const int lane = threadIdx.x & 31;
     const int n = static_cast<int>(blockIdx.x) * (kThreads / 32) + static_cast<int>(threadIdx.x >> 5);
     const int b = blockIdx.y;
-    if (n >= p.a.rows || (p.a.n_rows && n >= p.a.n_rows[b])) return;
+    if (n >= p.a.rows) return;
+    const int n_rows = p.a.n_rows ? p.a.n_rows[b] : p.a.rows;
     const long long t = static_cast<long long>(p.a.first ? p.a.first[b] : 0) + n;
+    if (n >= n_rows) return;
     const int page = t >= 0 && t < paged_rows(p.cache) ? page_of(p.cache, b, static_cast<int>(t)) : -1;
     uint16_t* out = static_cast<uint16_t*>(p.a.out) + b * p.a.out_batch + n * p.a.out_row;
     uint32_t o[8], key = 0;
