@@ -15,6 +15,9 @@
 // Bound: bytes (128 in and 128 out per query head; 1152 in and 416 out per row).  Warps work
 // alone, as in mla_rope.cu: a warp takes up to 32 heads of one token, eight lanes a head, or
 // the token's row, of which a lane has 16 consecutive latent values: a block with its scale.
+// 4696 ragged tokens of 128 heads (161 MB): 32 us, 5.0 TB/s; the same loads and stores with nothing computed take 28.5.
+// Heads' arithmetic is on pairs of fp32 numbers, and the norm's sums and roots of a warp's 32 heads are one lane's each
+// (one number at a time, every lane a root per head: 38 us, issue slots half taken).
 #include <cmath>
 #include <cstdint>
 

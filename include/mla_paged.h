@@ -115,10 +115,10 @@ MLA_API int mla_paged_read(const mla_paged_read_args *args, void *stream);
  *     s_t = (q_lat . c_t + q_rope . k_rope_t) * scale
  *     lse = ln sum_t exp(s_t),     out = sum_t exp(s_t - lse) c_t
  *
- * q_lat enters the product in f16, scaled by a power of two per query row (values far below the
- * row's largest lose bits: 2^-25 of the largest at most); latents are exact, key values and
- * q_rope are bf16.  Probabilities enter the second product in f16 (2^-12 each); sums and
- * statistics are fp32.
+ * q_lat enters the product in f16 times a power of two per query row, set by the largest of
+ * |q_lat| and |q_rope| / kv_scale: values down to 2^-31 of it are exact, smaller ones off by at
+ * most 2^-39 of it.  Latents are exact; key values and q_rope are bf16.  Probabilities enter the
+ * second product in f16 (2^-12 each); sums and statistics are fp32.
  *
  * What a token does not attend does not reach its result, whatever the bytes are.  An attended
  * row with a NaN, or whose score is NaN or +infinity, makes the whole result of the (token,
