@@ -25,6 +25,10 @@ def random_pages(n_pages, page_rows, g, kv_scale=1.0, spread=1.0):
     return raw.view(n_pages, page_rows, 416)
 
 
+# 16 query rows per token are taken by one kernel, 48 by the other
+BOTH = pytest.mark.parametrize("H", [16, 48])
+
+
 class Case:
     """Requests over pages in random order; everything that no token attends is NaN."""
 
@@ -119,8 +123,9 @@ def test_attention(kw, fp32):
     dict(d_pos=[640], Q=64, H=16, window=30, sink=1, page_rows=128), dict(d_pos=[1279], window=256, sink=128, page_rows=128),
     dict(d_pos=[3000], window=2 ** 31 - 1, sink=2 ** 31 - 1), dict(d_pos=[500], window=3, sink=2 ** 31 - 1),
 ], ids=str)
-def test_window(kw):
-    c = Case(**kw).on_gpu()
+@BOTH
+def test_window(kw, H):
+    c = Case(**{"H": H, **kw}).on_gpu()
     c.forward()
     c.check()
 
@@ -131,14 +136,16 @@ def test_window(kw):
     dict(d_pos=[400], window=50, sink=20, gone=[(0, 1), (0, 24)]),
     dict(d_pos=[256 + 127], page_rows=128, gone=[(0, 1)]),
 ], ids=str)
-def test_rows_without_pages(kw):
-    c = Case(**kw).on_gpu()
+@BOTH
+def test_rows_without_pages(kw, H):
+    c = Case(**{"H": H, **kw}).on_gpu()
     c.forward()
     c.check()
 
 
-def test_rows_behind_the_table():
-    c = Case([47], page_rows=16)
+@BOTH
+def test_rows_behind_the_table(H):
+    c = Case([47], H=H, page_rows=16)
     c.table[0][3] = -1                # rows 48 .. 63 have no page, and the table ends there
     want = c.expected()
     c.d_pos = [1000]
@@ -148,8 +155,9 @@ def test_rows_behind_the_table():
 
 
 @pytest.mark.parametrize("what", ["scale", "key"])
-def test_nan_in_an_attended_row(what):
-    c = Case([300, 200], Q=2, H=16)
+@BOTH
+def test_nan_in_an_attended_row(what, H):
+    c = Case([300, 200], Q=2, H=H)
     page, slot = c.table[0][300 // 16], 300 % 16      # the first token's own row
     if what == "scale":
         c.pages[page, slot, 256 + 5] = 0x7f
@@ -162,8 +170,9 @@ def test_nan_in_an_attended_row(what):
     assert bool(c.lse[1].isfinite().all()) and bool(c.out[1].isfinite().all())
 
 
-def test_nan_queries_stay_in_their_rows():
-    c = Case([300], Q=2, H=16)
+@BOTH
+def test_nan_queries_stay_in_their_rows(H):
+    c = Case([300], Q=2, H=H)
     c.q[0, 0, 3, 17] = math.nan
     c.q[0, 1, 5, 570] = math.inf
     want = c.expected()
@@ -173,14 +182,15 @@ def test_nan_queries_stay_in_their_rows():
     for i, h in ((0, 3), (1, 5)):
         assert bool(c.lse[0, i, h].isnan()) or bool(c.lse[0, i, h] == math.inf)
     for (_, i), (o, l, tol_o, tol_l) in want.items():
-        ok = torch.tensor([(i, h) not in ((0, 3), (1, 5)) for h in range(16)])
+        ok = torch.tensor([(i, h) not in ((0, 3), (1, 5)) for h in range(H)])
         assert bool(((c.out[0, i].cpu().double() - o).abs() <= tol_o)[ok].all())
 
 
 @pytest.mark.parametrize("gain", [1e-30, 1e-4, 300.0, 1e30])
-def test_queries_of_any_size(gain):
+@BOTH
+def test_queries_of_any_size(gain, H):
     """A query's size times the scale is what counts: far from f16's range, the same result."""
-    c = Case([400], Q=2, H=16, gain=gain, scale=576 ** -0.5 / gain * 1.0)
+    c = Case([400], Q=2, H=H, gain=gain, scale=576 ** -0.5 / gain * 1.0)
     if not c.scale < 2.0 ** 60:
         c.scale = 2.0 ** 59
     c.on_gpu()
@@ -188,8 +198,9 @@ def test_queries_of_any_size(gain):
     c.check()
 
 
-def test_small_query_values_beside_large_ones():
-    c = Case([200], Q=1, H=16)
+@BOTH
+def test_small_query_values_beside_large_ones(H):
+    c = Case([200], Q=1, H=H)
     c.q[..., 0] *= 2.0 ** 20          # the others still count, exactly
     c.scale = 2.0 ** -22
     c.on_gpu()
@@ -197,8 +208,9 @@ def test_small_query_values_beside_large_ones():
     c.check()
 
 
-def test_zero_queries_average_the_rows():
-    c = Case([999], H=3, fp32=True)
+@BOTH
+def test_zero_queries_average_the_rows(H):
+    c = Case([999], H=H - 13, fp32=True)
     c.q.zero_()
     c.on_gpu()
     c.forward()
@@ -206,9 +218,10 @@ def test_zero_queries_average_the_rows():
     assert float((c.lse - math.log(1000)).abs().max()) <= 4 * ref.F32 * math.log(1000) + 2.0 ** -21
 
 
-def test_layers_of_one_pool():
+@BOTH
+def test_layers_of_one_pool(H):
     """Pages with a stride: one layer of a pool that holds several."""
-    c = Case([300, 77], Q=2, H=16, page_rows=32)
+    c = Case([300, 77], Q=2, H=H, page_rows=32)
     c.on_gpu()
     pool = torch.full((c.pages.shape[0], 3, 32, 416), NAN_ROW, dtype=torch.uint8, device="cuda")
     pool[:, 1] = c.t_pages
@@ -217,9 +230,10 @@ def test_layers_of_one_pool():
     c.check()
 
 
-def test_shared_pages():
+@BOTH
+def test_shared_pages(H):
     """Two requests over the same pages, and one that goes on alone behind them."""
-    c = Case([95, 95, 40], Q=2, H=16, page_rows=16)
+    c = Case([95, 95, 40], Q=2, H=H, page_rows=16)
     for k in range(4):
         c.table[1][k] = c.table[0][k]
     c.pages = torch.where((c.pages == NAN_ROW).all(-1, keepdim=True), torch.zeros(1, dtype=torch.uint8), c.pages)
@@ -247,9 +261,10 @@ def test_long_and_many(kw):
     assert torch.equal(c.lse, lse) and torch.equal(c.out, out)
 
 
-def test_pages_past_four_gigabytes():
+@BOTH
+def test_pages_past_four_gigabytes(H):
     page_rows, n_pages = 1024, 11000  # 4.7 GB
-    c = Case([2500], Q=2, H=16, page_rows=page_rows, spare=0)
+    c = Case([2500], Q=2, H=H, page_rows=page_rows, spare=0)
     pages = torch.zeros(n_pages, page_rows, 416, dtype=torch.uint8, device="cuda")
     to = {p: n_pages - 1 - 40 * k for k, p in enumerate(c.table[0][:3])}
     for p, far in to.items():
@@ -262,8 +277,9 @@ def test_pages_past_four_gigabytes():
     c.check(want)
 
 
-def test_replayed_graph_follows_lengths_and_tables():
-    a, b = Case([300, 40], Q=2, H=16, seed=1), Case([123, 290], Q=2, H=16, seed=2)
+@BOTH
+def test_replayed_graph_follows_lengths_and_tables(H):
+    a, b = Case([300, 40], Q=2, H=H, seed=1), Case([123, 290], Q=2, H=H, seed=2)
     a.on_gpu()
     b.on_gpu()
     n = max(a.pages.shape[0], b.pages.shape[0])
@@ -271,7 +287,7 @@ def test_replayed_graph_follows_lengths_and_tables():
     pages = torch.zeros(n, 16, 416, dtype=torch.uint8, device="cuda")
     table, d, q = torch.full((2, columns), -1, **I32), torch.zeros(2, **I32), torch.zeros_like(a.t_q)
     out, lse = torch.zeros_like(a.out), torch.zeros_like(a.lse)
-    plan = mla.paged_plan(batch=2, tokens=2, heads=16, scale=a.scale, pdl=True)
+    plan = mla.paged_plan(batch=2, tokens=2, heads=H, scale=a.scale, pdl=True)
     scratch = mla.paged_alloc_scratch(plan)
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
@@ -304,9 +320,10 @@ def test_two_streams_with_scratch_of_their_own():
     b.check()
 
 
-def test_a_wait_that_runs_out_is_reported():
-    c = Case([300], H=16).on_gpu()
-    plan = mla.paged_plan(batch=1, tokens=1, heads=16, scale=c.scale, stall_test=True)
+@BOTH
+def test_a_wait_that_runs_out_is_reported(H):
+    c = Case([300], H=H).on_gpu()
+    plan = mla.paged_plan(batch=1, tokens=1, heads=H, scale=c.scale, stall_test=True)
     _, scratch = c.forward(plan=plan)
     torch.cuda.synchronize()
     assert mla.status_word(plan, scratch) == mla.EDEVICE
