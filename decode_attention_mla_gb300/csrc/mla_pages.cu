@@ -643,6 +643,12 @@ __global__ void __launch_bounds__(kMoveThreads) mla_compact_move_kernel(const __
 
 bool off(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to != 0; }
 
+// Outputs may be their inputs, but not lie across them.
+bool across(const void* in, const void* out, size_t ints) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(in), b = reinterpret_cast<uintptr_t>(out);
+    return a != b && (a < b ? b - a : a - b) < 4 * ints;
+}
+
 bool sizes_ok(int batch, int columns, int n_pages) {
     return batch >= 1 && batch <= 4096 && columns >= 1 && n_pages >= 1 && n_pages <= (1 << 30) &&
            static_cast<long long>(batch) * columns < (1ll << 30);
@@ -740,6 +746,9 @@ int mla_pages_fork(const mla_pages_fork_args* args, void* scratch, size_t scratc
     if (off(args->page_table, 4) || off(args->d_pos, 4) || off(args->parent, 4) || off(args->rows, 4) ||
         off(args->page_table_out, 4) || off(args->d_pos_out, 4) || off(args->refs, 4) || off(args->missing, 4))
         return MLA_EALIGN;
+    if (across(args->page_table, args->page_table_out, static_cast<size_t>(args->batch) * args->columns) ||
+        across(args->d_pos, args->d_pos_out, args->batch))
+        return MLA_EINVAL;
     if (!scratch || off(scratch, 256) || scratch_bytes < fork_bytes(args->batch, args->columns, args->n_pages))
         return MLA_ESCRATCH;
     ForkParams p{};
@@ -774,6 +783,9 @@ int mla_pages_compact(const mla_pages_compact_args* args, void* scratch, size_t 
     if (off(args->page_table, 4) || off(args->refs, 4) || off(args->page_table_out, 4) || off(args->refs_out, 4) ||
         off(args->used, 4))
         return MLA_EALIGN;
+    if (across(args->page_table, args->page_table_out, static_cast<size_t>(args->batch) * args->columns) ||
+        across(args->refs, args->refs_out, args->n_pages))
+        return MLA_EINVAL;
     if (!scratch || off(scratch, 256) || scratch_bytes < compact_bytes(args->n_pages)) return MLA_ESCRATCH;
     CompactParams p{};
     p.a = *args;

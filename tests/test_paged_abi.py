@@ -131,7 +131,7 @@ BAD_POOL = [
     (dict(missing=None), mla.EINVAL), (dict(reserve=-1), mla.EINVAL), (dict(window=-1), mla.EINVAL),
     (dict(sink=-1), mla.EINVAL), (dict(parent=PTR + 2), mla.EALIGN), (dict(rows=PTR + 2), mla.EALIGN),
     (dict(refs=PTR + 2), mla.EALIGN), (dict(scratch=None), mla.ESCRATCH), (dict(scratch=PTR + 4), mla.ESCRATCH),
-    (dict(nbytes=100), mla.ESCRATCH),
+    (dict(nbytes=100), mla.ESCRATCH), (dict(page_table_out=PTR + 56), mla.EINVAL), (dict(d_pos_out=PTR - 8), mla.EINVAL),
 ])
 def test_fork_refusals(kw, status):
     kw = dict(kw)
@@ -143,7 +143,7 @@ def test_fork_refusals(kw, status):
 @pytest.mark.parametrize("kw,status", BAD_POOL + [
     (dict(refs=None), mla.EINVAL), (dict(refs_out=None), mla.EINVAL), (dict(used=None), mla.EINVAL),
     (dict(refs=PTR + 2), mla.EALIGN), (dict(used=PTR + 2), mla.EALIGN), (dict(scratch=None), mla.ESCRATCH),
-    (dict(nbytes=100), mla.ESCRATCH),
+    (dict(nbytes=100), mla.ESCRATCH), (dict(page_table_out=PTR - 56), mla.EINVAL), (dict(refs_out=PTR + 36), mla.EINVAL),
 ])
 def test_compact_refusals(kw, status):
     kw = dict(kw)
