@@ -96,7 +96,13 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
     return v + before;
 }
 
-// Hand out pages (one block).  All of its threads have passed a barrier behind the counts.
+// Hand out pages (one block).  All of its threads have passed a barrier behind the counts, which other blocks have made
+// (kShared: this one, in its shared memory).
+template <bool kShared>
+__device__ __forceinline__ int counted(const int* at) {
+    return kShared ? *at : __ldcg(at);
+}
+template <bool kShared>
 __device__ void fork_place(const ForkParams& p) {
     __shared__ int sums[32];
     const int batch = p.a.batch, columns = p.a.columns;
@@ -107,15 +113,15 @@ __device__ void fork_place(const ForkParams& p) {
         int need = 0, from = -1;
         if (b < batch) {
             int parent;
-            const int n = __ldcg(p.rows + b);
+            const int n = counted<kShared>(p.rows + b);
             fork_rows(p, b, parent);
             const int end = parent < 0 ? 0 : fork_end(p, n);
             const int part = n & ((1 << p.shift) - 1), last = n >> p.shift;
             need = max(0, end - last);
             if (part) {
-                const int page = __ldcg(p.table + static_cast<long long>(b) * columns + last);
+                const int page = counted<kShared>(p.table + static_cast<long long>(b) * columns + last);
                 if (page >= 0) {
-                    if (__ldcg(p.a.refs + page) > 0 || __ldcg(p.keeper + page) != b)
+                    if (counted<kShared>(p.a.refs + page) > 0 || counted<kShared>(p.keeper + page) != b)
                         from = page;
                     else
                         --need;                            // it stays
@@ -131,9 +137,9 @@ __device__ void fork_place(const ForkParams& p) {
     __syncthreads();
     // ---- last pages that stay
     for (int b = threadIdx.x; b < batch; b += kPlaceThreads) {
-        const int n = __ldcg(p.rows + b), part = n & ((1 << p.shift) - 1);
+        const int n = counted<kShared>(p.rows + b), part = n & ((1 << p.shift) - 1);
         if (part == 0 || p.src[b] >= 0) continue;
-        const int page = __ldcg(p.table + static_cast<long long>(b) * columns + (n >> p.shift));
+        const int page = counted<kShared>(p.table + static_cast<long long>(b) * columns + (n >> p.shift));
         if (page >= 0) p.a.refs[page] = 1;
     }
     __syncthreads();
@@ -145,7 +151,7 @@ __device__ void fork_place(const ForkParams& p) {
         int mine = 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            is[k] = i + k < p.a.n_pages && __ldcg(p.a.refs + i + k) == 0;
+            is[k] = i + k < p.a.n_pages && counted<kShared>(p.a.refs + i + k) == 0;
             mine += is[k];
         }
         int total;
@@ -163,14 +169,14 @@ __device__ void fork_place(const ForkParams& p) {
     // ---- and who gets them
     for (int b = threadIdx.x; b < batch; b += kPlaceThreads) {
         int parent;
-        const int n = __ldcg(p.rows + b);
+        const int n = counted<kShared>(p.rows + b);
         fork_rows(p, b, parent);
         const int end = parent < 0 ? 0 : fork_end(p, n);
         const int part = n & ((1 << p.shift) - 1), last = n >> p.shift;
         int* row = p.table + static_cast<long long>(b) * columns;
         int at = p.first[b], to = -1, rows = n;
         for (int c = last; c < end; ++c) {
-            if (c == last && part && p.src[b] < 0 && __ldcg(row + c) >= 0) continue;   // it stays
+            if (c == last && part && p.src[b] < 0 && counted<kShared>(row + c) >= 0) continue;   // it stays
             const int page = at < have ? p.free[at] : -1;
             ++at;
             if (page >= 0) p.a.refs[page] = 1;
@@ -222,7 +228,7 @@ __global__ void __launch_bounds__(kPlaceThreads) mla_fork_count_kernel(const __g
     __syncthreads();
     if (!is_last) return;
     __threadfence();
-    fork_place(p);
+    fork_place<false>(p);
 }
 
 // Eight loads a thread on their way; thread `at` of `threads`.
@@ -259,29 +265,41 @@ __global__ void __launch_bounds__(kThreads) mla_fork_write_kernel(const __grid_c
     fork_copy(p, b, threadIdx.x, kThreads);
 }
 
-// All of it in one block, one launch for three.
-__global__ void __launch_bounds__(kPlaceThreads) mla_fork_small_kernel(const __grid_constant__ ForkParams p) {
-    grid_dependency_wait();
-    allow_dependent_launch();
+// All of it in one block, one launch for three, what is counted in shared memory.
+constexpr int kSmallPages = 1024, kSmallEntries = 1024;
+__global__ void __launch_bounds__(kPlaceThreads) mla_fork_small_kernel(const __grid_constant__ ForkParams args) {
+    __shared__ int refs[kSmallPages], keeper[kSmallPages], table[kSmallEntries], taken[kSmallPages];
+    __shared__ int rows[kSmallEntries], first[kSmallEntries], src[kSmallEntries], dst[kSmallEntries];
+    ForkParams p = args;
+    p.a.refs = refs;
+    p.keeper = keeper;
+    p.table = table;
+    p.free = taken;
+    p.rows = rows;
+    p.first = first;
+    p.src = src;
+    p.dst = dst;
     const int entries = p.a.batch * p.a.columns;
     for (int i = threadIdx.x; i < p.a.n_pages; i += kPlaceThreads) {
-        p.a.refs[i] = 0;
-        p.keeper[i] = kNobody;
+        refs[i] = 0;
+        keeper[i] = kNobody;
     }
     __syncthreads();
+    grid_dependency_wait();
+    allow_dependent_launch();
     for (int e = threadIdx.x; e < entries; e += kPlaceThreads) {
         const int b = e / p.a.columns, c = e - b * p.a.columns;
         int parent;
         const int n = fork_rows(p, b, parent);
         fork_entry(p, b, c, parent, n);
-        if (c == 0) p.rows[b] = n;
+        if (c == 0) rows[b] = n;
     }
-    __threadfence();
     __syncthreads();
-    fork_place(p);
+    fork_place<true>(p);
     __syncthreads();
-    for (int e = threadIdx.x; e < entries; e += kPlaceThreads) p.a.page_table_out[e] = p.table[e];
-    for (int b = threadIdx.x; b < p.a.batch; b += kPlaceThreads) p.a.d_pos_out[b] = p.rows[b];
+    for (int e = threadIdx.x; e < entries; e += kPlaceThreads) p.a.page_table_out[e] = table[e];
+    for (int i = threadIdx.x; i < p.a.n_pages; i += kPlaceThreads) args.a.refs[i] = refs[i];
+    for (int b = threadIdx.x; b < p.a.batch; b += kPlaceThreads) p.a.d_pos_out[b] = rows[b];
     // copies, kThreads threads a request
     for (int b = threadIdx.x / kThreads; b < p.a.batch; b += kPlaceThreads / kThreads)
         fork_copy(p, b, threadIdx.x % kThreads, kThreads);
@@ -677,7 +695,7 @@ size_t compact_bytes(int n_pages) {
 // each request with a copy of 64 rows of 416 bytes): 6.9 for 9.0 (1 x 40, 512), 10.5 for 11.7 (4 x 40, 512); but 13.9 for
 // 11.6 (16 x 256, 4096; copies of 16 rows) and 19.1 for 13.2 (8 x 1000, 8192).
 bool fork_is_small(const mla_pages_fork_args* a) {
-    return a->n_pages <= 1024 && static_cast<long long>(a->batch) * a->columns <= 1024 &&
+    return a->n_pages <= kSmallPages && static_cast<long long>(a->batch) * a->columns <= kSmallEntries &&
            static_cast<long long>(a->batch) * a->page_rows * a->row_bytes <= 128 << 10;
 }
 
