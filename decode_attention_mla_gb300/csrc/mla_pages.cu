@@ -7,7 +7,7 @@
 // minima of integers: the same in any order), by whose last block the pages are handed
 // out (one block: its scan of refs ends as soon as it has found enough free pages);
 // then the tables written and the shared last pages copied.  The new table waits in
-// scratch, since a request's row may be another's parent.  A small fork is one block's.
+// scratch, since a request's row may be another's parent.  Smaller forks are one block's.
 //
 // compact.  The k-th page in use behind the front goes to the k-th hole in it.  Pools of up to
 // kBitsPages pages take one launch: every block counts all of them itself, which costs it
@@ -16,7 +16,7 @@
 // per 4096 pages; lists of holes and moving pages; moves, tables and references.
 //
 // Bound: bytes (tables and references, and the rows that are copied), below that the
-// launches, each a chain of a few loads.  256 requests with 65300 entries, a pool of 65536: 14.4 us.
+// launches, each a chain of a few loads.  256 requests with 65300 entries, a pool of 65536: 13.8 us.
 // 7700 pages of 26 KB moved by bulk copies: 74 us, 5.6 TB/s (by loads and stores of a thread's own, 82).
 #include <algorithm>
 #include <atomic>
@@ -31,6 +31,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kPlaceThreads = 1024;
+constexpr int kMostRequests = 4096;
 constexpr int kChunk = 4096;                               // pages per block of the counts
 constexpr int kNobody = 0x7fffffff;
 
@@ -43,7 +44,6 @@ struct ForkParams {
     int* table;                                            // [B][columns] the new table
     int* keeper;                                           // [n_pages] first request that ends in the page
     int* rows;                                             // [B] n
-    int* first;                                            // [B] pages taken by the requests before
     int* src;                                              // [B] page to copy, or -1
     int* dst;                                              // [B]
     int* free;                                             // pages taken, in order
@@ -105,43 +105,41 @@ __device__ __forceinline__ int counted(const int* at) {
 template <bool kShared>
 __device__ void fork_place(const ForkParams& p) {
     __shared__ int sums[32];
-    const int batch = p.a.batch, columns = p.a.columns;
+    struct Request {
+        int n, end;                                        // rows, column behind those reserved
+        int page;                                          // that n ends in, or -1
+        bool copied;                                       // it is not this request's to keep
+        int at;                                            // its first page among those taken
+    } mine[kMostRequests / kPlaceThreads];
+    const int batch = p.a.batch, columns = p.a.columns, rows_mask = (1 << p.shift) - 1;
     // ---- what each request needs: a copy of its last page, pages behind it
     int needed = 0;
-    for (int b0 = 0; b0 < batch; b0 += kPlaceThreads) {
-        const int b = b0 + threadIdx.x;
-        int need = 0, from = -1;
+#pragma unroll 1
+    for (int q = 0; q * kPlaceThreads < batch; ++q) {
+        const int b = q * kPlaceThreads + threadIdx.x;
+        Request r{0, 0, -1, false, 0};
         if (b < batch) {
             int parent;
-            const int n = counted<kShared>(p.rows + b);
+            r.n = counted<kShared>(p.rows + b);
             fork_rows(p, b, parent);
-            const int end = parent < 0 ? 0 : fork_end(p, n);
-            const int part = n & ((1 << p.shift) - 1), last = n >> p.shift;
-            need = max(0, end - last);
-            if (part) {
-                const int page = counted<kShared>(p.table + static_cast<long long>(b) * columns + last);
-                if (page >= 0) {
-                    if (counted<kShared>(p.a.refs + page) > 0 || counted<kShared>(p.keeper + page) != b)
-                        from = page;
-                    else
-                        --need;                            // it stays
-                }
+            if (parent >= 0) r.end = fork_end(p, r.n);
+            if (r.n & rows_mask) {
+                r.page = counted<kShared>(p.table + static_cast<long long>(b) * columns + (r.n >> p.shift));
+                if (r.page >= 0)
+                    r.copied = counted<kShared>(p.a.refs + r.page) > 0 || counted<kShared>(p.keeper + r.page) != b;
             }
-            p.src[b] = from;
+            p.src[b] = r.copied ? r.page : -1;
         }
+        const int need = max(0, r.end - (r.n >> p.shift)) - (r.page >= 0 && !r.copied);
         int total;
-        const int incl = block_scan(need, sums, total);
-        if (b < batch) p.first[b] = needed + incl - need;
+        r.at = needed + block_scan(need, sums, total) - need;
         needed += total;
+        mine[q] = r;
     }
-    __syncthreads();
-    // ---- last pages that stay
-    for (int b = threadIdx.x; b < batch; b += kPlaceThreads) {
-        const int n = counted<kShared>(p.rows + b), part = n & ((1 << p.shift) - 1);
-        if (part == 0 || p.src[b] >= 0) continue;
-        const int page = counted<kShared>(p.table + static_cast<long long>(b) * columns + (n >> p.shift));
-        if (page >= 0) p.a.refs[page] = 1;
-    }
+    // ---- last pages that stay  (all have looked at the references)
+#pragma unroll 1
+    for (int q = 0; q * kPlaceThreads + static_cast<int>(threadIdx.x) < batch; ++q)
+        if (mine[q].page >= 0 && !mine[q].copied) p.a.refs[mine[q].page] = 1;
     __syncthreads();
     // ---- the first free pages
     int found = 0;
@@ -167,23 +165,21 @@ __device__ void fork_place(const ForkParams& p) {
     const int have = min(found, needed);
     __syncthreads();
     // ---- and who gets them
-    for (int b = threadIdx.x; b < batch; b += kPlaceThreads) {
-        int parent;
-        const int n = counted<kShared>(p.rows + b);
-        fork_rows(p, b, parent);
-        const int end = parent < 0 ? 0 : fork_end(p, n);
-        const int part = n & ((1 << p.shift) - 1), last = n >> p.shift;
+#pragma unroll 1
+    for (int q = 0; q * kPlaceThreads + static_cast<int>(threadIdx.x) < batch; ++q) {
+        const int b = q * kPlaceThreads + threadIdx.x;
+        const Request r = mine[q];
+        const int last = r.n >> p.shift;
         int* row = p.table + static_cast<long long>(b) * columns;
-        int at = p.first[b], to = -1, rows = n;
-        for (int c = last; c < end; ++c) {
-            if (c == last && part && p.src[b] < 0 && counted<kShared>(row + c) >= 0) continue;   // it stays
+        int at = r.at, to = -1, rows = r.n;
+        for (int c = last + (r.page >= 0 && !r.copied); c < r.end; ++c) {
             const int page = at < have ? p.free[at] : -1;
             ++at;
             if (page >= 0) p.a.refs[page] = 1;
             row[c] = page;
-            if (c == last && p.src[b] >= 0) {
+            if (c == last && r.copied) {
                 to = page;
-                if (page < 0) rows = n - part;
+                if (page < 0) rows = r.n & ~rows_mask;
             }
         }
         p.dst[b] = to;
@@ -192,21 +188,21 @@ __device__ void fork_place(const ForkParams& p) {
     if (threadIdx.x == 0) *p.a.missing = needed - have;
 }
 
-// Entry c of request b, which has n rows: into the new table, and counted.
-__device__ __forceinline__ void fork_entry(const ForkParams& p, int b, int c, int parent, int n) {
-    int page = -1;
+// Entry c of request b, which has n rows of its parent's: the page, or -1.
+__device__ __forceinline__ int fork_page(const ForkParams& p, int c, int parent, int n) {
     const long long t0 = static_cast<long long>(c) << p.shift, t1 = t0 + (1 << p.shift);
-    if (t0 < n) {
-        page = p.a.page_table[static_cast<long long>(parent) * p.a.columns + c];
-        if (page < 0 || page >= p.a.n_pages) page = -1;
-        // (no later token attends rows up to n - window)
-        if (p.a.window > 0 && t0 >= p.a.sink && t1 <= static_cast<long long>(n) + 1 - p.a.window) page = -1;
-        if (page >= 0) {
-            if (t1 <= n)
-                atomicAdd(p.a.refs + page, 1);
-            else
-                atomicMin(p.keeper + page, b);
-        }
+    // (no later token attends rows up to n - window)
+    if (t0 >= n || (p.a.window > 0 && t0 >= p.a.sink && t1 <= static_cast<long long>(n) + 1 - p.a.window)) return -1;
+    const int page = p.a.page_table[static_cast<long long>(parent) * p.a.columns + c];
+    return page >= p.a.n_pages ? -1 : max(page, -1);
+}
+// ... into the new table, and counted.
+__device__ __forceinline__ void fork_entry(const ForkParams& p, int b, int c, int page, int n) {
+    if (page >= 0) {
+        if ((static_cast<long long>(c) + 1) << p.shift <= n)
+            atomicAdd(p.a.refs + page, 1);
+        else
+            atomicMin(p.keeper + page, b);
     }
     p.table[static_cast<long long>(b) * p.a.columns + c] = page;
 }
@@ -220,7 +216,7 @@ __global__ void __launch_bounds__(kPlaceThreads) mla_fork_count_kernel(const __g
     int parent;
     const int n = fork_rows(p, b, parent);
     for (int c = blockIdx.x * kPlaceThreads + threadIdx.x; c < p.a.columns; c += gridDim.x * kPlaceThreads)
-        fork_entry(p, b, c, parent, n);
+        fork_entry(p, b, c, fork_page(p, c, parent, n), n);
     if (blockIdx.x == 0 && threadIdx.x == 0) p.rows[b] = n;
     __threadfence();
     __syncthreads();
@@ -265,44 +261,69 @@ __global__ void __launch_bounds__(kThreads) mla_fork_write_kernel(const __grid_c
     fork_copy(p, b, threadIdx.x, kThreads);
 }
 
-// All of it in one block, one launch for three, what is counted in shared memory.
-constexpr int kSmallPages = 1024, kSmallEntries = 1024;
-__global__ void __launch_bounds__(kPlaceThreads) mla_fork_small_kernel(const __grid_constant__ ForkParams args) {
-    __shared__ int refs[kSmallPages], keeper[kSmallPages], table[kSmallEntries], taken[kSmallPages];
-    __shared__ int rows[kSmallEntries], first[kSmallEntries], src[kSmallEntries], dst[kSmallEntries];
+// All of it in one block, counted in shared memory, but for large copies, which take a second launch.  Measured
+// against the three launches, us (requests x columns, pages of the pool): 4.4 and 7.8 (1 x 40, 512), 8.4 and 10.5 (32 x 64,
+// 2048), 9.6 and 13.1 (2 x 4096, 8192), 11.2 and 14.1 (4 x 3000, 12000); but 12.1 and 9.7 (200 x 100, 1000).
+constexpr int kBlockBytes = 192 << 10, kBlockEntries = 16384, kOwnCopies = 128 << 10;
+long long fork_block_bytes(const mla_pages_fork_args& a) {
+    return 12ll * a.n_pages + 4ll * a.batch * a.columns + 12ll * a.batch;
+}
+template <bool kCopies>
+__global__ void __launch_bounds__(kPlaceThreads) mla_fork_block_kernel(const __grid_constant__ ForkParams args) {
+    extern __shared__ __align__(16) int smem[];
+    constexpr int kAhead = 4;
+    const int entries = args.a.batch * args.a.columns, batch = args.a.batch, columns = args.a.columns;
     ForkParams p = args;
-    p.a.refs = refs;
-    p.keeper = keeper;
-    p.table = table;
-    p.free = taken;
-    p.rows = rows;
-    p.first = first;
-    p.src = src;
-    p.dst = dst;
-    const int entries = p.a.batch * p.a.columns;
+    p.a.refs = smem;
+    p.keeper = p.a.refs + p.a.n_pages;
+    p.free = p.keeper + p.a.n_pages;
+    p.table = p.free + p.a.n_pages;
+    p.rows = p.table + entries;
+    p.src = p.rows + batch;
+    p.dst = p.src + batch;
     for (int i = threadIdx.x; i < p.a.n_pages; i += kPlaceThreads) {
-        refs[i] = 0;
-        keeper[i] = kNobody;
+        p.a.refs[i] = 0;
+        p.keeper[i] = kNobody;
     }
-    __syncthreads();
     grid_dependency_wait();
     allow_dependent_launch();
-    for (int e = threadIdx.x; e < entries; e += kPlaceThreads) {
-        const int b = e / p.a.columns, c = e - b * p.a.columns;
-        int parent;
-        const int n = fork_rows(p, b, parent);
-        fork_entry(p, b, c, parent, n);
-        if (c == 0) rows[b] = n;
+    for (int b = threadIdx.x; b < batch; b += kPlaceThreads) p.rows[b] = fork_rows(p, b, p.dst[b]);   // (dst: the parent, so far)
+    __syncthreads();
+    for (int e0 = threadIdx.x; e0 < entries; e0 += kAhead * kPlaceThreads) {
+        int page[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int e = e0 + k * kPlaceThreads, b = e / columns;
+            page[k] = e < entries ? fork_page(p, e - b * columns, p.dst[b], p.rows[b]) : -1;
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int e = e0 + k * kPlaceThreads, b = e / columns;
+            if (e < entries) fork_entry(p, b, e - b * columns, page[k], p.rows[b]);
+        }
     }
     __syncthreads();
     fork_place<true>(p);
     __syncthreads();
-    for (int e = threadIdx.x; e < entries; e += kPlaceThreads) p.a.page_table_out[e] = table[e];
-    for (int i = threadIdx.x; i < p.a.n_pages; i += kPlaceThreads) args.a.refs[i] = refs[i];
-    for (int b = threadIdx.x; b < p.a.batch; b += kPlaceThreads) p.a.d_pos_out[b] = rows[b];
+    for (int e = threadIdx.x; e < entries; e += kPlaceThreads) p.a.page_table_out[e] = p.table[e];
+    for (int i = threadIdx.x; i < p.a.n_pages; i += kPlaceThreads) args.a.refs[i] = p.a.refs[i];
+    for (int b = threadIdx.x; b < batch; b += kPlaceThreads) {
+        p.a.d_pos_out[b] = p.rows[b];
+        if (!kCopies) {
+            args.rows[b] = p.rows[b];
+            args.src[b] = p.src[b];
+            args.dst[b] = p.dst[b];
+        }
+    }
     // copies, kThreads threads a request
-    for (int b = threadIdx.x / kThreads; b < p.a.batch; b += kPlaceThreads / kThreads)
-        fork_copy(p, b, threadIdx.x % kThreads, kThreads);
+    if (kCopies)
+        for (int b = threadIdx.x / kThreads; b < batch; b += kPlaceThreads / kThreads)
+            fork_copy(p, b, threadIdx.x % kThreads, kThreads);
+}
+__global__ void __launch_bounds__(kThreads) mla_fork_copy_kernel(const __grid_constant__ ForkParams p) {
+    grid_dependency_wait();
+    allow_dependent_launch();
+    fork_copy(p, blockIdx.x, threadIdx.x, kThreads);
 }
 
 // ---- compact --------------------------------------------------------------------
@@ -668,7 +689,7 @@ bool across(const void* in, const void* out, size_t ints) {
 }
 
 bool sizes_ok(int batch, int columns, int n_pages) {
-    return batch >= 1 && batch <= 4096 && columns >= 1 && n_pages >= 1 && n_pages <= (1 << 30) &&
+    return batch >= 1 && batch <= kMostRequests && columns >= 1 && n_pages >= 1 && n_pages <= (1 << 30) &&
            static_cast<long long>(batch) * columns < (1ll << 30);
 }
 
@@ -684,19 +705,11 @@ int check(const void* pages, long long page_stride, int n_pages, int page_rows, 
 // Scratch: fork's and compact's arrays, whichever are more.
 size_t fork_bytes(int batch, int columns, int n_pages) {
     const size_t entries = static_cast<size_t>(batch) * columns;
-    return 256 + up256(4 * entries) + 2 * up256(4 * static_cast<size_t>(n_pages)) + 4 * up256(4 * static_cast<size_t>(batch));
+    return 256 + up256(4 * entries) + 2 * up256(4 * static_cast<size_t>(n_pages)) + 3 * up256(4 * static_cast<size_t>(batch));
 }
 size_t compact_bytes(int n_pages) {
     const size_t n = static_cast<size_t>(n_pages);
     return 256 + up256(4 * ((n + kChunk - 1) / kChunk)) + 4 * up256(4 * n);
-}
-
-// One block does all of a small fork, in one launch for three.  Measured, us (requests x pages named, pages of the pool;
-// each request with a copy of 64 rows of 416 bytes): 6.9 for 9.0 (1 x 40, 512), 10.5 for 11.7 (4 x 40, 512); but 13.9 for
-// 11.6 (16 x 256, 4096; copies of 16 rows) and 19.1 for 13.2 (8 x 1000, 8192).
-bool fork_is_small(const mla_pages_fork_args* a) {
-    return a->n_pages <= kSmallPages && static_cast<long long>(a->batch) * a->columns <= kSmallEntries &&
-           static_cast<long long>(a->batch) * a->page_rows * a->row_bytes <= 128 << 10;
 }
 
 struct Carver {
@@ -725,20 +738,22 @@ cudaError_t launch(void (*kernel)(Params), dim3 grid, int threads, const Params&
 
 constexpr size_t kBitsSmem = sizeof(MoveRing) + sizeof(PageBits);
 static_assert(kBitsSmem <= 227 * 1024, "fits shared memory");
-std::atomic<int> g_moves_prepared[kMaxDevices];
+std::atomic<int> g_pages_prepared[kMaxDevices];
 
 // The device's SMs, and once per device the kernels' shared memory.
-int prepare_moves(int* sms) {
+int prepare_pages(int* sms) {
     int dev = 0;
     int rc = current_device(&dev);
     if (rc == MLA_OK) rc = device_sm_count(dev, sms);
-    if (rc != MLA_OK || g_moves_prepared[dev].load(std::memory_order_acquire)) return rc;
+    if (rc != MLA_OK || g_pages_prepared[dev].load(std::memory_order_acquire)) return rc;
     cudaError_t e = cudaFuncSetAttribute(mla_compact_bits_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(kBitsSmem));
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(mla_compact_move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(sizeof(MoveRing)));
-    if (e == cudaSuccess) g_moves_prepared[dev].store(1, std::memory_order_release);
+    for (auto kernel : {mla_fork_block_kernel<false>, mla_fork_block_kernel<true>})
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBlockBytes);
+    if (e == cudaSuccess) g_pages_prepared[dev].store(1, std::memory_order_release);
     return launch_status(e);
 }
 
@@ -778,10 +793,19 @@ int mla_pages_fork(const mla_pages_fork_args* args, void* scratch, size_t scratc
     p.keeper = c.take(args->n_pages);
     p.free = c.take(args->n_pages);
     p.rows = c.take(args->batch);
-    p.first = c.take(args->batch);
     p.src = c.take(args->batch);
     p.dst = c.take(args->batch);
-    if (fork_is_small(args)) return launch_status(launch(mla_fork_small_kernel, dim3(1), kPlaceThreads, p, stream));
+    if (fork_block_bytes(*args) <= kBlockBytes && args->batch * args->columns <= kBlockEntries) {
+        int sms = 0;
+        rc = prepare_pages(&sms);
+        if (rc != MLA_OK) return rc;
+        const size_t smem = static_cast<size_t>(fork_block_bytes(*args));
+        if (static_cast<long long>(args->batch) * args->page_rows * args->row_bytes <= kOwnCopies)
+            return launch_status(launch(mla_fork_block_kernel<true>, dim3(1), kPlaceThreads, p, stream, smem));
+        cudaError_t e = launch(mla_fork_block_kernel<false>, dim3(1), kPlaceThreads, p, stream, smem);
+        if (e == cudaSuccess) e = launch(mla_fork_copy_kernel, dim3(args->batch), kThreads, p, stream);
+        return launch_status(e);
+    }
     const dim3 count((args->columns + kPlaceThreads - 1) / kPlaceThreads, args->batch);
     p.blocks = static_cast<int>(count.x * count.y);
     const int clear = std::min((args->n_pages + kThreads - 1) / kThreads, 1024);
@@ -816,7 +840,7 @@ int mla_pages_compact(const mla_pages_compact_args* args, void* scratch, size_t 
     p.mover = c.take(args->n_pages);
     p.mover_refs = c.take(args->n_pages);
     int sms = 0;
-    rc = prepare_moves(&sms);
+    rc = prepare_pages(&sms);
     if (rc != MLA_OK) return rc;
     if (args->n_pages <= kBitsPages) {
         p.bits = reinterpret_cast<uint32_t*>(p.hole);

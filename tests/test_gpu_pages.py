@@ -133,7 +133,8 @@ def test_tables_with_entries_that_are_no_pages():
 @pytest.mark.parametrize("n_pages,batch,columns,page_rows", [(5000, 40, 130, 8), (9000, 3, 1500, 8), (4096, 64, 33, 16),
                                                              (20000, 600, 20, 8), (8193, 2, 2, 64), (65536, 30, 400, 8),
                                                              (65537, 300, 40, 8), (80000, 2, 9000, 8), (8192, 4, 2048, 8),
-                                                             (33, 1, 32, 8), (65535, 65, 300, 16)])
+                                                             (33, 1, 32, 8), (65535, 65, 300, 16),
+                                                             (9000, 2500, 3, 8), (12000, 3000, 8, 8)])
 def test_larger_pools(n_pages, batch, columns, page_rows):
     rnd = random.Random(n_pages)
     most = min(columns * page_rows - 1, (n_pages * page_rows) // (2 * batch))
