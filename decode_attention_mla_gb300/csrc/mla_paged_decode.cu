@@ -11,9 +11,10 @@
 // brings them back transposed for P V.  Its scores are partial sums, which the warps exchange through shared memory;
 // warp w then has the whole scores of rows 8 w .. + 7, and hands their probabilities to the others; and its part of O,
 // 16 x 128 fp32, stays in registers.  Two groups take slots in turn, each with a running maximum and sum of its own,
-// and are joined at an item's end.  (Measured on 32 requests of 16 heads, 168 us now: values widened a second time from the
-// bytes for P V, 186; two chains of products beside each other in the place of four, 183; transposed by movmatrix instead of
-// through shared memory, 180; three groups, which have 144 registers a thread, 187.)
+// and are joined at an item's end.  (Measured on 32 requests of 16 heads, 162 us now: values widened a second time from the
+// bytes for P V, 187; two chains of products beside each other in the place of four, 183; transposed by movmatrix instead of
+// through shared memory, 180; three groups, which have 144 registers a thread, 187; queries read from shared memory, without a
+// split of the registers, 168; the next slot's scores between a slot's softmax and its P V, 177.)
 //
 // Orders.  The contraction over features may go in any order: lane 4 g + j has, of row g of eight, features 16 j ..
 // 16 j + 15 of 64 (a block: eight bytes of codes), four to a k-step.  Rows of a slot lie 416 bytes apart, eight banks on, so
@@ -27,11 +28,11 @@
 // Work split: units of 64 rows (a slot per group) of all requests' blocks of sixteen query rows, one equal run per SM; pieces and
 // their merge as in mla_tree_attend.cu.
 //
-// Bound: 30 cycles of shared memory per row and SM (16 of them the widened values' way there and back, 4 the queries'
-// fragments), beside 17 of MMAs and 19 for its bytes from HBM; what is measured is 42, the rest being the chain from a
-// slot's bytes to its P V, which two warps a scheduler hide in part.  Bytes alone, nothing computed: 87 us of those 168.
+// Bound: 26 cycles of shared memory per row and SM (16 of them the widened values' way there and back, 4 the partial
+// scores'), beside 17 of MMAs and 19 for its bytes from HBM; what is measured is 40, the rest being the chain from a
+// slot's bytes to its P V, which two warps a scheduler hide in part.  Bytes alone, nothing computed: 87 us of those 162.
 //
-// Warps: 0-3 and 4-7 the groups, 8 bulk copies and the run's items, 9 empty requests.
+// Warps: 0-3 and 4-7 the groups, 8 bulk copies and the run's items, 9 empty requests, 10 and 11 none.
 #include <cmath>
 
 #include "mla_paged.cuh"
@@ -42,11 +43,15 @@ namespace {
 constexpr int kGroups = 2;
 constexpr int kSlotRows = 32, kUnitRows = kGroups * kSlotRows;
 constexpr int kSlotBytes = kSlotRows * MLA_Q4_ROW;
-constexpr int kRing = 4 * kGroups;
+constexpr int kRing = 3 * kGroups;                         // (131072 rows, 16 heads: 34 us; with 4 * kGroups 38, 2 * kGroups 34, but
+                                                           // 32 requests 165 for 162)
 constexpr int kWarps = 4;                                  // of a group
 constexpr int kGroupThreads = 32 * kWarps, kComputeThreads = kGroups * kGroupThreads;
 constexpr int kProducerWarp = kGroups * kWarps, kEmptyWarp = kProducerWarp + 1;
-constexpr int kThreads = 32 * (kEmptyWarp + 1);
+constexpr int kThreads = 32 * (kProducerWarp + 4);
+// Three warpgroups of 168 registers a thread at launch: two that compute, and one for the rest.
+constexpr int kLaunchRegs = 168, kComputeRegs = 208, kOtherRegs = 88;
+static_assert(kThreads == 384 && kGroups * kComputeRegs + kOtherRegs <= 3 * kLaunchRegs, "an increase never waits for more than there is");
 constexpr int kBarAll = 1, kBarGroup = 2;                  // hardware barriers: of all groups, of each
 constexpr int kBlockRows = kDecodeBlockRows;
 constexpr float kRescaleLog2 = 8.0f;                       // move the reference when a max grows past 2^8
@@ -350,6 +355,9 @@ __device__ void compute(const PagedParams& p, Shared& sh, int group, int w, int 
         const long long row0 = static_cast<long long>(it.b) * p.tokens * p.heads + it.rb * kBlockRows;
         if (group == 0) load_queries(p, sh, w, lane, row0, live);
         named_barrier_sync(kBarAll, kComputeThreads);
+        uint4 held[9];                                     // this lane's query fragments
+#pragma unroll
+        for (int k = 0; k < 9; ++k) held[k] = sh.q[k][w][lane];
         const float c2[2] = {sh.factor[g] * p.scale_log2 * p.kv_scale, sh.factor[g + 8] * p.scale_log2 * p.kv_scale};
         // slots whose rows every token attends: up to all_to, from all_from on or before sink
         const int all_to = row_int(static_cast<long long>(it.d_pos) + 1);
@@ -373,7 +381,7 @@ __device__ void compute(const PagedParams& p, Shared& sh, int group, int w, int 
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const uint2 rope = *reinterpret_cast<const uint2*>(at + 8 * e * MLA_Q4_ROW + kQ4Rope + 32 * w + 8 * j);
-                const uint4 q = sh.q[8][w][lane];
+                const uint4 q = held[8];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) acc[e][k] = 0.f;
                 mma_bf16(acc[e], {q.x, q.y, q.z, q.w}, rope.x, rope.y);
@@ -391,7 +399,7 @@ __device__ void compute(const PagedParams& p, Shared& sh, int group, int w, int 
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     uint32_t h[4][4];
-                    const uint4 q0 = sh.q[4 * k + 2 * i][w][lane], q1 = sh.q[4 * k + 2 * i + 1][w][lane];
+                    const uint4 q0 = held[4 * k + 2 * i], q1 = held[4 * k + 2 * i + 1];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         widen_e2m1(i == 0 ? raw[e].x : raw[e].y, h[e]);
@@ -632,31 +640,35 @@ __global__ void __launch_bounds__(kThreads, 1) mla_paged_decode_kernel(const __g
     __syncthreads();
     grid_dependency_wait();
     allow_dependent_launch();
-    if (warp == kProducerWarp) {
-        if (lane == 0) {
-            for (int i = 0; i < kTreePieces; ++i) p.merge[i * p.clusters + blockIdx.x].pieces = 0;
-            __threadfence_block();
-            if (p.stall_test && blockIdx.x == 0) {
-                // test hook: a wait that runs out, so the abort path runs for real
-                volatile int never = 0;
-                if (!mbar_wait_bounded(&sh.stall_bar, 0, &never, kStallTestCycles)) raise(p, sh);
+    if (warp < kProducerWarp) {
+        warpgroup_regs_increase<kComputeRegs>();
+        compute(p, sh, warp / kWarps, warp % kWarps, lane);
+    } else {
+        warpgroup_regs_decrease<kOtherRegs>();
+        if (warp == kProducerWarp) {
+            if (lane == 0) {
+                for (int i = 0; i < kTreePieces; ++i) p.merge[i * p.clusters + blockIdx.x].pieces = 0;
+                __threadfence_block();
+                if (p.stall_test && blockIdx.x == 0) {
+                    // test hook: a wait that runs out, so the abort path runs for real
+                    volatile int never = 0;
+                    if (!mbar_wait_bounded(&sh.stall_bar, 0, &never, kStallTestCycles)) raise(p, sh);
+                }
+            }
+            __syncwarp();
+            produce(p, sh, lane);
+        } else if (warp == kEmptyWarp) {
+            // requests without rows: their tokens' outputs
+            for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
+                const TreeRequest r = load_paged_request<kUnitRows>(p, b);
+                if (r.hi > 0 || r.n_tok == 0) continue;
+                const long long row0 = static_cast<long long>(b) * p.tokens * p.heads;
+                const int rows = r.n_tok * p.heads, per = p.a.out_fp32 ? 128 : 64;   // 16-byte units per row
+                for (int i = lane; i < rows; i += 32) p.a.lse[row0 + i] = -INFINITY;
+                uint4* o = reinterpret_cast<uint4*>(p.a.out) + row0 * per;
+                for (int i = lane; i < rows * per; i += 32) o[i] = make_uint4(0, 0, 0, 0);
             }
         }
-        __syncwarp();
-        produce(p, sh, lane);
-    } else if (warp == kEmptyWarp) {
-        // requests without rows: their tokens' outputs
-        for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
-            const TreeRequest r = load_paged_request<kUnitRows>(p, b);
-            if (r.hi > 0 || r.n_tok == 0) continue;
-            const long long row0 = static_cast<long long>(b) * p.tokens * p.heads;
-            const int rows = r.n_tok * p.heads, per = p.a.out_fp32 ? 128 : 64;   // 16-byte units per row
-            for (int i = lane; i < rows; i += 32) p.a.lse[row0 + i] = -INFINITY;
-            uint4* o = reinterpret_cast<uint4*>(p.a.out) + row0 * per;
-            for (int i = lane; i < rows * per; i += 32) o[i] = make_uint4(0, 0, 0, 0);
-        }
-    } else {
-        compute(p, sh, warp / kWarps, warp % kWarps, lane);
     }
     __syncthreads();
     if (*static_cast<volatile int*>(&sh.abort_flag)) {
@@ -670,6 +682,11 @@ __global__ void __launch_bounds__(kThreads, 1) mla_paged_decode_kernel(const __g
 }  // namespace
 
 cudaError_t paged_decode_prepare() {
+    // (the split of the registers counts on those of the launch)
+    cudaFuncAttributes fa{};
+    const cudaError_t e = cudaFuncGetAttributes(&fa, mla_paged_decode_kernel);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs < kLaunchRegs || fa.maxThreadsPerBlock < kThreads) return cudaErrorInvalidConfiguration;
     return cudaFuncSetAttribute(mla_paged_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 static_cast<int>(sizeof(Shared)));
 }
