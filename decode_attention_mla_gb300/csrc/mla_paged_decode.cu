@@ -11,10 +11,10 @@
 // brings them back transposed for P V.  Its scores are partial sums, which the warps exchange through shared memory;
 // warp w then has the whole scores of rows 8 w .. + 7, and hands their probabilities to the others; and its part of O,
 // 16 x 128 fp32, stays in registers.  Two groups take slots in turn, each with a running maximum and sum of its own,
-// and are joined at an item's end.  (Measured on 32 requests of 16 heads, 162 us now: values widened a second time from the
+// and are joined at an item's end.  (Measured on 32 requests of 16 heads, 157 us now: values widened a second time from the
 // bytes for P V, 187; two chains of products beside each other in the place of four, 183; transposed by movmatrix instead of
 // through shared memory, 180; three groups, which have 144 registers a thread, 187; queries read from shared memory, without a
-// split of the registers, 168; the next slot's scores between a slot's softmax and its P V, 177.)
+// split of the registers, 168; an item's end left to one group, 162; the next slot's scores between a slot's softmax and its P V, 177.)
 //
 // Orders.  The contraction over features may go in any order: lane 4 g + j has, of row g of eight, features 16 j ..
 // 16 j + 15 of 64 (a block: eight bytes of codes), four to a k-step.  Rows of a slot lie 416 bytes apart, eight banks on, so
@@ -29,8 +29,8 @@
 // their merge as in mla_tree_attend.cu.
 //
 // Bound: 26 cycles of shared memory per row and SM (16 of them the widened values' way there and back, 4 the partial
-// scores'), beside 17 of MMAs and 19 for its bytes from HBM; what is measured is 40, the rest being the chain from a
-// slot's bytes to its P V, which two warps a scheduler hide in part.  Bytes alone, nothing computed: 87 us of those 162.
+// scores'), beside 17 of MMAs and 19 for its bytes from HBM; what is measured is 39, the rest being the chain from a
+// slot's bytes to its P V, which two warps a scheduler hide in part.  Bytes alone, nothing computed: 87 us of those 157.
 //
 // Warps: 0-3 and 4-7 the groups, 8 bulk copies and the run's items, 9 empty requests, 10 and 11 none.
 #include <cmath>
@@ -40,7 +40,7 @@
 namespace mla {
 namespace {
 
-constexpr int kGroups = 2;
+constexpr int kGroups = 2;                                 // (that halve an item's O between them at its end)
 constexpr int kSlotRows = 32, kUnitRows = kGroups * kSlotRows;
 constexpr int kSlotBytes = kSlotRows * MLA_Q4_ROW;
 constexpr int kRing = 3 * kGroups;                         // (131072 rows, 16 heads: 34 us; with 4 * kGroups 38, 2 * kGroups 34, but
@@ -70,7 +70,7 @@ struct __align__(128) Shared {
     uint8_t ring[kRing][kSlotBytes];
     float4 part[kGroups][kWarps][4][32];                         // per group: partial scores by warp, eight rows, lane
     // per group and warp: a slot's values of the warp's features in f16, 256 bytes a row, 16-byte unit u of row r at u ^
-    // (r mod 8); at an item's end the O of all groups but the first
+    // (r mod 8); at an item's end half of its O, for the other group
     float4 v[kGroups][kWarps][kSlotRows * 16];
     uint4 q[9][kWarps][32];                                // query fragments by k-step (the last: key values), warp, lane
     uint16_t p[kGroups][16][40];                                 // per group: probabilities, row by row (padded)
@@ -541,33 +541,36 @@ __device__ void compute(const PagedParams& p, Shared& sh, int group, int w, int 
                 sh.sum[group][g + 8 * h] = l[h];
             }
         }
-        if (group > 0) {
+        // each group hands half of its features' O to the other (its own values of the other's half of the slot's are used up)
 #pragma unroll
-            for (int m = 0; m < 16; ++m) sh.v[group][w][32 * m + lane] = make_float4(o[m][0], o[m][1], o[m][2], o[m][3]);
+        for (int m = 0; m < 8; ++m) {
+            const float(&give)[4] = group == 0 ? o[8 + m] : o[m];
+            sh.v[group][w][32 * m + lane] = make_float4(give[0], give[1], give[2], give[3]);
+            if (group == 1) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[m][k] = o[8 + m][k];
+            }
         }
         if (named_barrier_or(kBarAll, kComputeThreads, false)) return;   // a group has left
-        if (group == 0) {
-            float by[kGroups][2], lse2[2];
+        {
+            const int other = 1 - group;
+            float own[2], theirs[2], lse2[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                float m = m_ref[h], sum = 0.f;
-#pragma unroll
-                for (int k = 1; k < kGroups; ++k) m = fmaxf(m, sh.top[k][g + 8 * h]);
-#pragma unroll
-                for (int k = 0; k < kGroups; ++k) {
-                    // (a group without rows has the sum 0 and O = 0; a NaN stays one)
-                    const float t = sh.top[k][g + 8 * h];
-                    by[k][h] = t > -INFINITY ? ex2_approx(t - m) : 1.f;
-                    sum = fmaf(sh.sum[k][g + 8 * h], by[k][h], sum);
-                }
+                const int r = g + 8 * h;
+                const float t = sh.top[other][r], m = fmaxf(m_ref[h], t);
+                // (a group without rows has the sum 0 and O = 0; a NaN stays one)
+                own[h] = m_ref[h] > -INFINITY ? ex2_approx(m_ref[h] - m) : 1.f;
+                theirs[h] = t > -INFINITY ? ex2_approx(t - m) : 1.f;
+                const float sum = fmaf(sh.sum[other][r], theirs[h], l[h] * own[h]);
                 const float inv = sum == 0.f ? 0.f : p.kv_scale / sum;
                 lse2[h] = sum == 0.f ? -INFINITY : (m - kProbLog2) + log2f(sum);
-#pragma unroll
-                for (int k = 0; k < kGroups; ++k) by[k][h] *= inv;
+                own[h] *= inv;
+                theirs[h] *= inv;
             }
             const bool whole = it.hi - it.lo == it.n_units;
             const int slot = kTreePieces * static_cast<int>(blockIdx.x) + (item == 0 ? 0 : 1);
-            if (w == 0 && j == 0) {
+            if (group == 0 && w == 0 && j == 0) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     if (g + 8 * h >= live) continue;
@@ -577,41 +580,35 @@ __device__ void compute(const PagedParams& p, Shared& sh, int group, int w, int 
                         p.lse_part[slot * 32 + g + 8 * h] = lse2[h];
                 }
             }
-            if (w == 0 && lane == 0 && !whole && it.lo == 0)
+            if (group == 0 && w == 0 && lane == 0 && !whole && it.lo == 0)
                 p.merge[blockIdx.x] = TreeMerge{it.b, it.rb, live | (item == 0 ? 0 : 1) << 16, it.runs};
 #pragma unroll
-            for (int m = 0; m < 16; ++m)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) o[m][k] *= by[0][k >> 1];
-#pragma unroll
-            for (int k = 1; k < kGroups; ++k)
-#pragma unroll
-                for (int m = 0; m < 16; ++m) {
-                    const float4 v = sh.v[k][w][32 * m + lane];
-                    o[m][0] = fmaf(v.x, by[k][0], o[m][0]);
-                    o[m][1] = fmaf(v.y, by[k][0], o[m][1]);
-                    o[m][2] = fmaf(v.z, by[k][1], o[m][2]);
-                    o[m][3] = fmaf(v.w, by[k][1], o[m][3]);
-                }
-            // rows g, g + 8; features 128 w + 8 m + 2 j, + 1
+            for (int m = 0; m < 8; ++m) {
+                const float4 v = sh.v[other][w][32 * m + lane];
+                o[m][0] = fmaf(v.x, theirs[0], o[m][0] * own[0]);
+                o[m][1] = fmaf(v.y, theirs[0], o[m][1] * own[0]);
+                o[m][2] = fmaf(v.z, theirs[1], o[m][2] * own[1]);
+                o[m][3] = fmaf(v.w, theirs[1], o[m][3] * own[1]);
+            }
+            // rows g, g + 8; features 128 w + 64 group + 8 m + 2 j, + 1
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int r = g + 8 * h;
                 if (r >= live) continue;
-                const int from = 128 * w + 2 * j;
+                const int from = 128 * w + 64 * group + 2 * j;
                 if (!whole) {
                     float* piece = p.part + (static_cast<long long>(slot) * (kDLatent / 4) * 32 + r) * 4 + (j & 1) * 2;
 #pragma unroll
-                    for (int m = 0; m < 16; ++m)
-                        *reinterpret_cast<float2*>(piece + (32 * w + 2 * m + (j >> 1)) * 128) = make_float2(o[m][2 * h], o[m][2 * h + 1]);
+                    for (int m = 0; m < 8; ++m)
+                        *reinterpret_cast<float2*>(piece + (32 * w + 16 * group + 2 * m + (j >> 1)) * 128) = make_float2(o[m][2 * h], o[m][2 * h + 1]);
                 } else if (p.a.out_fp32) {
                     float* dst = static_cast<float*>(p.a.out) + (row0 + r) * kDLatent + from;
 #pragma unroll
-                    for (int m = 0; m < 16; ++m) *reinterpret_cast<float2*>(dst + 8 * m) = make_float2(o[m][2 * h], o[m][2 * h + 1]);
+                    for (int m = 0; m < 8; ++m) *reinterpret_cast<float2*>(dst + 8 * m) = make_float2(o[m][2 * h], o[m][2 * h + 1]);
                 } else {
                     uint16_t* dst = static_cast<uint16_t*>(p.a.out) + (row0 + r) * kDLatent + from;
 #pragma unroll
-                    for (int m = 0; m < 16; ++m) *reinterpret_cast<uint32_t*>(dst + 8 * m) = pack_bf16x2(o[m][2 * h], o[m][2 * h + 1]);
+                    for (int m = 0; m < 8; ++m) *reinterpret_cast<uint32_t*>(dst + 8 * m) = pack_bf16x2(o[m][2 * h], o[m][2 * h + 1]);
                 }
             }
         }
