@@ -1,5 +1,6 @@
 // mla_paged.cu -- attention over the 4-bit paged cache: plan, checks and launch
 // (include/mla_paged.h).
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -84,16 +85,23 @@ int prepare(cudaStream_t st, bool may_capture) {
     return MLA_OK;
 }
 
-// Few query rows: on warp-level MMAs, an SM's run each.  Measured against the tcgen05 kernel, us (requests x cache rows), for
-// 16 query rows per request: 14.5 and 16.7 (1 x 255), 24.7 and 30.9 (8 x 4096), 26.8 and 38.0 (32 x 2000), 154 and 253
-// (32 x 32768); for 32: 15.4 and 18.1, 27.6 and 30.9, 35.0 and 38.2, 287 and 253; for 48: 16.5 and 20.6, 30.9 and 34.5,
-// 45.8 and 41.2, 421 and 257.  (How long the requests are, the host does not know.  It counts units of 64 rows in an int.)
-constexpr int kFewRows = 32;
+// Few query rows, or little work: on warp-level MMAs, sixteen query rows at a time and an SM's run each; the tcgen05 kernel does
+// 128 in the time of 16, but takes about 5 us longer to begin and end.
+// Rows.  Measured, us (requests x cache rows): with 16 query rows per request 10.1 and 13.4 (1 x 255), 19.3 and 29.4 (8 x 4096), 144
+// and 250 (32 x 32768); with 32 10.2 and 13.5, 23.1 and 30.0, 271 and 251; with 48 27.4 and 33.3 (8 x 4096), 400 and 253.
+// Work, in units of 64 cache rows per SM, a block of sixteen query rows counting as two more (requests x query rows x cache
+// rows): 1 x 128 x 255 0.3 units, 10.2 and 15.4 us; 1 x 128 x 2000 1.8, 14.3 and 16.7; 8 x 128 x 255 2.5, 12.6 and 17.5; 2 x 64 x
+// 3000 2.6, 18.0 and 18.5; 7 x 64 x 1000 3.3, 17.3 and 19.8; but 1 x 128 x 4000 3.4, 19.2 and 17.4; 1 x 128 x 10000 8.4, 25.5 and 22.0.
+// (How long the requests are, the host does not know: it takes the table's length, or what a window leaves of it.  The kernel
+// counts units in an int.)
+constexpr int kFewRows = 32, kFewUnits = 3;
 bool few_rows(const mla_paged_plan_t* pl, const mla_paged_args* a) {
     const long long rows = static_cast<long long>(pl->shape.tokens) * pl->shape.heads;
-    const long long blocks = (rows + kDecodeBlockRows - 1) / kDecodeBlockRows;
-    const long long units = static_cast<long long>(a->cache.columns) * a->cache.page_rows / 64 + 2;
-    return rows <= kFewRows && pl->shape.batch * blocks * units < (1ll << 30);
+    const long long blocks = pl->shape.batch * ((rows + kDecodeBlockRows - 1) / kDecodeBlockRows);
+    const long long table = static_cast<long long>(a->cache.columns) * a->cache.page_rows;
+    if (blocks * (table / 64 + 2) >= (1ll << 30)) return false;
+    const long long seen = a->window > 0 ? static_cast<long long>(a->window) + a->sink + pl->shape.tokens : table;
+    return rows <= kFewRows || blocks * (std::min(table, seen) / 64 + 3) <= static_cast<long long>(kFewUnits) * pl->num_sms;
 }
 
 PagedParams params(const mla_paged_plan_t* pl, const mla_paged_args* a, void* scratch, bool few) {

@@ -25,20 +25,21 @@ def random_pages(n_pages, page_rows, g, kv_scale=1.0, spread=1.0):
     return raw.view(n_pages, page_rows, 416)
 
 
-# 16 query rows per token are taken by one kernel, 48 by the other
-BOTH = pytest.mark.parametrize("H", [16, 48])
+# heads, and SMs to plan for (0: all): few query rows and little work are one kernel's, 48 heads on two SMs the other's
+BOTH = pytest.mark.parametrize("H,sms", [(16, 0), (48, 0), (48, 2)])
+SMS = pytest.mark.parametrize("sms", [0, 2, 8])
 
 
 class Case:
     """Requests over pages in random order; everything that no token attends is NaN."""
 
     def __init__(self, d_pos, Q=1, H=16, page_rows=16, n_tokens=None, window=0, sink=0, kv_scale=1.0, seed=0, gone=(),
-                 fp32=False, spare=2, scale=576 ** -0.5, gain=1.0):
+                 fp32=False, spare=2, scale=576 ** -0.5, gain=1.0, sms=0):
         g = torch.Generator().manual_seed(seed)
         rnd = random.Random(seed)
         B = len(d_pos)
         self.d_pos, self.n_tokens, self.window, self.sink = d_pos, n_tokens or [Q] * B, window, sink
-        self.kv_scale, self.scale, self.fp32 = kv_scale, scale, fp32
+        self.kv_scale, self.scale, self.fp32, self.sms = kv_scale, scale, fp32, sms
         need = [-(-(max(d, -1) + Q) // page_rows) for d in d_pos]
         n_pages = sum(need) + spare
         order = list(range(n_pages))
@@ -72,7 +73,7 @@ class Case:
 
     def forward(self, pdl=False, plan=None, scratch=None, **kw):
         B, Q, H, _ = self.q.shape
-        plan = plan or mla.paged_plan(batch=B, tokens=Q, heads=H, scale=self.scale, pdl=pdl)
+        plan = plan or mla.paged_plan(batch=B, tokens=Q, heads=H, scale=self.scale, num_sms=self.sms, pdl=pdl)
         scratch = mla.paged_alloc_scratch(plan) if scratch is None else scratch
         mla.paged_forward(plan, self.t_q, self.t_pages, self.t_table, self.out, self.lse, scratch, d_pos=self.t_d,
                           n_tokens=self.t_n, window=self.window, sink=self.sink, kv_scale=self.kv_scale, **kw)
@@ -108,8 +109,9 @@ class Case:
     dict(d_pos=[2500], Q=2, H=32), dict(d_pos=[64, 63], Q=1, H=17, page_rows=64),
 ], ids=str)
 @pytest.mark.parametrize("fp32", [False, True])
-def test_attention(kw, fp32):
-    c = Case(**kw, fp32=fp32).on_gpu()
+@SMS
+def test_attention(kw, fp32, sms):
+    c = Case(**kw, fp32=fp32, sms=sms).on_gpu()
     plan, scratch = c.forward()
     c.check()
     assert mla.status_word(plan, scratch) == 0
@@ -124,8 +126,8 @@ def test_attention(kw, fp32):
     dict(d_pos=[3000], window=2 ** 31 - 1, sink=2 ** 31 - 1), dict(d_pos=[500], window=3, sink=2 ** 31 - 1),
 ], ids=str)
 @BOTH
-def test_window(kw, H):
-    c = Case(**{"H": H, **kw}).on_gpu()
+def test_window(kw, H, sms):
+    c = Case(**{"H": H, **kw}, sms=sms).on_gpu()
     c.forward()
     c.check()
 
@@ -137,15 +139,15 @@ def test_window(kw, H):
     dict(d_pos=[256 + 127], page_rows=128, gone=[(0, 1)]),
 ], ids=str)
 @BOTH
-def test_rows_without_pages(kw, H):
-    c = Case(**{"H": H, **kw}).on_gpu()
+def test_rows_without_pages(kw, H, sms):
+    c = Case(**{"H": H, **kw}, sms=sms).on_gpu()
     c.forward()
     c.check()
 
 
 @BOTH
-def test_rows_behind_the_table(H):
-    c = Case([47], H=H, page_rows=16)
+def test_rows_behind_the_table(H, sms):
+    c = Case([47], H=H, page_rows=16, sms=sms)
     c.table[0][3] = -1                # rows 48 .. 63 have no page, and the table ends there
     want = c.expected()
     c.d_pos = [1000]
@@ -156,8 +158,8 @@ def test_rows_behind_the_table(H):
 
 @pytest.mark.parametrize("what", ["scale", "key"])
 @BOTH
-def test_nan_in_an_attended_row(what, H):
-    c = Case([300, 200], Q=2, H=H)
+def test_nan_in_an_attended_row(what, H, sms):
+    c = Case([300, 200], Q=2, H=H, sms=sms)
     page, slot = c.table[0][300 // 16], 300 % 16      # the first token's own row
     if what == "scale":
         c.pages[page, slot, 256 + 5] = 0x7f
@@ -171,8 +173,8 @@ def test_nan_in_an_attended_row(what, H):
 
 
 @BOTH
-def test_nan_queries_stay_in_their_rows(H):
-    c = Case([300], Q=2, H=H)
+def test_nan_queries_stay_in_their_rows(H, sms):
+    c = Case([300], Q=2, H=H, sms=sms)
     c.q[0, 0, 3, 17] = math.nan
     c.q[0, 1, 5, 570] = math.inf
     want = c.expected()
@@ -188,9 +190,9 @@ def test_nan_queries_stay_in_their_rows(H):
 
 @pytest.mark.parametrize("gain", [1e-30, 1e-4, 300.0, 1e30])
 @BOTH
-def test_queries_of_any_size(gain, H):
+def test_queries_of_any_size(gain, H, sms):
     """A query's size times the scale is what counts: far from f16's range, the same result."""
-    c = Case([400], Q=2, H=H, gain=gain, scale=576 ** -0.5 / gain * 1.0)
+    c = Case([400], Q=2, H=H, sms=sms, gain=gain, scale=576 ** -0.5 / gain * 1.0)
     if not c.scale < 2.0 ** 60:
         c.scale = 2.0 ** 59
     c.on_gpu()
@@ -199,8 +201,8 @@ def test_queries_of_any_size(gain, H):
 
 
 @BOTH
-def test_small_query_values_beside_large_ones(H):
-    c = Case([200], Q=1, H=H)
+def test_small_query_values_beside_large_ones(H, sms):
+    c = Case([200], Q=1, H=H, sms=sms)
     c.q[..., 0] *= 2.0 ** 20          # the others still count, exactly
     c.scale = 2.0 ** -22
     c.on_gpu()
@@ -209,8 +211,8 @@ def test_small_query_values_beside_large_ones(H):
 
 
 @BOTH
-def test_zero_queries_average_the_rows(H):
-    c = Case([999], H=H - 13, fp32=True)
+def test_zero_queries_average_the_rows(H, sms):
+    c = Case([999], H=H - 13, fp32=True, sms=sms)
     c.q.zero_()
     c.on_gpu()
     c.forward()
@@ -219,9 +221,9 @@ def test_zero_queries_average_the_rows(H):
 
 
 @BOTH
-def test_layers_of_one_pool(H):
+def test_layers_of_one_pool(H, sms):
     """Pages with a stride: one layer of a pool that holds several."""
-    c = Case([300, 77], Q=2, H=H, page_rows=32)
+    c = Case([300, 77], Q=2, H=H, sms=sms, page_rows=32)
     c.on_gpu()
     pool = torch.full((c.pages.shape[0], 3, 32, 416), NAN_ROW, dtype=torch.uint8, device="cuda")
     pool[:, 1] = c.t_pages
@@ -231,9 +233,9 @@ def test_layers_of_one_pool(H):
 
 
 @BOTH
-def test_shared_pages(H):
+def test_shared_pages(H, sms):
     """Two requests over the same pages, and one that goes on alone behind them."""
-    c = Case([95, 95, 40], Q=2, H=H, page_rows=16)
+    c = Case([95, 95, 40], Q=2, H=H, sms=sms, page_rows=16)
     for k in range(4):
         c.table[1][k] = c.table[0][k]
     c.pages = torch.where((c.pages == NAN_ROW).all(-1, keepdim=True), torch.zeros(1, dtype=torch.uint8), c.pages)
@@ -262,9 +264,9 @@ def test_long_and_many(kw):
 
 
 @BOTH
-def test_pages_past_four_gigabytes(H):
+def test_pages_past_four_gigabytes(H, sms):
     page_rows, n_pages = 1024, 11000  # 4.7 GB
-    c = Case([2500], Q=2, H=H, page_rows=page_rows, spare=0)
+    c = Case([2500], Q=2, H=H, sms=sms, page_rows=page_rows, spare=0)
     pages = torch.zeros(n_pages, page_rows, 416, dtype=torch.uint8, device="cuda")
     to = {p: n_pages - 1 - 40 * k for k, p in enumerate(c.table[0][:3])}
     for p, far in to.items():
@@ -278,7 +280,7 @@ def test_pages_past_four_gigabytes(H):
 
 
 @BOTH
-def test_replayed_graph_follows_lengths_and_tables(H):
+def test_replayed_graph_follows_lengths_and_tables(H, sms):
     a, b = Case([300, 40], Q=2, H=H, seed=1), Case([123, 290], Q=2, H=H, seed=2)
     a.on_gpu()
     b.on_gpu()
@@ -287,7 +289,7 @@ def test_replayed_graph_follows_lengths_and_tables(H):
     pages = torch.zeros(n, 16, 416, dtype=torch.uint8, device="cuda")
     table, d, q = torch.full((2, columns), -1, **I32), torch.zeros(2, **I32), torch.zeros_like(a.t_q)
     out, lse = torch.zeros_like(a.out), torch.zeros_like(a.lse)
-    plan = mla.paged_plan(batch=2, tokens=2, heads=H, scale=a.scale, pdl=True)
+    plan = mla.paged_plan(batch=2, tokens=2, heads=H, scale=a.scale, num_sms=sms, pdl=True)
     scratch = mla.paged_alloc_scratch(plan)
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
@@ -321,9 +323,9 @@ def test_two_streams_with_scratch_of_their_own():
 
 
 @BOTH
-def test_a_wait_that_runs_out_is_reported(H):
-    c = Case([300], H=H).on_gpu()
-    plan = mla.paged_plan(batch=1, tokens=1, heads=H, scale=c.scale, stall_test=True)
+def test_a_wait_that_runs_out_is_reported(H, sms):
+    c = Case([300], H=H, sms=sms).on_gpu()
+    plan = mla.paged_plan(batch=1, tokens=1, heads=H, scale=c.scale, num_sms=sms, stall_test=True)
     _, scratch = c.forward(plan=plan)
     torch.cuda.synchronize()
     assert mla.status_word(plan, scratch) == mla.EDEVICE
