@@ -16,8 +16,6 @@ constexpr int kPagedMagic = 0x4d4c5034;                    // "MLP4"
 bool off(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to != 0; }
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-float scale_log2(float scale) { return static_cast<float>(scale * 1.4426950408889634); }
-
 int check_shape(const mla_paged_shape* s) {
     if (!s) return MLA_EINVAL;
     if (s->batch < 1 || s->batch > 4096 || s->tokens < 1 || s->tokens > MLA_PAGED_MAX_TOKENS) return MLA_EINVAL;
@@ -117,7 +115,6 @@ PagedParams params(const mla_paged_plan_t* pl, const mla_paged_args* a, void* sc
     p.heads = pl->shape.heads;
     p.clusters = few ? pl->grid : pl->grid / 2;
     p.block_rows = few ? kDecodeBlockRows : kTreeBlockRows;
-    p.scale_log2 = scale_log2(pl->shape.scale);
     p.merge = reinterpret_cast<TreeMerge*>(base + kMergeOffset);
     p.cut = reinterpret_cast<TreeCut*>(p.merge + kTreePieces * p.clusters);
     p.part = reinterpret_cast<float*>(base + pl->part_offset);
@@ -127,6 +124,10 @@ PagedParams params(const mla_paged_plan_t* pl, const mla_paged_args* a, void* sc
     p.cache = paged_cache(&a->cache);
     p.q = static_cast<const uint16_t*>(a->q);
     p.kv_scale = a->cache.kv_scale;
+    int carry = 0;                                         // (a mantissa next to 1 is rounded up to it)
+    p.unit = 2 * std::frexp(static_cast<float>(std::frexp(pl->shape.scale * 1.4426950408889634 * p.kv_scale, &p.unit_exp)), &carry);
+    p.unit_exp += carry - 1;
+    p.least_exp = std::max(-126, -126 - p.unit_exp);
     p.window = a->window;
     p.sink = a->sink;
     return p;

@@ -11,8 +11,21 @@ struct PagedParams : TreeParams {                          // (of a.*: d_pos, n_
     PagedCache cache;
     const uint16_t* q;
     float kv_scale;
+    float unit;                                            // scale * log2(e) * kv_scale = unit * 2^unit_exp, unit in [1, 2)
+    int unit_exp, least_exp;
     int window, sink;
 };
+
+// A query row is held times 2^-e, which brings its largest value, `top`, to 2^14 .. 2^15, and its scores are the sums of
+// products times unit * 2^(e + unit_exp).  That factor is neither 0 nor infinite: a masked score is -infinity, and times 0
+// it would be NaN, as a score of 0 would be times infinity.  So e is not below least_exp (the row is held smaller, where
+// the scores' factor is 2^-126 .. 2^-125); a factor above fp32's range is its largest.
+__device__ __forceinline__ int query_exp(const PagedParams& p, float top) {
+    return min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127 - 14, p.least_exp), 126);
+}
+// -126 .. 127: the scores' factor is unit times 2 to it.
+__device__ __forceinline__ int factor_exp(const PagedParams& p, int e) { return min(p.unit_exp + e, 127); }
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
 constexpr int kDecodeBlockRows = 16;                       // query rows per block of the kernel for few of them
 

@@ -86,7 +86,7 @@ struct __align__(1024) Shared {
     uint8_t p[2][kChunkBytes];                             // P, 64 rows x 128 keys in two key atoms
     float red_max[4][64], red_sum[4][64];                  // by quarter of the tile's keys, row
     Item items[kItems];                                    // by item mod kItems
-    int8_t q_exp[4][64];                                   // by item mod 4: a query row is held times 2^-q_exp
+    int8_t factor_exp[4][64];                              // by item mod 4: of a query row's scores, as of factor_exp()
     // used in the even CTA, arrivals of both
     uint64_t k_ready[kSlots], rope_ready, v_ready[2], q_ready, p_ready, o_free;
     // in each CTA, arrivals of the MMA thread
@@ -286,7 +286,7 @@ __device__ __forceinline__ void fill_queries(const PagedParams& p, Shared& sh, l
         }
         // (magnitudes as fp32 bits are in the order of integers)
         top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-        const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127 - 14, -126), 126);
+        const int e = query_exp(p, top);
         const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
@@ -299,7 +299,7 @@ __device__ __forceinline__ void fill_queries(const PagedParams& p, Shared& sh, l
             }
             if (k < 2 || lane < 8) st_shared_v4(at + 4 * k * kChunkBytes, o[0], o[1], o[2], o[3]);
         }
-        if (lane == 0) sh.q_exp[item & 3][8 * fill + i] = static_cast<int8_t>(e);
+        if (lane == 0) sh.factor_exp[item & 3][8 * fill + i] = static_cast<int8_t>(factor_exp(p, e));
     }
 }
 
@@ -634,8 +634,7 @@ __device__ void softmax(const PagedParams& p, Shared& sh, uint32_t tmem, uint32_
         const int all_to = row_int(static_cast<long long>(it.d_pos) + 1);
         const int all_from = p.window > 0 ? row_int(static_cast<long long>(it.d_pos) + it.n_tok - p.window) : 0;
         bad |= !warp_wait(&sh.abort_flag, &sh.q_local[item & 1], (item >> 1) & 1);
-        const float c2 = p.scale_log2 * p.kv_scale *
-                         (live ? __uint_as_float(static_cast<uint32_t>(127 + sh.q_exp[item & 3][row]) << 23) : 1.f);
+        const float c2 = p.unit * (live ? power_of_two(sh.factor_exp[item & 3][row]) : 1.f);
         float m_ref = -INFINITY, l = 0.f;
         bool last;
         do {

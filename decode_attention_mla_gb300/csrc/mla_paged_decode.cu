@@ -76,7 +76,7 @@ struct __align__(128) Shared {
     uint16_t p[kGroups][16][40];                                 // per group: probabilities, row by row (padded)
     float red[kGroups][kWarps][16];                        // per group: maxima or sums by warp, row
     float top[kGroups][16], sum[kGroups][16];              // ... at an item's end
-    float factor[16];                                      // what the query rows were divided by
+    float factor[16];                                      // of the query rows' scores
     Item items[kItems];
     uint64_t full[kRing], empty[kRing];
     uint64_t item_full[kItems], item_empty[kItems];
@@ -310,9 +310,9 @@ __device__ __forceinline__ void load_queries(const PagedParams& p, Shared& sh, i
         float top = 0.f;
 #pragma unroll
         for (int k = 0; k < kWarps; ++k) top = fmaxf(top, sh.red[0][k][g + 8 * h]);
-        const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23) - 127 - 14, -126), 126);
+        const int e = query_exp(p, top);
         scale[h] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        if (w == 0 && j == 0) sh.factor[g + 8 * h] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        if (w == 0 && j == 0) sh.factor[g + 8 * h] = p.unit * power_of_two(factor_exp(p, e));
     }
     // k-step 2 k + s: features 64 (k / 2) + 16 j + 8 (k mod 2) + 4 s, + 1 (registers 0, 1) and + 2, + 3 (2, 3); rows g (0, 2)
     // and g + 8 (1, 3)
@@ -358,7 +358,7 @@ __device__ void compute(const PagedParams& p, Shared& sh, int group, int w, int 
         uint4 held[9];                                     // this lane's query fragments
 #pragma unroll
         for (int k = 0; k < 9; ++k) held[k] = sh.q[k][w][lane];
-        const float c2[2] = {sh.factor[g] * p.scale_log2 * p.kv_scale, sh.factor[g + 8] * p.scale_log2 * p.kv_scale};
+        const float c2[2] = {sh.factor[g], sh.factor[g + 8]};
         // slots whose rows every token attends: up to all_to, from all_from on or before sink
         const int all_to = row_int(static_cast<long long>(it.d_pos) + 1);
         const int all_from = p.window > 0 ? row_int(static_cast<long long>(it.d_pos) + it.n_tok - p.window) : 0;
