@@ -50,15 +50,25 @@ struct ForkParams {
     int* ticket;
 };
 
-// Rows that request b goes on with, and its parent (-1: it ends).
-__device__ __forceinline__ int fork_rows(const ForkParams& p, int b, int& parent) {
-    parent = p.a.parent ? p.a.parent[b] : b;
-    if (parent < 0 || parent >= p.a.batch) {
-        parent = -1;
-        return 0;
-    }
-    const int n = max(p.a.d_pos[parent], 0);
-    return min(min(n, p.a.rows ? max(p.a.rows[b], 0) : n), p.a.columns << p.shift);
+// Request b's parent (-1: it ends).
+__device__ __forceinline__ int fork_parent(const ForkParams& p, int b) {
+    const int parent = p.a.parent ? p.a.parent[b] : b;
+    return parent >= 0 && parent < p.a.batch ? parent : -1;
+}
+// n rows, by a request's entries, or their full pages' where the page that they end in is missing.  (Not inlined: forks
+// without a window do not call it, and four beams took 6.9 us for 6.7 with its code among theirs.)
+__device__ __noinline__ int without_missing(const int* entries, int n_pages, int n, int shift) {
+    const int part = n & ((1 << shift) - 1);
+    return part && static_cast<unsigned>(entries[n >> shift]) >= static_cast<unsigned>(n_pages) ? n - part : n;
+}
+// Rows that request b goes on with.  Where they end in a page that is missing, the rows of that page are not there, and n
+// falls to the full pages before it: here with a window, since n says what a window gives back, else in fork_place (one look-up
+// less in a row).
+__device__ __forceinline__ int fork_rows(const ForkParams& p, int b, int parent) {
+    if (parent < 0) return 0;
+    const int d = max(p.a.d_pos[parent], 0);
+    const int n = min(min(d, p.a.rows ? max(p.a.rows[b], 0) : d), p.a.columns << p.shift);
+    return p.a.window > 0 ? without_missing(p.a.page_table + static_cast<long long>(parent) * p.a.columns, p.a.n_pages, n, p.shift) : n;
 }
 // Column behind the last one that request b reserves, n rows kept.
 __device__ __forceinline__ int fork_end(const ForkParams& p, int n) {
@@ -119,15 +129,16 @@ __device__ void fork_place(const ForkParams& p) {
         const int b = q * kPlaceThreads + threadIdx.x;
         Request r{0, 0, -1, false, 0};
         if (b < batch) {
-            int parent;
+            const bool goes_on = fork_parent(p, b) >= 0;
             r.n = counted<kShared>(p.rows + b);
-            fork_rows(p, b, parent);
-            if (parent >= 0) r.end = fork_end(p, r.n);
             if (r.n & rows_mask) {
                 r.page = counted<kShared>(p.table + static_cast<long long>(b) * columns + (r.n >> p.shift));
                 if (r.page >= 0)
                     r.copied = counted<kShared>(p.a.refs + r.page) > 0 || counted<kShared>(p.keeper + r.page) != b;
+                else
+                    r.n &= ~rows_mask;
             }
+            if (goes_on) r.end = fork_end(p, r.n);
             p.src[b] = r.copied ? r.page : -1;
         }
         const int need = max(0, r.end - (r.n >> p.shift)) - (r.page >= 0 && !r.copied);
@@ -213,8 +224,7 @@ __global__ void __launch_bounds__(kPlaceThreads) mla_fork_count_kernel(const __g
     grid_dependency_wait();
     allow_dependent_launch();
     const int b = blockIdx.y;
-    int parent;
-    const int n = fork_rows(p, b, parent);
+    const int parent = fork_parent(p, b), n = fork_rows(p, b, parent);
     for (int c = blockIdx.x * kPlaceThreads + threadIdx.x; c < p.a.columns; c += gridDim.x * kPlaceThreads)
         fork_entry(p, b, c, fork_page(p, c, parent, n), n);
     if (blockIdx.x == 0 && threadIdx.x == 0) p.rows[b] = n;
@@ -287,7 +297,11 @@ __global__ void __launch_bounds__(kPlaceThreads) mla_fork_block_kernel(const __g
     }
     grid_dependency_wait();
     allow_dependent_launch();
-    for (int b = threadIdx.x; b < batch; b += kPlaceThreads) p.rows[b] = fork_rows(p, b, p.dst[b]);   // (dst: the parent, so far)
+    for (int b = threadIdx.x; b < batch; b += kPlaceThreads) {
+        const int parent = fork_parent(p, b);
+        p.dst[b] = parent;                                 // (so far)
+        p.rows[b] = fork_rows(p, b, parent);
+    }
     __syncthreads();
     for (int e0 = threadIdx.x; e0 < entries; e0 += kAhead * kPlaceThreads) {
         int page[kAhead];

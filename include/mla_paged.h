@@ -192,7 +192,8 @@ typedef struct {
     int *missing;               /* (device) int32 [1]: pages that there were too few of */
 } mla_pages_fork_args;
 
-/* Pages that a request of the next step names, after n = min(rows[b], d_pos[parent[b]]) rows:
+/* Pages that a request of the next step names, after n = min(rows[b], d_pos[parent[b]]) rows, rounded down to full
+ * pages where the page that they would end in is missing (those rows are not there):
  *   - full ones (rows 0 .. n - 1 fill them) are its parent's, shared;
  *   - a last one that n ends in: its parent's, if no request has that page as a full one and of those that
  *     end in it this one comes first; otherwise a copy of its n % page_rows rows in a page of its own;
@@ -200,8 +201,10 @@ typedef struct {
  * All other entries are -1, and pages that no entry names are free (there is no list of free
  * pages: refs is made anew from the tables).  Pages are taken, in the order of requests and columns,
  * the lowest free number first.  Where they run out, entries stay -1 and `missing` counts them; a
- * request whose last page could not be copied gets n rounded down to full pages.  Columns past the table's end
- * are not reserved.
+ * request whose last page could not be copied gets n rounded down to full pages too (a window has given pages back by
+ * the n before that).  Columns past the table's end are not reserved.
+ * Rows appended where an entry is -1 are not written.  A caller that finds `missing` above 0 does not count them in d_pos:
+ * a later call takes them back where n ends in a missing page, but full pages that are missing stay gaps.
  * Errors: MLA_EINVAL, MLA_EALIGN, MLA_ESCRATCH, MLA_ECUDA. */
 MLA_API int mla_pages_fork(const mla_pages_fork_args *args, void *scratch, size_t scratch_bytes, void *stream);
 

@@ -123,6 +123,8 @@ class Pages:
                 continue
             have = max(self.d_pos[parent[b]], 0)
             n[b] = min(have, max(rows[b], 0) if rows is not None else have, columns * ps)
+            if n[b] % ps and not 0 <= self.table[parent[b]][n[b] // ps] < self.n_pages:
+                n[b] = n[b] // ps * ps                    # the rows of a last page that is missing are not there
             for c in range(columns):
                 page = self.table[parent[b]][c]
                 if c * ps >= n[b] or not 0 <= page < self.n_pages:
