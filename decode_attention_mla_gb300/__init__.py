@@ -594,6 +594,12 @@ def _strides(t, name, shape, last):
     return [p] + [int(t.stride(i)) if t.shape[i] > 1 else 0 for i in range(last)]
 
 
+def _apart(t, name, dims):
+    """Refuse an output whose entries lie in one place (the strides of its first `dims` dimensions are used)."""
+    if any(t.stride(i) == 0 and t.shape[i] > 1 for i in range(dims)):
+        raise ValueError(f"{name} is an expanded tensor: its entries would be written to one place")
+
+
 class RopeTable:
     """Angles per position of the rotated pairs (``mla_rope_table``), on the device."""
 
@@ -932,16 +938,18 @@ def paged_append(table: RopeTable, positions, *, stream=None, **kw) -> None:
 
 
 def paged_read_make_args(out, pages, page_table, *, first=None, n_rows=None, kv_scale: float = 1.0) -> PagedReadArgs:
-    """Arguments of :func:`paged_read_args`.  ``out``: bf16 [B, N, 576], any strides that are multiples of 8;
+    """Arguments of :func:`paged_read_args`.  ``out``: bf16 [B, N, 576], any strides that are multiples of 8, not expanded;
     ``first``, ``n_rows``: int32 [B] (None: 0, N)."""
     torch = _torch or _tc()
     if out.dim() != 3:
         raise ValueError("out must be [B, N, 576]")
     B, N, _ = out.shape
+    _apart(out, "out", 2)
     a = PagedReadArgs(cache=_paged_cache(pages, page_table, kv_scale, B), batch=int(B), rows=int(N),
                       first=_maybe(first, "first", torch.int32, (B,)), n_rows=_maybe(n_rows, "n_rows", torch.int32, (B,)))
     a.out, a.out_batch, a.out_row = _strides(out, "out", (B, N, D_ROW), 2)
-    a.out_row = a.out_row or D_ROW
+    if N == 1:
+        a.out_row = D_ROW                  # never used
     a._device = _device()
     a._keep = (out, pages, page_table, first, n_rows)
     return a

@@ -371,6 +371,8 @@ __global__ void __launch_bounds__(kThreads) mla_paged_read_kernel(const __grid_c
 
 bool off(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to != 0; }
 bool off8(long long stride) { return stride % 8 != 0; }
+// Several entries of `width` elements lie in one place, or across one another.
+bool piled(int count, long long stride, int width) { return count > 1 && stride > -width && stride < width; }
 
 int check(const mla_paged_append_args* a) {
     if (!a || a->batch < 1 || a->batch > 65535 || a->tokens < 1 || a->tokens > (1 << 28)) return MLA_EINVAL;
@@ -462,6 +464,7 @@ extern "C" int mla_paged_read(const mla_paged_read_args* args, void* stream) {
     if (mla::off(args->out, 16) || mla::off8(args->out_batch) || mla::off8(args->out_row) || mla::off(args->first, 4) ||
         mla::off(args->n_rows, 4))
         return MLA_EALIGN;
+    if (mla::piled(args->batch, args->out_batch, MLA_D_ROW)) return MLA_EINVAL;
     const mla::ReadParams p{*args, mla::paged_cache(&args->cache), args->cache.kv_scale};
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr;

@@ -103,7 +103,8 @@ typedef struct {
     const int *first;           /* (device) int32 [B]; NULL = 0 */
     const int *n_rows;          /* (device) int32 [B], clamped to 0 .. N; NULL = N */
     void *out;                  /* (device) bf16 [B][N][576], 16-byte aligned */
-    long long out_batch, out_row;   /* strides in elements, multiples of 8, out_row >= 576 */
+    long long out_batch, out_row;   /* strides in elements, multiples of 8, out_row >= 576; requests in places
+                                       of their own: |out_batch| >= 576 where batch > 1 */
 } mla_paged_read_args;
 MLA_API int mla_paged_read(const mla_paged_read_args *args, void *stream);
 
