@@ -886,7 +886,7 @@ def paged_append_make_args(table: RopeTable, positions, *, q_rope=None, q=None, 
     """Arguments of :func:`paged_append_args`.
 
     ``positions``: int32 [B, N].  Queries: ``q_rope`` bf16 [B, N, H, 64] (any strides, multiples of 8),
-    normalised with ``q_norm`` (bf16 [64]) if given, is rotated into ``q[..., 512:]`` of bf16 [B, N, H, 576].
+    normalised with ``q_norm`` (bf16 [64]) if given, is rotated into ``q[..., 512:]`` of bf16 [B, N, H, 576] (not expanded).
     Rows: ``c`` bf16 [B, N, 512], normalised with ``c_norm`` (bf16 [512]) if given, goes in 4 bits, and ``k_rope``
     bf16 [B, N, 64], normalised with ``k_norm`` if given and rotated, in bf16 to row ``d_pos[b] + n`` of request b
     in ``pages`` (uint8 [n_pages, page_rows, 416]) by ``page_table`` (int32 [B, columns]).  ``kv_scale``: a power
@@ -905,6 +905,7 @@ def paged_append_make_args(table: RopeTable, positions, *, q_rope=None, q=None, 
         a.q_rope, a.q_rope_batch, a.q_rope_token, a.q_rope_head = _strides(q_rope, "q_rope", (B, N, H, D_ROPE), 3)
         _need(q, "q", torch.bfloat16, (B, N, H, D_ROW), contiguous=False)
         part = q[..., D_LATENT:]
+        _apart(part, "q", 3)
         a.q_out, a.q_out_batch, a.q_out_token, a.q_out_head = _strides(part, "q", (B, N, H, D_ROPE), 3)
     elif q_norm is not None:
         raise ValueError("q_norm belongs to q_rope and q")

@@ -400,6 +400,9 @@ int check(const mla_paged_append_args* a) {
          off(a->q_norm, 16)))
         return MLA_EALIGN;
     if (off(a->turns, 8) || off(a->positions, 4) || off(a->n_tokens, 4)) return MLA_EALIGN;
+    if (a->heads > 0 && (piled(a->batch, a->q_out_batch, kDRope) || piled(a->tokens, a->q_out_token, kDRope) ||
+                         piled(a->heads, a->q_out_head, kDRope)))
+        return MLA_EINVAL;
     return MLA_OK;
 }
 

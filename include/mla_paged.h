@@ -75,7 +75,8 @@ typedef struct {
     const int *n_tokens;        /* (device) int32 [B], clamped to 0 .. N; NULL = N */
     const void *q_rope;         /* (device) bf16 [B][N][heads][64], 16-byte aligned, strides multiples of 8 */
     long long q_rope_batch, q_rope_token, q_rope_head;
-    void *q_out;                /* (device) as in mla_rope_args */
+    void *q_out;                /* (device) as in mla_rope_args; heads in places of their own: strides of 64 or more
+                                   (or -64 or less) where there are several requests, tokens, heads */
     long long q_out_batch, q_out_token, q_out_head;
     const void *c;              /* (device) bf16 [B][N][512] */
     long long c_batch, c_token;

@@ -70,3 +70,29 @@ def test_library_refuses_reads_into_one_place(kw, status):
     c = mla.PagedCache(pages=PTR, page_stride=64 * 416, n_pages=10, page_rows=64, page_table=PTR, columns=4, kv_scale=1.0)
     a = mla.PagedReadArgs(**{**dict(cache=c, batch=2, rows=5, out=PTR, out_batch=2880, out_row=576), **kw})
     assert mla.lib().mla_paged_read(ctypes.byref(a), None) == status
+
+
+def append_args(q):
+    B, N = q.shape[:2]
+    table = mla.RopeTable(torch.zeros(32, dtype=torch.int64), 64, True, 1.0)
+    return mla.paged_append_make_args(table, torch.zeros(B, N, dtype=torch.int32), q_rope=bf16(*q.shape[:3], 64), q=q)
+
+
+@pytest.mark.parametrize("dim", [0, 1, 2])
+def test_queries_written_to_an_expanded_tensor_are_refused(dim, on_host):
+    shape = [2, 3, 4, 576]
+    wide = list(shape)
+    shape[dim] = 1
+    append_args(bf16(*shape))
+    append_args(bf16(*wide))
+    with pytest.raises(ValueError, match="expanded"):
+        append_args(bf16(*shape).expand(wide))
+
+
+@pytest.mark.parametrize("kw", [dict(q_out_batch=0), dict(q_out_token=0), dict(q_out_head=0), dict(q_out_head=56),
+                                dict(q_out_token=-56)])
+def test_library_refuses_queries_in_one_place(kw):
+    a = mla.PagedAppendArgs(**{**dict(batch=2, tokens=3, heads=16, rot_dim=64, interleaved=1, amplitude=1.0, turns=PTR,
+                                      positions=PTR, q_rope=PTR, q_rope_batch=576, q_rope_token=192, q_rope_head=64,
+                                      q_out=PTR, q_out_batch=27648, q_out_token=9216, q_out_head=576, eps=1e-6), **kw})
+    assert mla.lib().mla_paged_append(ctypes.byref(a), None) == mla.EINVAL
