@@ -373,7 +373,8 @@ def _run_compact(s):
 
 # The state's tensors whose addresses are in a call's arguments.
 LAID_OUT = dict(
-    append=itemgetter("positions", "q_proj", "q", "kv_proj", "pages", "table", "n_tokens", "d_pos", "values"),
+    append=itemgetter("positions", "q_proj", "q", "kv_proj", "pages", "table", "n_tokens", "d_pos", "values", "c_norm",
+                      "k_norm", "q_norm"),
     attend=itemgetter("q", "pages", "table", "out", "lse", "n_tokens", "d_pos"),
     fork=itemgetter("pages", "table", "table_out", "d_pos", "d_pos_out", "refs_out", "count", "parent", "rows"),
     compact=itemgetter("pages", "table", "table_out", "refs", "refs_out", "count"))
@@ -390,6 +391,7 @@ def _own(s):
         h = None
     if op == "append":
         if h is None:
+            # (the base of every state's inv_freq)
             table = mla.rope_table(rot_dim=ROPE, base=10000.0, interleaved=case["interleaved"])
             a = mla.paged_append_make_args(
                 table, s["positions"], q_rope=s["q_proj"][..., 128:], q=s["q"], c=s["kv_proj"][..., :LATENT],
