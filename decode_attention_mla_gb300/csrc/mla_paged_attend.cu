@@ -20,8 +20,9 @@
 // 2^14 .. 2^15 (values down to 2^-31 of it stay exact); the scores' factor takes it back.
 //
 // Rounding: P enters the product as one f16 of 2^7 times the probability (relative to the reference,
-// which lags the maximum by 2^8 at most: at most 2^15), 2^-12 each, so bf16 and fp32 outputs are the
-// same product; O and the statistics are fp32, sums use the unrounded probabilities.
+// which lags the maximum by 2^8 at most: at most 2^15), off by up to 2^-11 each (below 2^-21 of the reference,
+// where f16 is subnormal, by up to 2^-32 of it); bf16 and fp32 outputs are the same product, so an fp32 output is not closer than
+// that.  O and the statistics are fp32, sums use the unrounded probabilities.
 //
 // What a token does not attend must not reach it: masked scores become -infinity and P = 0; the
 // only value of V that is not finite, an E4M3 scale's NaN, becomes 0 there (a token that attends such

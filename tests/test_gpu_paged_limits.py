@@ -4,10 +4,13 @@ import math
 import pytest
 import torch
 
+import decode_attention_mla_gb300 as mla
 import perf.more_operators as measured
+import _paged_ref as ref
 from test_gpu_paged import BOTH, Append, Case
 
 pytestmark = pytest.mark.gpu
+I32 = dict(dtype=torch.int32, device="cuda")
 
 # a last tile that the rows end in; a window; rows without a page
 WHERE = [dict(d_pos=[999]), dict(d_pos=[999, 40], Q=2, window=300, sink=5), dict(d_pos=[999], gone=[(0, 3), (0, 62)])]
@@ -90,3 +93,31 @@ def test_measured_append_follows_weights_that_are_replaced(monkeypatch):
         got, want = measured.run(a), measured.run(b)
         assert all(torch.equal(x, y) for x, y in zip(got, want))
     assert not any(torch.equal(x, y) for x, y in zip(got, first))
+
+
+@BOTH
+def test_probabilities_are_rounded_once_to_f16(H, sms):
+    """Two rows, of which the second's latents are 1: the output is its probability, off by half a step of f16's eleven bits
+    (2^-11), and where that is subnormal by half of 2^-31 of the largest."""
+    Q = 64
+    pages = torch.zeros(1, 8, 416, dtype=torch.uint8)
+    pages[0, 1, :256], pages[0, 1, 256:288] = 0x22, 0x38          # 1.0 times 1.0
+    pages[0, 1, 288:290] = torch.tensor([0x80, 0x3f], dtype=torch.uint8)
+    q = torch.zeros(Q, 1, H, 576)
+    q[..., 512] = torch.linspace(-24, 24, Q * H).view(Q, 1, H)
+    q = q.bfloat16()
+    s = q[..., 512].double()
+    plan = mla.paged_plan(batch=Q, tokens=1, heads=H, scale=1.0, num_sms=sms)
+    out, lse = torch.zeros(Q, 1, H, 512, device="cuda"), torch.zeros(Q, 1, H, device="cuda")
+    mla.paged_forward(plan, q.cuda(), pages.cuda(), torch.zeros(Q, 1, **I32), out, lse, mla.paged_alloc_scratch(plan),
+                      d_pos=torch.ones(Q, **I32))
+    p = torch.sigmoid(s)
+    # besides: the score in base 2 (its factor's rounding and its own), the reference and the difference to it (each of the
+    # score and 7 more at most), both exponentials (2^-21), the sum and its reciprocal
+    rest = (4 * 1.4427 * s.abs() + 28) * ref.F32 + 2 * 2.0 ** -21 + 4 * ref.F32
+    tol = p * (ref.F16 + rest) + 2.0 ** -32
+    err = (out.cpu().double() - p[..., None]).abs()
+    assert bool((err <= tol[..., None]).all()), f"off by {float((err / tol[..., None]).max()):.4g} bounds"
+    want = torch.logaddexp(s, torch.zeros_like(s))
+    assert bool(((lse.cpu().double() - want).abs() <= rest + want.abs() * 4 * ref.F32).all())
+    assert float((err / p[..., None]).where((p > 1e-4)[..., None], 0).max()) > 2.0 ** -12
