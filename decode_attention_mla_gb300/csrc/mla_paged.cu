@@ -90,8 +90,10 @@ int prepare(cudaStream_t st, bool may_capture) {
 // Work, in units of 64 cache rows per SM, a block of sixteen query rows counting as two more (requests x query rows x cache
 // rows): 1 x 128 x 255 0.3 units, 10.2 and 15.4 us; 1 x 128 x 2000 1.8, 14.3 and 16.7; 8 x 128 x 255 2.5, 12.6 and 17.5; 2 x 64 x
 // 3000 2.6, 18.0 and 18.5; 7 x 64 x 1000 3.3, 17.3 and 19.8; but 1 x 128 x 4000 3.4, 19.2 and 17.4; 1 x 128 x 10000 8.4, 25.5 and 22.0.
-// (How long the requests are, the host does not know: it takes the table's length, or what a window leaves of it.  The kernel
-// counts units in an int.)
+// (How long the requests are, the host does not know: it takes the table's length, or what a window leaves of it.  So the rule
+// by work is one for tables about as long as their requests, and with 17 .. 32 query rows and long caches the choice is the
+// slower one by the 8 % above: a table for 32768 rows says nothing of whether 4096 or 32768 are in it.  The kernel counts
+// units in an int.)
 constexpr int kFewRows = 32, kFewUnits = 3;
 bool few_rows(const mla_paged_plan_t* pl, const mla_paged_args* a) {
     const long long rows = static_cast<long long>(pl->shape.tokens) * pl->shape.heads;

@@ -74,7 +74,7 @@ struct __align__(16) Item {
     int b, lo, hi, tile;                                   // tiles lo .. hi - 1, from `tile` on and round
     int near, skip, d_pos, n_tok;                          // as r.lo, r.base of the request, and its own
     int rb, flags, n_rb, n_tiles;
-    int begin, item, unused[2];
+    int begin, unused[3];
 };
 constexpr int kWhole = 1, kOpens = 2, kCut = 4;
 constexpr int kItems = 4;
@@ -132,7 +132,6 @@ __device__ void scout(const PagedParams& p, Shared& sh, int lane) {
             i.n_rb = c.n_rb;
             i.n_tiles = c.n_tiles;
             i.begin = c.begin;
-            i.item = c.item;
             mbar_arrive(&sh.item_full[c.item % kItems]);
         }
         __syncwarp();
@@ -349,8 +348,6 @@ __device__ void fill(const PagedParams& p, Shared& sh, uint32_t rank, int nth, i
 struct Producer {
     const PagedMaps& maps;
     const PagedParams& p;
-    Shared& sh;
-    const uint32_t rank;
     const int lane, box;                                   // rows per box; a lane has one of those of 64 rows
     const uint64_t policy;
 
@@ -376,7 +373,7 @@ struct Producer {
 
 // K and the key values of this CTA's 64 rows.
 __device__ void produce_keys(const PagedMaps& maps, const PagedParams& p, Shared& sh, uint32_t rank, int lane) {
-    const Producer pr{maps, p, sh, rank, lane, box_rows(p.cache), l2_policy_evict_normal()};
+    const Producer pr{maps, p, lane, box_rows(p.cache), l2_policy_evict_normal()};
     const uint32_t rope_bar = map_to_rank(&sh.rope_ready, 0);
     const int mine = 64 * static_cast<int>(rank);
     Walk c;
@@ -414,7 +411,7 @@ __device__ void produce_keys(const PagedMaps& maps, const PagedParams& p, Shared
 // V of the tile's rows, this CTA's 256 features; and this CTA's 64 rows of a later tile on their way to L2.
 constexpr int kAhead = 3;                                  // tiles
 __device__ void produce_values(const PagedMaps& maps, const PagedParams& p, Shared& sh, uint32_t rank, int lane) {
-    const Producer pr{maps, p, sh, rank, lane, box_rows(p.cache), l2_policy_evict_normal()};
+    const Producer pr{maps, p, lane, box_rows(p.cache), l2_policy_evict_normal()};
     Walk c;
     bool ok = c.start(sh);
     if (c.left <= 0) return;

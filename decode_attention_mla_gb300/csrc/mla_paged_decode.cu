@@ -1,10 +1,10 @@
 // mla_paged_decode.cu -- attention over the 4-bit paged cache for few query rows:
 // warp-level MMAs on values widened in registers (include/mla_paged.h).
 //
-// Sixteen query rows (token * heads + head) are one MMA tile, and rows need be widened for nobody
-// else, so nothing is gained by operands in shared memory: the tcgen05 kernel (mla_paged_attend.cu) writes
-// and reads them there, 390 KB per 128 rows of a pair, whatever the number of query rows.  Here rows stay as they
-// are in shared memory (416 bytes), and are widened on their way from there to the MMAs.
+// Sixteen query rows (token * heads + head) are one MMA tile.  The tcgen05 kernel (mla_paged_attend.cu) passes 470 KB
+// through each SM's shared memory per 128 cache rows of a pair, whatever the number of query rows.  Here rows stay as they
+// are in shared memory (416 bytes) and are widened in registers: straight into the fragments of Q K^T, and by way of shared
+// memory, which transposes them, into those of P V.
 //
 // A group of four warps shares the 32 rows of a slot.  Warp w has features 128 w .. + 127 (and 16 of the 64 key
 // values): it widens them once, into the fragments of Q K^T and to shared memory of its own, from where ldmatrix
