@@ -119,9 +119,11 @@ MLA_API int mla_paged_read(const mla_paged_read_args *args, void *stream);
  *
  * q_lat enters the product in f16 times a power of two per query row, set by the largest of
  * |q_lat| and |q_rope| / kv_scale: values down to 2^-31 of it are exact, smaller ones off by at
- * most 2^-39 of it.  Latents are exact; key values and q_rope are bf16.  Probabilities enter the
- * second product in f16, for bf16 and fp32 outputs alike: off by up to 2^-11 each, those below 2^-21 of the
- * largest by up to 2^-32 of it; sums and statistics are fp32.
+ * most 2^-39 of it.  (Where that largest times scale * kv_scale is below 2^-110, scores are off by less
+ * than 2^-100 instead; above 2^141, scores that are not 0 may come out smaller than they are, or infinite.)
+ * Latents are exact; key values and q_rope are bf16.  Probabilities enter the second product in f16, for
+ * bf16 and fp32 outputs alike: off by up to 2^-11 each, those below 2^-21 of the largest by up to 2^-32 of
+ * it; sums and statistics are fp32.
  *
  * What a token does not attend does not reach its result, whatever the bytes are.  An attended
  * row with a NaN, or whose score is NaN or +infinity, makes the whole result of the (token,
